@@ -96,7 +96,8 @@ typedef enum {
     W4A4_ERR_WORKSPACE = 4,        /* a buffer size is below the size query's result */
     W4A4_ERR_CUDA = 5,             /* the CUDA runtime reported an error */
     W4A4_ERR_TIMEOUT = 6,          /* a bounded device-side wait gave up */
-    W4A4_ERR_NO_DEVICE = 7         /* no usable sm_103 device is current */
+    W4A4_ERR_NO_DEVICE = 7,        /* no usable sm_103 device is current */
+    W4A4_ERR_INDEX = 8             /* a page, sequence, position or length in device memory lay outside its table */
 } w4a4_status;
 
 /* Kernel selection for w4a4_linear_select / w4a4_debug_group_partials. */
@@ -310,6 +311,153 @@ w4a4_status w4a16_pack_weights_asym(const float* W, const uint16_t* L_down, cons
 w4a4_status w4a16_linear_asym(const uint16_t* X, const void* packed, size_t packed_bytes, const uint16_t* colscale,
                               const uint16_t* bias, int M, int N, int K, int r, uint16_t* Y, cudaStream_t stream);
 
+/* ---- the rest of a decoder layer: paged key-value cache, attention of one new
+ * token per sequence over it, and the norms around a block.  Element types: */
+typedef enum { W4A4_F16 = 0, W4A4_BF16 = 1, W4A4_F32 = 2, W4A4_E4M3 = 3 } w4a4_dtype;
+
+/* A view of a paged cache.  Two pools of `pages` pages, a page being the keys
+ * (values) of page_size consecutive tokens of one sequence.  Row (page p, token
+ * slot t, head h) is head_dim contiguous elements at element offset
+ * p * page_stride + t * token_stride + h * head_stride (64-bit), so that both
+ * [page][token][head][dim] and [page][head][token][dim] pools, and pools of
+ * several layers in one buffer, are taken as they are.  page_table [seqs][max_pages]
+ * (row stride table_stride): token j of sequence s is in page
+ * page_table[s][j / page_size], slot j % page_size.
+ *   dtype      W4A4_F16, W4A4_BF16 or W4A4_E4M3; an E4M3 element stands for
+ *              code * k_scale[head] (v_scale[head]); NULL scales mean 1
+ *   head_dim   64, 96, 128 or 256
+ *   strides    non-negative, of whole 16 bytes; the pools 16-byte aligned
+ * `bytes` is sizeof(w4a4_kv_cache), and so in the argument structs below; a
+ * call with another value returns W4A4_ERR_INVALID_ARG.  The structs live on the
+ * host and are read during the call only. */
+typedef struct {
+    uint64_t bytes;
+    void* k;
+    void* v;
+    const float* k_scale;
+    const float* v_scale;
+    const int32_t* page_table;
+    int64_t k_page_stride, k_token_stride, k_head_stride;
+    int64_t v_page_stride, v_token_stride, v_head_stride;
+    int64_t table_stride;
+    int32_t seqs, max_pages, pages, page_size, kv_heads, head_dim, dtype, reserved;
+} w4a4_kv_cache;
+
+/* Keys and values of new tokens into the cache, normalised and rotated on the way
+ * ("W4A4 CUDA Kernel for Voice Clone", 3.4 and 5: the per-head q/k RMSNorm and the
+ * rotation between the qkv linear and attention).
+ * For token t < tokens of sequence s = seqs[t] (NULL: s = t) at position
+ * p = positions[t], and x a head of q [t], k [t] (head_dim elements; rows
+ * addressed by token and head strides in elements, e.g. slices of the qkv output):
+ *   x'    = q_gain ? x / sqrt(mean x^2 + eps) * q_gain : x     (k_gain for k)
+ *   y     = x' with, for i < rot_dim / 2 and c, n = rope[p][0][i], rope[p][1][i],
+ *           (y_a, y_b) = (x'_a c - x'_b n, x'_b c + x'_a n),
+ *           (a, b) = (i, i + rot_dim / 2), or (2 i, 2 i + 1) if interleaved
+ *   q_out[t] = y (may be q itself with the same strides); the cache's row
+ *   (s, p) of the head = y for keys and the unrotated v for values.
+ * Arithmetic in fp32, one rounding to the stored type (E4M3: of y / k_scale,
+ * IEEE division, to nearest even, saturating at 448; NaN stays NaN).
+ * rope: fp32 [rope_rows][2][rot_dim / 2] (cosines, then sines), NULL: no
+ * rotation; w4a4_rope_table fills one.  rot_dim % 16 == 0, <= head_dim.
+ * dtype W4A4_F16 or W4A4_BF16 (q, k, v, q_out, gains); the cache has the same
+ * type or W4A4_E4M3.  seqs[t] < 0 marks a padding token: nothing is stored and
+ * its q_out row is zero.  A token whose sequence, position (against the page
+ * table's width and, with rope, rope_rows) or page lies outside its table is
+ * treated as padding and sets W4A4_ERR_INDEX in the device status.  Two tokens
+ * of one call must not name the same row of the cache.  tokens == 0: no-op. */
+typedef struct {
+    uint64_t bytes;
+    const void* q;
+    const void* k;
+    const void* v;
+    void* q_out;
+    const int32_t* positions;
+    const int32_t* seqs;
+    const float* rope;
+    const void* q_gain;
+    const void* k_gain;
+    int64_t q_token_stride, q_head_stride, k_token_stride, k_head_stride, v_token_stride, v_head_stride;
+    int64_t out_token_stride, out_head_stride;
+    int32_t tokens, q_heads, dtype, rope_rows, rot_dim, interleaved;
+    float eps;
+    int32_t reserved;
+} w4a4_kv_append_args;
+w4a4_status w4a4_kv_append(const w4a4_kv_cache* cache, const w4a4_kv_append_args* args, cudaStream_t stream);
+/* rope[p][0][i] = cos(p theta^(-2 i / rot_dim)), rope[p][1][i] = the sine; the
+ * angle in fp64, each value rounded once.  fp32 [rows][2][rot_dim / 2]. */
+w4a4_status w4a4_rope_table(float* rope, int rows, int rot_dim, double theta, cudaStream_t stream);
+
+/* Attention of one new token per sequence over the cache.  For sequence b with
+ * n = lengths[b] cached tokens (its new one among them) and query head h of
+ * key-value head g = h / (q_heads / kv_heads), over the tokens
+ * j in [max(0, n - window), n)  (window 0: all of [0, n)):
+ *   a_j = scale q[b][h] . k_j[g],   lse = log sum_j exp(a_j),
+ *   out[b][h] = sum_j exp(a_j - lse) v_j[g]
+ * (natural logarithm; E4M3 keys and values times their head's scales).  A
+ * sequence without tokens gives out = 0 and lse = -inf, as does one whose a_j
+ * are all -inf.  Slots outside the range are never used, whatever they hold.
+ * q, out: dtype W4A4_F16 or W4A4_BF16 (the cache: the same or W4A4_E4M3), row
+ * (b, h) at b * token_stride + h * head_stride; lse fp32 [seqs][q_heads] or NULL;
+ * lengths int32 [seqs]; cache->seqs sequences; q_heads % kv_heads == 0.
+ * Scores, statistics and sums are fp32; the probabilities are rounded to the
+ * matrix instruction's operand type (fp16, for bf16 caches bf16).  A length
+ * outside [0, max_pages * page_size] is clamped, tokens of a page outside
+ * [0, pages) are left out; both set W4A4_ERR_INDEX.
+ * workspace: w4a4_paged_attention_workspace_bytes bytes (0: bad arguments),
+ * zeroed once by the caller and left zeroed where it has to be: it holds the
+ * parts of sequences that are split between CTAs.  Calls that may overlap on the
+ * GPU must not share it.  The result does not depend on the order in which the
+ * CTAs finish: the parts are joined in the order of the tokens. */
+typedef struct {
+    uint64_t bytes;
+    const void* q;
+    void* out;
+    float* lse;
+    const int32_t* lengths;
+    void* workspace;
+    uint64_t workspace_bytes;
+    int64_t q_token_stride, q_head_stride, out_token_stride, out_head_stride;
+    float scale;
+    int32_t q_heads, dtype, window;
+} w4a4_paged_attention_args;
+size_t w4a4_paged_attention_workspace_bytes(int seqs, int q_heads, int kv_heads, int head_dim);
+w4a4_status w4a4_paged_attention(const w4a4_kv_cache* cache, const w4a4_paged_attention_args* args,
+                                 cudaStream_t stream);
+
+/* The residual stream between two blocks in one pass.  Row m < rows, width W:
+ *   r'[m] = r[m] + scale * gate[m] (.) post(y[m]),   x[m] = pre(r'[m])
+ * y: the block's output; r, r': the residual stream (r_out may be r itself); x:
+ * the next block's input.  post, pre: W4A4_NORM_NONE (identity),
+ *   W4A4_NORM_RMS    z / sqrt(mean z^2 + eps) * gain
+ *   W4A4_NORM_LAYER  (z - mean z) / sqrt(mean (z - mean z)^2 + eps) * gain + bias
+ * with gain, bias [width] (NULL: 1 and 0).  gate: row m / rows_per_gate
+ * of [.][width] at stride gate_stride (rows_per_gate 0: one row for all; gate
+ * NULL: 1).  x may be NULL (only the stream is wanted).  dtype W4A4_F16 or
+ * W4A4_BF16: y, x, gate, gains and biases; res_dtype: r and r', the same or
+ * W4A4_F32.  fp32 arithmetic; x is taken from r' before its rounding.
+ * width % 8 == 0, 8 <= width <= 16384; row strides in elements, >= width, of
+ * whole 16 bytes.  rows == 0: no-op. */
+#define W4A4_NORM_NONE 0
+#define W4A4_NORM_RMS 1
+#define W4A4_NORM_LAYER 2
+typedef struct {
+    uint64_t bytes;
+    const void* y;
+    const void* r;
+    void* r_out;
+    void* x;
+    const void* gate;
+    const void* post_gain;
+    const void* post_bias;
+    const void* pre_gain;
+    const void* pre_bias;
+    int64_t y_stride, r_stride, r_out_stride, x_stride, gate_stride;
+    int32_t rows, width, rows_per_gate, dtype, res_dtype, post, pre;
+    float scale, eps;
+    int32_t reserved;
+} w4a4_block_norm_args;
+w4a4_status w4a4_block_norm(const w4a4_block_norm_args* args, cudaStream_t stream);
+
 /* ---- debug / validation entry points (small shapes; they synchronise `stream`)
  * Unpack the packed weights: codes int8 [N, K], scales fp16 [N, K/64],
  * L_down fp16 [K, r], L_up fp16 [r, N] (the last two may be NULL). */
@@ -337,8 +485,10 @@ w4a4_status w4a4_debug_group_partials(const void* act_ws, size_t act_ws_bytes, c
 w4a4_status w4a4_debug_forward_partials(const uint16_t* X, const void* packed, size_t packed_bytes, int M, int N,
                                         int K, int r, void* act_ws, size_t act_ws_bytes, int32_t* P,
                                         cudaStream_t stream);
-/* Reads and clears the device status word written by bounded waits
- * (W4A4_OK or W4A4_ERR_TIMEOUT); synchronises the device. */
+/* Reads and clears the device status words written by bounded waits
+ * (W4A4_ERR_TIMEOUT) and by the paged-cache kernels, where an index they read
+ * from device memory lay outside its table (W4A4_ERR_INDEX); W4A4_OK if
+ * neither.  Synchronises the device. */
 w4a4_status w4a4_device_status(void);
 
 /* ---- dispatch and diagnostics ([INT4] "Failure modes": log the kernel chosen) */

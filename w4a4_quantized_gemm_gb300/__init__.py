@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -20,12 +21,15 @@ LIB_PATH = os.path.join(_HERE, "libw4a4.so")
 
 W4A4_OK = 0
 W4A4_ERR_TIMEOUT = 6
+W4A4_ERR_INDEX = 8
+NORM_NONE, NORM_RMS, NORM_LAYER = 0, 1, 2
 KERNEL_AUTO, KERNEL_TC, KERNEL_SMALLM, KERNEL_SMALLM_TC, KERNEL_FUSED = 0, 1, 2, 3, 4
 GROUP = 64
 
 _STATUS = {
     0: "W4A4_OK", 1: "W4A4_ERR_INVALID_ARG", 2: "W4A4_ERR_UNSUPPORTED_SHAPE", 3: "W4A4_ERR_MISALIGNED",
     4: "W4A4_ERR_WORKSPACE", 5: "W4A4_ERR_CUDA", 6: "W4A4_ERR_TIMEOUT", 7: "W4A4_ERR_NO_DEVICE",
+    8: "W4A4_ERR_INDEX",
 }
 
 
@@ -65,6 +69,11 @@ SIGNATURES = {
     "w4a4_debug_unpack_weights": (I, [P, I, I, I, P, P, P, P, P]),
     "w4a4_debug_unpack_act": (I, [P, I, I, I, P, P, P, P, P]),
     "w4a4_debug_group_partials": (I, [P, Z, P, Z, I, I, I, I, I, P, P]),
+    "w4a4_kv_append": (I, [P, P, P]),
+    "w4a4_rope_table": (I, [P, I, I, ctypes.c_double, P]),
+    "w4a4_paged_attention_workspace_bytes": (Z, [I, I, I, I]),
+    "w4a4_paged_attention": (I, [P, P, P]),
+    "w4a4_block_norm": (I, [P, P]),
     "w4a4_device_status": (I, []),
     "w4a4_status_string": (ctypes.c_char_p, [I]),
     "w4a4_last_dispatch": (ctypes.c_char_p, []),
@@ -342,6 +351,187 @@ def w4a4_stream_k() -> bool:
 
 def w4a4_set_stream_k(on: bool):
     lib().w4a4_set_stream_k(1 if on else 0)
+
+
+# ------------------------------------ paged cache, its attention, block norms
+_DTYPE = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2, torch.float8_e4m3fn: 3}  # w4a4_dtype
+# The argument structs of include/w4a4.h, field by field, each opening with its size.
+_CACHE = struct.Struct("=Q5Q7q8i")       # pointers; strides; sizes and type
+_APPEND = struct.Struct("=Q9Q8q6ifi")
+_ATTENTION = struct.Struct("=Q5QQ4qf3i")
+_BLOCK_NORM = struct.Struct("=Q9Q5q7iffi")
+
+
+def _refuse(where: str, status: int = 1):
+    raise W4A4Error(status, where)
+
+
+def _rows(t, where: str, heads: int, dim: int, dtype, device: int):
+    """Pointer and strides of a [rows, heads, dim] tensor whose last dimension is contiguous."""
+    n, h, d = t.shape
+    a, b, c = t.stride()
+    if h != heads or d != dim or t.dtype != dtype or t.get_device() != device or c != 1:
+        _refuse(where)
+    return n, t.data_ptr(), a, b
+
+
+def _ints(t, where: str, n: int, device: int) -> int:
+    if t.dtype != torch.int32 or t.get_device() != device or t.numel() != n or not t.is_contiguous():
+        _refuse(where)
+    return t.data_ptr()
+
+
+def _vector(t, where: str, n: int, dtype, device: int) -> int:
+    if t is None:
+        return 0
+    if t.dtype != dtype or t.get_device() != device or t.numel() != n or not t.is_contiguous():
+        _refuse(where)
+    return t.data_ptr()
+
+
+class PagedKVCache:
+    """A view of a paged key-value cache (w4a4_kv_cache) and the workspace of its attention.
+
+    k, v: pools [pages, page_size, kv_heads, head_dim] in fp16, bf16 or float8_e4m3fn with any
+    strides (a [pages, kv_heads, page_size, head_dim] pool is passed as its transpose(1, 2)).
+    page_table: int32 [seqs, max_pages].  k_scale, v_scale: fp32 [kv_heads] of 8-bit pools.
+    The tensors are the caller's: their contents may change between calls, the tensors not.
+    Attention calls that may overlap on the GPU need a cache object (a workspace) each.
+    """
+
+    def __init__(self, k, v, page_table, k_scale=None, v_scale=None):
+        where = "PagedKVCache"
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or page_table.dim() != 2:
+            _refuse(where)
+        if k.dtype not in _DTYPE or k.stride(3) != 1 or v.stride(3) != 1 or not k.is_cuda or not v.is_cuda:
+            _refuse(where)
+        self.device = k.get_device()
+        if v.get_device() != self.device or page_table.get_device() != self.device:
+            _refuse(where)
+        if page_table.dtype != torch.int32 or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+            _refuse(where)
+        self.pages, self.page_size, self.kv_heads, self.head_dim = k.shape
+        self.seqs, self.max_pages = page_table.shape
+        self.dtype = k.dtype
+        scales = [_vector(t, where, self.kv_heads, torch.float32, self.device) for t in (k_scale, v_scale)]
+        self._keep = (k, v, page_table, k_scale, v_scale)
+        self._struct = _CACHE.pack(_CACHE.size, k.data_ptr(), v.data_ptr(), *scales, page_table.data_ptr(),
+                                   *k.stride()[:3], *v.stride()[:3], max(page_table.stride(0), self.max_pages),
+                                   self.seqs, self.max_pages, self.pages, self.page_size, self.kv_heads,
+                                   self.head_dim, _DTYPE[k.dtype], 0)
+        self._ws = {}
+
+    def workspace(self, q_heads: int):
+        """The workspace of attention with q_heads query heads: allocated and zeroed at its first use."""
+        ws = self._ws.get(q_heads)
+        if ws is None:
+            n = lib().w4a4_paged_attention_workspace_bytes(self.seqs, q_heads, self.kv_heads, self.head_dim)
+            if n == 0:
+                _refuse("w4a4_paged_attention_workspace_bytes", 2)
+            ws = torch.zeros(n, dtype=torch.uint8, device=f"cuda:{self.device}")
+            self._ws[q_heads] = ws
+        return ws
+
+
+def w4a4_rope_table(rows: int, rot_dim: int, theta: float, out=None, stream=None):
+    """fp32 [rows, 2, rot_dim / 2]: cosines and sines of position * theta^(-2 i / rot_dim)."""
+    if out is None:
+        out = torch.empty((rows, 2, rot_dim // 2), dtype=torch.float32, device="cuda")
+    if out.shape != (rows, 2, rot_dim // 2) or out.dtype != torch.float32:
+        _refuse("w4a4_rope_table")
+    _check(lib().w4a4_rope_table(_ptr(out), rows, rot_dim, theta, _stream(stream)), "w4a4_rope_table")
+    return out
+
+
+def w4a4_kv_append(q, k, v, positions, cache, q_out, seqs=None, rope=None, q_gain=None, k_gain=None,
+                   eps: float = 1e-6, interleaved: bool = False, stream=None):
+    """Keys and values of new tokens into `cache`, q and k normalised (gains given) and rotated
+    (rope given) on the way; the rotated queries go to q_out, which may be q.
+
+    q, q_out [tokens, q_heads, dim], k, v [tokens, kv_heads, dim]: fp16 or bf16, last dimension
+    contiguous (slices of a fused q|k|v output).  positions, seqs: int32 [tokens]; seqs None: token
+    t belongs to sequence t, negative: padding.  rope: fp32 [rows, 2, rot_dim / 2]
+    (w4a4_rope_table)."""
+    where = "w4a4_kv_append"
+    dtype, dim, dev = q.dtype, cache.head_dim, cache.device
+    heads = q.shape[1]
+    tokens, qp, q0, q1 = _rows(q, where, heads, dim, dtype, dev)
+    nk, kp, k0, k1 = _rows(k, where, cache.kv_heads, dim, dtype, dev)
+    nv, vp, v0, v1 = _rows(v, where, cache.kv_heads, dim, dtype, dev)
+    no, op, o0, o1 = _rows(q_out, where, heads, dim, dtype, dev)
+    if nk != tokens or nv != tokens or no != tokens or dtype not in _DTYPE:
+        _refuse(where)
+    rp = rows = rot = 0
+    if rope is not None:
+        rows, two, half = rope.shape
+        rot = 2 * half
+        rp = _vector(rope, where, rows * rot, torch.float32, dev)
+        if two != 2:
+            _refuse(where)
+    args = _APPEND.pack(_APPEND.size, qp, kp, vp, op, _ints(positions, where, tokens, dev),
+                        0 if seqs is None else _ints(seqs, where, tokens, dev), rp,
+                        _vector(q_gain, where, dim, dtype, dev), _vector(k_gain, where, dim, dtype, dev),
+                        q0, q1, k0, k1, v0, v1, o0, o1, tokens, heads, _DTYPE[dtype], rows, rot,
+                        1 if interleaved else 0, eps, 0)
+    _check(lib().w4a4_kv_append(cache._struct, args, _stream(stream)), where)
+
+
+def w4a4_paged_attention(q, cache, lengths, out, lse=None, scale=None, window: int = 0, workspace=None, stream=None):
+    """out [seqs, q_heads, dim] = attention of one new token per sequence, q, over the first
+    lengths[b] tokens (int32 [seqs]) that `cache` holds of each, or the last `window` of them.
+
+    scale: of the scores, dim ** -0.5 by default.  lse: fp32 [seqs, q_heads] or None.  workspace:
+    zeroed uint8 of w4a4_paged_attention_workspace_bytes, by default the cache object's own."""
+    where = "w4a4_paged_attention"
+    dtype, dim, dev = q.dtype, cache.head_dim, cache.device
+    heads = q.shape[1]
+    n, qp, q0, q1 = _rows(q, where, heads, dim, dtype, dev)
+    no, op, o0, o1 = _rows(out, where, heads, dim, dtype, dev)
+    if n != cache.seqs or no != n or dtype not in _DTYPE:
+        _refuse(where)
+    ws = cache.workspace(heads) if workspace is None else workspace
+    args = _ATTENTION.pack(_ATTENTION.size, qp, op, _vector(lse, where, n * heads, torch.float32, dev),
+                           _ints(lengths, where, n, dev), ws.data_ptr(), ws.numel() * ws.element_size(),
+                           q0, q1, o0, o1, dim ** -0.5 if scale is None else scale, heads, _DTYPE[dtype], window)
+    _check(lib().w4a4_paged_attention(cache._struct, args, _stream(stream)), where)
+
+
+def w4a4_block_norm(y, r, x, r_out, gate=None, rows_per_gate: int = 0, scale: float = 1.0, post: int = NORM_RMS,
+                    post_gain=None, post_bias=None, pre: int = NORM_RMS, pre_gain=None, pre_bias=None,
+                    eps: float = 1e-6, stream=None):
+    """r_out = r + scale * gate * post(y); x = pre(r_out): the norm after a block, its gate and
+    residual scale, the residual addition and the norm before the next block in one pass.
+
+    y, x [rows, width] fp16 or bf16 (x None: not wanted); r, r_out the same type or fp32 (r_out may
+    be r).  post, pre: NORM_NONE, NORM_RMS or NORM_LAYER.  gate: [width] or [gates, width], row m
+    under gate row m // rows_per_gate (0: one row for all)."""
+    where = "w4a4_block_norm"
+    dtype, dev = y.dtype, y.get_device()
+    rows, width = y.shape
+    for t in (r, r_out) if x is None else (r, r_out, x):
+        if t.shape != y.shape or t.stride(1) != 1 or t.get_device() != dev:
+            _refuse(where)
+    if dtype not in _DTYPE or r.dtype not in _DTYPE or r_out.dtype != r.dtype or y.stride(1) != 1 or dev < 0:
+        _refuse(where)
+    gp = gs = 0
+    if gate is not None:
+        gates = gate.numel() // width
+        need = -(-rows // rows_per_gate) if rows_per_gate > 0 else 1
+        if gate.dtype != dtype or gate.get_device() != dev or gate.shape[-1] != width or gate.stride(-1) != 1:
+            _refuse(where)
+        if gate.dim() > 2 or gates < need:
+            _refuse(where)
+        gp, gs = gate.data_ptr(), gate.stride(0) if gate.dim() == 2 else width
+    xp = xs = 0
+    if x is not None:
+        if x.dtype != dtype:
+            _refuse(where)
+        xp, xs = x.data_ptr(), x.stride(0)
+    vec = [_vector(t, where, width, dtype, dev) for t in (post_gain, post_bias, pre_gain, pre_bias)]
+    args = _BLOCK_NORM.pack(_BLOCK_NORM.size, y.data_ptr(), r.data_ptr(), r_out.data_ptr(), xp, gp, *vec,
+                            y.stride(0), r.stride(0), r_out.stride(0), xs, gs, rows, width, rows_per_gate,
+                            _DTYPE[dtype], _DTYPE[r.dtype], post, pre, scale, eps, 0)
+    _check(lib().w4a4_block_norm(args, _stream(stream)), where)
 
 
 # ------------------------------------------------------------- layer helper

@@ -70,7 +70,41 @@ w4a4_status device_status_words() {
     const w4a4_status d = smtc_read_and_clear_status();
     const w4a4_status e = q_read_and_clear_status();
     const w4a4_status f = fused_read_and_clear_status();
-    return a != W4A4_OK ? a : b != W4A4_OK ? b : c != W4A4_OK ? c : d != W4A4_OK ? d : e != W4A4_OK ? e : f;
+    const w4a4_status g = append_read_and_clear_status();
+    const w4a4_status h = attention_read_and_clear_status();
+    for (const w4a4_status st : {a, b, c, d, e, f, g, h})
+        if (st != W4A4_OK) return st;
+    return W4A4_OK;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+bool is_act(int dtype) { return dtype == W4A4_F16 || dtype == W4A4_BF16; }
+// A row stride in elements of `size` bytes that keeps every row 16-byte aligned.
+// The bound keeps stride * index below 2^63 bytes for every 31-bit index.
+bool good_stride(int64_t stride, int size) {
+    return stride >= 0 && stride <= (int64_t(1) << 29) && stride * size % 16 == 0;
+}
+
+// Everything a call can check of a cache without reading device memory.
+w4a4_status check_cache(const w4a4_kv_cache* c) {
+    if (!c || c->bytes != sizeof(*c)) return W4A4_ERR_INVALID_ARG;
+    if (c->seqs < 0 || c->max_pages < 0 || c->pages < 0 || c->page_size < 1 || c->kv_heads < 1)
+        return W4A4_ERR_INVALID_ARG;
+    if (!is_act(c->dtype) && c->dtype != W4A4_E4M3) return W4A4_ERR_INVALID_ARG;
+    if (int64_t(c->max_pages) * c->page_size > INT32_MAX) return W4A4_ERR_UNSUPPORTED_SHAPE;
+    if (c->head_dim != 64 && c->head_dim != 96 && c->head_dim != 128 && c->head_dim != 256)
+        return W4A4_ERR_UNSUPPORTED_SHAPE;
+    const int size = c->dtype == W4A4_E4M3 ? 1 : 2;
+    for (const int64_t st : {c->k_page_stride, c->k_token_stride, c->k_head_stride, c->v_page_stride,
+                             c->v_token_stride, c->v_head_stride})
+        if (!good_stride(st, size)) return W4A4_ERR_MISALIGNED;
+    if (c->table_stride < c->max_pages || c->table_stride > INT32_MAX) return W4A4_ERR_INVALID_ARG;
+    if (c->pages > 0 && (!c->k || !c->v)) return W4A4_ERR_INVALID_ARG;
+    if (c->seqs > 0 && c->max_pages > 0 && !c->page_table) return W4A4_ERR_INVALID_ARG;
+    if (!aligned16(c->k) || !aligned16(c->v) || !aligned4(c->page_table) || !aligned4(c->k_scale) ||
+        !aligned4(c->v_scale))
+        return W4A4_ERR_MISALIGNED;
+    return W4A4_OK;
 }
 }  // namespace
 
@@ -171,6 +205,7 @@ const char* w4a4_status_string(int status) {
         case W4A4_ERR_CUDA: return "CUDA runtime error";
         case W4A4_ERR_TIMEOUT: return "bounded device wait timed out";
         case W4A4_ERR_NO_DEVICE: return "no sm_103 device is current";
+        case W4A4_ERR_INDEX: return "an index in device memory lies outside its table";
         default: return "unknown status";
     }
 }
@@ -464,6 +499,95 @@ w4a4_status w4a4_rmsnorm_f16(const uint16_t* Y, int M, int ld_y, int K, uint16_t
     w4a4_status st = check_device();
     if (st != W4A4_OK) return st;
     launch_rmsnorm_f16(Y, M, ld_y, K, W4A4_RMSNORM_EPS, X, stream);
+    return launch_status();
+}
+
+w4a4_status w4a4_kv_append(const w4a4_kv_cache* cache, const w4a4_kv_append_args* a, cudaStream_t stream) {
+    w4a4_status st = check_cache(cache);
+    if (st != W4A4_OK) return st;
+    if (!a || a->bytes != sizeof(*a) || a->tokens < 0 || a->q_heads < 0 || !is_act(a->dtype)) return W4A4_ERR_INVALID_ARG;
+    if (cache->dtype != a->dtype && cache->dtype != W4A4_E4M3) return W4A4_ERR_INVALID_ARG;
+    if (a->q_heads > 65536 || cache->kv_heads > 65536) return W4A4_ERR_UNSUPPORTED_SHAPE;
+    if (a->rope && (a->rope_rows < 1 || a->rot_dim < 16)) return W4A4_ERR_INVALID_ARG;
+    if (a->rope && (a->rot_dim % 16 != 0 || a->rot_dim > cache->head_dim)) return W4A4_ERR_UNSUPPORTED_SHAPE;
+    if (a->tokens == 0) return W4A4_OK;
+    if (!a->k || !a->v || !a->positions || (a->q_heads > 0 && (!a->q || !a->q_out))) return W4A4_ERR_INVALID_ARG;
+    for (const void* p : {a->q, a->k, a->v, static_cast<const void*>(a->q_out), a->q_gain, a->k_gain,
+                          static_cast<const void*>(a->rope)})
+        if (!aligned16(p)) return W4A4_ERR_MISALIGNED;
+    if (!aligned4(a->positions) || !aligned4(a->seqs)) return W4A4_ERR_MISALIGNED;
+    for (const int64_t s : {a->q_token_stride, a->q_head_stride, a->k_token_stride, a->k_head_stride,
+                            a->v_token_stride, a->v_head_stride, a->out_token_stride, a->out_head_stride})
+        if (!good_stride(s, 2)) return W4A4_ERR_MISALIGNED;
+    if (a->q_heads > 0 && a->q == a->q_out &&
+        (a->q_token_stride != a->out_token_stride || a->q_head_stride != a->out_head_stride))
+        return W4A4_ERR_INVALID_ARG;
+    if ((st = check_device()) != W4A4_OK) return st;
+    launch_kv_append(*cache, *a, stream);
+    return launch_status();
+}
+
+w4a4_status w4a4_rope_table(float* rope, int rows, int rot_dim, double theta, cudaStream_t stream) {
+    if (rows < 0 || !(theta > 0.0)) return W4A4_ERR_INVALID_ARG;
+    if (rot_dim < 16 || rot_dim % 16 != 0 || rot_dim > 256) return W4A4_ERR_UNSUPPORTED_SHAPE;
+    if (rows == 0) return W4A4_OK;
+    if (!rope) return W4A4_ERR_INVALID_ARG;
+    if (!aligned16(rope)) return W4A4_ERR_MISALIGNED;
+    w4a4_status st = check_device();
+    if (st != W4A4_OK) return st;
+    launch_rope_table(rope, rows, rot_dim, theta, stream);
+    return launch_status();
+}
+
+size_t w4a4_paged_attention_workspace_bytes(int seqs, int q_heads, int kv_heads, int head_dim) {
+    if (seqs < 0 || kv_heads < 1 || q_heads < kv_heads || q_heads % kv_heads != 0) return 0;
+    if (head_dim != 64 && head_dim != 96 && head_dim != 128 && head_dim != 256) return 0;
+    return attention_workspace_bytes(seqs, q_heads, kv_heads, head_dim);
+}
+
+w4a4_status w4a4_paged_attention(const w4a4_kv_cache* cache, const w4a4_paged_attention_args* a,
+                                 cudaStream_t stream) {
+    w4a4_status st = check_cache(cache);
+    if (st != W4A4_OK) return st;
+    if (!a || a->bytes != sizeof(*a) || a->window < 0 || !is_act(a->dtype)) return W4A4_ERR_INVALID_ARG;
+    if (cache->dtype != a->dtype && cache->dtype != W4A4_E4M3) return W4A4_ERR_INVALID_ARG;
+    if (a->q_heads < 1) return W4A4_ERR_INVALID_ARG;
+    if (a->q_heads % cache->kv_heads != 0 || a->q_heads > 65536) return W4A4_ERR_UNSUPPORTED_SHAPE;
+    if (int64_t(cache->seqs) * a->q_heads > (1 << 24)) return W4A4_ERR_UNSUPPORTED_SHAPE;
+    if (cache->seqs == 0) return W4A4_OK;
+    if (!a->q || !a->out || !a->lengths || !a->workspace) return W4A4_ERR_INVALID_ARG;
+    if (!aligned16(a->q) || !aligned16(a->out) || !aligned16(a->workspace) || !aligned4(a->lse) ||
+        !aligned4(a->lengths))
+        return W4A4_ERR_MISALIGNED;
+    for (const int64_t s : {a->q_token_stride, a->q_head_stride, a->out_token_stride, a->out_head_stride})
+        if (!good_stride(s, 2)) return W4A4_ERR_MISALIGNED;
+    if (a->workspace_bytes < attention_workspace_bytes(cache->seqs, a->q_heads, cache->kv_heads, cache->head_dim))
+        return W4A4_ERR_WORKSPACE;
+    if ((st = check_device()) != W4A4_OK) return st;
+    return launch_paged_attention(*cache, *a, stream);
+}
+
+w4a4_status w4a4_block_norm(const w4a4_block_norm_args* a, cudaStream_t stream) {
+    if (!a || a->bytes != sizeof(*a) || a->rows < 0 || a->rows_per_gate < 0) return W4A4_ERR_INVALID_ARG;
+    if (!is_act(a->dtype) || (a->res_dtype != a->dtype && a->res_dtype != W4A4_F32)) return W4A4_ERR_INVALID_ARG;
+    for (const int kind : {a->post, a->pre})
+        if (kind < W4A4_NORM_NONE || kind > W4A4_NORM_LAYER) return W4A4_ERR_INVALID_ARG;
+    if (a->width < 8 || a->width % 8 != 0 || a->width > 16384) return W4A4_ERR_UNSUPPORTED_SHAPE;
+    if (a->rows == 0) return W4A4_OK;
+    if (!a->y || !a->r || !a->r_out) return W4A4_ERR_INVALID_ARG;
+    for (const void* p : {a->y, a->r, static_cast<const void*>(a->r_out), static_cast<const void*>(a->x), a->gate,
+                          a->post_gain, a->post_bias, a->pre_gain, a->pre_bias})
+        if (!aligned16(p)) return W4A4_ERR_MISALIGNED;
+    const int rs = a->res_dtype == W4A4_F32 ? 4 : 2;
+    if (!good_stride(a->y_stride, 2) || !good_stride(a->r_stride, rs) || !good_stride(a->r_out_stride, rs) ||
+        (a->x && !good_stride(a->x_stride, 2)) || (a->gate && !good_stride(a->gate_stride, 2)))
+        return W4A4_ERR_MISALIGNED;
+    if (a->y_stride < a->width || a->r_stride < a->width || a->r_out_stride < a->width ||
+        (a->x && a->x_stride < a->width) || (a->gate && a->rows_per_gate > 0 && a->gate_stride < a->width))
+        return W4A4_ERR_INVALID_ARG;
+    w4a4_status st = check_device();
+    if (st != W4A4_OK) return st;
+    launch_block_norm(*a, stream);
     return launch_status();
 }
 

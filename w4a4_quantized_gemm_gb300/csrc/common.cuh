@@ -216,4 +216,6 @@ w4a4_status w4a16_read_and_clear_status();   // bounded-wait status of the W4A16
 w4a4_status smtc_read_and_clear_status();    // bounded-wait status of the tcgen05 small-M kernel
 w4a4_status q_read_and_clear_status();       // bounded-wait status of the activation kernel
 w4a4_status fused_read_and_clear_status();   // bounded-wait status of the fused small-M linear
+w4a4_status append_read_and_clear_status();     // index status of the cache append
+w4a4_status attention_read_and_clear_status();  // index status of the paged attention
 }  // namespace w4a4

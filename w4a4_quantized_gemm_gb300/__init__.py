@@ -113,9 +113,9 @@ def _ptr(t):
     return ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
+def _stream(stream, device=None):
+    if stream is None:  # the handle itself: building a torch.cuda.Stream object takes 3 us, longer than a launch
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if device is None else device)
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
@@ -366,25 +366,22 @@ def _refuse(where: str, status: int = 1):
     raise W4A4Error(status, where)
 
 
+# A call's host time is mostly these checks (a tensor attribute takes 0.1 us and a launch 2), so each
+# reads an attribute once and anything the C side checks as well is left to it.
 def _rows(t, where: str, heads: int, dim: int, dtype, device: int):
-    """Pointer and strides of a [rows, heads, dim] tensor whose last dimension is contiguous."""
+    """Length, pointer and strides of a [rows, heads, dim] tensor whose last dimension is contiguous."""
     n, h, d = t.shape
     a, b, c = t.stride()
-    if h != heads or d != dim or t.dtype != dtype or t.get_device() != device or c != 1:
+    if h != heads or d != dim or c != 1 or t.dtype is not dtype or t.get_device() != device:
         _refuse(where)
     return n, t.data_ptr(), a, b
 
 
-def _ints(t, where: str, n: int, device: int) -> int:
-    if t.dtype != torch.int32 or t.get_device() != device or t.numel() != n or not t.is_contiguous():
-        _refuse(where)
-    return t.data_ptr()
-
-
 def _vector(t, where: str, n: int, dtype, device: int) -> int:
+    """Pointer of a contiguous tensor of n elements, or 0 for None."""
     if t is None:
         return 0
-    if t.dtype != dtype or t.get_device() != device or t.numel() != n or not t.is_contiguous():
+    if t.dtype is not dtype or t.numel() != n or t.get_device() != device or not t.is_contiguous():
         _refuse(where)
     return t.data_ptr()
 
@@ -453,27 +450,27 @@ def w4a4_kv_append(q, k, v, positions, cache, q_out, seqs=None, rope=None, q_gai
     t belongs to sequence t, negative: padding.  rope: fp32 [rows, 2, rot_dim / 2]
     (w4a4_rope_table)."""
     where = "w4a4_kv_append"
-    dtype, dim, dev = q.dtype, cache.head_dim, cache.device
+    dtype, dim, dev, kvh = q.dtype, cache.head_dim, cache.device, cache.kv_heads
     heads = q.shape[1]
     tokens, qp, q0, q1 = _rows(q, where, heads, dim, dtype, dev)
-    nk, kp, k0, k1 = _rows(k, where, cache.kv_heads, dim, dtype, dev)
-    nv, vp, v0, v1 = _rows(v, where, cache.kv_heads, dim, dtype, dev)
+    nk, kp, k0, k1 = _rows(k, where, kvh, dim, dtype, dev)
+    nv, vp, v0, v1 = _rows(v, where, kvh, dim, dtype, dev)
     no, op, o0, o1 = _rows(q_out, where, heads, dim, dtype, dev)
-    if nk != tokens or nv != tokens or no != tokens or dtype not in _DTYPE:
+    if not nk == nv == no == tokens or dtype not in _DTYPE:
         _refuse(where)
-    rp = rows = rot = 0
+    rp = rows = half = 0
     if rope is not None:
         rows, two, half = rope.shape
-        rot = 2 * half
-        rp = _vector(rope, where, rows * rot, torch.float32, dev)
+        rp = _vector(rope, where, 2 * rows * half, torch.float32, dev)
         if two != 2:
             _refuse(where)
-    args = _APPEND.pack(_APPEND.size, qp, kp, vp, op, _ints(positions, where, tokens, dev),
-                        0 if seqs is None else _ints(seqs, where, tokens, dev), rp,
-                        _vector(q_gain, where, dim, dtype, dev), _vector(k_gain, where, dim, dtype, dev),
-                        q0, q1, k0, k1, v0, v1, o0, o1, tokens, heads, _DTYPE[dtype], rows, rot,
-                        1 if interleaved else 0, eps, 0)
-    _check(lib().w4a4_kv_append(cache._struct, args, _stream(stream)), where)
+    args = _APPEND.pack(_APPEND.size, qp, kp, vp, op, _vector(positions, where, tokens, torch.int32, dev),
+                        _vector(seqs, where, tokens, torch.int32, dev), rp, _vector(q_gain, where, dim, dtype, dev),
+                        _vector(k_gain, where, dim, dtype, dev), q0, q1, k0, k1, v0, v1, o0, o1, tokens, heads,
+                        _DTYPE[dtype], rows, 2 * half, interleaved, eps, 0)
+    status = lib().w4a4_kv_append(cache._struct, args, _stream(stream, dev))
+    if status:
+        _refuse(where, status)
 
 
 def w4a4_paged_attention(q, cache, lengths, out, lse=None, scale=None, window: int = 0, workspace=None, stream=None):
@@ -491,9 +488,11 @@ def w4a4_paged_attention(q, cache, lengths, out, lse=None, scale=None, window: i
         _refuse(where)
     ws = cache.workspace(heads) if workspace is None else workspace
     args = _ATTENTION.pack(_ATTENTION.size, qp, op, _vector(lse, where, n * heads, torch.float32, dev),
-                           _ints(lengths, where, n, dev), ws.data_ptr(), ws.numel() * ws.element_size(),
+                           _vector(lengths, where, n, torch.int32, dev), ws.data_ptr(), ws.numel() * ws.element_size(),
                            q0, q1, o0, o1, dim ** -0.5 if scale is None else scale, heads, _DTYPE[dtype], window)
-    _check(lib().w4a4_paged_attention(cache._struct, args, _stream(stream)), where)
+    status = lib().w4a4_paged_attention(cache._struct, args, _stream(stream, dev))
+    if status:
+        _refuse(where, status)
 
 
 def w4a4_block_norm(y, r, x, r_out, gate=None, rows_per_gate: int = 0, scale: float = 1.0, post: int = NORM_RMS,
@@ -506,32 +505,36 @@ def w4a4_block_norm(y, r, x, r_out, gate=None, rows_per_gate: int = 0, scale: fl
     be r).  post, pre: NORM_NONE, NORM_RMS or NORM_LAYER.  gate: [width] or [gates, width], row m
     under gate row m // rows_per_gate (0: one row for all)."""
     where = "w4a4_block_norm"
-    dtype, dev = y.dtype, y.get_device()
-    rows, width = y.shape
-    for t in (r, r_out) if x is None else (r, r_out, x):
-        if t.shape != y.shape or t.stride(1) != 1 or t.get_device() != dev:
+    dtype, res, dev, shape = y.dtype, r.dtype, y.get_device(), y.shape
+    rows, width = shape
+
+    def stride(t, kind):
+        a, b = t.stride()
+        if b != 1 or t.dtype is not kind or t.shape != shape or t.get_device() != dev:
             _refuse(where)
-    if dtype not in _DTYPE or r.dtype not in _DTYPE or r_out.dtype != r.dtype or y.stride(1) != 1 or dev < 0:
+        return a
+
+    ys, rs, ros = stride(y, dtype), stride(r, res), stride(r_out, res)
+    if dtype not in _DTYPE or res not in _DTYPE or dev < 0:
         _refuse(where)
-    gp = gs = 0
+    gp = gs = xp = xs = 0
     if gate is not None:
-        gates = gate.numel() // width
-        need = -(-rows // rows_per_gate) if rows_per_gate > 0 else 1
-        if gate.dtype != dtype or gate.get_device() != dev or gate.shape[-1] != width or gate.stride(-1) != 1:
+        gs = gate.stride(0) if gate.dim() == 2 else width
+        gates, need = gate.numel() // width, -(-rows // rows_per_gate) if rows_per_gate > 0 else 1
+        if gate.dtype is not dtype or gate.get_device() != dev or gate.shape[-1] != width or gate.stride(-1) != 1 or \
+                gate.dim() > 2 or gates < need:
             _refuse(where)
-        if gate.dim() > 2 or gates < need:
-            _refuse(where)
-        gp, gs = gate.data_ptr(), gate.stride(0) if gate.dim() == 2 else width
-    xp = xs = 0
+        gp = gate.data_ptr()
     if x is not None:
-        if x.dtype != dtype:
-            _refuse(where)
-        xp, xs = x.data_ptr(), x.stride(0)
-    vec = [_vector(t, where, width, dtype, dev) for t in (post_gain, post_bias, pre_gain, pre_bias)]
-    args = _BLOCK_NORM.pack(_BLOCK_NORM.size, y.data_ptr(), r.data_ptr(), r_out.data_ptr(), xp, gp, *vec,
-                            y.stride(0), r.stride(0), r_out.stride(0), xs, gs, rows, width, rows_per_gate,
-                            _DTYPE[dtype], _DTYPE[r.dtype], post, pre, scale, eps, 0)
-    _check(lib().w4a4_block_norm(args, _stream(stream)), where)
+        xp, xs = x.data_ptr(), stride(x, dtype)
+    args = _BLOCK_NORM.pack(_BLOCK_NORM.size, y.data_ptr(), r.data_ptr(), r_out.data_ptr(), xp, gp,
+                            _vector(post_gain, where, width, dtype, dev), _vector(post_bias, where, width, dtype, dev),
+                            _vector(pre_gain, where, width, dtype, dev), _vector(pre_bias, where, width, dtype, dev),
+                            ys, rs, ros, xs, gs, rows, width, rows_per_gate, _DTYPE[dtype], _DTYPE[res], post, pre,
+                            scale, eps, 0)
+    status = lib().w4a4_block_norm(args, _stream(stream, dev))
+    if status:
+        _refuse(where, status)
 
 
 # ------------------------------------------------------------- layer helper

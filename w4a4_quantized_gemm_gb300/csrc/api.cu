@@ -14,6 +14,8 @@ namespace w4a4 {
 
 namespace {
 thread_local char t_dispatch[256] = "none";
+thread_local const char* t_format = nullptr;  // set_dispatch_ints: written out when it is asked for
+thread_local int t_numbers[8];
 int g_small_m_threshold = -1;  // -1: read W4A4_SMALL_M on first use
 constexpr int kStreamKDefault = 0;  // stream-K measured slower than split-K / round-robin on every layer shape
 constexpr int kDefaultSmallM = 32;  // M <= this -> weight-streaming kernel, else tcgen05 tiles (measured crossover: 32..48)
@@ -45,6 +47,8 @@ w4a4_status check_device() {
         cudaGetLastError();
         return W4A4_ERR_NO_DEVICE;
     }
+    static std::atomic<uint64_t> known{0};  // devices found to be sm_103
+    if (dev >= 0 && dev < 64 && (known.load(std::memory_order_relaxed) >> dev & 1)) return W4A4_OK;
     int major = 0, minor = 0;
     if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess) {
@@ -52,6 +56,7 @@ w4a4_status check_device() {
         return W4A4_ERR_NO_DEVICE;
     }
     if (major != 10 || minor != 3) return W4A4_ERR_NO_DEVICE;  // built for sm_103a only
+    if (dev >= 0 && dev < 64) known.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
     return W4A4_OK;
 }
 
@@ -113,7 +118,28 @@ void set_dispatch(const char* fmt, ...) {
     va_start(ap, fmt);
     vsnprintf(t_dispatch, sizeof(t_dispatch), fmt, ap);
     va_end(ap);
+    t_format = nullptr;
     if (log_enabled()) std::fprintf(stderr, "[w4a4] %s\n", t_dispatch);
+}
+
+namespace {
+void write_dispatch() {
+    if (!t_format) return;
+    const int* n = t_numbers;
+    std::snprintf(t_dispatch, sizeof(t_dispatch), t_format, n[0], n[1], n[2], n[3], n[4], n[5], n[6], n[7]);
+    t_format = nullptr;
+}
+}  // namespace
+
+void set_dispatch_ints(const char* fmt, std::initializer_list<int> numbers) {
+    t_format = fmt;
+    int i = 0;
+    for (const int n : numbers)
+        if (i < 8) t_numbers[i++] = n;
+    if (log_enabled()) {
+        write_dispatch();
+        std::fprintf(stderr, "[w4a4] %s\n", t_dispatch);
+    }
 }
 
 w4a4_status launch_status() {
@@ -210,7 +236,10 @@ const char* w4a4_status_string(int status) {
     }
 }
 
-const char* w4a4_last_dispatch(void) { return t_dispatch; }
+const char* w4a4_last_dispatch(void) {
+    write_dispatch();
+    return t_dispatch;
+}
 
 int w4a4_small_m_threshold(void) {
     std::lock_guard<std::mutex> lk(g_mu);

@@ -4,144 +4,328 @@
 // gate, add, norm) would move a row ten times; here y and r are read once and r' and
 // x written once, which is the HBM bound.
 //
-// One CTA per row.  A thread keeps CH chunks of eight elements of y and r in
-// registers (fp32) through both norms, so the reductions are the only exchanges:
-// each is a warp shuffle and one pass through shared memory.  The variance of a
-// LayerNorm is summed about the mean in a second reduction, not as a difference of
-// squares, so that a row with a large mean keeps its digits.
+// A CTA takes every grid-th row, a thread the same columns of each: CH chunks of eight
+// elements in registers (fp32) through both norms.  The gains, biases and a shared gate
+// are read once for all rows (packed, in registers), and the next row is requested
+// before this one is worked on.  The arithmetic is done on pairs (f32x2), and a missing
+// gain or bias is a vector of ones or zeros rather than a choice per element: one row
+// per CTA in scalar fp32 took 54 instructions an element, which were the bound.  At
+// 8192 x 4096 (bf16 on an fp32 stream, two LayerNorms, gate rows) 64 us, 6.3 TB/s of the
+// 403 MB that have to move; that first form 90 us.
+//
+// The statistics are the only exchanges: a warp's sums by shuffles, the warps' through
+// shared memory behind one barrier.  The variance of a LayerNorm is never a difference
+// of squares: a warp sums squares about its own mean, and the warps' moments are joined by
+//   mean = sum n_w mean_w / W,   var W = sum (v_w + n_w (mean_w - mean)^2),
+// so a row with a large mean keeps its digits without a second barrier.
+#include <atomic>
+
 #include "elem.cuh"
 #include "kernels.h"
+#include "tc_ptx.cuh"
 
 namespace w4a4 {
 namespace {
 
-// Sum over the CTA, the same bits in every thread (fixed order).  `slot` alternates
-// between consecutive calls, so one barrier per call separates its reads from the
-// next call's writes.
-template <int NT>
-__device__ __forceinline__ float block_sum(float v, float (*red)[NT / 32], int slot) {
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if constexpr (NT == 32) return v;
-    if ((threadIdx.x & 31) == 0) red[slot][threadIdx.x >> 5] = v;
-    __syncthreads();
-    float t = 0.f;
+    return v;
+}
+template <int N>  // over each group of N lanes (a power of two)
+__device__ __forceinline__ float group_sum(float v) {
 #pragma unroll
-    for (int w = 0; w < NT / 32; ++w) t += red[slot][w];
-    return t;
+    for (int o = N / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
 }
 
-// z -> norm(z) in place; chunk c of this thread is elements (c * NT + tid) * 8 ..
-// and takes part while that is below W.
+// Pairs of fp32 in a 64-bit register.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    return uint64_t(__float_as_uint(b)) << 32 | __float_as_uint(a);
+}
+__device__ __forceinline__ uint64_t both(float a) { return pair(a, a); }
+__device__ __forceinline__ float lo(uint64_t p) { return __uint_as_float(uint32_t(p)); }
+__device__ __forceinline__ float hi(uint64_t p) { return __uint_as_float(uint32_t(p >> 32)); }
+template <class T>
+__device__ __forceinline__ uint64_t up2(uint32_t w) {
+    const float2 f = T::up(w);
+    return pair(f.x, f.y);
+}
+template <class T>
+__device__ __forceinline__ uint32_t down2(uint64_t p) { return T::down(lo(p), hi(p)); }
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) {
+    return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+
+// 16 bytes that are read once: not kept in L1, where they would displace the vectors.
+__device__ __forceinline__ uint4 ld_once(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+// Eight fp32: one 32-byte access where the row allows it (two 16-byte ones at a stride
+// of 32 bytes would each touch half of every sector).
+__device__ __forceinline__ void ld_once8(const float* p, bool wide, uint4 (&v)[2]) {
+    if (wide)
+        asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+                     : "=r"(v[0].x), "=r"(v[0].y), "=r"(v[0].z), "=r"(v[0].w), "=r"(v[1].x), "=r"(v[1].y),
+                       "=r"(v[1].z), "=r"(v[1].w)
+                     : "l"(p)
+                     : "memory");
+    else
+        v[0] = ld_once(p), v[1] = ld_once(p + 4);
+}
+
+// A thread's chunks of a vector [W] of a 16-bit type; `fill` (two elements) where there
+// is none.  Held in registers for all rows, or read where they are used (CH > 2: too
+// many to hold).
 template <class T, int NT, int CH>
-__device__ __forceinline__ void normalise(float (&z)[CH][8], int kind, const void* gain, const void* bias, int W,
-                                          float eps, float (*red)[NT / 32], int& slot) {
+struct Vector {
+    static constexpr bool kHeld = CH <= 2;
+    const char* at;
+    uint32_t fill;
+    uint4 v[kHeld ? CH : 1];
+    __device__ __forceinline__ uint4 read(int c, int W) const {
+        const int k = (c * NT + threadIdx.x) * 8;
+        return at && k < W ? *reinterpret_cast<const uint4*>(at + 2 * k) : make_uint4(fill, fill, fill, fill);
+    }
+    __device__ __forceinline__ void init(const void* p, float missing, int W) {
+        at = static_cast<const char*>(p);
+        fill = T::down(missing, missing);
+        if constexpr (kHeld)
+#pragma unroll
+            for (int c = 0; c < CH; ++c) v[c] = read(c, W);
+    }
+    __device__ __forceinline__ uint4 get(int c, int W) {
+        if constexpr (kHeld) {
+            // opaque, or the compiler converts it once for all rows and holds twice the registers
+            asm volatile("" : "+r"(v[c].x), "+r"(v[c].y), "+r"(v[c].z), "+r"(v[c].w));
+            return v[c];
+        }
+        return read(c, W);
+    }
+};
+
+// z -> norm(z) in place; chunk c of this thread is elements (c * NT + tid) * 8 ..
+// and takes part while that is below W (the others are zero).  Every thread gets the
+// same statistics (fixed order).  LAYER: one of the row's norms is a LayerNorm (an
+// RMSNorm beside it takes the mean and the bias as zero); without it the mean, the
+// bias and their work are left out (fp16, 4096 x 8192: 52 us with them, 46 without).
+template <class T, int NT, int CH, bool LAYER>
+__device__ __forceinline__ void normalise(uint64_t (&z)[CH][4], int kind, Vector<T, NT, CH>& gain,
+                                          Vector<T, NT, CH>& bias, int W, float eps, float4 (&red)[NT / 32]) {
     if (kind == W4A4_NORM_NONE) return;
+    constexpr int kWarps = NT / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const float n = 1.f / float(W);
-    float mean = 0.f;
-    if (kind == W4A4_NORM_LAYER) {
-        float s = 0.f;
+    float mean = 0.f, held = 1.f;
+    if (LAYER && kind == W4A4_NORM_LAYER) {
+        int h = 0;  // elements of this warp that take part
+#pragma unroll
+        for (int c = 0; c < CH; ++c) h += min(256, max(0, W - (c * NT + warp * 32) * 8));
+        held = float(h);
+        uint64_t s = 0;
 #pragma unroll
         for (int c = 0; c < CH; ++c)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) s += z[c][j];
-        mean = block_sum<NT>(s, red, slot) * n;
-        slot ^= 1;
+            for (int i = 0; i < 4; ++i) s = tc::fadd2_b64(s, z[c][i]);
+        mean = warp_sum(lo(s) + hi(s)) / fmaxf(held, 1.f);
     }
-    float ss = 0.f;
+    uint64_t q = 0;
+    const uint64_t off = both(-mean);
 #pragma unroll
     for (int c = 0; c < CH; ++c)
-        if ((c * NT + int(threadIdx.x)) * 8 < W)
+        if (!LAYER || (c * NT + int(threadIdx.x)) * 8 < W)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) ss += (z[c][j] - mean) * (z[c][j] - mean);
-    const float inv = 1.f / sqrtf(block_sum<NT>(ss, red, slot) * n + eps);
-    slot ^= 1;
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-        const int k = (c * NT + threadIdx.x) * 8;
-        if (k >= W) continue;
-        float g[8], b[8];
-        if (gain) load8<T>(gain, k, g);
-        if (kind == W4A4_NORM_LAYER && bias) load8<T>(bias, k, b);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            float v = (z[c][j] - mean) * inv;
-            if (gain) v *= g[j];
-            if (kind == W4A4_NORM_LAYER && bias) v += b[j];
-            z[c][j] = v;
+            for (int i = 0; i < 4; ++i) {
+                const uint64_t d = LAYER ? tc::fadd2_b64(z[c][i], off) : z[c][i];
+                q = tc::ffma2_b64(d, d, q);
+            }
+    float v = warp_sum(lo(q) + hi(q));
+    if constexpr (kWarps > 1) {
+        if (lane == 0) red[warp] = make_float4(mean, held, v, mean * held);
+        __syncthreads();
+        // lane w of each kWarps takes warp w's moments: the same sums, in the same order, in all
+        const float4 of = red[lane % kWarps];
+        v = of.z;
+        if (LAYER && kind == W4A4_NORM_LAYER) {
+            mean = group_sum<kWarps>(of.w) * n;
+            v += of.y * (of.x - mean) * (of.x - mean);
         }
+        v = group_sum<kWarps>(v);
     }
-}
-
-template <class T, class R, int NT, int CH>
-__global__ void __launch_bounds__(NT) block_norm_kernel(const w4a4_block_norm_args a) {
-    __shared__ float red[2][NT / 32];
-    pdl_wait();
-    pdl_launch_dependents();
-    const int64_t m = blockIdx.x;
-    const int W = a.width;
-    const int64_t gate_at = a.rows_per_gate ? m / a.rows_per_gate * a.gate_stride : 0;
-    float y[CH][8], r[CH][8];
+    const uint64_t inv = both(rsqrtf(v * n + eps));  // rsqrtf: 2 ulp
+    const uint64_t less = both(-mean);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-        const int k = (c * NT + threadIdx.x) * 8;
-        if (k < W) {
-            load8<T>(a.y, m * a.y_stride + k, y[c]);
-            load8<R>(a.r, m * a.r_stride + k, r[c]);
+        const uint4 g = gain.get(c, W);
+        if constexpr (LAYER) {
+            const uint4 b = bias.get(c, W);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                z[c][i] = tc::ffma2_b64(tc::fmul2_b64(tc::fadd2_b64(z[c][i], less), inv), up2<T>(word(g, i)),
+                                        up2<T>(word(b, i)));
         } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) y[c][j] = r[c][j] = 0.f;
+            for (int i = 0; i < 4; ++i) z[c][i] = tc::fmul2_b64(tc::fmul2_b64(z[c][i], inv), up2<T>(word(g, i)));
         }
-    }
-    int slot = 0;
-    normalise<T, NT, CH>(y, a.post, a.post_gain, a.post_bias, W, a.eps, red, slot);
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-        const int k = (c * NT + threadIdx.x) * 8;
-        if (k >= W) continue;
-        float g[8];
-        if (a.gate) load8<T>(a.gate, gate_at + k, g);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) r[c][j] += a.scale * (a.gate ? g[j] * y[c][j] : y[c][j]);
-        store8<R>(a.r_out, m * a.r_out_stride + k, r[c]);
-    }
-    if (!a.x) return;
-    normalise<T, NT, CH>(r, a.pre, a.pre_gain, a.pre_bias, W, a.eps, red, slot);
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-        const int k = (c * NT + threadIdx.x) * 8;
-        if (k < W) store8<T>(a.x, m * a.x_stride + k, r[c]);
     }
 }
 
-template <class T, class R, int NT, int CH>
+template <class T, class R, int NT, int CH, bool LAYER>
+__global__ void __launch_bounds__(NT, CH == 2 ? 512 / NT : 1) block_norm_kernel(const w4a4_block_norm_args a) {
+    // a norm's partial sums; two sets that rows alternate between, so that a row's
+    // barriers separate its reads from the next use of the set
+    __shared__ float4 red[2][2][NT / 32];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int W = a.width;
+    const bool wide = R::kSize == 4 && ((reinterpret_cast<uintptr_t>(a.r) | reinterpret_cast<uintptr_t>(a.r_out)) & 31) == 0 &&
+                      ((a.r_stride | a.r_out_stride) & 7) == 0;
+    const bool row_gate = a.gate && a.rows_per_gate;
+    Vector<T, NT, CH> post_gain, post_bias, pre_gain, pre_bias, gate;
+    uint4 ny[CH], nr[CH][R::kSize / 2], ng[CH];  // the next row, as it is in memory
+#pragma unroll
+    for (int c = 0; c < CH; ++c)  // chunks past the row stay zero
+        ny[c] = ng[c] = nr[c][0] = nr[c][R::kSize / 2 - 1] = make_uint4(0, 0, 0, 0);
+    auto request = [&](uint32_t m) {
+        const char* y = static_cast<const char*>(a.y) + 2 * (m * a.y_stride);
+        const char* r = static_cast<const char*>(a.r) + R::kSize * (m * a.r_stride);
+        const char* gates = static_cast<const char*>(a.gate);
+        if (row_gate) gates += 2 * (m / uint32_t(a.rows_per_gate) * a.gate_stride);
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int k = (c * NT + threadIdx.x) * 8;
+            if (k >= W) continue;
+            ny[c] = ld_once(y + 2 * k);
+            if constexpr (R::kSize == 4)
+                ld_once8(reinterpret_cast<const float*>(r) + k, wide, nr[c]);
+            else
+                nr[c][0] = ld_once(r + 2 * k);
+            if (row_gate) ng[c] = *reinterpret_cast<const uint4*>(gates + 2 * k);
+        }
+    };
+    request(blockIdx.x);
+    post_gain.init(a.post_gain, 1.f, W);
+    post_bias.init(a.post == W4A4_NORM_LAYER ? a.post_bias : nullptr, 0.f, W);
+    pre_gain.init(a.pre_gain, 1.f, W);
+    pre_bias.init(a.pre == W4A4_NORM_LAYER ? a.pre_bias : nullptr, 0.f, W);
+    gate.init(row_gate ? nullptr : a.gate, 1.f, W);
+    const uint64_t scale = both(a.scale);
+    int set = 0;
+    const uint32_t rows = a.rows;
+    for (uint32_t m = blockIdx.x; m < rows; m += gridDim.x, set ^= 1) {
+        char* r_row = static_cast<char*>(a.r_out) + R::kSize * (m * a.r_out_stride);
+        char* x_row = static_cast<char*>(a.x) + 2 * (m * a.x_stride);
+        uint64_t y[CH][4], r[CH][4];
+        uint4 g[CH];
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                y[c][i] = up2<T>(word(ny[c], i));
+                if constexpr (R::kSize == 4)
+                    r[c][i] = uint64_t(word(nr[c][i / 2], i % 2 * 2 + 1)) << 32 | word(nr[c][i / 2], i % 2 * 2);
+                else
+                    r[c][i] = up2<R>(word(nr[c][0], i));
+            }
+            g[c] = ng[c];
+        }
+        if (m + gridDim.x < rows) request(m + gridDim.x);
+        normalise<T, NT, CH, LAYER>(y, a.post, post_gain, post_bias, W, a.eps, red[set][0]);
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int k = (c * NT + threadIdx.x) * 8;
+            if (LAYER || a.gate) {
+                if (!row_gate) g[c] = gate.get(c, W);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    r[c][i] = tc::ffma2_b64(tc::fmul2_b64(scale, up2<T>(word(g[c], i))), y[c][i], r[c][i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) r[c][i] = tc::ffma2_b64(scale, y[c][i], r[c][i]);
+            }
+            if (k < W) {
+                char* dst = r_row + R::kSize * k;
+                if constexpr (R::kSize == 4) {
+                    if (wide) {
+                        const uint32_t w[8] = {uint32_t(r[c][0]), uint32_t(r[c][0] >> 32), uint32_t(r[c][1]),
+                                               uint32_t(r[c][1] >> 32), uint32_t(r[c][2]), uint32_t(r[c][2] >> 32),
+                                               uint32_t(r[c][3]), uint32_t(r[c][3] >> 32)};
+                        tc::st_global_v8(dst, w);
+                    } else {
+                        reinterpret_cast<ulonglong2*>(dst)[0] = make_ulonglong2(r[c][0], r[c][1]);
+                        reinterpret_cast<ulonglong2*>(dst)[1] = make_ulonglong2(r[c][2], r[c][3]);
+                    }
+                } else {
+                    *reinterpret_cast<uint4*>(dst) =
+                        make_uint4(down2<R>(r[c][0]), down2<R>(r[c][1]), down2<R>(r[c][2]), down2<R>(r[c][3]));
+                }
+            } else {  // the rest of a row takes part in no statistics
+#pragma unroll
+                for (int i = 0; i < 4; ++i) r[c][i] = 0;
+            }
+        }
+        if (!a.x) continue;
+        normalise<T, NT, CH, LAYER>(r, a.pre, pre_gain, pre_bias, W, a.eps, red[set][1]);
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int k = (c * NT + threadIdx.x) * 8;
+            if (k < W)
+                *reinterpret_cast<uint4*>(x_row + 2 * k) =
+                    make_uint4(down2<T>(r[c][0]), down2<T>(r[c][1]), down2<T>(r[c][2]), down2<T>(r[c][3]));
+        }
+    }
+}
+
+template <class T, class R, int NT, int CH, bool LAYER>
 void launch_k(const w4a4_block_norm_args& a, cudaStream_t s) {
+    static std::atomic<int> per_sm{0};  // CTAs that an SM holds (registers), the same on every device
+    int n = per_sm.load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, block_norm_kernel<T, R, NT, CH, LAYER>, NT, 0) != cudaSuccess ||
+            n < 1)
+            n = 1;
+        per_sm.store(n, std::memory_order_relaxed);
+    }
+    const int full = n * device_sm_count();
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
     cfg.attrs = attr;
     cfg.numAttrs = add_pdl_attr(attr, 0);
-    cfg.gridDim = dim3(unsigned(a.rows));
+    cfg.gridDim = dim3(unsigned(a.rows < full ? a.rows : full));
     cfg.blockDim = dim3(NT);
     cfg.stream = s;
-    cudaLaunchKernelEx(&cfg, block_norm_kernel<T, R, NT, CH>, a);
-    set_dispatch("block_norm rows=%d width=%d threads=%d chunks/thread=%d", a.rows, a.width, NT, CH);
+    cudaLaunchKernelEx(&cfg, block_norm_kernel<T, R, NT, CH, LAYER>, a);
+    set_dispatch_ints("block_norm rows=%d width=%d threads=%d chunks/thread=%d grid=%d",
+                      {a.rows, a.width, NT, CH, int(cfg.gridDim.x)});
+}
+
+template <class T, class R, bool LAYER>
+void launch_l(const w4a4_block_norm_args& a, cudaStream_t s) {
+    const int chunks = a.width / 8;
+    if (chunks <= 32)
+        launch_k<T, R, 32, 1, LAYER>(a, s);
+    else if (chunks <= 64)
+        launch_k<T, R, 64, 1, LAYER>(a, s);
+    else if (chunks <= 128)
+        launch_k<T, R, 128, 1, LAYER>(a, s);
+    else if (chunks <= 256)
+        launch_k<T, R, 128, 2, LAYER>(a, s);
+    else if (chunks <= 512)
+        launch_k<T, R, 256, 2, LAYER>(a, s);
+    else if (chunks <= 1024)
+        launch_k<T, R, 512, 2, LAYER>(a, s);
+    else
+        launch_k<T, R, 512, 4, LAYER>(a, s);
 }
 
 template <class T, class R>
 void launch_r(const w4a4_block_norm_args& a, cudaStream_t s) {
-    const int chunks = a.width / 8;
-    if (chunks <= 32)
-        launch_k<T, R, 32, 1>(a, s);
-    else if (chunks <= 128)
-        launch_k<T, R, 128, 1>(a, s);
-    else if (chunks <= 256)
-        launch_k<T, R, 256, 1>(a, s);
-    else if (chunks <= 512)
-        launch_k<T, R, 256, 2>(a, s);
-    else if (chunks <= 1024)
-        launch_k<T, R, 512, 2>(a, s);
-    else
-        launch_k<T, R, 512, 4>(a, s);
+    a.post == W4A4_NORM_LAYER || a.pre == W4A4_NORM_LAYER ? launch_l<T, R, true>(a, s) : launch_l<T, R, false>(a, s);
 }
 
 }  // namespace

@@ -6,6 +6,7 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <stdint.h>
+#include <initializer_list>
 
 #include "../../include/w4a4.h"
 
@@ -203,6 +204,9 @@ __device__ __forceinline__ uint4 ldg_nc_v4(const void* p) {
 // ---- host-side launch helpers (implemented in api.cu) ----------------------
 namespace w4a4 {
 void set_dispatch(const char* fmt, ...);
+// The same for a text of at most eight ints, written out only when it is read: the
+// formatting takes about a fifth of a short launch's host time.
+void set_dispatch_ints(const char* fmt, std::initializer_list<int> numbers);
 w4a4_status launch_status();  // maps cudaGetLastError() to a status
 int device_sm_count();        // multiprocessors of the current device (cached)
 // Appends the programmatic-stream-serialisation attribute (the launch may

@@ -73,9 +73,9 @@ __device__ __forceinline__ void store8(void* row, int64_t i, const float (&x)[8]
     }
 }
 
-// Reads and clears a kernel's index status word (host).
+// Reads and clears the status a kernel left in its device word (host).
 template <class Symbol>
-w4a4_status take_index_status(const Symbol& word) {
+w4a4_status take_status_word(const Symbol& word) {
     int v = 0;
     if (cudaMemcpyFromSymbol(&v, word, sizeof(int)) != cudaSuccess) {
         cudaGetLastError();
@@ -84,7 +84,7 @@ w4a4_status take_index_status(const Symbol& word) {
     if (v != 0) {
         const int zero = 0;
         cudaMemcpyToSymbol(word, &zero, sizeof(int));
-        return W4A4_ERR_INDEX;
+        return w4a4_status(v);
     }
     return W4A4_OK;
 }

@@ -6,24 +6,31 @@
 // Every cached byte is read once and used for 2 G flops, far below what the matrix
 // units need to be the limit, so the bound is HBM traffic and the kernel is built to
 // keep copies in flight:
-//  * The work is cut into units of 64 tokens of one (sequence, key-value head,
-//    chunk of up to 16 of its query heads), in that order, and each CTA of a grid that
-//    fills the GPU once takes an equal, contiguous run of units, whatever the lengths.
-//    The lengths are read on the device, so a captured graph serves growing sequences.
-//  * A CTA is four warps; a warp takes 16 tokens of each unit and runs on its own: it
-//    copies its key and value rows into a ring of stages in shared memory (16-byte
-//    asynchronous copies, rows looked up in the page table one stage ahead of the
-//    copy) and keeps a running maximum, sum and output in registers (one pass).
-//    Only the end of a (sequence, head) synchronises the warps.
-//  * Scores are m16n8k16 warp MMAs with the query heads as rows: at one token per
-//    sequence a tile has at most 16 useful rows, so the 128-row tcgen05 tile would
-//    stand idle and cost an extra trip through tensor memory.
+//  * The work is cut into units: `span` tokens of one (sequence, group of key-value
+//    heads, chunk of up to 16 of their query heads).  Each CTA of a grid that fills the
+//    GPU once takes an equal, contiguous run of units, whatever the lengths.  The
+//    lengths are read on the device, so a captured graph serves growing sequences.
+//  * A CTA is four warps that share a unit out: 16 or 32 tokens of one key-value head
+//    each (one head and consecutive tokens, or several heads and the same tokens, see
+//    `together`).  A warp runs on its own: it copies its key and value rows into a ring
+//    of stages in shared memory, the page table looked up one stage ahead of the copy,
+//    and keeps a running maximum, sum and output in registers (one pass).  Only the end
+//    of a (sequence, head) synchronises the warps.
+//  * Rows of 256 bytes and more are fetched by one bulk copy each, shorter ones by
+//    16-byte asynchronous copies: alone, streaming 4 GB, bulk copies reach 7.1 TB/s with
+//    256-byte rows (16-byte copies: 6.8) but start about 37 G rows a second, so 4.7
+//    (6.7) with 128-byte and 2.8 (6.1) with 64-byte rows.
+//  * Scores are m16n8k16 warp MMAs with 16 tokens as rows and 8 query heads as columns:
+//    at one token per sequence there are G <= 16 useful columns, so the 128-row tcgen05
+//    tile would stand idle.  The scores' transposed fragments are the probabilities
+//    operand of the second product, whose rows are the head's elements.
 //  * A run that ends inside a (sequence, head) leaves its maximum, sum and output in
 //    the workspace; the CTA that comes last joins the parts in token order.
 #include <atomic>
 
 #include "elem.cuh"
 #include "kernels.h"
+#include "tc_ptx.cuh"
 
 namespace w4a4 {
 namespace {
@@ -31,31 +38,36 @@ namespace {
 __device__ int g_attention_status = 0;
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
-constexpr int kKeys = 16;               // tokens of a unit that a warp takes
-constexpr int kUnit = kWarps * kKeys;   // tokens of a unit
-constexpr int kRows = 16;               // query heads of a chunk (rows of the MMA)
-constexpr int kMaxCtas = 320;           // CTAs of a launch at most (two per SM)
+constexpr int kChunk = 16;              // query heads of a chunk
+constexpr int kPartRows = 32;           // rows of a part in the workspace
+constexpr int kMaxCtas = 480;           // CTAs of a launch at most (three per SM)
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 enum Cache { kF16, kBF16, kE4M3 };
 
-// Shared-memory plan of one head dimension and cache type.  A row is padded to an
-// odd number of 16-byte pieces: the eight rows of an ldmatrix then lie in different
-// banks.   The rings take
-// what two CTAs per SM leave (one at D = 256 of a 16-bit type).
-template <int D, int CT, bool WIDE>
+// Shared-memory plan of one head dimension, cache type and number NT of 8-head column
+// tiles.  A row is padded to an odd number of 16-byte pieces: the eight rows of an
+// ldmatrix then lie in different banks.  The stage that a warp has just used also
+// holds its output when the warps are joined.
+template <int D, int CT, int NT>
 struct Plan {
     static constexpr int kSize = CT == kE4M3 ? 1 : 2;
-    static constexpr int kChunks = D * kSize / 16;                  // 16-byte pieces of a row
-    static constexpr int kRow = (kChunks | 1) * 16;                 // bytes of a row in shared memory
-    static constexpr int kStage = 2 * kKeys * kRow;                 // keys, then values
-    static constexpr int kPerSM = kStage > 10000 ? 1 : 2;           // CTAs per SM
-    static constexpr int kOutRows = WIDE ? 16 : 8;
-    static constexpr int kMerge = 2 * kOutRows * D * 4;             // two warps' outputs
+    static constexpr int kRowBytes = D * kSize;
+    static constexpr bool kBulk = kRowBytes >= 512;
+    static constexpr int kPieces = kRowBytes / 16;
+    static constexpr int kRow = (kPieces | 1) * 16;                 // bytes of a row in shared memory
+    // Tokens of a warp's step: 32 where a row is short, to halve the steps' fixed cost
+    static constexpr int kTokens = CT == kE4M3 || D == 64 ? 32 : 16;
+    static constexpr int kStage = 2 * kTokens * kRow;               // keys, then values
+    static constexpr int kPerSM = kStage > 10000 ? 1 : kStage < 6000 ? 3 : 2;  // CTAs
     static constexpr int kRoom = 228 * 1024 / kPerSM - 1280;        // of an SM, less 1 KB a CTA and the static part
-    static constexpr int kStages = (kRoom - kMerge - 2 * kWarps * kRows * 4) / (kWarps * (kStage + 4));
+    static constexpr int kFixed = 2 * kWarps * kChunk * 4;          // the warps' maxima and sums
+    static constexpr int kStages = (kRoom - kFixed) / (kWarps * (kStage + 16));
+    static constexpr int kOutRow = D + 4;                           // floats of a joined row
     static constexpr int kRing = kWarps * kStages * kStage;
-    static constexpr int kBytes = kRing + kMerge + (2 * kWarps * kRows + kWarps * kStages) * 4;
+    static constexpr int kBytes = kRing + kFixed + kWarps * kStages * 16;
     static_assert(kStages >= 2 && kBytes <= 227 * 1024 - 256, "shared memory");
+    static_assert(8 * NT * kOutRow * 4 <= kStage, "a stage holds a warp's output");
 };
 
 struct Args {
@@ -65,10 +77,13 @@ struct Args {
     float* lse;
     const int32_t* lengths;
     int32_t* arrived;  // [seqs][heads] parts that have arrived; zero between calls
-    float* parts;      // [2 * CTAs][kRows * D outputs, kRows maxima, kRows sums]
+    float* parts;      // [2 * CTAs][kPartRows * D outputs, kPartRows maxima, kPartRows sums]
     int64_t q_token, q_head, o_token, o_head;
     float scale_log2;
-    int q_heads, group, chunks, heads, window;  // heads = kv_heads * chunks
+    int q_heads, group, chunks, window;
+    int together;  // key-value heads of a unit: 1, 2 or 4
+    int heads;     // (kv_heads / together) * chunks: head groups of a sequence
+    int span;      // tokens of a unit
     bool q_bf16;
 };
 
@@ -83,6 +98,11 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr)
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr)
                  : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {  // of 16-bit elements, over the warp
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(d) : "r"(a));
+    return d;
 }
 __device__ __forceinline__ void mma_bf16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -109,9 +129,13 @@ __device__ __forceinline__ float exp2_approx(float x) {  // 2 ulp; 2^-inf = 0
     asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
     return y;
 }
-// 16 bytes global -> shared; `bytes` of them (0 or 16) are read, the rest is zero.
-__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, int bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+__device__ __forceinline__ float ref_of(float top) {  // what is subtracted: nothing while every score is -inf
+    return top == -INFINITY ? 0.f : top;
+}
+__device__ __forceinline__ int add_acq_rel(int32_t* p, int v) {
+    int old;
+    asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], %2;\n" : "=r"(old) : "l"(p), "r"(v) : "memory");
+    return old;
 }
 
 // Tokens of sequence b that take part: [lo, lo + n).
@@ -122,12 +146,12 @@ __device__ __forceinline__ void range_of(const Args& A, int b, int& lo, int& n) 
     n = len - lo;
 }
 
-// A place in the sequence of units: tile `tile` of (sequence b, head chunk hc).
+// A place in the sequence of units: tile `tile` of (sequence b, head group hc).
 struct Cursor {
     int b, hc, tile, tiles, lo, n;
     __device__ __forceinline__ void enter(const Args& A) {
         range_of(A, b, lo, n);
-        tiles = (n + kUnit - 1) / kUnit;
+        tiles = (n + A.span - 1) / A.span;
     }
     __device__ __forceinline__ void advance(const Args& A) {  // to the next unit, if there is one
         if (++tile < tiles) return;
@@ -151,26 +175,30 @@ __device__ __forceinline__ float row_shift(float top) {
     return exp2f(float(13 - e));
 }
 
-template <int D, int CT, bool WIDE>
-__global__ void __launch_bounds__(kThreads, Plan<D, CT, WIDE>::kPerSM) paged_attention_kernel(const Args A) {
-    using P = Plan<D, CT, WIDE>;
+template <int D, int CT, int NT>
+__global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_attention_kernel(const Args A) {
+    using P = Plan<D, CT, NT>;
+    constexpr int kTokens = P::kTokens, kSubs = kTokens / 16, kSteps = D / 16;
     extern __shared__ __align__(128) uint8_t smem[];
-    float* merge = reinterpret_cast<float*>(smem + P::kRing);
-    float* warp_max = merge + P::kMerge / 4;        // [kWarps][kRows]
-    float* warp_sum = warp_max + kWarps * kRows;    // [kWarps][kRows]
-    uint32_t* masks = reinterpret_cast<uint32_t*>(warp_sum + kWarps * kRows);  // [kWarps][kStages]
+    float* warp_max = reinterpret_cast<float*>(smem + P::kRing);  // [kWarps][kChunk]
+    float* warp_sum = warp_max + kWarps * kChunk;                 // [kWarps][kChunk]
+    uint64_t* bars = reinterpret_cast<uint64_t*>(warp_sum + kWarps * kChunk);  // [kWarps][kStages]
+    uint32_t* masks = reinterpret_cast<uint32_t*>(bars + kWarps * P::kStages);  // [kWarps][kStages]
     __shared__ int64_t scan[kWarps];
-    __shared__ int64_t s_prefix, s_total;
-    __shared__ int s_seq, s_last;
+    __shared__ int64_t s_prefix;
+    __shared__ int s_seq, s_last, s_abort;
 
-    pdl_wait();
-    pdl_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int quad = lane >> 2, in_quad = lane & 3;
+    if (P::kBulk && lane < P::kStages) tc::mbar_init(smem_u32(bars + warp * P::kStages + lane), 1);
+    if (P::kBulk) tc::fence_mbar_init();
+    if (tid == 0) s_abort = 0;
+    pdl_wait();
+    pdl_launch_dependents();
     const int B = A.c.seqs;
 
     // ---- this CTA's run of units: a scan over the sequences' tile counts
-    int64_t first, count, total;
+    int64_t first, count, total, ctas;
     Cursor at;
     int64_t seq_tiles;  // tiles of the sequences before at.b
     {
@@ -183,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, WIDE>::kPerSM) paged_att
             bad |= len < 0 || len > A.c.max_pages * A.c.page_size;
             int lo, n;
             range_of(A, b, lo, n);
-            mine += (n + kUnit - 1) / kUnit;
+            mine += (n + A.span - 1) / A.span;
         }
         if (bad && blockIdx.x == 0) atomicExch(&g_attention_status, int(W4A4_ERR_INDEX));
         int64_t upto = mine;
@@ -194,11 +222,14 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, WIDE>::kPerSM) paged_att
         }
         if (lane == 31) scan[warp] = upto;
         __syncthreads();
-        for (int w = 0; w < warp; ++w) upto += scan[w];
-        if (tid == kThreads - 1) s_total = upto;
-        __syncthreads();
-        total = s_total * A.heads;
-        const int64_t ctas = min(int64_t(gridDim.x), total);
+        total = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) upto += scan[w];
+            total += scan[w];
+        }
+        total *= A.heads;
+        ctas = min(int64_t(gridDim.x), total);
         // sequences without tokens: zeros, from whichever CTA their number falls to
         for (int b = blockIdx.x; b < B; b += gridDim.x) {
             int lo, n;
@@ -221,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, WIDE>::kPerSM) paged_att
             for (int b = b0; b < b1; ++b) {
                 int lo, n;
                 range_of(A, b, lo, n);
-                const int t = (n + kUnit - 1) / kUnit;
+                const int t = (n + A.span - 1) / A.span;
                 if (tile < before + t) {
                     s_seq = b;
                     s_prefix = before;
@@ -238,17 +269,20 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, WIDE>::kPerSM) paged_att
         at.hc = int(in / at.tiles);
         at.tile = int(in - int64_t(at.hc) * at.tiles);
     }
-    const int64_t ctas = min(int64_t(gridDim.x), total);
 
     // ---- the warp's ring of stages
-    uint8_t* ring = smem + warp * P::kStages * P::kStage;
-    const uint32_t ring_addr = smem_u32(ring);
+    const int sharers = kWarps / A.together;  // warps of a key-value head
+    const int my_head = warp / sharers, my_tokens = (warp % sharers) * kTokens;
+    auto kv_head = [&](int hc) { return hc / A.chunks * A.together + my_head; };
+    const uint32_t ring = smem_u32(smem) + warp * P::kStages * P::kStage;
+    uint32_t* my_masks = masks + warp * P::kStages;
+    const uint32_t my_bars = smem_u32(bars + warp * P::kStages);
     Cursor put = at;
     int64_t to_put = count;
-    int page = 0, slot = 0;  // of token lane % 16 of the next unit to copy
-    bool in_range = false;
+    int page = 0, slot = 0;  // of token lane % kTokens of the next unit to copy
+    bool in_range = false, dead = false;
     auto look_up = [&] {
-        const int j = put.tile * kUnit + warp * kKeys + (lane & 15);
+        const int j = put.tile * A.span + my_tokens + (lane & (kTokens - 1));
         in_range = to_put > 0 && j < put.n;
         if (in_range) {
             const int tok = put.lo + j, p = tok / A.c.page_size;
@@ -257,75 +291,94 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, WIDE>::kPerSM) paged_att
         }
     };
     auto copy_unit = [&](int stage) {
-        const bool ok = in_range && page >= 0 && page < A.c.pages;
-        if (in_range && !ok) atomicExch(&g_attention_status, int(W4A4_ERR_INDEX));
-        const uint32_t mask = __ballot_sync(0xffffffffu, ok) & 0xffffu;
-        if (lane == 0) masks[warp * P::kStages + stage] = mask;
-        if (mask) {
-            const int kvh = put.hc / A.chunks;
-            // lanes 0-15 address the keys of their token, lanes 16-31 the values
-            const bool keys = lane < 16;
+        const bool ok = in_range && page >= 0 && page < A.c.pages && !dead;
+        if (in_range && !ok && !dead) atomicExch(&g_attention_status, int(W4A4_ERR_INDEX));
+        const uint32_t mask = __ballot_sync(0xffffffffu, ok) & (kTokens == 32 ? 0xffffffffu : 0xffffu);
+        if (lane == 0) my_masks[stage] = mask;
+        const uint32_t dst = ring + stage * P::kStage;
+        const int kvh = kv_head(put.hc);
+        auto row_of = [&](bool keys) {
             const int64_t off = !ok ? 0
                                 : keys ? page * A.c.k_page_stride + slot * A.c.k_token_stride + kvh * A.c.k_head_stride
                                        : page * A.c.v_page_stride + slot * A.c.v_token_stride + kvh * A.c.v_head_stride;
-            const char* row = static_cast<const char*>(keys ? A.c.k : A.c.v) + off * P::kSize;
-            const uint32_t dst = ring_addr + stage * P::kStage;
+            return static_cast<const char*>(keys ? A.c.k : A.c.v) + off * P::kSize;
+        };
+        if constexpr (P::kBulk) {
+            const uint32_t bar = my_bars + stage * 8;
+            if (lane == 0) tc::mbar_expect_tx(bar, __popc(mask) * 2 * P::kRowBytes);
+            __syncwarp();
+            // a value row without a token is multiplied by a zero probability: it must be finite
+            auto clear = [&](uint32_t row) {
+                for (int i = 0; i < P::kRowBytes; i += 16)
+                    asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};\n" ::"r"(row + i), "r"(0) : "memory");
+                tc::fence_proxy_async_smem();
+            };
+            if constexpr (kTokens == 32) {
+                const uint32_t row = dst + lane * P::kRow;
+                if (ok) {
+                    tc::bulk_g2s(row, row_of(true), P::kRowBytes, bar);
+                    tc::bulk_g2s(row + kTokens * P::kRow, row_of(false), P::kRowBytes, bar);
+                } else if (mask) {
+                    clear(row + kTokens * P::kRow);
+                }
+            } else {  // lanes 0-15 the keys of their token, lanes 16-31 the values
+                if (ok)
+                    tc::bulk_g2s(dst + lane * P::kRow, row_of(lane < 16), P::kRowBytes, bar);
+                else if (mask && lane >= 16)
+                    clear(dst + lane * P::kRow);
+            }
+        } else {
+            if (mask) {
+                const char* mine = row_of(kTokens == 32 || lane < 16);
+                const char* other = kTokens == 32 ? row_of(false) : mine;
 #pragma unroll
-            for (int i = 0; i < P::kChunks; ++i) {  // 32 rows of kChunks pieces, a warp's width at a time
-                const int piece = i * 32 + lane, r = piece / P::kChunks, c = piece % P::kChunks;
-                const char* src = reinterpret_cast<const char*>(
-                    __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row), r));
-                cp_async16_zfill(dst + r * P::kRow + c * 16, src + c * 16, (mask >> (r & 15) & 1) * 16);
+                for (int i = 0; i < 2 * kTokens * P::kPieces / 32; ++i) {  // a warp's width of pieces at a time
+                    const int piece = i * 32 + lane, r = piece / P::kPieces, c = piece % P::kPieces;
+                    const char* from = kTokens == 32 && i >= P::kPieces ? other : mine;
+                    const char* src = reinterpret_cast<const char*>(
+                        __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(from), r & 31));
+                    tc::cp_async16_zfill(dst + r * P::kRow + c * 16, src + c * 16,
+                                         (mask >> (r & (kTokens - 1)) & 1) * 16);
+                }
             }
         }
-        if (to_put > 0) {
-            --to_put;
-            if (to_put > 0) put.advance(A);
-            look_up();
-        }
+        if (--to_put > 0) put.advance(A);
+        look_up();
     };
     look_up();
+    __syncwarp();
 #pragma unroll
     for (int s = 0; s < P::kStages - 1; ++s) {
         if (to_put > 0) copy_unit(s);
-        cp_async_commit();
+        if (!P::kBulk) cp_async_commit();
     }
 
-    // ---- running softmax of this warp's tokens for the chunk's heads: rows quad and
-    // quad + 8 (WIDE) of the tile; out[t] are the MMA accumulators of 8 columns each
-    constexpr int kSteps = D / 16;
-    uint32_t qf[kSteps][WIDE ? 4 : 2];
-    float out[D / 8][4];
-    float top[2], sum[2], factor[2];
+    // ---- running softmax of this warp's tokens: columns 8 t + 2 (lane % 4) + {0, 1} are
+    // query heads; out[m][t] is rows (elements of the head) 16 m + quad and + 8
+    uint32_t qf[kSteps][NT][2];
+    float out[kSteps][NT][4];
+    float top[NT][2], sum[NT][2], factor[NT][2];
     int rows = 0;
     bool fresh = true;
-
-    int stage = 0;
+    int stage = 0, parity = 0;
     for (int64_t it = 0; it < count; ++it) {
-        const int fill = stage == 0 ? P::kStages - 1 : stage - 1;
-        if (to_put > 0) copy_unit(fill);
-        cp_async_commit();
+        if (to_put > 0) copy_unit(stage == 0 ? P::kStages - 1 : stage - 1);
+        if (!P::kBulk) cp_async_commit();
 
-        const int kvh = at.hc / A.chunks, row0 = kvh * A.group + (at.hc - kvh * A.chunks) * kRows;
+        const int kvh = kv_head(at.hc), in_group = at.hc % A.chunks * kChunk;
+        const int row0 = kvh * A.group + in_group;  // this warp's first query head
         if (fresh) {
             fresh = false;
-            rows = min(kRows, (kvh + 1) * A.group - row0);
-#pragma unroll
-            for (int t = 0; t < D / 8; ++t)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) out[t][j] = 0.f;
+            rows = min(kChunk, A.group - in_group);
             const float ks = CT == kE4M3 && A.c.k_scale ? A.c.k_scale[kvh] : 1.f;
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                top[half] = -INFINITY, sum[half] = 0.f;
-                if (half == 1 && !WIDE) continue;
-                const int row = quad + 8 * half;
+            for (int t = 0; t < NT; ++t) {
+                const int row = 8 * t + quad;
                 const char* src = static_cast<const char*>(A.q) + 2 * (at.b * A.q_token + (row0 + row) * A.q_head);
-                float shift = 1.f;
 #pragma unroll
                 for (int s = 0; s < kSteps; ++s) {
-                    // The MMA's columns 2 (lane % 4) + {0, 1} and those + 8 stand for these
-                    // elements; E4M3 rows come four consecutive elements to a lane, so
+                    // The MMA's k-columns 2 (lane % 4) + {0, 1} and those + 8 stand for these
+                    // elements; E4M3 keys come four consecutive elements to a lane, so
                     // there both pairs are taken from four consecutive ones.
                     const int e = CT == kE4M3 ? 16 * s + 4 * in_quad : 16 * s + 2 * in_quad;
                     uint32_t lo = 0, hi = 0;
@@ -333,16 +386,16 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, WIDE>::kPerSM) paged_att
                         lo = *reinterpret_cast<const uint32_t*>(src + 2 * e);
                         hi = *reinterpret_cast<const uint32_t*>(src + 2 * (e + (CT == kE4M3 ? 2 : 8)));
                     }
-                    qf[s][WIDE ? half : 0] = lo;
-                    qf[s][WIDE ? 2 + half : 1] = hi;
+                    qf[s][t][0] = lo, qf[s][t][1] = hi;
                 }
+                float shift = 1.f;
                 if (CT == kE4M3 && A.q_bf16) {
                     float big = 0.f;
 #pragma unroll
                     for (int s = 0; s < kSteps; ++s)
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            const float2 f = BF16::up(qf[s][WIDE ? 2 * i + half : i]);
+                            const float2 f = BF16::up(qf[s][t][i]);
                             big = fmaxf(big, fmaxf(fabsf(f.x), fabsf(f.y)));
                         }
                     big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
@@ -352,266 +405,311 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, WIDE>::kPerSM) paged_att
                     for (int s = 0; s < kSteps; ++s)
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            uint32_t& w = qf[s][WIDE ? 2 * i + half : i];
-                            const float2 f = BF16::up(w);
-                            w = F16::down(f.x * shift, f.y * shift);
+                            const float2 f = BF16::up(qf[s][t][i]);
+                            qf[s][t][i] = F16::down(f.x * shift, f.y * shift);
                         }
                 }
-                factor[half] = A.scale_log2 * ks / shift;
+                const float mine = A.scale_log2 * ks / shift;  // of head quad; the scores' columns are other heads
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    factor[t][j] = CT == kE4M3 ? __shfl_sync(0xffffffffu, mine, (2 * in_quad + j) * 4) : mine;
+                    top[t][j] = -INFINITY, sum[t][j] = 0.f;
+                }
+#pragma unroll
+                for (int m = 0; m < kSteps; ++m)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) out[m][t][j] = 0.f;
             }
         }
 
-        cp_async_wait<P::kStages - 1>();
-        __syncwarp();
-        const uint32_t mask = masks[warp * P::kStages + stage];
+        if constexpr (P::kBulk) {
+            __syncwarp();
+            if (!tc::warp_wait_parity(my_bars + stage * 8, parity, &s_abort, kWaitLimitNs)) {
+                if (lane == 0) {
+                    s_abort = 1;
+                    atomicExch(&g_attention_status, int(W4A4_ERR_TIMEOUT));
+                }
+                dead = true;
+            }
+        } else {
+            cp_async_wait<P::kStages - 1>();
+            __syncwarp();
+        }
+        const uint32_t mask = my_masks[stage];
+        const uint32_t keys = ring + stage * P::kStage, values = keys + kTokens * P::kRow;
         if (mask) {
-            const uint32_t keys = ring_addr + stage * P::kStage, values = keys + kKeys * P::kRow;
-            float s[2][4] = {};  // scores of tokens 0-7 and 8-15
-            if constexpr (CT == kE4M3) {
-                // an 8x8 b16 matrix is 8 tokens x 16 E4M3 elements: one k-step
-                const uint32_t base = keys + ((lane & 7) + (lane & 8)) * P::kRow + (lane >> 4) * 16;
+            float s[kSubs][NT][4];  // tokens 16 u + quad (two heads), then + 8
 #pragma unroll
-                for (int st = 0; st < kSteps; st += 2) {
-                    uint32_t r[4];
-                    ldmatrix4(r, base + st * 16);
+            for (int u = 0; u < kSubs; ++u) {
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const uint32_t a[4] = {qf[st + u][0], WIDE ? qf[st + u][1] : 0u, qf[st + u][WIDE ? 2 : 1],
-                                               WIDE ? qf[st + u][3 % (WIDE ? 4 : 2)] : 0u};
+                for (int t = 0; t < NT; ++t)
 #pragma unroll
-                        for (int t = 0; t < 2; ++t)
-                            mma<CT>(s[t], a, e4m3x2_to_f16x2(r[2 * u + t] & 0xffffu), e4m3x2_to_f16x2(r[2 * u + t] >> 16));
-                    }
-                }
-            } else {
-                const uint32_t base = keys + ((lane & 7) + (lane >> 4) * 8) * P::kRow + (lane >> 3 & 1) * 16;
-#pragma unroll
-                for (int st = 0; st < kSteps; ++st) {
-                    uint32_t r[4];
-                    ldmatrix4(r, base + st * 32);
-                    const uint32_t a[4] = {qf[st][0], WIDE ? qf[st][1] : 0u, qf[st][WIDE ? 2 : 1],
-                                           WIDE ? qf[st][3 % (WIDE ? 4 : 2)] : 0u};
-                    mma<CT>(s[0], a, r[0], r[1]);
-                    mma<CT>(s[1], a, r[2], r[3]);
-                }
-            }
-            uint32_t pf[4] = {0u, 0u, 0u, 0u};  // probabilities as the A operand
-#pragma unroll
-            for (int half = 0; half < (WIDE ? 2 : 1); ++half) {
-                float mx = -INFINITY;
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        float& v = s[t][2 * half + j];
-                        v = mask >> (8 * t + 2 * in_quad + j) & 1 ? v * factor[half] : -INFINITY;
-                        mx = fmaxf(mx, v);
-                    }
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                const float now = fmaxf(top[half], mx);
-                const float ref = now == -INFINITY ? 0.f : now;  // all scores -inf so far: nothing, not NaN
-                const float fade = exp2_approx(top[half] - ref);
-                top[half] = now;
-                float add = 0.f;
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const float a = exp2_approx(s[t][2 * half] - ref), b = exp2_approx(s[t][2 * half + 1] - ref);
-                    add += a + b;
-                    pf[2 * t + half] = CT == kBF16 ? BF16::down(a, b) : F16::down(a, b);
-                }
-                sum[half] = sum[half] * fade + add;
-#pragma unroll
-                for (int t = 0; t < D / 8; ++t) {
-                    out[t][2 * half] *= fade;
-                    out[t][2 * half + 1] *= fade;
-                }
-            }
-            const uint32_t base = values + (lane & 15) * P::kRow + (lane >> 4) * 16;
-#pragma unroll
-            for (int c = 0; c < P::kChunks; c += 2) {
-                uint32_t r[4];
-                ldmatrix4_trans(r, base + c * 16);
+                    for (int j = 0; j < 4; ++j) s[u][t][j] = 0.f;
+                const uint32_t base = keys + (16 * u + (lane & 15)) * P::kRow + (lane >> 4) * 16;
                 if constexpr (CT == kE4M3) {
-                    // a register holds (token, d), (token, d + 1), (token + 1, d), (token + 1, d + 1):
-                    // the even and the odd elements of a 16-byte piece are two MMA tiles
+                    // an 8x8 b16 matrix is 8 tokens x 16 E4M3 elements: one k-step
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const uint32_t lo = prmt(r[2 * u], 0u, 0x3120u), hi = prmt(r[2 * u + 1], 0u, 0x3120u);
-                        mma<CT>(out[2 * (c + u)], pf, e4m3x2_to_f16x2(lo & 0xffffu), e4m3x2_to_f16x2(hi & 0xffffu));
-                        mma<CT>(out[2 * (c + u) + 1], pf, e4m3x2_to_f16x2(lo >> 16), e4m3x2_to_f16x2(hi >> 16));
+                    for (int st = 0; st < kSteps; st += 2) {
+                        uint32_t r[4];
+                        ldmatrix4(r, base + st * 16);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t a[4] = {e4m3x2_to_f16x2(r[2 * h] & 0xffffu),
+                                                   e4m3x2_to_f16x2(r[2 * h + 1] & 0xffffu),
+                                                   e4m3x2_to_f16x2(r[2 * h] >> 16), e4m3x2_to_f16x2(r[2 * h + 1] >> 16)};
+#pragma unroll
+                            for (int t = 0; t < NT; ++t) mma<CT>(s[u][t], a, qf[st + h][t][0], qf[st + h][t][1]);
+                        }
                     }
                 } else {
-                    mma<CT>(out[c], pf, r[0], r[1]);
-                    mma<CT>(out[c + 1], pf, r[2], r[3]);
+#pragma unroll
+                    for (int st = 0; st < kSteps; ++st) {
+                        uint32_t a[4];
+                        ldmatrix4(a, base + st * 32);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) mma<CT>(s[u][t], a, qf[st][t][0], qf[st][t][1]);
+                    }
+                }
+            }
+            // Scores in units of log2, tokens that do not take part at -inf.  The subtracted
+            // maximum is only renewed when a score exceeds it by more than 8: up to there a
+            // probability (at most 2^8) is as exact in its type, and the reduction over the
+            // warp and the rescaling of the output are left out of most steps.
+            bool over = false;
+#pragma unroll
+            for (int u = 0; u < kSubs; ++u)
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float& v = s[u][t][j];
+                        v = mask >> (16 * u + 8 * (j >> 1) + quad) & 1 ? v * factor[t][j & 1] : -INFINITY;
+                        over |= v > top[t][j & 1] + 8.f;
+                    }
+            if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        float m = top[t][j];
+#pragma unroll
+                        for (int u = 0; u < kSubs; ++u) m = fmaxf(m, fmaxf(s[u][t][j], s[u][t][j + 2]));
+#pragma unroll
+                        for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                        const float fade = exp2_approx(top[t][j] - ref_of(m));
+                        top[t][j] = m;
+                        sum[t][j] *= fade;
+#pragma unroll
+                        for (int i = 0; i < kSteps; ++i) {
+                            out[i][t][j] *= fade;
+                            out[i][t][j + 2] *= fade;
+                        }
+                    }
+            }
+            uint32_t pf[kSubs][NT][2];  // probabilities [token][head] as the product's second operand
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                const float r0 = ref_of(top[t][0]), r1 = ref_of(top[t][1]);
+#pragma unroll
+                for (int u = 0; u < kSubs; ++u)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float a = exp2_approx(s[u][t][2 * h] - r0), b = exp2_approx(s[u][t][2 * h + 1] - r1);
+                        sum[t][0] += a;
+                        sum[t][1] += b;
+                        pf[u][t][h] = transpose8x8(CT == kBF16 ? BF16::down(a, b) : F16::down(a, b));
+                    }
+            }
+#pragma unroll
+            for (int u = 0; u < kSubs; ++u) {
+                if constexpr (CT == kE4M3) {
+                    // a register holds (token, d), (token, d + 1), (token + 1, d), (token + 1, d + 1):
+                    // the even and the odd elements of a 16-byte piece are the MMA's rows 0-7 and 8-15
+                    const uint32_t base = values + (16 * u + (lane & 15)) * P::kRow + (lane >> 4) * 16;
+#pragma unroll
+                    for (int m = 0; m < kSteps; m += 2) {
+                        uint32_t r[4];
+                        ldmatrix4_trans(r, base + m * 16);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t x = prmt(r[2 * h], 0u, 0x3120u), y = prmt(r[2 * h + 1], 0u, 0x3120u);
+                            const uint32_t a[4] = {e4m3x2_to_f16x2(x & 0xffffu), e4m3x2_to_f16x2(x >> 16),
+                                                   e4m3x2_to_f16x2(y & 0xffffu), e4m3x2_to_f16x2(y >> 16)};
+#pragma unroll
+                            for (int t = 0; t < NT; ++t) mma<CT>(out[m + h][t], a, pf[u][t][0], pf[u][t][1]);
+                        }
+                    }
+                } else {
+                    const uint32_t base =
+                        values + (16 * u + (lane & 7) + (lane >> 4) * 8) * P::kRow + (lane >> 3 & 1) * 16;
+#pragma unroll
+                    for (int m = 0; m < kSteps; ++m) {
+                        uint32_t a[4];
+                        ldmatrix4_trans(a, base + m * 32);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) mma<CT>(out[m][t], a, pf[u][t][0], pf[u][t][1]);
+                    }
                 }
             }
         }
         __syncwarp();
-        if (++stage == P::kStages) stage = 0;
+        const int used = stage;
+        if (++stage == P::kStages) stage = 0, parity ^= 1;
 
         if (at.tile + 1 < at.tiles && it + 1 < count) {
             ++at.tile;
             continue;
         }
 
-        // ---- the end of this CTA's part of (sequence, head chunk): join the warps
+        // ---- the end of this CTA's part of (sequence, head group): join the warps.  Each
+        // leaves its output as [head][element] in the stage it has just used.
         fresh = true;
+        float* mine = reinterpret_cast<float*>(smem + (warp * P::kStages + used) * P::kStage);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            sum[half] += __shfl_xor_sync(0xffffffffu, sum[half], 1);
-            sum[half] += __shfl_xor_sync(0xffffffffu, sum[half], 2);
-            if (in_quad == 0) {
-                warp_max[warp * kRows + quad + 8 * half] = top[half];
-                warp_sum[warp * kRows + quad + 8 * half] = sum[half];
-            }
-        }
-        __syncthreads();
-        float all_max[2], all_sum[2];
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int row = quad + 8 * half;
-            float m = -INFINITY, l = 0.f;
+            for (int j = 0; j < 2; ++j) {
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) m = fmaxf(m, warp_max[w * kRows + row]);
-            const float ref = m == -INFINITY ? 0.f : m;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) l += warp_sum[w * kRows + row] * exp2_approx(warp_max[w * kRows + row] - ref);
-            all_max[half] = m, all_sum[half] = l;
-            const float f = exp2_approx(top[half] - ref);
-#pragma unroll
-            for (int t = 0; t < D / 8; ++t) {
-                out[t][2 * half] *= f;
-                out[t][2 * half + 1] *= f;
-            }
-        }
-        // warps 2 and 3 hand over to 0 and 1, then 1 to 0; a lane meets its own layout
-        auto give = [&](int to) {
-            float* buf = merge + to * P::kOutRows * D;
-#pragma unroll
-            for (int t = 0; t < D / 8; ++t)
-#pragma unroll
-                for (int half = 0; half < (WIDE ? 2 : 1); ++half)
-                    *reinterpret_cast<float2*>(buf + ((t * (WIDE ? 2 : 1) + half) * 32 + lane) * 2) =
-                        make_float2(out[t][2 * half], out[t][2 * half + 1]);
-        };
-        auto take = [&](int from) {
-            const float* buf = merge + from * P::kOutRows * D;
-#pragma unroll
-            for (int t = 0; t < D / 8; ++t)
-#pragma unroll
-                for (int half = 0; half < (WIDE ? 2 : 1); ++half) {
-                    const float2 v = *reinterpret_cast<const float2*>(buf + ((t * (WIDE ? 2 : 1) + half) * 32 + lane) * 2);
-                    out[t][2 * half] += v.x;
-                    out[t][2 * half + 1] += v.y;
+                for (int o = 4; o < 32; o <<= 1) sum[t][j] += __shfl_xor_sync(0xffffffffu, sum[t][j], o);
+                const int head = 8 * t + 2 * in_quad + j;
+                if (quad == 0) {
+                    warp_max[warp * kChunk + head] = top[t][j];
+                    warp_sum[warp * kChunk + head] = sum[t][j];
                 }
-        };
-        if (warp >= 2) give(warp - 2);
-        __syncthreads();
-        if (warp < 2) take(warp);
-        if (warp == 1) give(1);
+                float* row = mine + head * P::kOutRow;
+#pragma unroll
+                for (int m = 0; m < kSteps; ++m) {
+                    if constexpr (CT == kE4M3) {
+                        *reinterpret_cast<float2*>(row + 16 * m + 2 * quad) = make_float2(out[m][t][j], out[m][t][j + 2]);
+                    } else {
+                        row[16 * m + quad] = out[m][t][j];
+                        row[16 * m + quad + 8] = out[m][t][j + 2];
+                    }
+                }
+            }
         __syncthreads();
 
         const int64_t seg = seq_tiles * A.heads + int64_t(at.hc) * at.tiles;  // its first unit
-        const int64_t c0 = ((seg + 1) * ctas - 1) / total;
-        const int64_t c1 = ((seg + at.tiles) * ctas - 1) / total;
-        const bool whole = c0 == c1;
-        auto slot_of = [&](int64_t c) {  // a CTA's first and last (sequence, head) may be shared
-            return A.parts + (2 * c + (c == c0 && total * c / ctas < seg ? 1 : 0)) * (kRows * D + 2 * kRows);
+        const bool whole = seg >= first && seg + at.tiles <= first + count;
+        int64_t c0 = 0, c1 = 0;  // the CTAs that share it
+        int first_slot = 0;      // of c0: 1 if its run starts with another (sequence, head)
+        if (!whole) {
+            c0 = ((seg + 1) * ctas - 1) / total;
+            c1 = ((seg + at.tiles) * ctas - 1) / total;
+            first_slot = total * c0 / ctas < seg ? 1 : 0;
+        }
+        constexpr int kPart = kPartRows * (D + 2);
+        auto part_of = [&](int64_t c) { return A.parts + (2 * c + (c == c0 ? first_slot : 0)) * kPart; };
+        const int all_rows = A.together * rows, items = all_rows * (D / 4);
+        // query head of row r, and the values' scale
+        const int group_head = at.hc / A.chunks * A.together;
+        auto head_of = [&](int r) { return (group_head + r / rows) * A.group + in_group + r % rows; };
+        auto write = [&](int r, int e, const float4& o, float m, float l) {
+            const float vs = CT == kE4M3 && A.c.v_scale ? A.c.v_scale[group_head + r / rows] : 1.f;
+            const float inv = l == 0.f ? 0.f : vs / l;
+            const int h = head_of(r);
+            uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<char*>(A.out) + 2 * (at.b * A.o_token + h * A.o_head + e));
+            const float x0 = o.x * inv, x1 = o.y * inv, x2 = o.z * inv, x3 = o.w * inv;
+            *reinterpret_cast<uint2*>(dst) = A.q_bf16 ? make_uint2(BF16::down(x0, x1), BF16::down(x2, x3))
+                                                      : make_uint2(F16::down(x0, x1), F16::down(x2, x3));
+            if (A.lse && e == 0) A.lse[int64_t(at.b) * A.q_heads + h] = (m + log2f(l)) * 0.693147180559945309f;
         };
-        const float vs = CT == kE4M3 && A.c.v_scale ? A.c.v_scale[kvh] : 1.f;
-        // Columns of accumulator pair t: 8 t + 2 (lane % 4) + {0, 1}; for E4M3 values
-        // pair t holds the even (t even) or odd elements of 16-byte piece t / 2.
-        if (warp == 0) {
-            take(1);
-#pragma unroll
-            for (int half = 0; half < (WIDE ? 2 : 1); ++half) {
-                const int row = quad + 8 * half;
-                if (row >= rows) continue;
-                if (whole) {
-                    const float inv = all_sum[half] == 0.f ? 0.f : vs / all_sum[half];
-                    char* dst = static_cast<char*>(A.out) + 2 * (at.b * A.o_token + (row0 + row) * A.o_head);
-                    auto down = [&](float x, float y) { return A.q_bf16 ? BF16::down(x, y) : F16::down(x, y); };
-#pragma unroll
-                    for (int t = 0; t < D / 8; t += 2) {
-                        const float x0 = out[t][2 * half] * inv, x1 = out[t][2 * half + 1] * inv;
-                        const float y0 = out[t + 1][2 * half] * inv, y1 = out[t + 1][2 * half + 1] * inv;
-                        if constexpr (CT == kE4M3) {
-                            *reinterpret_cast<uint2*>(dst + 2 * (8 * t + 4 * in_quad)) = make_uint2(down(x0, y0), down(x1, y1));
-                        } else {
-                            *reinterpret_cast<uint32_t*>(dst + 2 * (8 * t + 2 * in_quad)) = down(x0, x1);
-                            *reinterpret_cast<uint32_t*>(dst + 2 * (8 * t + 8 + 2 * in_quad)) = down(y0, y1);
-                        }
-                    }
-                    if (A.lse && in_quad == 0)
-                        A.lse[int64_t(at.b) * A.q_heads + row0 + row] =
-                            (all_max[half] + log2f(all_sum[half])) * 0.693147180559945309f;
-                } else {
-                    float* dst = slot_of(blockIdx.x) + row * D;
-#pragma unroll
-                    for (int t = 0; t < D / 8; t += 2) {
-                        if constexpr (CT == kE4M3) {
-                            *reinterpret_cast<float4*>(dst + 8 * t + 4 * in_quad) = make_float4(
-                                out[t][2 * half], out[t + 1][2 * half], out[t][2 * half + 1], out[t + 1][2 * half + 1]);
-                        } else {
-                            *reinterpret_cast<float2*>(dst + 8 * t + 2 * in_quad) =
-                                make_float2(out[t][2 * half], out[t][2 * half + 1]);
-                            *reinterpret_cast<float2*>(dst + 8 * t + 8 + 2 * in_quad) =
-                                make_float2(out[t + 1][2 * half], out[t + 1][2 * half + 1]);
-                        }
-                    }
-                    if (in_quad == 0) {
-                        float* stat = slot_of(blockIdx.x) + kRows * D + row;
-                        stat[0] = all_max[half];
-                        stat[kRows] = all_sum[half];
-                    }
+        for (int i = tid; i < items; i += kThreads) {
+            const int r = i / (D / 4), e = i % (D / 4) * 4, hh = r / rows, row = r % rows;
+            float m = -INFINITY, l = 0.f;
+            for (int w = hh * sharers; w < (hh + 1) * sharers; ++w) m = fmaxf(m, warp_max[w * kChunk + row]);
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int w = hh * sharers; w < (hh + 1) * sharers; ++w) {
+                const float f = exp2_approx(warp_max[w * kChunk + row] - ref_of(m));
+                const float4 v = *reinterpret_cast<const float4*>(
+                    smem + (w * P::kStages + used) * P::kStage + (row * P::kOutRow + e) * 4);
+                l += f * warp_sum[w * kChunk + row];
+                o.x += f * v.x, o.y += f * v.y, o.z += f * v.z, o.w += f * v.w;
+            }
+            if (whole) {
+                write(r, e, o, m, l);
+            } else {
+                float* part = part_of(blockIdx.x);
+                *reinterpret_cast<float4*>(part + r * D + e) = o;
+                if (e == 0) {
+                    part[kPartRows * D + r] = m;
+                    part[kPartRows * D + kPartRows + r] = l;
                 }
             }
         }
+        if (P::kBulk) tc::fence_proxy_async_smem();  // the stage's next rows are written by the async proxy
+        __syncthreads();
         if (!whole) {
-            // The parts' writes come before the count; the last CTA reads them after it.
-            if (warp == 0) {
-                __threadfence();
-                __syncwarp();
-                if (lane == 0) {
-                    int32_t* count_at = A.arrived + int64_t(at.b) * A.heads + at.hc;
-                    const int parts = int(c1 - c0) + 1;
-                    const bool last = atomicAdd(count_at, 1) == parts - 1;
-                    if (last) *count_at = 0;
-                    s_last = last;
-                    __threadfence();
-                }
+            // The barrier puts the CTA's writes before thread 0's release; the CTA that counts
+            // the last part has acquired all of them.
+            const int n = int(c1 - c0) + 1;
+            if (tid == 0) {
+                int32_t* counter = A.arrived + int64_t(at.b) * A.heads + at.hc;
+                s_last = add_acq_rel(counter, 1) == n - 1;
+                if (s_last) *counter = 0;
             }
             __syncthreads();
             if (s_last) {
-                for (int row = warp; row < rows; row += kWarps) {  // a warp joins a row
-                    float m = -INFINITY;
-                    for (int64_t c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, __ldcg(slot_of(c) + kRows * D + row));
+                // A thread takes four elements of a row over all parts, or over every ways-th
+                // where there are fewer elements than threads.
+                float* meet = reinterpret_cast<float*>(smem + used * P::kStage);  // [ways][items][6]
+                const int ways = max(1, kThreads / items);
+                for (int i0 = 0; i0 < items; i0 += kThreads) {
+                    const int i = i0 + tid % min(items, kThreads), way = tid / min(items, kThreads);
+                    const int r = i / (D / 4), e = i % (D / 4) * 4;
+                    float m = -INFINITY, l = 0.f;
+                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (i < items && way < ways) {
+                        constexpr int kBatch = 8;
+                        for (int p0 = way; p0 < n; p0 += ways * kBatch) {
+                            float pm[kBatch], pl[kBatch];
+                            float4 po[kBatch];
 #pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                    const float ref = m == -INFINITY ? 0.f : m;
-                    float l = 0.f;
-                    float acc[D / 32] = {};
-#pragma unroll 4
-                    for (int64_t c = c0; c <= c1; ++c) {
-                        const float* part = slot_of(c);
-                        const float w = exp2_approx(__ldcg(part + kRows * D + row) - ref);
-                        l += w * __ldcg(part + kRows * D + kRows + row);
+                            for (int k = 0; k < kBatch; ++k) {
+                                const int p = p0 + k * ways;
+                                pm[k] = -INFINITY, pl[k] = 0.f;
+                                po[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                                if (p < n) {
+                                    const float* part = part_of(c0 + p);
+                                    po[k] = __ldcg(reinterpret_cast<const float4*>(part + r * D + e));
+                                    pm[k] = __ldcg(part + kPartRows * D + r);
+                                    pl[k] = __ldcg(part + kPartRows * D + kPartRows + r);
+                                }
+                            }
+                            float now = m;
 #pragma unroll
-                        for (int i = 0; i < D / 32; ++i) acc[i] += w * __ldcg(part + row * D + i * 32 + lane);
+                            for (int k = 0; k < kBatch; ++k) now = fmaxf(now, pm[k]);
+                            const float fade = exp2_approx(m - ref_of(now));
+                            m = now;
+                            l *= fade, o.x *= fade, o.y *= fade, o.z *= fade, o.w *= fade;
+#pragma unroll
+                            for (int k = 0; k < kBatch; ++k) {
+                                const float f = exp2_approx(pm[k] - ref_of(m));
+                                l += f * pl[k];
+                                o.x += f * po[k].x, o.y += f * po[k].y, o.z += f * po[k].z, o.w += f * po[k].w;
+                            }
+                        }
                     }
-                    const float inv = l == 0.f ? 0.f : vs / l;
-                    uint16_t* dst = static_cast<uint16_t*>(A.out) + at.b * A.o_token + (row0 + row) * A.o_head;
-#pragma unroll
-                    for (int i = 0; i < D / 32; ++i) {
-                        const float x = acc[i] * inv;
-                        dst[i * 32 + lane] = uint16_t(A.q_bf16 ? BF16::down(x, 0.f) : F16::down(x, 0.f));
+                    if (ways > 1) {
+                        float* at_me = meet + tid * 6;
+                        at_me[0] = m, at_me[1] = l, at_me[2] = o.x, at_me[3] = o.y, at_me[4] = o.z, at_me[5] = o.w;
+                        __syncthreads();
+                        if (tid < items)
+                            for (int w = 1; w < ways; ++w) {
+                                const float* v = meet + (tid + w * items) * 6;
+                                const float now = fmaxf(m, v[0]);
+                                const float f = exp2_approx(m - ref_of(now)), g = exp2_approx(v[0] - ref_of(now));
+                                m = now;
+                                l = l * f + g * v[1];
+                                o.x = o.x * f + g * v[2], o.y = o.y * f + g * v[3];
+                                o.z = o.z * f + g * v[4], o.w = o.w * f + g * v[5];
+                            }
                     }
-                    if (A.lse && lane == 0)
-                        A.lse[int64_t(at.b) * A.q_heads + row0 + row] = (m + log2f(l)) * 0.693147180559945309f;
+                    if (i < items && way == 0) write(r, e, o, m, l);
                 }
+                if (P::kBulk) tc::fence_proxy_async_smem();
+                __syncthreads();
             }
-            __syncthreads();
         }
 
         if (it + 1 < count) {
@@ -623,28 +721,38 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, WIDE>::kPerSM) paged_att
 }
 
 size_t counters_bytes(int seqs, int heads) { return align256(size_t(seqs) * heads * 4); }
-int chunks_of(int group) { return (group + kRows - 1) / kRows; }
+int chunks_of(int group) { return (group + kChunk - 1) / kChunk; }
 
-template <int D, int CT, bool WIDE>
-w4a4_status launch_w(const Args& A, cudaStream_t s) {
-    using P = Plan<D, CT, WIDE>;
-    // CUDA keeps a kernel's shared-memory limit per device; setting it again is cheap but not free
-    static std::atomic<uint64_t> ready{0};
+template <int D, int CT, int NT>
+w4a4_status launch_n(Args& A, cudaStream_t s) {
+    using P = Plan<D, CT, NT>;
+    static std::atomic<uint64_t> ready{0};  // devices on which the kernel's shared-memory limit has been raised
     int dev = 0;
     cudaGetDevice(&dev);
-    if (dev < 0 || dev >= 64 || !(ready.load() >> dev & 1)) {
-        if (cudaFuncSetAttribute(paged_attention_kernel<D, CT, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (dev < 0 || dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+        if (cudaFuncSetAttribute(paged_attention_kernel<D, CT, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  P::kBytes) != cudaSuccess)
             return launch_status();
         if (dev >= 0 && dev < 64) ready.fetch_or(uint64_t(1) << dev);
     }
-    // As many CTAs as the GPU holds at once, or one per unit where there can be fewer.
     const int64_t longest = int64_t(A.c.max_pages) * A.c.page_size;
     const int64_t keys = A.window > 0 && A.window < longest ? A.window : longest;
-    const int64_t units = int64_t(A.c.seqs) * A.heads * ((keys + kUnit - 1) / kUnit);
-    int64_t grid = P::kPerSM * device_sm_count();
-    if (grid > kMaxCtas) grid = kMaxCtas;
-    if (grid > units) grid = units > 0 ? units : 1;
+    int64_t full = P::kPerSM * device_sm_count();  // CTAs the GPU holds at once
+    if (full > kMaxCtas) full = kMaxCtas;
+    // Heads side by side: where a token's heads are adjacent rows, the four warps take
+    // four heads (two, where NT or kv_heads leaves no more) of the same tokens, so that
+    // what they fetch together is one long row.  Not where there is little work: it
+    // makes (sequence, head) groups fewer and their splits, and so the join, longer.
+    A.together = 1;
+    const bool adjacent = A.c.k_head_stride == D && A.c.v_head_stride == D && A.c.kv_heads > 1;
+    if (adjacent && A.chunks == 1 && int64_t(A.c.seqs) * A.c.kv_heads * keys > 8 * full * kWarps * P::kTokens)
+        while (A.together < kPartRows / (8 * NT) && A.together < kWarps && A.c.kv_heads % (2 * A.together) == 0)
+            A.together *= 2;
+    A.heads = A.c.kv_heads / A.together * A.chunks;
+    A.span = kWarps / A.together * P::kTokens;
+    // As many CTAs as the GPU holds, or one per unit where there can be fewer.
+    const int64_t units = int64_t(A.c.seqs) * A.heads * ((keys + A.span - 1) / A.span);
+    const int64_t grid = units < 1 ? 1 : units < full ? units : full;
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
     cfg.attrs = attr;
@@ -653,19 +761,21 @@ w4a4_status launch_w(const Args& A, cudaStream_t s) {
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = P::kBytes;
     cfg.stream = s;
-    cudaLaunchKernelEx(&cfg, paged_attention_kernel<D, CT, WIDE>, A);
-    set_dispatch("paged_attention mma.m16n8k16 seqs=%d heads=%d/%d dim=%d %s stages=%d grid=%d", A.c.seqs, A.q_heads,
-                 A.c.kv_heads, D, CT == kF16 ? "f16" : CT == kBF16 ? "bf16" : "e4m3", P::kStages, int(grid));
+    cudaLaunchKernelEx(&cfg, paged_attention_kernel<D, CT, NT>, static_cast<const Args&>(A));
+    set_dispatch_ints(CT == kF16    ? "paged_attention f16 seqs=%d heads=%d/%d dim=%d stages=%d heads/unit=%d grid=%d"
+                      : CT == kBF16 ? "paged_attention bf16 seqs=%d heads=%d/%d dim=%d stages=%d heads/unit=%d grid=%d"
+                                    : "paged_attention e4m3 seqs=%d heads=%d/%d dim=%d stages=%d heads/unit=%d grid=%d",
+                      {A.c.seqs, A.q_heads, A.c.kv_heads, D, P::kStages, A.together, int(grid)});
     return launch_status();
 }
 
 template <int D, int CT>
-w4a4_status launch_c(const Args& A, cudaStream_t s) {
-    return A.group > 8 ? launch_w<D, CT, true>(A, s) : launch_w<D, CT, false>(A, s);
+w4a4_status launch_c(Args& A, cudaStream_t s) {
+    return A.group > 8 ? launch_n<D, CT, 2>(A, s) : launch_n<D, CT, 1>(A, s);
 }
 
 template <int D>
-w4a4_status launch_d(const Args& A, cudaStream_t s) {
+w4a4_status launch_d(Args& A, cudaStream_t s) {
     return A.c.dtype == W4A4_F16    ? launch_c<D, kF16>(A, s)
            : A.c.dtype == W4A4_BF16 ? launch_c<D, kBF16>(A, s)
                                     : launch_c<D, kE4M3>(A, s);
@@ -673,24 +783,23 @@ w4a4_status launch_d(const Args& A, cudaStream_t s) {
 
 }  // namespace
 
-w4a4_status attention_read_and_clear_status() { return take_index_status(g_attention_status); }
+w4a4_status attention_read_and_clear_status() { return take_status_word(g_attention_status); }
 
 size_t attention_workspace_bytes(int seqs, int q_heads, int kv_heads, int head_dim) {
     const int heads = kv_heads * chunks_of(q_heads / kv_heads);
-    return counters_bytes(seqs, heads) + size_t(2) * kMaxCtas * (kRows * head_dim + 2 * kRows) * 4;
+    return counters_bytes(seqs, heads) + size_t(2) * kMaxCtas * kPartRows * (head_dim + 2) * 4;
 }
 
 w4a4_status launch_paged_attention(const w4a4_kv_cache& c, const w4a4_paged_attention_args& a, cudaStream_t s) {
     Args A;
     A.c = c;
     A.q = a.q, A.out = a.out, A.lse = a.lse, A.lengths = a.lengths;
+    A.q_heads = a.q_heads;
     A.group = a.q_heads / c.kv_heads;
     A.chunks = chunks_of(A.group);
-    A.heads = c.kv_heads * A.chunks;
-    A.q_heads = a.q_heads;
     A.window = a.window;
     A.arrived = static_cast<int32_t*>(a.workspace);
-    A.parts = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + counters_bytes(c.seqs, A.heads));
+    A.parts = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + counters_bytes(c.seqs, c.kv_heads * A.chunks));
     A.q_token = a.q_token_stride, A.q_head = a.q_head_stride;
     A.o_token = a.out_token_stride, A.o_head = a.out_head_stride;
     A.scale_log2 = a.scale * 1.44269504088896341f;

@@ -16,16 +16,17 @@
 //    of stages in shared memory, the page table looked up one stage ahead of the copy,
 //    and keeps a running maximum, sum and output in registers (one pass).  Only the end
 //    of a (sequence, head) synchronises the warps.
-//  * Rows of 256 bytes and more are fetched by one bulk copy each, shorter ones by
-//    16-byte asynchronous copies: alone, streaming 4 GB, bulk copies reach 7.1 TB/s with
-//    256-byte rows (16-byte copies: 6.8) but start about 37 G rows a second, so 4.7
-//    (6.7) with 128-byte and 2.8 (6.1) with 64-byte rows.
+//  * The copies are 16 bytes a lane.  One bulk copy per row streams faster alone (4 GB in
+//    256-byte rows: 7.1 TB/s against 6.8) but holds the issuing warp for tens of cycles a
+//    row, and here the warp also has the arithmetic: 850 us instead of 692 on a batch of
+//    4.3 GB, and only a third of the rate where rows are 64 bytes.
 //  * Scores are m16n8k16 warp MMAs with 16 tokens as rows and 8 query heads as columns:
 //    at one token per sequence there are G <= 16 useful columns, so the 128-row tcgen05
 //    tile would stand idle.  The scores' transposed fragments are the probabilities
 //    operand of the second product, whose rows are the head's elements.
-//  * A run that ends inside a (sequence, head) leaves its maximum, sum and output in
-//    the workspace; the CTA that comes last joins the parts in token order.
+//  * A run that ends inside a (sequence, head group) leaves its maximum, sum and output in
+//    the workspace.  Parts are joined sixteen at a time, in token order, by the CTA that
+//    completes the sixteen, and those by the CTA that completes the last.
 #include <atomic>
 
 #include "elem.cuh"
@@ -40,8 +41,8 @@ __device__ int g_attention_status = 0;
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kChunk = 16;              // query heads of a chunk
 constexpr int kPartRows = 32;           // rows of a part in the workspace
-constexpr int kMaxCtas = 480;           // CTAs of a launch at most (three per SM)
-constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr int kMaxSms = 160;
+constexpr int kJoin = 16;               // parts that are joined at a time
 
 enum Cache { kF16, kBF16, kE4M3 };
 
@@ -53,7 +54,6 @@ template <int D, int CT, int NT>
 struct Plan {
     static constexpr int kSize = CT == kE4M3 ? 1 : 2;
     static constexpr int kRowBytes = D * kSize;
-    static constexpr bool kBulk = kRowBytes >= 512;
     static constexpr int kPieces = kRowBytes / 16;
     static constexpr int kRow = (kPieces | 1) * 16;                 // bytes of a row in shared memory
     // Tokens of a warp's step: 32 where a row is short, to halve the steps' fixed cost
@@ -62,37 +62,50 @@ struct Plan {
     static constexpr int kPerSM = kStage > 10000 ? 1 : kStage < 6000 ? 3 : 2;  // CTAs
     static constexpr int kRoom = 228 * 1024 / kPerSM - 1280;        // of an SM, less 1 KB a CTA and the static part
     static constexpr int kFixed = 2 * kWarps * kChunk * 4;          // the warps' maxima and sums
-    static constexpr int kStages = (kRoom - kFixed) / (kWarps * (kStage + 16));
+    static constexpr int kStages = (kRoom - kFixed) / (kWarps * (kStage + 4));
     static constexpr int kOutRow = D + 4;                           // floats of a joined row
     static constexpr int kRing = kWarps * kStages * kStage;
-    static constexpr int kBytes = kRing + kFixed + kWarps * kStages * 16;
+    static constexpr int kBytes = kRing + kFixed + kWarps * kStages * 4;
     static_assert(kStages >= 2 && kBytes <= 227 * 1024 - 256, "shared memory");
+    static_assert(kPerSM <= (D == 64 ? 3 : D == 256 ? 1 : 2), "max_ctas");
     static_assert(8 * NT * kOutRow * 4 <= kStage, "a stage holds a warp's output");
+};
+
+// Division by a number that the host knows, 1 <= d < 2^31: n / d = n * mul >> shift for
+// 0 <= n < 2^31, mul = ceil(2^shift / d), shift = 31 + ceil(log2 d).  (A division takes a
+// hundred and fifty cycles, and a short sequence's way through the kernel has a dozen.)
+struct Divisor {
+    uint32_t mul, shift;
+    explicit Divisor(int d = 1) {
+        shift = 31;
+        while ((1ll << (shift - 31)) < d) ++shift;
+        mul = uint32_t(((1ull << shift) + d - 1) / d);
+    }
+    __device__ __forceinline__ int quotient(int n) const { return int(uint64_t(uint32_t(n)) * mul >> shift); }
 };
 
 struct Args {
     w4a4_kv_cache c;
+    int page_stride[2], token_stride[2], head_stride[2];  // of keys and values, in bytes
+    int longest;  // tokens a row of the page table holds
     const void* q;
     void* out;
     float* lse;
     const int32_t* lengths;
-    int32_t* arrived;  // [seqs][heads] parts that have arrived; zero between calls
-    float* parts;      // [2 * CTAs][kPartRows * D outputs, kPartRows maxima, kPartRows sums]
+    int32_t* arrived;  // [seqs][heads] joined sixteens that have arrived; zero between calls, as is
+    int32_t* joined;   // [2 * CTAs] parts of the sixteen that opens with this one that have arrived
+    float* parts;      // [2][2 * CTAs][kPartRows * D outputs, kPartRows maxima, kPartRows sums]: parts, then joins
+    int64_t joined_at;  // from a part to where its sixteen's join goes, in floats
     int64_t q_token, q_head, o_token, o_head;
     float scale_log2;
     int q_heads, group, chunks, window;
-    int together;  // key-value heads of a unit: 1, 2 or 4
-    int heads;     // (kv_heads / together) * chunks: head groups of a sequence
-    int span;      // tokens of a unit
+    int together;    // key-value heads of a unit: 1, 2 or 4
+    int heads;       // (kv_heads / together) * chunks: head groups of a sequence
+    int span_log2;   // log2 of the tokens of a unit
+    Divisor by_page, by_ctas, by_chunks, by_group;  // page size, grid, chunks, group
     bool q_bf16;
 };
 
-__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
 __device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -138,20 +151,31 @@ __device__ __forceinline__ int add_acq_rel(int32_t* p, int v) {
     return old;
 }
 
+// How the units are shared out: the first `more` CTAs take each + 1, the others each.
+struct Share {
+    int each, more;
+    __device__ __forceinline__ int start(int c) const { return each * c + min(c, more); }
+    __device__ __forceinline__ int owner(int unit) const {
+        const int longer = more * (each + 1);
+        return unit < longer ? unit / (each + 1) : more + (unit - longer) / each;
+    }
+};
+
 // Tokens of sequence b that take part: [lo, lo + n).
 __device__ __forceinline__ void range_of(const Args& A, int b, int& lo, int& n) {
-    int len = A.lengths[b];
-    len = max(0, min(len, A.c.max_pages * A.c.page_size));
+    const int len = max(0, min(A.lengths[b], A.longest));
     lo = A.window > 0 ? max(0, len - A.window) : 0;
     n = len - lo;
 }
+
+__device__ __forceinline__ int tiles_of(const Args& A, int n) { return int((uint32_t(n) + (1u << A.span_log2) - 1) >> A.span_log2); }
 
 // A place in the sequence of units: tile `tile` of (sequence b, head group hc).
 struct Cursor {
     int b, hc, tile, tiles, lo, n;
     __device__ __forceinline__ void enter(const Args& A) {
         range_of(A, b, lo, n);
-        tiles = (n + A.span - 1) / A.span;
+        tiles = tiles_of(A, n);
     }
     __device__ __forceinline__ void advance(const Args& A) {  // to the next unit, if there is one
         if (++tile < tiles) return;
@@ -182,176 +206,162 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
     extern __shared__ __align__(128) uint8_t smem[];
     float* warp_max = reinterpret_cast<float*>(smem + P::kRing);  // [kWarps][kChunk]
     float* warp_sum = warp_max + kWarps * kChunk;                 // [kWarps][kChunk]
-    uint64_t* bars = reinterpret_cast<uint64_t*>(warp_sum + kWarps * kChunk);  // [kWarps][kStages]
-    uint32_t* masks = reinterpret_cast<uint32_t*>(bars + kWarps * P::kStages);  // [kWarps][kStages]
-    __shared__ int64_t scan[kWarps];
-    __shared__ int64_t s_prefix;
-    __shared__ int s_seq, s_last, s_abort;
+    uint32_t* masks = reinterpret_cast<uint32_t*>(warp_sum + kWarps * kChunk);  // [kWarps][kStages]
+    __shared__ int scan[kWarps];
+    __shared__ int s_seq, s_prefix, s_last;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int quad = lane >> 2, in_quad = lane & 3;
-    if (P::kBulk && lane < P::kStages) tc::mbar_init(smem_u32(bars + warp * P::kStages + lane), 1);
-    if (P::kBulk) tc::fence_mbar_init();
-    if (tid == 0) s_abort = 0;
     pdl_wait();
     pdl_launch_dependents();
     const int B = A.c.seqs;
 
-    // ---- this CTA's run of units: a scan over the sequences' tile counts
-    int64_t first, count, total, ctas;
+    // ---- this CTA's run of units: a scan over the sequences' tile counts.  Up to 32
+    // sequences each warp does it for itself, a lane a sequence; more are shared out to the
+    // CTA's threads, several in a row to each.
+    int first, count;
+    Share share;
     Cursor at;
-    int64_t seq_tiles;  // tiles of the sequences before at.b
+    int seq_tiles;  // tiles of the sequences before at.b
     {
-        const int per = (B + kThreads - 1) / kThreads;
-        const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
-        int64_t mine = 0;
-        bool bad = false;
+        const bool few = B <= 32;
+        const int per = few ? 1 : (B + kThreads - 1) / kThreads, me = few ? lane : tid;
+        const int b0 = min(B, me * per), b1 = min(B, b0 + per);
+        int mine = 0, lo = 0, n = 0;
+        bool bad = false, empty = false;
         for (int b = b0; b < b1; ++b) {
             const int len = A.lengths[b];
-            bad |= len < 0 || len > A.c.max_pages * A.c.page_size;
-            int lo, n;
+            bad |= len < 0 || len > A.longest;
             range_of(A, b, lo, n);
-            mine += (n + A.span - 1) / A.span;
+            empty |= n == 0;
+            mine += tiles_of(A, n);
         }
         if (bad && blockIdx.x == 0) atomicExch(&g_attention_status, int(W4A4_ERR_INDEX));
-        int64_t upto = mine;
+        int upto = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+            const int v = __shfl_up_sync(0xffffffffu, upto, o);
             if (lane >= o) upto += v;
         }
-        if (lane == 31) scan[warp] = upto;
-        __syncthreads();
-        total = 0;
+        int total = __shfl_sync(0xffffffffu, upto, 31);
+        if (few) {
+            empty = __any_sync(0xffffffffu, empty);
+        } else {
+            if (lane == 31) scan[warp] = upto;
+            empty = __syncthreads_or(empty);
+            total = 0;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) upto += scan[w];
-            total += scan[w];
+            for (int w = 0; w < kWarps; ++w) {
+                if (w < warp) upto += scan[w];
+                total += scan[w];
+            }
         }
         total *= A.heads;
-        ctas = min(int64_t(gridDim.x), total);
         // sequences without tokens: zeros, from whichever CTA their number falls to
-        for (int b = blockIdx.x; b < B; b += gridDim.x) {
-            int lo, n;
-            range_of(A, b, lo, n);
-            if (n > 0) continue;
-            for (int i = tid; i < A.q_heads * (D / 8); i += kThreads) {
-                const int h = i / (D / 8), e = i % (D / 8) * 8;
-                *reinterpret_cast<uint4*>(static_cast<char*>(A.out) + 2 * (b * A.o_token + h * A.o_head + e)) =
-                    make_uint4(0, 0, 0, 0);
-            }
-            if (A.lse)
-                for (int h = tid; h < A.q_heads; h += kThreads) A.lse[int64_t(b) * A.q_heads + h] = -INFINITY;
-        }
-        if (blockIdx.x >= ctas) return;
-        first = total * blockIdx.x / ctas;
-        count = total * (blockIdx.x + 1) / ctas - first;
-        const int64_t tile = first / A.heads;  // compared with whole sequences: heads * tiles units each
-        int64_t before = upto - mine;
-        if (mine > 0 && before <= tile && tile < upto) {
-            for (int b = b0; b < b1; ++b) {
-                int lo, n;
-                range_of(A, b, lo, n);
-                const int t = (n + A.span - 1) / A.span;
-                if (tile < before + t) {
-                    s_seq = b;
-                    s_prefix = before;
-                    break;
+        if (empty)
+            for (int b = blockIdx.x; b < B; b += gridDim.x) {
+                int l, tokens;
+                range_of(A, b, l, tokens);
+                if (tokens > 0) continue;
+                for (int i = tid; i < A.q_heads * (D / 8); i += kThreads) {
+                    const int h = i / (D / 8), e = i % (D / 8) * 8;
+                    *reinterpret_cast<uint4*>(static_cast<char*>(A.out) + 2 * (b * A.o_token + h * A.o_head + e)) =
+                        make_uint4(0, 0, 0, 0);
                 }
-                before += t;
+                if (A.lse)
+                    for (int h = tid; h < A.q_heads; h += kThreads) A.lse[int64_t(b) * A.q_heads + h] = -INFINITY;
             }
+        if (int(blockIdx.x) >= total) return;
+        share.each = total < int(gridDim.x) ? 1 : A.by_ctas.quotient(total);
+        share.more = total < int(gridDim.x) ? 0 : total - share.each * int(gridDim.x);
+        first = share.start(blockIdx.x);
+        count = share.start(blockIdx.x + 1) - first;
+        int before = upto - mine;
+        const bool here = before * A.heads <= first && first < upto * A.heads;
+        if (few) {
+            at.b = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+            seq_tiles = __shfl_sync(0xffffffffu, before, at.b);
+            at.lo = __shfl_sync(0xffffffffu, lo, at.b);
+            at.n = __shfl_sync(0xffffffffu, n, at.b);
+            at.tiles = __shfl_sync(0xffffffffu, mine, at.b);
+        } else {
+            if (here) {
+                int seq = b0;
+                for (; seq < b1; ++seq) {
+                    range_of(A, seq, lo, n);
+                    const int t = tiles_of(A, n);
+                    if (first < (before + t) * A.heads) break;
+                    before += t;
+                }
+                s_seq = seq, s_prefix = before;
+            }
+            __syncthreads();
+            at.b = s_seq;
+            seq_tiles = s_prefix;
+            at.enter(A);
         }
-        __syncthreads();
-        at.b = s_seq;
-        seq_tiles = s_prefix;
-        at.enter(A);
-        const int64_t in = first - seq_tiles * A.heads;
-        at.hc = int(in / at.tiles);
-        at.tile = int(in - int64_t(at.hc) * at.tiles);
+        const int in = first - seq_tiles * A.heads;
+        at.hc = in / at.tiles;
+        at.tile = in - at.hc * at.tiles;
     }
 
     // ---- the warp's ring of stages
-    const int sharers = kWarps / A.together;  // warps of a key-value head
-    const int my_head = warp / sharers, my_tokens = (warp % sharers) * kTokens;
-    auto kv_head = [&](int hc) { return hc / A.chunks * A.together + my_head; };
+    const int sharers = kWarps / A.together;  // warps of a key-value head (a power of two)
+    const int my_tokens = (warp & (sharers - 1)) * kTokens, my_head = (warp * A.together) / kWarps;
+    auto kv_head = [&](int hc) { return A.by_chunks.quotient(hc) * A.together + my_head; };
     const uint32_t ring = smem_u32(smem) + warp * P::kStages * P::kStage;
     uint32_t* my_masks = masks + warp * P::kStages;
-    const uint32_t my_bars = smem_u32(bars + warp * P::kStages);
-    Cursor put = at;
-    int64_t to_put = count;
-    int page = 0, slot = 0;  // of token lane % kTokens of the next unit to copy
-    bool in_range = false, dead = false;
-    auto look_up = [&] {
-        const int j = put.tile * A.span + my_tokens + (lane & (kTokens - 1));
-        in_range = to_put > 0 && j < put.n;
-        if (in_range) {
-            const int tok = put.lo + j, p = tok / A.c.page_size;
-            slot = tok - p * A.c.page_size;
-            page = A.c.page_table[put.b * A.c.table_stride + p];
-        }
+    // The page table is read two units ahead of the copy: `next` and `after` are the next
+    // two units to copy, `ahead` the place of the one whose look-up comes next.
+    struct Ahead {
+        int page, slot, kvh;  // of token lane % kTokens; the unit's key-value head
+        bool in_range;
     };
+    Cursor ahead = at;
+    int to_put = count, to_look = count;
+    auto look_up = [&](Ahead& u) {
+        u.in_range = false;
+        if (to_look <= 0) return;
+        const int j = (ahead.tile << A.span_log2) + my_tokens + (lane & (kTokens - 1));
+        u.in_range = j < ahead.n;
+        u.kvh = kv_head(ahead.hc);
+        if (u.in_range) {
+            const int tok = ahead.lo + j, p = A.by_page.quotient(tok);
+            u.slot = tok - p * A.c.page_size;
+            u.page = A.c.page_table[ahead.b * A.c.table_stride + p];
+        }
+        if (--to_look > 0) ahead.advance(A);
+    };
+    Ahead next, after;
+    look_up(next);
+    look_up(after);
     auto copy_unit = [&](int stage) {
-        const bool ok = in_range && page >= 0 && page < A.c.pages && !dead;
-        if (in_range && !ok && !dead) atomicExch(&g_attention_status, int(W4A4_ERR_INDEX));
+        const bool ok = next.in_range && next.page >= 0 && next.page < A.c.pages;
+        if (next.in_range && !ok) atomicExch(&g_attention_status, int(W4A4_ERR_INDEX));
         const uint32_t mask = __ballot_sync(0xffffffffu, ok) & (kTokens == 32 ? 0xffffffffu : 0xffffu);
         if (lane == 0) my_masks[stage] = mask;
-        const uint32_t dst = ring + stage * P::kStage;
-        const int kvh = kv_head(put.hc);
-        auto row_of = [&](bool keys) {
-            const int64_t off = !ok ? 0
-                                : keys ? page * A.c.k_page_stride + slot * A.c.k_token_stride + kvh * A.c.k_head_stride
-                                       : page * A.c.v_page_stride + slot * A.c.v_token_stride + kvh * A.c.v_head_stride;
-            return static_cast<const char*>(keys ? A.c.k : A.c.v) + off * P::kSize;
-        };
-        if constexpr (P::kBulk) {
-            const uint32_t bar = my_bars + stage * 8;
-            if (lane == 0) tc::mbar_expect_tx(bar, __popc(mask) * 2 * P::kRowBytes);
-            __syncwarp();
-            // a value row without a token is multiplied by a zero probability: it must be finite
-            auto clear = [&](uint32_t row) {
-                for (int i = 0; i < P::kRowBytes; i += 16)
-                    asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};\n" ::"r"(row + i), "r"(0) : "memory");
-                tc::fence_proxy_async_smem();
+        if (mask) {
+            const uint32_t dst = ring + stage * P::kStage;
+            auto row_of = [&](int kv) {
+                const int64_t off = int64_t(next.page) * A.page_stride[kv] + int64_t(next.slot) * A.token_stride[kv] +
+                                    int64_t(next.kvh) * A.head_stride[kv];
+                return reinterpret_cast<unsigned long long>(kv ? A.c.v : A.c.k) + (ok ? off : 0);
             };
-            if constexpr (kTokens == 32) {
-                const uint32_t row = dst + lane * P::kRow;
-                if (ok) {
-                    tc::bulk_g2s(row, row_of(true), P::kRowBytes, bar);
-                    tc::bulk_g2s(row + kTokens * P::kRow, row_of(false), P::kRowBytes, bar);
-                } else if (mask) {
-                    clear(row + kTokens * P::kRow);
-                }
-            } else {  // lanes 0-15 the keys of their token, lanes 16-31 the values
-                if (ok)
-                    tc::bulk_g2s(dst + lane * P::kRow, row_of(lane < 16), P::kRowBytes, bar);
-                else if (mask && lane >= 16)
-                    clear(dst + lane * P::kRow);
-            }
-        } else {
-            if (mask) {
-                const char* mine = row_of(kTokens == 32 || lane < 16);
-                const char* other = kTokens == 32 ? row_of(false) : mine;
+            // with 16 tokens, lanes 0-15 address the keys of their token, lanes 16-31 the values
+            const unsigned long long mine = row_of(kTokens == 32 || lane < 16 ? 0 : 1);
+            const unsigned long long other = kTokens == 32 ? row_of(1) : mine;
 #pragma unroll
-                for (int i = 0; i < 2 * kTokens * P::kPieces / 32; ++i) {  // a warp's width of pieces at a time
-                    const int piece = i * 32 + lane, r = piece / P::kPieces, c = piece % P::kPieces;
-                    const char* from = kTokens == 32 && i >= P::kPieces ? other : mine;
-                    const char* src = reinterpret_cast<const char*>(
-                        __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(from), r & 31));
-                    tc::cp_async16_zfill(dst + r * P::kRow + c * 16, src + c * 16,
-                                         (mask >> (r & (kTokens - 1)) & 1) * 16);
-                }
+            for (int i = 0; i < 2 * kTokens * P::kPieces / 32; ++i) {  // a warp's width of pieces at a time
+                const int piece = i * 32 + lane, r = piece / P::kPieces, c = piece % P::kPieces;
+                const char* src = reinterpret_cast<const char*>(
+                    __shfl_sync(0xffffffffu, kTokens == 32 && i >= P::kPieces ? other : mine, r & 31));
+                tc::cp_async16_zfill(dst + r * P::kRow + c * 16, src + c * 16, (mask >> (r & (kTokens - 1)) & 1) * 16);
             }
         }
-        if (--to_put > 0) put.advance(A);
-        look_up();
+        --to_put;
+        next = after;
+        look_up(after);
     };
-    look_up();
-    __syncwarp();
-#pragma unroll
-    for (int s = 0; s < P::kStages - 1; ++s) {
-        if (to_put > 0) copy_unit(s);
-        if (!P::kBulk) cp_async_commit();
-    }
 
     // ---- running softmax of this warp's tokens: columns 8 t + 2 (lane % 4) + {0, 1} are
     // query heads; out[m][t] is rows (elements of the head) 16 m + quad and + 8
@@ -360,12 +370,14 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
     float top[NT][2], sum[NT][2], factor[NT][2];
     int rows = 0;
     bool fresh = true;
-    int stage = 0, parity = 0;
-    for (int64_t it = 0; it < count; ++it) {
-        if (to_put > 0) copy_unit(stage == 0 ? P::kStages - 1 : stage - 1);
-        if (!P::kBulk) cp_async_commit();
+    int stage = 0, fill = 0;
+    for (int it = 1 - P::kStages; it < count; ++it) {  // the first kStages - 1 steps only copy
+        if (to_put > 0) copy_unit(fill);
+        cp_async_commit();
+        if (++fill == P::kStages) fill = 0;
+        if (it < 0) continue;
 
-        const int kvh = kv_head(at.hc), in_group = at.hc % A.chunks * kChunk;
+        const int kvh = kv_head(at.hc), in_group = (at.hc - A.by_chunks.quotient(at.hc) * A.chunks) * kChunk;
         const int row0 = kvh * A.group + in_group;  // this warp's first query head
         if (fresh) {
             fresh = false;
@@ -422,19 +434,8 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
             }
         }
 
-        if constexpr (P::kBulk) {
-            __syncwarp();
-            if (!tc::warp_wait_parity(my_bars + stage * 8, parity, &s_abort, kWaitLimitNs)) {
-                if (lane == 0) {
-                    s_abort = 1;
-                    atomicExch(&g_attention_status, int(W4A4_ERR_TIMEOUT));
-                }
-                dead = true;
-            }
-        } else {
-            cp_async_wait<P::kStages - 1>();
-            __syncwarp();
-        }
+        cp_async_wait<P::kStages - 1>();
+        __syncwarp();
         const uint32_t mask = my_masks[stage];
         const uint32_t keys = ring + stage * P::kStage, values = keys + kTokens * P::kRow;
         if (mask) {
@@ -451,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
 #pragma unroll
                     for (int st = 0; st < kSteps; st += 2) {
                         uint32_t r[4];
-                        ldmatrix4(r, base + st * 16);
+                        tc::ldsm_x4(r, base + st * 16);
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const uint32_t a[4] = {e4m3x2_to_f16x2(r[2 * h] & 0xffffu),
@@ -465,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
 #pragma unroll
                     for (int st = 0; st < kSteps; ++st) {
                         uint32_t a[4];
-                        ldmatrix4(a, base + st * 32);
+                        tc::ldsm_x4(a, base + st * 32);
 #pragma unroll
                         for (int t = 0; t < NT; ++t) mma<CT>(s[u][t], a, qf[st][t][0], qf[st][t][1]);
                     }
@@ -554,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
         }
         __syncwarp();
         const int used = stage;
-        if (++stage == P::kStages) stage = 0, parity ^= 1;
+        if (++stage == P::kStages) stage = 0;
 
         if (at.tile + 1 < at.tiles && it + 1 < count) {
             ++at.tile;
@@ -589,79 +590,102 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
             }
         __syncthreads();
 
-        const int64_t seg = seq_tiles * A.heads + int64_t(at.hc) * at.tiles;  // its first unit
+        const int seg = seq_tiles * A.heads + at.hc * at.tiles;  // its first unit
         const bool whole = seg >= first && seg + at.tiles <= first + count;
-        int64_t c0 = 0, c1 = 0;  // the CTAs that share it
-        int first_slot = 0;      // of c0: 1 if its run starts with another (sequence, head)
+        int c0 = 0, c1 = 0;  // the CTAs that share it
+        int first_slot = 0;  // of c0: 1 if its run starts with another (sequence, head)
         if (!whole) {
-            c0 = ((seg + 1) * ctas - 1) / total;
-            c1 = ((seg + at.tiles) * ctas - 1) / total;
-            first_slot = total * c0 / ctas < seg ? 1 : 0;
+            c0 = share.owner(seg);
+            c1 = share.owner(seg + at.tiles - 1);
+            first_slot = share.start(c0) < seg ? 1 : 0;
         }
         constexpr int kPart = kPartRows * (D + 2);
-        auto part_of = [&](int64_t c) { return A.parts + (2 * c + (c == c0 ? first_slot : 0)) * kPart; };
+        auto slot_of = [&](int c) { return 2 * c + (c == c0 ? first_slot : 0); };
+        auto part_of = [&](int c) { return A.parts + int64_t(slot_of(c)) * kPart; };
         const int all_rows = A.together * rows, items = all_rows * (D / 4);
-        // query head of row r, and the values' scale
-        const int group_head = at.hc / A.chunks * A.together;
-        auto head_of = [&](int r) { return (group_head + r / rows) * A.group + in_group + r % rows; };
+        // row r is query head `row` of key-value head hh of the unit's; rows = group where there are several
+        auto head_in_unit = [&](int r) { return A.together == 1 ? 0 : A.by_group.quotient(r); };
+        const int unit_head = kvh - my_head;
         auto write = [&](int r, int e, const float4& o, float m, float l) {
-            const float vs = CT == kE4M3 && A.c.v_scale ? A.c.v_scale[group_head + r / rows] : 1.f;
+            const int hh = head_in_unit(r), h = (unit_head + hh) * A.group + in_group + r - hh * rows;
+            const float vs = CT == kE4M3 && A.c.v_scale ? A.c.v_scale[unit_head + hh] : 1.f;
             const float inv = l == 0.f ? 0.f : vs / l;
-            const int h = head_of(r);
             uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<char*>(A.out) + 2 * (at.b * A.o_token + h * A.o_head + e));
             const float x0 = o.x * inv, x1 = o.y * inv, x2 = o.z * inv, x3 = o.w * inv;
             *reinterpret_cast<uint2*>(dst) = A.q_bf16 ? make_uint2(BF16::down(x0, x1), BF16::down(x2, x3))
                                                       : make_uint2(F16::down(x0, x1), F16::down(x2, x3));
             if (A.lse && e == 0) A.lse[int64_t(at.b) * A.q_heads + h] = (m + log2f(l)) * 0.693147180559945309f;
         };
+        auto leave = [&](float* part, int r, int e, const float4& o, float m, float l) {
+            *reinterpret_cast<float4*>(part + r * D + e) = o;
+            if (e == 0) part[kPartRows * D + r] = m, part[kPartRows * D + kPartRows + r] = l;
+        };
+#pragma unroll 1
         for (int i = tid; i < items; i += kThreads) {
-            const int r = i / (D / 4), e = i % (D / 4) * 4, hh = r / rows, row = r % rows;
+            const int r = i / (D / 4), e = i % (D / 4) * 4, hh = head_in_unit(r), row = r - hh * rows;
+            float wm[kWarps], wl[kWarps];
+            float4 wo[kWarps];
             float m = -INFINITY, l = 0.f;
-            for (int w = hh * sharers; w < (hh + 1) * sharers; ++w) m = fmaxf(m, warp_max[w * kChunk + row]);
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int w = hh * sharers; w < (hh + 1) * sharers; ++w) {
-                const float f = exp2_approx(warp_max[w * kChunk + row] - ref_of(m));
-                const float4 v = *reinterpret_cast<const float4*>(
-                    smem + (w * P::kStages + used) * P::kStage + (row * P::kOutRow + e) * 4);
-                l += f * warp_sum[w * kChunk + row];
-                o.x += f * v.x, o.y += f * v.y, o.z += f * v.z, o.w += f * v.w;
-            }
-            if (whole) {
-                write(r, e, o, m, l);
-            } else {
-                float* part = part_of(blockIdx.x);
-                *reinterpret_cast<float4*>(part + r * D + e) = o;
-                if (e == 0) {
-                    part[kPartRows * D + r] = m;
-                    part[kPartRows * D + kPartRows + r] = l;
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) {
+                const int w = hh * sharers + k;
+                wm[k] = -INFINITY, wl[k] = 0.f;
+                wo[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (k < sharers) {
+                    wm[k] = warp_max[w * kChunk + row], wl[k] = warp_sum[w * kChunk + row];
+                    wo[k] = *reinterpret_cast<const float4*>(smem + (w * P::kStages + used) * P::kStage +
+                                                             (row * P::kOutRow + e) * 4);
                 }
+                m = fmaxf(m, wm[k]);
             }
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) {
+                const float f = exp2_approx(wm[k] - ref_of(m));
+                l += f * wl[k];
+                o.x += f * wo[k].x, o.y += f * wo[k].y, o.z += f * wo[k].z, o.w += f * wo[k].w;
+            }
+            if (whole)
+                write(r, e, o, m, l);
+            else
+                leave(part_of(blockIdx.x), r, e, o, m, l);
         }
-        if (P::kBulk) tc::fence_proxy_async_smem();  // the stage's next rows are written by the async proxy
         __syncthreads();
         if (!whole) {
+            const int n = c1 - c0 + 1, sixteens = (n + kJoin - 1) / kJoin;
+            const int c_first = c0 + (int(blockIdx.x) - c0) / kJoin * kJoin;  // of this CTA's sixteen
+            const int in_sixteen = min(kJoin, c1 + 1 - c_first);
             // The barrier puts the CTA's writes before thread 0's release; the CTA that counts
             // the last part has acquired all of them.
-            const int n = int(c1 - c0) + 1;
-            if (tid == 0) {
-                int32_t* counter = A.arrived + int64_t(at.b) * A.heads + at.hc;
-                s_last = add_acq_rel(counter, 1) == n - 1;
-                if (s_last) *counter = 0;
-            }
-            __syncthreads();
-            if (s_last) {
-                // A thread takes four elements of a row over all parts, or over every ways-th
-                // where there are fewer elements than threads.
-                float* meet = reinterpret_cast<float*>(smem + used * P::kStage);  // [ways][items][6]
-                const int ways = max(1, kThreads / items);
+            auto arrive = [&](int32_t* counter, int parts) {
+                if (tid == 0) {
+                    s_last = add_acq_rel(counter, 1) == parts - 1;
+                    if (s_last) *counter = 0;
+                }
+                __syncthreads();
+                return s_last != 0;
+            };
+            // Level 0 joins the parts of this CTA's sixteen, level 1 the joined sixteens.  A thread
+            // takes four elements of a row over all parts, or over every ways-th where there
+            // are fewer elements than threads.
+            float* meet = reinterpret_cast<float*>(smem + used * P::kStage);  // [ways][items][6]
+            const int width = min(items, kThreads), ways = kThreads / width, my_way = tid / width, my_item = tid - my_way * width;
+            for (int level = 0; level < 2; ++level) {
+                if (!(level == 0 ? arrive(A.joined + slot_of(c_first), in_sixteen)
+                                 : arrive(A.arrived + int64_t(at.b) * A.heads + at.hc, sixteens)))
+                    break;
+                const int from = level == 0 ? c_first : c0;
+                const int step = level == 0 ? 1 : kJoin, parts = level == 0 ? in_sixteen : sixteens;
+                const bool last = level == 1 || sixteens == 1;
                 for (int i0 = 0; i0 < items; i0 += kThreads) {
-                    const int i = i0 + tid % min(items, kThreads), way = tid / min(items, kThreads);
+                    const int i = i0 + my_item, way = my_way;
                     const int r = i / (D / 4), e = i % (D / 4) * 4;
                     float m = -INFINITY, l = 0.f;
                     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
                     if (i < items && way < ways) {
                         constexpr int kBatch = 8;
-                        for (int p0 = way; p0 < n; p0 += ways * kBatch) {
+#pragma unroll 1
+                        for (int p0 = way; p0 < parts; p0 += ways * kBatch) {
                             float pm[kBatch], pl[kBatch];
                             float4 po[kBatch];
 #pragma unroll
@@ -669,8 +693,8 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
                                 const int p = p0 + k * ways;
                                 pm[k] = -INFINITY, pl[k] = 0.f;
                                 po[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                                if (p < n) {
-                                    const float* part = part_of(c0 + p);
+                                if (p < parts) {
+                                    const float* part = part_of(from + p * step) + (level ? A.joined_at : 0);
                                     po[k] = __ldcg(reinterpret_cast<const float4*>(part + r * D + e));
                                     pm[k] = __ldcg(part + kPartRows * D + r);
                                     pl[k] = __ldcg(part + kPartRows * D + kPartRows + r);
@@ -695,6 +719,7 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
                         at_me[0] = m, at_me[1] = l, at_me[2] = o.x, at_me[3] = o.y, at_me[4] = o.z, at_me[5] = o.w;
                         __syncthreads();
                         if (tid < items)
+#pragma unroll 1
                             for (int w = 1; w < ways; ++w) {
                                 const float* v = meet + (tid + w * items) * 6;
                                 const float now = fmaxf(m, v[0]);
@@ -705,10 +730,15 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
                                 o.z = o.z * f + g * v[4], o.w = o.w * f + g * v[5];
                             }
                     }
-                    if (i < items && way == 0) write(r, e, o, m, l);
+                    if (i < items && way == 0) {
+                        if (last)
+                            write(r, e, o, m, l);
+                        else
+                            leave(part_of(c_first) + A.joined_at, r, e, o, m, l);
+                    }
                 }
-                if (P::kBulk) tc::fence_proxy_async_smem();
                 __syncthreads();
+                if (last) break;
             }
         }
 
@@ -720,7 +750,12 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
     }
 }
 
-size_t counters_bytes(int seqs, int heads) { return align256(size_t(seqs) * heads * 4); }
+// CTAs of a launch at most: as many as the plan of any cache type puts on an SM.
+constexpr int max_ctas(int head_dim) { return kMaxSms * (head_dim == 64 ? 3 : head_dim == 256 ? 1 : 2); }
+size_t part_floats(int head_dim) { return size_t(kPartRows) * (head_dim + 2); }
+size_t counters_bytes(int seqs, int heads, int head_dim) {
+    return align256((size_t(seqs) * heads + 2 * max_ctas(head_dim)) * 4);
+}
 int chunks_of(int group) { return (group + kChunk - 1) / kChunk; }
 
 template <int D, int CT, int NT>
@@ -737,22 +772,28 @@ w4a4_status launch_n(Args& A, cudaStream_t s) {
     }
     const int64_t longest = int64_t(A.c.max_pages) * A.c.page_size;
     const int64_t keys = A.window > 0 && A.window < longest ? A.window : longest;
-    int64_t full = P::kPerSM * device_sm_count();  // CTAs the GPU holds at once
-    if (full > kMaxCtas) full = kMaxCtas;
-    // Heads side by side: where a token's heads are adjacent rows, the four warps take
-    // four heads (two, where NT or kv_heads leaves no more) of the same tokens, so that
-    // what they fetch together is one long row.  Not where there is little work: it
-    // makes (sequence, head) groups fewer and their splits, and so the join, longer.
+    int64_t full = P::kPerSM * int64_t(device_sm_count());  // CTAs the GPU holds at once
+    if (full > max_ctas(D)) full = max_ctas(D);
+    // Heads side by side: the four warps take four heads (two, where NT or kv_heads leaves no
+    // more) of the same tokens.  With heads that are adjacent rows, what they fetch together
+    // is one long row (64-byte rows: 3.5 TB/s alone); with sequences of no more than one
+    // head's unit, no warp is left without tokens and there is nothing to join.  In between,
+    // it would make (sequence, head group) pairs fewer and their splits, so the joins, longer.
     A.together = 1;
-    const bool adjacent = A.c.k_head_stride == D && A.c.v_head_stride == D && A.c.kv_heads > 1;
-    if (adjacent && A.chunks == 1 && int64_t(A.c.seqs) * A.c.kv_heads * keys > 8 * full * kWarps * P::kTokens)
+    const bool adjacent = A.c.k_head_stride == D && A.c.v_head_stride == D;
+    const int64_t all = int64_t(A.c.seqs) * A.c.kv_heads * keys;
+    if (A.chunks == 1 && ((adjacent && all > 16 * full * kWarps * P::kTokens) || keys <= kWarps * P::kTokens))
         while (A.together < kPartRows / (8 * NT) && A.together < kWarps && A.c.kv_heads % (2 * A.together) == 0)
             A.together *= 2;
     A.heads = A.c.kv_heads / A.together * A.chunks;
-    A.span = kWarps / A.together * P::kTokens;
+    A.span_log2 = A.together == 1 ? 2 : A.together == 2 ? 1 : 0;
+    A.span_log2 += P::kTokens == 32 ? 5 : 4;
+    const int64_t span = int64_t(1) << A.span_log2;
     // As many CTAs as the GPU holds, or one per unit where there can be fewer.
-    const int64_t units = int64_t(A.c.seqs) * A.heads * ((keys + A.span - 1) / A.span);
+    const int64_t units = int64_t(A.c.seqs) * A.heads * ((keys + span - 1) / span);
+    if (units > INT32_MAX) return W4A4_ERR_UNSUPPORTED_SHAPE;
     const int64_t grid = units < 1 ? 1 : units < full ? units : full;
+    A.by_ctas = Divisor(int(grid));
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
     cfg.attrs = attr;
@@ -787,7 +828,7 @@ w4a4_status attention_read_and_clear_status() { return take_status_word(g_attent
 
 size_t attention_workspace_bytes(int seqs, int q_heads, int kv_heads, int head_dim) {
     const int heads = kv_heads * chunks_of(q_heads / kv_heads);
-    return counters_bytes(seqs, heads) + size_t(2) * kMaxCtas * kPartRows * (head_dim + 2) * 4;
+    return counters_bytes(seqs, heads, head_dim) + 4 * max_ctas(head_dim) * part_floats(head_dim) * 4;
 }
 
 w4a4_status launch_paged_attention(const w4a4_kv_cache& c, const w4a4_paged_attention_args& a, cudaStream_t s) {
@@ -798,8 +839,18 @@ w4a4_status launch_paged_attention(const w4a4_kv_cache& c, const w4a4_paged_atte
     A.group = a.q_heads / c.kv_heads;
     A.chunks = chunks_of(A.group);
     A.window = a.window;
-    A.arrived = static_cast<int32_t*>(a.workspace);
-    A.parts = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + counters_bytes(c.seqs, c.kv_heads * A.chunks));
+    A.longest = c.max_pages * c.page_size;
+    const int size = c.dtype == W4A4_E4M3 ? 1 : 2;  // strides are at most 2^29 elements
+    A.page_stride[0] = int(c.k_page_stride * size), A.page_stride[1] = int(c.v_page_stride * size);
+    A.token_stride[0] = int(c.k_token_stride * size), A.token_stride[1] = int(c.v_token_stride * size);
+    A.head_stride[0] = int(c.k_head_stride * size), A.head_stride[1] = int(c.v_head_stride * size);
+    A.by_page = Divisor(c.page_size);
+    A.by_chunks = Divisor(A.chunks);
+    A.by_group = Divisor(A.group);
+    A.joined = static_cast<int32_t*>(a.workspace);
+    A.arrived = A.joined + 2 * max_ctas(c.head_dim);
+    A.joined_at = 2 * max_ctas(c.head_dim) * int64_t(part_floats(c.head_dim));
+    A.parts = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + counters_bytes(c.seqs, c.kv_heads * A.chunks, c.head_dim));
     A.q_token = a.q_token_stride, A.q_head = a.q_head_stride;
     A.o_token = a.out_token_stride, A.o_head = a.out_head_stride;
     A.scale_log2 = a.scale * 1.44269504088896341f;

@@ -39,7 +39,6 @@ namespace {
 __device__ int g_attention_status = 0;
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
-constexpr int kChunk = 16;              // query heads of a chunk
 constexpr int kPartRows = 32;           // rows of a part in the workspace
 constexpr int kMaxSms = 160;
 constexpr int kJoin = 16;               // parts that are joined at a time
@@ -61,6 +60,7 @@ struct Plan {
     static constexpr int kStage = 2 * kTokens * kRow;               // keys, then values
     static constexpr int kPerSM = kStage > 10000 ? 1 : kStage < 6000 ? 3 : 2;  // CTAs
     static constexpr int kRoom = 228 * 1024 / kPerSM - 1280;        // of an SM, less 1 KB a CTA and the static part
+    static constexpr int kChunk = 8 * NT;                           // query heads of a chunk
     static constexpr int kFixed = 2 * kWarps * kChunk * 4;          // the warps' maxima and sums
     static constexpr int kStages = (kRoom - kFixed) / (kWarps * (kStage + 4));
     static constexpr int kOutRow = D + 4;                           // floats of a joined row
@@ -99,10 +99,11 @@ struct Args {
     int64_t q_token, q_head, o_token, o_head;
     float scale_log2;
     int q_heads, group, chunks, window;
-    int together;    // key-value heads of a unit: 1, 2 or 4
-    int heads;       // (kv_heads / together) * chunks: head groups of a sequence
+    int together;    // head chunks of a unit: 1, 2 or 4
+    int heads;       // kv_heads * chunks / together: units' head groups of a sequence
+    int rows;        // query heads of a chunk (the last of a key-value head may have fewer)
     int span_log2;   // log2 of the tokens of a unit
-    Divisor by_page, by_ctas, by_chunks, by_group;  // page size, grid, chunks, group
+    Divisor by_page, by_ctas, by_chunks, by_rows;  // page size, grid, chunks, rows
     bool q_bf16;
 };
 
@@ -202,7 +203,7 @@ __device__ __forceinline__ float row_shift(float top) {
 template <int D, int CT, int NT>
 __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_attention_kernel(const Args A) {
     using P = Plan<D, CT, NT>;
-    constexpr int kTokens = P::kTokens, kSubs = kTokens / 16, kSteps = D / 16;
+    constexpr int kChunk = P::kChunk, kTokens = P::kTokens, kSubs = kTokens / 16, kSteps = D / 16;
     extern __shared__ __align__(128) uint8_t smem[];
     float* warp_max = reinterpret_cast<float*>(smem + P::kRing);  // [kWarps][kChunk]
     float* warp_sum = warp_max + kWarps * kChunk;                 // [kWarps][kChunk]
@@ -306,13 +307,12 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
     }
 
     // ---- the warp's ring of stages
-    const int sharers = kWarps / A.together;  // warps of a key-value head (a power of two)
-    const int my_tokens = (warp & (sharers - 1)) * kTokens, my_head = (warp * A.together) / kWarps;
-    auto kv_head = [&](int hc) { return A.by_chunks.quotient(hc) * A.together + my_head; };
+    const int sharers = kWarps / A.together;  // warps of a head chunk (a power of two)
+    const int my_tokens = (warp & (sharers - 1)) * kTokens, my_chunk = (warp * A.together) / kWarps;
     const uint32_t ring = smem_u32(smem) + warp * P::kStages * P::kStage;
     uint32_t* my_masks = masks + warp * P::kStages;
-    // The page table is read two units ahead of the copy: `next` and `after` are the next
-    // two units to copy, `ahead` the place of the one whose look-up comes next.
+    // The page table is read three units ahead of the copy: `next`, `after` and `later` are
+    // the next units to copy, `ahead` the place of the one whose look-up comes next.
     struct Ahead {
         int page, slot, kvh;  // of token lane % kTokens; the unit's key-value head
         bool in_range;
@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
         if (to_look <= 0) return;
         const int j = (ahead.tile << A.span_log2) + my_tokens + (lane & (kTokens - 1));
         u.in_range = j < ahead.n;
-        u.kvh = kv_head(ahead.hc);
+        u.kvh = A.by_chunks.quotient(ahead.hc * A.together + my_chunk);
         if (u.in_range) {
             const int tok = ahead.lo + j, p = A.by_page.quotient(tok);
             u.slot = tok - p * A.c.page_size;
@@ -332,9 +332,45 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
         }
         if (--to_look > 0) ahead.advance(A);
     };
-    Ahead next, after;
+    Ahead next, after, later;
     look_up(next);
     look_up(after);
+    look_up(later);
+
+    // ---- running softmax of this warp's tokens: columns 8 t + 2 (lane % 4) + {0, 1} are
+    // query heads; out[m][t] is rows (elements of the head) 16 m + quad and + 8
+    uint32_t qf[kSteps][NT][2];
+    float out[kSteps][NT][4];
+    float top[NT][2], sum[NT][2], factor[NT][2];
+    int kvh = 0, in_group = 0;  // this warp's key-value head, and its chunk's first query head in the group
+    bool fresh = true;
+    // The queries of a place are requested before its first rows are copied, or while the
+    // place before it is joined: behind the copies they would take microseconds.
+    auto load_q = [&](const Cursor& to) {
+        const int v = to.hc * A.together + my_chunk;
+        kvh = A.by_chunks.quotient(v);
+        in_group = (v - kvh * A.chunks) * kChunk;
+        const int rows = min(kChunk, A.group - in_group);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int row = 8 * t + quad;
+            const char* src = static_cast<const char*>(A.q) +
+                              2 * (to.b * A.q_token + (kvh * A.group + in_group + row) * A.q_head);
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+                // The MMA's k-columns 2 (lane % 4) + {0, 1} and those + 8 stand for these
+                // elements; E4M3 keys come four consecutive elements to a lane, so there both
+                // pairs are taken from four consecutive ones.
+                const int e = CT == kE4M3 ? 16 * s + 4 * in_quad : 16 * s + 2 * in_quad;
+                qf[s][t][0] = qf[s][t][1] = 0;
+                if (row < rows) {
+                    qf[s][t][0] = *reinterpret_cast<const uint32_t*>(src + 2 * e);
+                    qf[s][t][1] = *reinterpret_cast<const uint32_t*>(src + 2 * (e + (CT == kE4M3 ? 2 : 8)));
+                }
+            }
+        }
+    };
+    load_q(at);
     auto copy_unit = [&](int stage) {
         const bool ok = next.in_range && next.page >= 0 && next.page < A.c.pages;
         if (next.in_range && !ok) atomicExch(&g_attention_status, int(W4A4_ERR_INDEX));
@@ -360,16 +396,10 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
         }
         --to_put;
         next = after;
-        look_up(after);
+        after = later;
+        look_up(later);
     };
 
-    // ---- running softmax of this warp's tokens: columns 8 t + 2 (lane % 4) + {0, 1} are
-    // query heads; out[m][t] is rows (elements of the head) 16 m + quad and + 8
-    uint32_t qf[kSteps][NT][2];
-    float out[kSteps][NT][4];
-    float top[NT][2], sum[NT][2], factor[NT][2];
-    int rows = 0;
-    bool fresh = true;
     int stage = 0, fill = 0;
     for (int it = 1 - P::kStages; it < count; ++it) {  // the first kStages - 1 steps only copy
         if (to_put > 0) copy_unit(fill);
@@ -377,29 +407,11 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
         if (++fill == P::kStages) fill = 0;
         if (it < 0) continue;
 
-        const int kvh = kv_head(at.hc), in_group = (at.hc - A.by_chunks.quotient(at.hc) * A.chunks) * kChunk;
-        const int row0 = kvh * A.group + in_group;  // this warp's first query head
         if (fresh) {
             fresh = false;
-            rows = min(kChunk, A.group - in_group);
             const float ks = CT == kE4M3 && A.c.k_scale ? A.c.k_scale[kvh] : 1.f;
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                const int row = 8 * t + quad;
-                const char* src = static_cast<const char*>(A.q) + 2 * (at.b * A.q_token + (row0 + row) * A.q_head);
-#pragma unroll
-                for (int s = 0; s < kSteps; ++s) {
-                    // The MMA's k-columns 2 (lane % 4) + {0, 1} and those + 8 stand for these
-                    // elements; E4M3 keys come four consecutive elements to a lane, so
-                    // there both pairs are taken from four consecutive ones.
-                    const int e = CT == kE4M3 ? 16 * s + 4 * in_quad : 16 * s + 2 * in_quad;
-                    uint32_t lo = 0, hi = 0;
-                    if (row < rows) {
-                        lo = *reinterpret_cast<const uint32_t*>(src + 2 * e);
-                        hi = *reinterpret_cast<const uint32_t*>(src + 2 * (e + (CT == kE4M3 ? 2 : 8)));
-                    }
-                    qf[s][t][0] = lo, qf[s][t][1] = hi;
-                }
                 float shift = 1.f;
                 if (CT == kE4M3 && A.q_bf16) {
                     float big = 0.f;
@@ -588,33 +600,42 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
                     }
                 }
             }
+        const Cursor was = at;
+        const int seg = seq_tiles * A.heads + was.hc * was.tiles;  // its first unit
+        if (it + 1 < count) {
+            at.tile = at.tiles;
+            at.advance(A);
+            if (at.b != was.b) seq_tiles += was.tiles;
+            load_q(at);
+        }
         __syncthreads();
 
-        const int seg = seq_tiles * A.heads + at.hc * at.tiles;  // its first unit
-        const bool whole = seg >= first && seg + at.tiles <= first + count;
+        const bool whole = seg >= first && seg + was.tiles <= first + count;
         int c0 = 0, c1 = 0;  // the CTAs that share it
-        int first_slot = 0;  // of c0: 1 if its run starts with another (sequence, head)
+        int first_slot = 0;  // of c0: 1 if its run starts with another (sequence, head group)
         if (!whole) {
             c0 = share.owner(seg);
-            c1 = share.owner(seg + at.tiles - 1);
+            c1 = share.owner(seg + was.tiles - 1);
             first_slot = share.start(c0) < seg ? 1 : 0;
         }
         constexpr int kPart = kPartRows * (D + 2);
         auto slot_of = [&](int c) { return 2 * c + (c == c0 ? first_slot : 0); };
         auto part_of = [&](int c) { return A.parts + int64_t(slot_of(c)) * kPart; };
-        const int all_rows = A.together * rows, items = all_rows * (D / 4);
-        // row r is query head `row` of key-value head hh of the unit's; rows = group where there are several
-        auto head_in_unit = [&](int r) { return A.together == 1 ? 0 : A.by_group.quotient(r); };
-        const int unit_head = kvh - my_head;
+        // Row r is query head `row` of the unit's head chunk `chunk`, which a last chunk may lack.
+        const int items = A.together * A.rows * (D / 4);
+        auto chunk_of = [&](int r) { return A.together == 1 ? 0 : A.by_rows.quotient(r); };
         auto write = [&](int r, int e, const float4& o, float m, float l) {
-            const int hh = head_in_unit(r), h = (unit_head + hh) * A.group + in_group + r - hh * rows;
-            const float vs = CT == kE4M3 && A.c.v_scale ? A.c.v_scale[unit_head + hh] : 1.f;
+            const int chunk = chunk_of(r), v = was.hc * A.together + chunk, head = A.by_chunks.quotient(v);
+            const int in = (v - head * A.chunks) * kChunk + r - chunk * A.rows;  // in the head's group
+            if (in >= A.group) return;
+            const int h = head * A.group + in;
+            const float vs = CT == kE4M3 && A.c.v_scale ? A.c.v_scale[head] : 1.f;
             const float inv = l == 0.f ? 0.f : vs / l;
-            uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<char*>(A.out) + 2 * (at.b * A.o_token + h * A.o_head + e));
+            uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<char*>(A.out) + 2 * (was.b * A.o_token + h * A.o_head + e));
             const float x0 = o.x * inv, x1 = o.y * inv, x2 = o.z * inv, x3 = o.w * inv;
             *reinterpret_cast<uint2*>(dst) = A.q_bf16 ? make_uint2(BF16::down(x0, x1), BF16::down(x2, x3))
                                                       : make_uint2(F16::down(x0, x1), F16::down(x2, x3));
-            if (A.lse && e == 0) A.lse[int64_t(at.b) * A.q_heads + h] = (m + log2f(l)) * 0.693147180559945309f;
+            if (A.lse && e == 0) A.lse[int64_t(was.b) * A.q_heads + h] = (m + log2f(l)) * 0.693147180559945309f;
         };
         auto leave = [&](float* part, int r, int e, const float4& o, float m, float l) {
             *reinterpret_cast<float4*>(part + r * D + e) = o;
@@ -622,13 +643,13 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
         };
 #pragma unroll 1
         for (int i = tid; i < items; i += kThreads) {
-            const int r = i / (D / 4), e = i % (D / 4) * 4, hh = head_in_unit(r), row = r - hh * rows;
+            const int r = i / (D / 4), e = i % (D / 4) * 4, chunk = chunk_of(r), row = r - chunk * A.rows;
             float wm[kWarps], wl[kWarps];
             float4 wo[kWarps];
             float m = -INFINITY, l = 0.f;
 #pragma unroll
             for (int k = 0; k < kWarps; ++k) {
-                const int w = hh * sharers + k;
+                const int w = chunk * sharers + k;
                 wm[k] = -INFINITY, wl[k] = 0.f;
                 wo[k] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (k < sharers) {
@@ -672,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
             const int width = min(items, kThreads), ways = kThreads / width, my_way = tid / width, my_item = tid - my_way * width;
             for (int level = 0; level < 2; ++level) {
                 if (!(level == 0 ? arrive(A.joined + slot_of(c_first), in_sixteen)
-                                 : arrive(A.arrived + int64_t(at.b) * A.heads + at.hc, sixteens)))
+                                 : arrive(A.arrived + int64_t(was.b) * A.heads + was.hc, sixteens)))
                     break;
                 const int from = level == 0 ? c_first : c0;
                 const int step = level == 0 ? 1 : kJoin, parts = level == 0 ? in_sixteen : sixteens;
@@ -742,21 +763,16 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
             }
         }
 
-        if (it + 1 < count) {
-            const int was = at.b, tiles = at.tiles;
-            at.advance(A);
-            if (at.b != was) seq_tiles += tiles;
-        }
     }
 }
 
 // CTAs of a launch at most: as many as the plan of any cache type puts on an SM.
 constexpr int max_ctas(int head_dim) { return kMaxSms * (head_dim == 64 ? 3 : head_dim == 256 ? 1 : 2); }
+int most_groups(int q_heads, int kv_heads) { return kv_heads * ((q_heads / kv_heads + 7) / 8); }  // of a sequence
 size_t part_floats(int head_dim) { return size_t(kPartRows) * (head_dim + 2); }
 size_t counters_bytes(int seqs, int heads, int head_dim) {
     return align256((size_t(seqs) * heads + 2 * max_ctas(head_dim)) * 4);
 }
-int chunks_of(int group) { return (group + kChunk - 1) / kChunk; }
 
 template <int D, int CT, int NT>
 w4a4_status launch_n(Args& A, cudaStream_t s) {
@@ -774,18 +790,25 @@ w4a4_status launch_n(Args& A, cudaStream_t s) {
     const int64_t keys = A.window > 0 && A.window < longest ? A.window : longest;
     int64_t full = P::kPerSM * int64_t(device_sm_count());  // CTAs the GPU holds at once
     if (full > max_ctas(D)) full = max_ctas(D);
-    // Heads side by side: the four warps take four heads (two, where NT or kv_heads leaves no
-    // more) of the same tokens.  With heads that are adjacent rows, what they fetch together
-    // is one long row (64-byte rows: 3.5 TB/s alone); with sequences of no more than one
-    // head's unit, no warp is left without tokens and there is nothing to join.  In between,
-    // it would make (sequence, head group) pairs fewer and their splits, so the joins, longer.
+    A.chunks = (A.group + P::kChunk - 1) / P::kChunk;
+    A.rows = A.group < P::kChunk ? A.group : P::kChunk;
+    A.by_chunks = Divisor(A.chunks);
+    A.by_rows = Divisor(A.rows);
+    const int chunks = A.c.kv_heads * A.chunks;  // of a sequence
+    // Head chunks side by side: the warps take two or four of them and the same tokens.
+    // Chunks of one head read the same rows, which then come from HBM once.  Heads that are
+    // adjacent rows make one long row of what the warps fetch together (64-byte rows alone:
+    // 3.5 TB/s).  With sequences of one step and more of them than CTAs, no warp is left
+    // without tokens.  In between, it would make (sequence, head group) pairs fewer and
+    // their splits, so the joins, longer.
     A.together = 1;
     const bool adjacent = A.c.k_head_stride == D && A.c.v_head_stride == D;
-    const int64_t all = int64_t(A.c.seqs) * A.c.kv_heads * keys;
-    if (A.chunks == 1 && ((adjacent && all > 16 * full * kWarps * P::kTokens) || keys <= kWarps * P::kTokens))
-        while (A.together < kPartRows / (8 * NT) && A.together < kWarps && A.c.kv_heads % (2 * A.together) == 0)
+    const int64_t work = int64_t(A.c.seqs) * chunks * keys;
+    if (A.chunks > 1 || (adjacent && work > 16 * full * kWarps * P::kTokens) ||
+        (keys <= P::kTokens && int64_t(A.c.seqs) * chunks > full))
+        while (A.together < kPartRows / P::kChunk && A.together < kWarps && chunks % (2 * A.together) == 0)
             A.together *= 2;
-    A.heads = A.c.kv_heads / A.together * A.chunks;
+    A.heads = chunks / A.together;
     A.span_log2 = A.together == 1 ? 2 : A.together == 2 ? 1 : 0;
     A.span_log2 += P::kTokens == 32 ? 5 : 4;
     const int64_t span = int64_t(1) << A.span_log2;
@@ -812,7 +835,11 @@ w4a4_status launch_n(Args& A, cudaStream_t s) {
 
 template <int D, int CT>
 w4a4_status launch_c(Args& A, cudaStream_t s) {
-    return A.group > 8 ? launch_n<D, CT, 2>(A, s) : launch_n<D, CT, 1>(A, s);
+    // 16 heads a chunk where the group has more than 8; at D = 256 their output alone would
+    // take 128 registers, and two chunks of 8 side by side are faster MEASURED
+    if constexpr (D < 256)
+        if (A.group > 8) return launch_n<D, CT, 2>(A, s);
+    return launch_n<D, CT, 1>(A, s);
 }
 
 template <int D>
@@ -827,8 +854,7 @@ w4a4_status launch_d(Args& A, cudaStream_t s) {
 w4a4_status attention_read_and_clear_status() { return take_status_word(g_attention_status); }
 
 size_t attention_workspace_bytes(int seqs, int q_heads, int kv_heads, int head_dim) {
-    const int heads = kv_heads * chunks_of(q_heads / kv_heads);
-    return counters_bytes(seqs, heads, head_dim) + 4 * max_ctas(head_dim) * part_floats(head_dim) * 4;
+    return counters_bytes(seqs, most_groups(q_heads, kv_heads), head_dim) + 4 * max_ctas(head_dim) * part_floats(head_dim) * 4;
 }
 
 w4a4_status launch_paged_attention(const w4a4_kv_cache& c, const w4a4_paged_attention_args& a, cudaStream_t s) {
@@ -837,7 +863,6 @@ w4a4_status launch_paged_attention(const w4a4_kv_cache& c, const w4a4_paged_atte
     A.q = a.q, A.out = a.out, A.lse = a.lse, A.lengths = a.lengths;
     A.q_heads = a.q_heads;
     A.group = a.q_heads / c.kv_heads;
-    A.chunks = chunks_of(A.group);
     A.window = a.window;
     A.longest = c.max_pages * c.page_size;
     const int size = c.dtype == W4A4_E4M3 ? 1 : 2;  // strides are at most 2^29 elements
@@ -845,12 +870,10 @@ w4a4_status launch_paged_attention(const w4a4_kv_cache& c, const w4a4_paged_atte
     A.token_stride[0] = int(c.k_token_stride * size), A.token_stride[1] = int(c.v_token_stride * size);
     A.head_stride[0] = int(c.k_head_stride * size), A.head_stride[1] = int(c.v_head_stride * size);
     A.by_page = Divisor(c.page_size);
-    A.by_chunks = Divisor(A.chunks);
-    A.by_group = Divisor(A.group);
     A.joined = static_cast<int32_t*>(a.workspace);
     A.arrived = A.joined + 2 * max_ctas(c.head_dim);
     A.joined_at = 2 * max_ctas(c.head_dim) * int64_t(part_floats(c.head_dim));
-    A.parts = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + counters_bytes(c.seqs, c.kv_heads * A.chunks, c.head_dim));
+    A.parts = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + counters_bytes(c.seqs, most_groups(a.q_heads, c.kv_heads), c.head_dim));
     A.q_token = a.q_token_stride, A.q_head = a.q_head_stride;
     A.o_token = a.out_token_stride, A.o_head = a.out_head_stride;
     A.scale_log2 = a.scale * 1.44269504088896341f;

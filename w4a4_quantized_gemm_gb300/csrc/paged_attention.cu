@@ -41,6 +41,7 @@ __device__ int g_attention_status = 0;
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kPartRows = 32;           // rows of a part in the workspace
 constexpr int kMaxSms = 160;
+constexpr int kFewUnits = 8;            // runs shorter than this are single pieces
 constexpr int kJoin = 16;               // parts that are joined at a time
 
 enum Cache { kF16, kBF16, kE4M3 };
@@ -132,11 +133,11 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
     else
         mma_f16_16816(d, a, b0, b1);
 }
-// Two E4M3 bytes (low 16 bits) -> fp16 pair, exact.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
-    uint32_t d;
-    asm("{\n.reg .b16 t;\ncvt.u16.u32 t, %1;\ncvt.rn.f16x2.e4m3x2 %0, t;\n}\n" : "=r"(d) : "r"(two));
-    return d;
+// Four E4M3 bytes -> two fp16 pairs (bytes 0, 1 and 2, 3), exact.
+__device__ __forceinline__ void e4m3x4_to_f16x2(uint32_t four, uint32_t& low, uint32_t& high) {
+    asm("{\n.reg .b16 a, b;\nmov.b32 {a, b}, %2;\ncvt.rn.f16x2.e4m3x2 %0, a;\ncvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
+        : "=r"(low), "=r"(high)
+        : "r"(four));
 }
 __device__ __forceinline__ float exp2_approx(float x) {  // 2 ulp; 2^-inf = 0
     float y;
@@ -220,8 +221,13 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
     // ---- this CTA's run of units: a scan over the sequences' tile counts.  Up to 32
     // sequences each warp does it for itself, a lane a sequence; more are shared out to the
     // CTA's threads, several in a row to each.
+    // A run of few units, though, is one piece of one (sequence, head group), so that a CTA
+    // has one part to leave and one join to take part in: pieces of at most `piece` units,
+    // the least for which there are CTAs enough (8 sequences of 700 tokens: 9.2 us, 10.8
+    // with runs over two (sequence, head group)s).
     int first, count;
     Share share;
+    int piece = 0, c0 = 0, c1 = 0;  // piece > 0: the CTAs that share this one's (sequence, head group)
     Cursor at;
     int seq_tiles;  // tiles of the sequences before at.b
     {
@@ -272,20 +278,59 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
                 if (A.lse)
                     for (int h = tid; h < A.q_heads; h += kThreads) A.lse[int64_t(b) * A.q_heads + h] = -INFINITY;
             }
-        if (int(blockIdx.x) >= total) return;
+        if (total == 0) return;
         share.each = total < int(gridDim.x) ? 1 : A.by_ctas.quotient(total);
         share.more = total < int(gridDim.x) ? 0 : total - share.each * int(gridDim.x);
         first = share.start(blockIdx.x);
         count = share.start(blockIdx.x + 1) - first;
         int before = upto - mine;
         const bool here = before * A.heads <= first && first < upto * A.heads;
-        if (few) {
+        const int groups = __popc(__ballot_sync(0xffffffffu, mine > 0)) * A.heads;  // (few)
+        if (few && total > int(gridDim.x) && share.each < kFewUnits && groups <= int(gridDim.x)) {
+            int pieces = 0;
+            piece = share.each + (share.more > 0);
+            for (int tries = 0; tries < 8; ++tries) {
+                pieces = (mine + piece - 1) / piece;  // of this lane's sequence, per head group
+                int all = pieces;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+                all *= A.heads;
+                if (all <= int(gridDim.x)) break;
+                piece = tries < 7 ? max(piece + 1, A.by_ctas.quotient(piece * all)) : 0;
+            }
+            if (piece > 0) {
+                int upto_pieces = pieces;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int v = __shfl_up_sync(0xffffffffu, upto_pieces, o);
+                    if (lane >= o) upto_pieces += v;
+                }
+                const int c = blockIdx.x, from = (upto_pieces - pieces) * A.heads;  // CTAs before the sequence's
+                const uint32_t mine_is = __ballot_sync(0xffffffffu, from <= c && c < upto_pieces * A.heads);
+                if (mine_is == 0) return;
+                at.b = __ffs(mine_is) - 1;
+                seq_tiles = __shfl_sync(0xffffffffu, before, at.b);
+                at.lo = __shfl_sync(0xffffffffu, lo, at.b);
+                at.n = __shfl_sync(0xffffffffu, n, at.b);
+                at.tiles = __shfl_sync(0xffffffffu, mine, at.b);
+                pieces = __shfl_sync(0xffffffffu, pieces, at.b);
+                const int in = c - __shfl_sync(0xffffffffu, from, at.b);
+                at.hc = in / pieces;
+                const int k = in - at.hc * pieces;
+                c0 = c - k, c1 = c0 + pieces - 1;
+                at.tile = at.tiles * k / pieces;
+                count = at.tiles * (k + 1) / pieces - at.tile;
+                first = (seq_tiles * A.heads) + at.hc * at.tiles + at.tile;
+            }
+        }
+        if (piece == 0 && int(blockIdx.x) >= total) return;
+        if (piece == 0 && few) {
             at.b = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
             seq_tiles = __shfl_sync(0xffffffffu, before, at.b);
             at.lo = __shfl_sync(0xffffffffu, lo, at.b);
             at.n = __shfl_sync(0xffffffffu, n, at.b);
             at.tiles = __shfl_sync(0xffffffffu, mine, at.b);
-        } else {
+        } else if (piece == 0) {
             if (here) {
                 int seq = b0;
                 for (; seq < b1; ++seq) {
@@ -301,9 +346,11 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
             seq_tiles = s_prefix;
             at.enter(A);
         }
-        const int in = first - seq_tiles * A.heads;
-        at.hc = in / at.tiles;
-        at.tile = in - at.hc * at.tiles;
+        if (piece == 0) {
+            const int in = first - seq_tiles * A.heads;
+            at.hc = in / at.tiles;
+            at.tile = in - at.hc * at.tiles;
+        }
     }
 
     // ---- the warp's ring of stages
@@ -467,9 +514,9 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
                         tc::ldsm_x4(r, base + st * 16);
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            const uint32_t a[4] = {e4m3x2_to_f16x2(r[2 * h] & 0xffffu),
-                                                   e4m3x2_to_f16x2(r[2 * h + 1] & 0xffffu),
-                                                   e4m3x2_to_f16x2(r[2 * h] >> 16), e4m3x2_to_f16x2(r[2 * h + 1] >> 16)};
+                            uint32_t a[4];
+                            e4m3x4_to_f16x2(r[2 * h], a[0], a[2]);
+                            e4m3x4_to_f16x2(r[2 * h + 1], a[1], a[3]);
 #pragma unroll
                             for (int t = 0; t < NT; ++t) mma<CT>(s[u][t], a, qf[st + h][t][0], qf[st + h][t][1]);
                         }
@@ -488,17 +535,20 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
             // maximum is only renewed when a score exceeds it by more than 8: up to there a
             // probability (at most 2^8) is as exact in its type, and the reduction over the
             // warp and the rescaling of the output are left out of most steps.
+            constexpr uint32_t kFull = kTokens == 32 ? 0xffffffffu : 0xffffu;
             bool over = false;
 #pragma unroll
-            for (int u = 0; u < kSubs; ++u)
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
+                for (int j = 0; j < 4; ++j) {
+                    const float limit = top[t][j & 1] + 8.f;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        float& v = s[u][t][j];
-                        v = mask >> (16 * u + 8 * (j >> 1) + quad) & 1 ? v * factor[t][j & 1] : -INFINITY;
-                        over |= v > top[t][j & 1] + 8.f;
+                    for (int u = 0; u < kSubs; ++u) {
+                        s[u][t][j] *= factor[t][j & 1];
+                        if (mask != kFull && !(mask >> (16 * u + 8 * (j >> 1) + quad) & 1)) s[u][t][j] = -INFINITY;
+                        over |= s[u][t][j] > limit;
                     }
+                }
             if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
@@ -545,9 +595,9 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
                         ldmatrix4_trans(r, base + m * 16);
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            const uint32_t x = prmt(r[2 * h], 0u, 0x3120u), y = prmt(r[2 * h + 1], 0u, 0x3120u);
-                            const uint32_t a[4] = {e4m3x2_to_f16x2(x & 0xffffu), e4m3x2_to_f16x2(x >> 16),
-                                                   e4m3x2_to_f16x2(y & 0xffffu), e4m3x2_to_f16x2(y >> 16)};
+                            uint32_t a[4];
+                            e4m3x4_to_f16x2(prmt(r[2 * h], 0u, 0x3120u), a[0], a[1]);
+                            e4m3x4_to_f16x2(prmt(r[2 * h + 1], 0u, 0x3120u), a[2], a[3]);
 #pragma unroll
                             for (int t = 0; t < NT; ++t) mma<CT>(out[m + h][t], a, pf[u][t][0], pf[u][t][1]);
                         }
@@ -611,9 +661,8 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
         __syncthreads();
 
         const bool whole = seg >= first && seg + was.tiles <= first + count;
-        int c0 = 0, c1 = 0;  // the CTAs that share it
         int first_slot = 0;  // of c0: 1 if its run starts with another (sequence, head group)
-        if (!whole) {
+        if (!whole && piece == 0) {
             c0 = share.owner(seg);
             c1 = share.owner(seg + was.tiles - 1);
             first_slot = share.start(c0) < seg ? 1 : 0;
@@ -796,15 +845,19 @@ w4a4_status launch_n(Args& A, cudaStream_t s) {
     A.by_rows = Divisor(A.rows);
     const int chunks = A.c.kv_heads * A.chunks;  // of a sequence
     // Head chunks side by side: the warps take two or four of them and the same tokens.
-    // Chunks of one head read the same rows, which then come from HBM once.  Heads that are
-    // adjacent rows make one long row of what the warps fetch together (64-byte rows alone:
-    // 3.5 TB/s).  With sequences of one step and more of them than CTAs, no warp is left
-    // without tokens.  In between, it would make (sequence, head group) pairs fewer and
-    // their splits, so the joins, longer.
+    //  * Chunks of one head read the same rows, which then come from HBM once.
+    //  * Short rows of adjacent heads make one longer row of what the warps fetch together:
+    //    64 sequences of 8192 tokens, E4M3, D = 64: 101 us, one head at a time 137 us;
+    //    D = 96, fp16: 270 and 348 us.  From 256-byte rows on it makes no difference (D = 128,
+    //    fp16: 685 and 686 us at 128 sequences), and where there is less work it makes (sequence, head
+    //    group) pairs fewer and their splits, so the joins, longer (8 x 5000 tokens, D = 128:
+    //    40 and 34 us).
+    //  * With sequences of one step, and more of them than CTAs, no warp is left without
+    //    tokens (128 sequences of 4 tokens: 4.9 and 12.7 us).
     A.together = 1;
-    const bool adjacent = A.c.k_head_stride == D && A.c.v_head_stride == D;
+    const bool adjacent = P::kRowBytes < 256 && A.c.k_head_stride == D && A.c.v_head_stride == D;
     const int64_t work = int64_t(A.c.seqs) * chunks * keys;
-    if (A.chunks > 1 || (adjacent && work > 16 * full * kWarps * P::kTokens) ||
+    if (A.chunks > 1 || (adjacent && work > 64 * full * kWarps * P::kTokens) ||
         (keys <= P::kTokens && int64_t(A.c.seqs) * chunks > full))
         while (A.together < kPartRows / P::kChunk && A.together < kWarps && chunks % (2 * A.together) == 0)
             A.together *= 2;
@@ -836,7 +889,8 @@ w4a4_status launch_n(Args& A, cudaStream_t s) {
 template <int D, int CT>
 w4a4_status launch_c(Args& A, cudaStream_t s) {
     // 16 heads a chunk where the group has more than 8; at D = 256 their output alone would
-    // take 128 registers, and two chunks of 8 side by side are faster MEASURED
+    // take 128 registers, and two chunks of 8 side by side are faster (64 sequences of 8192
+    // tokens, groups of 16, fp16: 1084 us against 1345)
     if constexpr (D < 256)
         if (A.group > 8) return launch_n<D, CT, 2>(A, s);
     return launch_n<D, CT, 1>(A, s);

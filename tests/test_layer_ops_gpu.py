@@ -209,6 +209,42 @@ def test_attention_long_split_and_joined(dtype, hkv, group):
         assert torch.equal(again.view(torch.int16), out.view(torch.int16)) and torch.equal(lse2, lse)
 
 
+@pytest.mark.parametrize("lengths, hkv, group, dim", [
+    ([700, 650, 1, 0, 702, 700, 699, 688], 8, 2, 128),   # runs of two or three units: single pieces
+    ([3000] * 3, 16, 1, 64), ([5000, 40], 2, 16, 96), ([2000], 1, 11, 256),
+    ([4096] * 6, 8, 1, 128),                             # runs over two sequences' heads
+    ([1] * 40, 8, 1, 64), ([16] * 45, 4, 2, 128),        # one step a sequence, more of them than CTAs
+])
+@pytest.mark.parametrize("dtype", [F16, E4M3])
+def test_attention_shares_of_the_work(lengths, hkv, group, dim, dtype):
+    """Each way the units are shared out among the CTAs, and its joins."""
+    c = Cache(lengths, 16, hkv, dim, dtype, seed=sum(lengths) + dim)
+    check_attention(c, randn(gen(30), len(lengths), hkv * group, dim).to(F16), lengths)
+
+
+def test_attention_heads_side_by_side_and_defaults():
+    """A page table wide enough for the heads of short adjacent rows to be taken together; E4M3
+    without scales; a negative scale."""
+    lengths = [100, 3, 900, 64, 0]
+    for dtype, dim, hkv in ((F16, 64, 4), (E4M3, 64, 6), (BF16, 96, 2), (E4M3, 128, 8)):
+        c = Cache(lengths, 64, hkv, dim, dtype, seed=31, scales=False, wide=40000)
+        q = (0.1 * randn(gen(32), 5, 3 * hkv, dim) if dtype == E4M3 else randn(gen(32), 5, 3 * hkv, dim))
+        check_attention(c, q.to(BF16 if dtype == BF16 else F16), lengths, what=f"{dtype} {dim}")
+    assert "heads/unit=" in w4.w4a4_last_dispatch()
+    c = Cache(lengths, 64, 2, 64, F16, seed=33)
+    q = randn(gen(34), 5, 4, 64).to(F16)
+    out, _ = attend(c, q, lengths, scale=-0.1)
+    want, _ = attend(c, -q, lengths, scale=0.1)
+    assert torch.equal(out, want)
+
+
+def test_attention_refuses_more_units_than_it_can_number():
+    """Sizes alone, on the host: nothing is launched, so the pointers are never used."""
+    args = w4._ATTENTION.pack(w4._ATTENTION.size, 256, 256, 0, 256, 256, 1 << 40, 128 * 64, 64, 128 * 64, 64, 0.1, 128, 0, 0)
+    cache = w4._CACHE.pack(w4._CACHE.size, 256, 256, 0, 0, 256, *(1024, 64, 64) * 2, 1 << 27, 64, 1 << 27, 8, 8, 128, 64, 0, 0)
+    assert w4.lib().w4a4_paged_attention(cache, args, None) == 2
+
+
 def test_attention_extreme_scores():
     """Scores up to +-1e4 (one token takes all), queries beyond fp16's range against an 8-bit cache."""
     lengths = [100, 1, 700]

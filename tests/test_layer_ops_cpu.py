@@ -10,6 +10,7 @@ import pytest
 import torch
 
 import w4a4_quantized_gemm_gb300 as w4
+from tests.layer_structs import FORMATS, fields, pack
 from w4a4_quantized_gemm_gb300 import build as wbuild
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -23,48 +24,34 @@ def L():
     return w4.lib()
 
 
-def _fields(name):
-    """Field names of a struct of the header, in order."""
-    src = open(os.path.join(ROOT, "include", "w4a4.h")).read()
-    src = re.sub(r"/\*.*?\*/", "", src, flags=re.S)
-    body = re.search(r"typedef struct \{([^}]*)\} %s;" % name, src).group(1)
-    return [re.sub(r".*[ *]", "", part.strip()) for line in body.split(";") for part in line.split(",") if part.strip()]
-
-
-def _pack(fmt, name, values):
-    names = _fields(name)
-    assert set(values) <= set(names), set(values) - set(names)
-    return fmt.pack(*[values.get(n, 0) for n in names])
-
-
 def cache(**over):
     d, size = over.get("head_dim", 128), 1 if over.get("dtype") == 3 else 2
-    v = dict(bytes=w4._CACHE.size, k=A, v=A, page_table=A, k_page_stride=16 * 8 * d, k_token_stride=8 * d,
+    v = dict(k=A, v=A, page_table=A, k_page_stride=16 * 8 * d, k_token_stride=8 * d,
              k_head_stride=d, v_page_stride=16 * 8 * d, v_token_stride=8 * d, v_head_stride=d, table_stride=10,
              seqs=4, max_pages=10, pages=40, page_size=16, kv_heads=8, head_dim=d, dtype=0)
     assert d * size % 16 == 0 or "k_head_stride" in over
-    return _pack(w4._CACHE, "w4a4_kv_cache", {**v, **over})
+    return pack("w4a4_kv_cache", **{**v, **over})
 
 
 def append(**over):
-    v = dict(bytes=w4._APPEND.size, q=A, k=A, v=A, q_out=A + 64, positions=A, rope=A, q_token_stride=4096,
+    v = dict(q=A, k=A, v=A, q_out=A + 64, positions=A, rope=A, q_token_stride=4096,
              q_head_stride=128, k_token_stride=4096, k_head_stride=128, v_token_stride=4096, v_head_stride=128,
              out_token_stride=2048, out_head_stride=128, tokens=4, q_heads=16, dtype=0, rope_rows=100, rot_dim=128,
              eps=1e-6)
-    return _pack(w4._APPEND, "w4a4_kv_append_args", {**v, **over})
+    return pack("w4a4_kv_append_args", **{**v, **over})
 
 
 def attention(**over):
-    v = dict(bytes=w4._ATTENTION.size, q=A, out=A, lengths=A, workspace=A, workspace_bytes=1 << 40,
+    v = dict(q=A, out=A, lengths=A, workspace=A, workspace_bytes=1 << 40,
              q_token_stride=2048, q_head_stride=128, out_token_stride=2048, out_head_stride=128, scale=0.1,
              q_heads=16, dtype=0)
-    return _pack(w4._ATTENTION, "w4a4_paged_attention_args", {**v, **over})
+    return pack("w4a4_paged_attention_args", **{**v, **over})
 
 
 def norm(**over):
-    v = dict(bytes=w4._BLOCK_NORM.size, y=A, r=A, r_out=A, x=A, y_stride=1024, r_stride=1024, r_out_stride=1024,
+    v = dict(y=A, r=A, r_out=A, x=A, y_stride=1024, r_stride=1024, r_out_stride=1024,
              x_stride=1024, rows=4, width=1024, dtype=0, res_dtype=0, post=1, pre=1, scale=1.0, eps=1e-6)
-    return _pack(w4._BLOCK_NORM, "w4a4_block_norm_args", {**v, **over})
+    return pack("w4a4_block_norm_args", **{**v, **over})
 
 
 def test_struct_layouts_match_the_header(tmp_path):
@@ -73,21 +60,21 @@ def test_struct_layouts_match_the_header(tmp_path):
         r"#include <cuda_runtime_api.h>", "", open(os.path.join(ROOT, "include", "w4a4.h")).read()) +
         "int main(void) {\n" + "".join(
             'printf("%s.%s %%zu\\n", offsetof(%s, %s));\n' % (n, f, n, f) for n in
-            ("w4a4_kv_cache", "w4a4_kv_append_args", "w4a4_paged_attention_args", "w4a4_block_norm_args")
-            for f in _fields(n)) + "return 0; }\n")
+            FORMATS
+            for f in fields(n)) + "return 0; }\n")
     exe = tmp_path / "sizes"
     subprocess.run(["gcc", "-o", str(exe), str(src)], check=True)
     want = dict(l.split() for l in subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.splitlines())
-    for fmt, name in ((w4._CACHE, "w4a4_kv_cache"), (w4._APPEND, "w4a4_kv_append_args"),
-                      (w4._ATTENTION, "w4a4_paged_attention_args"), (w4._BLOCK_NORM, "w4a4_block_norm_args")):
+    for name, fmt in FORMATS.items():
         codes = [c for n, c in re.findall(r"(\d*)([Qqif])", fmt.format) for _ in range(int(n or 1))]
-        names = _fields(name)
+        names = fields(name)
         assert len(codes) == len(names), name
         at = 0
         for c, f in zip(codes, names):
             assert int(want[f"{name}.{f}"]) == at, f"{name}.{f}"
             at += 8 if c in "Qq" else 4
         assert at == fmt.size
+    assert w4._CACHE.format == FORMATS["w4a4_kv_cache"].format
 
 
 @pytest.mark.parametrize("over, status", [
@@ -180,7 +167,7 @@ def test_rope_table_refusals(L):
     assert L.w4a4_rope_table(None, 0, 128, 1e6, None) == 0
 
 
-def test_binding_refuses_tensors_it_cannot_describe():
+def test_binding_refuses_tensors_it_cannot_describe(L):
     """On the host, from shapes and types alone: no device is touched."""
     k = torch.zeros(2, 16, 8, 128, dtype=torch.float16)
     table = torch.zeros(1, 2, dtype=torch.int32)
@@ -189,9 +176,11 @@ def test_binding_refuses_tensors_it_cannot_describe():
         with pytest.raises(w4.W4A4Error):
             w4.PagedKVCache(*args)
     y = torch.zeros(3, 64, dtype=torch.float16)
-    for args in ((y, y, y, y), (y, y[:2], y, y), (y, y, y[:, ::2], y)):
+    for args in ((y, y, y, y), (y, y[:2], y, y), (y, y, y[:, ::2], y), (None, y, y, y), (y, "r", y, y), (y.to_sparse(), y, y, y)):
         with pytest.raises(w4.W4A4Error):
             w4.w4a4_block_norm(*args)
+    with pytest.raises(TypeError):
+        w4._calls().block_norm(y)
 
 
 def test_status_string_of_the_index_status(L):

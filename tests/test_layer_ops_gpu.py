@@ -10,6 +10,7 @@ import pytest
 import torch
 
 import w4a4_quantized_gemm_gb300 as w4
+from tests.layer_structs import pack
 
 pytestmark = pytest.mark.gpu
 
@@ -240,8 +241,11 @@ def test_attention_heads_side_by_side_and_defaults():
 
 def test_attention_refuses_more_units_than_it_can_number():
     """Sizes alone, on the host: nothing is launched, so the pointers are never used."""
-    args = w4._ATTENTION.pack(w4._ATTENTION.size, 256, 256, 0, 256, 256, 1 << 40, 128 * 64, 64, 128 * 64, 64, 0.1, 128, 0, 0)
-    cache = w4._CACHE.pack(w4._CACHE.size, 256, 256, 0, 0, 256, *(1024, 64, 64) * 2, 1 << 27, 64, 1 << 27, 8, 8, 128, 64, 0, 0)
+    args = pack("w4a4_paged_attention_args", q=256, out=256, lengths=256, workspace=256, workspace_bytes=1 << 40,
+                q_token_stride=8192, q_head_stride=64, out_token_stride=8192, out_head_stride=64, scale=0.1, q_heads=128)
+    cache = pack("w4a4_kv_cache", k=256, v=256, page_table=256, k_page_stride=1024, k_token_stride=64, k_head_stride=64,
+                 v_page_stride=1024, v_token_stride=64, v_head_stride=64, table_stride=1 << 27, seqs=64,
+                 max_pages=1 << 27, pages=8, page_size=8, kv_heads=128, head_dim=64)
     assert w4.lib().w4a4_paged_attention(cache, args, None) == 2
 
 

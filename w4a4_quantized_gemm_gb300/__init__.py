@@ -113,9 +113,9 @@ def _ptr(t):
     return ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(stream, device=None):
-    if stream is None:  # the handle itself: building a torch.cuda.Stream object takes 3 us, longer than a launch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if device is None else device)
+def _stream(stream):
+    if stream is None:
+        stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
@@ -355,35 +355,24 @@ def w4a4_set_stream_k(on: bool):
 
 # ------------------------------------ paged cache, its attention, block norms
 _DTYPE = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2, torch.float8_e4m3fn: 3}  # w4a4_dtype
-# The argument structs of include/w4a4.h, field by field, each opening with its size.
-_CACHE = struct.Struct("=Q5Q7q8i")       # pointers; strides; sizes and type
-_APPEND = struct.Struct("=Q9Q8q6ifi")
-_ATTENTION = struct.Struct("=Q5QQ4qf3i")
-_BLOCK_NORM = struct.Struct("=Q9Q5q7iffi")
+_CACHE = struct.Struct("=Q5Q7q8i")  # w4a4_kv_cache: size, pointers, strides, sizes and type
+
+_native = None
+
+
+def _calls():
+    """The native entry of these operators (csrc/binding.cpp): it reads the tensors, checks them against
+    each other and calls the C ABI."""
+    global _native
+    if _native is None:
+        lib()  # raises if nothing is built
+        from . import _binding
+        _native = _binding
+    return _native
 
 
 def _refuse(where: str, status: int = 1):
     raise W4A4Error(status, where)
-
-
-# A call's host time is mostly these checks (a tensor attribute takes 0.1 us and a launch 2), so each
-# reads an attribute once and anything the C side checks as well is left to it.
-def _rows(t, where: str, heads: int, dim: int, dtype, device: int):
-    """Length, pointer and strides of a [rows, heads, dim] tensor whose last dimension is contiguous."""
-    n, h, d = t.shape
-    a, b, c = t.stride()
-    if h != heads or d != dim or c != 1 or t.dtype is not dtype or t.get_device() != device:
-        _refuse(where)
-    return n, t.data_ptr(), a, b
-
-
-def _vector(t, where: str, n: int, dtype, device: int) -> int:
-    """Pointer of a contiguous tensor of n elements, or 0 for None."""
-    if t is None:
-        return 0
-    if t.dtype is not dtype or t.numel() != n or t.get_device() != device or not t.is_contiguous():
-        _refuse(where)
-    return t.data_ptr()
 
 
 class PagedKVCache:
@@ -410,7 +399,11 @@ class PagedKVCache:
         self.pages, self.page_size, self.kv_heads, self.head_dim = k.shape
         self.seqs, self.max_pages = page_table.shape
         self.dtype = k.dtype
-        scales = [_vector(t, where, self.kv_heads, torch.float32, self.device) for t in (k_scale, v_scale)]
+        for t in (k_scale, v_scale):
+            if t is not None and (t.dtype != torch.float32 or t.numel() != self.kv_heads or not t.is_contiguous() or
+                                  t.get_device() != self.device):
+                _refuse(where)
+        scales = [0 if t is None else t.data_ptr() for t in (k_scale, v_scale)]
         self._keep = (k, v, page_table, k_scale, v_scale)
         self._struct = _CACHE.pack(_CACHE.size, k.data_ptr(), v.data_ptr(), *scales, page_table.data_ptr(),
                                    *k.stride()[:3], *v.stride()[:3], max(page_table.stride(0), self.max_pages),
@@ -449,28 +442,10 @@ def w4a4_kv_append(q, k, v, positions, cache, q_out, seqs=None, rope=None, q_gai
     contiguous (slices of a fused q|k|v output).  positions, seqs: int32 [tokens]; seqs None: token
     t belongs to sequence t, negative: padding.  rope: fp32 [rows, 2, rot_dim / 2]
     (w4a4_rope_table)."""
-    where = "w4a4_kv_append"
-    dtype, dim, dev, kvh = q.dtype, cache.head_dim, cache.device, cache.kv_heads
-    heads = q.shape[1]
-    tokens, qp, q0, q1 = _rows(q, where, heads, dim, dtype, dev)
-    nk, kp, k0, k1 = _rows(k, where, kvh, dim, dtype, dev)
-    nv, vp, v0, v1 = _rows(v, where, kvh, dim, dtype, dev)
-    no, op, o0, o1 = _rows(q_out, where, heads, dim, dtype, dev)
-    if not nk == nv == no == tokens or dtype not in _DTYPE:
-        _refuse(where)
-    rp = rows = half = 0
-    if rope is not None:
-        rows, two, half = rope.shape
-        rp = _vector(rope, where, 2 * rows * half, torch.float32, dev)
-        if two != 2:
-            _refuse(where)
-    args = _APPEND.pack(_APPEND.size, qp, kp, vp, op, _vector(positions, where, tokens, torch.int32, dev),
-                        _vector(seqs, where, tokens, torch.int32, dev), rp, _vector(q_gain, where, dim, dtype, dev),
-                        _vector(k_gain, where, dim, dtype, dev), q0, q1, k0, k1, v0, v1, o0, o1, tokens, heads,
-                        _DTYPE[dtype], rows, 2 * half, interleaved, eps, 0)
-    status = lib().w4a4_kv_append(cache._struct, args, _stream(stream, dev))
+    status = _calls().kv_append(cache._struct, cache.device, q, k, v, positions, q_out, seqs, rope, q_gain, k_gain, eps,
+                                interleaved, stream)
     if status:
-        _refuse(where, status)
+        _refuse("w4a4_kv_append", status)
 
 
 def w4a4_paged_attention(q, cache, lengths, out, lse=None, scale=None, window: int = 0, workspace=None, stream=None):
@@ -479,20 +454,13 @@ def w4a4_paged_attention(q, cache, lengths, out, lse=None, scale=None, window: i
 
     scale: of the scores, dim ** -0.5 by default.  lse: fp32 [seqs, q_heads] or None.  workspace:
     zeroed uint8 of w4a4_paged_attention_workspace_bytes, by default the cache object's own."""
-    where = "w4a4_paged_attention"
-    dtype, dim, dev = q.dtype, cache.head_dim, cache.device
-    heads = q.shape[1]
-    n, qp, q0, q1 = _rows(q, where, heads, dim, dtype, dev)
-    no, op, o0, o1 = _rows(out, where, heads, dim, dtype, dev)
-    if n != cache.seqs or no != n or dtype not in _DTYPE:
-        _refuse(where)
-    ws = cache.workspace(heads) if workspace is None else workspace
-    args = _ATTENTION.pack(_ATTENTION.size, qp, op, _vector(lse, where, n * heads, torch.float32, dev),
-                           _vector(lengths, where, n, torch.int32, dev), ws.data_ptr(), ws.numel() * ws.element_size(),
-                           q0, q1, o0, o1, dim ** -0.5 if scale is None else scale, heads, _DTYPE[dtype], window)
-    status = lib().w4a4_paged_attention(cache._struct, args, _stream(stream, dev))
+    if scale is None:
+        scale = cache.head_dim ** -0.5
+    if workspace is None:
+        workspace = cache.workspace(q.shape[1])
+    status = _calls().paged_attention(cache._struct, cache.device, q, lengths, out, lse, scale, window, workspace, stream)
     if status:
-        _refuse(where, status)
+        _refuse("w4a4_paged_attention", status)
 
 
 def w4a4_block_norm(y, r, x, r_out, gate=None, rows_per_gate: int = 0, scale: float = 1.0, post: int = NORM_RMS,
@@ -504,37 +472,10 @@ def w4a4_block_norm(y, r, x, r_out, gate=None, rows_per_gate: int = 0, scale: fl
     y, x [rows, width] fp16 or bf16 (x None: not wanted); r, r_out the same type or fp32 (r_out may
     be r).  post, pre: NORM_NONE, NORM_RMS or NORM_LAYER.  gate: [width] or [gates, width], row m
     under gate row m // rows_per_gate (0: one row for all)."""
-    where = "w4a4_block_norm"
-    dtype, res, dev, shape = y.dtype, r.dtype, y.get_device(), y.shape
-    rows, width = shape
-
-    def stride(t, kind):
-        a, b = t.stride()
-        if b != 1 or t.dtype is not kind or t.shape != shape or t.get_device() != dev:
-            _refuse(where)
-        return a
-
-    ys, rs, ros = stride(y, dtype), stride(r, res), stride(r_out, res)
-    if dtype not in _DTYPE or res not in _DTYPE or dev < 0:
-        _refuse(where)
-    gp = gs = xp = xs = 0
-    if gate is not None:
-        gs = gate.stride(0) if gate.dim() == 2 else width
-        gates, need = gate.numel() // width, -(-rows // rows_per_gate) if rows_per_gate > 0 else 1
-        if gate.dtype is not dtype or gate.get_device() != dev or gate.shape[-1] != width or gate.stride(-1) != 1 or \
-                gate.dim() > 2 or gates < need:
-            _refuse(where)
-        gp = gate.data_ptr()
-    if x is not None:
-        xp, xs = x.data_ptr(), stride(x, dtype)
-    args = _BLOCK_NORM.pack(_BLOCK_NORM.size, y.data_ptr(), r.data_ptr(), r_out.data_ptr(), xp, gp,
-                            _vector(post_gain, where, width, dtype, dev), _vector(post_bias, where, width, dtype, dev),
-                            _vector(pre_gain, where, width, dtype, dev), _vector(pre_bias, where, width, dtype, dev),
-                            ys, rs, ros, xs, gs, rows, width, rows_per_gate, _DTYPE[dtype], _DTYPE[res], post, pre,
-                            scale, eps, 0)
-    status = lib().w4a4_block_norm(args, _stream(stream, dev))
+    status = _calls().block_norm(y, r, x, r_out, gate, rows_per_gate, scale, post, post_gain, post_bias, pre, pre_gain,
+                                 pre_bias, eps, stream)
     if status:
-        _refuse(where, status)
+        _refuse("w4a4_block_norm", status)
 
 
 # ------------------------------------------------------------- layer helper

@@ -1,7 +1,9 @@
 """Build the in-tree CUDA library ``libw4a4.so`` for sm_103a with nvcc.
 
 Each translation unit is compiled in parallel into ``_build/`` and linked into
-``w4a4_quantized_gemm_gb300/libw4a4.so`` (static CUDA runtime, no torch).
+``w4a4_quantized_gemm_gb300/libw4a4.so`` (static CUDA runtime, no torch).  The
+Python entry of the decoder-layer operators, ``csrc/binding.cpp``, is compiled
+with g++ against the installed torch into ``_binding.so``, which uses that library.
 Rebuilds only when a source or header is newer than the library.
 """
 from __future__ import annotations
@@ -10,6 +12,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -17,6 +20,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libw4a4.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING = os.path.join(HERE, "_binding.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
                      "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]
@@ -34,14 +39,14 @@ def sources():
 
 
 def _deps():
-    return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
+    return sources() + [BINDING_SRC] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
         glob.glob(os.path.join(ROOT, "include", "*.h"))
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
@@ -59,8 +64,23 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed for {src}:\n{res.stderr}")
         return obj, res.stderr
 
+    def compile_binding():
+        obj = os.path.join(BUILD, "binding.o")
+        import torch
+        import torch.utils.cpp_extension as ext
+        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-c", BINDING_SRC, "-o", obj,
+               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+               "-I", os.path.join(ROOT, "include"), "-I", os.path.join(os.path.dirname(os.path.dirname(nvcc)), "include"),
+               "-isystem", sysconfig.get_paths()["include"], *(x for p in ext.include_paths() for x in ("-isystem", p))]
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError(f"g++ failed for {BINDING_SRC}:\n{res.stderr}")
+        return obj, [x for p in ext.library_paths() for x in ("-L" + p, "-Wl,-rpath," + p)]
+
     with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
+        binding = ex.submit(compile_binding)
         results = list(ex.map(compile_one, sources()))
+        binding_obj, torch_libs = binding.result()
     if verbose:
         for obj, log in results:
             print(f"== {os.path.basename(obj)}\n{log}")
@@ -70,6 +90,13 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{res.stderr}")
     os.replace(tmp, LIB)
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-shared", "-o", tmp, binding_obj, "-L" + HERE, "-l:libw4a4.so", "-Wl,-rpath,$ORIGIN", *torch_libs,
+           "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"link failed:\n{res.stderr}")
+    os.replace(tmp, BINDING)
     return LIB
 
 

@@ -7,7 +7,7 @@
 // with c, n the cosine and sine of the token's position times the pair's frequency.
 // Every byte is read once and written once, so the bound is HBM traffic.
 //
-// One CTA of 64 threads takes one token (a slice of its heads when there are few
+// One CTA takes one token (a slice of its heads when there are few
 // tokens): the heads of a token share position, page and rotation, which are looked up
 // once and stay in registers.  A head belongs to D / 16 lanes (eight with two idle ones
 // at D = 96), each with the two 16-byte pieces that hold both elements of its pairs, so
@@ -22,28 +22,34 @@ namespace {
 
 __device__ int g_append_status = 0;
 
-constexpr int kThreads = 64;
+// Two forms.  Many tokens: one warp a CTA in at most 78 registers, so that an SM holds 26
+// (8192 tokens of 48 heads of 128, fp16: 33.6 us, 6.1 TB/s; two warps without the limit
+// 40 us).  Few, which all fit at once: the gains of q and k are requested with the first
+// heads and kept, 700 tokens of 32 heads 3.9 us instead of 4.3, one token 2.3 us either way.
+constexpr int kFew = 5;  // tokens per SM up to which they are few
+constexpr int threads_of(bool many) { return many ? 32 : 64; }
+constexpr int per_sm(bool many) { return many ? 26 : 10; }  // CTAs that an SM holds
 constexpr int kAhead = 2;  // heads whose pieces a lane holds at once
 
 // One 8-element piece to the cache, in its type.
 template <class T, bool E4M3>
-__device__ __forceinline__ void store_piece(void* pool, int64_t at, const float (&x)[8], float scale) {
+__device__ __forceinline__ void store_piece(void* pool, int64_t at, const float (&x)[8], float per_scale) {
     if constexpr (E4M3) {
         uint2 o;
-        o.x = e4m3x2(x[0] / scale, x[1] / scale) | e4m3x2(x[2] / scale, x[3] / scale) << 16;
-        o.y = e4m3x2(x[4] / scale, x[5] / scale) | e4m3x2(x[6] / scale, x[7] / scale) << 16;
+        o.x = e4m3x2(x[0] * per_scale, x[1] * per_scale) | e4m3x2(x[2] * per_scale, x[3] * per_scale) << 16;
+        o.y = e4m3x2(x[4] * per_scale, x[5] * per_scale) | e4m3x2(x[6] * per_scale, x[7] * per_scale) << 16;
         *reinterpret_cast<uint2*>(static_cast<char*>(pool) + at) = o;
     } else {
         store8<T>(pool, at, x);
     }
 }
 
-template <class T, bool E4M3, int LPH>  // LPH: lanes of a head's group (4, 8 or 16)
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(const w4a4_kv_cache c, const w4a4_kv_append_args a) {
+template <class T, bool E4M3, int LPH, bool MANY>  // LPH: lanes of a head's group (4, 8 or 16)
+__global__ void __launch_bounds__(threads_of(MANY), per_sm(MANY)) kv_append_kernel(const w4a4_kv_cache c, const w4a4_kv_append_args a) {
     pdl_wait();
     pdl_launch_dependents();
     const int t = blockIdx.x, lane = threadIdx.x % LPH, group = threadIdx.x / LPH;
-    constexpr int kGroups = kThreads / LPH;
+    constexpr int kGroups = threads_of(MANY) / LPH;
     const int D = c.head_dim, R = a.rope ? a.rot_dim : 0;
     const bool has = lane < D / 16, inter = a.interleaved != 0;
     // This lane's elements e[0] .. + 7 and e[1] .. + 7: a pair's halves while they are
@@ -71,6 +77,16 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const w4a4_kv_cache
         }
     };
     load(0);
+
+    // This lane's gains, of q and of k.
+    const bool norms = a.q_gain || a.k_gain;
+    const float per_head = 1.f / float(D);
+    uint4 gains[4] = {};
+    if (!MANY && norms && has) {
+        const char *qg = static_cast<const char*>(a.q_gain), *kg = static_cast<const char*>(a.k_gain);
+        if (qg) gains[0] = *reinterpret_cast<const uint4*>(qg + 2 * e0), gains[1] = *reinterpret_cast<const uint4*>(qg + 2 * e1);
+        if (kg) gains[2] = *reinterpret_cast<const uint4*>(kg + 2 * e0), gains[3] = *reinterpret_cast<const uint4*>(kg + 2 * e1);
+    }
 
     // The token's place.  Anything outside its table makes it a padding token.
     const int seq = a.seqs ? a.seqs[t] : t;
@@ -117,18 +133,23 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const w4a4_kv_cache
             float x[8], y[8];
             up8<T>(raw[u][0], x);
             up8<T>(raw[u][1], y);
-            if (a.q_gain || a.k_gain) {
+            if (norms) {
                 float ss = 0.f;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) ss += x[j] * x[j] + y[j] * y[j];
 #pragma unroll
                 for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                const void* gain = is_q ? a.q_gain : a.k_gain;
-                if (!is_v && gain && has) {
-                    const float inv = 1.f / sqrtf(ss / float(D) + a.eps);
+                if (is_q ? a.q_gain != nullptr : !is_v && a.k_gain) {
+                    const float inv = rsqrtf(ss * per_head + a.eps);  // 2 ulp
                     float g[8], h[8];
-                    load8<T>(gain, e0, g);
-                    load8<T>(gain, e1, h);
+                    if constexpr (MANY) {
+                        const void* gain = is_q ? a.q_gain : a.k_gain;
+                        load8<T>(gain, e0 < D ? e0 : 0, g);
+                        load8<T>(gain, e1 < D ? e1 : 0, h);
+                    } else {
+                        up8<T>(is_q ? gains[0] : gains[2], g);
+                        up8<T>(is_q ? gains[1] : gains[3], h);
+                    }
 #pragma unroll
                     for (int j = 0; j < 8; ++j) x[j] = x[j] * inv * g[j], y[j] = y[j] * inv * h[j];
                 }
@@ -166,9 +187,9 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const w4a4_kv_cache
                 const int64_t to = is_v ? page * c.v_page_stride + slot * c.v_token_stride + h * c.v_head_stride
                                         : page * c.k_page_stride + slot * c.k_token_stride + h * c.k_head_stride;
                 const float* scales = is_v ? c.v_scale : c.k_scale;
-                const float scale = E4M3 && scales ? scales[h] : 1.f;
-                store_piece<T, E4M3>(pool, to + e0, x, scale);
-                store_piece<T, E4M3>(pool, to + e1, y, scale);
+                const float per_scale = E4M3 && scales ? __frcp_rn(scales[h]) : 1.f;
+                store_piece<T, E4M3>(pool, to + e0, x, per_scale);
+                store_piece<T, E4M3>(pool, to + e1, y, per_scale);
             }
         }
     }
@@ -187,28 +208,37 @@ __global__ void rope_table_kernel(float* rope, int64_t n, int half, double log2_
     }
 }
 
-template <class T, bool E4M3>
-void launch_t(const w4a4_kv_cache& c, const w4a4_kv_append_args& a, cudaStream_t s) {
+template <class T, bool E4M3, bool MANY>
+void launch_m(const w4a4_kv_cache& c, const w4a4_kv_append_args& a, cudaStream_t s) {
     const int lph = c.head_dim <= 64 ? 4 : c.head_dim <= 128 ? 8 : 16;
-    const int groups = kThreads / lph, rows = a.q_heads + 2 * c.kv_heads;
-    // Few tokens: a token's heads are spread over CTAs until two per SM have work.
-    const int most = (rows + groups - 1) / groups, want = (2 * device_sm_count() + a.tokens - 1) / a.tokens;
+    const int groups = threads_of(MANY) / lph, rows = a.q_heads + 2 * c.kv_heads;
+    // A token's heads are spread over as many CTAs as the GPU holds at once.
+    const int most = (rows + groups - 1) / groups, room = per_sm(MANY) * device_sm_count() / a.tokens;
+    const int want = room > 1 ? room : 1;
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
     cfg.attrs = attr;
     cfg.numAttrs = add_pdl_attr(attr, 0);
     cfg.gridDim = dim3(unsigned(a.tokens), unsigned(most < want ? most : want));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(threads_of(MANY));
     cfg.stream = s;
     if (lph == 4)
-        cudaLaunchKernelEx(&cfg, kv_append_kernel<T, E4M3, 4>, c, a);
+        cudaLaunchKernelEx(&cfg, kv_append_kernel<T, E4M3, 4, MANY>, c, a);
     else if (lph == 8)
-        cudaLaunchKernelEx(&cfg, kv_append_kernel<T, E4M3, 8>, c, a);
+        cudaLaunchKernelEx(&cfg, kv_append_kernel<T, E4M3, 8, MANY>, c, a);
     else
-        cudaLaunchKernelEx(&cfg, kv_append_kernel<T, E4M3, 16>, c, a);
-    set_dispatch_ints(E4M3 ? "kv_append tokens=%d heads=%d+2x%d dim=%d e4m3 cache grid=%dx%d"
-                           : "kv_append tokens=%d heads=%d+2x%d dim=%d 16-bit cache grid=%dx%d",
-                      {a.tokens, a.q_heads, c.kv_heads, c.head_dim, a.tokens, int(cfg.gridDim.y)});
+        cudaLaunchKernelEx(&cfg, kv_append_kernel<T, E4M3, 16, MANY>, c, a);
+    set_dispatch_ints(E4M3 ? "kv_append tokens=%d heads=%d+2x%d dim=%d e4m3 cache threads=%d grid=%dx%d"
+                           : "kv_append tokens=%d heads=%d+2x%d dim=%d 16-bit cache threads=%d grid=%dx%d",
+                      {a.tokens, a.q_heads, c.kv_heads, c.head_dim, threads_of(MANY), a.tokens, int(cfg.gridDim.y)});
+}
+
+template <class T, bool E4M3>
+void launch_t(const w4a4_kv_cache& c, const w4a4_kv_append_args& a, cudaStream_t s) {
+    if (a.tokens > kFew * device_sm_count())
+        launch_m<T, E4M3, true>(c, a, s);
+    else
+        launch_m<T, E4M3, false>(c, a, s);
 }
 
 }  // namespace

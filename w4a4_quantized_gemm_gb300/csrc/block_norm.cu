@@ -4,7 +4,8 @@
 // gate, add, norm) would move a row ten times; here y and r are read once and r' and
 // x written once, which is the HBM bound.
 //
-// A CTA takes every grid-th row, a thread the same columns of each: CH chunks of eight
+// A CTA takes every grid-th row (narrow rows: several at a time), a thread the same
+// columns of each: CH chunks of eight
 // elements in registers (fp32) through both norms.  The gains, biases and a shared gate
 // are read once for all rows (packed, in registers), and the next row is requested
 // before this one is worked on.  The arithmetic is done on pairs (f32x2), and a missing
@@ -27,11 +28,6 @@
 namespace w4a4 {
 namespace {
 
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
 template <int N>  // over each group of N lanes (a power of two)
 __device__ __forceinline__ float group_sum(float v) {
 #pragma unroll
@@ -82,14 +78,14 @@ __device__ __forceinline__ void ld_once8(const float* p, bool wide, uint4 (&v)[2
 // A thread's chunks of a vector [W] of a 16-bit type; `fill` (two elements) where there
 // is none.  Held in registers for all rows, or read where they are used (CH > 2: too
 // many to hold).
-template <class T, int NT, int CH>
+template <class T, int NC, int CH>
 struct Vector {
     static constexpr bool kHeld = CH <= 2;
     const char* at;
     uint32_t fill;
     uint4 v[kHeld ? CH : 1];
     __device__ __forceinline__ uint4 read(int c, int W) const {
-        const int k = (c * NT + threadIdx.x) * 8;
+        const int k = (c * NC + threadIdx.x % NC) * 8;
         return at && k < W ? *reinterpret_cast<const uint4*>(at + 2 * k) : make_uint4(fill, fill, fill, fill);
     }
     __device__ __forceinline__ void init(const void* p, float missing, int W) {
@@ -109,42 +105,42 @@ struct Vector {
     }
 };
 
-// z -> norm(z) in place; chunk c of this thread is elements (c * NT + tid) * 8 ..
-// and takes part while that is below W (the others are zero).  Every thread gets the
-// same statistics (fixed order).  LAYER: one of the row's norms is a LayerNorm (an
+// z -> norm(z) in place; chunk c of this thread is elements (c * NC + tid % NC) * 8 ..
+// and takes part while that is below W (the others are zero).  NC threads, in one or
+// several warps, have a row and get the same statistics (fixed order).  LAYER: one of the row's norms is a LayerNorm (an
 // RMSNorm beside it takes the mean and the bias as zero); without it the mean, the
 // bias and their work are left out (fp16, 4096 x 8192: 52 us with them, 46 without).
-template <class T, int NT, int CH, bool LAYER>
-__device__ __forceinline__ void normalise(uint64_t (&z)[CH][4], int kind, Vector<T, NT, CH>& gain,
-                                          Vector<T, NT, CH>& bias, int W, float eps, float4 (&red)[NT / 32]) {
+template <class T, int NC, int CH, bool LAYER>
+__device__ __forceinline__ void normalise(uint64_t (&z)[CH][4], int kind, Vector<T, NC, CH>& gain,
+                                          Vector<T, NC, CH>& bias, int W, float eps, float4* red) {
     if (kind == W4A4_NORM_NONE) return;
-    constexpr int kWarps = NT / 32;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kWarps = NC > 32 ? NC / 32 : 1, kLanes = NC < 32 ? NC : 32;
+    const int warp = kWarps > 1 ? threadIdx.x >> 5 : 0, lane = threadIdx.x & 31;
     const float n = 1.f / float(W);
     float mean = 0.f, held = 1.f;
     if (LAYER && kind == W4A4_NORM_LAYER) {
         int h = 0;  // elements of this warp that take part
 #pragma unroll
-        for (int c = 0; c < CH; ++c) h += min(256, max(0, W - (c * NT + warp * 32) * 8));
+        for (int c = 0; c < CH; ++c) h += min(8 * kLanes, max(0, W - (c * NC + warp * 32) * 8));
         held = float(h);
         uint64_t s = 0;
 #pragma unroll
         for (int c = 0; c < CH; ++c)
 #pragma unroll
             for (int i = 0; i < 4; ++i) s = tc::fadd2_b64(s, z[c][i]);
-        mean = warp_sum(lo(s) + hi(s)) / fmaxf(held, 1.f);
+        mean = group_sum<kLanes>(lo(s) + hi(s)) / fmaxf(held, 1.f);
     }
     uint64_t q = 0;
     const uint64_t off = both(-mean);
 #pragma unroll
     for (int c = 0; c < CH; ++c)
-        if (!LAYER || (c * NT + int(threadIdx.x)) * 8 < W)
+        if (!LAYER || (c * NC + int(threadIdx.x % NC)) * 8 < W)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const uint64_t d = LAYER ? tc::fadd2_b64(z[c][i], off) : z[c][i];
                 q = tc::ffma2_b64(d, d, q);
             }
-    float v = warp_sum(lo(q) + hi(q));
+    float v = group_sum<kLanes>(lo(q) + hi(q));
     if constexpr (kWarps > 1) {
         if (lane == 0) red[warp] = make_float4(mean, held, v, mean * held);
         __syncthreads();
@@ -175,7 +171,7 @@ __device__ __forceinline__ void normalise(uint64_t (&z)[CH][4], int kind, Vector
     }
 }
 
-template <class T, class R, int NT, int CH, bool LAYER>
+template <class T, class R, int NT, int NC, int CH, bool LAYER>  // NT threads, NC to a row
 __global__ void __launch_bounds__(NT, CH == 2 ? 512 / NT : 1) block_norm_kernel(const w4a4_block_norm_args a) {
     // a norm's partial sums; two sets that rows alternate between, so that a row's
     // barriers separate its reads from the next use of the set
@@ -186,11 +182,13 @@ __global__ void __launch_bounds__(NT, CH == 2 ? 512 / NT : 1) block_norm_kernel(
     const bool wide = R::kSize == 4 && ((reinterpret_cast<uintptr_t>(a.r) | reinterpret_cast<uintptr_t>(a.r_out)) & 31) == 0 &&
                       ((a.r_stride | a.r_out_stride) & 7) == 0;
     const bool row_gate = a.gate && a.rows_per_gate;
-    Vector<T, NT, CH> post_gain, post_bias, pre_gain, pre_bias, gate;
+    Vector<T, NC, CH> post_gain, post_bias, pre_gain, pre_bias, gate;
     uint4 ny[CH], nr[CH][R::kSize / 2], ng[CH];  // the next row, as it is in memory
 #pragma unroll
     for (int c = 0; c < CH; ++c)  // chunks past the row stay zero
         ny[c] = ng[c] = nr[c][0] = nr[c][R::kSize / 2 - 1] = make_uint4(0, 0, 0, 0);
+    constexpr uint32_t kRows = NT / NC;  // of a CTA at a time
+    const uint32_t rows = a.rows, step = gridDim.x * kRows, mine = NT > NC ? threadIdx.x / NC : 0;
     auto request = [&](uint32_t m) {
         const char* y = static_cast<const char*>(a.y) + 2 * (m * a.y_stride);
         const char* r = static_cast<const char*>(a.r) + R::kSize * (m * a.r_stride);
@@ -198,8 +196,8 @@ __global__ void __launch_bounds__(NT, CH == 2 ? 512 / NT : 1) block_norm_kernel(
         if (row_gate) gates += 2 * (m / uint32_t(a.rows_per_gate) * a.gate_stride);
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            const int k = (c * NT + threadIdx.x) * 8;
-            if (k >= W) continue;
+            const int k = (c * NC + threadIdx.x % NC) * 8;
+            if (k >= W || m >= rows) continue;
             ny[c] = ld_once(y + 2 * k);
             if constexpr (R::kSize == 4)
                 ld_once8(reinterpret_cast<const float*>(r) + k, wide, nr[c]);
@@ -208,7 +206,7 @@ __global__ void __launch_bounds__(NT, CH == 2 ? 512 / NT : 1) block_norm_kernel(
             if (row_gate) ng[c] = *reinterpret_cast<const uint4*>(gates + 2 * k);
         }
     };
-    request(blockIdx.x);
+    request(blockIdx.x * kRows + mine);
     post_gain.init(a.post_gain, 1.f, W);
     post_bias.init(a.post == W4A4_NORM_LAYER ? a.post_bias : nullptr, 0.f, W);
     pre_gain.init(a.pre_gain, 1.f, W);
@@ -216,8 +214,10 @@ __global__ void __launch_bounds__(NT, CH == 2 ? 512 / NT : 1) block_norm_kernel(
     gate.init(row_gate ? nullptr : a.gate, 1.f, W);
     const uint64_t scale = both(a.scale);
     int set = 0;
-    const uint32_t rows = a.rows;
-    for (uint32_t m = blockIdx.x; m < rows; m += gridDim.x, set ^= 1) {
+    // a warp's last rows may be missing: its lanes stay for the shuffles
+    for (uint32_t first = blockIdx.x * kRows; first < rows; first += step, set ^= 1) {
+        const uint32_t m = first + mine;
+        const bool row = kRows == 1 || m < rows;
         char* r_row = static_cast<char*>(a.r_out) + R::kSize * (m * a.r_out_stride);
         char* x_row = static_cast<char*>(a.x) + 2 * (m * a.x_stride);
         uint64_t y[CH][4], r[CH][4];
@@ -234,11 +234,11 @@ __global__ void __launch_bounds__(NT, CH == 2 ? 512 / NT : 1) block_norm_kernel(
             }
             g[c] = ng[c];
         }
-        if (m + gridDim.x < rows) request(m + gridDim.x);
-        normalise<T, NT, CH, LAYER>(y, a.post, post_gain, post_bias, W, a.eps, red[set][0]);
+        if (first + step < rows) request(m + step);
+        normalise<T, NC, CH, LAYER>(y, a.post, post_gain, post_bias, W, a.eps, red[set][0]);
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            const int k = (c * NT + threadIdx.x) * 8;
+            const int k = (c * NC + threadIdx.x % NC) * 8;
             if (LAYER || a.gate) {
                 if (!row_gate) g[c] = gate.get(c, W);
 #pragma unroll
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(NT, CH == 2 ? 512 / NT : 1) block_norm_kernel(
 #pragma unroll
                 for (int i = 0; i < 4; ++i) r[c][i] = tc::ffma2_b64(scale, y[c][i], r[c][i]);
             }
-            if (k < W) {
+            if (k < W && row) {
                 char* dst = r_row + R::kSize * k;
                 if constexpr (R::kSize == 4) {
                     if (wide) {
@@ -264,42 +264,42 @@ __global__ void __launch_bounds__(NT, CH == 2 ? 512 / NT : 1) block_norm_kernel(
                     *reinterpret_cast<uint4*>(dst) =
                         make_uint4(down2<R>(r[c][0]), down2<R>(r[c][1]), down2<R>(r[c][2]), down2<R>(r[c][3]));
                 }
-            } else {  // the rest of a row takes part in no statistics
+            } else if (k >= W) {  // the rest of a row takes part in no statistics
 #pragma unroll
                 for (int i = 0; i < 4; ++i) r[c][i] = 0;
             }
         }
         if (!a.x) continue;
-        normalise<T, NT, CH, LAYER>(r, a.pre, pre_gain, pre_bias, W, a.eps, red[set][1]);
+        normalise<T, NC, CH, LAYER>(r, a.pre, pre_gain, pre_bias, W, a.eps, red[set][1]);
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            const int k = (c * NT + threadIdx.x) * 8;
-            if (k < W)
+            const int k = (c * NC + threadIdx.x % NC) * 8;
+            if (k < W && row)
                 *reinterpret_cast<uint4*>(x_row + 2 * k) =
                     make_uint4(down2<T>(r[c][0]), down2<T>(r[c][1]), down2<T>(r[c][2]), down2<T>(r[c][3]));
         }
     }
 }
 
-template <class T, class R, int NT, int CH, bool LAYER>
+template <class T, class R, int NT, int NC, int CH, bool LAYER>
 void launch_k(const w4a4_block_norm_args& a, cudaStream_t s) {
     static std::atomic<int> per_sm{0};  // CTAs that an SM holds (registers), the same on every device
     int n = per_sm.load(std::memory_order_relaxed);
     if (n == 0) {
-        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, block_norm_kernel<T, R, NT, CH, LAYER>, NT, 0) != cudaSuccess ||
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, block_norm_kernel<T, R, NT, NC, CH, LAYER>, NT, 0) != cudaSuccess ||
             n < 1)
             n = 1;
         per_sm.store(n, std::memory_order_relaxed);
     }
-    const int full = n * device_sm_count();
+    const int64_t full = n * int64_t(device_sm_count()), ctas = (int64_t(a.rows) * NC + NT - 1) / NT;
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
     cfg.attrs = attr;
     cfg.numAttrs = add_pdl_attr(attr, 0);
-    cfg.gridDim = dim3(unsigned(a.rows < full ? a.rows : full));
+    cfg.gridDim = dim3(unsigned(ctas < full ? ctas : full));
     cfg.blockDim = dim3(NT);
     cfg.stream = s;
-    cudaLaunchKernelEx(&cfg, block_norm_kernel<T, R, NT, CH, LAYER>, a);
+    cudaLaunchKernelEx(&cfg, block_norm_kernel<T, R, NT, NC, CH, LAYER>, a);
     set_dispatch_ints("block_norm rows=%d width=%d threads=%d chunks/thread=%d grid=%d",
                       {a.rows, a.width, NT, CH, int(cfg.gridDim.x)});
 }
@@ -307,20 +307,26 @@ void launch_k(const w4a4_block_norm_args& a, cudaStream_t s) {
 template <class T, class R, bool LAYER>
 void launch_l(const w4a4_block_norm_args& a, cudaStream_t s) {
     const int chunks = a.width / 8;
-    if (chunks <= 32)
-        launch_k<T, R, 32, 1, LAYER>(a, s);
+    // Narrow rows share a warp, and a CTA has four: 8192 rows of 64 (fp16) take 1.7 us, one
+    // row to a CTA of one warp 4.2 us; 8192 of 512 take 4.9 us, two warps to a row 5.9 us.
+    if (chunks <= 8)
+        launch_k<T, R, 128, 8, 1, LAYER>(a, s);
+    else if (chunks <= 16)
+        launch_k<T, R, 128, 16, 1, LAYER>(a, s);
+    else if (chunks <= 32)
+        launch_k<T, R, 128, 32, 1, LAYER>(a, s);
     else if (chunks <= 64)
-        launch_k<T, R, 64, 1, LAYER>(a, s);
+        launch_k<T, R, 128, 32, 2, LAYER>(a, s);
     else if (chunks <= 128)
-        launch_k<T, R, 128, 1, LAYER>(a, s);
+        launch_k<T, R, 128, 128, 1, LAYER>(a, s);
     else if (chunks <= 256)
-        launch_k<T, R, 128, 2, LAYER>(a, s);
+        launch_k<T, R, 128, 128, 2, LAYER>(a, s);
     else if (chunks <= 512)
-        launch_k<T, R, 256, 2, LAYER>(a, s);
+        launch_k<T, R, 256, 256, 2, LAYER>(a, s);
     else if (chunks <= 1024)
-        launch_k<T, R, 512, 2, LAYER>(a, s);
+        launch_k<T, R, 512, 512, 2, LAYER>(a, s);
     else
-        launch_k<T, R, 512, 4, LAYER>(a, s);
+        launch_k<T, R, 512, 512, 4, LAYER>(a, s);
 }
 
 template <class T, class R>

@@ -104,7 +104,8 @@ struct Args {
     int heads;       // kv_heads * chunks / together: units' head groups of a sequence
     int rows;        // query heads of a chunk (the last of a key-value head may have fewer)
     int span_log2;   // log2 of the tokens of a unit
-    Divisor by_page, by_ctas, by_chunks, by_rows;  // page size, grid, chunks, rows
+    Divisor by_page, by_ctas, by_chunks, by_rows, by_items;  // page size, grid, chunks, rows, items
+    int items;       // outputs of a unit, four elements each
     bool q_bf16;
 };
 
@@ -158,6 +159,7 @@ struct Share {
     int each, more;
     __device__ __forceinline__ int start(int c) const { return each * c + min(c, more); }
     __device__ __forceinline__ int owner(int unit) const {
+        if (each == 1 && more == 0) return unit;
         const int longer = more * (each + 1);
         return unit < longer ? unit / (each + 1) : more + (unit - longer) / each;
     }
@@ -245,12 +247,11 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
         }
         if (bad && blockIdx.x == 0) atomicExch(&g_attention_status, int(W4A4_ERR_INDEX));
         int upto = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
+        for (int o = 1; o < min(B, 32); o <<= 1) {
             const int v = __shfl_up_sync(0xffffffffu, upto, o);
             if (lane >= o) upto += v;
         }
-        int total = __shfl_sync(0xffffffffu, upto, 31);
+        int total = __shfl_sync(0xffffffffu, upto, min(B, 32) - 1);
         if (few) {
             empty = __any_sync(0xffffffffu, empty);
         } else {
@@ -348,7 +349,8 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
         }
         if (piece == 0) {
             const int in = first - seq_tiles * A.heads;
-            at.hc = in / at.tiles;
+            // in + 1/2 is at least 1 / (2 tiles) away from a multiple of tiles
+            at.hc = in < (1 << 20) ? int(__fdividef(in + 0.5f, at.tiles)) : in / at.tiles;
             at.tile = in - at.hc * at.tiles;
         }
     }
@@ -522,13 +524,22 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
                         }
                     }
                 } else {
+                    float odd[NT][4] = {};  // two chains of MMAs, so that neither waits for every result
 #pragma unroll
-                    for (int st = 0; st < kSteps; ++st) {
-                        uint32_t a[4];
+                    for (int st = 0; st < kSteps; st += 2) {
+                        uint32_t a[4], b[4];
                         tc::ldsm_x4(a, base + st * 32);
+                        tc::ldsm_x4(b, base + st * 32 + 32);
 #pragma unroll
-                        for (int t = 0; t < NT; ++t) mma<CT>(s[u][t], a, qf[st][t][0], qf[st][t][1]);
+                        for (int t = 0; t < NT; ++t) {
+                            mma<CT>(s[u][t], a, qf[st][t][0], qf[st][t][1]);
+                            mma<CT>(odd[t], b, qf[st + 1][t][0], qf[st + 1][t][1]);
+                        }
                     }
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) s[u][t][j] += odd[t][j];
                 }
             }
             // Scores in units of log2, tokens that do not take part at -inf.  The subtracted
@@ -671,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
         auto slot_of = [&](int c) { return 2 * c + (c == c0 ? first_slot : 0); };
         auto part_of = [&](int c) { return A.parts + int64_t(slot_of(c)) * kPart; };
         // Row r is query head `row` of the unit's head chunk `chunk`, which a last chunk may lack.
-        const int items = A.together * A.rows * (D / 4);
+        const int items = A.items;
         auto chunk_of = [&](int r) { return A.together == 1 ? 0 : A.by_rows.quotient(r); };
         auto write = [&](int r, int e, const float4& o, float m, float l) {
             const int chunk = chunk_of(r), v = was.hc * A.together + chunk, head = A.by_chunks.quotient(v);
@@ -739,7 +750,8 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
             // takes four elements of a row over all parts, or over every ways-th where there
             // are fewer elements than threads.
             float* meet = reinterpret_cast<float*>(smem + used * P::kStage);  // [ways][items][6]
-            const int width = min(items, kThreads), ways = kThreads / width, my_way = tid / width, my_item = tid - my_way * width;
+            const int width = min(items, kThreads), ways = A.by_items.quotient(kThreads);
+            const int my_way = A.by_items.quotient(tid), my_item = tid - my_way * width;
             for (int level = 0; level < 2; ++level) {
                 if (!(level == 0 ? arrive(A.joined + slot_of(c_first), in_sixteen)
                                  : arrive(A.arrived + int64_t(was.b) * A.heads + was.hc, sixteens)))
@@ -846,22 +858,25 @@ w4a4_status launch_n(Args& A, cudaStream_t s) {
     const int chunks = A.c.kv_heads * A.chunks;  // of a sequence
     // Head chunks side by side: the warps take two or four of them and the same tokens.
     //  * Chunks of one head read the same rows, which then come from HBM once.
-    //  * Short rows of adjacent heads make one longer row of what the warps fetch together:
-    //    64 sequences of 8192 tokens, E4M3, D = 64: 101 us, one head at a time 137 us;
-    //    D = 96, fp16: 270 and 348 us.  From 256-byte rows on it makes no difference (D = 128,
-    //    fp16: 685 and 686 us at 128 sequences), and where there is less work it makes (sequence, head
-    //    group) pairs fewer and their splits, so the joins, longer (8 x 5000 tokens, D = 128:
+    //  * Rows of adjacent heads make one longer row of what the warps fetch together: 64
+    //    sequences of 8192 tokens, E4M3, D = 64: 101 us, one head at a time 137 us; E4M3,
+    //    D = 256: 346 and 408 us; fp16, D = 96: 270 and 348 us, D = 256: 684 and 704 us.  Not
+    //    at D = 128 of a 16-bit type (128 sequences: 685 and 686 us; in groups of 16 heads
+    //    365 and 350 us), and not where there is less work: it makes (sequence, head group)
+    //    pairs fewer and their splits, so the joins, longer (8 x 5000 tokens, fp16, D = 128:
     //    40 and 34 us).
     //  * With sequences of one step, and more of them than CTAs, no warp is left without
     //    tokens (128 sequences of 4 tokens: 4.9 and 12.7 us).
     A.together = 1;
-    const bool adjacent = P::kRowBytes < 256 && A.c.k_head_stride == D && A.c.v_head_stride == D;
+    const bool adjacent = (CT == kE4M3 || D != 128) && A.c.k_head_stride == D && A.c.v_head_stride == D;
     const int64_t work = int64_t(A.c.seqs) * chunks * keys;
     if (A.chunks > 1 || (adjacent && work > 64 * full * kWarps * P::kTokens) ||
         (keys <= P::kTokens && int64_t(A.c.seqs) * chunks > full))
         while (A.together < kPartRows / P::kChunk && A.together < kWarps && chunks % (2 * A.together) == 0)
             A.together *= 2;
     A.heads = chunks / A.together;
+    A.items = A.together * A.rows * (D / 4);
+    A.by_items = Divisor(A.items < kThreads ? A.items : kThreads);
     A.span_log2 = A.together == 1 ? 2 : A.together == 2 ? 1 : 0;
     A.span_log2 += P::kTokens == 32 ? 5 : 4;
     const int64_t span = int64_t(1) << A.span_log2;

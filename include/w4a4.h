@@ -326,6 +326,7 @@ typedef enum { W4A4_F16 = 0, W4A4_BF16 = 1, W4A4_F32 = 2, W4A4_E4M3 = 3 } w4a4_d
  *   dtype      W4A4_F16, W4A4_BF16 or W4A4_E4M3; an E4M3 element stands for
  *              code * k_scale[head] (v_scale[head]); NULL scales mean 1
  *   head_dim   64, 96, 128 or 256
+ *   max_pages * page_size <= 2^30 tokens of a sequence
  *   strides    non-negative, of whole 16 bytes; the pools 16-byte aligned
  * `bytes` is sizeof(w4a4_kv_cache), and so in the argument structs below; a
  * call with another value returns W4A4_ERR_INVALID_ARG.  The structs live on the

@@ -83,6 +83,7 @@ def test_struct_layouts_match_the_header(tmp_path):
     (dict(k=A + 8), 3), (dict(v=A + 2), 3), (dict(page_table=A + 2), 3), (dict(k_scale=A + 1), 3),
     (dict(k_token_stride=1028), 3), (dict(v_head_stride=-128), 3), (dict(k_page_stride=1 << 40), 3),
     (dict(dtype=3, k_token_stride=1032), 3), (dict(table_stride=9), 1), (dict(max_pages=1 << 28, table_stride=1 << 28), 2),
+    (dict(max_pages=(1 << 26) + 1, table_stride=1 << 27), 2), (dict(table_stride=0), 1),
     (dict(pages=-1), 1),
 ])
 def test_cache_refusals(L, over, status):

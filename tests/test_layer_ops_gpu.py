@@ -338,6 +338,30 @@ def test_attention_strided_queries_other_streams_and_graphs():
     assert w4.w4a4_device_status() == 0
 
 
+def test_attention_tables_and_workspaces_it_refuses():
+    """One row of the page table for all sequences (stride 0); a workspace first asked for inside a capture."""
+    c = Cache([40, 40], 16, 2, 64, F16)
+    q = randn(gen(35), 2, 4, 64).to(F16).cuda()
+    n, out = torch.full((2,), 40, dtype=torch.int32, device="cuda"), torch.empty_like(q)
+    shared = w4.PagedKVCache(c.gk, c.gv, c.gt[:1].expand(2, -1))
+    with pytest.raises(w4.W4A4Error):
+        w4.w4a4_paged_attention(q, shared, n, out)
+    graph, raised = torch.cuda.CUDAGraph(), False
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        torch.zeros_like(q)
+        try:
+            w4.w4a4_paged_attention(q, c.handle, n, out)
+        except w4.W4A4Error as e:
+            raised = e.status == 4
+    assert raised
+    one = w4.PagedKVCache(c.gk, c.gv, c.gt[:1].as_strided((1, c.gt.shape[1]), (1, 1)))  # a single row's stride says nothing
+    w4.w4a4_paged_attention(q[:1], one, n[:1], out[:1])
+    torch.cuda.synchronize()
+    o, _, t, _ = attention_ref(q[:1].cpu(), c, [40], 0.125, 0)
+    check(out[:1], o, t, "one row")
+
+
 def test_attention_offsets_beyond_32_bits():
     """Pages more than 2^31 elements apart (a pool among other data)."""
     page, hkv, dim, stride = 16, 2, 64, 1 << 29

@@ -406,19 +406,24 @@ class PagedKVCache:
         scales = [0 if t is None else t.data_ptr() for t in (k_scale, v_scale)]
         self._keep = (k, v, page_table, k_scale, v_scale)
         self._struct = _CACHE.pack(_CACHE.size, k.data_ptr(), v.data_ptr(), *scales, page_table.data_ptr(),
-                                   *k.stride()[:3], *v.stride()[:3], max(page_table.stride(0), self.max_pages),
+                                   *k.stride()[:3], *v.stride()[:3],
+                                   page_table.stride(0) if self.seqs > 1 else self.max_pages,
                                    self.seqs, self.max_pages, self.pages, self.page_size, self.kv_heads,
                                    self.head_dim, _DTYPE[k.dtype], 0)
         self._ws = {}
 
     def workspace(self, q_heads: int):
-        """The workspace of attention with q_heads query heads: allocated and zeroed at its first use."""
+        """The workspace of attention with q_heads query heads: allocated and zeroed at its first use,
+        which must not be inside a graph capture (its zeroing would only run with the graph)."""
         ws = self._ws.get(q_heads)
         if ws is None:
+            if torch.cuda.is_current_stream_capturing():
+                _refuse("PagedKVCache.workspace: call it before the capture", 4)
             n = lib().w4a4_paged_attention_workspace_bytes(self.seqs, q_heads, self.kv_heads, self.head_dim)
             if n == 0:
                 _refuse("w4a4_paged_attention_workspace_bytes", 2)
             ws = torch.zeros(n, dtype=torch.uint8, device=f"cuda:{self.device}")
+            torch.cuda.current_stream(self.device).synchronize()  # zeroed for calls on any stream
             self._ws[q_heads] = ws
         return ws
 

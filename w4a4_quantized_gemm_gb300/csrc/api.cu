@@ -96,7 +96,7 @@ w4a4_status check_cache(const w4a4_kv_cache* c) {
     if (c->seqs < 0 || c->max_pages < 0 || c->pages < 0 || c->page_size < 1 || c->kv_heads < 1)
         return W4A4_ERR_INVALID_ARG;
     if (!is_act(c->dtype) && c->dtype != W4A4_E4M3) return W4A4_ERR_INVALID_ARG;
-    if (int64_t(c->max_pages) * c->page_size > INT32_MAX) return W4A4_ERR_UNSUPPORTED_SHAPE;
+    if (int64_t(c->max_pages) * c->page_size > (1 << 30)) return W4A4_ERR_UNSUPPORTED_SHAPE;
     if (c->head_dim != 64 && c->head_dim != 96 && c->head_dim != 128 && c->head_dim != 256)
         return W4A4_ERR_UNSUPPORTED_SHAPE;
     const int size = c->dtype == W4A4_E4M3 ? 1 : 2;

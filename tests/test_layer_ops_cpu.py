@@ -180,8 +180,20 @@ def test_binding_refuses_tensors_it_cannot_describe(L):
     for args in ((y, y, y, y), (y, y[:2], y, y), (y, y, y[:, ::2], y), (None, y, y, y), (y, "r", y, y), (y.to_sparse(), y, y, y)):
         with pytest.raises(w4.W4A4Error):
             w4.w4a4_block_norm(*args)
-    with pytest.raises(TypeError):
-        w4._calls().block_norm(y)
+    for args, named in (((y,), {}), ((y, y, y, y), dict(y=y)), ((y, y, y, y), dict(gain=y)), ((y,) * 16, {})):
+        with pytest.raises(TypeError):
+            w4.w4a4_block_norm(*args, **named)
+    for args, named in (((y, y, y, y), dict(eps="a")), ((y, y, y, y), dict(rows_per_gate=1.5)), ((y, y, y, y), dict(stream="s"))):
+        with pytest.raises(w4.W4A4Error):
+            w4.w4a4_block_norm(*args, **named)
+    for cache in (None, object(), 3):
+        with pytest.raises(w4.W4A4Error):
+            w4.w4a4_paged_attention(y, cache, y, y)
+        with pytest.raises(w4.W4A4Error):
+            w4.w4a4_kv_append(y, y, y, y, cache, y)
+    with pytest.raises(AttributeError):
+        w4.w4a4_no_such_function
+    assert "rows_per_gate" in w4.w4a4_block_norm.__doc__
 
 
 def test_status_string_of_the_index_status(L):

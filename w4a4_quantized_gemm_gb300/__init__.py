@@ -357,18 +357,19 @@ def w4a4_set_stream_k(on: bool):
 _DTYPE = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2, torch.float8_e4m3fn: 3}  # w4a4_dtype
 _CACHE = struct.Struct("=Q5Q7q8i")  # w4a4_kv_cache: size, pointers, strides, sizes and type
 
-_native = None
+_NATIVE = ("w4a4_kv_append", "w4a4_paged_attention", "w4a4_block_norm")
 
 
-def _calls():
-    """The native entry of these operators (csrc/binding.cpp): it reads the tensors, checks them against
-    each other and calls the C ABI."""
-    global _native
-    if _native is None:
-        lib()  # raises if nothing is built
-        from . import _binding
-        _native = _binding
-    return _native
+def __getattr__(name: str):
+    """w4a4_kv_append, w4a4_paged_attention and w4a4_block_norm are native functions (csrc/binding.cpp: they
+    read the tensors, check them against each other and call the C ABI), loaded at their first use."""
+    if name not in _NATIVE:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    lib()  # raises if nothing is built
+    from . import _binding
+    for n in _NATIVE:
+        globals()[n] = getattr(_binding, n)
+    return globals()[name]
 
 
 def _refuse(where: str, status: int = 1):
@@ -436,51 +437,6 @@ def w4a4_rope_table(rows: int, rot_dim: int, theta: float, out=None, stream=None
         _refuse("w4a4_rope_table")
     _check(lib().w4a4_rope_table(_ptr(out), rows, rot_dim, theta, _stream(stream)), "w4a4_rope_table")
     return out
-
-
-def w4a4_kv_append(q, k, v, positions, cache, q_out, seqs=None, rope=None, q_gain=None, k_gain=None,
-                   eps: float = 1e-6, interleaved: bool = False, stream=None):
-    """Keys and values of new tokens into `cache`, q and k normalised (gains given) and rotated
-    (rope given) on the way; the rotated queries go to q_out, which may be q.
-
-    q, q_out [tokens, q_heads, dim], k, v [tokens, kv_heads, dim]: fp16 or bf16, last dimension
-    contiguous (slices of a fused q|k|v output).  positions, seqs: int32 [tokens]; seqs None: token
-    t belongs to sequence t, negative: padding.  rope: fp32 [rows, 2, rot_dim / 2]
-    (w4a4_rope_table)."""
-    status = _calls().kv_append(cache._struct, cache.device, q, k, v, positions, q_out, seqs, rope, q_gain, k_gain, eps,
-                                interleaved, stream)
-    if status:
-        _refuse("w4a4_kv_append", status)
-
-
-def w4a4_paged_attention(q, cache, lengths, out, lse=None, scale=None, window: int = 0, workspace=None, stream=None):
-    """out [seqs, q_heads, dim] = attention of one new token per sequence, q, over the first
-    lengths[b] tokens (int32 [seqs]) that `cache` holds of each, or the last `window` of them.
-
-    scale: of the scores, dim ** -0.5 by default.  lse: fp32 [seqs, q_heads] or None.  workspace:
-    zeroed uint8 of w4a4_paged_attention_workspace_bytes, by default the cache object's own."""
-    if scale is None:
-        scale = cache.head_dim ** -0.5
-    if workspace is None:
-        workspace = cache.workspace(q.shape[1])
-    status = _calls().paged_attention(cache._struct, cache.device, q, lengths, out, lse, scale, window, workspace, stream)
-    if status:
-        _refuse("w4a4_paged_attention", status)
-
-
-def w4a4_block_norm(y, r, x, r_out, gate=None, rows_per_gate: int = 0, scale: float = 1.0, post: int = NORM_RMS,
-                    post_gain=None, post_bias=None, pre: int = NORM_RMS, pre_gain=None, pre_bias=None,
-                    eps: float = 1e-6, stream=None):
-    """r_out = r + scale * gate * post(y); x = pre(r_out): the norm after a block, its gate and
-    residual scale, the residual addition and the norm before the next block in one pass.
-
-    y, x [rows, width] fp16 or bf16 (x None: not wanted); r, r_out the same type or fp32 (r_out may
-    be r).  post, pre: NORM_NONE, NORM_RMS or NORM_LAYER.  gate: [width] or [gates, width], row m
-    under gate row m // rows_per_gate (0: one row for all)."""
-    status = _calls().block_norm(y, r, x, r_out, gate, rows_per_gate, scale, post, post_gain, post_bias, pre, pre_gain,
-                                 pre_bias, eps, stream)
-    if status:
-        _refuse("w4a4_block_norm", status)
 
 
 # ------------------------------------------------------------- layer helper

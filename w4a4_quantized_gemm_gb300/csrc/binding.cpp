@@ -5,9 +5,11 @@
 // launch (5 us beside 2 us on the Grace host), which a decode step's short kernels
 // cannot hide; here it is 0.1 us.
 //
-// Each function takes its arguments by position and returns a w4a4_status as an int
-// (W4A4_ERR_INVALID_ARG for a tensor it cannot describe); None stands for NULL.
+// Arguments go by position or name, None stands for NULL; a call that is refused
+// raises the package's W4A4Error (W4A4_ERR_INVALID_ARG for a tensor that does not fit).
 #include <Python.h>
+
+#include <cmath>
 
 #include <ATen/core/Tensor.h>
 #include <c10/cuda/CUDAStream.h>
@@ -84,17 +86,50 @@ bool stream_of(PyObject* o, int dev, cudaStream_t& s) {
     return !PyErr_Occurred();
 }
 
-const w4a4_kv_cache* cache_of(PyObject* o) {
-    return PyBytes_Check(o) && PyBytes_GET_SIZE(o) == sizeof(w4a4_kv_cache)
-               ? reinterpret_cast<const w4a4_kv_cache*>(PyBytes_AS_STRING(o))
-               : nullptr;
+// Interned names, filled in when the module is loaded.
+PyObject *n_struct, *n_device, *n_ws, *n_workspace, *n_refuse;
+
+// What a PagedKVCache keeps for its calls: the C struct and its device.
+const w4a4_kv_cache* cache_of(PyObject* o, int& dev) {
+    PyObject* bytes = PyObject_GetAttr(o, n_struct);
+    if (!bytes) return nullptr;
+    const w4a4_kv_cache* c = nullptr;  // the object holds the bytes for the length of the call
+    if (PyBytes_Check(bytes) && PyBytes_GET_SIZE(bytes) == sizeof(w4a4_kv_cache))
+        c = reinterpret_cast<const w4a4_kv_cache*>(PyBytes_AS_STRING(bytes));
+    Py_DECREF(bytes);
+    PyObject* device = PyObject_GetAttr(o, n_device);
+    if (!device) return nullptr;
+    dev = int(PyLong_AsLong(device));
+    Py_DECREF(device);
+    return c;
 }
 
-// (cache, device, q, k, v, positions, q_out, seqs, rope, q_gain, k_gain, eps, interleaved, stream)
+// The cache object's workspace for `heads` query heads (a new reference).
+PyObject* workspace_of(PyObject* cache, int64_t heads) {
+    PyObject* key = PyLong_FromLongLong(heads);
+    PyObject* kept = PyObject_GetAttr(cache, n_ws);
+    PyObject* ws = kept && PyDict_Check(kept) ? PyDict_GetItemWithError(kept, key) : nullptr;
+    ws = ws ? Py_NewRef(ws) : PyErr_Occurred() ? nullptr : PyObject_CallMethodOneArg(cache, n_workspace, key);
+    Py_XDECREF(kept);
+    Py_DECREF(key);
+    return ws;
+}
+
+// A parameter's default: required, or one of these.
+enum Default { kRequired, kNone, kZero, kOne, kOneF, kEps, kFalse };
+struct Param {
+    const char* name;
+    Default def;
+};
+
+constexpr Param kAppend[] = {{"q", kRequired},    {"k", kRequired},  {"v", kRequired},    {"positions", kRequired},
+                             {"cache", kRequired}, {"q_out", kRequired}, {"seqs", kNone},  {"rope", kNone},
+                             {"q_gain", kNone},   {"k_gain", kNone}, {"eps", kEps},       {"interleaved", kFalse},
+                             {"stream", kNone}};
 w4a4_status kv_append(PyObject* const* a) {
-    const w4a4_kv_cache* c = cache_of(a[0]);
-    const int dev = int(PyLong_AsLong(a[1]));
-    const at::Tensor* q = tensor(a[2], dev);
+    int dev = -1;
+    const w4a4_kv_cache* c = cache_of(a[4], dev);
+    const at::Tensor* q = c ? tensor(a[0], dev) : nullptr;
     w4a4_kv_append_args x{};
     x.bytes = sizeof(x);
     if (!c || !q || q->dim() != 3 || !type_of(q->scalar_type(), x.dtype)) return W4A4_ERR_INVALID_ARG;
@@ -102,60 +137,72 @@ w4a4_status kv_append(PyObject* const* a) {
     const int64_t n = q->size(0), heads = q->size(1);
     const void* out = nullptr;
     if (!fits(n) || !fits(heads) ||
-        !heads_of(a[2], dev, type, n, heads, c->head_dim, x.q, x.q_token_stride, x.q_head_stride) ||
-        !heads_of(a[3], dev, type, n, c->kv_heads, c->head_dim, x.k, x.k_token_stride, x.k_head_stride) ||
-        !heads_of(a[4], dev, type, n, c->kv_heads, c->head_dim, x.v, x.v_token_stride, x.v_head_stride) ||
-        !vector_of(a[5], dev, ScalarType::Int, n, x.positions) ||
-        !heads_of(a[6], dev, type, n, heads, c->head_dim, out, x.out_token_stride, x.out_head_stride) ||
-        !vector_of(a[7], dev, ScalarType::Int, n, x.seqs) || !vector_of(a[9], dev, type, c->head_dim, x.q_gain) ||
-        !vector_of(a[10], dev, type, c->head_dim, x.k_gain))
+        !heads_of(a[0], dev, type, n, heads, c->head_dim, x.q, x.q_token_stride, x.q_head_stride) ||
+        !heads_of(a[1], dev, type, n, c->kv_heads, c->head_dim, x.k, x.k_token_stride, x.k_head_stride) ||
+        !heads_of(a[2], dev, type, n, c->kv_heads, c->head_dim, x.v, x.v_token_stride, x.v_head_stride) ||
+        !vector_of(a[3], dev, ScalarType::Int, n, x.positions) ||
+        !heads_of(a[5], dev, type, n, heads, c->head_dim, out, x.out_token_stride, x.out_head_stride) ||
+        !vector_of(a[6], dev, ScalarType::Int, n, x.seqs) || !vector_of(a[8], dev, type, c->head_dim, x.q_gain) ||
+        !vector_of(a[9], dev, type, c->head_dim, x.k_gain))
         return W4A4_ERR_INVALID_ARG;
     x.q_out = const_cast<void*>(out);
-    if (a[8] != Py_None) {
-        const at::Tensor* rope = tensor(a[8], dev);
+    if (a[7] != Py_None) {
+        const at::Tensor* rope = tensor(a[7], dev);
         if (!rope || rope->dim() != 3 || rope->size(1) != 2 || !fits(rope->size(0)) || !fits(2 * rope->size(2)) ||
-            !vector_of(a[8], dev, ScalarType::Float, rope->numel(), x.rope))
+            !vector_of(a[7], dev, ScalarType::Float, rope->numel(), x.rope))
             return W4A4_ERR_INVALID_ARG;
         x.rope_rows = int32_t(rope->size(0)), x.rot_dim = int32_t(2 * rope->size(2));
         if (!x.rope) return W4A4_ERR_INVALID_ARG;  // an empty table
     }
     x.tokens = int32_t(n), x.q_heads = int32_t(heads);
-    x.eps = float(PyFloat_AsDouble(a[11]));
-    x.interleaved = PyObject_IsTrue(a[12]);
+    x.eps = float(PyFloat_AsDouble(a[10]));
+    x.interleaved = PyObject_IsTrue(a[11]);
     cudaStream_t stream;
-    if (!stream_of(a[13], dev, stream) || PyErr_Occurred()) return W4A4_ERR_INVALID_ARG;
+    if (!stream_of(a[12], dev, stream) || PyErr_Occurred()) return W4A4_ERR_INVALID_ARG;
     return w4a4_kv_append(c, &x, stream);
 }
 
-// (cache, device, q, lengths, out, lse, scale, window, workspace, stream)
+constexpr Param kAttention[] = {{"q", kRequired}, {"cache", kRequired}, {"lengths", kRequired}, {"out", kRequired},
+                                {"lse", kNone},   {"scale", kNone},     {"window", kZero},      {"workspace", kNone},
+                                {"stream", kNone}};
 w4a4_status paged_attention(PyObject* const* a) {
-    const w4a4_kv_cache* c = cache_of(a[0]);
-    const int dev = int(PyLong_AsLong(a[1]));
-    const at::Tensor *q = tensor(a[2], dev), *ws = tensor(a[8], dev);
+    int dev = -1;
+    const w4a4_kv_cache* c = cache_of(a[1], dev);
+    const at::Tensor* q = c ? tensor(a[0], dev) : nullptr;
     w4a4_paged_attention_args x{};
     x.bytes = sizeof(x);
-    if (!c || !q || !ws || q->dim() != 3 || !type_of(q->scalar_type(), x.dtype) || !ws->is_contiguous())
-        return W4A4_ERR_INVALID_ARG;
+    if (!q || q->dim() != 3 || !type_of(q->scalar_type(), x.dtype)) return W4A4_ERR_INVALID_ARG;
     const ScalarType type = q->scalar_type();
     const int64_t n = c->seqs, heads = q->size(1);
     const void* out = nullptr;
-    if (!fits(heads) || !heads_of(a[2], dev, type, n, heads, c->head_dim, x.q, x.q_token_stride, x.q_head_stride) ||
-        !vector_of(a[3], dev, ScalarType::Int, n, x.lengths) ||
-        !heads_of(a[4], dev, type, n, heads, c->head_dim, out, x.out_token_stride, x.out_head_stride) ||
-        !vector_of(a[5], dev, ScalarType::Float, n * heads, x.lse))
+    if (!fits(heads) || !heads_of(a[0], dev, type, n, heads, c->head_dim, x.q, x.q_token_stride, x.q_head_stride) ||
+        !vector_of(a[2], dev, ScalarType::Int, n, x.lengths) ||
+        !heads_of(a[3], dev, type, n, heads, c->head_dim, out, x.out_token_stride, x.out_head_stride) ||
+        !vector_of(a[4], dev, ScalarType::Float, n * heads, x.lse))
         return W4A4_ERR_INVALID_ARG;
     x.out = const_cast<void*>(out);
-    x.workspace = ws->data_ptr(), x.workspace_bytes = uint64_t(ws->nbytes());
-    x.scale = float(PyFloat_AsDouble(a[6]));
-    const int64_t window = PyLong_AsLongLong(a[7]);
+    x.scale = a[5] == Py_None ? 1.f / std::sqrt(float(c->head_dim)) : float(PyFloat_AsDouble(a[5]));
+    const int64_t window = PyLong_AsLongLong(a[6]);
     x.window = int32_t(window < INT32_MAX ? window : INT32_MAX);
     x.q_heads = int32_t(heads);
     cudaStream_t stream;
-    if (window < 0 || !stream_of(a[9], dev, stream) || PyErr_Occurred()) return W4A4_ERR_INVALID_ARG;
-    return w4a4_paged_attention(c, &x, stream);
+    if (window < 0 || !stream_of(a[8], dev, stream) || PyErr_Occurred()) return W4A4_ERR_INVALID_ARG;
+    PyObject* kept = a[7] == Py_None ? workspace_of(a[1], heads) : Py_NewRef(a[7]);
+    if (!kept) return W4A4_ERR_INVALID_ARG;  // its own error is set
+    const at::Tensor* ws = tensor(kept, dev);
+    w4a4_status st = W4A4_ERR_INVALID_ARG;
+    if (ws && ws->is_contiguous()) {
+        x.workspace = ws->data_ptr(), x.workspace_bytes = uint64_t(ws->nbytes());
+        st = w4a4_paged_attention(c, &x, stream);
+    }
+    Py_DECREF(kept);
+    return st;
 }
 
-// (y, r, x, r_out, gate, rows_per_gate, scale, post, post_gain, post_bias, pre, pre_gain, pre_bias, eps, stream)
+constexpr Param kNorm[] = {{"y", kRequired},   {"r", kRequired},     {"x", kRequired},       {"r_out", kRequired},
+                           {"gate", kNone},    {"rows_per_gate", kZero}, {"scale", kOneF},   {"post", kOne},
+                           {"post_gain", kNone}, {"post_bias", kNone}, {"pre", kOne},        {"pre_gain", kNone},
+                           {"pre_bias", kNone}, {"eps", kEps},         {"stream", kNone}};
 w4a4_status block_norm(PyObject* const* a) {
     w4a4_block_norm_args x{};
     x.bytes = sizeof(x);
@@ -193,30 +240,127 @@ w4a4_status block_norm(PyObject* const* a) {
     return w4a4_block_norm(&x, stream);
 }
 
-template <w4a4_status (*F)(PyObject* const*), int N>
-PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
-    w4a4_status st = W4A4_ERR_INVALID_ARG;
-    if (n != N) {
-        PyErr_Format(PyExc_TypeError, "%d arguments expected, got %zd", N, n);
+// The Python callable of F: fills in F's parameters, calls it, raises where it refuses.
+template <w4a4_status (*F)(PyObject* const*), const Param* P, int N>
+struct Function {
+    static PyObject* names[N];
+    static PyObject* defaults[N];
+    static const char* title;
+
+    static bool init(const char* name) {
+        title = name;
+        for (int i = 0; i < N; ++i) {
+            if (!(names[i] = PyUnicode_InternFromString(P[i].name))) return false;
+            switch (P[i].def) {
+                case kRequired: defaults[i] = nullptr; break;
+                case kNone: defaults[i] = Py_None; break;
+                case kZero: defaults[i] = PyLong_FromLong(0); break;
+                case kOne: defaults[i] = PyLong_FromLong(1); break;
+                case kOneF: defaults[i] = PyFloat_FromDouble(1.0); break;
+                case kEps: defaults[i] = PyFloat_FromDouble(1e-6); break;
+                case kFalse: defaults[i] = Py_False; break;
+            }
+        }
+        return true;
+    }
+
+    static PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kwnames) {
+        if (n > N) {
+            PyErr_Format(PyExc_TypeError, "%s() takes %d arguments, %zd were given", title, N, n);
+            return nullptr;
+        }
+        PyObject* a[N];
+        for (int i = 0; i < N; ++i) a[i] = i < n ? args[i] : nullptr;
+        const Py_ssize_t named = kwnames ? PyTuple_GET_SIZE(kwnames) : 0;
+        for (Py_ssize_t k = 0; k < named; ++k) {
+            PyObject* name = PyTuple_GET_ITEM(kwnames, k);
+            int i = 0;
+            while (i < N && name != names[i]) ++i;
+            if (i == N)  // not the interned string: compare the text
+                for (i = 0; i < N && PyUnicode_Compare(name, names[i]) != 0;) ++i;
+            if (i == N || a[i]) {
+                PyErr_Format(PyExc_TypeError, i == N ? "%s() has no argument %R" : "%s() got %R twice", title, name);
+                return nullptr;
+            }
+            a[i] = args[n + k];
+        }
+        for (int i = 0; i < N; ++i)
+            if (!a[i] && !(a[i] = defaults[i])) {
+                PyErr_Format(PyExc_TypeError, "%s() needs %R", title, names[i]);
+                return nullptr;
+            }
+        w4a4_status st = W4A4_ERR_INVALID_ARG;
+        try {
+            st = F(a);
+        } catch (const std::exception&) {  // torch refuses what it is asked about a tensor
+        }
+        if (st == W4A4_OK) Py_RETURN_NONE;
+        // an argument that is no number, an object that is no cache: the same refusal
+        if (PyErr_Occurred() && (PyErr_ExceptionMatches(PyExc_TypeError) || PyErr_ExceptionMatches(PyExc_AttributeError) ||
+                                 PyErr_ExceptionMatches(PyExc_OverflowError) || PyErr_ExceptionMatches(PyExc_ValueError)))
+            PyErr_Clear();
+        if (!PyErr_Occurred()) {
+            PyObject* package = PyImport_ImportModule("w4a4_quantized_gemm_gb300");
+            PyObject* refuse = package ? PyObject_GetAttr(package, n_refuse) : nullptr;
+            PyObject* done = refuse ? PyObject_CallFunction(refuse, "si", title, int(st)) : nullptr;
+            Py_XDECREF(done);
+            Py_XDECREF(refuse);
+            Py_XDECREF(package);
+            if (!PyErr_Occurred()) PyErr_Format(PyExc_RuntimeError, "%s: status %d", title, int(st));
+        }
         return nullptr;
     }
-    try {
-        st = F(args);
-    } catch (const std::exception&) {  // torch refuses what it is asked about the tensor
-    }
-    PyErr_Clear();  // an argument that is no number
-    return PyLong_FromLong(st);
+};
+template <w4a4_status (*F)(PyObject* const*), const Param* P, int N>
+PyObject* Function<F, P, N>::names[N];
+template <w4a4_status (*F)(PyObject* const*), const Param* P, int N>
+PyObject* Function<F, P, N>::defaults[N];
+template <w4a4_status (*F)(PyObject* const*), const Param* P, int N>
+const char* Function<F, P, N>::title;
+
+using Append = Function<kv_append, kAppend, sizeof(kAppend) / sizeof(Param)>;
+using Attention = Function<paged_attention, kAttention, sizeof(kAttention) / sizeof(Param)>;
+using Norm = Function<block_norm, kNorm, sizeof(kNorm) / sizeof(Param)>;
+
+template <class Fn>
+PyMethodDef method(const char* name, const char* doc) {
+    return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(Fn::call)), METH_FASTCALL | METH_KEYWORDS, doc};
 }
 
-template <w4a4_status (*F)(PyObject* const*), int N>
-constexpr PyMethodDef method(const char* name) {
-    return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(call<F, N>)), METH_FASTCALL, nullptr};
-}
-
-PyMethodDef methods[] = {method<kv_append, 14>("kv_append"), method<paged_attention, 10>("paged_attention"),
-                         method<block_norm, 15>("block_norm"), {nullptr, nullptr, 0, nullptr}};
+PyMethodDef methods[] = {
+    method<Append>("w4a4_kv_append",
+        "w4a4_kv_append(q, k, v, positions, cache, q_out, seqs=None, rope=None, q_gain=None, k_gain=None, eps=1e-06,\n"
+        "               interleaved=False, stream=None)\n--\n\n"
+        "Keys and values of new tokens into `cache` (a PagedKVCache), q and k normalised (gains given) and rotated\n"
+        "(rope given) on the way; the rotated queries go to q_out, which may be q.\n\n"
+        "q, q_out [tokens, q_heads, dim], k, v [tokens, kv_heads, dim]: fp16 or bf16, last dimension contiguous\n"
+        "(slices of a fused q|k|v output).  positions, seqs: int32 [tokens]; seqs None: token t belongs to sequence\n"
+        "t, negative: padding.  rope: fp32 [rows, 2, rot_dim / 2] (w4a4_rope_table).  q_gain, k_gain: [dim]."),
+    method<Attention>("w4a4_paged_attention",
+        "w4a4_paged_attention(q, cache, lengths, out, lse=None, scale=None, window=0, workspace=None, stream=None)\n"
+        "--\n\n"
+        "out [seqs, q_heads, dim] = attention of one new token per sequence, q, over the first lengths[b] tokens\n"
+        "(int32 [seqs]) that `cache` holds of each, or the last `window` of them.\n\n"
+        "scale: of the scores, dim ** -0.5 by default.  lse: fp32 [seqs, q_heads] or None.  workspace: zeroed uint8\n"
+        "of w4a4_paged_attention_workspace_bytes, by default the cache object's own."),
+    method<Norm>("w4a4_block_norm",
+        "w4a4_block_norm(y, r, x, r_out, gate=None, rows_per_gate=0, scale=1.0, post=1, post_gain=None,\n"
+        "                post_bias=None, pre=1, pre_gain=None, pre_bias=None, eps=1e-06, stream=None)\n--\n\n"
+        "r_out = r + scale * gate * post(y); x = pre(r_out): the norm after a block, its gate and residual scale, the\n"
+        "residual addition and the norm before the next block in one pass.\n\n"
+        "y, x [rows, width] fp16 or bf16 (x None: not wanted); r, r_out the same type or fp32 (r_out may be r).\n"
+        "post, pre: NORM_NONE, NORM_RMS (the default) or NORM_LAYER with gain and bias [width].  gate: [width] or [gates, width],\n"
+        "row m under gate row m // rows_per_gate (0: one row for all)."),
+    {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__binding() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__binding() {
+    if (!(n_struct = PyUnicode_InternFromString("_struct")) || !(n_device = PyUnicode_InternFromString("device")) ||
+        !(n_ws = PyUnicode_InternFromString("_ws")) || !(n_workspace = PyUnicode_InternFromString("workspace")) ||
+        !(n_refuse = PyUnicode_InternFromString("_refuse")) || !Append::init("w4a4_kv_append") ||
+        !Attention::init("w4a4_paged_attention") || !Norm::init("w4a4_block_norm"))
+        return nullptr;
+    return PyModule_Create(&module);
+}

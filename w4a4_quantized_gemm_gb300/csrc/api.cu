@@ -552,8 +552,7 @@ w4a4_status w4a4_kv_append(const w4a4_kv_cache* cache, const w4a4_kv_append_args
         (a->q_token_stride != a->out_token_stride || a->q_head_stride != a->out_head_stride))
         return W4A4_ERR_INVALID_ARG;
     if ((st = check_device()) != W4A4_OK) return st;
-    launch_kv_append(*cache, *a, stream);
-    return launch_status();
+    return launch_kv_append(*cache, *a, stream);
 }
 
 w4a4_status w4a4_rope_table(float* rope, int rows, int rot_dim, double theta, cudaStream_t stream) {
@@ -616,8 +615,7 @@ w4a4_status w4a4_block_norm(const w4a4_block_norm_args* a, cudaStream_t stream) 
         return W4A4_ERR_INVALID_ARG;
     w4a4_status st = check_device();
     if (st != W4A4_OK) return st;
-    launch_block_norm(*a, stream);
-    return launch_status();
+    return launch_block_norm(*a, stream);
 }
 
 w4a4_status w4a4_debug_unpack_weights(const void* packed, int N, int K, int r, int8_t* codes, uint16_t* scales,

@@ -23,6 +23,7 @@
 
 #include "elem.cuh"
 #include "kernels.h"
+#include "launch.cuh"
 #include "tc_ptx.cuh"
 
 namespace w4a4 {
@@ -282,7 +283,7 @@ __global__ void __launch_bounds__(NT, CH == 2 ? 512 / NT : 1) block_norm_kernel(
 }
 
 template <class T, class R, int NT, int NC, int CH, bool LAYER>
-void launch_k(const w4a4_block_norm_args& a, cudaStream_t s) {
+w4a4_status launch_k(const w4a4_block_norm_args& a, cudaStream_t s) {
     static std::atomic<int> per_sm{0};  // CTAs that an SM holds (registers), the same on every device
     int n = per_sm.load(std::memory_order_relaxed);
     if (n == 0) {
@@ -292,55 +293,47 @@ void launch_k(const w4a4_block_norm_args& a, cudaStream_t s) {
         per_sm.store(n, std::memory_order_relaxed);
     }
     const int64_t full = n * int64_t(device_sm_count()), ctas = (int64_t(a.rows) * NC + NT - 1) / NT;
-    cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute attr[1];
-    cfg.attrs = attr;
-    cfg.numAttrs = add_pdl_attr(attr, 0);
-    cfg.gridDim = dim3(unsigned(ctas < full ? ctas : full));
-    cfg.blockDim = dim3(NT);
-    cfg.stream = s;
-    cudaLaunchKernelEx(&cfg, block_norm_kernel<T, R, NT, NC, CH, LAYER>, a);
+    const unsigned grid = unsigned(ctas < full ? ctas : full);
     set_dispatch_ints("block_norm rows=%d width=%d threads=%d chunks/thread=%d grid=%d",
-                      {a.rows, a.width, NT, CH, int(cfg.gridDim.x)});
+                      {a.rows, a.width, NT, CH, int(grid)});
+    return launch<block_norm_kernel<T, R, NT, NC, CH, LAYER>>(dim3(grid), NT, 0, s, a);
 }
 
 template <class T, class R, bool LAYER>
-void launch_l(const w4a4_block_norm_args& a, cudaStream_t s) {
+w4a4_status launch_l(const w4a4_block_norm_args& a, cudaStream_t s) {
     const int chunks = a.width / 8;
     // Narrow rows share a warp, and a CTA has four: 8192 rows of 64 (fp16) take 1.7 us, one
     // row to a CTA of one warp 4.2 us; 8192 of 512 take 4.9 us, two warps to a row 5.9 us.
     if (chunks <= 8)
-        launch_k<T, R, 128, 8, 1, LAYER>(a, s);
+        return launch_k<T, R, 128, 8, 1, LAYER>(a, s);
     else if (chunks <= 16)
-        launch_k<T, R, 128, 16, 1, LAYER>(a, s);
+        return launch_k<T, R, 128, 16, 1, LAYER>(a, s);
     else if (chunks <= 32)
-        launch_k<T, R, 128, 32, 1, LAYER>(a, s);
+        return launch_k<T, R, 128, 32, 1, LAYER>(a, s);
     else if (chunks <= 64)
-        launch_k<T, R, 128, 32, 2, LAYER>(a, s);
+        return launch_k<T, R, 128, 32, 2, LAYER>(a, s);
     else if (chunks <= 128)
-        launch_k<T, R, 128, 128, 1, LAYER>(a, s);
+        return launch_k<T, R, 128, 128, 1, LAYER>(a, s);
     else if (chunks <= 256)
-        launch_k<T, R, 128, 128, 2, LAYER>(a, s);
+        return launch_k<T, R, 128, 128, 2, LAYER>(a, s);
     else if (chunks <= 512)
-        launch_k<T, R, 256, 256, 2, LAYER>(a, s);
+        return launch_k<T, R, 256, 256, 2, LAYER>(a, s);
     else if (chunks <= 1024)
-        launch_k<T, R, 512, 512, 2, LAYER>(a, s);
+        return launch_k<T, R, 512, 512, 2, LAYER>(a, s);
     else
-        launch_k<T, R, 512, 512, 4, LAYER>(a, s);
+        return launch_k<T, R, 512, 512, 4, LAYER>(a, s);
 }
 
 template <class T, class R>
-void launch_r(const w4a4_block_norm_args& a, cudaStream_t s) {
-    a.post == W4A4_NORM_LAYER || a.pre == W4A4_NORM_LAYER ? launch_l<T, R, true>(a, s) : launch_l<T, R, false>(a, s);
+w4a4_status launch_r(const w4a4_block_norm_args& a, cudaStream_t s) {
+    return a.post == W4A4_NORM_LAYER || a.pre == W4A4_NORM_LAYER ? launch_l<T, R, true>(a, s) : launch_l<T, R, false>(a, s);
 }
 
 }  // namespace
 
-void launch_block_norm(const w4a4_block_norm_args& a, cudaStream_t s) {
-    if (a.dtype == W4A4_F16)
-        a.res_dtype == W4A4_F32 ? launch_r<F16, F32>(a, s) : launch_r<F16, F16>(a, s);
-    else
-        a.res_dtype == W4A4_F32 ? launch_r<BF16, F32>(a, s) : launch_r<BF16, BF16>(a, s);
+w4a4_status launch_block_norm(const w4a4_block_norm_args& a, cudaStream_t s) {
+    if (a.dtype == W4A4_F16) return a.res_dtype == W4A4_F32 ? launch_r<F16, F32>(a, s) : launch_r<F16, F16>(a, s);
+    return a.res_dtype == W4A4_F32 ? launch_r<BF16, F32>(a, s) : launch_r<BF16, BF16>(a, s);
 }
 
 }  // namespace w4a4

@@ -16,6 +16,7 @@
 // HBM needs about 40 KB in flight per SM, and the first loads then cover the look-ups.
 #include "elem.cuh"
 #include "kernels.h"
+#include "launch.cuh"
 
 namespace w4a4 {
 namespace {
@@ -209,48 +210,34 @@ __global__ void rope_table_kernel(float* rope, int64_t n, int half, double log2_
 }
 
 template <class T, bool E4M3, bool MANY>
-void launch_m(const w4a4_kv_cache& c, const w4a4_kv_append_args& a, cudaStream_t s) {
+w4a4_status launch_m(const w4a4_kv_cache& c, const w4a4_kv_append_args& a, cudaStream_t s) {
     const int lph = c.head_dim <= 64 ? 4 : c.head_dim <= 128 ? 8 : 16;
     const int groups = threads_of(MANY) / lph, rows = a.q_heads + 2 * c.kv_heads;
     // A token's heads are spread over as many CTAs as the GPU holds at once.
     const int most = (rows + groups - 1) / groups, room = per_sm(MANY) * device_sm_count() / a.tokens;
     const int want = room > 1 ? room : 1;
-    cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute attr[1];
-    cfg.attrs = attr;
-    cfg.numAttrs = add_pdl_attr(attr, 0);
-    cfg.gridDim = dim3(unsigned(a.tokens), unsigned(most < want ? most : want));
-    cfg.blockDim = dim3(threads_of(MANY));
-    cfg.stream = s;
-    if (lph == 4)
-        cudaLaunchKernelEx(&cfg, kv_append_kernel<T, E4M3, 4, MANY>, c, a);
-    else if (lph == 8)
-        cudaLaunchKernelEx(&cfg, kv_append_kernel<T, E4M3, 8, MANY>, c, a);
-    else
-        cudaLaunchKernelEx(&cfg, kv_append_kernel<T, E4M3, 16, MANY>, c, a);
+    const dim3 grid(unsigned(a.tokens), unsigned(most < want ? most : want));
     set_dispatch_ints(E4M3 ? "kv_append tokens=%d heads=%d+2x%d dim=%d e4m3 cache threads=%d grid=%dx%d"
                            : "kv_append tokens=%d heads=%d+2x%d dim=%d 16-bit cache threads=%d grid=%dx%d",
-                      {a.tokens, a.q_heads, c.kv_heads, c.head_dim, threads_of(MANY), a.tokens, int(cfg.gridDim.y)});
+                      {a.tokens, a.q_heads, c.kv_heads, c.head_dim, threads_of(MANY), a.tokens, int(grid.y)});
+    if (lph == 4) return launch<kv_append_kernel<T, E4M3, 4, MANY>>(grid, threads_of(MANY), 0, s, c, a);
+    if (lph == 8) return launch<kv_append_kernel<T, E4M3, 8, MANY>>(grid, threads_of(MANY), 0, s, c, a);
+    return launch<kv_append_kernel<T, E4M3, 16, MANY>>(grid, threads_of(MANY), 0, s, c, a);
 }
 
 template <class T, bool E4M3>
-void launch_t(const w4a4_kv_cache& c, const w4a4_kv_append_args& a, cudaStream_t s) {
-    if (a.tokens > kFew * device_sm_count())
-        launch_m<T, E4M3, true>(c, a, s);
-    else
-        launch_m<T, E4M3, false>(c, a, s);
+w4a4_status launch_t(const w4a4_kv_cache& c, const w4a4_kv_append_args& a, cudaStream_t s) {
+    return a.tokens > kFew * device_sm_count() ? launch_m<T, E4M3, true>(c, a, s) : launch_m<T, E4M3, false>(c, a, s);
 }
 
 }  // namespace
 
 w4a4_status append_read_and_clear_status() { return take_status_word(g_append_status); }
 
-void launch_kv_append(const w4a4_kv_cache& c, const w4a4_kv_append_args& a, cudaStream_t s) {
+w4a4_status launch_kv_append(const w4a4_kv_cache& c, const w4a4_kv_append_args& a, cudaStream_t s) {
     const bool e4m3 = c.dtype == W4A4_E4M3;
-    if (a.dtype == W4A4_F16)
-        e4m3 ? launch_t<F16, true>(c, a, s) : launch_t<F16, false>(c, a, s);
-    else
-        e4m3 ? launch_t<BF16, true>(c, a, s) : launch_t<BF16, false>(c, a, s);
+    if (a.dtype == W4A4_F16) return e4m3 ? launch_t<F16, true>(c, a, s) : launch_t<F16, false>(c, a, s);
+    return e4m3 ? launch_t<BF16, true>(c, a, s) : launch_t<BF16, false>(c, a, s);
 }
 
 void launch_rope_table(float* rope, int rows, int rot_dim, double theta, cudaStream_t s) {

@@ -31,6 +31,7 @@
 
 #include "elem.cuh"
 #include "kernels.h"
+#include "launch.cuh"
 #include "tc_ptx.cuh"
 
 namespace w4a4 {
@@ -885,20 +886,11 @@ w4a4_status launch_n(Args& A, cudaStream_t s) {
     if (units > INT32_MAX) return W4A4_ERR_UNSUPPORTED_SHAPE;
     const int64_t grid = units < 1 ? 1 : units < full ? units : full;
     A.by_ctas = Divisor(int(grid));
-    cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute attr[1];
-    cfg.attrs = attr;
-    cfg.numAttrs = add_pdl_attr(attr, 0);
-    cfg.gridDim = dim3(unsigned(grid));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = P::kBytes;
-    cfg.stream = s;
-    cudaLaunchKernelEx(&cfg, paged_attention_kernel<D, CT, NT>, static_cast<const Args&>(A));
     set_dispatch_ints(CT == kF16    ? "paged_attention f16 seqs=%d heads=%d/%d dim=%d stages=%d heads/unit=%d grid=%d"
                       : CT == kBF16 ? "paged_attention bf16 seqs=%d heads=%d/%d dim=%d stages=%d heads/unit=%d grid=%d"
                                     : "paged_attention e4m3 seqs=%d heads=%d/%d dim=%d stages=%d heads/unit=%d grid=%d",
                       {A.c.seqs, A.q_heads, A.c.kv_heads, D, P::kStages, A.together, int(grid)});
-    return launch_status();
+    return launch<paged_attention_kernel<D, CT, NT>>(dim3(unsigned(grid)), kThreads, P::kBytes, s, A);
 }
 
 template <int D, int CT>

@@ -621,6 +621,14 @@ def test_norm_widths(width, rows):
     check_norm(BF16, F32, rows, width, 2, 2, "shared", seed=width)
 
 
+@pytest.mark.parametrize("rows, width", [(1301, 1024), (1500, 520), (20011, 64), (9001, 200), (5003, 512), (2503, 2048),
+                                         (1999, 4096), (400, 16384)])
+def test_norm_many_rows(rows, width):
+    """More rows than CTAs hold at once: each takes several, with the next one's loads in flight."""
+    check_norm(F16, F16, rows, width, 1, 1, "rows", seed=rows, per=7)
+    check_norm(BF16, F32, rows, width, 2, 2, "shared", seed=rows, in_place=True)
+
+
 def test_norm_options():
     check_norm(F16, F16, 700, 1024, 1, 1, "none", scale=1.0, gains=False, biases=False)
     check_norm(F16, F16, 50, 512, 2, 2, "rows", pad=24)

@@ -77,11 +77,11 @@ __device__ __forceinline__ void ld_once8(const float* p, bool wide, uint4 (&v)[2
 }
 
 // A thread's chunks of a vector [W] of a 16-bit type; `fill` (two elements) where there
-// is none.  Held in registers for all rows, or read where they are used (CH > 2: too
-// many to hold).
+// is none.  Held in registers for all rows, or read where they are used (512 threads of
+// four chunks: too many to hold).
 template <class T, int NC, int CH>
 struct Vector {
-    static constexpr bool kHeld = CH <= 2;
+    static constexpr bool kHeld = CH <= 2 || NC == 32;
     const char* at;
     uint32_t fill;
     uint4 v[kHeld ? CH : 1];
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(NT, CH == 2 ? 512 / NT : 1) block_norm_kernel(
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
             const int k = (c * NC + threadIdx.x % NC) * 8;
-            if (k >= W || m >= rows) continue;
+            if (k >= W || (kRows > 1 && m >= rows)) continue;
             ny[c] = ld_once(y + 2 * k);
             if constexpr (R::kSize == 4)
                 ld_once8(reinterpret_cast<const float*>(r) + k, wide, nr[c]);
@@ -304,6 +304,8 @@ w4a4_status launch_l(const w4a4_block_norm_args& a, cudaStream_t s) {
     const int chunks = a.width / 8;
     // Narrow rows share a warp, and a CTA has four: 8192 rows of 64 (fp16) take 1.7 us, one
     // row to a CTA of one warp 4.2 us; 8192 of 512 take 4.9 us, two warps to a row 5.9 us.
+    // Up to 1024 a warp has a row to itself where there are rows enough, without barriers:
+    // 8192 of 1024, LayerNorms, 13.3 us, four warps to a row 17.0 us; but 700 take 3.4 and 2.7.
     if (chunks <= 8)
         return launch_k<T, R, 128, 8, 1, LAYER>(a, s);
     else if (chunks <= 16)
@@ -312,6 +314,8 @@ w4a4_status launch_l(const w4a4_block_norm_args& a, cudaStream_t s) {
         return launch_k<T, R, 128, 32, 1, LAYER>(a, s);
     else if (chunks <= 64)
         return launch_k<T, R, 128, 32, 2, LAYER>(a, s);
+    else if (chunks <= 128 && a.rows > 8 * device_sm_count())
+        return launch_k<T, R, 128, 32, 4, LAYER>(a, s);
     else if (chunks <= 128)
         return launch_k<T, R, 128, 128, 1, LAYER>(a, s);
     else if (chunks <= 256)

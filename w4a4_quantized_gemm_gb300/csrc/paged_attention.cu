@@ -155,6 +155,12 @@ __device__ __forceinline__ int add_acq_rel(int32_t* p, int v) {
     return old;
 }
 
+// n / d for 0 <= n <= 2^20 and d >= 1: (n + 1/2) / d is at least 1 / (2 d) away from a whole
+// number, the division off by 2 ulp and the rounding of d, together less than n / d * 2^-21.
+// (An integer division takes a hundred cycles and more, and a short sequence's way through
+// the kernel had four: 2 x 603 tokens, D = 256: 11.4 -> 10.9 us.)
+__device__ __forceinline__ int small_quotient(int n, int d) { return int(__fdividef(n + 0.5f, float(d))); }
+
 // How the units are shared out: the first `more` CTAs take each + 1, the others each.
 struct Share {
     int each, more;
@@ -297,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
             if (groups <= ctas) {
                 piece = share.each + (share.more > 0);
                 for (int tries = 0; tries < 8; ++tries) {
-                    pieces = (mine + piece - 1) / piece;
+                    pieces = small_quotient(mine + piece - 1, piece);
                     int all;
                     upto_pieces = scan_of(pieces, all);
                     if (all * A.heads <= ctas) {
@@ -338,15 +344,15 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
             at.b = found[0], seq_tiles = found[1], at.lo = found[2], at.n = found[3], pieces = found[4], in = found[5];
             at.tiles = tiles_of(A, at.n);
         }
-        // in + 1/2 is at least 1 / (2 tiles) away from a multiple of tiles
         const int of = piece > 0 ? pieces : at.tiles;
-        at.hc = in < (1 << 20) ? int(__fdividef(in + 0.5f, of)) : in / of;
+        at.hc = in < (1 << 20) ? small_quotient(in, of) : in / of;
         at.tile = in - at.hc * of;
         if (piece > 0) {
             const int k = at.tile;
             c0 = c - k, c1 = c0 + pieces - 1;
-            at.tile = at.tiles * k / pieces;
-            count = at.tiles * (k + 1) / pieces - at.tile;
+            const int least = small_quotient(at.tiles, pieces), more = at.tiles - least * pieces;
+            at.tile = least * k + min(k, more);
+            count = least + (k < more);
             first = seq_tiles * A.heads + at.hc * at.tiles + at.tile;
         }
     }
@@ -686,7 +692,7 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
             if (in >= A.group) return;
             const int h = head * A.group + in;
             const float vs = CT == kE4M3 && A.c.v_scale ? A.c.v_scale[head] : 1.f;
-            const float inv = l == 0.f ? 0.f : vs / l;
+            const float inv = l == 0.f ? 0.f : __fdividef(vs, l);  // 2 ulp
             uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<char*>(A.out) + 2 * (was.b * A.o_token + h * A.o_head + e));
             const float x0 = o.x * inv, x1 = o.y * inv, x2 = o.z * inv, x3 = o.w * inv;
             *reinterpret_cast<uint2*>(dst) = A.q_bf16 ? make_uint2(BF16::down(x0, x1), BF16::down(x2, x3))

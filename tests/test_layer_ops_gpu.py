@@ -704,3 +704,9 @@ def test_norm_refusals_of_the_binding():
             w4.w4a4_block_norm(**{**good, **bad})
     w4.w4a4_block_norm(**good)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("tokens", [2500, 3100, 4200, 5600])
+def test_append_tokens_that_share_ctas_out(tokens):
+    """Many tokens of many heads: one or two CTAs a token, by how full the GPU's last time over is."""
+    run_append(F16, F16, 64, 64, False, True, 64, "NHD", tokens, [tokens - 697, 700], [tokens - 700, 700], 56, 4)

@@ -214,8 +214,14 @@ w4a4_status launch_m(const w4a4_kv_cache& c, const w4a4_kv_append_args& a, cudaS
     const int lph = c.head_dim <= 64 ? 4 : c.head_dim <= 128 ? 8 : 16;
     const int groups = threads_of(MANY) / lph, rows = a.q_heads + 2 * c.kv_heads;
     // A token's heads are spread over as many CTAs as the GPU holds at once.
-    const int most = (rows + groups - 1) / groups, room = per_sm(MANY) * device_sm_count() / a.tokens;
-    const int want = room > 1 ? room : 1;
+    const int most = (rows + groups - 1) / groups, full = per_sm(MANY) * device_sm_count();
+    int want = full / a.tokens > 1 ? full / a.tokens : 1;
+    // Many tokens that fill the GPU once or twice but for a quarter or more of the last time:
+    // two CTAs a token, where it has heads enough to repay the second look-up.  Of 48 heads of
+    // 128 (fp16), 2500 tokens take 12.4 us, 15.2 with one; 6000 tokens 28.5 and 31.5; but 4200
+    // (full and a little) 19.0 and 17.9, and 2500 tokens of 24 heads of 64 5.7 and 5.4.
+    const int over = a.tokens % full;
+    if (MANY && want == 1 && a.tokens < 2 * full && over > full / 8 && over <= full * 3 / 4 && most > 3 * kAhead) want = 2;
     const dim3 grid(unsigned(a.tokens), unsigned(most < want ? most : want));
     set_dispatch_ints(E4M3 ? "kv_append tokens=%d heads=%d+2x%d dim=%d e4m3 cache threads=%d grid=%dx%d"
                            : "kv_append tokens=%d heads=%d+2x%d dim=%d 16-bit cache threads=%d grid=%dx%d",

@@ -710,3 +710,17 @@ def test_norm_refusals_of_the_binding():
 def test_append_tokens_that_share_ctas_out(tokens):
     """Many tokens of many heads: one or two CTAs a token, by how full the GPU's last time over is."""
     run_append(F16, F16, 64, 64, False, True, 64, "NHD", tokens, [tokens - 697, 700], [tokens - 700, 700], 56, 4)
+
+
+@pytest.mark.parametrize("seqs, longest, hkv, group, dim, dtype, window", [
+    (200, 588, 1, 16, 96, E4M3, 400), (140, 300, 2, 4, 128, F16, 0), (152, 700, 1, 1, 64, F16, 0), (300, 200, 1, 4, 128, BF16, 0),
+    (150, 900, 1, 7, 256, E4M3, 0), (440, 150, 1, 2, 64, E4M3, 100), (1000, 70, 1, 2, 64, F16, 0)])
+def test_attention_short_runs_of_many_sequences(seqs, longest, hkv, group, dim, dtype, window):
+    """More sequences than a CTA has threads, some empty, some long: single pieces as long as there are CTAs for them."""
+    g = gen(seqs)
+    lengths = torch.randint(0, longest + 1, (seqs,), generator=g).tolist()
+    lengths[0], lengths[1], lengths[-1], lengths[-2] = 0, 4 * longest, longest, 0
+    c = Cache(lengths, 16, hkv, dim, dtype, seed=seqs)
+    check_attention(c, randn(g, seqs, hkv * group, dim).to(BF16 if dtype == BF16 else F16), lengths, window=window)
+    c = Cache([longest] * seqs, 16, hkv, dim, dtype, seed=seqs)
+    check_attention(c, randn(g, seqs, hkv * group, dim).to(BF16 if dtype == BF16 else F16), [longest] * seqs, window=window)

@@ -234,7 +234,8 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
     // A run of few units, though, is one piece of one (sequence, head group), so that a CTA
     // has one part to leave and one join to take part in: pieces of at most `piece` units,
     // the least for which there are CTAs enough (8 sequences of 700 tokens: 9.2 us, 10.8
-    // with runs over two (sequence, head group)s).
+    // with runs over two (sequence, head group)s; 200 windows of 588 tokens, 8-bit, D = 96: 13.4
+    // and 17.2 us).
     int first, count;
     Share share;
     int piece = 0, c0 = 0, c1 = 0;  // piece > 0: the CTAs that share this one's (sequence, head group)
@@ -244,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
         const bool few = B <= 32;
         const int per = few ? 1 : (B + kThreads - 1) / kThreads, me = few ? lane : tid;
         const int b0 = min(B, me * per), b1 = min(B, b0 + per);
-        int mine = 0, lo = 0, n = 0;
+        int mine = 0, first_tiles = 0, lo = 0, n = 0;
         bool bad = false, empty = false;
         for (int b = b0; b < b1; ++b) {
             const int len = A.lengths[b];
@@ -252,6 +253,7 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
             range_of(A, b, lo, n);
             empty |= n == 0;
             mine += tiles_of(A, n);
+            if (b == b0) first_tiles = mine;
         }
         if (bad && blockIdx.x == 0) atomicExch(&g_attention_status, int(W4A4_ERR_INDEX));
         // inclusive scan over the sequences, and their sum
@@ -297,13 +299,22 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
         const int ctas = gridDim.x, c = blockIdx.x;
         share.each = total < ctas ? 1 : A.by_ctas.quotient(total);
         share.more = total < ctas ? 0 : total - share.each * ctas;
-        int pieces = 0, upto_pieces = 0;  // of this thread's sequence, of those up to it; for all head groups
-        if (per == 1 && total > ctas && share.each < kFewUnits) {
-            const int groups = (few ? __popc(__ballot_sync(0xffffffffu, mine > 0)) : __syncthreads_count(mine > 0)) * A.heads;
+        int pieces = 0, upto_pieces = 0;  // of this thread's sequences, of those up to them; of a head group
+        auto pieces_of = [&](int tiles) { return small_quotient(tiles + piece - 1, piece); };
+        if (total > ctas && share.each < kFewUnits) {
+            // the (sequence, head group)s with tokens, or all where a thread has several sequences
+            const int groups = (few       ? __popc(__ballot_sync(0xffffffffu, mine > 0))
+                                : per > 1 ? B
+                                          : __syncthreads_count(mine > 0)) * A.heads;
             if (groups <= ctas) {
                 piece = share.each + (share.more > 0);
                 for (int tries = 0; tries < 8; ++tries) {
-                    pieces = small_quotient(mine + piece - 1, piece);
+                    pieces = pieces_of(first_tiles);
+                    for (int b = b0 + 1; b < b1; ++b) {
+                        int l, k;
+                        range_of(A, b, l, k);
+                        pieces += pieces_of(tiles_of(A, k));
+                    }
                     int all;
                     upto_pieces = scan_of(pieces, all);
                     if (all * A.heads <= ctas) {
@@ -318,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
         // the thread that has this CTA's first unit tells the others of its sequence
         first = share.start(c);
         count = share.start(c + 1) - first;
-        const int from = (upto_pieces - pieces) * A.heads;  // pieces before the sequence's
+        int from = (upto_pieces - pieces) * A.heads;  // pieces before the sequence's
         const bool here = piece > 0 ? from <= c && c < upto_pieces * A.heads
                                     : before * A.heads <= first && first < upto * A.heads;
         int b = b0;
@@ -326,7 +337,13 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
             for (; b < b1; ++b) {
                 range_of(A, b, lo, n);
                 mine = tiles_of(A, n);
-                if (first < (before + mine) * A.heads) break;
+                if (piece > 0) {
+                    pieces = pieces_of(mine);
+                    if (c < from + pieces * A.heads) break;
+                    from += pieces * A.heads;
+                } else if (first < (before + mine) * A.heads) {
+                    break;
+                }
                 before += mine;
             }
         int in = piece > 0 ? c - from : first - before * A.heads;  // into the sequence's pieces, or units
@@ -868,7 +885,7 @@ w4a4_status launch_n(Args& A, cudaStream_t s) {
     //    365 and 350 us).
     //  * Neither where there is less work: it makes (sequence, head group) pairs fewer and
     //    their splits, so the joins, longer (8 x 5000 tokens, fp16, D = 128: 40 and 34 us; 2
-    //    x 642, E4M3, D = 256, groups of 16: 39 and 10.9 us).
+    //    x 642, E4M3, D = 256, groups of 16: 39 and 10.6 us).
     //  * With sequences of one step, and more of them than CTAs, no warp is left without
     //    tokens (128 sequences of 4 tokens: 4.9 and 12.7 us).
     A.together = 1;

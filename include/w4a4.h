@@ -406,8 +406,9 @@ w4a4_status w4a4_rope_table(float* rope, int rows, int rot_dim, double theta, cu
  * [0, pages) are left out; both set W4A4_ERR_INDEX.
  * workspace: w4a4_paged_attention_workspace_bytes bytes (0: bad arguments),
  * zeroed once by the caller and left zeroed where it has to be: it holds the
- * parts of sequences that are split between CTAs.  Calls that may overlap on the
- * GPU must not share it.  The result does not depend on the order in which the
+ * parts of sequences that are split between CTAs.  A buffer that is large enough
+ * for each serves calls of any shapes, one after another; calls that may overlap
+ * on the GPU must not share it.  The result does not depend on the order in which the
  * CTAs finish: the parts are joined in the order of the tokens. */
 typedef struct {
     uint64_t bytes;

@@ -1,0 +1,45 @@
+"""The cache, attention and norm operators as a server uses them: workspaces shared and dropped, host threads,
+streams, devices, strides that no index uses; and values at the borders of their types.
+
+References and tolerances as in test_layer_ops_gpu."""
+import math
+import threading
+
+import pytest
+import torch
+
+import w4a4_quantized_gemm_gb300 as w4
+from tests.test_layer_ops_gpu import (BF16, E4M3, F16, F64, SLACK, Cache, attend, attention_ref, check, check_attention, gen,
+                                      randn, tiny, u)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from w4a4_quantized_gemm_gb300 import build
+    build.build()
+    w4.lib()
+    w4.w4a4_device_status()
+
+
+def test_attention_one_workspace_for_calls_of_all_shapes():
+    """A buffer that is large enough and was zeroed once serves any sequence of calls: split sequences of one
+    batch, a larger batch whose late sequence goes over more than sixteen CTAs, other head dimensions."""
+    shapes = [([5000], 8, 2, 128), ([1] * 8 + [40000] + [1] * 55, 8, 2, 128), ([700] * 3, 16, 1, 64), ([3000, 9], 2, 9, 96),
+              ([9000], 1, 8, 256), ([2] * 30 + [30000], 4, 1, 64)]
+    size = lambda lengths, hkv, group, dim: w4.lib().w4a4_paged_attention_workspace_bytes(len(lengths), hkv * group, hkv, dim)
+    ws = torch.zeros(max(size(*s) for s in shapes), dtype=torch.uint8, device="cuda")
+    calls = []
+    for i, (lengths, hkv, group, dim) in enumerate(shapes):
+        c = Cache(lengths, 16, hkv, dim, F16, seed=40 + i)
+        q = randn(gen(50 + i), len(lengths), hkv * group, dim).to(F16)
+        want, _ = check_attention(c, q, lengths, what=f"shape {i}")
+        calls.append((c, q.cuda(), torch.tensor(lengths, dtype=torch.int32, device="cuda"), want))
+    for turn in range(2):
+        for i, (c, q, n, want) in enumerate(calls):
+            out = torch.full_like(q, float("nan"))
+            w4.w4a4_paged_attention(q, c.handle, n, out, workspace=ws)
+            torch.cuda.synchronize()
+            assert torch.equal(out.view(torch.int16), want.view(torch.int16)), (turn, i)
+    assert w4.w4a4_device_status() == 0

@@ -570,7 +570,7 @@ w4a4_status w4a4_rope_table(float* rope, int rows, int rot_dim, double theta, cu
 size_t w4a4_paged_attention_workspace_bytes(int seqs, int q_heads, int kv_heads, int head_dim) {
     if (seqs < 0 || kv_heads < 1 || q_heads < kv_heads || q_heads % kv_heads != 0) return 0;
     if (head_dim != 64 && head_dim != 96 && head_dim != 128 && head_dim != 256) return 0;
-    return attention_workspace_bytes(seqs, q_heads, kv_heads, head_dim);
+    return attention_workspace_bytes(seqs, q_heads, kv_heads);
 }
 
 w4a4_status w4a4_paged_attention(const w4a4_kv_cache* cache, const w4a4_paged_attention_args* a,
@@ -589,7 +589,7 @@ w4a4_status w4a4_paged_attention(const w4a4_kv_cache* cache, const w4a4_paged_at
         return W4A4_ERR_MISALIGNED;
     for (const int64_t s : {a->q_token_stride, a->q_head_stride, a->out_token_stride, a->out_head_stride})
         if (!good_stride(s, 2)) return W4A4_ERR_MISALIGNED;
-    if (a->workspace_bytes < attention_workspace_bytes(cache->seqs, a->q_heads, cache->kv_heads, cache->head_dim))
+    if (a->workspace_bytes < attention_workspace_bytes(cache->seqs, a->q_heads, cache->kv_heads))
         return W4A4_ERR_WORKSPACE;
     if ((st = check_device()) != W4A4_OK) return st;
     return launch_paged_attention(*cache, *a, stream);

@@ -70,7 +70,7 @@ w4a4_status run_svd_lora(const float* W, int N, int K, int r, int rounds, int po
 w4a4_status launch_kv_append(const w4a4_kv_cache& c, const w4a4_kv_append_args& a, cudaStream_t s);
 void launch_rope_table(float* rope, int rows, int rot_dim, double theta, cudaStream_t s);
 // paged_attention.cu
-size_t attention_workspace_bytes(int seqs, int q_heads, int kv_heads, int head_dim);
+size_t attention_workspace_bytes(int seqs, int q_heads, int kv_heads);
 w4a4_status launch_paged_attention(const w4a4_kv_cache& c, const w4a4_paged_attention_args& a, cudaStream_t s);
 // block_norm.cu
 w4a4_status launch_block_norm(const w4a4_block_norm_args& a, cudaStream_t s);

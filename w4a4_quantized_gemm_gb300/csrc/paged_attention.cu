@@ -27,6 +27,7 @@
 //  * A run that ends inside a (sequence, head group) leaves its maximum, sum and output in
 //    the workspace.  Parts are joined sixteen at a time, in token order, by the CTA that
 //    completes the sixteen, and those by the CTA that completes the last.
+#include <algorithm>
 #include <atomic>
 
 #include "elem.cuh"
@@ -849,10 +850,14 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
 // CTAs of a launch at most: as many as the plan of any cache type puts on an SM.
 constexpr int max_ctas(int head_dim) { return kMaxSms * (head_dim == 64 ? 3 : head_dim == 256 ? 1 : 2); }
 int most_groups(int q_heads, int kv_heads) { return kv_heads * ((q_heads / kv_heads + 7) / 8); }  // of a sequence
-size_t part_floats(int head_dim) { return size_t(kPartRows) * (head_dim + 2); }
-size_t counters_bytes(int seqs, int heads, int head_dim) {
-    return align256((size_t(seqs) * heads + 2 * max_ctas(head_dim)) * 4);
-}
+constexpr size_t part_floats(int head_dim) { return size_t(kPartRows) * (head_dim + 2); }
+// The workspace: room for the parts and the joins of any head dimension, then the counters
+// of first joins, then those of last ones.  Where the counters start depends on no shape,
+// so that one buffer serves calls of all shapes: no part is ever written where another
+// call counts, and every counter is zero between calls.
+constexpr size_t parts_bytes(int head_dim) { return 4 * max_ctas(head_dim) * part_floats(head_dim) * 4; }
+constexpr size_t kPartsRoom = std::max({parts_bytes(64), parts_bytes(96), parts_bytes(128), parts_bytes(256)});
+constexpr int kMostCtas = std::max({max_ctas(64), max_ctas(96), max_ctas(128), max_ctas(256)});
 
 template <int D, int CT, int NT>
 w4a4_status launch_n(Args& A, cudaStream_t s) {
@@ -934,8 +939,8 @@ w4a4_status launch_d(Args& A, cudaStream_t s) {
 
 w4a4_status attention_read_and_clear_status() { return take_status_word(g_attention_status); }
 
-size_t attention_workspace_bytes(int seqs, int q_heads, int kv_heads, int head_dim) {
-    return counters_bytes(seqs, most_groups(q_heads, kv_heads), head_dim) + 4 * max_ctas(head_dim) * part_floats(head_dim) * 4;
+size_t attention_workspace_bytes(int seqs, int q_heads, int kv_heads) {
+    return kPartsRoom + align256((2 * kMostCtas + size_t(seqs) * most_groups(q_heads, kv_heads)) * 4);
 }
 
 w4a4_status launch_paged_attention(const w4a4_kv_cache& c, const w4a4_paged_attention_args& a, cudaStream_t s) {
@@ -951,10 +956,10 @@ w4a4_status launch_paged_attention(const w4a4_kv_cache& c, const w4a4_paged_atte
     A.token_stride[0] = int(c.k_token_stride * size), A.token_stride[1] = int(c.v_token_stride * size);
     A.head_stride[0] = int(c.k_head_stride * size), A.head_stride[1] = int(c.v_head_stride * size);
     A.by_page = Divisor(c.page_size);
-    A.joined = static_cast<int32_t*>(a.workspace);
-    A.arrived = A.joined + 2 * max_ctas(c.head_dim);
+    A.parts = static_cast<float*>(a.workspace);
     A.joined_at = 2 * max_ctas(c.head_dim) * int64_t(part_floats(c.head_dim));
-    A.parts = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + counters_bytes(c.seqs, most_groups(a.q_heads, c.kv_heads), c.head_dim));
+    A.joined = reinterpret_cast<int32_t*>(static_cast<char*>(a.workspace) + kPartsRoom);
+    A.arrived = A.joined + 2 * kMostCtas;
     A.q_token = a.q_token_stride, A.q_head = a.q_head_stride;
     A.o_token = a.out_token_stride, A.o_head = a.out_head_stride;
     A.scale_log2 = a.scale * 1.44269504088896341f;

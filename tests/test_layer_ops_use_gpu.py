@@ -43,3 +43,25 @@ def test_attention_one_workspace_for_calls_of_all_shapes():
             torch.cuda.synchronize()
             assert torch.equal(out.view(torch.int16), want.view(torch.int16)), (turn, i)
     assert w4.w4a4_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16, E4M3])
+def test_attention_rows_without_weight_are_zero_whatever_the_values(dtype):
+    """Every score -inf: out = 0 and lse = -inf, with infinities and NaN among the values."""
+    lengths = [40, 3000]
+    c = Cache(lengths, 16, 2, 64, F16 if dtype == E4M3 else dtype, seed=65)
+    act = BF16 if dtype == BF16 else F16
+    q = randn(gen(66), 2, 4, 64).abs().to(act)
+    if dtype == E4M3:  # E4M3 has no infinity: the query brings it
+        c = Cache(lengths, 16, 2, 64, E4M3, seed=65, scales=False)
+        c.k[..., 0] = torch.full_like(c.k[..., 0].float(), -1.0).to(E4M3)
+        q[..., 0] = math.inf
+    else:
+        c.k[..., 0] = -math.inf
+    v = c.v.float()
+    v[c.table[0, 1].long(), 3, 0, 5] = float("nan")
+    v[c.table[1, 100].long(), 7, 1, 6] = math.inf if dtype != E4M3 else float("nan")
+    c.v = v.to(c.dtype)
+    c.to_gpu()
+    out, lse = attend(c, q, lengths)
+    assert torch.all(out == 0) and torch.all(lse == -math.inf)

@@ -710,9 +710,12 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
             if (in >= A.group) return;
             const int h = head * A.group + in;
             const float vs = CT == kE4M3 && A.c.v_scale ? A.c.v_scale[head] : 1.f;
-            const float inv = l == 0.f ? 0.f : __fdividef(vs, l);  // 2 ulp
+            const float inv = __fdividef(vs, l);  // 2 ulp
             uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<char*>(A.out) + 2 * (was.b * A.o_token + h * A.o_head + e));
-            const float x0 = o.x * inv, x1 = o.y * inv, x2 = o.z * inv, x3 = o.w * inv;
+            // without weight: zeros, although a weight of zero times an infinite value or a NaN is in o
+            const bool none = l == 0.f;
+            const float x0 = none ? 0.f : o.x * inv, x1 = none ? 0.f : o.y * inv, x2 = none ? 0.f : o.z * inv,
+                        x3 = none ? 0.f : o.w * inv;
             *reinterpret_cast<uint2*>(dst) = A.q_bf16 ? make_uint2(BF16::down(x0, x1), BF16::down(x2, x3))
                                                       : make_uint2(F16::down(x0, x1), F16::down(x2, x3));
             if (A.lse && e == 0) A.lse[int64_t(was.b) * A.q_heads + h] = (m + log2f(l)) * 0.693147180559945309f;

@@ -65,3 +65,30 @@ def test_attention_rows_without_weight_are_zero_whatever_the_values(dtype):
     c.to_gpu()
     out, lse = attend(c, q, lengths)
     assert torch.all(out == 0) and torch.all(lse == -math.inf)
+
+
+@pytest.mark.parametrize("dtype, act", [(F16, F16), (BF16, BF16), (E4M3, F16)])
+@pytest.mark.parametrize("below", [12, 18, 26])
+def test_attention_many_small_weights_beside_a_large_one(dtype, act, below):
+    """One token takes nearly all the weight and has zero values, as a first token often does; the others, each
+    w = 2^(-1.03 below) of it, make the output: out = n w / (1 + n w) where their values are one.
+
+    Each weight is rounded once to the matrix instruction's type, the output once."""
+    tokens, dim, seqs = 8192, 64, 512  # more sequences than CTAs: whole sequences to a CTA
+    page = 64
+    k = torch.zeros(tokens // page, page, 1, dim)
+    v = torch.ones_like(k)
+    k[0, 0, 0, 0], v[0, 0] = float(below), 0.0
+    table = torch.arange(tokens // page, dtype=torch.int32).repeat(seqs, 1).cuda()  # all read the same pages
+    handle = w4.PagedKVCache(k.to(dtype).cuda(), v.to(dtype).cuda(), table)
+    q = torch.zeros(seqs, 2, dim)
+    q[..., 0] = 1.0
+    n = torch.full((seqs,), tokens, dtype=torch.int32, device="cuda")
+    out = torch.empty(seqs, 2, dim, dtype=act, device="cuda")
+    w4.w4a4_paged_attention(q.to(act).cuda(), handle, n, out, scale=1.03 * math.log(2.0))
+    torch.cuda.synchronize()
+    mass = (tokens - 1) * 2.0 ** (-1.03 * below)
+    ref = torch.full(out.shape, mass / (1 + mass), dtype=F64)
+    p_type = BF16 if dtype == BF16 else F16
+    err = ref * (u(p_type) + 64 * SLACK)
+    check(out, ref, err + u(act) * (ref + err) + tiny(act), f"{dtype} 2^-{below}")

@@ -214,6 +214,8 @@ __device__ __forceinline__ float row_shift(float top) {
 template <int D, int CT, int NT>
 __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_attention_kernel(const Args A) {
     using P = Plan<D, CT, NT>;
+    // bf16 probabilities have fp32's range: no lift, and the maximum may be further behind
+    constexpr float kLift = CT == kBF16 ? 0.f : 13.f, kSlack = CT == kBF16 ? 8.f : 2.f;
     constexpr int kChunk = P::kChunk, kTokens = P::kTokens, kSubs = kTokens / 16, kSteps = D / 16;
     extern __shared__ __align__(128) uint8_t smem[];
     float* warp_max = reinterpret_cast<float*>(smem + P::kRing);  // [kWarps][kChunk]
@@ -563,16 +565,19 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
                 }
             }
             // Scores in units of log2, tokens that do not take part at -inf.  The subtracted
-            // maximum is only renewed when a score exceeds it by more than 8: up to there a
-            // probability (at most 2^8) is as exact in its type, and the reduction over the
-            // warp and the rescaling of the output are left out of most steps.
+            // maximum is only renewed when a score exceeds it by more than kSlack, so that the
+            // reduction over the warp and the rescaling of the output are left out of most
+            // steps.  What is subtracted (`top`) lies kLift below the maximum: an fp16
+            // probability then goes up to 2^(kLift + kSlack) = 2^15, and is a normal number down
+            // to 2^-27 of the largest instead of 2^-14.  (Unlifted, tokens at 2^-25 were lost,
+            // and thousands of them beside one heavy token can make the output.)
             constexpr uint32_t kFull = kTokens == 32 ? 0xffffffffu : 0xffffu;
             bool over = false;
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float limit = top[t][j & 1] + 8.f;
+                    const float limit = top[t][j & 1] + (kLift + kSlack);
 #pragma unroll
                     for (int u = 0; u < kSubs; ++u) {
                         s[u][t][j] *= factor[t][j & 1];
@@ -585,11 +590,12 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        float m = top[t][j];
+                        float m = -INFINITY;
 #pragma unroll
                         for (int u = 0; u < kSubs; ++u) m = fmaxf(m, fmaxf(s[u][t][j], s[u][t][j + 2]));
 #pragma unroll
                         for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                        m = fmaxf(top[t][j], m - kLift);
                         const float fade = exp2_approx(top[t][j] - ref_of(m));
                         top[t][j] = m;
                         sum[t][j] *= fade;

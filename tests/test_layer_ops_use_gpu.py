@@ -92,3 +92,18 @@ def test_attention_many_small_weights_beside_a_large_one(dtype, act, below):
     p_type = BF16 if dtype == BF16 else F16
     err = ref * (u(p_type) + 64 * SLACK)
     check(out, ref, err + u(act) * (ref + err) + tiny(act), f"{dtype} 2^-{below}")
+
+
+def test_attention_infinite_bf16_query_beside_large_elements():
+    """An infinite element of a bf16 query against an 8-bit cache: the score is an infinity of its sign, also with
+    other elements outside fp16's range."""
+    lengths = [50]
+    c = Cache(lengths, 16, 1, 64, E4M3, seed=67, scales=False)
+    k = c.k.float()
+    k[..., 0], k[..., 1] = -1.0, 1.0
+    c.k = k.to(E4M3)
+    c.to_gpu()
+    q = torch.ones(1, 2, 64)
+    q[..., 0], q[..., 1] = math.inf, 1e6
+    out, lse = attend(c, q.to(BF16), lengths)
+    assert torch.all(out == 0) and torch.all(lse == -math.inf)

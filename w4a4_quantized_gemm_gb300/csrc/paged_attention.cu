@@ -204,10 +204,11 @@ struct Cursor {
 // Scale of a row of queries for the fp16 MMA of E4M3 caches: bf16 queries can lie
 // outside fp16's range, so a row is multiplied by the power of two that brings its
 // largest element into [2^13, 2^14) (exact for elements down to 2^-28 of it) and the
-// scores by its inverse.
+// scores by its inverse.  Beside an infinite element every finite one has to stay finite,
+// and no more: its scores are infinities or NaN.
 __device__ __forceinline__ float row_shift(float top) {
-    if (!(top > 0.f) || isinf(top)) return 1.f;
-    const int e = max(ilogbf(top), -100);
+    if (!(top > 0.f)) return 1.f;
+    const int e = isinf(top) ? 127 : max(ilogbf(top), -100);
     return exp2f(float(13 - e));
 }
 

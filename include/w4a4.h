@@ -356,8 +356,8 @@ typedef struct {
  *           (a, b) = (i, i + rot_dim / 2), or (2 i, 2 i + 1) if interleaved
  *   q_out[t] = y (may be q itself with the same strides); the cache's row
  *   (s, p) of the head = y for keys and the unrotated v for values.
- * Arithmetic in fp32, one rounding to the stored type (E4M3: of y times the
- * reciprocal of the head's scale, to nearest even, saturating at 448; NaN stays NaN).
+ * Arithmetic in fp32, one rounding to the stored type (E4M3: of y divided by the
+ * head's scale, to nearest even, saturating at 448; NaN stays NaN).
  * rope: fp32 [rope_rows][2][rot_dim / 2] (cosines, then sines), NULL: no
  * rotation; w4a4_rope_table fills one.  rot_dim % 16 == 0, <= head_dim.
  * dtype W4A4_F16 or W4A4_BF16 (q, k, v, q_out, gains); the cache has the same

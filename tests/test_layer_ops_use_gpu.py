@@ -107,3 +107,44 @@ def test_attention_infinite_bf16_query_beside_large_elements():
     q[..., 0], q[..., 1] = math.inf, 1e6
     out, lse = attend(c, q.to(BF16), lengths)
     assert torch.all(out == 0) and torch.all(lse == -math.inf)
+
+
+def test_append_to_an_8_bit_cache_divides_by_the_scale():
+    """The stored code is that of the quotient y / scale: ties go to even, and the smallest scales keep zeros."""
+    hkv = 6
+    c = Cache([64], 16, hkv, 64, E4M3, seed=68, fill=False)
+    scale = torch.tensor([3 / 64, 5 / 64, 7 / 64, 49 / 1024, 0.7, 2.0 ** -130])
+    c.ks, c.vs = scale, scale.flip(0).contiguous()
+    c.to_gpu()
+    ties = torch.tensor([m + 0.5 for m in range(8, 16)])  # halfway between neighbours of E4M3
+    x = torch.empty(64, hkv, 64)
+    for h in range(hkv):
+        e = torch.arange(64) % 4
+        x[:, h] = torch.where(torch.rand(64, 64, generator=gen(h)) < 0.5, 1.0, -1.0) * ties[torch.arange(64) % 8] * 2.0 ** -e * (
+            scale[h] if h < 5 else 1.0)
+    x[::3, 5] = 0.0
+    x = x.to(F16)
+    xv = x.flip(1).contiguous()
+    tok = torch.arange(64, dtype=torch.int32, device="cuda")
+    none = torch.empty(64, 0, 64, dtype=F16, device="cuda")
+    w4.w4a4_kv_append(none, x.cuda(), xv.cuda(), tok, c.handle, none, seqs=torch.zeros_like(tok))
+    torch.cuda.synchronize()
+    at = c.table[0, torch.arange(64) // 16].long(), torch.arange(64) % 16
+    for pool, y, s in ((c.gk, x, c.ks), (c.gv, xv, c.vs)):
+        want = (y.float() / s[:, None]).clamp(-448, 448).to(E4M3).float()
+        assert torch.equal(pool.float().cpu()[at], want)
+
+    # bf16 rows over fp32's range, and scales at its ends, zero among them
+    scale = torch.tensor([2.0 ** 120, 3e-30, 1.1, 0.0, 1.7e38, 2.0 ** -149])
+    c.ks.copy_(scale), c.vs.copy_(scale.flip(0))
+    c.to_gpu()
+    x = randn(gen(9), 64, hkv, 64) * 10.0 ** (60 * torch.rand(64, hkv, 64, generator=gen(10)) - 30)
+    x[0], x[1], x[2], x[3] = 0.0, math.inf, -math.inf, float("nan")
+    x[4:, 2] = 300 * randn(gen(11), 60, 64)
+    x = x.to(BF16)
+    w4.w4a4_kv_append(none.to(BF16), x.cuda(), x.cuda(), tok, c.handle, none.to(BF16), seqs=torch.zeros_like(tok))
+    torch.cuda.synchronize()
+    for pool, s in ((c.gk, c.ks), (c.gv, c.vs)):
+        want = (x.float() / s[:, None]).clamp(-448, 448).to(E4M3).float()
+        assert torch.equal(pool.float().cpu()[at].nan_to_num(nan=1e9), want.nan_to_num(nan=1e9))
+    assert w4.w4a4_device_status() == 0

@@ -148,3 +148,40 @@ def test_append_to_an_8_bit_cache_divides_by_the_scale():
         want = (x.float() / s[:, None]).clamp(-448, 448).to(E4M3).float()
         assert torch.equal(pool.float().cpu()[at].nan_to_num(nan=1e9), want.nan_to_num(nan=1e9))
     assert w4.w4a4_device_status() == 0
+
+
+def test_operators_called_first_in_a_fresh_thread():
+    """A thread whose first CUDA work is one of the operators, on tensors that another thread made."""
+    c = Cache([40], 16, 2, 64, F16, seed=62)
+    c.handle.workspace(4)
+    qkv = randn(gen(63), 1, 8, 64).to(F16).cuda()
+    pos, n = torch.tensor([39], dtype=torch.int32, device="cuda"), torch.tensor([40], dtype=torch.int32, device="cuda")
+    y = randn(gen(64), 3, 64).to(F16).cuda()
+
+    def run(op):
+        q, out = torch.zeros(1, 4, 64, dtype=F16, device="cuda"), torch.zeros(1, 4, 64, dtype=F16, device="cuda")
+        x, r = torch.zeros_like(y), torch.zeros_like(y)
+        torch.cuda.synchronize()
+        calls = {"append": lambda: w4.w4a4_kv_append(qkv[:, :4], qkv[:, 4:6], qkv[:, 6:], pos, c.handle, q),
+                 "attend": lambda: w4.w4a4_paged_attention(qkv[:, :4], c.handle, n, out),
+                 "norm": lambda: w4.w4a4_block_norm(y, y, x, r)}
+        return calls[op], (q, out, x, r)
+
+    for op in ("append", "attend", "norm"):
+        call, want = run(op)
+        call()  # handles, attributes and sizes are known from here on
+        call, got = run(op)
+        raised = []
+
+        def body():
+            try:
+                call()
+            except BaseException as e:
+                raised.append(e)
+
+        t = threading.Thread(target=body)
+        t.start()
+        t.join()
+        torch.cuda.synchronize()
+        assert not raised, (op, raised)
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), op

@@ -54,7 +54,14 @@ w4a4_status launch(dim3 grid, unsigned threads, unsigned smem, cudaStream_t stre
     cfg.attrs = &attr;
     cfg.numAttrs = add_pdl_attr(pdl, 0);
     void* params[] = {const_cast<void*>(static_cast<const void*>(&args))...};
-    return go(&cfg, fn, params, nullptr) == CUDA_SUCCESS ? W4A4_OK : W4A4_ERR_CUDA;
+    CUresult done = go(&cfg, fn, params, nullptr);
+    if (done == CUDA_ERROR_INVALID_CONTEXT) {
+        // The driver's entry point needs a context on the calling thread, and none of the cached
+        // look-ups above has bound one: a thread whose first CUDA call this is.
+        if (cudaSetDevice(dev) != cudaSuccess) return launch_status();
+        done = go(&cfg, fn, params, nullptr);
+    }
+    return done == CUDA_SUCCESS ? W4A4_OK : W4A4_ERR_CUDA;
 }
 
 }  // namespace w4a4

@@ -2,6 +2,7 @@
 streams, devices, strides that no index uses; and values at the borders of their types.
 
 References and tolerances as in test_layer_ops_gpu."""
+import ctypes
 import math
 import threading
 
@@ -185,3 +186,35 @@ def test_operators_called_first_in_a_fresh_thread():
         torch.cuda.synchronize()
         assert not raised, (op, raised)
         assert all(torch.equal(a, b) for a, b in zip(got, want)), op
+
+
+def on_device(t, index):
+    """`t`'s memory as a tensor that says it is on GPU `index`."""
+    class Tensor(ctypes.Structure):
+        _fields_ = [("data", ctypes.c_void_p), ("device_type", ctypes.c_int32), ("device_id", ctypes.c_int32),
+                    ("ndim", ctypes.c_int32), ("code", ctypes.c_uint8), ("bits", ctypes.c_uint8), ("lanes", ctypes.c_uint16),
+                    ("shape", ctypes.POINTER(ctypes.c_int64)), ("strides", ctypes.POINTER(ctypes.c_int64)),
+                    ("byte_offset", ctypes.c_uint64)]
+
+    class Managed(ctypes.Structure):
+        _fields_ = [("t", Tensor), ("ctx", ctypes.c_void_p), ("deleter", ctypes.c_void_p)]
+
+    shape, strides = (ctypes.c_int64 * t.dim())(*t.shape), (ctypes.c_int64 * t.dim())(*t.stride())
+    code = 2 if t.is_floating_point() else 0
+    m = Managed(Tensor(t.data_ptr(), 2, index, t.dim(), code, 8 * t.element_size(), 1, shape, strides, 0), None, None)
+    on_device.kept = getattr(on_device, "kept", []) + [(m, shape, strides, t)]
+    new = ctypes.pythonapi.PyCapsule_New
+    new.restype, new.argtypes = ctypes.py_object, [ctypes.c_void_p, ctypes.c_char_p, ctypes.c_void_p]
+    return torch.utils.dlpack.from_dlpack(new(ctypes.addressof(m), b"dltensor", None))
+
+
+def test_operators_do_not_run_on_another_device_than_their_tensors():
+    """Tensors that name another GPU than the current one, and a stream's handle, which says nothing of a device."""
+    there = torch.cuda.device_count()  # a GPU that the machine does not have; the memory is the current one's
+    y = torch.zeros(4, 64, dtype=F16, device="cuda")
+    x, r = torch.zeros_like(y), torch.zeros_like(y)
+    a = [on_device(t, there) for t in (y, y, x, r)]
+    assert all(t.get_device() == there for t in a)
+    with pytest.raises(w4.W4A4Error):
+        w4.w4a4_block_norm(*a, stream=0)
+    assert torch.cuda.current_device() == 0

@@ -5,13 +5,15 @@
 // launch (5 us beside 2 us on the Grace host), which a decode step's short kernels
 // cannot hide; here it is 0.1 us.
 //
-// Arguments go by position or name, None stands for NULL; a call that is refused
-// raises the package's W4A4Error (W4A4_ERR_INVALID_ARG for a tensor that does not fit).
+// Arguments go by position or name, None stands for NULL; a call runs on its tensors'
+// device, whichever is current.  One that is refused raises the package's W4A4Error
+// (W4A4_ERR_INVALID_ARG for a tensor that does not fit).
 #include <Python.h>
 
 #include <cmath>
 
 #include <ATen/core/Tensor.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -86,6 +88,14 @@ bool stream_of(PyObject* o, int dev, cudaStream_t& s) {
     return !PyErr_Occurred();
 }
 
+// Makes `dev` the current device, on which the C ABI works, for the length of a call.
+struct OnDevice {
+    c10::cuda::OptionalCUDAGuard guard;
+    explicit OnDevice(int dev) {
+        if (c10::cuda::current_device() != dev) guard.set_device(c10::Device(c10::kCUDA, c10::DeviceIndex(dev)));
+    }
+};
+
 // Interned names, filled in when the module is loaded.
 PyObject *n_struct, *n_device, *n_ws, *n_workspace, *n_refuse;
 
@@ -159,6 +169,7 @@ w4a4_status kv_append(PyObject* const* a) {
     x.interleaved = PyObject_IsTrue(a[11]);
     cudaStream_t stream;
     if (!stream_of(a[12], dev, stream) || PyErr_Occurred()) return W4A4_ERR_INVALID_ARG;
+    const OnDevice on(dev);
     return w4a4_kv_append(c, &x, stream);
 }
 
@@ -187,6 +198,7 @@ w4a4_status paged_attention(PyObject* const* a) {
     x.q_heads = int32_t(heads);
     cudaStream_t stream;
     if (window < 0 || !stream_of(a[8], dev, stream) || PyErr_Occurred()) return W4A4_ERR_INVALID_ARG;
+    const OnDevice on(dev);
     PyObject* kept = a[7] == Py_None ? workspace_of(a[1], heads) : Py_NewRef(a[7]);
     if (!kept) return W4A4_ERR_INVALID_ARG;  // its own error is set
     const at::Tensor* ws = tensor(kept, dev);
@@ -237,6 +249,7 @@ w4a4_status block_norm(PyObject* const* a) {
     x.post = int32_t(PyLong_AsLong(a[7])), x.pre = int32_t(PyLong_AsLong(a[10]));
     cudaStream_t stream;
     if (!stream_of(a[14], dev, stream) || PyErr_Occurred()) return W4A4_ERR_INVALID_ARG;
+    const OnDevice on(dev);
     return w4a4_block_norm(&x, stream);
 }
 

@@ -327,7 +327,9 @@ typedef enum { W4A4_F16 = 0, W4A4_BF16 = 1, W4A4_F32 = 2, W4A4_E4M3 = 3 } w4a4_d
  *              code * k_scale[head] (v_scale[head]); NULL scales mean 1
  *   head_dim   64, 96, 128 or 256
  *   max_pages * page_size <= 2^30 tokens of a sequence
- *   strides    non-negative, of whole 16 bytes; the pools 16-byte aligned
+ *   strides    non-negative, of whole 16 bytes; the pools 16-byte aligned.  Rows that a
+ *              call writes do not overlap (a stride below head_dim is refused); rows
+ *              that it only reads may be shared (a stride of 0)
  * `bytes` is sizeof(w4a4_kv_cache), and so in the argument structs below; a
  * call with another value returns W4A4_ERR_INVALID_ARG.  The structs live on the
  * host and are read during the call only. */
@@ -428,8 +430,8 @@ w4a4_status w4a4_paged_attention(const w4a4_kv_cache* cache, const w4a4_paged_at
 
 /* The residual stream between two blocks in one pass.  Row m < rows, width W:
  *   r'[m] = r[m] + scale * gate[m] (.) post(y[m]),   x[m] = pre(r'[m])
- * y: the block's output; r, r': the residual stream (r_out may be r itself); x:
- * the next block's input.  post, pre: W4A4_NORM_NONE (identity),
+ * y: the block's output; r, r': the residual stream (r_out may be r itself, with
+ * the same stride); x: the next block's input.  post, pre: W4A4_NORM_NONE (identity),
  *   W4A4_NORM_RMS    z / sqrt(mean z^2 + eps) * gain
  *   W4A4_NORM_LAYER  (z - mean z) / sqrt(mean (z - mean z)^2 + eps) * gain + bias
  * with gain, bias [width] (NULL: 1 and 0).  gate: row m / rows_per_gate

@@ -7,6 +7,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <mutex>
+#include <utility>
 
 #include "kernels.h"
 
@@ -89,6 +90,9 @@ bool is_act(int dtype) { return dtype == W4A4_F16 || dtype == W4A4_BF16; }
 bool good_stride(int64_t stride, int size) {
     return stride >= 0 && stride <= (int64_t(1) << 29) && stride * size % 16 == 0;
 }
+
+// Rows of `dim` elements that n indices reach at this stride, to be written: no two may overlap.
+bool apart(int64_t stride, int64_t n, int dim) { return n <= 1 || stride >= dim; }
 
 // Everything a call can check of a cache without reading device memory.
 w4a4_status check_cache(const w4a4_kv_cache* c) {
@@ -548,6 +552,13 @@ w4a4_status w4a4_kv_append(const w4a4_kv_cache* cache, const w4a4_kv_append_args
     for (const int64_t s : {a->q_token_stride, a->q_head_stride, a->k_token_stride, a->k_head_stride,
                             a->v_token_stride, a->v_head_stride, a->out_token_stride, a->out_head_stride})
         if (!good_stride(s, 2)) return W4A4_ERR_MISALIGNED;
+    if (!apart(a->out_token_stride, a->q_heads > 0 ? a->tokens : 0, cache->head_dim) ||
+        !apart(a->out_head_stride, a->q_heads, cache->head_dim))
+        return W4A4_ERR_INVALID_ARG;
+    for (const auto& [stride, n] : {std::pair{cache->k_page_stride, cache->pages}, {cache->v_page_stride, cache->pages},
+                                    {cache->k_token_stride, cache->page_size}, {cache->v_token_stride, cache->page_size},
+                                    {cache->k_head_stride, cache->kv_heads}, {cache->v_head_stride, cache->kv_heads}})
+        if (!apart(stride, n, cache->head_dim)) return W4A4_ERR_INVALID_ARG;
     if (a->q_heads > 0 && a->q == a->q_out &&
         (a->q_token_stride != a->out_token_stride || a->q_head_stride != a->out_head_stride))
         return W4A4_ERR_INVALID_ARG;
@@ -589,6 +600,8 @@ w4a4_status w4a4_paged_attention(const w4a4_kv_cache* cache, const w4a4_paged_at
         return W4A4_ERR_MISALIGNED;
     for (const int64_t s : {a->q_token_stride, a->q_head_stride, a->out_token_stride, a->out_head_stride})
         if (!good_stride(s, 2)) return W4A4_ERR_MISALIGNED;
+    if (!apart(a->out_token_stride, cache->seqs, cache->head_dim) || !apart(a->out_head_stride, a->q_heads, cache->head_dim))
+        return W4A4_ERR_INVALID_ARG;
     if (a->workspace_bytes < attention_workspace_bytes(cache->seqs, a->q_heads, cache->kv_heads))
         return W4A4_ERR_WORKSPACE;
     if ((st = check_device()) != W4A4_OK) return st;
@@ -613,6 +626,7 @@ w4a4_status w4a4_block_norm(const w4a4_block_norm_args* a, cudaStream_t stream) 
     if (a->y_stride < a->width || a->r_stride < a->width || a->r_out_stride < a->width ||
         (a->x && a->x_stride < a->width) || (a->gate && a->rows_per_gate > 0 && a->gate_stride < a->width))
         return W4A4_ERR_INVALID_ARG;
+    if (a->r == a->r_out && a->r_stride != a->r_out_stride) return W4A4_ERR_INVALID_ARG;
     w4a4_status st = check_device();
     if (st != W4A4_OK) return st;
     return launch_block_norm(*a, stream);

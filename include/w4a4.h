@@ -329,7 +329,8 @@ typedef enum { W4A4_F16 = 0, W4A4_BF16 = 1, W4A4_F32 = 2, W4A4_E4M3 = 3 } w4a4_d
  *   max_pages * page_size <= 2^30 tokens of a sequence
  *   strides    non-negative, of whole 16 bytes; the pools 16-byte aligned.  Rows that a
  *              call writes do not overlap (a stride below head_dim is refused); rows
- *              that it only reads may be shared (a stride of 0)
+ *              that it only reads may be shared (a stride of 0).  A stride that no index
+ *              uses (one page, token, head or row) is not looked at, here and below
  * `bytes` is sizeof(w4a4_kv_cache), and so in the argument structs below; a
  * call with another value returns W4A4_ERR_INVALID_ARG.  The structs live on the
  * host and are read during the call only. */

@@ -34,3 +34,38 @@ def test_inputs_may_share_rows(L):
     assert L.w4a4_kv_append(cache(), append(q_heads=1, out_head_stride=0), None) == GOOD
     assert L.w4a4_kv_append(cache(), append(q_heads=0, q=0, q_out=0, out_token_stride=0), None) == GOOD
     assert L.w4a4_block_norm(norm(r_out=A + 4096, r_out_stride=2048), None) == GOOD
+
+
+ODD = (0, 3, -5, 1 << 40)
+
+
+@no_gpu
+@pytest.mark.parametrize("odd", ODD)
+def test_strides_that_no_index_uses_are_not_looked_at(L, odd):
+    one = dict(tokens=1, q_token_stride=odd, k_token_stride=odd, v_token_stride=odd, out_token_stride=odd)
+    assert L.w4a4_kv_append(cache(), append(**one), None) == GOOD
+    assert L.w4a4_kv_append(cache(), append(**{**one, "q_out": A}), None) == GOOD  # in place: no stride differs
+    assert L.w4a4_kv_append(cache(), append(q_heads=1, q_head_stride=odd, out_head_stride=odd), None) == GOOD
+    single = dict(kv_heads=1, k_head_stride=odd, v_head_stride=odd)
+    assert L.w4a4_kv_append(cache(**single), append(k_head_stride=odd, v_head_stride=odd), None) == GOOD
+    assert L.w4a4_paged_attention(cache(**single), attention(), None) == GOOD
+    for over in (dict(pages=1, k_page_stride=odd, v_page_stride=odd), dict(page_size=1, k_token_stride=odd, v_token_stride=odd),
+                 dict(seqs=1, table_stride=odd)):
+        assert L.w4a4_kv_append(cache(**over), append(), None) == GOOD
+        assert L.w4a4_paged_attention(cache(**over), attention(), None) == GOOD
+    row = dict(q_token_stride=odd, out_token_stride=odd)
+    assert L.w4a4_paged_attention(cache(seqs=1), attention(**row), None) == GOOD
+    assert L.w4a4_paged_attention(cache(**single), attention(q_heads=1, q_head_stride=odd, out_head_stride=odd), None) == GOOD
+    row = dict(rows=1, y_stride=odd, r_stride=odd, r_out_stride=odd, x_stride=odd)
+    assert L.w4a4_block_norm(norm(**row), None) == GOOD
+    assert L.w4a4_block_norm(norm(gate=A, gate_stride=odd), None) == GOOD
+    assert L.w4a4_block_norm(norm(gate=A, gate_stride=odd, rows_per_gate=4), None) == GOOD
+
+
+@pytest.mark.parametrize("odd", ODD)
+def test_strides_that_an_index_uses_are(L, odd):
+    assert L.w4a4_kv_append(cache(), append(tokens=2, out_token_stride=odd), None) in (1, 3)
+    assert L.w4a4_paged_attention(cache(seqs=2), attention(out_token_stride=odd), None) in (1, 3)
+    assert L.w4a4_paged_attention(cache(seqs=2, table_stride=odd), attention(), None) == 1
+    assert L.w4a4_block_norm(norm(rows=2, y_stride=odd), None) in (1, 3)
+    assert L.w4a4_block_norm(norm(gate=A, gate_stride=odd, rows_per_gate=3), None) in (1, 3)

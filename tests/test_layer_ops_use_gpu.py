@@ -218,3 +218,37 @@ def test_operators_do_not_run_on_another_device_than_their_tensors():
     with pytest.raises(w4.W4A4Error):
         w4.w4a4_block_norm(*a, stream=0)
     assert torch.cuda.current_device() == 0
+
+
+def test_strides_that_no_index_uses():
+    """One row, token or head: its stride is whatever torch left there."""
+    g = gen(70)
+    wide = randn(g, 4, 67).to(F16).cuda()
+    y, r = wide[:1, :64], torch.randn(64, 1, generator=g).cuda().t()  # strides 67 and 1
+    x, ro = torch.empty(1, 64, dtype=F16, device="cuda"), torch.empty(1, 64, device="cuda")
+    want_x, want_r = torch.empty_like(x), torch.empty_like(ro)
+    w4.w4a4_block_norm(y, r, x, ro, gate=wide[:1, :64], rows_per_gate=5)
+    w4.w4a4_block_norm(y.clone(), r.clone(memory_format=torch.contiguous_format), want_x, want_r, gate=y.clone())
+    assert torch.equal(x, want_x) and torch.equal(ro, want_r)
+
+    c = Cache([40], 16, 2, 64, F16, seed=71)
+    rows = randn(g, 2, 8 * 64 + 1).to(F16).cuda()
+    q = rows[:1, :256].unflatten(1, (4, 64))  # a token stride of 513
+    n, pos = torch.tensor([40], dtype=torch.int32, device="cuda"), torch.tensor([39], dtype=torch.int32, device="cuda")
+    out = torch.empty(2, 4 * 64 + 3, dtype=F16, device="cuda")[:1, :256].unflatten(1, (4, 64))
+    w4.w4a4_paged_attention(q, c.handle, n, out)
+    check(out, attention_ref(q.cpu(), c, [40], 0.125, 0)[0], attention_ref(q.cpu(), c, [40], 0.125, 0)[2], "one sequence")
+    k, v = rows[:1, 256:384].unflatten(1, (2, 64)), rows[:1, 384:512].unflatten(1, (2, 64))
+    w4.w4a4_kv_append(q, k, v, pos, c.handle, out)
+    assert torch.equal(out, q) and torch.equal(c.gk[c.table[0, 2], 7], k[0]) and torch.equal(c.gv[c.table[0, 2], 7], v[0])
+
+    one = torch.randn(3, 16, 65, generator=g).to(F16).cuda()[:1, :, :64].unsqueeze(2)  # one page of one head, odd strides
+    pool = one.as_strided((1, 16, 1, 64), (1041, 64, 3, 1))
+    table = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    n = torch.tensor([16], dtype=torch.int32, device="cuda")
+    got, want = torch.empty(1, 1, 64, dtype=F16, device="cuda"), torch.empty(1, 1, 64, dtype=F16, device="cuda")
+    w4.w4a4_paged_attention(q[:, :1], w4.PagedKVCache(pool, pool, table), n, got)
+    w4.w4a4_paged_attention(q[:, :1].clone(), w4.PagedKVCache(pool.clone(memory_format=torch.contiguous_format),
+                                                              pool.clone(memory_format=torch.contiguous_format), table), n, want)
+    assert torch.equal(got, want)
+    assert w4.w4a4_device_status() == 0

@@ -91,12 +91,21 @@ bool good_stride(int64_t stride, int size) {
     return stride >= 0 && stride <= (int64_t(1) << 29) && stride * size % 16 == 0;
 }
 
+// A stride that no index uses says nothing: torch leaves any number there for a dimension of one.
+void used(int64_t& stride, int64_t n) { stride = n > 1 ? stride : 0; }
+
 // Rows of `dim` elements that n indices reach at this stride, to be written: no two may overlap.
 bool apart(int64_t stride, int64_t n, int dim) { return n <= 1 || stride >= dim; }
 
-// Everything a call can check of a cache without reading device memory.
-w4a4_status check_cache(const w4a4_kv_cache* c) {
-    if (!c || c->bytes != sizeof(*c)) return W4A4_ERR_INVALID_ARG;
+// Everything a call can check of a cache without reading device memory; `given` as the
+// kernels take it.
+w4a4_status check_cache(const w4a4_kv_cache* given, w4a4_kv_cache* c) {
+    if (!given || given->bytes != sizeof(*given)) return W4A4_ERR_INVALID_ARG;
+    *c = *given;
+    used(c->k_page_stride, c->pages), used(c->v_page_stride, c->pages);
+    used(c->k_token_stride, c->page_size), used(c->v_token_stride, c->page_size);
+    used(c->k_head_stride, c->kv_heads), used(c->v_head_stride, c->kv_heads);
+    if (c->seqs <= 1) c->table_stride = c->max_pages;
     if (c->seqs < 0 || c->max_pages < 0 || c->pages < 0 || c->page_size < 1 || c->kv_heads < 1)
         return W4A4_ERR_INVALID_ARG;
     if (!is_act(c->dtype) && c->dtype != W4A4_E4M3) return W4A4_ERR_INVALID_ARG;
@@ -535,10 +544,18 @@ w4a4_status w4a4_rmsnorm_f16(const uint16_t* Y, int M, int ld_y, int K, uint16_t
     return launch_status();
 }
 
-w4a4_status w4a4_kv_append(const w4a4_kv_cache* cache, const w4a4_kv_append_args* a, cudaStream_t stream) {
-    w4a4_status st = check_cache(cache);
+w4a4_status w4a4_kv_append(const w4a4_kv_cache* cache, const w4a4_kv_append_args* args, cudaStream_t stream) {
+    w4a4_kv_cache view;
+    w4a4_status st = check_cache(cache, &view);
     if (st != W4A4_OK) return st;
-    if (!a || a->bytes != sizeof(*a) || a->tokens < 0 || a->q_heads < 0 || !is_act(a->dtype)) return W4A4_ERR_INVALID_ARG;
+    if (!args || args->bytes != sizeof(*args)) return W4A4_ERR_INVALID_ARG;
+    cache = &view;
+    w4a4_kv_append_args x = *args;
+    const w4a4_kv_append_args* a = &x;
+    for (int64_t* s : {&x.q_token_stride, &x.k_token_stride, &x.v_token_stride, &x.out_token_stride}) used(*s, x.tokens);
+    used(x.q_head_stride, x.q_heads), used(x.out_head_stride, x.q_heads);
+    used(x.k_head_stride, cache->kv_heads), used(x.v_head_stride, cache->kv_heads);
+    if (a->tokens < 0 || a->q_heads < 0 || !is_act(a->dtype)) return W4A4_ERR_INVALID_ARG;
     if (cache->dtype != a->dtype && cache->dtype != W4A4_E4M3) return W4A4_ERR_INVALID_ARG;
     if (a->q_heads > 65536 || cache->kv_heads > 65536) return W4A4_ERR_UNSUPPORTED_SHAPE;
     if (a->rope && (a->rope_rows < 1 || a->rot_dim < 16)) return W4A4_ERR_INVALID_ARG;
@@ -584,11 +601,18 @@ size_t w4a4_paged_attention_workspace_bytes(int seqs, int q_heads, int kv_heads,
     return attention_workspace_bytes(seqs, q_heads, kv_heads);
 }
 
-w4a4_status w4a4_paged_attention(const w4a4_kv_cache* cache, const w4a4_paged_attention_args* a,
+w4a4_status w4a4_paged_attention(const w4a4_kv_cache* cache, const w4a4_paged_attention_args* args,
                                  cudaStream_t stream) {
-    w4a4_status st = check_cache(cache);
+    w4a4_kv_cache view;
+    w4a4_status st = check_cache(cache, &view);
     if (st != W4A4_OK) return st;
-    if (!a || a->bytes != sizeof(*a) || a->window < 0 || !is_act(a->dtype)) return W4A4_ERR_INVALID_ARG;
+    if (!args || args->bytes != sizeof(*args)) return W4A4_ERR_INVALID_ARG;
+    cache = &view;
+    w4a4_paged_attention_args x = *args;
+    const w4a4_paged_attention_args* a = &x;
+    used(x.q_token_stride, cache->seqs), used(x.out_token_stride, cache->seqs);
+    used(x.q_head_stride, x.q_heads), used(x.out_head_stride, x.q_heads);
+    if (a->window < 0 || !is_act(a->dtype)) return W4A4_ERR_INVALID_ARG;
     if (cache->dtype != a->dtype && cache->dtype != W4A4_E4M3) return W4A4_ERR_INVALID_ARG;
     if (a->q_heads < 1) return W4A4_ERR_INVALID_ARG;
     if (a->q_heads % cache->kv_heads != 0 || a->q_heads > 65536) return W4A4_ERR_UNSUPPORTED_SHAPE;
@@ -608,8 +632,14 @@ w4a4_status w4a4_paged_attention(const w4a4_kv_cache* cache, const w4a4_paged_at
     return launch_paged_attention(*cache, *a, stream);
 }
 
-w4a4_status w4a4_block_norm(const w4a4_block_norm_args* a, cudaStream_t stream) {
-    if (!a || a->bytes != sizeof(*a) || a->rows < 0 || a->rows_per_gate < 0) return W4A4_ERR_INVALID_ARG;
+w4a4_status w4a4_block_norm(const w4a4_block_norm_args* args, cudaStream_t stream) {
+    if (!args || args->bytes != sizeof(*args)) return W4A4_ERR_INVALID_ARG;
+    w4a4_block_norm_args z = *args;
+    const w4a4_block_norm_args* a = &z;
+    for (int64_t* s : {&z.y_stride, &z.r_stride, &z.r_out_stride, &z.x_stride})
+        if (z.rows == 1) *s = z.width;
+    if (z.rows_per_gate == 0 || z.rows <= z.rows_per_gate) z.gate_stride = z.width;  // one row of the gate
+    if (a->rows < 0 || a->rows_per_gate < 0) return W4A4_ERR_INVALID_ARG;
     if (!is_act(a->dtype) || (a->res_dtype != a->dtype && a->res_dtype != W4A4_F32)) return W4A4_ERR_INVALID_ARG;
     for (const int kind : {a->post, a->pre})
         if (kind < W4A4_NORM_NONE || kind > W4A4_NORM_LAYER) return W4A4_ERR_INVALID_ARG;

@@ -252,3 +252,30 @@ def test_strides_that_no_index_uses():
                                                               pool.clone(memory_format=torch.contiguous_format), table), n, want)
     assert torch.equal(got, want)
     assert w4.w4a4_device_status() == 0
+
+
+def test_attention_workspace_outlives_the_cache_object():
+    """A cache object dropped while a side stream still runs its attention: the memory of its workspace is not
+    handed out before that has ended."""
+    c = Cache([700], 16, 2, 64, F16, seed=60)
+    q = randn(gen(61), 1, 4, 64).to(F16).cuda()
+    n, out = torch.full((1,), 700, dtype=torch.int32, device="cuda"), torch.empty_like(q)
+    side = torch.cuda.Stream()
+    for given in (False, True):  # the side stream as the current one, and as an argument
+        handle = w4.PagedKVCache(c.gk, c.gv, c.gt)
+        ws = handle.workspace(4)
+        at, size = ws.data_ptr(), ws.numel()
+        del ws
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(200_000_000)  # a tenth of a second
+            if not given:
+                w4.w4a4_paged_attention(q, handle, n, out)
+        if given:
+            w4.w4a4_paged_attention(q, handle, n, out, stream=side)
+        del handle
+        again = torch.empty(size, dtype=torch.uint8, device="cuda")
+        busy = not side.query()
+        torch.cuda.synchronize()
+        assert busy and again.data_ptr() != at
+        del again

@@ -383,7 +383,9 @@ class PagedKVCache:
     strides (a [pages, kv_heads, page_size, head_dim] pool is passed as its transpose(1, 2)).
     page_table: int32 [seqs, max_pages].  k_scale, v_scale: fp32 [kv_heads] of 8-bit pools.
     The tensors are the caller's: their contents may change between calls, the tensors not.
-    Attention calls that may overlap on the GPU need a cache object (a workspace) each.
+    Attention calls that may overlap on the GPU need a cache object (a workspace) each.  The object
+    may be dropped while torch's streams still run its calls; a graph that captured one, or a stream
+    that is not torch's, needs it as long as it runs.
     """
 
     def __init__(self, k, v, page_table, k_scale=None, v_scale=None):
@@ -416,17 +418,17 @@ class PagedKVCache:
     def workspace(self, q_heads: int):
         """The workspace of attention with q_heads query heads: allocated and zeroed at its first use,
         which must not be inside a graph capture (its zeroing would only run with the graph)."""
-        ws = self._ws.get(q_heads)
-        if ws is None:
+        if q_heads not in self._ws:
             if torch.cuda.is_current_stream_capturing():
                 _refuse("PagedKVCache.workspace: call it before the capture", 4)
             n = lib().w4a4_paged_attention_workspace_bytes(self.seqs, q_heads, self.kv_heads, self.head_dim)
             if n == 0:
                 _refuse("w4a4_paged_attention_workspace_bytes", 2)
             ws = torch.zeros(n, dtype=torch.uint8, device=f"cuda:{self.device}")
-            torch.cuda.current_stream(self.device).synchronize()  # zeroed for calls on any stream
-            self._ws[q_heads] = ws
-        return ws
+            home = torch.cuda.current_stream(self.device)
+            home.synchronize()  # zeroed for calls on any stream
+            self._ws[q_heads] = ws, home.cuda_stream  # csrc/binding.cpp records the uses on other streams
+        return self._ws[q_heads][0]
 
 
 def w4a4_rope_table(rows: int, rot_dim: int, theta: float, out=None, stream=None):

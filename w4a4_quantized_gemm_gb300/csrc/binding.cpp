@@ -11,8 +11,10 @@
 #include <Python.h>
 
 #include <cmath>
+#include <memory>
 
 #include <ATen/core/Tensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -97,7 +99,7 @@ struct OnDevice {
 };
 
 // Interned names, filled in when the module is loaded.
-PyObject *n_struct, *n_device, *n_ws, *n_workspace, *n_refuse;
+PyObject *n_struct, *n_device, *n_ws, *n_workspace, *n_refuse, *n_stream_id;
 
 // What a PagedKVCache keeps for its calls: the C struct and its device.
 const w4a4_kv_cache* cache_of(PyObject* o, int& dev) {
@@ -114,15 +116,43 @@ const w4a4_kv_cache* cache_of(PyObject* o, int& dev) {
     return c;
 }
 
-// The cache object's workspace for `heads` query heads (a new reference).
+// The cache object's workspace for `heads` query heads and the stream that it was made on, as
+// the object keeps them: a new reference to (tensor, handle).
 PyObject* workspace_of(PyObject* cache, int64_t heads) {
     PyObject* key = PyLong_FromLongLong(heads);
     PyObject* kept = PyObject_GetAttr(cache, n_ws);
-    PyObject* ws = kept && PyDict_Check(kept) ? PyDict_GetItemWithError(kept, key) : nullptr;
-    ws = ws ? Py_NewRef(ws) : PyErr_Occurred() ? nullptr : PyObject_CallMethodOneArg(cache, n_workspace, key);
+    PyObject* pair = nullptr;
+    for (int tries = 0; tries < 2 && !pair && kept && PyDict_Check(kept); ++tries) {
+        pair = Py_XNewRef(PyDict_GetItemWithError(kept, key));
+        if (pair || PyErr_Occurred() || tries) break;
+        PyObject* made = PyObject_CallMethodOneArg(cache, n_workspace, key);
+        Py_XDECREF(made);
+        if (!made) break;
+    }
     Py_XDECREF(kept);
     Py_DECREF(key);
-    return ws;
+    if (pair && (!PyTuple_Check(pair) || PyTuple_GET_SIZE(pair) != 2)) Py_CLEAR(pair);
+    return pair;
+}
+
+// Keeps the allocator from handing `ws` out again while `s` may still use it, if the cache
+// object is dropped before then.  Only for streams that torch owns: at the memory's release
+// the allocator records an event on each, and one that the caller has made (a handle, an
+// external stream) may be gone by then.
+void keep_for(const at::Tensor& ws, PyObject* o, int dev, cudaStream_t s) {
+    if (PyLong_Check(o)) return;
+    int64_t id = 0;
+    if (o == Py_None) {
+        id = c10::cuda::getCurrentCUDAStream(c10::DeviceIndex(dev)).id();
+    } else {
+        PyObject* number = PyObject_GetAttr(o, n_stream_id);
+        if (number) id = PyLong_AsLongLong(number);
+        Py_XDECREF(number);
+        if (PyErr_Occurred()) return PyErr_Clear();  // no torch stream
+    }
+    if (id != 0 && id == int64_t(reinterpret_cast<intptr_t>(s))) return;  // an external stream's id is its handle
+    c10::cuda::CUDACachingAllocator::recordStream(
+        ws.storage().data_ptr(), c10::cuda::CUDAStream::unpack3(id, c10::DeviceIndex(dev), c10::DeviceType::CUDA));
 }
 
 // A parameter's default: required, or one of these.
@@ -199,16 +229,14 @@ w4a4_status paged_attention(PyObject* const* a) {
     cudaStream_t stream;
     if (window < 0 || !stream_of(a[8], dev, stream) || PyErr_Occurred()) return W4A4_ERR_INVALID_ARG;
     const OnDevice on(dev);
-    PyObject* kept = a[7] == Py_None ? workspace_of(a[1], heads) : Py_NewRef(a[7]);
+    const bool own = a[7] == Py_None;
+    const std::unique_ptr<PyObject, void (*)(PyObject*)> kept(own ? workspace_of(a[1], heads) : Py_NewRef(a[7]), Py_DecRef);
     if (!kept) return W4A4_ERR_INVALID_ARG;  // its own error is set
-    const at::Tensor* ws = tensor(kept, dev);
-    w4a4_status st = W4A4_ERR_INVALID_ARG;
-    if (ws && ws->is_contiguous()) {
-        x.workspace = ws->data_ptr(), x.workspace_bytes = uint64_t(ws->nbytes());
-        st = w4a4_paged_attention(c, &x, stream);
-    }
-    Py_DECREF(kept);
-    return st;
+    const at::Tensor* ws = tensor(own ? PyTuple_GET_ITEM(kept.get(), 0) : kept.get(), dev);
+    if (!ws || !ws->is_contiguous()) return W4A4_ERR_INVALID_ARG;
+    x.workspace = ws->data_ptr(), x.workspace_bytes = uint64_t(ws->nbytes());
+    if (own && PyLong_AsVoidPtr(PyTuple_GET_ITEM(kept.get(), 1)) != stream) keep_for(*ws, a[8], dev, stream);
+    return w4a4_paged_attention(c, &x, stream);
 }
 
 constexpr Param kNorm[] = {{"y", kRequired},   {"r", kRequired},     {"x", kRequired},       {"r_out", kRequired},
@@ -372,7 +400,7 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, n
 PyMODINIT_FUNC PyInit__binding() {
     if (!(n_struct = PyUnicode_InternFromString("_struct")) || !(n_device = PyUnicode_InternFromString("device")) ||
         !(n_ws = PyUnicode_InternFromString("_ws")) || !(n_workspace = PyUnicode_InternFromString("workspace")) ||
-        !(n_refuse = PyUnicode_InternFromString("_refuse")) || !Append::init("w4a4_kv_append") ||
+        !(n_refuse = PyUnicode_InternFromString("_refuse")) || !(n_stream_id = PyUnicode_InternFromString("stream_id")) || !Append::init("w4a4_kv_append") ||
         !Attention::init("w4a4_paged_attention") || !Norm::init("w4a4_block_norm"))
         return nullptr;
     return PyModule_Create(&module);

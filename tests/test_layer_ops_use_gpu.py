@@ -279,3 +279,21 @@ def test_attention_workspace_outlives_the_cache_object():
         torch.cuda.synchronize()
         assert busy and again.data_ptr() != at
         del again
+
+
+def test_rope_table_made_on_a_side_stream():
+    """The table's memory belongs to the stream that fills it: no memory whose last use on the current stream is
+    still to come."""
+    rows, rot = 4096, 128
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        held = torch.full((rows, 2, rot // 2), 7.0, device="cuda")
+        torch.cuda.synchronize()
+        torch.cuda._sleep(200_000_000)
+        copy = held.clone()
+        del held
+        table = w4.w4a4_rope_table(rows, rot, 1e4, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.all(copy == 7)
+        assert torch.equal(table, w4.w4a4_rope_table(rows, rot, 1e4))
+        del copy, table

@@ -432,9 +432,15 @@ class PagedKVCache:
 
 
 def w4a4_rope_table(rows: int, rot_dim: int, theta: float, out=None, stream=None):
-    """fp32 [rows, 2, rot_dim / 2]: cosines and sines of position * theta^(-2 i / rot_dim)."""
+    """fp32 [rows, 2, rot_dim / 2]: cosines and sines of position * theta^(-2 i / rot_dim).  A table that
+    the call makes belongs to the stream that fills it."""
     if out is None:
-        out = torch.empty((rows, 2, rot_dim // 2), dtype=torch.float32, device="cuda")
+        on = stream
+        if on is not None and not isinstance(on, torch.cuda.Stream):
+            handle = on.cuda_stream if hasattr(on, "cuda_stream") else int(on)
+            on = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+        with torch.cuda.stream(on):  # None: the current one
+            out = torch.empty((rows, 2, rot_dim // 2), dtype=torch.float32, device="cuda")
     if out.shape != (rows, 2, rot_dim // 2) or out.dtype != torch.float32:
         _refuse("w4a4_rope_table")
     _check(lib().w4a4_rope_table(_ptr(out), rows, rot_dim, theta, _stream(stream)), "w4a4_rope_table")

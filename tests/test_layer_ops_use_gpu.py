@@ -297,3 +297,10 @@ def test_rope_table_made_on_a_side_stream():
         assert torch.all(copy == 7)
         assert torch.equal(table, w4.w4a4_rope_table(rows, rot, 1e4))
         del copy, table
+
+
+def test_numbers_outside_an_int_are_refused():
+    y = torch.zeros(4, 64, dtype=F16, device="cuda")
+    for over in (dict(post=1 << 32), dict(pre=(1 << 32) + 2), dict(post=-(1 << 32))):
+        with pytest.raises(w4.W4A4Error):
+            w4.w4a4_block_norm(y, y, y.clone(), y.clone(), **over)

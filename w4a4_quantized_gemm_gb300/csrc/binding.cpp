@@ -274,9 +274,10 @@ w4a4_status block_norm(PyObject* const* a) {
         return W4A4_ERR_INVALID_ARG;
     x.rows = int32_t(rows), x.width = int32_t(width), x.rows_per_gate = int32_t(per);
     x.scale = float(PyFloat_AsDouble(a[6])), x.eps = float(PyFloat_AsDouble(a[13]));
-    x.post = int32_t(PyLong_AsLong(a[7])), x.pre = int32_t(PyLong_AsLong(a[10]));
+    const int64_t post = PyLong_AsLongLong(a[7]), pre = PyLong_AsLongLong(a[10]);
+    x.post = int32_t(post), x.pre = int32_t(pre);
     cudaStream_t stream;
-    if (!stream_of(a[14], dev, stream) || PyErr_Occurred()) return W4A4_ERR_INVALID_ARG;
+    if (!fits(post) || !fits(pre) || !stream_of(a[14], dev, stream) || PyErr_Occurred()) return W4A4_ERR_INVALID_ARG;
     const OnDevice on(dev);
     return w4a4_block_norm(&x, stream);
 }

@@ -18,6 +18,7 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libw4a4.so")
+BINDING_PATH = os.path.join(_HERE, "_binding.so")
 
 W4A4_OK = 0
 W4A4_ERR_TIMEOUT = 6
@@ -366,6 +367,8 @@ def __getattr__(name: str):
     if name not in _NATIVE:
         raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
     lib()  # raises if nothing is built
+    if not os.path.exists(BINDING_PATH):
+        raise ImportError(f"{BINDING_PATH} is missing: python w4a4_quantized_gemm_gb300/build.py says why it was not built")
     from . import _binding
     for n in _NATIVE:
         globals()[n] = getattr(_binding, n)

@@ -3,8 +3,9 @@
 Each translation unit is compiled in parallel into ``_build/`` and linked into
 ``w4a4_quantized_gemm_gb300/libw4a4.so`` (static CUDA runtime, no torch).  The
 Python entry of the decoder-layer operators, ``csrc/binding.cpp``, is compiled
-with g++ against the installed torch into ``_binding.so``, which uses that library.
-Rebuilds only when a source or header is newer than the library.
+with g++ against the installed torch into ``_binding.so``, which uses that library
+(the library is built without it where that cannot be done).
+Each is rebuilt only when a source or header of its own is newer.
 """
 from __future__ import annotations
 
@@ -13,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -38,20 +40,31 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _deps():
-    return sources() + [BINDING_SRC] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
-        glob.glob(os.path.join(ROOT, "include", "*.h"))
+def _headers():
+    return glob.glob(os.path.join(ROOT, "include", "*.h"))
+
+
+def _newer(target, deps) -> bool:
+    return os.path.exists(target) and all(os.path.getmtime(d) <= os.path.getmtime(target) for d in deps)
+
+
+def _library_up_to_date() -> bool:
+    return _newer(LIB, sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + _headers())
+
+
+def _binding_up_to_date() -> bool:
+    return _newer(BINDING, [BINDING_SRC] + _headers())
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    return all(os.path.getmtime(d) <= t for d in _deps())
+    return _library_up_to_date() and _binding_up_to_date()
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and up_to_date():
+    """Builds what is older than its sources.  Where the binding cannot be built (no Python or torch headers) the
+    library is all the same, with a warning; the operators that need the binding then raise ImportError."""
+    library, binding = force or not _library_up_to_date(), force or not _binding_up_to_date()
+    if not library and not binding:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
@@ -77,26 +90,30 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"g++ failed for {BINDING_SRC}:\n{res.stderr}")
         return obj, [x for p in ext.library_paths() for x in ("-L" + p, "-Wl,-rpath," + p)]
 
+    def link(cmd, target):
+        tmp = target + f".tmp{os.getpid()}"
+        res = subprocess.run([*cmd, "-o", tmp], capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError(f"link failed:\n{res.stderr}")
+        os.replace(tmp, target)
+
     with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
-        binding = ex.submit(compile_binding)
-        results = list(ex.map(compile_one, sources()))
-        binding_obj, torch_libs = binding.result()
+        binding_job = ex.submit(compile_binding) if binding else None
+        results = list(ex.map(compile_one, sources())) if library else []
     if verbose:
         for obj, log in results:
             print(f"== {os.path.basename(obj)}\n{log}")
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *[o for o, _ in results], "-Xcompiler", "-fPIC"]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError(f"link failed:\n{res.stderr}")
-    os.replace(tmp, LIB)
-    tmp = BINDING + f".tmp{os.getpid()}"
-    cmd = ["g++", "-shared", "-o", tmp, binding_obj, "-L" + HERE, "-l:libw4a4.so", "-Wl,-rpath,$ORIGIN", *torch_libs,
-           "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError(f"link failed:\n{res.stderr}")
-    os.replace(tmp, BINDING)
+    if library:
+        link([nvcc, *ARCH, "-shared", *[o for o, _ in results], "-Xcompiler", "-fPIC"], LIB)
+    if binding:
+        try:
+            obj, torch_libs = binding_job.result()
+            link(["g++", "-shared", obj, "-L" + HERE, "-l:libw4a4.so", "-Wl,-rpath,$ORIGIN", *torch_libs, "-ltorch_python",
+                  "-ltorch_cpu", "-lc10_cuda", "-lc10"], BINDING)
+        except (RuntimeError, ImportError, OSError) as e:
+            if os.path.exists(BINDING):
+                os.remove(BINDING)  # of other sources
+            warnings.warn(f"the binding of the decoder-layer operators was not built: {e}", RuntimeWarning)
     return LIB
 
 

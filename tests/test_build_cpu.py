@@ -50,3 +50,13 @@ def test_an_error_in_the_library_stays_an_error(tree):
     (tree / "csrc" / "a.cu").write_text("not C++\n")
     with pytest.raises(RuntimeError, match="nvcc failed"):
         wbuild.build()
+
+
+def test_binding_is_rebuilt_for_another_torch_or_python(tree, monkeypatch):
+    wbuild.build()
+    assert wbuild.up_to_date()
+    made = os.path.getmtime(tree / "libw4a4.so")
+    monkeypatch.setattr(torch, "__version__", "9.9.9")
+    assert not wbuild.up_to_date()
+    wbuild.build()
+    assert wbuild.up_to_date() and os.path.getmtime(tree / "libw4a4.so") == made

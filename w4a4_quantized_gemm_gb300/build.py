@@ -5,7 +5,8 @@ Each translation unit is compiled in parallel into ``_build/`` and linked into
 Python entry of the decoder-layer operators, ``csrc/binding.cpp``, is compiled
 with g++ against the installed torch into ``_binding.so``, which uses that library
 (the library is built without it where that cannot be done).
-Each is rebuilt only when a source or header of its own is newer.
+Each is rebuilt only when a source or header of its own is newer, the binding also
+for another Python or torch.
 """
 from __future__ import annotations
 
@@ -13,6 +14,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
 import warnings
 from concurrent.futures import ThreadPoolExecutor
@@ -52,8 +54,21 @@ def _library_up_to_date() -> bool:
     return _newer(LIB, sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + _headers())
 
 
+def _built_for() -> str:
+    """What the binding's machine code depends on beside its sources; kept in _build/binding.for."""
+    try:
+        import torch
+    except ImportError:
+        return ""
+    return f"python {sys.version} torch {torch.__version__} {torch.__file__}\n"
+
+
 def _binding_up_to_date() -> bool:
-    return _newer(BINDING, [BINDING_SRC] + _headers())
+    kept = os.path.join(BUILD, "binding.for")
+    if not _newer(BINDING, [BINDING_SRC] + _headers()) or not os.path.exists(kept):
+        return False
+    with open(kept) as f:
+        return f.read() == _built_for()
 
 
 def up_to_date() -> bool:
@@ -110,6 +125,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
             obj, torch_libs = binding_job.result()
             link(["g++", "-shared", obj, "-L" + HERE, "-l:libw4a4.so", "-Wl,-rpath,$ORIGIN", *torch_libs, "-ltorch_python",
                   "-ltorch_cpu", "-lc10_cuda", "-lc10"], BINDING)
+            with open(os.path.join(BUILD, "binding.for"), "w") as f:
+                f.write(_built_for())
         except (RuntimeError, ImportError, OSError) as e:
             if os.path.exists(BINDING):
                 os.remove(BINDING)  # of other sources
@@ -118,5 +135,4 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
 
 if __name__ == "__main__":
-    import sys
     print(build(force="--force" in sys.argv, verbose=True))

@@ -113,6 +113,13 @@ def paged_cache(seqs: int, tokens: int, kv_heads: int, dim: int, page_size: int 
     return w4.PagedKVCache(*pools, table)
 
 
+def check_status(where: str):
+    """Raises what a kernel has left in the device status; reading it clears it."""
+    status = w4.w4a4_device_status()
+    if status != w4.W4A4_OK:
+        raise w4.W4A4Error(status, where)
+
+
 def main(seqs: int = 32, tokens: int = 2048, layers: int = 28):
     hidden, inner, q_heads, kv_heads, dim = 1024, 3072, 16, 8, 128
     stack = [random_layer(hidden, inner, q_heads, kv_heads, dim, seqs, seed=i) for i in range(layers)]
@@ -142,8 +149,7 @@ def main(seqs: int = 32, tokens: int = 2048, layers: int = 28):
         graph.replay()
     end.record()
     torch.cuda.synchronize()
-    if w4.w4a4_device_status() != 0:
-        raise w4.W4A4Error(w4.w4a4_device_status(), "decoder step")
+    check_status("decoder step")
     ms = start.elapsed_time(end) / 20
     print(f"{layers} layers, {seqs} sequences of {tokens} tokens: {ms * 1e3:.0f} us a step, {seqs / ms * 1e3:.0f} tokens/s")
 

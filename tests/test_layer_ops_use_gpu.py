@@ -4,6 +4,7 @@ streams, devices, strides that no index uses; and values at the borders of their
 References and tolerances as in test_layer_ops_gpu."""
 import ctypes
 import math
+import re
 import threading
 
 import pytest
@@ -304,3 +305,28 @@ def test_numbers_outside_an_int_are_refused():
     for over in (dict(post=1 << 32), dict(pre=(1 << 32) + 2), dict(post=-(1 << 32))):
         with pytest.raises(w4.W4A4Error):
             w4.w4a4_block_norm(y, y, y.clone(), y.clone(), **over)
+
+
+def heads_of_a_unit():
+    return int(re.search(r"heads/unit=(\d+)", w4.w4a4_last_dispatch()).group(1))
+
+
+@pytest.mark.parametrize("dtype, dim, hkv, group, side_by_side", [
+    (F16, 256, 2, 11, 4), (E4M3, 256, 1, 16, 2), (F16, 256, 3, 9, 2),       # chunks of 8 query heads, the last one short
+    (F16, 64, 2, 37, 2), (BF16, 128, 2, 20, 2), (E4M3, 96, 4, 17, 2),       # chunks of 16
+    (F16, 96, 4, 3, 4), (E4M3, 64, 6, 3, 2), (E4M3, 128, 8, 5, 4), (BF16, 64, 2, 8, 2)])  # adjacent heads
+def test_attention_chunks_side_by_side(dtype, dim, hkv, group, side_by_side):
+    """Tables with room for much work: the warps of a CTA take several chunks of heads and the same tokens."""
+    lengths = [100, 3, 3000, 64, 0, 17]
+    c = Cache(lengths, 64, hkv, dim, dtype, seed=dim + group, wide=40000)
+    q = randn(gen(72), len(lengths), hkv * group, dim).to(BF16 if dtype == BF16 else F16)
+    check_attention(c, q, lengths, what=f"{dtype} {dim} {hkv}x{group}")
+    assert heads_of_a_unit() == side_by_side
+
+
+@pytest.mark.parametrize("dtype, dim, tokens", [(F16, 128, 16), (E4M3, 64, 32)])
+def test_attention_one_step_a_sequence_of_more_than_the_ctas(dtype, dim, tokens):
+    lengths = [tokens] * 90 + [1, 0, 5] * 30
+    c = Cache(lengths, tokens, 4, dim, dtype, seed=73)
+    check_attention(c, randn(gen(74), len(lengths), 8, dim).to(F16), lengths)
+    assert heads_of_a_unit() == 4

@@ -403,8 +403,9 @@ w4a4_status w4a4_rope_table(float* rope, int rows, int rot_dim, double theta, cu
  * q, out: dtype W4A4_F16 or W4A4_BF16 (the cache: the same or W4A4_E4M3), row
  * (b, h) at b * token_stride + h * head_stride; lse fp32 [seqs][q_heads] or NULL;
  * lengths int32 [seqs]; cache->seqs sequences; q_heads % kv_heads == 0.
- * Scores, statistics and sums are fp32; the probabilities are rounded to the
- * matrix instruction's operand type (fp16, for bf16 caches bf16).  A length
+ * Scores, statistics and sums are fp32; the probabilities go into the product as
+ * two numbers of the cache's type (2^-22 of fp32's for fp16, 2^-16 for bf16), with
+ * E4M3 caches as one of fp16.  A length
  * outside [0, max_pages * page_size] is clamped, tokens of a page outside
  * [0, pages) are left out; both set W4A4_ERR_INDEX.
  * workspace: w4a4_paged_attention_workspace_bytes bytes (0: bad arguments),

@@ -330,3 +330,29 @@ def test_attention_one_step_a_sequence_of_more_than_the_ctas(dtype, dim, tokens)
     c = Cache(lengths, tokens, 4, dim, dtype, seed=73)
     check_attention(c, randn(gen(74), len(lengths), 8, dim).to(F16), lengths)
     assert heads_of_a_unit() == 4
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("dim, group", [(64, 2), (128, 12), (256, 3)])
+def test_attention_weights_keep_more_bits_than_their_type(dtype, dim, group):
+    """Tokens of weight 1 and value 1 beside tokens whose weight w, next below 1, rounds to 1, and of value -1: the
+    output is (1 - w) / (1 + w), all of it what the weights' rounding would take away.
+
+    Rounded twice, a weight is off by u^2 at most; fp32 sums of 256 terms by 256 roundings of 2^-24; the output is
+    rounded once."""
+    tokens, page = 256, 16
+    w = 1 - 0.35 * torch.finfo(dtype).eps / 2
+    k = torch.zeros(tokens // page, page, 1, dim)
+    v = torch.ones_like(k)
+    k[:, 1::2, 0, 0], v[:, 1::2] = -1.0, -1.0
+    table = torch.arange(tokens // page, dtype=torch.int32).repeat(2, 1).cuda()
+    handle = w4.PagedKVCache(k.to(dtype).cuda(), v.to(dtype).cuda(), table)
+    q = torch.zeros(2, group, dim)
+    q[..., 0] = 1.0
+    n = torch.full((2,), tokens, dtype=torch.int32, device="cuda")
+    out = torch.empty(2, group, dim, dtype=dtype, device="cuda")
+    w4.w4a4_paged_attention(q.to(dtype).cuda(), handle, n, out, scale=-math.log(w))
+    torch.cuda.synchronize()
+    ref = torch.full(out.shape, (1 - w) / (1 + w), dtype=F64)
+    err = u(dtype) ** 2 + 2.0 ** -16
+    check(out, ref, ref * u(dtype) + err * (1 + u(dtype)) + tiny(dtype), f"{dtype}")

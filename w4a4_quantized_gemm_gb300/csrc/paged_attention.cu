@@ -607,7 +607,15 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
                         }
                     }
             }
-            uint32_t pf[kSubs][NT][2];  // probabilities [token][head] as the product's second operand
+            // Probabilities [token][head] as the product's second operand.  Rounded to its type they
+            // would add 0.7 (fp16) to 1 (bf16) of the outputs' own rounding to their error, so with
+            // 16-bit caches what the rounding leaves goes in as a second operand, in the shadow of
+            // HBM (128 sequences of 8192 tokens, fp16: 689 us with one operand, 693 with both; D = 256
+            // in groups of 16, the most: 1083 and 1113).  An 8-bit cache keeps the one rounding to
+            // fp16, 2^-11 beside the 2^-4 of its values: there the instructions are nearer to the
+            // limit (E4M3, D = 64: 103 and 108 us, D = 256: 348 and 366).
+            constexpr int kParts = CT == kE4M3 ? 1 : 2;
+            uint32_t pf[kSubs][NT][kParts][2];
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 const float r0 = ref_of(top[t][0]), r1 = ref_of(top[t][1]);
@@ -618,7 +626,13 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
                         const float a = exp2_approx(s[u][t][2 * h] - r0), b = exp2_approx(s[u][t][2 * h + 1] - r1);
                         sum[t][0] += a;
                         sum[t][1] += b;
-                        pf[u][t][h] = transpose8x8(CT == kBF16 ? BF16::down(a, b) : F16::down(a, b));
+                        const uint32_t p = CT == kBF16 ? BF16::down(a, b) : F16::down(a, b);
+                        pf[u][t][0][h] = transpose8x8(p);
+                        if constexpr (kParts == 2) {
+                            const float2 of = CT == kBF16 ? BF16::up(p) : F16::up(p);
+                            pf[u][t][1][h] = transpose8x8(CT == kBF16 ? BF16::down(a - of.x, b - of.y)
+                                                                      : F16::down(a - of.x, b - of.y));
+                        }
                     }
             }
 #pragma unroll
@@ -637,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
                             e4m3x4_to_f16x2(prmt(r[2 * h], 0u, 0x3120u), a[0], a[1]);
                             e4m3x4_to_f16x2(prmt(r[2 * h + 1], 0u, 0x3120u), a[2], a[3]);
 #pragma unroll
-                            for (int t = 0; t < NT; ++t) mma<CT>(out[m + h][t], a, pf[u][t][0], pf[u][t][1]);
+                            for (int t = 0; t < NT; ++t) mma<CT>(out[m + h][t], a, pf[u][t][0][0], pf[u][t][0][1]);
                         }
                     }
                 } else {
@@ -648,7 +662,9 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
                         uint32_t a[4];
                         ldmatrix4_trans(a, base + m * 32);
 #pragma unroll
-                        for (int t = 0; t < NT; ++t) mma<CT>(out[m][t], a, pf[u][t][0], pf[u][t][1]);
+                        for (int t = 0; t < NT; ++t)
+#pragma unroll
+                            for (int i = 0; i < kParts; ++i) mma<CT>(out[m][t], a, pf[u][t][i][0], pf[u][t][i][1]);
                     }
                 }
             }

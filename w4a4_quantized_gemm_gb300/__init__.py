@@ -3,7 +3,8 @@
 Thin Python binding of the C ABI in ``include/w4a4.h`` (library
 ``libw4a4.so`` built in-tree by ``build.py``).  Functions keep the C names and
 only marshal arguments: every step of the layer runs in the CUDA kernels.
-PyTorch is used by callers for device memory and streams.
+PyTorch is used by callers for device memory and streams; nothing is recorded for
+gradients.
 
 There is no CPU fallback: if the library is missing or no sm_103 device is
 current, calls raise.

@@ -384,7 +384,8 @@ PyMethodDef methods[] = {
         "out [seqs, q_heads, dim] = attention of one new token per sequence, q, over the first lengths[b] tokens\n"
         "(int32 [seqs]) that `cache` holds of each, or the last `window` of them.\n\n"
         "scale: of the scores, dim ** -0.5 by default.  lse: fp32 [seqs, q_heads] or None.  workspace: zeroed uint8\n"
-        "of w4a4_paged_attention_workspace_bytes, by default the cache object's own."),
+        "of w4a4_paged_attention_workspace_bytes, for calls of any shapes that do not overlap; by default the cache\n"
+        "object's own."),
     method<Norm>("w4a4_block_norm",
         "w4a4_block_norm(y, r, x, r_out, gate=None, rows_per_gate=0, scale=1.0, post=1, post_gain=None,\n"
         "                post_bias=None, pre=1, pre_gain=None, pre_bias=None, eps=1e-06, stream=None)\n--\n\n"

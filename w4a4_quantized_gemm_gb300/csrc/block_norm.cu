@@ -11,7 +11,7 @@
 // before this one is worked on.  The arithmetic is done on pairs (f32x2), and a missing
 // gain or bias is a vector of ones or zeros rather than a choice per element: one row
 // per CTA in scalar fp32 took 54 instructions an element, which were the bound.  At
-// 8192 x 4096 (bf16 on an fp32 stream, two LayerNorms, gate rows) 64 us, 6.3 TB/s of the
+// 8192 x 4096 (bf16 on an fp32 stream, two LayerNorms, gate rows) 65 us, 6.2 TB/s of the
 // 403 MB that have to move; that first form 90 us.
 //
 // The statistics are the only exchanges: a warp's sums by shuffles, the warps' through
@@ -19,7 +19,7 @@
 // row, the mean of the first eight elements that the warp holds:
 //   mean = p + sum(z - p) / n,   sum (z - mean)^2 = sum (z - p)^2 - (sum(z - p))^2 / n,
 // so that both sums go through the shuffles side by side instead of the squares after the
-// mean (4096 rows of 4096, fp16, two LayerNorms: 30.5 -> 27.3 us).  The difference is safe:
+// mean (4096 rows of 4096, fp16, two LayerNorms: 31.1 -> 27.7 us).  The difference is safe:
 // eight of the h <= 1024 elements (32 lanes of four chunks) have the mean p, so
 // (p - mean)^2 is at most h / 8 times the variance and the difference loses at most seven
 // of fp32's 24 bits, however large the mean.  The warps' moments are joined in the same
@@ -121,8 +121,8 @@ struct Vector {
 // and takes part while that is below W (the others are zero).  NC threads, in one or
 // several warps, have a row and get the same statistics (fixed order).  LAYER: one of the
 // row's norms is a LayerNorm (an RMSNorm beside it takes the mean and the bias as zero);
-// without it the mean, the bias and their work are left out (fp16, 4096 x 8192: 57 us with
-// them, 46 without).
+// without it the mean, the bias and their work are left out (fp16, 4096 x 12288: 115 us with
+// them, 88 without).
 template <class T, int NC, int CH, bool LAYER>
 __device__ __forceinline__ void normalise(uint64_t (&z)[CH][4], int kind, Vector<T, NC, CH>& gain,
                                           Vector<T, NC, CH>& bias, int W, float eps, float4* red) {
@@ -329,13 +329,14 @@ w4a4_status launch_k(const w4a4_block_norm_args& a, cudaStream_t s) {
 template <class T, class R, bool LAYER>
 w4a4_status launch_l(const w4a4_block_norm_args& a, cudaStream_t s) {
     const int chunks = a.width / 8;
-    // Narrow rows share a warp, and a CTA has four: 8192 rows of 64 (fp16) take 1.7 us, one
-    // row to a CTA of one warp 4.2 us; 8192 of 512 take 4.9 us, two warps to a row 5.9 us.
+    // Narrow rows share a warp, and a CTA has four: 8192 rows of 64 (fp16) take 1.9 us, one
+    // row to a CTA of one warp 4.9 us.  (8192 of 512 take 7.8 us, two warps to a row 7.7, but
+    // with the rows in L2 5.1 and 5.9.)
     // Up to 1024 a warp has a row to itself where there are rows enough, without barriers:
-    // 8192 of 1024, LayerNorms, 13.3 us, four warps to a row 17.0 us; but 700 take 3.4 and 2.7.
+    // 8192 of 1024, LayerNorms, 14.3 us, four warps to a row 17.1 us; but 700 take 3.2 and 2.8.
     // Above that two chunks a thread, and thread counts between the powers of two: with 128
-    // threads only, 4096 rows of 1200 (fp16, LayerNorms) take 12.9 us, with 96 threads 10.9; of
-    // 2560 24.2 us with 256 threads and 21.5 with 192, of 5120 53 us with 512 and 44.7 with 384.
+    // threads only, 4096 rows of 1200 (fp16, LayerNorms) take 13.7 us, with 96 threads 11.9; of
+    // 2560 25.4 us with 256 threads and 22.6 with 192, of 5120 53 us with 512 and 45.2 with 384.
     if (chunks <= 8)
         return launch_k<T, R, 128, 8, 1, LAYER>(a, s);
     else if (chunks <= 16)

@@ -24,9 +24,9 @@ namespace {
 __device__ int g_append_status = 0;
 
 // Two forms.  Many tokens: one warp a CTA in at most 78 registers, so that an SM holds 26
-// (8192 tokens of 48 heads of 128, fp16: 33.6 us, 6.1 TB/s; two warps without the limit
+// (8192 tokens of 48 heads of 128, fp16: 34.0 us, 6.1 TB/s; two warps without the limit
 // 40 us).  Few, which all fit at once: the gains of q and k are requested with the first
-// heads and kept, 700 tokens of 32 heads 3.9 us instead of 4.3, one token 2.3 us either way.
+// heads and kept, 700 tokens of 32 heads 4.7 us instead of 4.9, one token 2.4 us either way.
 constexpr int kFew = 5;  // tokens per SM up to which they are few
 constexpr int threads_of(bool many) { return many ? 32 : 64; }
 constexpr int per_sm(bool many) { return many ? 26 : 10; }  // CTAs that an SM holds
@@ -36,9 +36,9 @@ constexpr int kAhead = 2;  // heads whose pieces a lane holds at once
 // towards zero and lo of its sign.  The sum is rounded once, so a quotient that lies halfway
 // between two E4M3 values is found exactly, which hi alone misses; infinities, NaN and s = 0
 // come out as the division's.  8192 tokens of 32 + 2 x 8 heads of 128 take 33.1 us, 35.8 with a
-// division itself, 32.7 with hi alone; 4096 of 16 + 2 x 16 of 64 take 10.4, 12.1 and 9.5.  A
-// scale far from one is brought nearer by a power of two, and x with it, so that 1 / s is a
-// normal number.
+// division itself, 32.7 with hi alone; 4096 of 16 + 2 x 16 of 64 take 10.4, 12.1 and 9.5
+// (inputs in L2).  A scale far from one is brought nearer by a power of two, and x with it, so
+// that 1 / s is a normal number.
 struct Quotients {
     float by, hi, lo;
     __device__ __forceinline__ explicit Quotients(float s) {
@@ -246,8 +246,8 @@ w4a4_status launch_m(const w4a4_kv_cache& c, const w4a4_kv_append_args& a, cudaS
     int want = full / a.tokens > 1 ? full / a.tokens : 1;
     // Many tokens that fill the GPU once or twice but for a quarter or more of the last time:
     // two CTAs a token, where it has heads enough to repay the second look-up.  Of 48 heads of
-    // 128 (fp16), 2500 tokens take 12.4 us, 15.2 with one; 6000 tokens 28.5 and 31.5; but 4200
-    // (full and a little) 19.0 and 17.9, and 2500 tokens of 24 heads of 64 5.7 and 5.4.
+    // 128 (fp16), 2500 tokens take 16.4 us, 17.4 with one; 6000 tokens 29.4 and 31.6; but 4200
+    // (full and a little) 21.4 and 20.3, and 2500 tokens of 24 heads of 64 7.7 and 7.0.
     const int over = a.tokens % full;
     if (MANY && want == 1 && a.tokens < 2 * full && over > full / 8 && over <= full * 3 / 4 && most > 3 * kAhead) want = 2;
     const dim3 grid(unsigned(a.tokens), unsigned(most < want ? most : want));

@@ -13,7 +13,7 @@
 //  * A CTA is four warps that share a unit out: 16 or 32 tokens of one key-value head
 //    each (one head and consecutive tokens, or several heads and the same tokens, see
 //    `together`).  A warp runs on its own: it copies its key and value rows into a ring
-//    of stages in shared memory, the page table looked up one stage ahead of the copy,
+//    of stages in shared memory, the page table looked up three units ahead of the copy,
 //    and keeps a running maximum, sum and output in registers (one pass).  Only the end
 //    of a (sequence, head) synchronises the warps.
 //  * The copies are 16 bytes a lane.  One bulk copy per row streams faster alone (4 GB in
@@ -159,7 +159,8 @@ __device__ __forceinline__ int add_acq_rel(int32_t* p, int v) {
 // n / d for 0 <= n <= 2^20 and d >= 1: (n + 1/2) / d is at least 1 / (2 d) away from a whole
 // number, the division off by 2 ulp and the rounding of d, together less than n / d * 2^-21.
 // (An integer division takes a hundred cycles and more, and a short sequence's way through
-// the kernel had four: 2 x 603 tokens, D = 256: 11.4 -> 10.9 us.)
+// the kernel had four: 300 sequences of up to 300 tokens, one head: 13.4 us with
+// them, 13.1 with these.)
 __device__ __forceinline__ int small_quotient(int n, int d) { return int(__fdividef(n + 0.5f, float(d))); }
 
 // How the units are shared out: the first `more` CTAs take each + 1, the others each.
@@ -237,9 +238,9 @@ __global__ void __launch_bounds__(kThreads, Plan<D, CT, NT>::kPerSM) paged_atten
     // CTA's threads, several in a row to each beyond 128.
     // A run of few units, though, is one piece of one (sequence, head group), so that a CTA
     // has one part to leave and one join to take part in: pieces of at most `piece` units,
-    // the least for which there are CTAs enough (8 sequences of 700 tokens: 9.2 us, 10.8
-    // with runs over two (sequence, head group)s; 200 windows of 588 tokens, 8-bit, D = 96: 13.4
-    // and 17.2 us).
+    // the least for which there are CTAs enough (8 sequences of 700 tokens: 10.8 us, 12.3
+    // with runs over two (sequence, head group)s; 200 windows of 588 tokens, 8-bit, D = 96: 15.5
+    // and 20.3 us, both with the rows in HBM).
     int first, count;
     Share share;
     int piece = 0, c0 = 0, c1 = 0;  // piece > 0: the CTAs that share this one's (sequence, head group)
@@ -908,17 +909,19 @@ w4a4_status launch_n(Args& A, cudaStream_t s) {
     const int chunks = A.c.kv_heads * A.chunks;  // of a sequence
     // Head chunks side by side: the warps take two or four of them and the same tokens.
     //  * Chunks of one head read the same rows, which then come from HBM once (64 sequences
-    //    of 8192 tokens, fp16, D = 256, groups of 16: 1084 us).
+    //    of 8192 tokens, fp16, D = 256, groups of 16: 1113 us, one at a time 1397).
     //  * Rows of adjacent heads make one longer row of what the warps fetch together: 64
-    //    sequences of 8192 tokens, E4M3, D = 64: 101 us, one head at a time 137 us; E4M3,
-    //    D = 256: 346 and 408 us; fp16, D = 96: 270 and 348 us, D = 256: 684 and 704 us.  Not
-    //    at D = 128 of a 16-bit type (128 sequences: 685 and 686 us; in groups of 16 heads
-    //    365 and 350 us).
+    //    sequences of 8192 tokens, E4M3, D = 64: 103 us, one head at a time 140 us; E4M3,
+    //    D = 256: 353 and 409 us; fp16, D = 96: 275 and 352 us, D = 256: 703 and 707 us.  Not
+    //    at D = 128 of a 16-bit type (128 sequences: 689 and 693 us; in groups of 16 heads
+    //    366 and 345 us).
     //  * Neither where there is less work: it makes (sequence, head group) pairs fewer and
-    //    their splits, so the joins, longer (8 x 5000 tokens, fp16, D = 128: 40 and 34 us; 2
-    //    x 642, E4M3, D = 256, groups of 16: 39 and 10.6 us).
+    //    their splits, so the joins, longer (8 x 5000 tokens, fp16, D = 128: 40 and 35 us; 2
+    //    x 642, E4M3, D = 256, groups of 16: 32 and 12.4 us).  What work there is goes by
+    //    the page table's width, since the lengths are on the device: where the rules above
+    //    hold, short sequences in a table with room for long ones take the first time.
     //  * With sequences of one step, and more of them than CTAs, no warp is left without
-    //    tokens (128 sequences of 4 tokens: 4.9 and 12.7 us).
+    //    tokens (128 sequences of 4 tokens: 5.1 and 9.1 us).
     A.together = 1;
     const bool adjacent = (CT == kE4M3 || D != 128) && A.c.k_head_stride == D && A.c.v_head_stride == D;
     const int64_t work = int64_t(A.c.seqs) * chunks * keys;
@@ -948,7 +951,7 @@ template <int D, int CT>
 w4a4_status launch_c(Args& A, cudaStream_t s) {
     // 16 heads a chunk where the group has more than 8; at D = 256 their output alone would
     // take 128 registers, and two chunks of 8 side by side are faster (64 sequences of 8192
-    // tokens, groups of 16, fp16: 1084 us against 1345)
+    // tokens, groups of 16, fp16: 1113 us against 1934)
     if constexpr (D < 256)
         if (A.group > 8) return launch_n<D, CT, 2>(A, s);
     return launch_n<D, CT, 1>(A, s);

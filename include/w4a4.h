@@ -430,6 +430,95 @@ size_t w4a4_paged_attention_workspace_bytes(int seqs, int q_heads, int kv_heads,
 w4a4_status w4a4_paged_attention(const w4a4_kv_cache* cache, const w4a4_paged_attention_args* args,
                                  cudaStream_t stream);
 
+/* Queries and keys of new tokens normalised and rotated, where no cache takes the keys (a
+ * whole prompt that is attended to once; the same arithmetic as w4a4_kv_append's).  For
+ * token t < tokens at position p = positions[t], and x a head of q [t], k [t]:
+ *   x'    = q_gain ? x / sqrt(mean x^2 + eps) * q_gain : x     (k_gain for k)
+ *   y     = x' rotated by rope[p] as in w4a4_kv_append; q_out[t], k_out[t] = y
+ * in fp32 with one rounding to dtype (W4A4_F16 or W4A4_BF16: q, k, the outputs and
+ * gains).  q_out may be q and k_out k, with the same strides; apart from that the
+ * outputs overlap neither each other nor the inputs.  positions[t] < 0 marks a padding
+ * token: its output rows are zero, as are those of a position beyond rope_rows, which
+ * sets W4A4_ERR_INDEX.  positions may be NULL without rope (no token is padding).
+ * head_dim 64, 96, 128 or 256; rot_dim % 16 == 0, <= head_dim; q_heads or kv_heads may
+ * be 0.  Strides in elements, as elsewhere.  tokens == 0: no-op. */
+typedef struct {
+    uint64_t bytes;
+    const void* q;
+    const void* k;
+    void* q_out;
+    void* k_out;
+    const int32_t* positions;
+    const float* rope;
+    const void* q_gain;
+    const void* k_gain;
+    int64_t q_token_stride, q_head_stride, k_token_stride, k_head_stride;
+    int64_t q_out_token_stride, q_out_head_stride, k_out_token_stride, k_out_head_stride;
+    int32_t tokens, q_heads, kv_heads, head_dim, dtype, rope_rows, rot_dim, interleaved;
+    float eps;
+    int32_t reserved;
+} w4a4_qk_rope_args;
+w4a4_status w4a4_qk_rope(const w4a4_qk_rope_args* args, cudaStream_t stream);
+
+/* Attention over whole prompts, packed one behind the other.  Sequence b of seqs is the
+ * rows starts[b] <= i < starts[b + 1] of q, k, v and out (starts int32 [seqs + 1], on the
+ * device).  For row i of it and query head h of key-value head g = h / (q_heads / kv_heads),
+ * over the rows j of the same sequence that i sees:
+ *   a_j = scale q[i][h] . k_j[g],   lse = log sum_j exp(a_j),
+ *   out[i][h] = sum_j exp(a_j - lse) v_j[g].
+ * causal: i sees j <= i, with window > 0 only i - window < j; not causal (window must
+ * be 0): all rows.  A row whose a_j are all -inf (or that sees none) gives out = 0 and
+ * lse = -inf.  Rows that i does not see have no part in its output, whatever they hold; rows
+ * outside all sequences are neither read nor written.
+ * q, k, v, out: dtype W4A4_F16 or W4A4_BF16, head_dim 64, 96, 128 or 256, row (i, h) at
+ * i * token_stride + h * head_stride elements (16-byte aligned); lse fp32 [tokens][q_heads]
+ * or NULL.  q_heads % kv_heads == 0.  out overlaps no input.  Scores, statistics and sums
+ * are fp32, the probabilities go into the product as one number of dtype.  starts that
+ * decrease or leave [0, tokens] are clamped (rows that two sequences then share hold either
+ * one's result) and set W4A4_ERR_INDEX.  tokens == 0 or seqs == 0: no-op. */
+typedef struct {
+    uint64_t bytes;
+    const void* q;
+    const void* k;
+    const void* v;
+    void* out;
+    float* lse;
+    const int32_t* starts;
+    int64_t q_token_stride, q_head_stride, k_token_stride, k_head_stride;
+    int64_t v_token_stride, v_head_stride, out_token_stride, out_head_stride;
+    float scale;
+    int32_t tokens, seqs, q_heads, kv_heads, head_dim, dtype, window, causal, reserved;
+} w4a4_prompt_attention_args;
+w4a4_status w4a4_prompt_attention(const w4a4_prompt_attention_args* args, cudaStream_t stream);
+
+/* Attention of a chunk of new tokens of every sequence over the cache, which holds them
+ * already (w4a4_kv_append).  Sequence b of cache->seqs has the rows
+ * starts[b] <= i < starts[b + 1] of q and out and lengths[b] cached tokens: its last row is
+ * token lengths[b] - 1 of the cache, the row before it lengths[b] - 2, and so on.  Formulas,
+ * causal, window, types and rows without tokens as for w4a4_prompt_attention, over the
+ * tokens of the cache (W4A4_E4M3 ones times their head's scales; the cache has dtype or is
+ * W4A4_E4M3).  A row before token 0 (a chunk longer than lengths[b]) sees nothing.
+ * starts and lengths int32 on the device; lengths outside [0, max_pages * page_size] are
+ * clamped, tokens of a page outside [0, pages) are left out; both set W4A4_ERR_INDEX.
+ * workspace: as for w4a4_paged_attention, whose buffer serves these calls too, one after
+ * another (w4a4_paged_attention_workspace_bytes; calls that may overlap must not share it):
+ * it holds the parts of few rows over a long cache, which are joined in the tokens' order. */
+typedef struct {
+    uint64_t bytes;
+    const void* q;
+    void* out;
+    float* lse;
+    const int32_t* starts;
+    const int32_t* lengths;
+    void* workspace;
+    uint64_t workspace_bytes;
+    int64_t q_token_stride, q_head_stride, out_token_stride, out_head_stride;
+    float scale;
+    int32_t tokens, q_heads, dtype, window, causal;
+} w4a4_chunk_attention_args;
+w4a4_status w4a4_chunk_attention(const w4a4_kv_cache* cache, const w4a4_chunk_attention_args* args,
+                                 cudaStream_t stream);
+
 /* The residual stream between two blocks in one pass.  Row m < rows, width W:
  *   r'[m] = r[m] + scale * gate[m] (.) post(y[m]),   x[m] = pre(r'[m])
  * y: the block's output; r, r': the residual stream (r_out may be r itself, with

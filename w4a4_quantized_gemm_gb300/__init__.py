@@ -76,6 +76,9 @@ SIGNATURES = {
     "w4a4_paged_attention_workspace_bytes": (Z, [I, I, I, I]),
     "w4a4_paged_attention": (I, [P, P, P]),
     "w4a4_block_norm": (I, [P, P]),
+    "w4a4_qk_rope": (I, [P, P]),
+    "w4a4_prompt_attention": (I, [P, P]),
+    "w4a4_chunk_attention": (I, [P, P, P]),
     "w4a4_device_status": (I, []),
     "w4a4_status_string": (ctypes.c_char_p, [I]),
     "w4a4_last_dispatch": (ctypes.c_char_p, []),
@@ -359,12 +362,13 @@ def w4a4_set_stream_k(on: bool):
 _DTYPE = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2, torch.float8_e4m3fn: 3}  # w4a4_dtype
 _CACHE = struct.Struct("=Q5Q7q8i")  # w4a4_kv_cache: size, pointers, strides, sizes and type
 
-_NATIVE = ("w4a4_kv_append", "w4a4_paged_attention", "w4a4_block_norm")
+_NATIVE = ("w4a4_kv_append", "w4a4_paged_attention", "w4a4_block_norm", "w4a4_qk_rope", "w4a4_prompt_attention",
+           "w4a4_chunk_attention")
 
 
 def __getattr__(name: str):
-    """w4a4_kv_append, w4a4_paged_attention and w4a4_block_norm are native functions (csrc/binding.cpp: they
-    read the tensors, check them against each other and call the C ABI), loaded at their first use."""
+    """The decoder-layer operators (_NATIVE) are native functions (csrc/binding.cpp: they read the tensors,
+    check them against each other and call the C ABI), loaded at their first use."""
     if name not in _NATIVE:
         raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
     lib()  # raises if nothing is built

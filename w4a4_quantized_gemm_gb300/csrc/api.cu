@@ -3,6 +3,7 @@
 // Architecture, in depth", "Failure modes": no silent fallback, log which
 // kernel each layer uses).
 #include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
@@ -78,7 +79,9 @@ w4a4_status device_status_words() {
     const w4a4_status f = fused_read_and_clear_status();
     const w4a4_status g = append_read_and_clear_status();
     const w4a4_status h = attention_read_and_clear_status();
-    for (const w4a4_status st : {a, b, c, d, e, f, g, h})
+    const w4a4_status i = rope_read_and_clear_status();
+    const w4a4_status j = prompt_read_and_clear_status();
+    for (const w4a4_status st : {a, b, c, d, e, f, g, h, i, j})
         if (st != W4A4_OK) return st;
     return W4A4_OK;
 }
@@ -96,6 +99,12 @@ void used(int64_t& stride, int64_t n) { stride = n > 1 ? stride : 0; }
 
 // Rows of `dim` elements that n indices reach at this stride, to be written: no two may overlap.
 bool apart(int64_t stride, int64_t n, int dim) { return n <= 1 || stride >= dim; }
+
+// Rows of the prompt and chunk attention: their (row, head) pairs, and the pieces that they
+// make with every sequence's odd end, are counted in 31 bits.
+bool many_rows_fit(int tokens, int seqs, int q_heads) {
+    return seqs <= (1 << 20) && (int64_t(tokens) + 128 * int64_t(seqs)) * q_heads < (int64_t(1) << 31);
+}
 
 // Everything a call can check of a cache without reading device memory; `given` as the
 // kernels take it.
@@ -630,6 +639,112 @@ w4a4_status w4a4_paged_attention(const w4a4_kv_cache* cache, const w4a4_paged_at
         return W4A4_ERR_WORKSPACE;
     if ((st = check_device()) != W4A4_OK) return st;
     return launch_paged_attention(*cache, *a, stream);
+}
+
+w4a4_status w4a4_qk_rope(const w4a4_qk_rope_args* args, cudaStream_t stream) {
+    if (!args || args->bytes != sizeof(*args)) return W4A4_ERR_INVALID_ARG;
+    w4a4_qk_rope_args x = *args;
+    const w4a4_qk_rope_args* a = &x;
+    used(x.q_token_stride, x.tokens), used(x.q_out_token_stride, x.tokens);
+    used(x.k_token_stride, x.tokens), used(x.k_out_token_stride, x.tokens);
+    used(x.q_head_stride, x.q_heads), used(x.q_out_head_stride, x.q_heads);
+    used(x.k_head_stride, x.kv_heads), used(x.k_out_head_stride, x.kv_heads);
+    if (a->tokens < 0 || a->q_heads < 0 || a->kv_heads < 0 || !is_act(a->dtype)) return W4A4_ERR_INVALID_ARG;
+    if (a->head_dim != 64 && a->head_dim != 96 && a->head_dim != 128 && a->head_dim != 256)
+        return W4A4_ERR_UNSUPPORTED_SHAPE;
+    if (a->q_heads > 65536 || a->kv_heads > 65536) return W4A4_ERR_UNSUPPORTED_SHAPE;
+    if (a->rope && (a->rope_rows < 1 || a->rot_dim < 16 || !a->positions)) return W4A4_ERR_INVALID_ARG;
+    if (a->rope && (a->rot_dim % 16 != 0 || a->rot_dim > a->head_dim)) return W4A4_ERR_UNSUPPORTED_SHAPE;
+    if (a->tokens == 0 || a->q_heads + a->kv_heads == 0) return W4A4_OK;
+    if ((a->q_heads > 0 && (!a->q || !a->q_out)) || (a->kv_heads > 0 && (!a->k || !a->k_out))) return W4A4_ERR_INVALID_ARG;
+    for (const void* p : {a->q, a->k, static_cast<const void*>(a->q_out), static_cast<const void*>(a->k_out), a->q_gain,
+                          a->k_gain, static_cast<const void*>(a->rope)})
+        if (!aligned16(p)) return W4A4_ERR_MISALIGNED;
+    if (!aligned4(a->positions)) return W4A4_ERR_MISALIGNED;
+    for (const int64_t s : {a->q_token_stride, a->q_head_stride, a->k_token_stride, a->k_head_stride,
+                            a->q_out_token_stride, a->q_out_head_stride, a->k_out_token_stride, a->k_out_head_stride})
+        if (!good_stride(s, 2)) return W4A4_ERR_MISALIGNED;
+    for (const auto& [stride, n] : {std::pair{a->q_out_token_stride, a->q_heads > 0 ? a->tokens : 0},
+                                    {a->q_out_head_stride, a->q_heads},
+                                    {a->k_out_token_stride, a->kv_heads > 0 ? a->tokens : 0},
+                                    {a->k_out_head_stride, a->kv_heads}})
+        if (!apart(stride, n, a->head_dim)) return W4A4_ERR_INVALID_ARG;
+    // an output that is its own input has that one's strides, and no output is another's
+    if (a->q_heads > 0 && a->q == a->q_out &&
+        (a->q_token_stride != a->q_out_token_stride || a->q_head_stride != a->q_out_head_stride))
+        return W4A4_ERR_INVALID_ARG;
+    if (a->kv_heads > 0 && a->k == a->k_out &&
+        (a->k_token_stride != a->k_out_token_stride || a->k_head_stride != a->k_out_head_stride))
+        return W4A4_ERR_INVALID_ARG;
+    if (a->q_heads > 0 && a->kv_heads > 0 && (a->q_out == a->k_out || a->q_out == a->k || a->k_out == a->q))
+        return W4A4_ERR_INVALID_ARG;
+    w4a4_status st = check_device();
+    if (st != W4A4_OK) return st;
+    return launch_qk_rope(*a, stream);
+}
+
+w4a4_status w4a4_prompt_attention(const w4a4_prompt_attention_args* args, cudaStream_t stream) {
+    if (!args || args->bytes != sizeof(*args)) return W4A4_ERR_INVALID_ARG;
+    w4a4_prompt_attention_args x = *args;
+    const w4a4_prompt_attention_args* a = &x;
+    used(x.q_token_stride, x.tokens), used(x.out_token_stride, x.tokens);
+    used(x.k_token_stride, x.tokens), used(x.v_token_stride, x.tokens);
+    used(x.q_head_stride, x.q_heads), used(x.out_head_stride, x.q_heads);
+    used(x.k_head_stride, x.kv_heads), used(x.v_head_stride, x.kv_heads);
+    if (a->tokens < 0 || a->seqs < 0 || !is_act(a->dtype)) return W4A4_ERR_INVALID_ARG;
+    if (a->window < 0 || (a->window > 0 && !a->causal) || !std::isfinite(a->scale)) return W4A4_ERR_INVALID_ARG;
+    if (a->q_heads < 1 || a->kv_heads < 1) return W4A4_ERR_INVALID_ARG;
+    if (a->q_heads % a->kv_heads != 0 || a->q_heads > 65535) return W4A4_ERR_UNSUPPORTED_SHAPE;
+    if (a->head_dim != 64 && a->head_dim != 96 && a->head_dim != 128 && a->head_dim != 256)
+        return W4A4_ERR_UNSUPPORTED_SHAPE;
+    if (!many_rows_fit(a->tokens, a->seqs, a->q_heads)) return W4A4_ERR_UNSUPPORTED_SHAPE;
+    if (a->tokens == 0 || a->seqs == 0) return W4A4_OK;
+    if (!a->q || !a->k || !a->v || !a->out || !a->starts) return W4A4_ERR_INVALID_ARG;
+    for (const void* p : {a->q, a->k, a->v, static_cast<const void*>(a->out)})
+        if (!aligned16(p)) return W4A4_ERR_MISALIGNED;
+    if (!aligned4(a->lse) || !aligned4(a->starts)) return W4A4_ERR_MISALIGNED;
+    for (const int64_t s : {a->q_token_stride, a->q_head_stride, a->k_token_stride, a->k_head_stride,
+                            a->v_token_stride, a->v_head_stride, a->out_token_stride, a->out_head_stride})
+        if (!good_stride(s, 2)) return W4A4_ERR_MISALIGNED;
+    if (!apart(a->out_token_stride, a->tokens, a->head_dim) || !apart(a->out_head_stride, a->q_heads, a->head_dim))
+        return W4A4_ERR_INVALID_ARG;
+    if (a->out == a->q || a->out == a->k || a->out == a->v) return W4A4_ERR_INVALID_ARG;
+    w4a4_status st = check_device();
+    if (st != W4A4_OK) return st;
+    return launch_prompt_attention(*a, stream);
+}
+
+w4a4_status w4a4_chunk_attention(const w4a4_kv_cache* cache, const w4a4_chunk_attention_args* args,
+                                 cudaStream_t stream) {
+    w4a4_kv_cache view;
+    w4a4_status st = check_cache(cache, &view);
+    if (st != W4A4_OK) return st;
+    if (!args || args->bytes != sizeof(*args)) return W4A4_ERR_INVALID_ARG;
+    cache = &view;
+    w4a4_chunk_attention_args x = *args;
+    const w4a4_chunk_attention_args* a = &x;
+    used(x.q_token_stride, x.tokens), used(x.out_token_stride, x.tokens);
+    used(x.q_head_stride, x.q_heads), used(x.out_head_stride, x.q_heads);
+    if (a->tokens < 0 || !is_act(a->dtype)) return W4A4_ERR_INVALID_ARG;
+    if (a->window < 0 || (a->window > 0 && !a->causal) || !std::isfinite(a->scale)) return W4A4_ERR_INVALID_ARG;
+    if (cache->dtype != a->dtype && cache->dtype != W4A4_E4M3) return W4A4_ERR_INVALID_ARG;
+    if (a->q_heads < 1) return W4A4_ERR_INVALID_ARG;
+    if (a->q_heads % cache->kv_heads != 0 || a->q_heads > 65535) return W4A4_ERR_UNSUPPORTED_SHAPE;
+    if (!many_rows_fit(a->tokens, cache->seqs, a->q_heads)) return W4A4_ERR_UNSUPPORTED_SHAPE;
+    if (a->tokens == 0 || cache->seqs == 0) return W4A4_OK;
+    if (!a->q || !a->out || !a->starts || !a->lengths || !a->workspace) return W4A4_ERR_INVALID_ARG;
+    if (!aligned16(a->q) || !aligned16(a->out) || !aligned16(a->workspace) || !aligned4(a->lse) ||
+        !aligned4(a->starts) || !aligned4(a->lengths))
+        return W4A4_ERR_MISALIGNED;
+    for (const int64_t s : {a->q_token_stride, a->q_head_stride, a->out_token_stride, a->out_head_stride})
+        if (!good_stride(s, 2)) return W4A4_ERR_MISALIGNED;
+    if (!apart(a->out_token_stride, a->tokens, cache->head_dim) || !apart(a->out_head_stride, a->q_heads, cache->head_dim))
+        return W4A4_ERR_INVALID_ARG;
+    if (a->out == a->q || a->out == cache->k || a->out == cache->v) return W4A4_ERR_INVALID_ARG;
+    if (a->workspace_bytes < attention_workspace_bytes(cache->seqs, a->q_heads, cache->kv_heads))
+        return W4A4_ERR_WORKSPACE;
+    if ((st = check_device()) != W4A4_OK) return st;
+    return launch_chunk_attention(*cache, *a, stream);
 }
 
 w4a4_status w4a4_block_norm(const w4a4_block_norm_args* args, cudaStream_t stream) {

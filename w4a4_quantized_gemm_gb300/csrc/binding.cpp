@@ -1,6 +1,7 @@
 // Python entry of the decoder-layer operators (cache append, paged attention, block
-// norm): checks the tensors, fills the argument struct of include/w4a4.h and calls the
-// C ABI.  A call of one of them takes a dozen tensors, and reading their type, shape,
+// norm, rotation without a cache, prompt and chunk attention): checks the tensors, fills
+// the argument struct of include/w4a4.h and calls the C ABI.  A call of one of them takes
+// a dozen tensors, and reading their type, shape,
 // strides, device and pointer through Python attributes takes twice as long as the
 // launch (5 us beside 2 us on the Grace host), which a decode step's short kernels
 // cannot hide; here it is 0.1 us.
@@ -155,8 +156,33 @@ void keep_for(const at::Tensor& ws, PyObject* o, int dev, cudaStream_t s) {
         ws.storage().data_ptr(), c10::cuda::CUDAStream::unpack3(id, c10::DeviceIndex(dev), c10::DeviceType::CUDA));
 }
 
+// A rotation table, fp32 [rows, 2, rot_dim / 2], or None.
+bool rope_of(PyObject* o, int dev, const float*& p, int32_t& rows, int32_t& rot_dim) {
+    p = nullptr, rows = rot_dim = 0;
+    if (o == Py_None) return true;
+    const at::Tensor* rope = tensor(o, dev);
+    if (!rope || rope->dim() != 3 || rope->size(1) != 2 || !fits(rope->size(0)) || !fits(2 * rope->size(2)) ||
+        !vector_of(o, dev, ScalarType::Float, rope->numel(), p))
+        return false;
+    rows = int32_t(rope->size(0)), rot_dim = int32_t(2 * rope->size(2));
+    return p != nullptr;  // not an empty table
+}
+
+// The workspace of an attention call over `cache`: the one given, or the cache object's own, held by `kept`.
+bool attention_workspace(PyObject* given, PyObject* cache, PyObject* stream, int64_t heads, int dev, cudaStream_t s,
+                         std::unique_ptr<PyObject, void (*)(PyObject*)>& kept, void*& p, uint64_t& bytes) {
+    const bool own = given == Py_None;
+    kept.reset(own ? workspace_of(cache, heads) : Py_NewRef(given));
+    if (!kept) return false;  // its own error is set
+    const at::Tensor* ws = tensor(own ? PyTuple_GET_ITEM(kept.get(), 0) : kept.get(), dev);
+    if (!ws || !ws->is_contiguous()) return false;
+    p = ws->data_ptr(), bytes = uint64_t(ws->nbytes());
+    if (own && PyLong_AsVoidPtr(PyTuple_GET_ITEM(kept.get(), 1)) != s) keep_for(*ws, stream, dev, s);
+    return true;
+}
+
 // A parameter's default: required, or one of these.
-enum Default { kRequired, kNone, kZero, kOne, kOneF, kEps, kFalse };
+enum Default { kRequired, kNone, kZero, kOne, kOneF, kEps, kFalse, kTrue };
 struct Param {
     const char* name;
     Default def;
@@ -186,14 +212,7 @@ w4a4_status kv_append(PyObject* const* a) {
         !vector_of(a[9], dev, type, c->head_dim, x.k_gain))
         return W4A4_ERR_INVALID_ARG;
     x.q_out = const_cast<void*>(out);
-    if (a[7] != Py_None) {
-        const at::Tensor* rope = tensor(a[7], dev);
-        if (!rope || rope->dim() != 3 || rope->size(1) != 2 || !fits(rope->size(0)) || !fits(2 * rope->size(2)) ||
-            !vector_of(a[7], dev, ScalarType::Float, rope->numel(), x.rope))
-            return W4A4_ERR_INVALID_ARG;
-        x.rope_rows = int32_t(rope->size(0)), x.rot_dim = int32_t(2 * rope->size(2));
-        if (!x.rope) return W4A4_ERR_INVALID_ARG;  // an empty table
-    }
+    if (!rope_of(a[7], dev, x.rope, x.rope_rows, x.rot_dim)) return W4A4_ERR_INVALID_ARG;
     x.tokens = int32_t(n), x.q_heads = int32_t(heads);
     x.eps = float(PyFloat_AsDouble(a[10]));
     x.interleaved = PyObject_IsTrue(a[11]);
@@ -229,13 +248,9 @@ w4a4_status paged_attention(PyObject* const* a) {
     cudaStream_t stream;
     if (window < 0 || !stream_of(a[8], dev, stream) || PyErr_Occurred()) return W4A4_ERR_INVALID_ARG;
     const OnDevice on(dev);
-    const bool own = a[7] == Py_None;
-    const std::unique_ptr<PyObject, void (*)(PyObject*)> kept(own ? workspace_of(a[1], heads) : Py_NewRef(a[7]), Py_DecRef);
-    if (!kept) return W4A4_ERR_INVALID_ARG;  // its own error is set
-    const at::Tensor* ws = tensor(own ? PyTuple_GET_ITEM(kept.get(), 0) : kept.get(), dev);
-    if (!ws || !ws->is_contiguous()) return W4A4_ERR_INVALID_ARG;
-    x.workspace = ws->data_ptr(), x.workspace_bytes = uint64_t(ws->nbytes());
-    if (own && PyLong_AsVoidPtr(PyTuple_GET_ITEM(kept.get(), 1)) != stream) keep_for(*ws, a[8], dev, stream);
+    std::unique_ptr<PyObject, void (*)(PyObject*)> kept(nullptr, Py_DecRef);
+    if (!attention_workspace(a[7], a[1], a[8], heads, dev, stream, kept, x.workspace, x.workspace_bytes))
+        return W4A4_ERR_INVALID_ARG;
     return w4a4_paged_attention(c, &x, stream);
 }
 
@@ -282,6 +297,110 @@ w4a4_status block_norm(PyObject* const* a) {
     return w4a4_block_norm(&x, stream);
 }
 
+constexpr Param kRope[] = {{"q", kRequired},     {"k", kRequired}, {"positions", kRequired}, {"q_out", kRequired},
+                           {"k_out", kRequired}, {"rope", kNone},  {"q_gain", kNone},        {"k_gain", kNone},
+                           {"eps", kEps},        {"interleaved", kFalse}, {"stream", kNone}};
+w4a4_status qk_rope(PyObject* const* a) {
+    w4a4_qk_rope_args x{};
+    x.bytes = sizeof(x);
+    if (!THPVariable_Check(a[0]) || !THPVariable_Check(a[1])) return W4A4_ERR_INVALID_ARG;
+    const at::Tensor &q = THPVariable_Unpack(a[0]), &k = THPVariable_Unpack(a[1]);
+    if (!q.defined() || !k.defined() || !q.is_cuda() || q.dim() != 3 || k.dim() != 3 || !type_of(q.scalar_type(), x.dtype))
+        return W4A4_ERR_INVALID_ARG;
+    const int dev = q.get_device();
+    const ScalarType type = q.scalar_type();
+    const int64_t n = q.size(0), heads = q.size(1), kv = k.size(1), dim = q.size(2);
+    const void *q_out = nullptr, *k_out = nullptr;
+    if (!fits(n) || !fits(heads) || !fits(kv) || !fits(dim) ||
+        !heads_of(a[0], dev, type, n, heads, dim, x.q, x.q_token_stride, x.q_head_stride) ||
+        !heads_of(a[1], dev, type, n, kv, dim, x.k, x.k_token_stride, x.k_head_stride) ||
+        !vector_of(a[2], dev, ScalarType::Int, n, x.positions) ||
+        !heads_of(a[3], dev, type, n, heads, dim, q_out, x.q_out_token_stride, x.q_out_head_stride) ||
+        !heads_of(a[4], dev, type, n, kv, dim, k_out, x.k_out_token_stride, x.k_out_head_stride) ||
+        !rope_of(a[5], dev, x.rope, x.rope_rows, x.rot_dim) || !vector_of(a[6], dev, type, dim, x.q_gain) ||
+        !vector_of(a[7], dev, type, dim, x.k_gain))
+        return W4A4_ERR_INVALID_ARG;
+    x.q_out = const_cast<void*>(q_out), x.k_out = const_cast<void*>(k_out);
+    x.tokens = int32_t(n), x.q_heads = int32_t(heads), x.kv_heads = int32_t(kv), x.head_dim = int32_t(dim);
+    x.eps = float(PyFloat_AsDouble(a[8]));
+    x.interleaved = PyObject_IsTrue(a[9]);
+    cudaStream_t stream;
+    if (!stream_of(a[10], dev, stream) || PyErr_Occurred()) return W4A4_ERR_INVALID_ARG;
+    const OnDevice on(dev);
+    return w4a4_qk_rope(&x, stream);
+}
+
+// scale, window and causal of an attention call
+template <class X>
+bool mask_of(PyObject* scale, PyObject* window, PyObject* causal, int dim, X& x) {
+    x.scale = scale == Py_None ? 1.f / std::sqrt(float(dim)) : float(PyFloat_AsDouble(scale));
+    const int64_t w = PyLong_AsLongLong(window);
+    x.window = int32_t(w < INT32_MAX ? w : INT32_MAX);
+    x.causal = PyObject_IsTrue(causal);
+    return w >= 0 && !PyErr_Occurred();
+}
+
+constexpr Param kPrompt[] = {{"q", kRequired}, {"k", kRequired}, {"v", kRequired}, {"starts", kRequired}, {"out", kRequired},
+                             {"lse", kNone},   {"scale", kNone}, {"window", kZero}, {"causal", kTrue}, {"stream", kNone}};
+w4a4_status prompt_attention(PyObject* const* a) {
+    w4a4_prompt_attention_args x{};
+    x.bytes = sizeof(x);
+    if (!THPVariable_Check(a[0]) || !THPVariable_Check(a[1]) || !THPVariable_Check(a[3])) return W4A4_ERR_INVALID_ARG;
+    const at::Tensor &q = THPVariable_Unpack(a[0]), &k = THPVariable_Unpack(a[1]), &starts = THPVariable_Unpack(a[3]);
+    if (!q.defined() || !k.defined() || !starts.defined() || !q.is_cuda() || q.dim() != 3 || k.dim() != 3 ||
+        starts.numel() < 1 || !type_of(q.scalar_type(), x.dtype))
+        return W4A4_ERR_INVALID_ARG;
+    const int dev = q.get_device();
+    const ScalarType type = q.scalar_type();
+    const int64_t n = q.size(0), heads = q.size(1), kv = k.size(1), dim = q.size(2), seqs = starts.numel() - 1;
+    const void* out = nullptr;
+    if (!fits(n) || !fits(heads) || !fits(kv) || !fits(dim) || !fits(seqs) ||
+        !heads_of(a[0], dev, type, n, heads, dim, x.q, x.q_token_stride, x.q_head_stride) ||
+        !heads_of(a[1], dev, type, n, kv, dim, x.k, x.k_token_stride, x.k_head_stride) ||
+        !heads_of(a[2], dev, type, n, kv, dim, x.v, x.v_token_stride, x.v_head_stride) ||
+        !vector_of(a[3], dev, ScalarType::Int, seqs + 1, x.starts) ||
+        !heads_of(a[4], dev, type, n, heads, dim, out, x.out_token_stride, x.out_head_stride) ||
+        !vector_of(a[5], dev, ScalarType::Float, n * heads, x.lse) || !mask_of(a[6], a[7], a[8], int(dim), x))
+        return W4A4_ERR_INVALID_ARG;
+    x.out = const_cast<void*>(out);
+    x.tokens = int32_t(n), x.seqs = int32_t(seqs), x.q_heads = int32_t(heads), x.kv_heads = int32_t(kv);
+    x.head_dim = int32_t(dim);
+    cudaStream_t stream;
+    if (!stream_of(a[9], dev, stream) || PyErr_Occurred()) return W4A4_ERR_INVALID_ARG;
+    const OnDevice on(dev);
+    return w4a4_prompt_attention(&x, stream);
+}
+
+constexpr Param kChunk[] = {{"q", kRequired}, {"cache", kRequired}, {"starts", kRequired}, {"lengths", kRequired},
+                            {"out", kRequired}, {"lse", kNone},     {"scale", kNone},      {"window", kZero},
+                            {"causal", kTrue},  {"workspace", kNone}, {"stream", kNone}};
+w4a4_status chunk_attention(PyObject* const* a) {
+    int dev = -1;
+    const w4a4_kv_cache* c = cache_of(a[1], dev);
+    const at::Tensor* q = c ? tensor(a[0], dev) : nullptr;
+    w4a4_chunk_attention_args x{};
+    x.bytes = sizeof(x);
+    if (!q || q->dim() != 3 || !type_of(q->scalar_type(), x.dtype)) return W4A4_ERR_INVALID_ARG;
+    const ScalarType type = q->scalar_type();
+    const int64_t n = q->size(0), heads = q->size(1);
+    const void* out = nullptr;
+    if (!fits(n) || !fits(heads) || !heads_of(a[0], dev, type, n, heads, c->head_dim, x.q, x.q_token_stride, x.q_head_stride) ||
+        !vector_of(a[2], dev, ScalarType::Int, int64_t(c->seqs) + 1, x.starts) ||
+        !vector_of(a[3], dev, ScalarType::Int, c->seqs, x.lengths) ||
+        !heads_of(a[4], dev, type, n, heads, c->head_dim, out, x.out_token_stride, x.out_head_stride) ||
+        !vector_of(a[5], dev, ScalarType::Float, n * heads, x.lse) || !mask_of(a[6], a[7], a[8], c->head_dim, x))
+        return W4A4_ERR_INVALID_ARG;
+    x.out = const_cast<void*>(out);
+    x.tokens = int32_t(n), x.q_heads = int32_t(heads);
+    cudaStream_t stream;
+    if (!stream_of(a[10], dev, stream) || PyErr_Occurred()) return W4A4_ERR_INVALID_ARG;
+    const OnDevice on(dev);
+    std::unique_ptr<PyObject, void (*)(PyObject*)> kept(nullptr, Py_DecRef);
+    if (!attention_workspace(a[9], a[1], a[10], heads, dev, stream, kept, x.workspace, x.workspace_bytes))
+        return W4A4_ERR_INVALID_ARG;
+    return w4a4_chunk_attention(c, &x, stream);
+}
+
 // The Python callable of F: fills in F's parameters, calls it, raises where it refuses.
 template <w4a4_status (*F)(PyObject* const*), const Param* P, int N>
 struct Function {
@@ -301,6 +420,7 @@ struct Function {
                 case kOneF: defaults[i] = PyFloat_FromDouble(1.0); break;
                 case kEps: defaults[i] = PyFloat_FromDouble(1e-6); break;
                 case kFalse: defaults[i] = Py_False; break;
+                case kTrue: defaults[i] = Py_True; break;
             }
         }
         return true;
@@ -363,6 +483,9 @@ const char* Function<F, P, N>::title;
 using Append = Function<kv_append, kAppend, sizeof(kAppend) / sizeof(Param)>;
 using Attention = Function<paged_attention, kAttention, sizeof(kAttention) / sizeof(Param)>;
 using Norm = Function<block_norm, kNorm, sizeof(kNorm) / sizeof(Param)>;
+using Rope = Function<qk_rope, kRope, sizeof(kRope) / sizeof(Param)>;
+using Prompt = Function<prompt_attention, kPrompt, sizeof(kPrompt) / sizeof(Param)>;
+using Chunk = Function<chunk_attention, kChunk, sizeof(kChunk) / sizeof(Param)>;
 
 template <class Fn>
 PyMethodDef method(const char* name, const char* doc) {
@@ -394,6 +517,30 @@ PyMethodDef methods[] = {
         "y, x [rows, width] fp16 or bf16 (x None: not wanted); r, r_out the same type or fp32 (r_out may be r).\n"
         "post, pre: NORM_NONE, NORM_RMS (the default) or NORM_LAYER with gain and bias [width].  gate: [width] or [gates, width],\n"
         "row m under gate row m // rows_per_gate (0: one row for all)."),
+    method<Rope>("w4a4_qk_rope",
+        "w4a4_qk_rope(q, k, positions, q_out, k_out, rope=None, q_gain=None, k_gain=None, eps=1e-06,\n"
+        "             interleaved=False, stream=None)\n--\n\n"
+        "q_out, k_out = queries and keys normalised (gains given) and rotated (rope given), without a cache.\n\n"
+        "q, q_out [tokens, q_heads, dim], k, k_out [tokens, kv_heads, dim]: fp16 or bf16, last dimension contiguous;\n"
+        "q_out may be q, k_out may be k.  positions: int32 [tokens], negative: padding (rows of zeros); None without\n"
+        "rope.  rope: fp32 [rows, 2, rot_dim / 2] (w4a4_rope_table).  q_gain, k_gain: [dim]."),
+    method<Prompt>("w4a4_prompt_attention",
+        "w4a4_prompt_attention(q, k, v, starts, out, lse=None, scale=None, window=0, causal=True, stream=None)\n"
+        "--\n\n"
+        "out [tokens, q_heads, dim] = attention over prompts packed one behind the other: sequence b is the rows\n"
+        "starts[b] .. starts[b + 1] - 1 (int32 [seqs + 1], on the device).  Rows outside all of them stay as they are.\n\n"
+        "q [tokens, q_heads, dim], k, v [tokens, kv_heads, dim]: fp16 or bf16, last dimension contiguous (slices of a\n"
+        "fused q|k|v output).  causal: a row sees itself and the rows before it, with window > 0 the last `window` of\n"
+        "them; else every row of its sequence.  scale: of the scores, dim ** -0.5 by default.  lse: fp32\n"
+        "[tokens, q_heads] or None."),
+    method<Chunk>("w4a4_chunk_attention",
+        "w4a4_chunk_attention(q, cache, starts, lengths, out, lse=None, scale=None, window=0, causal=True,\n"
+        "                     workspace=None, stream=None)\n--\n\n"
+        "out [tokens, q_heads, dim] = attention of a chunk of new tokens of every sequence over `cache`, which holds them\n"
+        "already: rows starts[b] .. starts[b + 1] - 1 (int32 [seqs + 1]) are the last of the lengths[b] tokens\n"
+        "(int32 [seqs]) that the cache holds of sequence b.\n\n"
+        "causal, window, scale, lse: as for w4a4_prompt_attention.  workspace: as for w4a4_paged_attention, by default\n"
+        "the cache object's own."),
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
@@ -403,7 +550,8 @@ PyMODINIT_FUNC PyInit__binding() {
     if (!(n_struct = PyUnicode_InternFromString("_struct")) || !(n_device = PyUnicode_InternFromString("device")) ||
         !(n_ws = PyUnicode_InternFromString("_ws")) || !(n_workspace = PyUnicode_InternFromString("workspace")) ||
         !(n_refuse = PyUnicode_InternFromString("_refuse")) || !(n_stream_id = PyUnicode_InternFromString("stream_id")) || !Append::init("w4a4_kv_append") ||
-        !Attention::init("w4a4_paged_attention") || !Norm::init("w4a4_block_norm"))
+        !Attention::init("w4a4_paged_attention") || !Norm::init("w4a4_block_norm") || !Rope::init("w4a4_qk_rope") ||
+        !Prompt::init("w4a4_prompt_attention") || !Chunk::init("w4a4_chunk_attention"))
         return nullptr;
     return PyModule_Create(&module);
 }

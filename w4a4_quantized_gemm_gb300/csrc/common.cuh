@@ -222,4 +222,6 @@ w4a4_status q_read_and_clear_status();       // bounded-wait status of the activ
 w4a4_status fused_read_and_clear_status();   // bounded-wait status of the fused small-M linear
 w4a4_status append_read_and_clear_status();     // index status of the cache append
 w4a4_status attention_read_and_clear_status();  // index status of the paged attention
+w4a4_status rope_read_and_clear_status();       // index status of the rotation without a cache
+w4a4_status prompt_read_and_clear_status();     // index and bounded-wait status of the prompt and chunk attention
 }  // namespace w4a4

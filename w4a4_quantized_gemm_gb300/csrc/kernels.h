@@ -72,6 +72,11 @@ void launch_rope_table(float* rope, int rows, int rot_dim, double theta, cudaStr
 // paged_attention.cu
 size_t attention_workspace_bytes(int seqs, int q_heads, int kv_heads);
 w4a4_status launch_paged_attention(const w4a4_kv_cache& c, const w4a4_paged_attention_args& a, cudaStream_t s);
+// qk_rope.cu
+w4a4_status launch_qk_rope(const w4a4_qk_rope_args& a, cudaStream_t s);
+// prompt_attention.cu
+w4a4_status launch_prompt_attention(const w4a4_prompt_attention_args& a, cudaStream_t s);
+w4a4_status launch_chunk_attention(const w4a4_kv_cache& c, const w4a4_chunk_attention_args& a, cudaStream_t s);
 // block_norm.cu
 w4a4_status launch_block_norm(const w4a4_block_norm_args& a, cudaStream_t s);
 void launch_rmsnorm_f16(const uint16_t* Y, int M, int ld_y, int K, double eps, uint16_t* X, cudaStream_t s);

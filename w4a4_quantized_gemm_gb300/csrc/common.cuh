@@ -167,6 +167,19 @@ __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;\n" ::"n"(N));
 }
 
+// Division by a number that the host knows, 1 <= d < 2^31: n / d = n * mul >> shift for
+// 0 <= n < 2^31, mul = ceil(2^shift / d), shift = 31 + ceil(log2 d).  (A division takes a
+// hundred and fifty cycles, and a short sequence's way through the kernel has a dozen.)
+struct Divisor {
+    uint32_t mul, shift;
+    explicit Divisor(int d = 1) {
+        shift = 31;
+        while ((1ll << (shift - 31)) < d) ++shift;
+        mul = uint32_t(((1ull << shift) + d - 1) / d);
+    }
+    __device__ __forceinline__ int quotient(int n) const { return int(uint64_t(uint32_t(n)) * mul >> shift); }
+};
+
 __device__ __forceinline__ uint2 ldg_nc_v2(const void* p) {
     uint2 v;
     asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];\n" : "=r"(v.x), "=r"(v.y) : "l"(p));

@@ -37,6 +37,13 @@ __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
     return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
 
+// Four E4M3 bytes -> two fp16 pairs (bytes 0, 1 and 2, 3), exact.
+__device__ __forceinline__ void e4m3x4_to_f16x2(uint32_t four, uint32_t& low, uint32_t& high) {
+    asm("{\n.reg .b16 a, b;\nmov.b32 {a, b}, %2;\ncvt.rn.f16x2.e4m3x2 %0, a;\ncvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
+        : "=r"(low), "=r"(high)
+        : "r"(four));
+}
+
 // Eight consecutive elements of a row, 16-byte aligned.
 template <class T>
 __device__ __forceinline__ void up8(const uint4& w, float (&x)[8]) {

@@ -71,6 +71,7 @@ w4a4_status launch_kv_append(const w4a4_kv_cache& c, const w4a4_kv_append_args& 
 void launch_rope_table(float* rope, int rows, int rot_dim, double theta, cudaStream_t s);
 // paged_attention.cu
 size_t attention_workspace_bytes(int seqs, int q_heads, int kv_heads);
+size_t attention_parts_bytes();  // its front, for parts: nothing has to be there between calls
 w4a4_status launch_paged_attention(const w4a4_kv_cache& c, const w4a4_paged_attention_args& a, cudaStream_t s);
 // qk_rope.cu
 w4a4_status launch_qk_rope(const w4a4_qk_rope_args& a, cudaStream_t s);

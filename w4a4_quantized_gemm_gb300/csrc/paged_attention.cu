@@ -74,19 +74,6 @@ struct Plan {
     static_assert(8 * NT * kOutRow * 4 <= kStage, "a stage holds a warp's output");
 };
 
-// Division by a number that the host knows, 1 <= d < 2^31: n / d = n * mul >> shift for
-// 0 <= n < 2^31, mul = ceil(2^shift / d), shift = 31 + ceil(log2 d).  (A division takes a
-// hundred and fifty cycles, and a short sequence's way through the kernel has a dozen.)
-struct Divisor {
-    uint32_t mul, shift;
-    explicit Divisor(int d = 1) {
-        shift = 31;
-        while ((1ll << (shift - 31)) < d) ++shift;
-        mul = uint32_t(((1ull << shift) + d - 1) / d);
-    }
-    __device__ __forceinline__ int quotient(int n) const { return int(uint64_t(uint32_t(n)) * mul >> shift); }
-};
-
 struct Args {
     w4a4_kv_cache c;
     int page_stride[2], token_stride[2], head_stride[2];  // of keys and values, in bytes
@@ -135,12 +122,6 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
         mma_bf16_16816(d, a, b0, b1);
     else
         mma_f16_16816(d, a, b0, b1);
-}
-// Four E4M3 bytes -> two fp16 pairs (bytes 0, 1 and 2, 3), exact.
-__device__ __forceinline__ void e4m3x4_to_f16x2(uint32_t four, uint32_t& low, uint32_t& high) {
-    asm("{\n.reg .b16 a, b;\nmov.b32 {a, b}, %2;\ncvt.rn.f16x2.e4m3x2 %0, a;\ncvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
-        : "=r"(low), "=r"(high)
-        : "r"(four));
 }
 __device__ __forceinline__ float exp2_approx(float x) {  // 2 ulp; 2^-inf = 0
     float y;
@@ -967,6 +948,8 @@ w4a4_status launch_d(Args& A, cudaStream_t s) {
 }  // namespace
 
 w4a4_status attention_read_and_clear_status() { return take_status_word(g_attention_status); }
+
+size_t attention_parts_bytes() { return kPartsRoom; }
 
 size_t attention_workspace_bytes(int seqs, int q_heads, int kv_heads) {
     return kPartsRoom + align256((2 * kMostCtas + size_t(seqs) * most_groups(q_heads, kv_heads)) * 4);

@@ -1,0 +1,991 @@
+// Attention of many query rows at once: over whole prompts packed one behind the other, and
+// of a chunk of new tokens of every sequence over a paged key-value cache.
+//   a_j = scale q . k_j,   out = sum_j exp(a_j) v_j / sum_j exp(a_j)
+// for the q_heads / kv_heads = G query heads that share a key-value head.
+//
+// A row of the matrix products is a (token, head of the group) pair, so that the heads of a
+// group share the keys that are loaded.  A unit of work is up to 256 consecutive rows of one
+// (sequence, key-value head) and the keys that they see, in tiles of 128.  A persistent CTA
+// per SM takes units, the long ones of a sequence first, every other round backwards.
+//
+//  * Two streams of work run side by side, each with its scores (128 x 128 fp32) and its output
+//    (128 x D fp32) in tensor memory: while the tensor cores work for one, four warps turn the
+//    scores of the other into probabilities.  The streams are the two halves of 256 rows over
+//    the same keys, or, for 128 rows or fewer, even and odd tiles of the same rows' keys, joined
+//    at the end.  D = 256 leaves room for one output and one stream, with two score tiles.
+//  * Scores are tcgen05.mma of queries and keys in shared memory; the probabilities replace
+//    their scores in tensor memory as 16-bit numbers and are the first operand of the product
+//    with the values.  A row of scores is one thread's: 128 registers, no exchange.
+//  * One pass: the running maximum that is subtracted is renewed, and the output rescaled,
+//    only where the scores exceed it by more than kSlack (as a power of two).
+//  * Four warps copy keys and values, 16 bytes a lane, into a ring of stages: any stride, any
+//    page size, E4M3 rows turned into 16-bit ones on the way.  Rows that no query of the unit
+//    sees are not read: they are zeros.
+//  * Values of masked keys meet probabilities of zero in the product, and zero times infinity
+//    or NaN is not zero.  A row whose output is not finite is computed again from its own keys
+//    alone, if keys that it does not see hold such values (careful_row).
+#pragma once
+#include <algorithm>
+#include <atomic>
+#include <type_traits>
+
+#include "elem.cuh"
+#include "kernels.h"
+#include "launch.cuh"
+#include "tc_ptx.cuh"
+
+namespace w4a4 {
+namespace prompt {
+
+constexpr int kThreads = 512;
+constexpr int kTile = 128;                 // keys of a tile, rows of a stream
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr uint32_t kSuspendNs = 20000;
+constexpr int kSoftmaxWarps = 8, kCopyWarps = 4, kMmaWarp = 12, kPlanWarp = 13;
+constexpr int kCopyThreads = 32 * kCopyWarps;
+constexpr int kLostTiles = 16;
+constexpr int kMaxParts = 156;             // of a call
+constexpr int kPartFloats = 256 * 130;     // of one: [rows][D] outputs, [256] maxima, [256] sums
+
+// Keys and values: rows of the packed prompts (table NULL), or of a paged cache.
+struct Keys {
+    const char* pool[2] = {};              // keys, values
+    int64_t page_stride[2] = {};           // in bytes, and so below
+    int token_stride[2] = {}, head_stride[2] = {};
+    const float* scale[2] = {};            // of E4M3 rows, per key-value head
+    const int32_t* table = nullptr;
+    int64_t table_stride = 0;
+    int page_size = 1, pages = 0, longest = 0;
+    Divisor by_page;
+};
+
+struct Args {
+    Keys keys;
+    const char* q;
+    char* out;
+    float* lse;
+    const int32_t *starts, *lengths = nullptr;
+    float* parts = nullptr;                // NULL: units are not split
+    int4* parts_of = nullptr;              // [kMaxParts][2]: (begin, head, row0, rows), (first part, parts of the unit)
+    int64_t q_token, q_head, o_token, o_head;  // elements
+    float scale;
+    int tokens, seqs, q_heads, kv_heads, group, window;
+    bool causal;
+    Divisor by_group;
+};
+
+struct Sequence {
+    int begin, rows, length;               // its rows [begin, begin + rows) of q and its keys
+};
+
+// A unit of work, or a piece of one: what the warps need to know of it.
+struct Unit {
+    int live;                              // 0: there are no more
+    int b, head;                           // sequence, key-value head
+    int row0, rows;                        // rows (token * G + head of the group) of the sequence
+    int begin;                             // the sequence's first token in q
+    int first, length;                     // its place among the keys, and how many there are
+    int key0, end, tiles;                  // keys [key0, end), in tiles
+    int tiles0;                            // of the first stream
+    int shared;                            // the streams are halves of the rows
+    int part;                              // where a piece of a unit goes, -1: the unit is whole
+    int first_part, pieces;
+};
+static_assert(sizeof(Unit) == 64, "copied as four int4");
+
+template <int D>
+struct Plan {
+    static constexpr int kDs = D < 128 ? D : 128;               // elements of a stage's rows
+    static constexpr int kHalves = D / kDs;
+    static constexpr int kPlanes = (kDs + 63) / 64;
+    static constexpr int kStage = kPlanes * kTile * 128;
+    static constexpr int kStreams = D == 256 ? 1 : 2;
+    static constexpr int kQTile = kHalves * kStage;
+    static constexpr int kQ = kStreams * kQTile;
+    static constexpr int kStages = D == 64 ? 11 : 5;
+    static constexpr int kMl = kQ + kStages * kStage;           // [2][128] maxima, then sums, of the streams
+    static constexpr int kUnits = kMl + 2 * 2 * kTile * 4;      // [2] units
+    static constexpr int kBars = kUnits + 2 * int(sizeof(Unit));
+    static constexpr int kFlags = kBars + (2 * kStages + 17) * 8;
+    static constexpr int kLost = kFlags + 16;                   // [kLostTiles][4] keys of a tile on pages outside the pool
+    static constexpr int kBytes = kLost + kLostTiles * 16;
+    // Copies are at most the ring ahead of the scores' products, and those two tiles ahead of
+    // the probabilities.
+    static_assert(kLostTiles >= kStages + 3, "a word is read before it is written again");
+    static_assert(kBytes <= 227 * 1024, "shared memory");
+    // tensor memory: a stream's scores (and probabilities) and its output
+    static constexpr uint32_t scores(int buf) { return D == 256 ? 128 * buf : 256 * buf; }
+    static constexpr uint32_t output(int stream) { return D == 256 ? 256 : 256 * stream + 128; }
+};
+
+__device__ __forceinline__ float ex2(float x) {  // 2 ulp; 2^-inf = 0
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+    return y;
+}
+
+static __device__ int g_prompt_status = 0;
+
+__device__ __forceinline__ Sequence sequence(const Args& A, int b, bool& bad) {
+    Sequence s;
+    const int from = A.starts[b], to = A.starts[b + 1];
+    s.begin = max(0, min(from, A.tokens));
+    const int end = max(s.begin, min(to, A.tokens));
+    bad = from < 0 || to < from || to > A.tokens;
+    s.rows = end - s.begin;
+    s.length = s.rows;
+    if (A.lengths) {
+        const int n = A.lengths[b];
+        s.length = max(0, min(n, A.keys.longest));
+        bad |= n != s.length;
+    }
+    return s;
+}
+
+// Keys [lo, hi) that the row's token at `place` sees.
+__device__ __forceinline__ void sees(const Args& A, int place, int length, int& lo, int& hi) {
+    hi = A.causal ? max(0, min(place, length - 1) + 1) : length;
+    lo = A.window > 0 ? max(0, min(place, INT32_MAX - 1) + 1 - A.window) : 0;
+}
+
+// Where key j's row of head `head` is, in keys (w = 0) or values (1); nullptr: on no page.
+__device__ __forceinline__ const char* key_row(const Args& A, int b, int begin, int head, int j, int w) {
+    const Keys& K = A.keys;
+    const int64_t at = int64_t(head) * K.head_stride[w];
+    if (!K.table) return K.pool[w] + at + int64_t(begin + j) * K.token_stride[w];
+    const int p = K.by_page.quotient(j);
+    const int page = K.table[b * K.table_stride + p];
+    if (page < 0 || page >= K.pages) return nullptr;
+    return K.pool[w] + at + page * K.page_stride[w] + int64_t(j - p * K.page_size) * K.token_stride[w];
+}
+
+template <class T, bool E4M3>
+__device__ __forceinline__ float element(const char* row, int e) {
+    if constexpr (E4M3) {
+        __nv_fp8_e4m3 x;
+        x.__x = *reinterpret_cast<const uint8_t*>(row + e);
+        return float(x);
+    } else {
+        return T::up(*reinterpret_cast<const uint16_t*>(row + 2 * e)).x;
+    }
+}
+
+// Whether a value of keys [lo, hi) is infinite or NaN (a warp).
+template <int D, bool E4M3, bool BF>
+__device__ __noinline__ bool odd_values(const Args& A, const Unit& U, int lo, int hi) {
+    bool odd = false;
+    for (int j = lo + int(threadIdx.x & 31); j < hi; j += 32) {
+        const char* row = key_row(A, U.b, U.begin, U.head, j, 1);
+        if (!row) continue;
+        for (int i = 0; i < D * (E4M3 ? 1 : 2) / 16; ++i) {
+            const uint4 v = reinterpret_cast<const uint4*>(row)[i];
+            for (const uint32_t w : {v.x, v.y, v.z, v.w})
+                if constexpr (E4M3) {
+                    for (int s = 0; s < 32; s += 8) odd |= (w >> s & 0x7Fu) == 0x7Fu;
+                } else {
+                    const uint32_t m = BF ? 0x7F80u : 0x7C00u;
+                    odd |= (w & m) == m || (w >> 16 & m) == m;
+                }
+        }
+    }
+    return __any_sync(0xffffffffu, odd);
+}
+
+// sum_j 2^(a_j - ref) v_j * by over the keys [lo, hi) alone, elements [e0, e1) of the row, by a warp:
+// what the tiles give where no masked value is infinite or NaN.  To `out` in type T, or as fp32.
+template <int D, class T, bool E4M3>
+__device__ __noinline__ void careful_row(const Args& A, const Unit& U, int flat, int lo, int hi, float scale2, float ref,
+                                         float by, void* out, bool fp32, int e0, int e1) {
+    constexpr int kPer = D / 32;
+    const int lane = threadIdx.x & 31;
+    const int token = A.by_group.quotient(flat), h = U.head * A.group + flat - token * A.group;
+    const char* qr = A.q + 2 * ((U.begin + token) * A.q_token + h * A.q_head);
+    float q[kPer], o[kPer] = {};
+    for (int e = 0; e < kPer; ++e) q[e] = element<T, false>(qr, lane + 32 * e);
+    for (int j = lo; j < hi; ++j) {
+        const char *k = key_row(A, U.b, U.begin, U.head, j, 0), *v = key_row(A, U.b, U.begin, U.head, j, 1);
+        if (!k || !v) continue;
+        float a = 0.f;
+        for (int e = 0; e < kPer; ++e) a = fmaf(q[e], element<T, E4M3>(k, lane + 32 * e), a);
+        for (int x = 16; x > 0; x >>= 1) a += __shfl_xor_sync(0xffffffffu, a, x);
+        const float p = ex2(fmaf(a, scale2, -ref));
+        for (int e = 0; e < kPer; ++e) o[e] = fmaf(p, element<T, E4M3>(v, lane + 32 * e), o[e]);
+    }
+    for (int e = 0; e < kPer; ++e) {
+        const int i = lane + 32 * e;
+        if (i < e0 || i >= e1) continue;
+        if (fp32)
+            static_cast<float*>(out)[i] = o[e] * by;
+        else
+            static_cast<uint16_t*>(out)[i] = uint16_t(T::down(o[e] * by, 0.f));
+    }
+}
+
+// ---- the plan: which rows a unit has, and how units are split where they are few
+// The first CTA's warp that makes the plan reports bad starts and lengths.
+struct Share {
+    int rows;          // of a unit
+    int piece;         // tiles of a piece, 0: units are whole
+};
+
+// Tiles that a block of rows of this sequence sees at most.
+__device__ __forceinline__ int most_tiles(const Args& A, const Sequence& s) {
+    const int all = (s.length + kTile - 1) / kTile;
+    if (A.window == 0) return all;
+    const int64_t span = int64_t(A.window) + 256 / A.group + 1;
+    return int(min(int64_t(all), (span + kTile - 1) / kTile + 1));
+}
+__device__ __forceinline__ int blocks_of(const Args& A, const Sequence& s, int rows) {
+    return int((int64_t(s.rows) * A.group + rows - 1) / rows);
+}
+
+template <class F>
+__device__ __forceinline__ int64_t sum_over_sequences(const Args& A, F f) {
+    int64_t sum = 0;
+    for (int b = threadIdx.x & 31; b < A.seqs; b += 32) {
+        bool bad;
+        sum += f(sequence(A, b, bad));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    return sum;
+}
+
+template <int D>
+__device__ Share share_out(const Args& A) {
+    const int ctas = gridDim.x;
+    Share r{128, 0};
+    if (Plan<D>::kStreams == 2) {
+        // 256 rows a unit where there are units enough, or tiles enough to split them into
+        const int64_t units = A.kv_heads * sum_over_sequences(A, [&](const Sequence& s) { return blocks_of(A, s, 256); });
+        if (units >= ctas) r.rows = 256;
+    }
+    if (!A.parts) return r;
+    for (int rows = r.rows == 256 || Plan<D>::kStreams == 1 ? r.rows : 256; rows >= r.rows; rows -= 128) {
+        const int64_t units = A.kv_heads * sum_over_sequences(A, [&](const Sequence& s) { return blocks_of(A, s, rows); });
+        const int64_t tiles = A.kv_heads * sum_over_sequences(A, [&](const Sequence& s) {
+            return int64_t(blocks_of(A, s, rows)) * most_tiles(A, s);
+        });
+        if (rows == 256 && r.rows == 128 && tiles < 8 * ctas) continue;
+        r.rows = rows;
+        if (units >= ctas) return r;
+        int piece = int(max(int64_t(2), (tiles + ctas - 1) / ctas));
+        for (int tries = 0; tries < 8; ++tries) {
+            const int64_t all = A.kv_heads * sum_over_sequences(A, [&](const Sequence& s) {
+                return int64_t(blocks_of(A, s, rows)) * max(1, (most_tiles(A, s) + piece - 1) / piece);
+            });
+            if (all <= ctas) {
+                r.piece = piece;
+                return r;
+            }
+            piece = int(max(int64_t(piece) + 1, piece * all / ctas));
+        }
+        return r;
+    }
+    return r;
+}
+
+// Where unit `want` is, for numbers that grow from call to call (a warp).
+struct Walk {
+    int base, before;  // sequences from `base` on, and the units before them
+    __device__ __forceinline__ bool find(const Args& A, const Share& share, int want, Unit& U) {
+        const int lane = threadIdx.x & 31;
+        while (base < A.seqs) {
+            Sequence s{0, 0, 0};
+            bool bad;
+            int pieces = 1, units = 0;
+            if (base + lane < A.seqs) {
+                s = sequence(A, base + lane, bad);
+                if (share.piece > 0) pieces = max(1, (most_tiles(A, s) + share.piece - 1) / share.piece);
+                units = blocks_of(A, s, share.rows) * A.kv_heads * pieces;
+            }
+            int upto = units;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += v;
+            }
+            const uint32_t beyond = __ballot_sync(0xffffffffu, before + upto > want);
+            if (beyond == 0) {
+                before += __shfl_sync(0xffffffffu, upto, 31);
+                base += 32;
+                continue;
+            }
+            const int at = __ffs(beyond) - 1;
+            const int in = want - before - __shfl_sync(0xffffffffu, upto - units, at);
+            pieces = __shfl_sync(0xffffffffu, pieces, at);
+            units = __shfl_sync(0xffffffffu, units, at);
+            s.begin = __shfl_sync(0xffffffffu, s.begin, at);
+            s.rows = __shfl_sync(0xffffffffu, s.rows, at);
+            s.length = __shfl_sync(0xffffffffu, s.length, at);
+            fill(A, share, base + at, s, units, pieces, want, in, U);
+            return true;
+        }
+        return false;
+    }
+    // The last blocks of a sequence, which see the most keys, come first.
+    __device__ __forceinline__ void fill(const Args& A, const Share& share, int b, const Sequence& s, int units, int pieces,
+                                         int want, int in, Unit& U) {
+        const int per = A.kv_heads * pieces, back = in / per, rest = in - back * per;
+        const int head = rest / pieces, piece = rest - head * pieces;
+        const int block = units / per - 1 - back;
+        U.live = 1;
+        U.b = b, U.head = head;
+        U.row0 = block * share.rows;
+        U.rows = min(share.rows, s.rows * A.group - U.row0);
+        U.begin = s.begin, U.first = s.length - s.rows, U.length = s.length;
+        if (!A.causal) U.first = 0;
+        int lo, hi, unused, hi0;
+        const int from = A.by_group.quotient(U.row0), to = A.by_group.quotient(U.row0 + U.rows - 1);
+        sees(A, U.first + from, U.length, lo, unused);
+        sees(A, U.first + to, U.length, unused, hi);
+        lo = min(lo, hi) & ~(kTile - 1);
+        int tiles = (hi - lo + kTile - 1) / kTile;
+        U.part = -1;
+        U.first_part = want - piece, U.pieces = pieces;
+        if (pieces > 1) {
+            const int t0 = min(tiles, piece * share.piece), t1 = min(tiles, t0 + share.piece);
+            U.part = want;
+            lo += t0 * kTile;
+            tiles = t1 - t0;
+            hi = min(hi, lo + tiles * kTile);
+        }
+        U.key0 = lo, U.end = hi, U.tiles = tiles;
+        U.shared = U.rows > kTile;
+        U.tiles0 = tiles;
+        if (U.shared) {
+            sees(A, U.first + A.by_group.quotient(U.row0 + kTile - 1), U.length, unused, hi0);
+            U.tiles0 = max(0, min(tiles, (hi0 - lo + kTile - 1) / kTile));
+        }
+    }
+};
+
+template <int D, class T, bool E4M3>
+__global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_constant__ Args A) {
+    using namespace tc;
+    using P = Plan<D>;
+    constexpr bool BF = std::is_same_v<T, BF16>;
+    // fp16 probabilities are taken up to 2^15, so that weights down to 2^-38 of the largest
+    // keep the bits of their rounding: thousands of small ones beside one heavy key can make
+    // the output.  bf16 ones have fp32's range.
+    constexpr float kLift = BF ? 0.f : 13.f, kSlack = BF ? 8.f : 2.f;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    int& abort_flag = *reinterpret_cast<int*>(smem + P::kFlags);
+    int& never_abort = *reinterpret_cast<int*>(smem + P::kFlags + 4);
+    uint32_t& tmem_base = *reinterpret_cast<uint32_t*>(smem + P::kFlags + 8);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    volatile int* abort = &abort_flag;
+    const uint32_t base = smem_u32(smem);
+    const uint32_t ring = base + P::kQ;
+    const uint32_t bars = base + P::kBars;
+    auto full = [&](int s) { return bars + 8 * s; };
+    auto empty = [&](int s) { return bars + 8 * (P::kStages + s); };
+    const uint32_t more = bars + 16 * P::kStages;
+    const uint32_t q_full = more, q_free = more + 8, o_free = more + 16, pv_done = more + 24, all_done = more + 32;
+    auto s_full = [&](int i) { return more + 40 + 8 * i; };
+    auto p_full = [&](int i) { return more + 56 + 8 * i; };
+    auto o_full = [&](int i) { return more + 72 + 8 * i; };
+    auto u_full = [&](int i) { return more + 88 + 8 * i; };
+    auto u_free = [&](int i) { return more + 104 + 8 * i; };
+    const uint32_t ml_full = more + 120, ml_free = more + 128;
+    Unit* units = reinterpret_cast<Unit*>(smem + P::kUnits);
+    volatile uint32_t* lost = reinterpret_cast<volatile uint32_t*>(smem + P::kLost);
+
+    if (tid == 0) {
+        abort_flag = (base & 1023u) != 0;  // the swizzle's atoms start on 1024-byte boundaries
+        never_abort = 0;
+        // a copying thread arrives when its copies have; with them in flight the warp once more, for its kLost word
+        for (int s = 0; s < P::kStages; ++s)
+            mbar_init(full(s), kCopyThreads + (E4M3 ? 0 : kCopyWarps)), mbar_init(empty(s), 1);
+        mbar_init(q_full, kCopyThreads), mbar_init(q_free, 1);
+        mbar_init(o_free, kSoftmaxWarps), mbar_init(pv_done, 1), mbar_init(all_done, 1);
+        mbar_init(ml_full, kSoftmaxWarps), mbar_init(ml_free, kSoftmaxWarps);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(s_full(i), 1), mbar_init(p_full(i), 4), mbar_init(o_full(i), 1);
+            mbar_init(u_full(i), 1), mbar_init(u_free(i), kSoftmaxWarps + kCopyWarps + 1);
+        }
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) tmem_alloc(smem_u32(&tmem_base), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base;
+    pdl_wait();
+    pdl_launch_dependents();
+
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (warp_wait_parity_suspend(bar, parity, abort, kWaitNs, kSuspendNs)) return true;
+        *abort = 1;
+        return false;
+    };
+    // The next unit, for every warp that works on it; false: there are no more.
+    auto next_unit = [&](uint32_t n, Unit& U) {
+        const int i = n & 1;
+        if (!wait(u_full(i), n >> 1 & 1)) return false;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) reinterpret_cast<int4*>(&U)[k] = reinterpret_cast<const int4*>(units + i)[k];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(u_free(i));
+        return U.live != 0;
+    };
+
+    auto plan = [&]() {
+        if (blockIdx.x == 0) {
+            bool any = false;
+            for (int b = lane; b < A.seqs; b += 32) {
+                bool bad;
+                sequence(A, b, bad);
+                any |= bad;
+            }
+            if (any) atomicExch(&g_prompt_status, int(W4A4_ERR_INDEX));
+        }
+        const Share share = share_out<D>(A);
+        Walk walk{0, 0};
+        for (uint32_t n = 0;; ++n) {
+            const int turn = int(n & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+            Unit U{};
+            const bool live = walk.find(A, share, int(n * gridDim.x) + turn, U);
+            if (n == 0 && A.parts && lane == 0) {
+                const bool part = live && U.part >= 0;
+                A.parts_of[2 * blockIdx.x] = make_int4(U.begin, U.head, U.row0, U.rows);
+                A.parts_of[2 * blockIdx.x + 1] = make_int4(U.first_part, part ? U.pieces : 0, 0, 0);
+            }
+            if (n >= 2 && !wait(u_free(n & 1), (n >> 1 & 1) ^ 1)) return;
+            if (lane == 0) {
+                units[n & 1] = U;
+                mbar_arrive(u_full(n & 1));
+            }
+            if (!live) return;
+        }
+    };
+
+    auto copy = [&]() {
+        const int t = tid - 32 * kSoftmaxWarps, w = t >> 5;
+        constexpr int kSize = E4M3 ? 1 : 2;
+        constexpr int kPieces = P::kDs * kSize / 16;     // of a stage's row
+        constexpr int kQPieces = D * 2 / 16;
+        const Keys& K = A.keys;
+        uint32_t n_stage = 0, n_q = 0, n_tile = 0;
+        Unit U;
+        for (uint32_t n = 0; next_unit(n, U); ++n) {
+            if (U.tiles == 0) continue;
+            // Page and slot of the key that this lane looks up: key 32 w + lane of a tile.
+            int page = -1, slot = 0;
+            auto look_up = [&](int tile) {
+                const int j = U.key0 + tile * kTile + 32 * w + lane;
+                page = -1;
+                if (tile < U.tiles && j < U.end) {
+                    const int p = K.by_page.quotient(j);
+                    slot = j - p * K.page_size;
+                    page = K.table[U.b * K.table_stride + p];
+                }
+            };
+            if (K.table) look_up(0);
+            // queries
+            if (n_q > 0 && !wait(q_free, (n_q - 1) & 1)) return;
+            for (int h = 0; h < (U.shared ? 2 : 1); ++h) {
+                const uint32_t to = base + h * P::kQTile;
+#pragma unroll 4
+                for (int i = 0; i < kQPieces; ++i) {
+                    const int id = i * kCopyThreads + t, row = id / kQPieces, c = id - row * kQPieces;
+                    const int flat = U.row0 + h * kTile + row;
+                    const bool ok = h * kTile + row < U.rows;
+                    const int token = A.by_group.quotient(ok ? flat : 0), g = ok ? flat - token * A.group : 0;
+                    const char* src = A.q + 2 * ((U.begin + token) * A.q_token + (U.head * A.group + g) * A.q_head) + 16 * c;
+                    cp_async16_zfill(to + (c >> 3) * (kTile * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4), src, ok ? 16 : 0);
+                }
+            }
+            cp_async_mbar_arrive_noinc(q_full);
+            ++n_q;
+            // In the order of use: the values of a tile go behind the keys of the tile after it
+            // (shared rows) or of the two after it.
+            const int lag = P::kStreams == 2 && U.shared ? 1 : 2;
+            uint32_t ok[3] = {0, 0, 0};              // of a tile and the two before it: keys that are there,
+            int64_t k_off = 0, v_off[3] = {0, 0, 0};  // and where this lane's is
+            for (int u = 0; u < U.tiles + lag; ++u) {
+                ok[2] = ok[1], ok[1] = ok[0];
+                v_off[2] = v_off[1], v_off[1] = v_off[0];
+                if (u < U.tiles) {
+                    const int j0 = U.key0 + u * kTile + 32 * w;
+                    if (K.table) {
+                        const bool good = page >= 0 && page < K.pages;
+                        ok[0] = __ballot_sync(0xffffffffu, good);
+                        const uint32_t bad = __ballot_sync(0xffffffffu, !good && j0 + lane < U.end);
+                        if (lane == 0) {
+                            if (bad) atomicExch(&g_prompt_status, int(W4A4_ERR_INDEX));
+                            lost[(n_tile + u) % kLostTiles * 4 + w] = bad;
+                        }
+                        k_off = good ? page * K.page_stride[0] + int64_t(slot) * K.token_stride[0] : 0;
+                        v_off[0] = good ? page * K.page_stride[1] + int64_t(slot) * K.token_stride[1] : 0;
+                        look_up(u + 1);
+                    } else {
+                        const int have = max(0, min(32, U.end - j0));
+                        ok[0] = have == 32 ? 0xffffffffu : (1u << have) - 1;
+                    }
+                }
+#pragma unroll 1
+                for (int x = 0; x < 2 * P::kHalves; ++x) {
+                    const int kv = x < P::kHalves ? 1 : 0, half = x - (1 - kv) * P::kHalves;  // values, then keys
+                    if (kv ? u < lag : u >= U.tiles) continue;
+                    const uint32_t there = kv ? (lag == 1 ? ok[1] : ok[2]) : ok[0];
+                    const int64_t mine = kv ? (lag == 1 ? v_off[1] : v_off[2]) : k_off;
+                    const int j0 = U.key0 + (kv ? u - lag : u) * kTile + 32 * w;
+                    const int st = n_stage % P::kStages;
+                    if (n_stage >= P::kStages && !wait(empty(st), (n_stage / P::kStages - 1) & 1)) return;
+                    const uint32_t to = ring + st * P::kStage;
+                    const char* pool = K.pool[kv] + int64_t(U.head) * K.head_stride[kv] + half * P::kDs * kSize;
+                    auto source = [&](int r, int c) {
+                        const char* src = pool + 16 * c;
+                        if (K.table)
+                            src += __shfl_sync(0xffffffffu, mine, r);
+                        else if (there >> r & 1)
+                            src += int64_t(U.begin + j0 + r) * K.token_stride[kv];
+                        return src;
+                    };
+                    if constexpr (!E4M3) {
+#pragma unroll
+                        for (int i = 0; i < kPieces; ++i) {
+                            const int id = i * 32 + lane, r = id / kPieces, c = id - r * kPieces, row = 32 * w + r;
+                            cp_async16_zfill(to + (c >> 3) * (kTile * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4),
+                                             source(r, c), there >> r & 1 ? 16 : 0);
+                        }
+                        cp_async_mbar_arrive_noinc(full(st));
+                        if (lane == 0) mbar_arrive(full(st));
+                    } else {
+                        uint4 raw[kPieces];
+#pragma unroll
+                        for (int i = 0; i < kPieces; ++i) {
+                            const int id = i * 32 + lane, r = id / kPieces, c = id - r * kPieces;
+                            const char* src = source(r, c);
+                            raw[i] = there >> r & 1 ? ldg_stream_v4(src) : make_uint4(0, 0, 0, 0);
+                        }
+#pragma unroll
+                        for (int i = 0; i < kPieces; ++i) {
+                            const int id = i * 32 + lane, r = id / kPieces, c = id - r * kPieces, row = 32 * w + r;
+                            const uint32_t four[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+                            uint32_t two[8];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                e4m3x4_to_f16x2(four[k], two[2 * k], two[2 * k + 1]);
+                                if constexpr (BF) {  // exact: four significant bits
+                                    const float2 f = F16::up(two[2 * k]), g = F16::up(two[2 * k + 1]);
+                                    two[2 * k] = BF16::down(f.x, f.y), two[2 * k + 1] = BF16::down(g.x, g.y);
+                                }
+                            }
+                            uint8_t* dst = smem + (to - base) + (c >> 2) * (kTile * 128) + row * 128;
+#pragma unroll
+                            for (int y = 0; y < 2; ++y)
+                                *reinterpret_cast<uint4*>(dst + (((2 * (c & 3) + y) ^ (row & 7)) << 4)) =
+                                    make_uint4(two[4 * y], two[4 * y + 1], two[4 * y + 2], two[4 * y + 3]);
+                        }
+                        fence_proxy_async_smem();
+                        mbar_arrive(full(st));
+                    }
+                    ++n_stage;
+                }
+            }
+            n_tile += U.tiles;
+        }
+        cp_async_commit();
+        cp_async_wait<0>();
+    };
+
+    // Products in the order P V of step u - 2, then Q K of step u.  A step is one stream's
+    // tile: streams take turns, or tiles where there is one (D = 256) or the rows are shared.
+    auto multiply = [&]() {
+        constexpr uint32_t kQk = idesc_m128_16bit(kTile, BF, false);
+        constexpr uint32_t kPv = idesc_m128_16bit(P::kDs, BF, true);
+        uint32_t stages = 0, n_q = 0, n_o = 0, np[2] = {0, 0};  // stages before the unit; completed uses
+        Unit U;
+        for (uint32_t n = 0; next_unit(n, U); ++n) {
+            if (U.tiles == 0) continue;
+            const bool shared = P::kStreams == 2 && U.shared;
+            const int steps = shared ? 2 * U.tiles : U.tiles;
+            auto active = [&](int u) { return !(shared && (u & 1) == 0 && (u >> 1) >= U.tiles0); };
+            auto tile_of = [&](int u) { return shared ? u >> 1 : u; };
+            auto stage_of = [&](int tile, int kv, int half) {  // in the order of the copies
+                const int at = shared ? 2 * tile + kv
+                               : kv   ? (tile == U.tiles - 1 ? 2 * tile + 1 : 2 * tile + 2)
+                                      : max(0, 2 * tile - 1);
+                return stages + at * P::kHalves + half;
+            };
+            auto ready = [&](uint32_t st) {
+                if (!wait(full(st % P::kStages), st / P::kStages & 1)) return false;
+                fence_proxy_async_smem();  // the copies went through the generic proxy
+                return true;
+            };
+            if (!wait(q_full, n_q & 1)) return;
+            ++n_q;
+            fence_proxy_async_smem();
+            uint32_t started[2] = {0, 0};
+            for (int u = 0; u < steps + 2; ++u) {
+                if (u >= 2 && active(u - 2)) {
+                    const int w = u - 2, tile = tile_of(w), buf = w & 1, stream = P::kStreams == 2 ? buf : 0;
+                    if (!wait(p_full(buf), np[buf]++ & 1)) return;
+                    if (u == 2 || (u == 3 && !active(0)))
+                        if (n_o > 0 && !wait(o_free, (n_o - 1) & 1)) return;
+                    tc_fence_after();
+#pragma unroll
+                    for (int half = 0; half < P::kHalves; ++half) {
+                        const uint32_t st = stage_of(tile, 1, half);
+                        if (!ready(st)) return;
+                        const uint32_t v = ring + st % P::kStages * P::kStage;
+                        if (lane == 0) {
+#pragma unroll
+                            for (int k = 0; k < kTile / 16; ++k)
+                                mma_f16_tmem_a(tmem + P::output(stream) + half * P::kDs, tmem + P::scores(buf) + 8 * k,
+                                               sdesc_sw128(v + k * 2048, kTile * 128), kPv, started[stream] | (k > 0));
+                            if (!shared || (w & 1)) mma_commit(empty(st % P::kStages));
+                        }
+                    }
+                    started[stream] = 1;
+                    if (lane == 0) {
+                        if constexpr (P::kStreams == 1) mma_commit(pv_done);
+                        const int last = P::kStreams == 1 ? steps - 1
+                                         : shared         ? (stream ? steps - 1 : 2 * (U.tiles0 - 1))
+                                                          : (((steps - 1) & 1) == stream ? steps - 1 : steps - 2);
+                        if (w == last) mma_commit(o_full(stream));
+                    }
+                }
+                if (u < steps && active(u)) {
+                    const int tile = tile_of(u), buf = u & 1;
+                    const uint32_t q = base + (shared ? buf * P::kQTile : 0);
+#pragma unroll
+                    for (int half = 0; half < P::kHalves; ++half) {
+                        const uint32_t st = stage_of(tile, 0, half);
+                        if (!ready(st)) return;
+                        const uint32_t k0 = ring + st % P::kStages * P::kStage;
+                        if (lane == 0) {
+#pragma unroll
+                            for (int k = 0; k < P::kDs / 16; ++k) {
+                                const uint32_t at = (k >> 2) * (kTile * 128) + (k & 3) * 32;
+                                mma_f16(tmem + P::scores(buf), sdesc_sw128(q + half * P::kStage + at), sdesc_sw128(k0 + at), kQk,
+                                        half > 0 || k > 0);
+                            }
+                            if (!shared || (u & 1)) mma_commit(empty(st % P::kStages));
+                        }
+                    }
+                    if (lane == 0) {
+                        mma_commit(s_full(buf));
+                        if (u == steps - 1) mma_commit(q_free);
+                    }
+                }
+                __syncwarp();
+            }
+            ++n_o;
+            stages += 2 * P::kHalves * U.tiles;
+        }
+    };
+
+    auto softmax = [&]() {
+        const int stream = warp >> 2, row = tid & 127;
+        const uint32_t lanes = uint32_t(warp & 3) << 21;  // this warp's lanes of tensor memory
+        float* ml = reinterpret_cast<float*>(smem + P::kMl);
+        uint32_t ns[2] = {0, 0}, n_out[2] = {0, 0}, n_tile = 0, n_ml = 0;
+        Unit U;
+        for (uint32_t n = 0; next_unit(n, U); ++n) {
+            const bool shared = P::kStreams == 2 && U.shared;
+            // scores go by |scale|, keys' scale and log2 e; a negative scale turns their sign, and
+            // a scale of zero makes them zero
+            float scale2 = A.scale * 1.44269504088896341f, v_scale = 1.f, flip = 1.f;
+            if (E4M3 && A.keys.scale[0]) scale2 *= A.keys.scale[0][U.head];
+            if (E4M3 && A.keys.scale[1]) v_scale = A.keys.scale[1][U.head];
+            const float signed2 = scale2;
+            if (!(scale2 > 0.f)) {
+                flip = scale2 < 0.f ? -1.f : scale2 == 0.f ? 0.f : scale2;  // NaN stays
+                scale2 = scale2 < 0.f ? -scale2 : 1.f;
+            }
+            const int local = (shared ? stream * kTile : 0) + row;
+            const bool valid = local < U.rows;
+            const int flat = U.row0 + local, token = A.by_group.quotient(valid ? flat : 0);
+            int lo = 0, hi = INT32_MAX;
+            if (valid) sees(A, U.first + token, U.length, lo, hi);
+            const bool idle = (local & ~31) >= U.rows;  // none of the warp's rows is one
+            const int mine = P::kStreams == 1 ? (stream == 0 ? U.tiles : 0)
+                             : shared         ? (stream == 0 ? U.tiles0 : U.tiles)
+                                              : (U.tiles + 1 - stream) / 2;
+            float top = -INFINITY, sum = 0.f;  // what is subtracted (of the scores as they come), and the sum
+            for (int i = 0; i < mine; ++i) {
+                const int tile = P::kStreams == 1 || shared ? i : 2 * i + stream;
+                const int buf = P::kStreams == 1 ? i & 1 : stream;
+                if (!wait(s_full(buf), ns[buf]++ & 1)) return;
+                tc_fence_after();
+                const uint32_t at = tmem + lanes + P::scores(buf);
+                if (!idle) {
+                    float s[kTile];
+#pragma unroll
+                    for (int c = 0; c < kTile; c += 32) tmem_ld32_at(at + c, s + c);
+                    tmem_wait_ld();
+                    if (flip != 1.f) {
+#pragma unroll
+                        for (int c = 0; c < kTile; ++c) s[c] *= flip;
+                    }
+                    const int j0 = U.key0 + tile * kTile;
+                    if (!__all_sync(0xffffffffu, lo <= j0 && hi >= j0 + kTile)) {
+                        const int a = lo - j0, b = hi - j0;
+#pragma unroll
+                        for (int c = 0; c < kTile; ++c) s[c] = c >= a && c < b ? s[c] : -INFINITY;
+                    }
+                    if (A.keys.table) {
+                        const volatile uint32_t* bad = lost + (n_tile + tile) % kLostTiles * 4;
+                        const uint32_t bits[4] = {bad[0], bad[1], bad[2], bad[3]};
+                        if ((bits[0] | bits[1] | bits[2] | bits[3]) != 0) {
+#pragma unroll
+                            for (int c = 0; c < kTile; ++c) s[c] = bits[c / 32] >> (c % 32) & 1 ? -INFINITY : s[c];
+                        }
+                    }
+                    float m[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                    for (int c = 4; c < kTile; c += 8)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            m[k] = c + 4 + k < kTile ? fmaxf(fmaxf(m[k], s[c + k]), s[c + 4 + k]) : fmaxf(m[k], s[c + k]);
+                    const float most = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+                    const bool renew = (most - top) * scale2 > kSlack;
+                    if (__any_sync(0xffffffffu, renew)) {
+                        // what is there so far was taken relative to the old maximum
+                        const float by = renew ? ex2((top - most) * scale2) : 1.f;
+                        if (renew) top = most;
+                        sum *= by;
+                        if (i > 0) {
+                            if constexpr (P::kStreams == 1)  // the product before this one, still under way
+                                if (!wait(pv_done, (n_tile + i - 1) & 1)) return;
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 32) {
+                                float o[32];
+                                tmem_ld32(tmem + lanes + P::output(P::kStreams == 1 ? 0 : stream) + c, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) o[k] *= by;
+                                tmem_st32(tmem + lanes + P::output(P::kStreams == 1 ? 0 : stream) + c, o);
+                            }
+                        }
+                    }
+                    const float ref = (top == -INFINITY ? 0.f : top * scale2) - kLift;
+                    const uint64_t by2 = f2_pack(scale2, scale2), less = f2_pack(-ref, -ref);
+                    uint64_t sums[4] = {0, 0, 0, 0};
+#pragma unroll
+                    for (int c = 0; c < kTile; c += 64) {
+                        float p[32];
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) {
+                            const float2 x = f2_unpack(ffma2_b64(f2_pack(s[c + 2 * k], s[c + 2 * k + 1]), by2, less));
+                            const float a = ex2(x.x), b = ex2(x.y);
+                            sums[k & 3] = fadd2_b64(sums[k & 3], f2_pack(a, b));
+                            p[k] = __uint_as_float(T::down(a, b));
+                        }
+                        tmem_st32(at + c / 2, p);
+                    }
+                    const float2 x = f2_unpack(fadd2_b64(fadd2_b64(sums[0], sums[1]), fadd2_b64(sums[2], sums[3])));
+                    sum += x.x + x.y;
+                    tmem_wait_st();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full(buf));
+            }
+            n_tile += U.tiles;
+
+            // ---- the output: a stream's rows, or half of the elements of the rows that the
+            // streams (or the only one) have worked on together
+            const bool has0 = P::kStreams == 2 && shared ? U.tiles0 > 0 : U.tiles > 0;
+            const bool has1 = P::kStreams == 2 && (shared ? U.tiles > 0 : U.tiles > 1);
+            const bool reads0 = has0 && !(shared && stream == 1), reads1 = has1 && !(shared && stream == 0);
+            float most = top == -INFINITY ? -INFINITY : top * scale2, w0 = 1.f, w1 = 1.f;
+            if (!shared) {
+                if (n_ml > 0 && !wait(ml_free, (n_ml - 1) & 1)) return;
+                ml[stream * kTile + row] = most;
+                ml[(2 + stream) * kTile + row] = sum;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(ml_full);
+                if (!wait(ml_full, n_ml & 1)) return;
+                const float m0 = ml[row], m1 = ml[kTile + row];
+                most = fmaxf(m0, m1);
+                w0 = m0 == -INFINITY ? 0.f : ex2(m0 - most), w1 = m1 == -INFINITY ? 0.f : ex2(m1 - most);
+                sum = ml[2 * kTile + row] * w0 + ml[3 * kTile + row] * w1;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(ml_free);
+                ++n_ml;
+            }
+            if (reads0 && !wait(o_full(0), n_out[0] & 1)) return;
+            if (reads1 && !wait(o_full(1), n_out[1] & 1)) return;
+            n_out[0] += has0, n_out[1] += has1;
+            tc_fence_after();
+            const int e0 = !shared && stream == 1 ? D / 2 : 0, e1 = shared || stream == 1 ? D : D / 2;
+            const bool none = sum == 0.f;  // no key, or only scores of -inf
+            const float by = U.part >= 0 ? 1.f : none ? 0.f : v_scale / sum;
+            float* part = U.part >= 0 ? A.parts + int64_t(U.part) * kPartFloats : nullptr;
+            const int h = U.head * A.group + flat - token * A.group;
+            char* dst = part ? reinterpret_cast<char*>(part + local * D)
+                             : A.out + 2 * ((U.begin + token) * A.o_token + h * A.o_head);
+            float odd = 0.f;  // NaN once an element is infinite or NaN
+            if (!idle) {
+                w0 *= by, w1 *= by;
+#pragma unroll 1
+                for (int e = e0; e < e1; e += 16) {
+                    float x[16], y[16];
+                    if (reads0) tmem_ld16(tmem + lanes + P::output(0) + e, x);
+                    if (reads1) tmem_ld16(tmem + lanes + P::output(P::kStreams - 1) + e, y);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        x[k] = (reads0 && w0 != 0.f ? x[k] * w0 : 0.f) + (reads1 && w1 != 0.f ? y[k] * w1 : 0.f);
+                        if (none) x[k] = 0.f;
+                        odd = fmaf(x[k], 0.f, odd);
+                    }
+                    if (!valid) continue;
+                    if (part) {
+#pragma unroll
+                        for (int k = 0; k < 16; k += 4)
+                            *reinterpret_cast<float4*>(dst + 4 * (e + k)) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 16; k += 8)
+                            *reinterpret_cast<uint4*>(dst + 2 * (e + k)) =
+                                make_uint4(T::down(x[k], x[k + 1]), T::down(x[k + 2], x[k + 3]),
+                                           T::down(x[k + 4], x[k + 5]), T::down(x[k + 6], x[k + 7]));
+                    }
+                }
+            }
+            if (U.tiles > 0) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(o_free);
+            }
+            if (valid && (shared || stream == 0)) {
+                if (part)
+                    part[256 * 128 + local] = most, part[256 * 129 + local] = sum;
+                else if (A.lse)
+                    A.lse[int64_t(U.begin + token) * A.q_heads + h] =
+                        none ? -INFINITY : 0.693147180559945309f * (most - kLift + log2f(sum));
+            }
+            const uint32_t again = __ballot_sync(0xffffffffu, valid && odd != 0.f && sum < INFINITY);
+            if (again != 0) {
+                // keys that were in the tiles and that not every row of the warp sees
+                const int last_lo = __reduce_max_sync(0xffffffffu, valid ? lo : 0);
+                const int first_hi = __reduce_min_sync(0xffffffffu, valid ? hi : INT32_MAX);
+                if (odd_values<D, E4M3, BF>(A, U, U.key0, min(U.end, last_lo)) ||
+                    odd_values<D, E4M3, BF>(A, U, max(U.key0, first_hi), U.end))
+                    for (uint32_t left = again; left != 0; left &= left - 1) {
+                        const int r = __ffs(left) - 1;
+                        auto of = [&](auto v) { return __shfl_sync(0xffffffffu, v, r); };
+                        careful_row<D, T, E4M3>(A, U, of(flat), max(of(lo), U.key0), min(of(hi), U.end), signed2,
+                                                of(most) - kLift, of(by),
+                                                reinterpret_cast<void*>(of(reinterpret_cast<unsigned long long>(dst))),
+                                                part != nullptr, e0, e1);
+                    }
+            }
+        }
+    };
+
+    if (warp < kSoftmaxWarps) {
+        regs_inc<192>();
+        softmax();
+    } else if (warp < kSoftmaxWarps + kCopyWarps) {
+        regs_dec<80>();
+        copy();
+    } else {
+        regs_dec<48>();
+        if (warp == kMmaWarp) {
+            multiply();
+            // what has been issued ends before its operands and tensor memory go away
+            if (lane == 0) mma_commit(all_done);
+            __syncwarp();
+            volatile int* never = &never_abort;
+            warp_wait_parity_suspend(all_done, 0, never, kWaitNs, kSuspendNs);
+        } else if (warp == kPlanWarp) {
+            plan();
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_relinquish();
+        tmem_dealloc(tmem, 512);
+    }
+    if (tid == 0 && *abort) atomicExch(&g_prompt_status, int(W4A4_ERR_TIMEOUT));
+}
+
+// The parts of split units joined, in the order of their keys: part i of n takes the i-th
+// n-th of the rows.  Four elements a thread.
+template <int D, class T, bool E4M3>
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args A) {
+    constexpr float kLift = std::is_same_v<T, BF16> ? 0.f : 13.f;
+    constexpr int kPer = D / 4, kRows = 256 / kPer;  // threads of a row, rows at a time
+    pdl_wait();
+    pdl_launch_dependents();
+    const int4 a = A.parts_of[2 * blockIdx.x], b = A.parts_of[2 * blockIdx.x + 1];
+    const int begin = a.x, head = a.y, row0 = a.z, rows = a.w, first = b.x, pieces = b.y;
+    if (pieces == 0) return;
+    const int me = int(blockIdx.x) - first;
+    const int from = rows * me / pieces, to = rows * (me + 1) / pieces;
+    const int e = threadIdx.x % kPer * 4;
+    const float v_scale = E4M3 && A.keys.scale[1] ? A.keys.scale[1][head] : 1.f;
+    for (int r = from + threadIdx.x / kPer; r < to && threadIdx.x < kPer * kRows; r += kRows) {
+        const float* part = A.parts + int64_t(first) * kPartFloats;
+        float most = -INFINITY;
+        for (int i = 0; i < pieces; ++i) most = fmaxf(most, part[int64_t(i) * kPartFloats + 256 * 128 + r]);
+        float sum = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int i = 0; i < pieces; ++i) {
+            const float* p = part + int64_t(i) * kPartFloats;
+            const float m = p[256 * 128 + r], l = p[256 * 129 + r];
+            const float4 x = *reinterpret_cast<const float4*>(p + r * D + e);
+            if (m == -INFINITY) continue;  // the part saw nothing
+            const float w = ex2(m - most);
+            sum = fmaf(w, l, sum);
+            if (w != 0.f) o.x = fmaf(w, x.x, o.x), o.y = fmaf(w, x.y, o.y), o.z = fmaf(w, x.z, o.z), o.w = fmaf(w, x.w, o.w);
+        }
+        const bool none = sum == 0.f;
+        const float by = none ? 0.f : v_scale / sum;
+        if (none) o = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int flat = row0 + r, token = A.by_group.quotient(flat), h = head * A.group + flat - token * A.group;
+        *reinterpret_cast<uint2*>(A.out + 2 * ((begin + token) * A.o_token + h * A.o_head + e)) =
+            make_uint2(T::down(o.x * by, o.y * by), T::down(o.z * by, o.w * by));
+        if (A.lse && e == 0)
+            A.lse[int64_t(begin + token) * A.q_heads + h] =
+                none ? -INFINITY : 0.693147180559945309f * (most - kLift + log2f(sum));
+    }
+}
+
+template <int D, class T, bool E4M3>
+w4a4_status run(Args& A, cudaStream_t s) {
+    using P = Plan<D>;
+    auto kernel = attention_kernel<D, T, E4M3>;
+    static std::atomic<uint64_t> ready{0};  // devices
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 64) return W4A4_ERR_CUDA;
+    if (!(ready.load(std::memory_order_acquire) >> dev & 1)) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kBytes) != cudaSuccess)
+            return launch_status();
+        ready.fetch_or(uint64_t(1) << dev, std::memory_order_release);
+    }
+    // A CTA per SM, or one per unit where there can be fewer.  Units are fewer than SMs if the
+    // rows of all sequences are; then parts of them are worth a second launch where the cache
+    // can be long.
+    const int sms = std::min(device_sm_count(), kMaxParts);
+    const int64_t rows = int64_t(A.tokens) * A.group;
+    const int64_t most = A.kv_heads * ((rows + kTile - 1) / kTile + A.seqs);
+    const int64_t least = A.kv_heads * ((rows + P::kStreams * kTile - 1) / (P::kStreams * kTile));
+    const int64_t keys = A.window > 0 ? std::min(int64_t(A.keys.longest), int64_t(A.window) + A.tokens) : A.keys.longest;
+    if (!(A.parts && least < sms && keys > 4 * kTile)) A.parts = nullptr;
+    const int grid = A.parts ? sms : int(std::min(int64_t(sms), most));
+    constexpr bool bf16 = std::is_same_v<T, BF16>;
+    const char* text = !A.lengths ? (bf16 ? "prompt_attention bf16 tokens=%d seqs=%d heads=%d/%d dim=%d stages=%d grid=%d parts=%d"
+                                          : "prompt_attention f16 tokens=%d seqs=%d heads=%d/%d dim=%d stages=%d grid=%d parts=%d")
+                       : E4M3     ? "chunk_attention e4m3 tokens=%d seqs=%d heads=%d/%d dim=%d stages=%d grid=%d parts=%d"
+                       : bf16     ? "chunk_attention bf16 tokens=%d seqs=%d heads=%d/%d dim=%d stages=%d grid=%d parts=%d"
+                                  : "chunk_attention f16 tokens=%d seqs=%d heads=%d/%d dim=%d stages=%d grid=%d parts=%d";
+    set_dispatch_ints(text, {A.tokens, A.seqs, A.q_heads, A.kv_heads, D, P::kStages, grid, A.parts != nullptr});
+    w4a4_status st = launch<attention_kernel<D, T, E4M3>>(dim3(unsigned(grid)), kThreads, P::kBytes, s, A);
+    if (st == W4A4_OK && A.parts) st = launch<join_kernel<D, T, E4M3>>(dim3(unsigned(grid)), 256, 0, s, A);
+    return st;
+}
+
+}  // namespace prompt
+}  // namespace w4a4

@@ -330,6 +330,34 @@ __device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a, uint64_t b,
         "l"(a), "l"(b), "r"(idesc), "r"(acc)
         : "memory");
 }
+// Shared-memory matrix descriptors of tiles stored as planes of [rows][128 bytes] with the
+// 128-byte swizzle (a row's 16-byte pieces XORed with its number modulo 8; planes 1024-byte
+// aligned).  As a K-major operand a row is a row of the matrix and the plane's 64 16-bit
+// elements are a piece of its K; 8-row groups lie 1024 bytes apart.  As an MN-major operand a
+// row is one k and the plane's elements are 64 of the rows (columns) of the matrix; planes
+// are `plane` bytes apart.
+__device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t plane = 16) {
+    uint64_t d = 0;
+    d |= uint64_t((saddr & 0x3FFFFu) >> 4);
+    d |= uint64_t(plane >> 4) << 16;
+    d |= uint64_t(1024 >> 4) << 32;
+    d |= uint64_t(1) << 46;
+    d |= uint64_t(2) << 61;
+    return d;
+}
+// kind::f16 with the operands' type (bits 7-9, 10-12: 1 = BF16) and an MN-major B (bit 16).
+__host__ __device__ constexpr uint32_t idesc_m128_16bit(int n, bool bf16, bool b_mn) {
+    return idesc_m128(n) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? 1u << 16 : 0u);
+}
+// kind::f16 with the A operand in tensor memory: lane = row, k = 2 * column + half.
+__device__ __forceinline__ void mma_f16_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
+                                               uint32_t acc) {
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
 // Arrive on `bar` once every tcgen05 operation issued so far by this thread completes.
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar)

@@ -43,6 +43,7 @@ constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint32_t kSuspendNs = 20000;
 constexpr int kSoftmaxWarps = 8, kCopyWarps = 4, kMmaWarp = 12, kPlanWarp = 13;
 constexpr int kCopyThreads = 32 * kCopyWarps;
+constexpr int kCopyArrivals = 33;          // of a copying warp at a stage's barrier
 constexpr int kLostTiles = 16;
 constexpr int kMaxParts = 156;             // of a call
 constexpr int kPartFloats = 256 * 130;     // of one: [rows][D] outputs, [256] maxima, [256] sums
@@ -56,6 +57,7 @@ struct Keys {
     const int32_t* table = nullptr;
     int64_t table_stride = 0;
     int page_size = 1, pages = 0, longest = 0;
+    int box = 0;                           // keys that one copy of the tensor maps brings, 0: there are no maps
     Divisor by_page;
 };
 
@@ -122,6 +124,12 @@ __device__ __forceinline__ float ex2(float x) {  // 2 ulp; 2^-inf = 0
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
     return y;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
 }
 
 static __device__ int g_prompt_status = 0;
@@ -361,7 +369,8 @@ struct Walk {
 };
 
 template <int D, class T, bool E4M3>
-__global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_constant__ Args A) {
+__global__ void __launch_bounds__(kThreads, 1)
+attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
     using namespace tc;
     using P = Plan<D>;
     constexpr bool BF = std::is_same_v<T, BF16>;
@@ -394,9 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     if (tid == 0) {
         abort_flag = (base & 1023u) != 0;  // the swizzle's atoms start on 1024-byte boundaries
         never_abort = 0;
-        // a copying thread arrives when its copies have; with them in flight the warp once more, for its kLost word
-        for (int s = 0; s < P::kStages; ++s)
-            mbar_init(full(s), kCopyThreads + (E4M3 ? 0 : kCopyWarps)), mbar_init(empty(s), 1);
+        for (int s = 0; s < P::kStages; ++s) mbar_init(full(s), kCopyArrivals * kCopyWarps), mbar_init(empty(s), 1);
         mbar_init(q_full, kCopyThreads), mbar_init(q_free, 1);
         mbar_init(o_free, kSoftmaxWarps), mbar_init(pv_done, 1), mbar_init(all_done, 1);
         mbar_init(ml_full, kSoftmaxWarps), mbar_init(ml_free, kSoftmaxWarps);
@@ -411,6 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_base;
+    if (tid == 0 && A.keys.box > 0) prefetch_tensor_map(&k_map), prefetch_tensor_map(&v_map);
     pdl_wait();
     pdl_launch_dependents();
 
@@ -419,15 +427,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         *abort = 1;
         return false;
     };
-    // The next unit, for every warp that works on it; false: there are no more.
-    auto next_unit = [&](uint32_t n, Unit& U) {
-        const int i = n & 1;
-        if (!wait(u_full(i), n >> 1 & 1)) return false;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) reinterpret_cast<int4*>(&U)[k] = reinterpret_cast<const int4*>(units + i)[k];
+    // Unit n, for every warp that works on it; nullptr: there are no more.  done_with gives its
+    // place back.
+    auto unit = [&](uint32_t n) -> const Unit* {
+        if (!wait(u_full(n & 1), n >> 1 & 1)) return nullptr;
+        return units[n & 1].live ? units + (n & 1) : nullptr;
+    };
+    auto done_with = [&](uint32_t n) {
         __syncwarp();
-        if (lane == 0) mbar_arrive(u_free(i));
-        return U.live != 0;
+        if (lane == 0) mbar_arrive(u_free(n & 1));
     };
 
     auto plan = [&]() {
@@ -460,15 +468,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         }
     };
 
+    uint32_t n_stage = 0;  // copies begun
     auto copy = [&]() {
         const int t = tid - 32 * kSoftmaxWarps, w = t >> 5;
         constexpr int kSize = E4M3 ? 1 : 2;
         constexpr int kPieces = P::kDs * kSize / 16;     // of a stage's row
         constexpr int kQPieces = D * 2 / 16;
         const Keys& K = A.keys;
-        uint32_t n_stage = 0, n_q = 0, n_tile = 0;
-        Unit U;
-        for (uint32_t n = 0; next_unit(n, U); ++n) {
+        uint32_t n_q = 0, n_tile = 0;
+        for (uint32_t n = 0;; done_with(n++)) {
+            const Unit* const unit_n = unit(n);
+            if (!unit_n) return;
+            const Unit U = *unit_n;
             if (U.tiles == 0) continue;
             // Page and slot of the key that this lane looks up: key 32 w + lane of a tile.
             int page = -1, slot = 0;
@@ -503,9 +514,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             const int lag = P::kStreams == 2 && U.shared ? 1 : 2;
             uint32_t ok[3] = {0, 0, 0};              // of a tile and the two before it: keys that are there,
             int64_t k_off = 0, v_off[3] = {0, 0, 0};  // and where this lane's is
+            int pages[3] = {0, 0, 0}, slots[3] = {0, 0, 0};
             for (int u = 0; u < U.tiles + lag; ++u) {
                 ok[2] = ok[1], ok[1] = ok[0];
                 v_off[2] = v_off[1], v_off[1] = v_off[0];
+                pages[2] = pages[1], pages[1] = pages[0], slots[2] = slots[1], slots[1] = slots[0];
                 if (u < U.tiles) {
                     const int j0 = U.key0 + u * kTile + 32 * w;
                     if (K.table) {
@@ -518,6 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                         }
                         k_off = good ? page * K.page_stride[0] + int64_t(slot) * K.token_stride[0] : 0;
                         v_off[0] = good ? page * K.page_stride[1] + int64_t(slot) * K.token_stride[1] : 0;
+                        pages[0] = page, slots[0] = slot;
                         look_up(u + 1);
                     } else {
                         const int have = max(0, min(32, U.end - j0));
@@ -543,7 +557,22 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                             src += int64_t(U.begin + j0 + r) * K.token_stride[kv];
                         return src;
                     };
-                    if constexpr (!E4M3) {
+                    if (!E4M3 && K.box > 0 && there == 0xffffffffu) {
+                        // 32 rows that are all there: the copy engine brings them, a box a lane
+                        const int boxes = 32 / K.box;
+                        const int from = lane < boxes ? lane * K.box : 0;
+                        const int pg = K.table ? __shfl_sync(0xffffffffu, kv ? (lag == 1 ? pages[1] : pages[2]) : pages[0], from) : 0;
+                        const int y = K.table ? __shfl_sync(0xffffffffu, kv ? (lag == 1 ? slots[1] : slots[2]) : slots[0], from)
+                                              : U.begin + j0 + from;
+                        if (lane == 0) {
+                            mbar_expect_tx(full(st), 32 * 128 * P::kPlanes);
+                            mbar_arrive_n(full(st), kCopyArrivals - 1);
+                        }
+                        if (lane < boxes)
+                            for (int plane = 0; plane < P::kPlanes; ++plane)
+                                tma_load_4d(to + plane * (kTile * 128) + (32 * w + from) * 128, kv ? &v_map : &k_map,
+                                            half * P::kDs + 64 * plane, y, U.head, pg, full(st));
+                    } else if constexpr (!E4M3) {
 #pragma unroll
                         for (int i = 0; i < kPieces; ++i) {
                             const int id = i * 32 + lane, r = id / kPieces, c = id - r * kPieces, row = 32 * w + r;
@@ -581,100 +610,140 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                         }
                         fence_proxy_async_smem();
                         mbar_arrive(full(st));
+                        if (lane == 0) mbar_arrive(full(st));
                     }
                     ++n_stage;
                 }
             }
             n_tile += U.tiles;
         }
-        cp_async_commit();
-        cp_async_wait<0>();
     };
 
-    // Products in the order P V of step u - 2, then Q K of step u.  A step is one stream's
-    // tile: streams take turns, or tiles where there is one (D = 256) or the rows are shared.
+    // One thread issues the products, and every instruction of it between the arrival of the
+    // probabilities and the next scores delays them: descriptors are sums of a few words,
+    // stages are counted, nothing is waited for twice.
     auto multiply = [&]() {
         constexpr uint32_t kQk = idesc_m128_16bit(kTile, BF, false);
         constexpr uint32_t kPv = idesc_m128_16bit(P::kDs, BF, true);
-        uint32_t stages = 0, n_q = 0, n_o = 0, np[2] = {0, 0};  // stages before the unit; completed uses
-        Unit U;
-        for (uint32_t n = 0; next_unit(n, U); ++n) {
-            if (U.tiles == 0) continue;
-            const bool shared = P::kStreams == 2 && U.shared;
-            const int steps = shared ? 2 * U.tiles : U.tiles;
-            auto active = [&](int u) { return !(shared && (u & 1) == 0 && (u >> 1) >= U.tiles0); };
-            auto tile_of = [&](int u) { return shared ? u >> 1 : u; };
-            auto stage_of = [&](int tile, int kv, int half) {  // in the order of the copies
-                const int at = shared ? 2 * tile + kv
-                               : kv   ? (tile == U.tiles - 1 ? 2 * tile + 1 : 2 * tile + 2)
-                                      : max(0, 2 * tile - 1);
-                return stages + at * P::kHalves + half;
-            };
-            auto ready = [&](uint32_t st) {
-                if (!wait(full(st % P::kStages), st / P::kStages & 1)) return false;
-                fence_proxy_async_smem();  // the copies went through the generic proxy
-                return true;
-            };
-            if (!wait(q_full, n_q & 1)) return;
-            ++n_q;
+        // descriptors' low words (their high words are alike)
+        const uint32_t keys0 = uint32_t(sdesc_sw128(ring)), values0 = uint32_t(sdesc_sw128(ring, kTile * 128));
+        const uint32_t q0 = uint32_t(sdesc_sw128(base)), hi = uint32_t(sdesc_sw128(0) >> 32);
+        uint32_t st = 0, phase = 0;  // the stage that comes next, and its barrier's parity
+        uint32_t n_o = 0, p_phase = 0;  // units with an output; bit i: the parity of p_full(i)
+        uint32_t q_phase = 0;
+        auto wait1 = [&](uint32_t bar, uint32_t parity) {
+            if (wait_parity_suspend(bar, parity, abort, kWaitNs, kSuspendNs)) return true;
+            *abort = 1;
+            return false;
+        };
+        auto ready = [&](uint32_t s, uint32_t ph) {
+            if (!wait1(full(s), ph)) return false;
+            if (!E4M3) fence_proxy_async_smem();  // the copies went through the generic proxy
+            return true;
+        };
+        auto next_stage = [&]() {
+            if (++st == P::kStages) st = 0, phase ^= 1;
+        };
+        auto scores = [&](int buf, uint32_t q, uint32_t k, bool more) {
+            mma_f16_rows<P::kDs / 16>(tmem + P::scores(buf), q, k, hi, kQk, more);
+        };
+        auto output = [&](int stream, int buf, int half, uint32_t v, bool more) {
+            mma_f16_tmem_a_rows(tmem + P::output(stream) + half * P::kDs, tmem + P::scores(buf), v, hi, kPv, more);
+        };
+        auto wait_p = [&](int buf) {
+            const bool ok = wait1(p_full(buf), p_phase >> buf & 1);
+            p_phase ^= 1u << buf;
+            tc_fence_after();
+            return ok;
+        };
+        for (uint32_t n = 0;; ++n) {
+            const int i = n & 1;
+            if (!wait1(u_full(i), n >> 1 & 1)) return;
+            const Unit& U = units[i];
+            const bool live = U.live != 0, shared = P::kStreams == 2 && U.shared;
+            const int tiles = U.tiles, tiles0 = U.tiles0;
+            mbar_arrive(u_free(i));
+            if (!live) return;
+            if (tiles == 0) continue;
+            if (!wait1(q_full, q_phase)) return;
+            q_phase ^= 1;
             fence_proxy_async_smem();
-            uint32_t started[2] = {0, 0};
-            for (int u = 0; u < steps + 2; ++u) {
-                if (u >= 2 && active(u - 2)) {
-                    const int w = u - 2, tile = tile_of(w), buf = w & 1, stream = P::kStreams == 2 ? buf : 0;
-                    if (!wait(p_full(buf), np[buf]++ & 1)) return;
-                    if (u == 2 || (u == 3 && !active(0)))
-                        if (n_o > 0 && !wait(o_free, (n_o - 1) & 1)) return;
-                    tc_fence_after();
-#pragma unroll
-                    for (int half = 0; half < P::kHalves; ++half) {
-                        const uint32_t st = stage_of(tile, 1, half);
-                        if (!ready(st)) return;
-                        const uint32_t v = ring + st % P::kStages * P::kStage;
-                        if (lane == 0) {
-#pragma unroll
-                            for (int k = 0; k < kTile / 16; ++k)
-                                mma_f16_tmem_a(tmem + P::output(stream) + half * P::kDs, tmem + P::scores(buf) + 8 * k,
-                                               sdesc_sw128(v + k * 2048, kTile * 128), kPv, started[stream] | (k > 0));
-                            if (!shared || (w & 1)) mma_commit(empty(st % P::kStages));
+            bool free = n_o == 0;  // the last unit's output has been read
+            auto wait_o = [&]() { return free || (free = wait1(o_free, (n_o - 1) & 1)); };
+            if (shared) {
+                // both halves of the rows on a tile: P V of one, Q K of the next tile, then the other half's
+                if (!ready(st, phase)) return;
+                if (tiles0 > 0) {
+                    scores(0, q0, keys0 + st * (P::kStage >> 4), false);
+                    mma_commit(s_full(0));
+                }
+                scores(1, q0 + (P::kQTile >> 4), keys0 + st * (P::kStage >> 4), false);
+                mma_commit(s_full(1));
+                mma_commit(empty(st));
+                if (tiles == 1) mma_commit(q_free);
+                next_stage();
+                for (int t = 0; t < tiles; ++t) {
+                    const uint32_t v = st, v_phase = phase;
+                    next_stage();
+                    const uint32_t k = st, k_phase = phase;
+                    const bool more = t + 1 < tiles;
+                    if (more) next_stage();
+                    const uint32_t vd = values0 + v * (P::kStage >> 4), kd = keys0 + k * (P::kStage >> 4);
+                    if (!ready(v, v_phase)) return;
+                    if (more && !ready(k, k_phase)) return;
+                    if (t < tiles0) {
+                        if (!wait_p(0) || !wait_o()) return;
+                        output(0, 0, 0, vd, t > 0);
+                        if (t + 1 < tiles0) {
+                            scores(0, q0, kd, false);
+                            mma_commit(s_full(0));
+                        } else {
+                            mma_commit(o_full(0));
                         }
                     }
-                    started[stream] = 1;
-                    if (lane == 0) {
+                    if (!wait_p(1) || !wait_o()) return;
+                    output(P::kStreams - 1, 1, 0, vd, t > 0);
+                    if (more) {
+                        scores(1, q0 + (P::kQTile >> 4), kd, false);
+                        mma_commit(s_full(1));
+                        mma_commit(empty(v));
+                        mma_commit(empty(k));
+                        if (t + 2 == tiles) mma_commit(q_free);
+                    } else {
+                        mma_commit(o_full(1));
+                        mma_commit(empty(v));
+                    }
+                }
+            } else {
+                // tiles in turn, two under way: P V of one, Q K of the second after it
+                for (int t = -2; t < tiles; ++t) {
+                    const int buf = t & 1, stream = P::kStreams == 2 ? buf : 0;
+                    if (t >= 0) {
+#pragma unroll
+                        for (int half = 0; half < P::kHalves; ++half) {
+                            if (!ready(st, phase)) return;
+                            if (half == 0 && (!wait_p(buf) || !wait_o())) return;
+                            output(stream, buf, half, values0 + st * (P::kStage >> 4), t >= P::kStreams);
+                            mma_commit(empty(st));
+                            next_stage();
+                        }
                         if constexpr (P::kStreams == 1) mma_commit(pv_done);
-                        const int last = P::kStreams == 1 ? steps - 1
-                                         : shared         ? (stream ? steps - 1 : 2 * (U.tiles0 - 1))
-                                                          : (((steps - 1) & 1) == stream ? steps - 1 : steps - 2);
-                        if (w == last) mma_commit(o_full(stream));
+                        if (t + P::kStreams >= tiles) mma_commit(o_full(stream));
                     }
-                }
-                if (u < steps && active(u)) {
-                    const int tile = tile_of(u), buf = u & 1;
-                    const uint32_t q = base + (shared ? buf * P::kQTile : 0);
+                    if (t + 2 < tiles) {
 #pragma unroll
-                    for (int half = 0; half < P::kHalves; ++half) {
-                        const uint32_t st = stage_of(tile, 0, half);
-                        if (!ready(st)) return;
-                        const uint32_t k0 = ring + st % P::kStages * P::kStage;
-                        if (lane == 0) {
-#pragma unroll
-                            for (int k = 0; k < P::kDs / 16; ++k) {
-                                const uint32_t at = (k >> 2) * (kTile * 128) + (k & 3) * 32;
-                                mma_f16(tmem + P::scores(buf), sdesc_sw128(q + half * P::kStage + at), sdesc_sw128(k0 + at), kQk,
-                                        half > 0 || k > 0);
-                            }
-                            if (!shared || (u & 1)) mma_commit(empty(st % P::kStages));
+                        for (int half = 0; half < P::kHalves; ++half) {
+                            if (!ready(st, phase)) return;
+                            scores(buf, q0 + half * (P::kStage >> 4), keys0 + st * (P::kStage >> 4), half > 0);
+                            if (half == P::kHalves - 1) mma_commit(s_full(buf));
+                            mma_commit(empty(st));
+                            next_stage();
                         }
-                    }
-                    if (lane == 0) {
-                        mma_commit(s_full(buf));
-                        if (u == steps - 1) mma_commit(q_free);
+                        if (t + 3 == tiles) mma_commit(q_free);
                     }
                 }
-                __syncwarp();
             }
             ++n_o;
-            stages += 2 * P::kHalves * U.tiles;
         }
     };
 
@@ -683,8 +752,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         const uint32_t lanes = uint32_t(warp & 3) << 21;  // this warp's lanes of tensor memory
         float* ml = reinterpret_cast<float*>(smem + P::kMl);
         uint32_t ns[2] = {0, 0}, n_out[2] = {0, 0}, n_tile = 0, n_ml = 0;
-        Unit U;
-        for (uint32_t n = 0; next_unit(n, U); ++n) {
+        for (uint32_t n = 0;; done_with(n++)) {
+            const Unit* const unit_n = unit(n);
+            if (!unit_n) return;
+            const Unit& U = *unit_n;
             const bool shared = P::kStreams == 2 && U.shared;
             // scores go by |scale|, keys' scale and log2 e; a negative scale turns their sign, and
             // a scale of zero makes them zero
@@ -737,11 +808,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                     }
                     float m[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-                    for (int c = 4; c < kTile; c += 8)
+                    for (int c = 4; c + 8 <= kTile; c += 8)
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            m[k] = c + 4 + k < kTile ? fmaxf(fmaxf(m[k], s[c + k]), s[c + 4 + k]) : fmaxf(m[k], s[c + k]);
-                    const float most = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+                        for (int k = 0; k < 4; ++k) m[k] = max3(m[k], s[c + k], s[c + 4 + k]);
+                    const float most = fmaxf(max3(max3(m[0], m[1], m[2]), m[3], fmaxf(s[124], s[125])), fmaxf(s[126], s[127]));
                     const bool renew = (most - top) * scale2 > kSlack;
                     if (__any_sync(0xffffffffu, renew)) {
                         // what is there so far was taken relative to the old maximum
@@ -753,32 +823,32 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                                 if (!wait(pv_done, (n_tile + i - 1) & 1)) return;
                             tc_fence_after();
 #pragma unroll 1
-                            for (int c = 0; c < D; c += 32) {
-                                float o[32];
-                                tmem_ld32(tmem + lanes + P::output(P::kStreams == 1 ? 0 : stream) + c, o);
+                            for (int c = 0; c < D; c += 16) {
+                                float o[16];
+                                tmem_ld16(tmem + lanes + P::output(P::kStreams == 1 ? 0 : stream) + c, o);
                                 tmem_wait_ld();
 #pragma unroll
-                                for (int k = 0; k < 32; ++k) o[k] *= by;
-                                tmem_st32(tmem + lanes + P::output(P::kStreams == 1 ? 0 : stream) + c, o);
+                                for (int k = 0; k < 16; ++k) o[k] *= by;
+                                tmem_st16(tmem + lanes + P::output(P::kStreams == 1 ? 0 : stream) + c, o);
                             }
                         }
                     }
                     const float ref = (top == -INFINITY ? 0.f : top * scale2) - kLift;
                     const uint64_t by2 = f2_pack(scale2, scale2), less = f2_pack(-ref, -ref);
-                    uint64_t sums[4] = {0, 0, 0, 0};
+                    uint64_t sums[2] = {0, 0};
 #pragma unroll
-                    for (int c = 0; c < kTile; c += 64) {
-                        float p[32];
+                    for (int c = 0; c < kTile; c += 32) {
+                        uint32_t p[16];
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) {
+                        for (int k = 0; k < 16; ++k) {
                             const float2 x = f2_unpack(ffma2_b64(f2_pack(s[c + 2 * k], s[c + 2 * k + 1]), by2, less));
                             const float a = ex2(x.x), b = ex2(x.y);
-                            sums[k & 3] = fadd2_b64(sums[k & 3], f2_pack(a, b));
-                            p[k] = __uint_as_float(T::down(a, b));
+                            sums[k & 1] = fadd2_b64(sums[k & 1], f2_pack(a, b));
+                            p[k] = T::down(a, b);
                         }
-                        tmem_st32(at + c / 2, p);
+                        tmem_st16_b32(at + c / 2, p);
                     }
-                    const float2 x = f2_unpack(fadd2_b64(fadd2_b64(sums[0], sums[1]), fadd2_b64(sums[2], sums[3])));
+                    const float2 x = f2_unpack(fadd2_b64(sums[0], sums[1]));
                     sum += x.x + x.y;
                     tmem_wait_st();
                 }
@@ -881,20 +951,26 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     };
 
     if (warp < kSoftmaxWarps) {
-        regs_inc<192>();
+        regs_inc<184>();
         softmax();
     } else if (warp < kSoftmaxWarps + kCopyWarps) {
-        regs_dec<80>();
+        regs_dec<72>();
         copy();
+        cp_async_commit();
+        cp_async_wait<0>();
+        if (*abort)  // the copy engine's land before the shared memory goes away
+            for (uint32_t i = n_stage > P::kStages ? n_stage - P::kStages : 0; i < n_stage; ++i)
+                warp_wait_parity_suspend(full(i % P::kStages), i / P::kStages & 1, &never_abort, kWaitNs, kSuspendNs);
     } else {
-        regs_dec<48>();
+        regs_dec<72>();
         if (warp == kMmaWarp) {
-            multiply();
-            // what has been issued ends before its operands and tensor memory go away
-            if (lane == 0) mma_commit(all_done);
+            if (lane == 0) {
+                multiply();
+                // what has been issued ends before its operands and tensor memory go away
+                mma_commit(all_done);
+                wait_parity_suspend(all_done, 0, &never_abort, kWaitNs, kSuspendNs);
+            }
             __syncwarp();
-            volatile int* never = &never_abort;
-            warp_wait_parity_suspend(all_done, 0, never, kWaitNs, kSuspendNs);
         } else if (warp == kPlanWarp) {
             plan();
         }
@@ -952,6 +1028,27 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
     }
 }
 
+// The map of the keys (w = 0) or values: [page][head][token][dim], boxes of 64 elements of `box`
+// tokens with the 128-byte swizzle.
+template <int D, bool BF>
+bool encode(const Args& A, int w, int box, CUtensorMap& map) {
+    const EncodeFn go = driver_encode();
+    const Keys& K = A.keys;
+    const bool paged = K.table != nullptr;
+    const cuuint64_t tokens = paged ? K.page_size : A.tokens, pages = paged ? K.pages : 1;
+    const cuuint64_t dims[4] = {D, tokens, cuuint64_t(A.kv_heads), pages};
+    auto stride = [](int64_t bytes, cuuint64_t n) { return n > 1 ? cuuint64_t(bytes) : cuuint64_t(16); };  // of one: unused
+    const cuuint64_t strides[3] = {stride(K.token_stride[w], tokens), stride(K.head_stride[w], dims[2]),
+                                   stride(K.page_stride[w], pages)};
+    const cuuint32_t shape[4] = {64, cuuint32_t(box), 1, 1}, steps[4] = {1, 1, 1, 1};
+    for (const cuuint64_t s : strides)
+        if (s == 0) return false;  // rows that share memory
+    return go && pages > 0 &&
+           go(&map, BF ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<char*>(K.pool[w]),
+              dims, strides, shape, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D, class T, bool E4M3>
 w4a4_status run(Args& A, cudaStream_t s) {
     using P = Plan<D>;
@@ -976,13 +1073,17 @@ w4a4_status run(Args& A, cudaStream_t s) {
     if (!(A.parts && least < sms && keys > 4 * kTile)) A.parts = nullptr;
     const int grid = A.parts ? sms : int(std::min(int64_t(sms), most));
     constexpr bool bf16 = std::is_same_v<T, BF16>;
+    // Keys and values by the copy engine, eight rows or more a copy, where pages hold so many side by side.
+    CUtensorMap maps[2] = {};
+    const int box = !A.keys.table ? 32 : A.keys.page_size % 32 == 0 ? 32 : A.keys.page_size % 16 == 0 ? 16 : A.keys.page_size % 8 == 0 ? 8 : 0;
+    A.keys.box = !E4M3 && box > 0 && encode<D, bf16>(A, 0, box, maps[0]) && encode<D, bf16>(A, 1, box, maps[1]) ? box : 0;
     const char* text = !A.lengths ? (bf16 ? "prompt_attention bf16 tokens=%d seqs=%d heads=%d/%d dim=%d stages=%d grid=%d parts=%d"
                                           : "prompt_attention f16 tokens=%d seqs=%d heads=%d/%d dim=%d stages=%d grid=%d parts=%d")
                        : E4M3     ? "chunk_attention e4m3 tokens=%d seqs=%d heads=%d/%d dim=%d stages=%d grid=%d parts=%d"
                        : bf16     ? "chunk_attention bf16 tokens=%d seqs=%d heads=%d/%d dim=%d stages=%d grid=%d parts=%d"
                                   : "chunk_attention f16 tokens=%d seqs=%d heads=%d/%d dim=%d stages=%d grid=%d parts=%d";
     set_dispatch_ints(text, {A.tokens, A.seqs, A.q_heads, A.kv_heads, D, P::kStages, grid, A.parts != nullptr});
-    w4a4_status st = launch<attention_kernel<D, T, E4M3>>(dim3(unsigned(grid)), kThreads, P::kBytes, s, A);
+    w4a4_status st = launch<attention_kernel<D, T, E4M3>>(dim3(unsigned(grid)), kThreads, P::kBytes, s, A, maps[0], maps[1]);
     if (st == W4A4_OK && A.parts) st = launch<join_kernel<D, T, E4M3>>(dim3(unsigned(grid)), 256, 0, s, A);
     return st;
 }

@@ -266,6 +266,22 @@ __device__ __forceinline__ void bulk_g2s(uint32_t dst, const void* src, uint32_t
         : "memory");
 }
 
+// `count` arrivals at once.
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t count) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"(count) : "memory");
+}
+// A box of a 4-D tensor map (coordinates innermost first) into shared memory.
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* map, int x, int y, int z, int w, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];\n" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void prefetch_tensor_map(const void* map) {
+    asm volatile("prefetch.tensormap [%0];\n" ::"l"(map) : "memory");
+}
+
 // ---- tensor memory --------------------------------------------------------
 __device__ __forceinline__ void tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(dst_smem), "r"(ncols)
@@ -349,13 +365,89 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t plane =
 __host__ __device__ constexpr uint32_t idesc_m128_16bit(int n, bool bf16, bool b_mn) {
     return idesc_m128(n) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? 1u << 16 : 0u);
 }
-// kind::f16 with the A operand in tensor memory: lane = row, k = 2 * column + half.
-__device__ __forceinline__ void mma_f16_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
-                                               uint32_t acc) {
+// A row of kind::f16 MMAs in one block, so that their descriptors are sums of an immediate and
+// the first one's low word: left to the compiler, the sums of all of them are kept (and
+// spilled) between the rows, and loading them holds the tensor cores up.  `acc`: whether the
+// first one adds to the accumulator; the others do.
+// STEPS 16-element steps of K of two K-major operands in planes of 128 rows of 128 bytes.
+template <int STEPS>
+__device__ __forceinline__ void mma_f16_rows(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, bool acc) {
+    static_assert(STEPS == 4 || STEPS == 6 || STEPS == 8, "planes of four steps");
+    if constexpr (STEPS == 4)
+        asm volatile(
+            "{\n.reg .pred p, q;\n.reg .b64 a, b;\n.reg .b32 x, y;\nsetp.ne.b32 p, %5, 0;\nsetp.eq.b32 q, 0, 0;\n"
+            "add.u32 x, %1, 0;\nadd.u32 y, %2, 0;\nmov.b64 a, {x, %3};\nmov.b64 b, {y, %3};\n"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n"
+            "add.u32 x, %1, 2;\nadd.u32 y, %2, 2;\nmov.b64 a, {x, %3};\nmov.b64 b, {y, %3};\n"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, q;\n"
+            "add.u32 x, %1, 4;\nadd.u32 y, %2, 4;\nmov.b64 a, {x, %3};\nmov.b64 b, {y, %3};\n"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, q;\n"
+            "add.u32 x, %1, 6;\nadd.u32 y, %2, 6;\nmov.b64 a, {x, %3};\nmov.b64 b, {y, %3};\n"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, q;\n"
+            "}\n" ::"r"(d_tmem), "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(uint32_t(acc))
+            : "memory");
+    else if constexpr (STEPS == 6)
+        asm volatile(
+            "{\n.reg .pred p, q;\n.reg .b64 a, b;\n.reg .b32 x, y;\nsetp.ne.b32 p, %5, 0;\nsetp.eq.b32 q, 0, 0;\n"
+            "add.u32 x, %1, 0;\nadd.u32 y, %2, 0;\nmov.b64 a, {x, %3};\nmov.b64 b, {y, %3};\n"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n"
+            "add.u32 x, %1, 2;\nadd.u32 y, %2, 2;\nmov.b64 a, {x, %3};\nmov.b64 b, {y, %3};\n"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, q;\n"
+            "add.u32 x, %1, 4;\nadd.u32 y, %2, 4;\nmov.b64 a, {x, %3};\nmov.b64 b, {y, %3};\n"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, q;\n"
+            "add.u32 x, %1, 6;\nadd.u32 y, %2, 6;\nmov.b64 a, {x, %3};\nmov.b64 b, {y, %3};\n"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, q;\n"
+            "add.u32 x, %1, 1024;\nadd.u32 y, %2, 1024;\nmov.b64 a, {x, %3};\nmov.b64 b, {y, %3};\n"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, q;\n"
+            "add.u32 x, %1, 1026;\nadd.u32 y, %2, 1026;\nmov.b64 a, {x, %3};\nmov.b64 b, {y, %3};\n"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, q;\n"
+            "}\n" ::"r"(d_tmem), "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(uint32_t(acc))
+            : "memory");
+    else
+        asm volatile(
+            "{\n.reg .pred p, q;\n.reg .b64 a, b;\n.reg .b32 x, y;\nsetp.ne.b32 p, %5, 0;\nsetp.eq.b32 q, 0, 0;\n"
+            "add.u32 x, %1, 0;\nadd.u32 y, %2, 0;\nmov.b64 a, {x, %3};\nmov.b64 b, {y, %3};\n"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n"
+            "add.u32 x, %1, 2;\nadd.u32 y, %2, 2;\nmov.b64 a, {x, %3};\nmov.b64 b, {y, %3};\n"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, q;\n"
+            "add.u32 x, %1, 4;\nadd.u32 y, %2, 4;\nmov.b64 a, {x, %3};\nmov.b64 b, {y, %3};\n"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, q;\n"
+            "add.u32 x, %1, 6;\nadd.u32 y, %2, 6;\nmov.b64 a, {x, %3};\nmov.b64 b, {y, %3};\n"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, q;\n"
+            "add.u32 x, %1, 1024;\nadd.u32 y, %2, 1024;\nmov.b64 a, {x, %3};\nmov.b64 b, {y, %3};\n"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, q;\n"
+            "add.u32 x, %1, 1026;\nadd.u32 y, %2, 1026;\nmov.b64 a, {x, %3};\nmov.b64 b, {y, %3};\n"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, q;\n"
+            "add.u32 x, %1, 1028;\nadd.u32 y, %2, 1028;\nmov.b64 a, {x, %3};\nmov.b64 b, {y, %3};\n"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, q;\n"
+            "add.u32 x, %1, 1030;\nadd.u32 y, %2, 1030;\nmov.b64 a, {x, %3};\nmov.b64 b, {y, %3};\n"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, q;\n"
+            "}\n" ::"r"(d_tmem), "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(uint32_t(acc))
+            : "memory");
+}
+// The A operand 128 elements of K in tensor memory (lane = row, k = 2 * column + half), B an
+// MN-major operand of 128 rows.
+__device__ __forceinline__ void mma_f16_tmem_a_rows(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, uint32_t hi, uint32_t idesc,
+                                                    bool acc) {
     asm volatile(
-        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
+        "{\n.reg .pred p, q;\n.reg .b64 b;\n.reg .b32 x, y;\nsetp.ne.b32 p, %5, 0;\nsetp.eq.b32 q, 0, 0;\n"
+        "add.u32 x, %1, 0;\nadd.u32 y, %2, 0;\nmov.b64 b, {y, %3};\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, p;\n"
+        "add.u32 x, %1, 8;\nadd.u32 y, %2, 128;\nmov.b64 b, {y, %3};\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, q;\n"
+        "add.u32 x, %1, 16;\nadd.u32 y, %2, 256;\nmov.b64 b, {y, %3};\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, q;\n"
+        "add.u32 x, %1, 24;\nadd.u32 y, %2, 384;\nmov.b64 b, {y, %3};\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, q;\n"
+        "add.u32 x, %1, 32;\nadd.u32 y, %2, 512;\nmov.b64 b, {y, %3};\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, q;\n"
+        "add.u32 x, %1, 40;\nadd.u32 y, %2, 640;\nmov.b64 b, {y, %3};\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, q;\n"
+        "add.u32 x, %1, 48;\nadd.u32 y, %2, 768;\nmov.b64 b, {y, %3};\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, q;\n"
+        "add.u32 x, %1, 56;\nadd.u32 y, %2, 896;\nmov.b64 b, {y, %3};\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, q;\n"
+        "}\n" ::"r"(d_tmem), "r"(a_tmem), "r"(b), "r"(hi), "r"(idesc), "r"(uint32_t(acc))
         : "memory");
 }
 // Arrive on `bar` once every tcgen05 operation issued so far by this thread completes.

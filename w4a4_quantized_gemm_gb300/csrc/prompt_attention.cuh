@@ -108,7 +108,7 @@ struct Plan {
     static constexpr int kMl = kQ + kStages * kStage;           // [2][128] maxima, then sums, of the streams
     static constexpr int kUnits = kMl + 2 * 2 * kTile * 4;      // [2] units
     static constexpr int kBars = kUnits + 2 * int(sizeof(Unit));
-    static constexpr int kFlags = kBars + (2 * kStages + 17) * 8;
+    static constexpr int kFlags = kBars + (2 * kStages + 22) * 8;
     static constexpr int kLost = kFlags + 16;                   // [kLostTiles][4] keys of a tile on pages outside the pool
     static constexpr int kBytes = kLost + kLostTiles * 16;
     // Copies are at most the ring ahead of the scores' products, and those two tiles ahead of
@@ -126,6 +126,34 @@ __device__ __forceinline__ float ex2(float x) {  // 2 ulp; 2^-inf = 0
     return y;
 }
 
+// The same and its neighbours in the order in which they are written.
+__device__ __forceinline__ uint64_t ex2_in_order(uint64_t x) {
+    uint64_t y;
+    asm volatile(
+        "{\n.reg .f32 a, b;\nmov.b64 {a, b}, %1;\nex2.approx.ftz.f32 a, a;\nex2.approx.ftz.f32 b, b;\nmov.b64 %0, {a, b};\n}\n"
+        : "=l"(y)
+        : "l"(x));
+    return y;
+}
+__device__ __forceinline__ uint64_t ffma2_in_order(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm volatile("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t fadd2_in_order(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm volatile("add.rn.f32x2 %0, %1, %2;\n" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+template <class T>
+__device__ __forceinline__ uint32_t down_in_order(float a, float b) {  // T::down
+    uint32_t w;
+    if constexpr (std::is_same_v<T, BF16>)
+        asm volatile("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(w) : "f"(b), "f"(a));
+    else
+        asm volatile("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(w) : "f"(b), "f"(a));
+    return w;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -392,26 +420,28 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
     const uint32_t more = bars + 16 * P::kStages;
     const uint32_t q_full = more, q_free = more + 8, o_free = more + 16, pv_done = more + 24, all_done = more + 32;
     auto s_full = [&](int i) { return more + 40 + 8 * i; };
-    auto p_full = [&](int i) { return more + 56 + 8 * i; };
-    auto o_full = [&](int i) { return more + 72 + 8 * i; };
-    auto u_full = [&](int i) { return more + 88 + 8 * i; };
-    auto u_free = [&](int i) { return more + 104 + 8 * i; };
-    const uint32_t ml_full = more + 120, ml_free = more + 128;
+    auto p_full = [&](int i) { return more + 56 + 8 * i; };  // 2 * buffer + half of the keys
+    auto o_full = [&](int i) { return more + 88 + 8 * i; };
+    auto u_full = [&](int i) { return more + 104 + 8 * i; };
+    auto u_free = [&](int i) { return more + 120 + 8 * i; };
+    const uint32_t ml_full = more + 136, ml_free = more + 144;
+    auto turn = [&](int i) { return more + 152 + 8 * i; };
     Unit* units = reinterpret_cast<Unit*>(smem + P::kUnits);
     volatile uint32_t* lost = reinterpret_cast<volatile uint32_t*>(smem + P::kLost);
 
     if (tid == 0) {
         abort_flag = (base & 1023u) != 0;  // the swizzle's atoms start on 1024-byte boundaries
         never_abort = 0;
-        for (int s = 0; s < P::kStages; ++s) mbar_init(full(s), kCopyArrivals * kCopyWarps), mbar_init(empty(s), 1);
-        mbar_init(q_full, kCopyThreads), mbar_init(q_free, 1);
-        mbar_init(o_free, kSoftmaxWarps), mbar_init(pv_done, 1), mbar_init(all_done, 1);
+        for (int s = 0; s < P::kStages; ++s) mbar_init(full(s), kCopyArrivals * kCopyWarps), mbar_init(empty(s), 2);
+        mbar_init(q_full, kCopyThreads), mbar_init(q_free, 2);
+        mbar_init(o_free, kSoftmaxWarps), mbar_init(pv_done, 1), mbar_init(all_done, P::kStreams);
         mbar_init(ml_full, kSoftmaxWarps), mbar_init(ml_free, kSoftmaxWarps);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(s_full(i), 1), mbar_init(p_full(i), 4), mbar_init(o_full(i), 1);
-            mbar_init(u_full(i), 1), mbar_init(u_free(i), kSoftmaxWarps + kCopyWarps + 1);
+            mbar_init(s_full(i), 1), mbar_init(p_full(2 * i), 4), mbar_init(p_full(2 * i + 1), 4), mbar_init(o_full(i), 1);
+            mbar_init(turn(i), 1), mbar_init(u_full(i), 1), mbar_init(u_free(i), kSoftmaxWarps + kCopyWarps + P::kStreams);
         }
         fence_mbar_init();
+        mbar_arrive(turn(0));  // the first turn is the first stream's
     }
     if (warp == kMmaWarp) tmem_alloc(smem_u32(&tmem_base), 512);
     tc_fence_before();
@@ -619,42 +649,24 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
         }
     };
 
-    // One thread issues the products, and every instruction of it between the arrival of the
-    // probabilities and the next scores delays them: descriptors are sums of a few words,
-    // stages are counted, nothing is waited for twice.
-    auto multiply = [&]() {
+    // The products of a stream, issued by one thread: the queue of the tensor cores holds two or
+    // three, so what this thread does between the arrival of the probabilities and the next
+    // scores leaves them idle, but for the other stream's.  With both streams' products from one
+    // thread 8192 tokens of 32 heads of 128 take 450 us, and with descriptors that the compiler
+    // sums up 690.
+    auto multiply = [&](const int stream) {
         constexpr uint32_t kQk = idesc_m128_16bit(kTile, BF, false);
         constexpr uint32_t kPv = idesc_m128_16bit(P::kDs, BF, true);
+        constexpr int kAhead = P::kStreams == 1 ? 2 : 1;  // tiles whose scores are under way
         // descriptors' low words (their high words are alike)
         const uint32_t keys0 = uint32_t(sdesc_sw128(ring)), values0 = uint32_t(sdesc_sw128(ring, kTile * 128));
         const uint32_t q0 = uint32_t(sdesc_sw128(base)), hi = uint32_t(sdesc_sw128(0) >> 32);
-        uint32_t st = 0, phase = 0;  // the stage that comes next, and its barrier's parity
-        uint32_t n_o = 0, p_phase = 0;  // units with an output; bit i: the parity of p_full(i)
-        uint32_t q_phase = 0;
+        uint32_t stages = 0;                            // before this unit
+        uint32_t turns = 0, n_o = 0, p_phase = 0, q_phase = 0;  // units with an output; bit i: the parity of p_full(i, .)
         auto wait1 = [&](uint32_t bar, uint32_t parity) {
             if (wait_parity_suspend(bar, parity, abort, kWaitNs, kSuspendNs)) return true;
             *abort = 1;
             return false;
-        };
-        auto ready = [&](uint32_t s, uint32_t ph) {
-            if (!wait1(full(s), ph)) return false;
-            if (!E4M3) fence_proxy_async_smem();  // the copies went through the generic proxy
-            return true;
-        };
-        auto next_stage = [&]() {
-            if (++st == P::kStages) st = 0, phase ^= 1;
-        };
-        auto scores = [&](int buf, uint32_t q, uint32_t k, bool more) {
-            mma_f16_rows<P::kDs / 16>(tmem + P::scores(buf), q, k, hi, kQk, more);
-        };
-        auto output = [&](int stream, int buf, int half, uint32_t v, bool more) {
-            mma_f16_tmem_a_rows(tmem + P::output(stream) + half * P::kDs, tmem + P::scores(buf), v, hi, kPv, more);
-        };
-        auto wait_p = [&](int buf) {
-            const bool ok = wait1(p_full(buf), p_phase >> buf & 1);
-            p_phase ^= 1u << buf;
-            tc_fence_after();
-            return ok;
         };
         for (uint32_t n = 0;; ++n) {
             const int i = n & 1;
@@ -665,85 +677,103 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
             mbar_arrive(u_free(i));
             if (!live) return;
             if (tiles == 0) continue;
+            // this stream's tiles: `first`, `first` + `step`, ...
+            const int first = P::kStreams == 2 && !shared ? stream : 0, step = P::kStreams == 2 && !shared ? 2 : 1;
+            const int mine = shared ? (stream ? tiles : tiles0) : (tiles + step - 1 - first) / step;
+            // where the copies of a tile's keys (values) are in their order
+            auto keys_at = [&](int t) { return stages + P::kHalves * (shared ? 2 * t : max(0, 2 * t - 1)); };
+            auto values_at = [&](int t) {
+                return stages + P::kHalves * (shared || t == tiles - 1 ? 2 * t + 1 : 2 * t + 2);
+            };
+            auto ready = [&](uint32_t at) {
+                if (!wait1(full(at % P::kStages), at / P::kStages & 1)) return false;
+                if (!E4M3) fence_proxy_async_smem();  // copies of some went through the generic proxy
+                return true;
+            };
+            auto release = [&](uint32_t at) {  // once by each stream
+                mma_commit(empty(at % P::kStages));
+                if (!shared) mbar_arrive(empty(at % P::kStages));
+            };
             if (!wait1(q_full, q_phase)) return;
             q_phase ^= 1;
             fence_proxy_async_smem();
-            bool free = n_o == 0;  // the last unit's output has been read
-            auto wait_o = [&]() { return free || (free = wait1(o_free, (n_o - 1) & 1)); };
-            if (shared) {
-                // both halves of the rows on a tile: P V of one, Q K of the next tile, then the other half's
-                if (!ready(st, phase)) return;
-                if (tiles0 > 0) {
-                    scores(0, q0, keys0 + st * (P::kStage >> 4), false);
-                    mma_commit(s_full(0));
-                }
-                scores(1, q0 + (P::kQTile >> 4), keys0 + st * (P::kStage >> 4), false);
-                mma_commit(s_full(1));
-                mma_commit(empty(st));
-                if (tiles == 1) mma_commit(q_free);
-                next_stage();
-                for (int t = 0; t < tiles; ++t) {
-                    const uint32_t v = st, v_phase = phase;
-                    next_stage();
-                    const uint32_t k = st, k_phase = phase;
-                    const bool more = t + 1 < tiles;
-                    if (more) next_stage();
-                    const uint32_t vd = values0 + v * (P::kStage >> 4), kd = keys0 + k * (P::kStage >> 4);
-                    if (!ready(v, v_phase)) return;
-                    if (more && !ready(k, k_phase)) return;
-                    if (t < tiles0) {
-                        if (!wait_p(0) || !wait_o()) return;
-                        output(0, 0, 0, vd, t > 0);
-                        if (t + 1 < tiles0) {
-                            scores(0, q0, kd, false);
-                            mma_commit(s_full(0));
-                        } else {
-                            mma_commit(o_full(0));
-                        }
-                    }
-                    if (!wait_p(1) || !wait_o()) return;
-                    output(P::kStreams - 1, 1, 0, vd, t > 0);
-                    if (more) {
-                        scores(1, q0 + (P::kQTile >> 4), kd, false);
-                        mma_commit(s_full(1));
-                        mma_commit(empty(v));
-                        mma_commit(empty(k));
-                        if (t + 2 == tiles) mma_commit(q_free);
-                    } else {
-                        mma_commit(o_full(1));
-                        mma_commit(empty(v));
-                    }
-                }
-            } else {
-                // tiles in turn, two under way: P V of one, Q K of the second after it
-                for (int t = -2; t < tiles; ++t) {
-                    const int buf = t & 1, stream = P::kStreams == 2 ? buf : 0;
-                    if (t >= 0) {
+            const uint32_t q = q0 + (shared && stream ? P::kQTile >> 4 : 0);
+            auto keys_ready = [&](int x) {  // of this stream's x-th tile
+                const uint32_t at = keys_at(first + x * step);
+                return ready(at) && (P::kHalves == 1 || ready(at + 1));
+            };
+            auto scores = [&](int x) {
+                const int buf = P::kStreams == 1 ? x & 1 : stream;
+                const uint32_t at = keys_at(first + x * step);
 #pragma unroll
-                        for (int half = 0; half < P::kHalves; ++half) {
-                            if (!ready(st, phase)) return;
-                            if (half == 0 && (!wait_p(buf) || !wait_o())) return;
-                            output(stream, buf, half, values0 + st * (P::kStage >> 4), t >= P::kStreams);
-                            mma_commit(empty(st));
-                            next_stage();
-                        }
-                        if constexpr (P::kStreams == 1) mma_commit(pv_done);
-                        if (t + P::kStreams >= tiles) mma_commit(o_full(stream));
-                    }
-                    if (t + 2 < tiles) {
-#pragma unroll
-                        for (int half = 0; half < P::kHalves; ++half) {
-                            if (!ready(st, phase)) return;
-                            scores(buf, q0 + half * (P::kStage >> 4), keys0 + st * (P::kStage >> 4), half > 0);
-                            if (half == P::kHalves - 1) mma_commit(s_full(buf));
-                            mma_commit(empty(st));
-                            next_stage();
-                        }
-                        if (t + 3 == tiles) mma_commit(q_free);
-                    }
+                for (int half = 0; half < P::kHalves; ++half) {
+                    mma_f16_rows<P::kDs / 16>(tmem + P::scores(buf), q + half * (P::kStage >> 4),
+                                              keys0 + (at + half) % P::kStages * (P::kStage >> 4), hi, kQk, half > 0);
                 }
+                mma_commit(s_full(buf));
+            };
+            auto release_keys = [&](int x) {
+                const uint32_t at = keys_at(first + x * step);
+#pragma unroll
+                for (int half = 0; half < P::kHalves; ++half) release(at + half);
+                if (x == mine - 1) {
+                    mma_commit(q_free);
+                    if (P::kStreams == 1) mbar_arrive(q_free);
+                }
+            };
+            if (mine == 0) mbar_arrive(q_free);
+            // The streams take turns, so that the products of one end before the other's begin (side
+            // by side each takes twice as long, and then both streams wait).  Both go through as many.
+            const int other = P::kStreams == 1 ? 0 : shared ? (stream ? tiles0 : tiles) : (tiles + stream) / 2;
+            auto my_turn = [&]() { return P::kStreams == 1 || (wait1(turn(stream), turns & 1) && ++turns); };
+            auto pass = [&]() {
+                if (P::kStreams == 2) mbar_arrive(turn(stream ^ 1));
+            };
+            for (int x = 0; x < min(kAhead, mine); ++x)
+                if (!keys_ready(x)) return;
+            if (!my_turn()) return;
+            for (int x = 0; x < min(kAhead, mine); ++x) scores(x);
+            pass();
+            for (int x = 0; x < min(kAhead, mine); ++x) release_keys(x);
+            for (int x = 0; x < max(mine, other); ++x) {
+                if (x >= mine) {
+                    if (!my_turn()) return;
+                    pass();
+                    continue;
+                }
+                const int buf = P::kStreams == 1 ? x & 1 : stream;
+                const uint32_t at = values_at(first + x * step);
+                for (int half = 0; half < P::kHalves; ++half)
+                    if (!ready(at + half)) return;
+                if (x + kAhead < mine && !keys_ready(x + kAhead)) return;
+                if (x == 0 && n_o > 0 && !wait1(o_free, (n_o - 1) & 1)) return;  // the last unit's output has been read
+#pragma unroll
+                for (int part = 0; part < 2; ++part) {
+                    if (!wait1(p_full(2 * buf + part), p_phase >> buf & 1)) return;
+                    if (part == 0 && !my_turn()) return;
+                    tc_fence_after();
+#pragma unroll
+                    for (int half = 0; half < P::kHalves; ++half)
+                        mma_f16_tmem_a_rows(tmem + P::output(stream) + half * P::kDs, tmem + P::scores(buf) + 32 * part,
+                                            values0 + (at + half) % P::kStages * (P::kStage >> 4) + part * (64 * 128 >> 4), hi,
+                                            kPv, x > 0 || part > 0);
+                }
+                p_phase ^= 1u << buf;
+                if constexpr (P::kStreams == 1) mma_commit(pv_done);
+                if (x == mine - 1) mma_commit(o_full(stream));
+                if (x + kAhead < mine) scores(x + kAhead);
+                pass();
+                if (x + kAhead < mine) release_keys(x + kAhead);
+                for (int half = 0; half < P::kHalves; ++half) release(at + half);
+            }
+            for (int t = mine; shared && t < tiles; ++t) {  // tiles of the other stream alone
+                if (!ready(keys_at(t))) return;
+                mbar_arrive(empty(keys_at(t) % P::kStages));
+                if (!ready(values_at(t))) return;
+                mbar_arrive(empty(values_at(t) % P::kStages));
             }
             ++n_o;
+            stages += 2 * P::kHalves * tiles;
         }
     };
 
@@ -751,7 +781,7 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
         const int stream = warp >> 2, row = tid & 127;
         const uint32_t lanes = uint32_t(warp & 3) << 21;  // this warp's lanes of tensor memory
         float* ml = reinterpret_cast<float*>(smem + P::kMl);
-        uint32_t ns[2] = {0, 0}, n_out[2] = {0, 0}, n_tile = 0, n_ml = 0;
+        uint32_t s_phase = 0, o_phase = 0, n_tile = 0, n_ml = 0;  // bit i: the parity of s_full(i), o_full(i)
         for (uint32_t n = 0;; done_with(n++)) {
             const Unit* const unit_n = unit(n);
             if (!unit_n) return;
@@ -759,102 +789,141 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
             const bool shared = P::kStreams == 2 && U.shared;
             // scores go by |scale|, keys' scale and log2 e; a negative scale turns their sign, and
             // a scale of zero makes them zero
-            float scale2 = A.scale * 1.44269504088896341f, v_scale = 1.f, flip = 1.f;
+            float scale2 = A.scale * 1.44269504088896341f, flip = 1.f;
             if (E4M3 && A.keys.scale[0]) scale2 *= A.keys.scale[0][U.head];
-            if (E4M3 && A.keys.scale[1]) v_scale = A.keys.scale[1][U.head];
             const float signed2 = scale2;
             if (!(scale2 > 0.f)) {
                 flip = scale2 < 0.f ? -1.f : scale2 == 0.f ? 0.f : scale2;  // NaN stays
                 scale2 = scale2 < 0.f ? -scale2 : 1.f;
             }
-            const int local = (shared ? stream * kTile : 0) + row;
-            const bool valid = local < U.rows;
-            const int flat = U.row0 + local, token = A.by_group.quotient(valid ? flat : 0);
             int lo = 0, hi = INT32_MAX;
-            if (valid) sees(A, U.first + token, U.length, lo, hi);
-            const bool idle = (local & ~31) >= U.rows;  // none of the warp's rows is one
+            if (const int local = (shared ? stream * kTile : 0) + row; local < U.rows)
+                sees(A, U.first + A.by_group.quotient(U.row0 + local), U.length, lo, hi);
+            const bool idle = (shared ? stream * kTile : 0) + (row & ~31) >= U.rows;  // none of the warp's rows is one
             const int mine = P::kStreams == 1 ? (stream == 0 ? U.tiles : 0)
                              : shared         ? (stream == 0 ? U.tiles0 : U.tiles)
                                               : (U.tiles + 1 - stream) / 2;
             float top = -INFINITY, sum = 0.f;  // what is subtracted (of the scores as they come), and the sum
-            for (int i = 0; i < mine; ++i) {
-                const int tile = P::kStreams == 1 || shared ? i : 2 * i + stream;
-                const int buf = P::kStreams == 1 ? i & 1 : stream;
-                if (!wait(s_full(buf), ns[buf]++ & 1)) return;
-                tc_fence_after();
-                const uint32_t at = tmem + lanes + P::scores(buf);
-                if (!idle) {
-                    float s[kTile];
+            // The scores of the stream's i-th tile into probabilities.  They are loaded twice, once for
+            // their maximum and once, half a tile at a time, for their powers: kept in between they
+            // and their results were moved and spilled, 340 instructions of 900 for a warp's tile.
+            // `seen`: true, or a function of the number of a key in the tile: 32 bits from that one on.
+            auto probabilities = [&](auto seen, uint32_t at, int buf, int i) {
+                constexpr bool kAll = std::is_same_v<decltype(seen), bool>;
+                float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int c = 0; c < kTile; c += 32) tmem_ld32_at(at + c, s + c);
+                for (int part = 0; part < 2; ++part) {
+                    float s[64];
+                    tmem_ld32_at(at + 64 * part, s);
+                    tmem_ld32_at(at + 64 * part + 32, s + 32);
                     tmem_wait_ld();
                     if (flip != 1.f) {
 #pragma unroll
-                        for (int c = 0; c < kTile; ++c) s[c] *= flip;
+                        for (int c = 0; c < 64; ++c) s[c] *= flip;
                     }
-                    const int j0 = U.key0 + tile * kTile;
-                    if (!__all_sync(0xffffffffu, lo <= j0 && hi >= j0 + kTile)) {
-                        const int a = lo - j0, b = hi - j0;
+                    if constexpr (!kAll) {
+                        const uint32_t bits[2] = {seen(64 * part), seen(64 * part + 32)};
 #pragma unroll
-                        for (int c = 0; c < kTile; ++c) s[c] = c >= a && c < b ? s[c] : -INFINITY;
+                        for (int c = 0; c < 64; ++c) s[c] = bits[c / 32] >> (c % 32) & 1 ? s[c] : -INFINITY;
                     }
-                    if (A.keys.table) {
-                        const volatile uint32_t* bad = lost + (n_tile + tile) % kLostTiles * 4;
-                        const uint32_t bits[4] = {bad[0], bad[1], bad[2], bad[3]};
-                        if ((bits[0] | bits[1] | bits[2] | bits[3]) != 0) {
 #pragma unroll
-                            for (int c = 0; c < kTile; ++c) s[c] = bits[c / 32] >> (c % 32) & 1 ? -INFINITY : s[c];
-                        }
-                    }
-                    float m[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-                    for (int c = 4; c + 8 <= kTile; c += 8)
+                    for (int c = 0; c < 64; c += 8)
 #pragma unroll
                         for (int k = 0; k < 4; ++k) m[k] = max3(m[k], s[c + k], s[c + 4 + k]);
-                    const float most = fmaxf(max3(max3(m[0], m[1], m[2]), m[3], fmaxf(s[124], s[125])), fmaxf(s[126], s[127]));
-                    const bool renew = (most - top) * scale2 > kSlack;
-                    if (__any_sync(0xffffffffu, renew)) {
-                        // what is there so far was taken relative to the old maximum
-                        const float by = renew ? ex2((top - most) * scale2) : 1.f;
-                        if (renew) top = most;
-                        sum *= by;
-                        if (i > 0) {
-                            if constexpr (P::kStreams == 1)  // the product before this one, still under way
-                                if (!wait(pv_done, (n_tile + i - 1) & 1)) return;
-                            tc_fence_after();
+                }
+                const float most = fmaxf(max3(m[0], m[1], m[2]), m[3]);
+                const bool renew = i == 0 || (most - top) * scale2 > kSlack;
+                if (__any_sync(0xffffffffu, renew)) {
+                    // what is there so far was taken relative to the old maximum
+                    const float by = i == 0 ? 0.f : renew ? ex2((top - most) * scale2) : 1.f;
+                    if (renew) top = most;
+                    sum = i == 0 ? 0.f : sum * by;
+                    if (i > 0) {
+                        if constexpr (P::kStreams == 1)  // the product before this one, still under way
+                            if (!wait(pv_done, (n_tile + i - 1) & 1)) return false;
+                        tc_fence_after();
+                        const uint32_t o_at = tmem + lanes + P::output(P::kStreams == 1 ? 0 : stream);
 #pragma unroll 1
-                            for (int c = 0; c < D; c += 16) {
-                                float o[16];
-                                tmem_ld16(tmem + lanes + P::output(P::kStreams == 1 ? 0 : stream) + c, o);
-                                tmem_wait_ld();
+                        for (int c = 0; c < D; c += 32) {
+                            float o[32];
+                            tmem_ld32(o_at + c, o);
+                            tmem_wait_ld();
 #pragma unroll
-                                for (int k = 0; k < 16; ++k) o[k] *= by;
-                                tmem_st16(tmem + lanes + P::output(P::kStreams == 1 ? 0 : stream) + c, o);
+                            for (int k = 0; k < 32; ++k) o[k] *= by;
+                            tmem_st32(o_at + c, o);
+                        }
+                    }
+                }
+                const float ref = (top == -INFINITY ? 0.f : top * scale2) - kLift;
+                const uint64_t by2 = f2_pack(signed2, signed2), less = f2_pack(-ref, -ref);
+                uint64_t sums[2] = {0, 0};
+#pragma unroll
+                for (int part = 0; part < 2; ++part) {
+                    float s[64];
+                    tmem_ld32_at(at + 64 * part, s);
+                    tmem_ld32_at(at + 64 * part + 32, s + 32);
+                    tmem_wait_ld();
+                    // Pairs in a fixed order, each a few steps behind the last: ordered by the compiler
+                    // the sums come last, with all powers kept until then.
+                    uint32_t p[32], bits[2] = {0, 0};
+                    if constexpr (!kAll) bits[0] = seen(64 * part), bits[1] = seen(64 * part + 32);
+                    uint64_t x[32], e[32];
+#pragma unroll
+                    for (int k = 0; k < 32 + 6; ++k) {
+                        if (k < 32) {
+                            x[k] = ffma2_in_order(f2_pack(s[2 * k], s[2 * k + 1]), by2, less);
+                            if constexpr (!kAll) {
+                                const float2 y = f2_unpack(x[k]);
+                                x[k] = f2_pack(bits[k / 16] >> (2 * k % 32) & 1 ? y.x : -INFINITY,
+                                               bits[k / 16] >> (2 * k % 32 + 1) & 1 ? y.y : -INFINITY);
                             }
                         }
-                    }
-                    const float ref = (top == -INFINITY ? 0.f : top * scale2) - kLift;
-                    const uint64_t by2 = f2_pack(scale2, scale2), less = f2_pack(-ref, -ref);
-                    uint64_t sums[2] = {0, 0};
-#pragma unroll
-                    for (int c = 0; c < kTile; c += 32) {
-                        uint32_t p[16];
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            const float2 x = f2_unpack(ffma2_b64(f2_pack(s[c + 2 * k], s[c + 2 * k + 1]), by2, less));
-                            const float a = ex2(x.x), b = ex2(x.y);
-                            sums[k & 1] = fadd2_b64(sums[k & 1], f2_pack(a, b));
-                            p[k] = T::down(a, b);
+                        if (k >= 2 && k - 2 < 32) e[k - 2] = ex2_in_order(x[k - 2]);
+                        if (k >= 6) {
+                            sums[k & 1] = fadd2_in_order(sums[k & 1], e[k - 6]);
+                            const float2 y = f2_unpack(e[k - 6]);
+                            p[k - 6] = down_in_order<T>(y.x, y.y);
                         }
-                        tmem_st16_b32(at + c / 2, p);
                     }
-                    const float2 x = f2_unpack(fadd2_b64(sums[0], sums[1]));
-                    sum += x.x + x.y;
+                    tmem_st32_b32(at + 32 * part, p);
                     tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(p_full(2 * buf + part));
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(p_full(buf));
+                const float2 x = f2_unpack(fadd2_b64(sums[0], sums[1]));
+                sum += x.x + x.y;
+                return true;
+            };
+            for (int i = 0; i < mine; ++i) {
+                const int tile = P::kStreams == 1 || shared ? i : 2 * i + stream;
+                const int buf = P::kStreams == 1 ? i & 1 : stream;
+                if (!wait(s_full(buf), s_phase >> buf & 1)) return;
+                s_phase ^= 1u << buf;
+                tc_fence_after();
+                const uint32_t at = tmem + lanes + P::scores(buf);
+                if (!idle) {
+                    // keys [a, b) of the tile are seen, but for those on pages outside the pool
+                    const int a = lo - U.key0 - tile * kTile, b = hi - U.key0 - tile * kTile;
+                    const volatile uint32_t* bad = lost + (n_tile + tile) % kLostTiles * 4;
+                    bool all = a <= 0 && b >= kTile;
+                    if (A.keys.table) all = all && (bad[0] | bad[1] | bad[2] | bad[3]) == 0;
+                    if (__all_sync(0xffffffffu, all)) {
+                        if (!probabilities(true, at, buf, i)) return;
+                    } else {
+                        // of 32 keys from number c, a bit each
+                        auto seen = [&](int c) {
+                            const uint32_t below = b - c >= 32 ? 0xffffffffu : (1u << max(b - c, 0)) - 1;
+                            const uint32_t from = a - c >= 32 ? 0u : 0xffffffffu << max(a - c, 0);
+                            return below & from & (A.keys.table ? ~bad[c / 32] : 0xffffffffu);
+                        };
+                        if (!probabilities(seen, at, buf, i)) return;
+                    }
+                } else {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane < 2) mbar_arrive(p_full(2 * buf + lane));
+                }
             }
             n_tile += U.tiles;
 
@@ -879,10 +948,14 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
                 if (lane == 0) mbar_arrive(ml_free);
                 ++n_ml;
             }
-            if (reads0 && !wait(o_full(0), n_out[0] & 1)) return;
-            if (reads1 && !wait(o_full(1), n_out[1] & 1)) return;
-            n_out[0] += has0, n_out[1] += has1;
+            if (reads0 && !wait(o_full(0), o_phase & 1)) return;
+            if (reads1 && !wait(o_full(1), o_phase >> 1 & 1)) return;
+            o_phase ^= uint32_t(has0) | uint32_t(has1) << 1;
             tc_fence_after();
+            const int local = (shared ? stream * kTile : 0) + row;
+            const bool valid = local < U.rows;
+            const int flat = U.row0 + local, token = A.by_group.quotient(valid ? flat : 0);
+            const float v_scale = E4M3 && A.keys.scale[1] ? A.keys.scale[1][U.head] : 1.f;
             const int e0 = !shared && stream == 1 ? D / 2 : 0, e1 = shared || stream == 1 ? D : D / 2;
             const bool none = sum == 0.f;  // no key, or only scores of -inf
             const float by = U.part >= 0 ? 1.f : none ? 0.f : v_scale / sum;
@@ -951,10 +1024,10 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
     };
 
     if (warp < kSoftmaxWarps) {
-        regs_inc<184>();
+        regs_inc<160>();
         softmax();
     } else if (warp < kSoftmaxWarps + kCopyWarps) {
-        regs_dec<72>();
+        regs_dec<96>();
         copy();
         cp_async_commit();
         cp_async_wait<0>();
@@ -962,10 +1035,10 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
             for (uint32_t i = n_stage > P::kStages ? n_stage - P::kStages : 0; i < n_stage; ++i)
                 warp_wait_parity_suspend(full(i % P::kStages), i / P::kStages & 1, &never_abort, kWaitNs, kSuspendNs);
     } else {
-        regs_dec<72>();
-        if (warp == kMmaWarp) {
+        regs_dec<96>();
+        if (warp == kMmaWarp || (P::kStreams == 2 && warp == kMmaWarp + 2)) {
             if (lane == 0) {
-                multiply();
+                multiply((warp - kMmaWarp) >> 1);
                 // what has been issued ends before its operands and tensor memory go away
                 mma_commit(all_done);
                 wait_parity_suspend(all_done, 0, &never_abort, kWaitNs, kSuspendNs);

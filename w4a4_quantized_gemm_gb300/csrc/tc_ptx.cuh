@@ -425,8 +425,8 @@ __device__ __forceinline__ void mma_f16_rows(uint32_t d_tmem, uint32_t a, uint32
             "}\n" ::"r"(d_tmem), "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(uint32_t(acc))
             : "memory");
 }
-// The A operand 128 elements of K in tensor memory (lane = row, k = 2 * column + half), B an
-// MN-major operand of 128 rows.
+// The A operand 64 elements of K in tensor memory (lane = row, k = 2 * column + half), B an
+// MN-major operand of 64 rows of 128 bytes (a plane).
 __device__ __forceinline__ void mma_f16_tmem_a_rows(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, uint32_t hi, uint32_t idesc,
                                                     bool acc) {
     asm volatile(
@@ -438,14 +438,6 @@ __device__ __forceinline__ void mma_f16_tmem_a_rows(uint32_t d_tmem, uint32_t a_
         "add.u32 x, %1, 16;\nadd.u32 y, %2, 256;\nmov.b64 b, {y, %3};\n"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, q;\n"
         "add.u32 x, %1, 24;\nadd.u32 y, %2, 384;\nmov.b64 b, {y, %3};\n"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, q;\n"
-        "add.u32 x, %1, 32;\nadd.u32 y, %2, 512;\nmov.b64 b, {y, %3};\n"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, q;\n"
-        "add.u32 x, %1, 40;\nadd.u32 y, %2, 640;\nmov.b64 b, {y, %3};\n"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, q;\n"
-        "add.u32 x, %1, 48;\nadd.u32 y, %2, 768;\nmov.b64 b, {y, %3};\n"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, q;\n"
-        "add.u32 x, %1, 56;\nadd.u32 y, %2, 896;\nmov.b64 b, {y, %3};\n"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, q;\n"
         "}\n" ::"r"(d_tmem), "r"(a_tmem), "r"(b), "r"(hi), "r"(idesc), "r"(uint32_t(acc))
         : "memory");
@@ -529,6 +521,11 @@ __device__ __forceinline__ void tmem_st16_b32(uint32_t taddr, const uint32_t (&v
         "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
         "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
+}
+// 32 raw 32-bit words -> 32 lanes x 32 consecutive columns.
+__device__ __forceinline__ void tmem_st32_b32(uint32_t taddr, const uint32_t (&v)[32]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(taddr),
+                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31]));
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 

@@ -43,7 +43,6 @@ constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint32_t kSuspendNs = 20000;
 constexpr int kSoftmaxWarps = 8, kCopyWarps = 4, kMmaWarp = 12, kPlanWarp = 13;
 constexpr int kCopyThreads = 32 * kCopyWarps;
-constexpr int kCopyArrivals = 33;          // of a copying warp at a stage's barrier
 constexpr int kLostTiles = 16;
 constexpr int kMaxParts = 156;             // of a call
 constexpr int kPartFloats = 256 * 130;     // of one: [rows][D] outputs, [256] maxima, [256] sums
@@ -161,6 +160,11 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 
 static __device__ int g_prompt_status = 0;
+
+// Where 16-byte piece c of a row is in a tile of planes of 128 rows of 128 bytes.
+__device__ __forceinline__ uint32_t swizzled(int row, int c) {
+    return (c >> 3) * (kTile * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+}
 
 __device__ __forceinline__ Sequence sequence(const Args& A, int b, bool& bad) {
     Sequence s;
@@ -432,7 +436,9 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
     if (tid == 0) {
         abort_flag = (base & 1023u) != 0;  // the swizzle's atoms start on 1024-byte boundaries
         never_abort = 0;
-        for (int s = 0; s < P::kStages; ++s) mbar_init(full(s), kCopyArrivals * kCopyWarps), mbar_init(empty(s), 2);
+        // a copying warp's lanes arrive when their copies have, and one of them once more: for what the engine
+        // brings, or the warp's other words
+        for (int s = 0; s < P::kStages; ++s) mbar_init(full(s), 33 * kCopyWarps), mbar_init(empty(s), 2);
         mbar_init(q_full, kCopyThreads), mbar_init(q_free, 2);
         mbar_init(o_free, kSoftmaxWarps), mbar_init(pv_done, 1), mbar_init(all_done, P::kStreams);
         mbar_init(ml_full, kSoftmaxWarps), mbar_init(ml_free, kSoftmaxWarps);
@@ -498,154 +504,242 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
         }
     };
 
-    uint32_t n_stage = 0;  // copies begun
-    auto copy = [&]() {
-        const int t = tid - 32 * kSoftmaxWarps, w = t >> 5;
-        constexpr int kSize = E4M3 ? 1 : 2;
-        constexpr int kPieces = P::kDs * kSize / 16;     // of a stage's row
-        constexpr int kQPieces = D * 2 / 16;
+    // ---- queries, keys and values into shared memory
+    uint32_t n_stage = 0, n_q = 0;  // copies of stages begun, units whose queries were copied
+    auto copy_queries = [&](const Unit& U) {
+        if (n_q > 0 && !wait(q_free, (n_q - 1) & 1)) return false;
+        constexpr int kPieces = D * 2 / 16;
+        for (int h = 0; h < (U.shared ? 2 : 1); ++h) {
+            const uint32_t to = base + h * P::kQTile;
+#pragma unroll 4
+            for (int i = 0; i < kPieces; ++i) {
+                const int id = i * kCopyThreads + tid - 32 * kSoftmaxWarps, row = id / kPieces, c = id - row * kPieces;
+                const bool ok = h * kTile + row < U.rows;
+                const int flat = ok ? U.row0 + h * kTile + row : 0, token = A.by_group.quotient(flat), g = flat - token * A.group;
+                const char* src = A.q + 2 * ((U.begin + token) * A.q_token + (U.head * A.group + g) * A.q_head) + 16 * c;
+                cp_async16_zfill(to + swizzled(row, c), src, ok ? 16 : 0);
+            }
+        }
+        cp_async_mbar_arrive_noinc(q_full);
+        ++n_q;
+        return true;
+    };
+    // The place of the next copy in the ring, free to be written.
+    auto next_stage = [&](int& st) {
+        st = n_stage % P::kStages;
+        if (n_stage >= P::kStages && !wait(empty(st), (n_stage / P::kStages - 1) & 1)) return false;
+        ++n_stage;
+        return true;
+    };
+    // Copies go in the order of use: the values of a tile behind the keys of the tile after it
+    // (shared rows) or of the two after it.  copy_tiles(tiles, lag, look, send): look(u) prepares
+    // tile u, send(kv, half, age) copies its keys (age 0) or the values of the tile `age` before.
+    auto copy_tiles = [&](int tiles, int lag, auto look, auto send) {
+        for (int u = 0; u < tiles + lag; ++u) {
+            look(u);
+#pragma unroll 1
+            for (int half = 0; u >= lag && half < P::kHalves; ++half)
+                if (!send(1, half, lag, u - lag)) return false;
+#pragma unroll 1
+            for (int half = 0; u < tiles && half < P::kHalves; ++half)
+                if (!send(0, half, 0, u)) return false;
+        }
+        return true;
+    };
+    auto lag_of = [&](const Unit& U) { return P::kStreams == 2 && U.shared ? 1 : 2; };
+
+    // By the copy engine, each warp 32 rows of a tile, a box of K.box of them a lane; boxes that
+    // are not all there by the warp's own loads.  (One warp for all of them has fewer instructions
+    // but sends small boxes more slowly: pages of 24, D = 256 326 us and 180.)
+    auto copy_boxes = [&]() {
         const Keys& K = A.keys;
-        uint32_t n_q = 0, n_tile = 0;
+        const int box = K.box, boxes = 32 / box, w = warp - kSoftmaxWarps, my = 32 * w + lane * box;
+        const uint32_t all = (1u << boxes) - 1;
+        uint32_t n_tile = 0;
         for (uint32_t n = 0;; done_with(n++)) {
-            const Unit* const unit_n = unit(n);
-            if (!unit_n) return;
-            const Unit U = *unit_n;
-            if (U.tiles == 0) continue;
-            // Page and slot of the key that this lane looks up: key 32 w + lane of a tile.
-            int page = -1, slot = 0;
+            const Unit* const U = unit(n);
+            if (!U) return;
+            if (U->tiles == 0) continue;
+            const int key0 = U->key0, end = U->end, tiles = U->tiles, begin = U->begin, head = U->head;
+            const int64_t table = U->b * K.table_stride;
+            int page = 0, slot = 0;  // of this lane's box in the next tile
             auto look_up = [&](int tile) {
-                const int j = U.key0 + tile * kTile + 32 * w + lane;
-                page = -1;
-                if (tile < U.tiles && j < U.end) {
+                const int j = key0 + tile * kTile + my;
+                slot = begin + j;
+                if (K.table && lane < boxes && tile < tiles && j < end) {
                     const int p = K.by_page.quotient(j);
                     slot = j - p * K.page_size;
-                    page = K.table[U.b * K.table_stride + p];
+                    page = K.table[table + p];
+                }
+            };
+            look_up(0);
+            if (!copy_queries(*U)) return;
+            // of a tile and the two before it: this lane's page and slot, boxes that are all there, and that
+            // are in part
+            int pages[3] = {}, slots[3] = {};
+            uint32_t whole[3] = {}, some[3] = {};
+            auto look = [&](int u) {
+#pragma unroll
+                for (int k = 2; k > 0; --k)
+                    pages[k] = pages[k - 1], slots[k] = slots[k - 1], whole[k] = whole[k - 1], some[k] = some[k - 1];
+                if (u >= tiles) return;
+                const int j = key0 + u * kTile + my;
+                const bool in = lane < boxes && j < end, good = in && (!K.table || (page >= 0 && page < K.pages));
+                some[0] = __ballot_sync(0xffffffffu, good), whole[0] = __ballot_sync(0xffffffffu, good && j + box <= end);
+                pages[0] = page, slots[0] = slot;
+                if (K.table) {
+                    const uint32_t bad = __ballot_sync(0xffffffffu, in && !good);
+                    if (lane == 0) {
+                        uint32_t word = 0;
+                        for (int k = 0; bad != 0 && k < boxes; ++k)
+                            if (bad >> k & 1) word |= (0xffffffffu >> (32 - box)) << k * box;
+                        lost[(n_tile + u) % kLostTiles * 4 + w] = word;
+                        if (bad) atomicExch(&g_prompt_status, int(W4A4_ERR_INDEX));
+                    }
+                    look_up(u + 1);
+                } else {
+                    slot += kTile;
+                }
+            };
+            auto send = [&](int kv, int half, int age, int tile) {
+                int st;
+                if (!next_stage(st)) return false;
+                const uint32_t to = ring + st * P::kStage;
+                const uint32_t there = age == 0 ? whole[0] : age == 1 ? whole[1] : whole[2];
+                const int pg = age == 0 ? pages[0] : age == 1 ? pages[1] : pages[2];
+                const int sl = age == 0 ? slots[0] : age == 1 ? slots[1] : slots[2];
+                if (lane == 0) mbar_expect_tx(full(st), __popc(there) * box * 128 * P::kPlanes);
+                if (there >> lane & 1)
+                    for (int plane = 0; plane < P::kPlanes; ++plane)
+                        tma_load_4d(to + plane * (kTile * 128) + my * 128, kv ? &v_map : &k_map, half * P::kDs + 64 * plane, sl,
+                                    head, K.table ? pg : 0, full(st));
+                if (there != all) {
+                    const uint32_t s = age == 0 ? some[0] : age == 1 ? some[1] : some[2];
+                    const char* pool = K.pool[kv] + int64_t(head) * K.head_stride[kv] + half * P::kDs * 2;
+                    constexpr int kPieces = P::kDs * 2 / 16;
+                    for (int b = 0; b < boxes; ++b) {
+                        if (there >> b & 1) continue;
+                        const int have = s >> b & 1 ? end - (key0 + tile * kTile + 32 * w + b * box) : 0;
+                        const int p = __shfl_sync(0xffffffffu, pg, b), y = __shfl_sync(0xffffffffu, sl, b);
+                        const char* from = have > 0 ? pool + (K.table ? p * K.page_stride[kv] : 0) + int64_t(y) * K.token_stride[kv] : pool;
+                        for (int i = lane; i < box * kPieces; i += 32) {
+                            const int r = i / kPieces, c = i - r * kPieces;
+                            cp_async16_zfill(to + swizzled(32 * w + b * box + r, c), r < have ? from + int64_t(r) * K.token_stride[kv] + 16 * c : pool,
+                                             r < have ? 16 : 0);
+                        }
+                    }
+                }
+                cp_async_mbar_arrive_noinc(full(st));
+                return true;
+            };
+            if (!copy_tiles(tiles, lag_of(*U), look, send)) return;
+            n_tile += tiles;
+        }
+    };
+
+    // By loads of four warps, 32 rows of a tile each: pages of any size, E4M3 rows turned into
+    // 16-bit ones.
+    auto copy_rows = [&]() {
+        constexpr int kSize = E4M3 ? 1 : 2;
+        constexpr int kPieces = P::kDs * kSize / 16;  // of a stage's row
+        const Keys& K = A.keys;
+        const int w = warp - kSoftmaxWarps;
+        uint32_t n_tile = 0;
+        for (uint32_t n = 0;; done_with(n++)) {
+            const Unit* const U = unit(n);
+            if (!U) return;
+            if (U->tiles == 0) continue;
+            const int key0 = U->key0, end = U->end, tiles = U->tiles, begin = U->begin, head = U->head;
+            const int64_t table = U->b * K.table_stride;
+            int page = -1, slot = 0;  // of key 32 w + lane of the next tile
+            auto look_up = [&](int tile) {
+                const int j = key0 + tile * kTile + 32 * w + lane;
+                page = -1;
+                if (tile < tiles && j < end) {
+                    const int p = K.by_page.quotient(j);
+                    slot = j - p * K.page_size;
+                    page = K.table[table + p];
                 }
             };
             if (K.table) look_up(0);
-            // queries
-            if (n_q > 0 && !wait(q_free, (n_q - 1) & 1)) return;
-            for (int h = 0; h < (U.shared ? 2 : 1); ++h) {
-                const uint32_t to = base + h * P::kQTile;
-#pragma unroll 4
-                for (int i = 0; i < kQPieces; ++i) {
-                    const int id = i * kCopyThreads + t, row = id / kQPieces, c = id - row * kQPieces;
-                    const int flat = U.row0 + h * kTile + row;
-                    const bool ok = h * kTile + row < U.rows;
-                    const int token = A.by_group.quotient(ok ? flat : 0), g = ok ? flat - token * A.group : 0;
-                    const char* src = A.q + 2 * ((U.begin + token) * A.q_token + (U.head * A.group + g) * A.q_head) + 16 * c;
-                    cp_async16_zfill(to + (c >> 3) * (kTile * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4), src, ok ? 16 : 0);
-                }
-            }
-            cp_async_mbar_arrive_noinc(q_full);
-            ++n_q;
-            // In the order of use: the values of a tile go behind the keys of the tile after it
-            // (shared rows) or of the two after it.
-            const int lag = P::kStreams == 2 && U.shared ? 1 : 2;
-            uint32_t ok[3] = {0, 0, 0};              // of a tile and the two before it: keys that are there,
-            int64_t k_off = 0, v_off[3] = {0, 0, 0};  // and where this lane's is
-            int pages[3] = {0, 0, 0}, slots[3] = {0, 0, 0};
-            for (int u = 0; u < U.tiles + lag; ++u) {
+            if (!copy_queries(*U)) return;
+            uint32_t ok[3] = {};              // of a tile and the two before it: keys that are there,
+            int64_t k_off = 0, v_off[3] = {};  // and where this lane's is
+            auto look = [&](int u) {
                 ok[2] = ok[1], ok[1] = ok[0];
                 v_off[2] = v_off[1], v_off[1] = v_off[0];
-                pages[2] = pages[1], pages[1] = pages[0], slots[2] = slots[1], slots[1] = slots[0];
-                if (u < U.tiles) {
-                    const int j0 = U.key0 + u * kTile + 32 * w;
-                    if (K.table) {
-                        const bool good = page >= 0 && page < K.pages;
-                        ok[0] = __ballot_sync(0xffffffffu, good);
-                        const uint32_t bad = __ballot_sync(0xffffffffu, !good && j0 + lane < U.end);
-                        if (lane == 0) {
-                            if (bad) atomicExch(&g_prompt_status, int(W4A4_ERR_INDEX));
-                            lost[(n_tile + u) % kLostTiles * 4 + w] = bad;
-                        }
-                        k_off = good ? page * K.page_stride[0] + int64_t(slot) * K.token_stride[0] : 0;
-                        v_off[0] = good ? page * K.page_stride[1] + int64_t(slot) * K.token_stride[1] : 0;
-                        pages[0] = page, slots[0] = slot;
-                        look_up(u + 1);
-                    } else {
-                        const int have = max(0, min(32, U.end - j0));
-                        ok[0] = have == 32 ? 0xffffffffu : (1u << have) - 1;
+                if (u >= tiles) return;
+                const int j0 = key0 + u * kTile + 32 * w;
+                if (K.table) {
+                    const bool good = page >= 0 && page < K.pages;
+                    ok[0] = __ballot_sync(0xffffffffu, good);
+                    const uint32_t bad = __ballot_sync(0xffffffffu, !good && j0 + lane < end);
+                    if (lane == 0) {
+                        if (bad) atomicExch(&g_prompt_status, int(W4A4_ERR_INDEX));
+                        lost[(n_tile + u) % kLostTiles * 4 + w] = bad;
+                    }
+                    k_off = good ? page * K.page_stride[0] + int64_t(slot) * K.token_stride[0] : 0;
+                    v_off[0] = good ? page * K.page_stride[1] + int64_t(slot) * K.token_stride[1] : 0;
+                    look_up(u + 1);
+                } else {
+                    const int have = max(0, min(32, end - j0));
+                    ok[0] = have == 32 ? 0xffffffffu : (1u << have) - 1;
+                    if (lane < have) {
+                        k_off = int64_t(begin + j0 + lane) * K.token_stride[0];
+                        v_off[0] = int64_t(begin + j0 + lane) * K.token_stride[1];
                     }
                 }
-#pragma unroll 1
-                for (int x = 0; x < 2 * P::kHalves; ++x) {
-                    const int kv = x < P::kHalves ? 1 : 0, half = x - (1 - kv) * P::kHalves;  // values, then keys
-                    if (kv ? u < lag : u >= U.tiles) continue;
-                    const uint32_t there = kv ? (lag == 1 ? ok[1] : ok[2]) : ok[0];
-                    const int64_t mine = kv ? (lag == 1 ? v_off[1] : v_off[2]) : k_off;
-                    const int j0 = U.key0 + (kv ? u - lag : u) * kTile + 32 * w;
-                    const int st = n_stage % P::kStages;
-                    if (n_stage >= P::kStages && !wait(empty(st), (n_stage / P::kStages - 1) & 1)) return;
-                    const uint32_t to = ring + st * P::kStage;
-                    const char* pool = K.pool[kv] + int64_t(U.head) * K.head_stride[kv] + half * P::kDs * kSize;
-                    auto source = [&](int r, int c) {
-                        const char* src = pool + 16 * c;
-                        if (K.table)
-                            src += __shfl_sync(0xffffffffu, mine, r);
-                        else if (there >> r & 1)
-                            src += int64_t(U.begin + j0 + r) * K.token_stride[kv];
-                        return src;
-                    };
-                    if (!E4M3 && K.box > 0 && there == 0xffffffffu) {
-                        // 32 rows that are all there: the copy engine brings them, a box a lane
-                        const int boxes = 32 / K.box;
-                        const int from = lane < boxes ? lane * K.box : 0;
-                        const int pg = K.table ? __shfl_sync(0xffffffffu, kv ? (lag == 1 ? pages[1] : pages[2]) : pages[0], from) : 0;
-                        const int y = K.table ? __shfl_sync(0xffffffffu, kv ? (lag == 1 ? slots[1] : slots[2]) : slots[0], from)
-                                              : U.begin + j0 + from;
-                        if (lane == 0) {
-                            mbar_expect_tx(full(st), 32 * 128 * P::kPlanes);
-                            mbar_arrive_n(full(st), kCopyArrivals - 1);
-                        }
-                        if (lane < boxes)
-                            for (int plane = 0; plane < P::kPlanes; ++plane)
-                                tma_load_4d(to + plane * (kTile * 128) + (32 * w + from) * 128, kv ? &v_map : &k_map,
-                                            half * P::kDs + 64 * plane, y, U.head, pg, full(st));
-                    } else if constexpr (!E4M3) {
+            };
+            auto send = [&](int kv, int half, int age, int) {
+                int st;
+                if (!next_stage(st)) return false;
+                const uint32_t to = ring + st * P::kStage;
+                const uint32_t there = age == 0 ? ok[0] : age == 1 ? ok[1] : ok[2];
+                const int64_t mine = kv == 0 ? k_off : age == 1 ? v_off[1] : v_off[2];
+                const char* pool = K.pool[kv] + int64_t(head) * K.head_stride[kv] + half * P::kDs * kSize;
+                auto source = [&](int r, int c) { return pool + 16 * c + __shfl_sync(0xffffffffu, mine, r); };
+                if constexpr (!E4M3) {
 #pragma unroll
-                        for (int i = 0; i < kPieces; ++i) {
-                            const int id = i * 32 + lane, r = id / kPieces, c = id - r * kPieces, row = 32 * w + r;
-                            cp_async16_zfill(to + (c >> 3) * (kTile * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4),
-                                             source(r, c), there >> r & 1 ? 16 : 0);
-                        }
-                        cp_async_mbar_arrive_noinc(full(st));
-                        if (lane == 0) mbar_arrive(full(st));
-                    } else {
-                        uint4 raw[kPieces];
+                    for (int i = 0; i < kPieces; ++i) {
+                        const int id = i * 32 + lane, r = id / kPieces, c = id - r * kPieces;
+                        const char* src = source(r, c);
+                        cp_async16_zfill(to + swizzled(32 * w + r, c), there >> r & 1 ? src : pool, there >> r & 1 ? 16 : 0);
+                    }
+                    cp_async_mbar_arrive_noinc(full(st));
+                } else {
+                    uint4 raw[kPieces];
 #pragma unroll
-                        for (int i = 0; i < kPieces; ++i) {
-                            const int id = i * 32 + lane, r = id / kPieces, c = id - r * kPieces;
-                            const char* src = source(r, c);
-                            raw[i] = there >> r & 1 ? ldg_stream_v4(src) : make_uint4(0, 0, 0, 0);
-                        }
+                    for (int i = 0; i < kPieces; ++i) {
+                        const int id = i * 32 + lane, r = id / kPieces, c = id - r * kPieces;
+                        const char* src = source(r, c);
+                        raw[i] = there >> r & 1 ? ldg_stream_v4(src) : make_uint4(0, 0, 0, 0);
+                    }
 #pragma unroll
-                        for (int i = 0; i < kPieces; ++i) {
-                            const int id = i * 32 + lane, r = id / kPieces, c = id - r * kPieces, row = 32 * w + r;
-                            const uint32_t four[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-                            uint32_t two[8];
+                    for (int i = 0; i < kPieces; ++i) {
+                        const int id = i * 32 + lane, r = id / kPieces, c = id - r * kPieces, row = 32 * w + r;
+                        const uint32_t four[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+                        uint32_t two[8];
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                e4m3x4_to_f16x2(four[k], two[2 * k], two[2 * k + 1]);
-                                if constexpr (BF) {  // exact: four significant bits
-                                    const float2 f = F16::up(two[2 * k]), g = F16::up(two[2 * k + 1]);
-                                    two[2 * k] = BF16::down(f.x, f.y), two[2 * k + 1] = BF16::down(g.x, g.y);
-                                }
+                        for (int k = 0; k < 4; ++k) {
+                            e4m3x4_to_f16x2(four[k], two[2 * k], two[2 * k + 1]);
+                            if constexpr (BF) {  // exact: four significant bits
+                                const float2 f = F16::up(two[2 * k]), g = F16::up(two[2 * k + 1]);
+                                two[2 * k] = BF16::down(f.x, f.y), two[2 * k + 1] = BF16::down(g.x, g.y);
                             }
-                            uint8_t* dst = smem + (to - base) + (c >> 2) * (kTile * 128) + row * 128;
-#pragma unroll
-                            for (int y = 0; y < 2; ++y)
-                                *reinterpret_cast<uint4*>(dst + (((2 * (c & 3) + y) ^ (row & 7)) << 4)) =
-                                    make_uint4(two[4 * y], two[4 * y + 1], two[4 * y + 2], two[4 * y + 3]);
                         }
-                        fence_proxy_async_smem();
-                        mbar_arrive(full(st));
-                        if (lane == 0) mbar_arrive(full(st));
+#pragma unroll
+                        for (int y = 0; y < 2; ++y)
+                            *reinterpret_cast<uint4*>(smem + (to - base) + swizzled(row, 2 * c + y)) =
+                                make_uint4(two[4 * y], two[4 * y + 1], two[4 * y + 2], two[4 * y + 3]);
                     }
-                    ++n_stage;
+                    fence_proxy_async_smem();
+                    mbar_arrive(full(st));
                 }
-            }
-            n_tile += U.tiles;
+                if (lane == 0) mbar_arrive(full(st));  // for the warp's word of `lost`
+                return true;
+            };
+            if (!copy_tiles(tiles, lag_of(*U), look, send)) return;
+            n_tile += tiles;
         }
     };
 
@@ -898,17 +992,16 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
             for (int i = 0; i < mine; ++i) {
                 const int tile = P::kStreams == 1 || shared ? i : 2 * i + stream;
                 const int buf = P::kStreams == 1 ? i & 1 : stream;
+                // keys [a, b) of the tile are seen, but for those on pages outside the pool
+                const int a = lo - U.key0 - tile * kTile, b = hi - U.key0 - tile * kTile;
+                const bool all = __all_sync(0xffffffffu, a <= 0 && b >= kTile);
+                const uint32_t at = tmem + lanes + P::scores(buf);
                 if (!wait(s_full(buf), s_phase >> buf & 1)) return;
                 s_phase ^= 1u << buf;
                 tc_fence_after();
-                const uint32_t at = tmem + lanes + P::scores(buf);
                 if (!idle) {
-                    // keys [a, b) of the tile are seen, but for those on pages outside the pool
-                    const int a = lo - U.key0 - tile * kTile, b = hi - U.key0 - tile * kTile;
                     const volatile uint32_t* bad = lost + (n_tile + tile) % kLostTiles * 4;
-                    bool all = a <= 0 && b >= kTile;
-                    if (A.keys.table) all = all && (bad[0] | bad[1] | bad[2] | bad[3]) == 0;
-                    if (__all_sync(0xffffffffu, all)) {
+                    if (all && !(A.keys.table && (bad[0] | bad[1] | bad[2] | bad[3]) != 0)) {
                         if (!probabilities(true, at, buf, i)) return;
                     } else {
                         // of 32 keys from number c, a bit each
@@ -1028,7 +1121,10 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
         softmax();
     } else if (warp < kSoftmaxWarps + kCopyWarps) {
         regs_dec<96>();
-        copy();
+        if (!E4M3 && A.keys.box > 0)
+            copy_boxes();
+        else
+            copy_rows();
         cp_async_commit();
         cp_async_wait<0>();
         if (*abort)  // the copy engine's land before the shared memory goes away

@@ -73,6 +73,7 @@ struct Args {
     int tokens, seqs, q_heads, kv_heads, group, window;
     bool causal;
     Divisor by_group;
+    bool q_boxes = false;                  // queries come by the copy engine: 128 rows are whole tokens
 };
 
 struct Sequence {
@@ -109,7 +110,8 @@ struct Plan {
     static constexpr int kBars = kUnits + 2 * int(sizeof(Unit));
     static constexpr int kFlags = kBars + (2 * kStages + 22) * 8;
     static constexpr int kLost = kFlags + 16;                   // [kLostTiles][4] keys of a tile on pages outside the pool
-    static constexpr int kBytes = kLost + kLostTiles * 16;
+    static constexpr int kOrder = kLost + kLostTiles * 16;      // [64] sequences, see sort_sequences
+    static constexpr int kBytes = kOrder + 64;
     // Copies are at most the ring ahead of the scores' products, and those two tiles ahead of
     // the probabilities.
     static_assert(kLostTiles >= kStages + 3, "a word is read before it is written again");
@@ -279,10 +281,20 @@ __device__ __forceinline__ int blocks_of(const Args& A, const Sequence& s, int r
     return int((int64_t(s.rows) * A.group + rows - 1) / rows);
 }
 
+// n / d for d >= 1, exact: by a float division below 2^20 ((n + 1/2) / d is at least 1 / (2 d) from a
+// whole number, the division and the conversion off by less than n / d * 2^-21), which takes a
+// fifth of the time.
+__device__ __forceinline__ int quotient(int n, int d) {
+    return n < (1 << 20) ? int(__fdividef(n + 0.5f, float(d))) : n / d;
+}
+
+// f of every sequence, summed (a warp).  In fp32, exact below 2^24: what is decided by it is a
+// matter of speed where it is larger.
 template <class F>
-__device__ __forceinline__ int64_t sum_over_sequences(const Args& A, F f) {
-    int64_t sum = 0;
-    for (int b = threadIdx.x & 31; b < A.seqs; b += 32) {
+__device__ __forceinline__ float sum_over_sequences(const Args& A, const Sequence& mine, F f) {
+    const int lane = threadIdx.x & 31;
+    float sum = lane < A.seqs ? f(mine) : 0.f;
+    for (int b = lane + 32; b < A.seqs; b += 32) {
         bool bad;
         sum += f(sequence(A, b, bad));
     }
@@ -291,74 +303,101 @@ __device__ __forceinline__ int64_t sum_over_sequences(const Args& A, F f) {
     return sum;
 }
 
+// `mine`: the lane's sequence (of the first 32).
 template <int D>
-__device__ Share share_out(const Args& A) {
-    const int ctas = gridDim.x;
+__device__ __forceinline__ Share share_out(const Args& A, const Sequence& mine) {
+    const float ctas = gridDim.x;
+    auto units_of = [&](int rows) {
+        return A.kv_heads * sum_over_sequences(A, mine, [&](const Sequence& s) { return float(blocks_of(A, s, rows)); });
+    };
     Share r{128, 0};
-    if (Plan<D>::kStreams == 2) {
-        // 256 rows a unit where there are units enough, or tiles enough to split them into
-        const int64_t units = A.kv_heads * sum_over_sequences(A, [&](const Sequence& s) { return blocks_of(A, s, 256); });
-        if (units >= ctas) r.rows = 256;
-    }
-    if (!A.parts) return r;
-    for (int rows = r.rows == 256 || Plan<D>::kStreams == 1 ? r.rows : 256; rows >= r.rows; rows -= 128) {
-        const int64_t units = A.kv_heads * sum_over_sequences(A, [&](const Sequence& s) { return blocks_of(A, s, rows); });
-        const int64_t tiles = A.kv_heads * sum_over_sequences(A, [&](const Sequence& s) {
-            return int64_t(blocks_of(A, s, rows)) * most_tiles(A, s);
+    // 256 rows a unit where there are units enough, or (below) tiles enough to split them into
+    float units = Plan<D>::kStreams == 2 ? units_of(256) : 0.f;
+    if (units >= ctas) r.rows = 256;
+    if (!A.parts || r.rows == 256) return r;
+    const float units128 = units_of(128);
+    if (Plan<D>::kStreams == 1) units = units128;
+    const int wide = Plan<D>::kStreams == 1 ? 128 : 256;
+    for (int rows = wide; rows >= 128; rows -= 128) {
+        const float n = rows == wide ? units : units128;
+        if (n >= ctas) return r;
+        const float tiles = A.kv_heads * sum_over_sequences(A, mine, [&](const Sequence& s) {
+            return float(blocks_of(A, s, rows)) * most_tiles(A, s);
         });
-        if (rows == 256 && r.rows == 128 && tiles < 8 * ctas) continue;
+        if (rows == 256 && tiles < 8 * ctas) continue;
         r.rows = rows;
-        if (units >= ctas) return r;
-        int piece = int(max(int64_t(2), (tiles + ctas - 1) / ctas));
+        int piece = max(2, int(ceilf(tiles / ctas)));
         for (int tries = 0; tries < 8; ++tries) {
-            const int64_t all = A.kv_heads * sum_over_sequences(A, [&](const Sequence& s) {
-                return int64_t(blocks_of(A, s, rows)) * max(1, (most_tiles(A, s) + piece - 1) / piece);
+            const float all = A.kv_heads * sum_over_sequences(A, mine, [&](const Sequence& s) {
+                return float(blocks_of(A, s, rows)) * max(1, quotient(most_tiles(A, s) + piece - 1, piece));
             });
             if (all <= ctas) {
                 r.piece = piece;
                 return r;
             }
-            piece = int(max(int64_t(piece) + 1, piece * all / ctas));
+            piece = max(piece + 1, int(piece * all / ctas));
         }
         return r;
     }
     return r;
 }
 
+// Sequences with the longest units first, for up to kSorted of them: what is left for the last
+// round is short then (six chunks of 417 tokens, the later ones behind more, D = 256: 186 us, and
+// ... in the sequences' order).
+constexpr int kSorted = 64;
+__device__ __forceinline__ void sort_sequences(const Args& A, const Sequence& mine, uint8_t* order) {
+    const int lane = threadIdx.x & 31;
+    Sequence s2{0, 0, 0};
+    bool bad;
+    if (lane + 32 < A.seqs) s2 = sequence(A, lane + 32, bad);
+    const int key[2] = {mine.rows > 0 ? most_tiles(A, mine) : -1, s2.rows > 0 ? most_tiles(A, s2) : -1};
+    int rank[2] = {0, 0};
+    for (int k = 0; k < A.seqs; ++k) {
+        const int other = __shfl_sync(0xffffffffu, k < 32 ? key[0] : key[1], k & 31);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) rank[i] += other > key[i] || (other == key[i] && k < lane + 32 * i);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        if (lane + 32 * i < A.seqs) order[rank[i]] = uint8_t(lane + 32 * i);
+    __syncwarp();
+}
+
 // Where unit `want` is, for numbers that grow from call to call (a warp).
 struct Walk {
-    int base, before;  // sequences from `base` on, and the units before them
+    const uint8_t* order;    // of the sequences, nullptr: as they are
+    int base = -32, before = 0;  // sequences from `base` on, and the units before them
+    int b = 0, pieces = 1, units = 0, upto = 0;  // of this lane's: number, pieces of a unit, units, those up to it
+    Sequence s{0, 0, 0};
     __device__ __forceinline__ bool find(const Args& A, const Share& share, int want, Unit& U) {
         const int lane = threadIdx.x & 31;
         while (base < A.seqs) {
-            Sequence s{0, 0, 0};
-            bool bad;
-            int pieces = 1, units = 0;
-            if (base + lane < A.seqs) {
-                s = sequence(A, base + lane, bad);
-                if (share.piece > 0) pieces = max(1, (most_tiles(A, s) + share.piece - 1) / share.piece);
-                units = blocks_of(A, s, share.rows) * A.kv_heads * pieces;
-            }
-            int upto = units;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, upto, o);
-                if (lane >= o) upto += v;
-            }
             const uint32_t beyond = __ballot_sync(0xffffffffu, before + upto > want);
             if (beyond == 0) {
                 before += __shfl_sync(0xffffffffu, upto, 31);
                 base += 32;
+                b = base + lane;
+                pieces = 1, units = 0;
+                if (b < A.seqs) {
+                    bool bad;
+                    if (order) b = order[b];
+                    s = sequence(A, b, bad);
+                    if (share.piece > 0) pieces = max(1, quotient(most_tiles(A, s) + share.piece - 1, share.piece));
+                    units = blocks_of(A, s, share.rows) * A.kv_heads * pieces;
+                }
+                upto = units;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int v = __shfl_up_sync(0xffffffffu, upto, o);
+                    if (lane >= o) upto += v;
+                }
                 continue;
             }
             const int at = __ffs(beyond) - 1;
-            const int in = want - before - __shfl_sync(0xffffffffu, upto - units, at);
-            pieces = __shfl_sync(0xffffffffu, pieces, at);
-            units = __shfl_sync(0xffffffffu, units, at);
-            s.begin = __shfl_sync(0xffffffffu, s.begin, at);
-            s.rows = __shfl_sync(0xffffffffu, s.rows, at);
-            s.length = __shfl_sync(0xffffffffu, s.length, at);
-            fill(A, share, base + at, s, units, pieces, want, in, U);
+            auto of = [&](int v) { return __shfl_sync(0xffffffffu, v, at); };
+            fill(A, share, of(b), Sequence{of(s.begin), of(s.rows), of(s.length)}, of(units), of(pieces), want,
+                 want - before - of(upto - units), U);
             return true;
         }
         return false;
@@ -366,9 +405,9 @@ struct Walk {
     // The last blocks of a sequence, which see the most keys, come first.
     __device__ __forceinline__ void fill(const Args& A, const Share& share, int b, const Sequence& s, int units, int pieces,
                                          int want, int in, Unit& U) {
-        const int per = A.kv_heads * pieces, back = in / per, rest = in - back * per;
-        const int head = rest / pieces, piece = rest - head * pieces;
-        const int block = units / per - 1 - back;
+        const int per = A.kv_heads * pieces, back = quotient(in, per), rest = in - back * per;
+        const int head = quotient(rest, pieces), piece = rest - head * pieces;
+        const int block = quotient(units, per) - 1 - back;
         U.live = 1;
         U.b = b, U.head = head;
         U.row0 = block * share.rows;
@@ -402,7 +441,8 @@ struct Walk {
 
 template <int D, class T, bool E4M3>
 __global__ void __launch_bounds__(kThreads, 1)
-attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
+attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtensorMap q_map,
+                 const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
     using namespace tc;
     using P = Plan<D>;
     constexpr bool BF = std::is_same_v<T, BF16>;
@@ -455,6 +495,7 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
     tc_fence_after();
     const uint32_t tmem = tmem_base;
     if (tid == 0 && A.keys.box > 0) prefetch_tensor_map(&k_map), prefetch_tensor_map(&v_map);
+    if (tid == 32 && A.q_boxes) prefetch_tensor_map(&q_map);
     pdl_wait();
     pdl_launch_dependents();
 
@@ -475,17 +516,22 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
     };
 
     auto plan = [&]() {
+        Sequence mine{0, 0, 0};
+        bool any = false;
+        if (lane < A.seqs) mine = sequence(A, lane, any);
         if (blockIdx.x == 0) {
-            bool any = false;
-            for (int b = lane; b < A.seqs; b += 32) {
+            for (int b = lane + 32; b < A.seqs; b += 32) {
                 bool bad;
                 sequence(A, b, bad);
                 any |= bad;
             }
             if (any) atomicExch(&g_prompt_status, int(W4A4_ERR_INDEX));
         }
-        const Share share = share_out<D>(A);
-        Walk walk{0, 0};
+        uint8_t* const order = smem + P::kOrder;
+        const bool sorted = A.seqs > 1 && A.seqs <= kSorted;
+        if (sorted) sort_sequences(A, mine, order);
+        const Share share = share_out<D>(A, mine);
+        Walk walk{sorted ? order : nullptr};
         for (uint32_t n = 0;; ++n) {
             const int turn = int(n & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
             Unit U{};
@@ -508,6 +554,23 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
     uint32_t n_stage = 0, n_q = 0;  // copies of stages begun, units whose queries were copied
     auto copy_queries = [&](const Unit& U) {
         if (n_q > 0 && !wait(q_free, (n_q - 1) & 1)) return false;
+        ++n_q;
+        if (A.q_boxes) {
+            // (token, head) pairs side by side are a box of whole tokens.  Those behind the unit's rows,
+            // another sequence's or none, are rows of scores that nobody reads.
+            constexpr int kPlanes = P::kHalves * P::kPlanes;
+            const int i = tid - 32 * kSoftmaxWarps, tiles = U.shared ? 2 : 1;
+            if (i == 0)
+                mbar_expect_tx(q_full, tiles * P::kQTile);
+            else
+                mbar_arrive(q_full);
+            if (i < tiles * kPlanes) {
+                const int h = i / kPlanes, plane = i - h * kPlanes;
+                tma_load_4d(base + h * P::kQTile + plane * (kTile * 128), &q_map, 64 * plane, U.head * A.group,
+                            U.begin + A.by_group.quotient(U.row0 + h * kTile), 0, q_full);
+            }
+            return true;
+        }
         constexpr int kPieces = D * 2 / 16;
         for (int h = 0; h < (U.shared ? 2 : 1); ++h) {
             const uint32_t to = base + h * P::kQTile;
@@ -521,7 +584,6 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
             }
         }
         cp_async_mbar_arrive_noinc(q_full);
-        ++n_q;
         return true;
     };
     // The place of the next copy in the ring, free to be written.
@@ -609,10 +671,11 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
                 const int pg = age == 0 ? pages[0] : age == 1 ? pages[1] : pages[2];
                 const int sl = age == 0 ? slots[0] : age == 1 ? slots[1] : slots[2];
                 if (lane == 0) mbar_expect_tx(full(st), __popc(there) * box * 128 * P::kPlanes);
-                if (there >> lane & 1)
-                    for (int plane = 0; plane < P::kPlanes; ++plane)
-                        tma_load_4d(to + plane * (kTile * 128) + my * 128, kv ? &v_map : &k_map, half * P::kDs + 64 * plane, sl,
-                                    head, K.table ? pg : 0, full(st));
+                // lane 16 p + b: plane p of box b
+                const int from = lane & 15, y = __shfl_sync(0xffffffffu, sl, from), z = __shfl_sync(0xffffffffu, pg, from);
+                if (there >> from & 1 && lane < 16 * P::kPlanes)
+                    tma_load_4d(to + (lane >> 4) * (kTile * 128) + (32 * w + from * box) * 128, kv ? &v_map : &k_map,
+                                half * P::kDs + 64 * (lane >> 4), y, head, K.table ? z : 0, full(st));
                 if (there != all) {
                     const uint32_t s = age == 0 ? some[0] : age == 1 ? some[1] : some[2];
                     const char* pool = K.pool[kv] + int64_t(head) * K.head_stride[kv] + half * P::kDs * 2;
@@ -1197,24 +1260,21 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
     }
 }
 
-// The map of the keys (w = 0) or values: [page][head][token][dim], boxes of 64 elements of `box`
-// tokens with the 128-byte swizzle.
+// A map of [outer][middle][inner][dim] elements with these strides in bytes: boxes of 64 elements
+// of inner_box x middle_box rows with the 128-byte swizzle.
 template <int D, bool BF>
-bool encode(const Args& A, int w, int box, CUtensorMap& map) {
+bool encode(const char* p, int64_t inner, int64_t inner_stride, int64_t middle, int64_t middle_stride, int64_t outer,
+            int64_t outer_stride, int inner_box, int middle_box, CUtensorMap& map) {
     const EncodeFn go = driver_encode();
-    const Keys& K = A.keys;
-    const bool paged = K.table != nullptr;
-    const cuuint64_t tokens = paged ? K.page_size : A.tokens, pages = paged ? K.pages : 1;
-    const cuuint64_t dims[4] = {D, tokens, cuuint64_t(A.kv_heads), pages};
-    auto stride = [](int64_t bytes, cuuint64_t n) { return n > 1 ? cuuint64_t(bytes) : cuuint64_t(16); };  // of one: unused
-    const cuuint64_t strides[3] = {stride(K.token_stride[w], tokens), stride(K.head_stride[w], dims[2]),
-                                   stride(K.page_stride[w], pages)};
-    const cuuint32_t shape[4] = {64, cuuint32_t(box), 1, 1}, steps[4] = {1, 1, 1, 1};
+    const cuuint64_t dims[4] = {D, cuuint64_t(inner), cuuint64_t(middle), cuuint64_t(outer)};
+    auto stride = [](int64_t bytes, int64_t n) { return n > 1 ? cuuint64_t(bytes) : cuuint64_t(16); };  // of one: unused
+    const cuuint64_t strides[3] = {stride(inner_stride, inner), stride(middle_stride, middle), stride(outer_stride, outer)};
+    const cuuint32_t shape[4] = {64, cuuint32_t(inner_box), cuuint32_t(middle_box), 1}, steps[4] = {1, 1, 1, 1};
     for (const cuuint64_t s : strides)
         if (s == 0) return false;  // rows that share memory
-    return go && pages > 0 &&
-           go(&map, BF ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<char*>(K.pool[w]),
-              dims, strides, shape, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+    return go && outer > 0 &&
+           go(&map, BF ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<char*>(p), dims,
+              strides, shape, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1243,16 +1303,25 @@ w4a4_status run(Args& A, cudaStream_t s) {
     const int grid = A.parts ? sms : int(std::min(int64_t(sms), most));
     constexpr bool bf16 = std::is_same_v<T, BF16>;
     // Keys and values by the copy engine, eight rows or more a copy, where pages hold so many side by side.
-    CUtensorMap maps[2] = {};
-    const int box = !A.keys.table ? 32 : A.keys.page_size % 32 == 0 ? 32 : A.keys.page_size % 16 == 0 ? 16 : A.keys.page_size % 8 == 0 ? 8 : 0;
-    A.keys.box = !E4M3 && box > 0 && encode<D, bf16>(A, 0, box, maps[0]) && encode<D, bf16>(A, 1, box, maps[1]) ? box : 0;
+    CUtensorMap maps[3] = {};
+    const Keys& K = A.keys;
+    const bool paged = K.table != nullptr;
+    const int box = !paged ? 32 : K.page_size % 32 == 0 ? 32 : K.page_size % 16 == 0 ? 16 : K.page_size % 8 == 0 ? 8 : 0;
+    auto rows_of = [&](int w) {
+        return encode<D, bf16>(K.pool[w], paged ? K.page_size : A.tokens, K.token_stride[w], A.kv_heads, K.head_stride[w],
+                               paged ? K.pages : 1, K.page_stride[w], box, 1, maps[1 + w]);
+    };
+    A.keys.box = !E4M3 && box > 0 && rows_of(0) && rows_of(1) ? box : 0;
+    // ... and queries, where 128 rows are whole tokens.
+    A.q_boxes = kTile % A.group == 0 && encode<D, bf16>(A.q, A.q_heads, 2 * A.q_head, A.tokens, 2 * A.q_token, 1, 0, A.group,
+                                                        kTile / A.group, maps[0]);
     const char* text = !A.lengths ? (bf16 ? "prompt_attention bf16 tokens=%d seqs=%d heads=%d/%d dim=%d stages=%d grid=%d parts=%d"
                                           : "prompt_attention f16 tokens=%d seqs=%d heads=%d/%d dim=%d stages=%d grid=%d parts=%d")
                        : E4M3     ? "chunk_attention e4m3 tokens=%d seqs=%d heads=%d/%d dim=%d stages=%d grid=%d parts=%d"
                        : bf16     ? "chunk_attention bf16 tokens=%d seqs=%d heads=%d/%d dim=%d stages=%d grid=%d parts=%d"
                                   : "chunk_attention f16 tokens=%d seqs=%d heads=%d/%d dim=%d stages=%d grid=%d parts=%d";
     set_dispatch_ints(text, {A.tokens, A.seqs, A.q_heads, A.kv_heads, D, P::kStages, grid, A.parts != nullptr});
-    w4a4_status st = launch<attention_kernel<D, T, E4M3>>(dim3(unsigned(grid)), kThreads, P::kBytes, s, A, maps[0], maps[1]);
+    w4a4_status st = launch<attention_kernel<D, T, E4M3>>(dim3(unsigned(grid)), kThreads, P::kBytes, s, A, maps[0], maps[1], maps[2]);
     if (st == W4A4_OK && A.parts) st = launch<join_kernel<D, T, E4M3>>(dim3(unsigned(grid)), 256, 0, s, A);
     return st;
 }

@@ -964,9 +964,7 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
             // The scores of the stream's i-th tile into probabilities.  They are loaded twice, once for
             // their maximum and once, half a tile at a time, for their powers: kept in between they
             // and their results were moved and spilled, 340 instructions of 900 for a warp's tile.
-            // `seen`: true, or a function of the number of a key in the tile: 32 bits from that one on.
-            auto probabilities = [&](auto seen, uint32_t at, int buf, int i) {
-                constexpr bool kAll = std::is_same_v<decltype(seen), bool>;
+            auto probabilities = [&](uint32_t at, int buf, int i) {
                 float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                 for (int part = 0; part < 2; ++part) {
@@ -974,15 +972,6 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
                     tmem_ld32_at(at + 64 * part, s);
                     tmem_ld32_at(at + 64 * part + 32, s + 32);
                     tmem_wait_ld();
-                    if (flip != 1.f) {
-#pragma unroll
-                        for (int c = 0; c < 64; ++c) s[c] *= flip;
-                    }
-                    if constexpr (!kAll) {
-                        const uint32_t bits[2] = {seen(64 * part), seen(64 * part + 32)};
-#pragma unroll
-                        for (int c = 0; c < 64; ++c) s[c] = bits[c / 32] >> (c % 32) & 1 ? s[c] : -INFINITY;
-                    }
 #pragma unroll
                     for (int c = 0; c < 64; c += 8)
 #pragma unroll
@@ -1012,7 +1001,7 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
                     }
                 }
                 const float ref = (top == -INFINITY ? 0.f : top * scale2) - kLift;
-                const uint64_t by2 = f2_pack(signed2, signed2), less = f2_pack(-ref, -ref);
+                const uint64_t by2 = f2_pack(scale2, scale2), less = f2_pack(-ref, -ref);
                 uint64_t sums[2] = {0, 0};
 #pragma unroll
                 for (int part = 0; part < 2; ++part) {
@@ -1022,19 +1011,11 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
                     tmem_wait_ld();
                     // Pairs in a fixed order, each a few steps behind the last: ordered by the compiler
                     // the sums come last, with all powers kept until then.
-                    uint32_t p[32], bits[2] = {0, 0};
-                    if constexpr (!kAll) bits[0] = seen(64 * part), bits[1] = seen(64 * part + 32);
+                    uint32_t p[32];
                     uint64_t x[32], e[32];
 #pragma unroll
                     for (int k = 0; k < 32 + 6; ++k) {
-                        if (k < 32) {
-                            x[k] = ffma2_in_order(f2_pack(s[2 * k], s[2 * k + 1]), by2, less);
-                            if constexpr (!kAll) {
-                                const float2 y = f2_unpack(x[k]);
-                                x[k] = f2_pack(bits[k / 16] >> (2 * k % 32) & 1 ? y.x : -INFINITY,
-                                               bits[k / 16] >> (2 * k % 32 + 1) & 1 ? y.y : -INFINITY);
-                            }
-                        }
+                        if (k < 32) x[k] = ffma2_in_order(f2_pack(s[2 * k], s[2 * k + 1]), by2, less);
                         if (k >= 2 && k - 2 < 32) e[k - 2] = ex2_in_order(x[k - 2]);
                         if (k >= 6) {
                             sums[k & 1] = fadd2_in_order(sums[k & 1], e[k - 6]);
@@ -1057,29 +1038,36 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
                 const int buf = P::kStreams == 1 ? i & 1 : stream;
                 // keys [a, b) of the tile are seen, but for those on pages outside the pool
                 const int a = lo - U.key0 - tile * kTile, b = hi - U.key0 - tile * kTile;
-                const bool all = __all_sync(0xffffffffu, a <= 0 && b >= kTile);
+                const bool all = __all_sync(0xffffffffu, a <= 0 && b >= kTile && flip == 1.f);
                 const uint32_t at = tmem + lanes + P::scores(buf);
                 if (!wait(s_full(buf), s_phase >> buf & 1)) return;
                 s_phase ^= 1u << buf;
                 tc_fence_after();
-                if (!idle) {
-                    const volatile uint32_t* bad = lost + (n_tile + tile) % kLostTiles * 4;
-                    if (all && !(A.keys.table && (bad[0] | bad[1] | bad[2] | bad[3]) != 0)) {
-                        if (!probabilities(true, at, buf, i)) return;
-                    } else {
-                        // of 32 keys from number c, a bit each
-                        auto seen = [&](int c) {
-                            const uint32_t below = b - c >= 32 ? 0xffffffffu : (1u << max(b - c, 0)) - 1;
-                            const uint32_t from = a - c >= 32 ? 0u : 0xffffffffu << max(a - c, 0);
-                            return below & from & (A.keys.table ? ~bad[c / 32] : 0xffffffffu);
-                        };
-                        if (!probabilities(seen, at, buf, i)) return;
-                    }
-                } else {
+                if (idle) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane < 2) mbar_arrive(p_full(2 * buf + lane));
+                    continue;
                 }
+                const volatile uint32_t* bad = lost + (n_tile + tile) % kLostTiles * 4;
+                if (!all || (A.keys.table && (bad[0] | bad[1] | bad[2] | bad[3]) != 0)) {
+                    // The scores as they count, in their place: few instructions, where a second form of
+                    // what follows would have to be fetched for the one or two tiles that need it.
+#pragma unroll 1
+                    for (int c = 0; c < kTile; c += 16) {
+                        float s[16];
+                        tmem_ld16(at + c, s);
+                        uint32_t bits = b - c >= 16 ? 0xffffu : (1u << max(b - c, 0)) - 1;
+                        bits &= a - c >= 16 ? 0u : 0xffffu << max(a - c, 0);
+                        if (A.keys.table) bits &= ~(bad[c >> 5] >> (c & 16));
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) s[k] = bits >> k & 1 ? s[k] * flip : -INFINITY;
+                        tmem_st16(at + c, s);
+                    }
+                    tmem_wait_st();
+                }
+                if (!probabilities(at, buf, i)) return;
             }
             n_tile += U.tiles;
 

@@ -41,7 +41,7 @@ constexpr int kThreads = 512;
 constexpr int kTile = 128;                 // keys of a tile, rows of a stream
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint32_t kSuspendNs = 20000;
-constexpr int kSoftmaxWarps = 8, kCopyWarps = 4, kMmaWarp = 12, kPlanWarp = 13;
+constexpr int kSoftmaxWarps = 8, kCopyWarps = 4, kMmaWarp = 12, kPlanWarp = 13, kRawWarp = 15;
 constexpr int kCopyThreads = 32 * kCopyWarps;
 constexpr int kLostTiles = 16;
 constexpr int kMaxParts = 156;             // of a call
@@ -95,7 +95,8 @@ struct Unit {
 };
 static_assert(sizeof(Unit) == 64, "copied as four int4");
 
-template <int D>
+// 8-bit rows come into a ring of their own, from where they are turned into 16-bit ones.
+template <int D, bool E4M3>
 struct Plan {
     static constexpr int kDs = D < 128 ? D : 128;               // elements of a stage's rows
     static constexpr int kHalves = D / kDs;
@@ -104,18 +105,24 @@ struct Plan {
     static constexpr int kStreams = D == 256 ? 1 : 2;
     static constexpr int kQTile = kHalves * kStage;
     static constexpr int kQ = kStreams * kQTile;
-    static constexpr int kStages = D == 64 ? 11 : 5;
-    static constexpr int kMl = kQ + kStages * kStage;           // [2][128] maxima, then sums, of the streams
+    static constexpr int kStages = E4M3 ? (D == 64 ? 6 : D == 256 ? 4 : 3) : D == 64 ? 11 : 5;
+    static constexpr int kRawStages = E4M3 ? (D == 64 ? 8 : D == 256 ? 2 : 4) : 0;
+    static constexpr int kRawStage = kTile * kDs;
+    static constexpr int kRawRing = kRawStages > 0 ? kRawStages : 1;
+    static constexpr int kRaw = kQ + kStages * kStage;
+    static constexpr int kMl = kRaw + kRawStages * kRawStage;   // [2][128] maxima, then sums, of the streams
     static constexpr int kUnits = kMl + 2 * 2 * kTile * 4;      // [2] units
     static constexpr int kBars = kUnits + 2 * int(sizeof(Unit));
-    static constexpr int kFlags = kBars + (2 * kStages + 22) * 8;
+    static constexpr int kFlags = kBars + (2 * kStages + 22 + 2 * kRawStages) * 8;
     static constexpr int kLost = kFlags + 16;                   // [kLostTiles][4] keys of a tile on pages outside the pool
     static constexpr int kOrder = kLost + kLostTiles * 16;      // [64] sequences, see sort_sequences
-    static constexpr int kBytes = kOrder + 64;
-    // Copies are at most the ring ahead of the scores' products, and those two tiles ahead of
+    static constexpr int kThere = kOrder + 64;                  // [kRawStages][4] rows of a raw stage that are there
+    static constexpr int kBytes = kThere + kRawStages * 16;
+    // Copies are at most the rings ahead of the scores' products, and those two tiles ahead of
     // the probabilities.
-    static_assert(kLostTiles >= kStages + 3, "a word is read before it is written again");
+    static_assert(kLostTiles >= (kStages + kRawStages) / 2 + 5, "a word is read before it is written again");
     static_assert(kBytes <= 227 * 1024, "shared memory");
+    static_assert(kStages >= 2 * kHalves, "the values of a tile and the keys of the next are waited for together");
     // tensor memory: a stream's scores (and probabilities) and its output
     static constexpr uint32_t scores(int buf) { return D == 256 ? 128 * buf : 256 * buf; }
     static constexpr uint32_t output(int stream) { return D == 256 ? 256 : 256 * stream + 128; }
@@ -306,18 +313,19 @@ __device__ __forceinline__ float sum_over_sequences(const Args& A, const Sequenc
 // `mine`: the lane's sequence (of the first 32).
 template <int D>
 __device__ __forceinline__ Share share_out(const Args& A, const Sequence& mine) {
+    constexpr int kStreams = Plan<D, false>::kStreams;
     const float ctas = gridDim.x;
     auto units_of = [&](int rows) {
         return A.kv_heads * sum_over_sequences(A, mine, [&](const Sequence& s) { return float(blocks_of(A, s, rows)); });
     };
     Share r{128, 0};
     // 256 rows a unit where there are units enough, or (below) tiles enough to split them into
-    float units = Plan<D>::kStreams == 2 ? units_of(256) : 0.f;
+    float units = kStreams == 2 ? units_of(256) : 0.f;
     if (units >= ctas) r.rows = 256;
     if (!A.parts || r.rows == 256) return r;
     const float units128 = units_of(128);
-    if (Plan<D>::kStreams == 1) units = units128;
-    const int wide = Plan<D>::kStreams == 1 ? 128 : 256;
+    if (kStreams == 1) units = units128;
+    const int wide = kStreams == 1 ? 128 : 256;
     for (int rows = wide; rows >= 128; rows -= 128) {
         const float n = rows == wide ? units : units128;
         if (n >= ctas) return r;
@@ -444,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtensorMap q_map,
                  const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
     using namespace tc;
-    using P = Plan<D>;
+    using P = Plan<D, E4M3>;
     constexpr bool BF = std::is_same_v<T, BF16>;
     // fp16 probabilities are taken up to 2^15, so that weights down to 2^-38 of the largest
     // keep the bits of their rounding: thousands of small ones beside one heavy key can make
@@ -468,6 +476,8 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
     auto o_full = [&](int i) { return more + 88 + 8 * i; };
     auto u_full = [&](int i) { return more + 104 + 8 * i; };
     auto u_free = [&](int i) { return more + 120 + 8 * i; };
+    auto raw_full = [&](int s) { return more + 176 + 16 * s; };
+    auto raw_empty = [&](int s) { return more + 184 + 16 * s; };
     const uint32_t ml_full = more + 136, ml_free = more + 144;
     auto turn = [&](int i) { return more + 152 + 8 * i; };
     Unit* units = reinterpret_cast<Unit*>(smem + P::kUnits);
@@ -484,8 +494,9 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
         mbar_init(ml_full, kSoftmaxWarps), mbar_init(ml_free, kSoftmaxWarps);
         for (int i = 0; i < 2; ++i) {
             mbar_init(s_full(i), 1), mbar_init(p_full(2 * i), 4), mbar_init(p_full(2 * i + 1), 4), mbar_init(o_full(i), 1);
-            mbar_init(turn(i), 1), mbar_init(u_full(i), 1), mbar_init(u_free(i), kSoftmaxWarps + kCopyWarps + P::kStreams);
+            mbar_init(turn(i), 1), mbar_init(u_full(i), 1), mbar_init(u_free(i), kSoftmaxWarps + kCopyWarps + P::kStreams + (E4M3 ? 1 : 0));
         }
+        for (int s = 0; s < P::kRawStages; ++s) mbar_init(raw_full(s), 1), mbar_init(raw_empty(s), kCopyWarps);
         fence_mbar_init();
         mbar_arrive(turn(0));  // the first turn is the first stream's
     }
@@ -610,6 +621,25 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
     };
     auto lag_of = [&](const Unit& U) { return P::kStreams == 2 && U.shared ? 1 : 2; };
 
+    // 16 E4M3 elements, piece c of a row, as 16-bit ones into a stage.
+    auto widen16 = [&](const uint4& raw, uint8_t* stage, int row, int c) {
+        const uint32_t four[4] = {raw.x, raw.y, raw.z, raw.w};
+        uint32_t two[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            e4m3x4_to_f16x2(four[k], two[2 * k], two[2 * k + 1]);
+            if constexpr (BF) {  // exact: four significant bits
+                const float2 f = F16::up(two[2 * k]), g = F16::up(two[2 * k + 1]);
+                two[2 * k] = BF16::down(f.x, f.y), two[2 * k + 1] = BF16::down(g.x, g.y);
+            }
+        }
+        // pieces of one row and of the planes' same ones take turns, so that eight lanes hit all banks
+        const bool odd = c >> 2 & 1;
+        const uint4 lo = make_uint4(two[0], two[1], two[2], two[3]), hi = make_uint4(two[4], two[5], two[6], two[7]);
+        *reinterpret_cast<uint4*>(stage + swizzled(row, 2 * c + odd)) = odd ? hi : lo;
+        *reinterpret_cast<uint4*>(stage + swizzled(row, 2 * c + !odd)) = odd ? lo : hi;
+    };
+
     // By the copy engine, each warp 32 rows of a tile, a box of K.box of them a lane; boxes that
     // are not all there by the warp's own loads.  (One warp for all of them has fewer instructions
     // but sends small boxes more slowly: pages of 24, D = 256 326 us and 180.)
@@ -700,6 +730,114 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
         }
     };
 
+    // 8-bit rows by the copy engine, a box a lane, into their ring; pages behind a sequence's end
+    // come as they are, pages outside the pool do not.
+    uint32_t n_raw = 0;
+    auto copy_raw = [&]() {
+        const Keys& K = A.keys;
+        const int box = K.box, boxes = box > 0 ? kTile / box : 0, my = lane * box;
+        uint32_t* const there = reinterpret_cast<uint32_t*>(smem + P::kThere);
+        uint32_t n_tile = 0;
+        for (uint32_t n = 0;; done_with(n++)) {
+            const Unit* const U = unit(n);
+            if (!U) return;
+            if (U->tiles == 0 || box == 0) continue;
+            const int key0 = U->key0, end = U->end, tiles = U->tiles, head = U->head;
+            const int64_t table = U->b * K.table_stride;
+            int page = -1, slot = 0;  // of this lane's box in the next tile
+            auto look_up = [&](int tile) {
+                const int j = key0 + tile * kTile + my;
+                page = -1;
+                if (lane < boxes && tile < tiles && j < end) {
+                    const int p = K.by_page.quotient(j);
+                    slot = j - p * K.page_size;
+                    page = K.table[table + p];
+                }
+            };
+            look_up(0);
+            int pages[3] = {}, slots[3] = {};  // of a tile and the two before it,
+            uint32_t some[3] = {};             // and boxes on pages of the pool
+            auto look = [&](int u) {
+#pragma unroll
+                for (int k = 2; k > 0; --k) pages[k] = pages[k - 1], slots[k] = slots[k - 1], some[k] = some[k - 1];
+                if (u >= tiles) return;
+                const bool in = lane < boxes && key0 + u * kTile + my < end, good = in && page >= 0 && page < K.pages;
+                some[0] = __ballot_sync(0xffffffffu, good), pages[0] = page, slots[0] = slot;
+                const uint32_t bad = __ballot_sync(0xffffffffu, in && !good);
+                if (lane < 4) {
+                    uint32_t word = 0;
+                    for (int k = 0; bad != 0 && k < 32; k += box)
+                        if (bad >> quotient(32 * lane + k, box) & 1) word |= (0xffffffffu >> (32 - box)) << k;
+                    lost[(n_tile + u) % kLostTiles * 4 + lane] = word;
+                }
+                if (bad && lane == 0) atomicExch(&g_prompt_status, int(W4A4_ERR_INDEX));
+                look_up(u + 1);
+            };
+            auto send = [&](int kv, int half, int age, int tile) {
+                const int st = n_raw % P::kRawRing;
+                if (n_raw >= P::kRawRing && !wait(raw_empty(st), (n_raw / P::kRawRing - 1) & 1)) return false;
+                ++n_raw;
+                const uint32_t s = age == 0 ? some[0] : age == 1 ? some[1] : some[2];
+                const int pg = age == 0 ? pages[0] : age == 1 ? pages[1] : pages[2];
+                const int sl = age == 0 ? slots[0] : age == 1 ? slots[1] : slots[2];
+                if (lane < 4) {
+                    const int have = end - (key0 + tile * kTile + 32 * lane);
+                    uint32_t word = have >= 32 ? 0xffffffffu : have > 0 ? (1u << have) - 1 : 0;
+                    word &= ~lost[(n_tile + tile) % kLostTiles * 4 + lane];
+                    there[4 * st + lane] = word;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_expect_tx(raw_full(st), __popc(s) * box * P::kDs);
+                if (s >> lane & 1)
+                    tma_load_4d(base + P::kRaw + st * P::kRawStage + my * P::kDs, kv ? &v_map : &k_map, half * P::kDs, sl, head, pg,
+                                raw_full(st));
+                return true;
+            };
+            if (!copy_tiles(tiles, lag_of(*U), look, send)) return;
+            n_tile += tiles;
+        }
+    };
+    // ... and turned into 16-bit rows by four warps.
+    auto widen = [&]() {
+        uint32_t n_read = 0;
+        const volatile uint32_t* const there = reinterpret_cast<const volatile uint32_t*>(smem + P::kThere);
+        const int t = tid - 32 * kSoftmaxWarps;
+        for (uint32_t n = 0;; done_with(n++)) {
+            const Unit* const U = unit(n);
+            if (!U) return;
+            if (U->tiles == 0) continue;
+            const int stages = 2 * P::kHalves * U->tiles;
+            if (!copy_queries(*U)) return;
+            for (int x = 0; x < stages; ++x) {
+                constexpr int kRowPieces = P::kDs / 16, kPieces = kTile * kRowPieces / kCopyThreads;
+                const int from = n_read % P::kRawRing;
+                if (!wait(raw_full(from), n_read / P::kRawRing & 1)) return;
+                ++n_read;
+                int st;
+                if (!next_stage(st)) return;
+                const uint8_t* src = smem + P::kRaw + from * P::kRawStage + 16 * t;
+                uint8_t* dst = smem + P::kQ + st * P::kStage;
+                uint4 raw[kPieces];
+#pragma unroll
+                for (int i = 0; i < kPieces; ++i) {
+                    raw[i] = *reinterpret_cast<const uint4*>(src + 16 * kCopyThreads * i);
+                    const int row = (i * kCopyThreads + t) / kRowPieces;
+                    if (!(there[4 * from + (row >> 5)] >> (row & 31) & 1)) raw[i] = make_uint4(0, 0, 0, 0);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(raw_empty(from));
+#pragma unroll
+                for (int i = 0; i < kPieces; ++i) {
+                    const int id = i * kCopyThreads + t, row = id / kRowPieces;
+                    widen16(raw[i], dst, row, id - row * kRowPieces);
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(full(st));
+                if (lane == 0) mbar_arrive(full(st));
+            }
+        }
+    };
+
     // By loads of four warps, 32 rows of a tile each: pages of any size, E4M3 rows turned into
     // 16-bit ones.
     auto copy_rows = [&]() {
@@ -780,20 +918,7 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
 #pragma unroll
                     for (int i = 0; i < kPieces; ++i) {
                         const int id = i * 32 + lane, r = id / kPieces, c = id - r * kPieces, row = 32 * w + r;
-                        const uint32_t four[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-                        uint32_t two[8];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            e4m3x4_to_f16x2(four[k], two[2 * k], two[2 * k + 1]);
-                            if constexpr (BF) {  // exact: four significant bits
-                                const float2 f = F16::up(two[2 * k]), g = F16::up(two[2 * k + 1]);
-                                two[2 * k] = BF16::down(f.x, f.y), two[2 * k + 1] = BF16::down(g.x, g.y);
-                            }
-                        }
-#pragma unroll
-                        for (int y = 0; y < 2; ++y)
-                            *reinterpret_cast<uint4*>(smem + (to - base) + swizzled(row, 2 * c + y)) =
-                                make_uint4(two[4 * y], two[4 * y + 1], two[4 * y + 2], two[4 * y + 3]);
+                        widen16(raw[i], smem + (to - base), row, c);
                     }
                     fence_proxy_async_smem();
                     mbar_arrive(full(st));
@@ -1172,10 +1297,16 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
         softmax();
     } else if (warp < kSoftmaxWarps + kCopyWarps) {
         regs_dec<96>();
-        if (!E4M3 && A.keys.box > 0)
+        if constexpr (E4M3) {
+            if (A.keys.box > 0)
+                widen();
+            else
+                copy_rows();
+        } else if (A.keys.box > 0) {
             copy_boxes();
-        else
+        } else {
             copy_rows();
+        }
         cp_async_commit();
         cp_async_wait<0>();
         if (*abort)  // the copy engine's land before the shared memory goes away
@@ -1193,6 +1324,11 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
             __syncwarp();
         } else if (warp == kPlanWarp) {
             plan();
+        } else if (E4M3 && warp == kRawWarp) {
+            copy_raw();
+            if (*abort)
+                for (uint32_t i = n_raw > P::kRawRing ? n_raw - P::kRawRing : 0; i < n_raw; ++i)
+                    warp_wait_parity_suspend(raw_full(i % P::kRawRing), i / P::kRawRing & 1, &never_abort, kWaitNs, kSuspendNs);
         }
     }
     tc_fence_before();
@@ -1249,26 +1385,28 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
 }
 
 // A map of [outer][middle][inner][dim] elements with these strides in bytes: boxes of 64 elements
-// of inner_box x middle_box rows with the 128-byte swizzle.
+// of inner_box x middle_box rows with the 128-byte swizzle, or of whole stage rows of bytes.
 template <int D, bool BF>
-bool encode(const char* p, int64_t inner, int64_t inner_stride, int64_t middle, int64_t middle_stride, int64_t outer,
+bool encode(const char* p, bool bytes, int64_t inner, int64_t inner_stride, int64_t middle, int64_t middle_stride, int64_t outer,
             int64_t outer_stride, int inner_box, int middle_box, CUtensorMap& map) {
     const EncodeFn go = driver_encode();
     const cuuint64_t dims[4] = {D, cuuint64_t(inner), cuuint64_t(middle), cuuint64_t(outer)};
     auto stride = [](int64_t bytes, int64_t n) { return n > 1 ? cuuint64_t(bytes) : cuuint64_t(16); };  // of one: unused
     const cuuint64_t strides[3] = {stride(inner_stride, inner), stride(middle_stride, middle), stride(outer_stride, outer)};
-    const cuuint32_t shape[4] = {64, cuuint32_t(inner_box), cuuint32_t(middle_box), 1}, steps[4] = {1, 1, 1, 1};
+    const cuuint32_t shape[4] = {cuuint32_t(bytes ? (D < 128 ? D : 128) : 64), cuuint32_t(inner_box), cuuint32_t(middle_box), 1};
+    const cuuint32_t steps[4] = {1, 1, 1, 1};
     for (const cuuint64_t s : strides)
         if (s == 0) return false;  // rows that share memory
     return go && outer > 0 &&
-           go(&map, BF ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<char*>(p), dims,
-              strides, shape, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+           go(&map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : BF ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+              4, const_cast<char*>(p), dims, strides, shape, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              bytes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int D, class T, bool E4M3>
 w4a4_status run(Args& A, cudaStream_t s) {
-    using P = Plan<D>;
+    using P = Plan<D, E4M3>;
     auto kernel = attention_kernel<D, T, E4M3>;
     static std::atomic<uint64_t> ready{0};  // devices
     int dev = 0;
@@ -1296,12 +1434,12 @@ w4a4_status run(Args& A, cudaStream_t s) {
     const bool paged = K.table != nullptr;
     const int box = !paged ? 32 : K.page_size % 32 == 0 ? 32 : K.page_size % 16 == 0 ? 16 : K.page_size % 8 == 0 ? 8 : 0;
     auto rows_of = [&](int w) {
-        return encode<D, bf16>(K.pool[w], paged ? K.page_size : A.tokens, K.token_stride[w], A.kv_heads, K.head_stride[w],
+        return encode<D, bf16>(K.pool[w], E4M3, paged ? K.page_size : A.tokens, K.token_stride[w], A.kv_heads, K.head_stride[w],
                                paged ? K.pages : 1, K.page_stride[w], box, 1, maps[1 + w]);
     };
-    A.keys.box = !E4M3 && box > 0 && rows_of(0) && rows_of(1) ? box : 0;
+    A.keys.box = box > 0 && rows_of(0) && rows_of(1) ? box : 0;
     // ... and queries, where 128 rows are whole tokens.
-    A.q_boxes = kTile % A.group == 0 && encode<D, bf16>(A.q, A.q_heads, 2 * A.q_head, A.tokens, 2 * A.q_token, 1, 0, A.group,
+    A.q_boxes = kTile % A.group == 0 && encode<D, bf16>(A.q, false, A.q_heads, 2 * A.q_head, A.tokens, 2 * A.q_token, 1, 0, A.group,
                                                         kTile / A.group, maps[0]);
     const char* text = !A.lengths ? (bf16 ? "prompt_attention bf16 tokens=%d seqs=%d heads=%d/%d dim=%d stages=%d grid=%d parts=%d"
                                           : "prompt_attention f16 tokens=%d seqs=%d heads=%d/%d dim=%d stages=%d grid=%d parts=%d")

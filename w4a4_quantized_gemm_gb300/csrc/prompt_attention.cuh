@@ -37,12 +37,10 @@
 namespace w4a4 {
 namespace prompt {
 
-constexpr int kThreads = 512;
 constexpr int kTile = 128;                 // keys of a tile, rows of a stream
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint32_t kSuspendNs = 20000;
-constexpr int kSoftmaxWarps = 8, kCopyWarps = 4, kMmaWarp = 12, kPlanWarp = 13, kRawWarp = 15;
-constexpr int kCopyThreads = 32 * kCopyWarps;
+constexpr int kSoftmaxWarps = 8;
 constexpr int kLostTiles = 16;
 constexpr int kMaxParts = 156;             // of a call
 constexpr int kPartFloats = 256 * 130;     // of one: [rows][D] outputs, [256] maxima, [256] sums
@@ -105,10 +103,22 @@ struct Plan {
     static constexpr int kStreams = D == 256 ? 1 : 2;
     static constexpr int kQTile = kHalves * kStage;
     static constexpr int kQ = kStreams * kQTile;
-    static constexpr int kStages = E4M3 ? (D == 64 ? 6 : D == 256 ? 4 : 3) : D == 64 ? 11 : 5;
-    static constexpr int kRawStages = E4M3 ? (D == 64 ? 8 : D == 256 ? 2 : 4) : 0;
+    static constexpr int kStages = E4M3 ? (D == 64 ? 6 : 4) : D == 64 ? 11 : 5;
+    static constexpr int kRawStages = E4M3 ? (D == 64 ? 8 : 2) : 0;
     static constexpr int kRawStage = kTile * kDs;
+    static constexpr bool kRawSwizzled = kDs == 128;
     static constexpr int kRawRing = kRawStages > 0 ? kRawStages : 1;
+    // warps: softmax, copies (twice as many to widen 8-bit rows: 64 streams of 4 tokens ... us with four), then
+    // one that plans, two that issue products, one for the ring of 8-bit rows
+    static constexpr int kCopyWarps = E4M3 ? 8 : 4;
+    static constexpr int kMmaWarp = kSoftmaxWarps + kCopyWarps, kPlanWarp = kMmaWarp + 1, kRawWarp = kMmaWarp + 3;
+    static constexpr int kThreads = 32 * (kMmaWarp + 4);
+    // registers of their threads: as many in all as a block of so many threads is launched with
+    static constexpr int kLaunchRegs = E4M3 ? 96 : 128;
+    static constexpr int kSoftmaxRegs = E4M3 ? 144 : 160, kCopyRegs = E4M3 ? 64 : 96, kOtherRegs = E4M3 ? 64 : 96;
+    static_assert(32 * (kSoftmaxWarps * kSoftmaxRegs + kCopyWarps * kCopyRegs + 4 * kOtherRegs) <= kThreads * kLaunchRegs,
+                  "an increase beyond what the block has would wait forever");
+    static_assert(kThreads * kLaunchRegs <= 65536 && kThreads * (kLaunchRegs + 8) > 65536, "registers at launch");
     static constexpr int kRaw = kQ + kStages * kStage;
     static constexpr int kMl = kRaw + kRawStages * kRawStage;   // [2][128] maxima, then sums, of the streams
     static constexpr int kUnits = kMl + 2 * 2 * kTile * 4;      // [2] units
@@ -448,7 +458,7 @@ struct Walk {
 };
 
 template <int D, class T, bool E4M3>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__((Plan<D, E4M3>::kThreads), 1)
 attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtensorMap q_map,
                  const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
     using namespace tc;
@@ -458,6 +468,8 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
     // keep the bits of their rounding: thousands of small ones beside one heavy key can make
     // the output.  bf16 ones have fp32's range.
     constexpr float kLift = BF ? 0.f : 13.f, kSlack = BF ? 8.f : 2.f;
+    constexpr int kCopyWarps = P::kCopyWarps, kCopyThreads = 32 * kCopyWarps;
+    constexpr int kMmaWarp = P::kMmaWarp, kPlanWarp = P::kPlanWarp, kRawWarp = P::kRawWarp;
     extern __shared__ __align__(1024) uint8_t smem[];
     int& abort_flag = *reinterpret_cast<int*>(smem + P::kFlags);
     int& never_abort = *reinterpret_cast<int*>(smem + P::kFlags + 4);
@@ -488,7 +500,7 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
         never_abort = 0;
         // a copying warp's lanes arrive when their copies have, and one of them once more: for what the engine
         // brings, or the warp's other words
-        for (int s = 0; s < P::kStages; ++s) mbar_init(full(s), 33 * kCopyWarps), mbar_init(empty(s), 2);
+        for (int s = 0; s < P::kStages; ++s) mbar_init(full(s), 33 * (E4M3 && A.keys.box > 0 ? kCopyWarps : 4)), mbar_init(empty(s), 2);
         mbar_init(q_full, kCopyThreads), mbar_init(q_free, 2);
         mbar_init(o_free, kSoftmaxWarps), mbar_init(pv_done, 1), mbar_init(all_done, P::kStreams);
         mbar_init(ml_full, kSoftmaxWarps), mbar_init(ml_free, kSoftmaxWarps);
@@ -582,11 +594,11 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
             }
             return true;
         }
-        constexpr int kPieces = D * 2 / 16;
+        constexpr int kPieces = D * 2 / 16, kRounds = kTile * kPieces / kCopyThreads;
         for (int h = 0; h < (U.shared ? 2 : 1); ++h) {
             const uint32_t to = base + h * P::kQTile;
 #pragma unroll 4
-            for (int i = 0; i < kPieces; ++i) {
+            for (int i = 0; i < kRounds; ++i) {
                 const int id = i * kCopyThreads + tid - 32 * kSoftmaxWarps, row = id / kPieces, c = id - row * kPieces;
                 const bool ok = h * kTile + row < U.rows;
                 const int flat = ok ? U.row0 + h * kTile + row : 0, token = A.by_group.quotient(flat), g = flat - token * A.group;
@@ -622,7 +634,7 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
     auto lag_of = [&](const Unit& U) { return P::kStreams == 2 && U.shared ? 1 : 2; };
 
     // 16 E4M3 elements, piece c of a row, as 16-bit ones into a stage.
-    auto widen16 = [&](const uint4& raw, uint8_t* stage, int row, int c) {
+    auto widen16 = [&](const uint4& raw, uint8_t* stage, int row, int c, bool rows_apart) {
         const uint32_t four[4] = {raw.x, raw.y, raw.z, raw.w};
         uint32_t two[8];
 #pragma unroll
@@ -633,8 +645,9 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
                 two[2 * k] = BF16::down(f.x, f.y), two[2 * k + 1] = BF16::down(g.x, g.y);
             }
         }
-        // pieces of one row and of the planes' same ones take turns, so that eight lanes hit all banks
-        const bool odd = c >> 2 & 1;
+        // where eight lanes have pieces of one row, those of the second plane begin with the other half, so
+        // that they hit all banks
+        const bool odd = !rows_apart && (c >> 2 & 1);
         const uint4 lo = make_uint4(two[0], two[1], two[2], two[3]), hi = make_uint4(two[4], two[5], two[6], two[7]);
         *reinterpret_cast<uint4*>(stage + swizzled(row, 2 * c + odd)) = odd ? hi : lo;
         *reinterpret_cast<uint4*>(stage + swizzled(row, 2 * c + !odd)) = odd ? lo : hi;
@@ -815,21 +828,34 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
                 ++n_read;
                 int st;
                 if (!next_stage(st)) return;
-                const uint8_t* src = smem + P::kRaw + from * P::kRawStage + 16 * t;
+                const uint8_t* src = smem + P::kRaw + from * P::kRawStage;
                 uint8_t* dst = smem + P::kQ + st * P::kStage;
+                // piece c of a row: eight lanes take eight rows' where rows are 128 bytes (and swizzled),
+                // else what lies side by side
+                auto place = [&](int i, int& row, int& c) {
+                    const int id = i * kCopyThreads + t;
+                    if constexpr (P::kRawSwizzled) {
+                        row = (id & 7) | (id >> 6) << 3, c = id >> 3 & 7;
+                        return row * 128 + ((c ^ (row & 7)) << 4);
+                    } else {
+                        row = id / kRowPieces, c = id - row * kRowPieces;
+                        return 16 * id;
+                    }
+                };
                 uint4 raw[kPieces];
 #pragma unroll
                 for (int i = 0; i < kPieces; ++i) {
-                    raw[i] = *reinterpret_cast<const uint4*>(src + 16 * kCopyThreads * i);
-                    const int row = (i * kCopyThreads + t) / kRowPieces;
+                    int row, c;
+                    raw[i] = *reinterpret_cast<const uint4*>(src + place(i, row, c));
                     if (!(there[4 * from + (row >> 5)] >> (row & 31) & 1)) raw[i] = make_uint4(0, 0, 0, 0);
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(raw_empty(from));
 #pragma unroll
                 for (int i = 0; i < kPieces; ++i) {
-                    const int id = i * kCopyThreads + t, row = id / kRowPieces;
-                    widen16(raw[i], dst, row, id - row * kRowPieces);
+                    int row, c;
+                    place(i, row, c);
+                    widen16(raw[i], dst, row, c, P::kRawSwizzled);
                 }
                 fence_proxy_async_smem();
                 mbar_arrive(full(st));
@@ -864,6 +890,7 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
             };
             if (K.table) look_up(0);
             if (!copy_queries(*U)) return;
+            if (w >= 4) continue;  // (of the warps that widen 8-bit rows)
             uint32_t ok[3] = {};              // of a tile and the two before it: keys that are there,
             int64_t k_off = 0, v_off[3] = {};  // and where this lane's is
             auto look = [&](int u) {
@@ -918,7 +945,7 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
 #pragma unroll
                     for (int i = 0; i < kPieces; ++i) {
                         const int id = i * 32 + lane, r = id / kPieces, c = id - r * kPieces, row = 32 * w + r;
-                        widen16(raw[i], smem + (to - base), row, c);
+                        widen16(raw[i], smem + (to - base), row, c, false);
                     }
                     fence_proxy_async_smem();
                     mbar_arrive(full(st));
@@ -1293,10 +1320,10 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
     };
 
     if (warp < kSoftmaxWarps) {
-        regs_inc<160>();
+        regs_inc<P::kSoftmaxRegs>();
         softmax();
     } else if (warp < kSoftmaxWarps + kCopyWarps) {
-        regs_dec<96>();
+        regs_dec<P::kCopyRegs>();
         if constexpr (E4M3) {
             if (A.keys.box > 0)
                 widen();
@@ -1313,7 +1340,7 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
             for (uint32_t i = n_stage > P::kStages ? n_stage - P::kStages : 0; i < n_stage; ++i)
                 warp_wait_parity_suspend(full(i % P::kStages), i / P::kStages & 1, &never_abort, kWaitNs, kSuspendNs);
     } else {
-        regs_dec<96>();
+        regs_dec<P::kOtherRegs>();
         if (warp == kMmaWarp || (P::kStreams == 2 && warp == kMmaWarp + 2)) {
             if (lane == 0) {
                 multiply((warp - kMmaWarp) >> 1);
@@ -1385,7 +1412,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
 }
 
 // A map of [outer][middle][inner][dim] elements with these strides in bytes: boxes of 64 elements
-// of inner_box x middle_box rows with the 128-byte swizzle, or of whole stage rows of bytes.
+// of inner_box x middle_box rows with the 128-byte swizzle, or of whole stage rows of bytes (swizzled if 128).
 template <int D, bool BF>
 bool encode(const char* p, bool bytes, int64_t inner, int64_t inner_stride, int64_t middle, int64_t middle_stride, int64_t outer,
             int64_t outer_stride, int inner_box, int middle_box, CUtensorMap& map) {
@@ -1400,7 +1427,7 @@ bool encode(const char* p, bool bytes, int64_t inner, int64_t inner_stride, int6
     return go && outer > 0 &&
            go(&map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : BF ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
               4, const_cast<char*>(p), dims, strides, shape, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              bytes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+              bytes && D < 128 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1447,7 +1474,7 @@ w4a4_status run(Args& A, cudaStream_t s) {
                        : bf16     ? "chunk_attention bf16 tokens=%d seqs=%d heads=%d/%d dim=%d stages=%d grid=%d parts=%d"
                                   : "chunk_attention f16 tokens=%d seqs=%d heads=%d/%d dim=%d stages=%d grid=%d parts=%d";
     set_dispatch_ints(text, {A.tokens, A.seqs, A.q_heads, A.kv_heads, D, P::kStages, grid, A.parts != nullptr});
-    w4a4_status st = launch<attention_kernel<D, T, E4M3>>(dim3(unsigned(grid)), kThreads, P::kBytes, s, A, maps[0], maps[1], maps[2]);
+    w4a4_status st = launch<attention_kernel<D, T, E4M3>>(dim3(unsigned(grid)), P::kThreads, P::kBytes, s, A, maps[0], maps[1], maps[2]);
     if (st == W4A4_OK && A.parts) st = launch<join_kernel<D, T, E4M3>>(dim3(unsigned(grid)), 256, 0, s, A);
     return st;
 }

@@ -1,5 +1,6 @@
-"""A decoder layer served one token per sequence: the quantised linears with the paged cache, its
-attention and the fused block norms between them ("W4A4 CUDA Kernel for Voice Clone", 3.4 and 4: the
+"""A decoder layer served one token per sequence, a chunk of new tokens of every sequence, or whole
+prompts at once: the quantised linears with the paged cache, its attention and the fused block norms
+between them ("W4A4 CUDA Kernel for Voice Clone", 3.4 and 4: the
 kernels of a layer, captured in one CUDA graph).
 
     r, x -> qkv linear -> w4a4_kv_append (per-head q/k norm, rotation, cache) -> w4a4_paged_attention
@@ -7,12 +8,15 @@ kernels of a layer, captured in one CUDA graph).
          -> gate|up linear with SiLU(gate) * up -> down linear
          -> w4a4_block_norm (residual add, norm before the next layer)
 
+A chunk's attention is w4a4_chunk_attention (`W4A4DecoderLayer.chunk`); prompts that are attended to
+once and need no cache take w4a4_qk_rope and w4a4_prompt_attention (`W4A4DecoderLayer.prompt`).
+
 The module only allocates device buffers and issues the C-ABI calls.
 
     python -m w4a4_quantized_gemm_gb300.decoder [sequences] [tokens in the cache] [layers]
 
 builds a stack of 1024-wide layers (16 query and 8 key-value heads of 128) with random weights and
-prints the time of a decode step, captured as one CUDA graph.
+prints the time of a prompt of so many tokens and of a decode step, captured as one CUDA graph.
 """
 from __future__ import annotations
 
@@ -35,6 +39,24 @@ class _Packed:
         self.colscale, self.bias = colscale.contiguous(), None if bias is None else bias.contiguous()
 
 
+class _Rows:
+    """The buffers of a layer's pass over so many rows (tokens)."""
+
+    def __init__(self, layer, rows: int):
+        dev, hq, hkv, dim = layer.qkv.packed.device, layer.q_heads, layer.kv_heads, layer.dim
+
+        def buf(*shape):
+            return torch.empty(shape, dtype=torch.float16, device=dev)
+
+        hidden = layer.o.N
+        self.qkv_out, self.q, self.attn = buf(rows, layer.qkv.N), buf(rows, hq, dim), buf(rows, hq, dim)
+        self.o_out, self.x_mlp, self.down_out = buf(rows, hidden), buf(rows, hidden), buf(rows, hidden)
+        self.h = buf(rows, layer.gate_up.N // 2)
+        need = max(w4.act_workspace_bytes(rows, p.K, p.r) for p in (layer.qkv, layer.o, layer.gate_up, layer.down))
+        self.ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        self.split = self.qkv_out.unflatten(1, (hq + 2 * hkv, dim)).split((hq, hkv, hkv), dim=1)
+
+
 class W4A4DecoderLayer:
     """One layer's weights and the buffers of a decode step of `seqs` sequences.
 
@@ -51,41 +73,65 @@ class W4A4DecoderLayer:
         self.gate_up = _Packed(*gate_up, gate_up=True)
         self.q_heads, self.kv_heads, self.dim, self.seqs, self.eps = q_heads, kv_heads, head_dim, seqs, eps
         self.mlp_gain, self.q_gain, self.k_gain = mlp_gain, q_gain, k_gain
-        dev = self.qkv.packed.device
+        self._rows = {}
+        one = self.rows(seqs)
+        self.qkv_out, self.q, self.attn, self.split = one.qkv_out, one.q, one.attn, one.split
+        self.o_out, self.x_mlp, self.down_out, self.h, self.ws = one.o_out, one.x_mlp, one.down_out, one.h, one.ws
 
-        def buf(*shape):
-            return torch.empty(shape, dtype=torch.float16, device=dev)
+    def rows(self, n: int) -> _Rows:
+        """The buffers for n rows, made at their first use (before a graph capture, if it is to use them)."""
+        if n not in self._rows:
+            self._rows[n] = _Rows(self, n)
+        return self._rows[n]
 
-        hidden = self.o.N
-        self.qkv_out, self.q, self.attn = buf(seqs, self.qkv.N), buf(seqs, q_heads, head_dim), buf(seqs, q_heads, head_dim)
-        self.o_out, self.x_mlp, self.down_out = buf(seqs, hidden), buf(seqs, hidden), buf(seqs, hidden)
-        self.h = buf(seqs, self.gate_up.N // 2)
-        need = max(w4.act_workspace_bytes(seqs, p.K, p.r) for p in (self.qkv, self.o, self.gate_up, self.down))
-        self.ws = torch.empty(need, dtype=torch.uint8, device=dev)
-        qkv_rows = self.qkv_out.unflatten(1, (q_heads + 2 * kv_heads, head_dim))
-        self.split = qkv_rows.split((q_heads, kv_heads, kv_heads), dim=1)
+    def _linear(self, p, X, Y, ws, stream):
+        w4.w4a4_forward(X, p.packed, p.colscale, p.bias, Y, p.r, ws, stream=stream)
 
-    def _linear(self, p, X, Y, stream):
-        w4.w4a4_forward(X, p.packed, p.colscale, p.bias, Y, p.r, self.ws, stream=stream)
+    def _after_attention(self, b, r, next_gain, x_next, stream):
+        self._linear(self.o, b.attn.flatten(1), b.o_out, b.ws, stream)
+        w4.w4a4_block_norm(b.o_out, r, b.x_mlp, r, post=w4.NORM_NONE, pre_gain=self.mlp_gain, eps=self.eps,
+                           stream=stream)
+        g = self.gate_up
+        w4.w4a4_quantize_act(b.x_mlp, g.packed, b.ws, g.r, stream)
+        w4.w4a4_linear_silu_mul(b.ws, g.packed, g.colscale, g.bias, b.h, g.K, g.r, stream)
+        self._linear(self.down, b.h, b.down_out, b.ws, stream)
+        w4.w4a4_block_norm(b.down_out, r, x_next, r, post=w4.NORM_NONE, pre_gain=next_gain, eps=self.eps,
+                           stream=stream)
 
     def step(self, x, r, positions, lengths, cache, rope, next_gain, x_next, stream=None):
         """One token of each sequence: x [seqs, hidden] its normalised input, r the residual stream
         (fp16 or fp32, updated in place), positions = lengths - 1 the token's place, lengths the
         cache's with it.  x_next receives the next layer's input under next_gain."""
-        q, k, v = self.split
-        self._linear(self.qkv, x, self.qkv_out, stream)
-        w4.w4a4_kv_append(q, k, v, positions, cache, self.q, rope=rope, q_gain=self.q_gain, k_gain=self.k_gain,
+        b = self.rows(self.seqs)
+        q, k, v = b.split
+        self._linear(self.qkv, x, b.qkv_out, b.ws, stream)
+        w4.w4a4_kv_append(q, k, v, positions, cache, b.q, rope=rope, q_gain=self.q_gain, k_gain=self.k_gain,
                           eps=self.eps, stream=stream)
-        w4.w4a4_paged_attention(self.q, cache, lengths, self.attn, stream=stream)
-        self._linear(self.o, self.attn.view(self.seqs, -1), self.o_out, stream)
-        w4.w4a4_block_norm(self.o_out, r, self.x_mlp, r, post=w4.NORM_NONE, pre_gain=self.mlp_gain, eps=self.eps,
-                           stream=stream)
-        g = self.gate_up
-        w4.w4a4_quantize_act(self.x_mlp, g.packed, self.ws, g.r, stream)
-        w4.w4a4_linear_silu_mul(self.ws, g.packed, g.colscale, g.bias, self.h, g.K, g.r, stream)
-        self._linear(self.down, self.h, self.down_out, stream)
-        w4.w4a4_block_norm(self.down_out, r, x_next, r, post=w4.NORM_NONE, pre_gain=next_gain, eps=self.eps,
-                           stream=stream)
+        w4.w4a4_paged_attention(b.q, cache, lengths, b.attn, stream=stream)
+        self._after_attention(b, r, next_gain, x_next, stream)
+
+    def chunk(self, x, r, positions, owners, starts, lengths, cache, rope, next_gain, x_next, stream=None):
+        """A chunk of new tokens of every sequence, rows starts[b] .. starts[b + 1] - 1 of x [tokens, hidden]
+        and r; row t is token positions[t] of sequence owners[t].  They go into the cache, which holds
+        lengths[b] tokens of each with them, and are attended to over all of it.  The rest as for step."""
+        b = self.rows(x.shape[0])
+        q, k, v = b.split
+        self._linear(self.qkv, x, b.qkv_out, b.ws, stream)
+        w4.w4a4_kv_append(q, k, v, positions, cache, b.q, seqs=owners, rope=rope, q_gain=self.q_gain,
+                          k_gain=self.k_gain, eps=self.eps, stream=stream)
+        w4.w4a4_chunk_attention(b.q, cache, starts, lengths, b.attn, stream=stream)
+        self._after_attention(b, r, next_gain, x_next, stream)
+
+    def prompt(self, x, r, positions, starts, rope, next_gain, x_next, causal=True, stream=None):
+        """Whole prompts, packed one behind the other (rows starts[b] .. starts[b + 1] - 1), without a cache.
+        Rows of x outside all of them are padding: positions[t] < 0, and their results are not defined."""
+        b = self.rows(x.shape[0])
+        q, k, v = b.split
+        self._linear(self.qkv, x, b.qkv_out, b.ws, stream)
+        w4.w4a4_qk_rope(q, k, positions, q, k, rope=rope, q_gain=self.q_gain, k_gain=self.k_gain, eps=self.eps,
+                        stream=stream)
+        w4.w4a4_prompt_attention(q, k, v, starts, b.attn, causal=causal, stream=stream)
+        self._after_attention(b, r, next_gain, x_next, stream)
 
 
 def random_layer(hidden: int, inner: int, q_heads: int, kv_heads: int, dim: int, seqs: int, rank: int = 32,
@@ -136,6 +182,28 @@ def main(seqs: int = 32, tokens: int = 2048, layers: int = 28):
         for i, (layer, cache) in enumerate(zip(stack, caches)):
             layer.step(x[i % 2], r, positions, lengths, cache, rope, gain, x[(i + 1) % 2])
 
+    # the first sequence's prompt, into the caches, with no rows of the others
+    starts = torch.full((seqs + 1,), tokens, dtype=torch.int32, device="cuda")
+    starts[0] = 0
+    owners = torch.zeros(tokens, dtype=torch.int32, device="cuda")
+    places = torch.arange(tokens, dtype=torch.int32, device="cuda")
+    stream = torch.randn(tokens, hidden, device="cuda")
+    rows = [torch.randn(tokens, hidden, device="cuda").half() for _ in range(2)]
+
+    def prefill():
+        for i, (layer, cache) in enumerate(zip(stack, caches)):
+            layer.chunk(rows[i % 2], stream, places, owners, starts, lengths, cache, rope, gain, rows[(i + 1) % 2])
+
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    for _ in range(2):  # the first pass makes buffers and workspaces
+        start.record()
+        prefill()
+        end.record()
+    torch.cuda.synchronize()
+    check_status("prompt")
+    ms = start.elapsed_time(end)
+    print(f"{layers} layers, a prompt of {tokens} tokens: {ms:.2f} ms, {tokens / ms * 1e3:.0f} tokens/s")
+
     forward()  # warm-up: workspaces exist before the capture
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
@@ -143,7 +211,6 @@ def main(seqs: int = 32, tokens: int = 2048, layers: int = 28):
         forward()
     for _ in range(3):
         graph.replay()
-    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
     start.record()
     for _ in range(20):
         graph.replay()

@@ -396,6 +396,27 @@ def test_chunk_few_rows_over_a_long_cache(dtype, act, dim, rows, lengths, window
         assert torch.equal(out, again) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("dtype, act, dim", [(F16, F16, 128), (F16, F16, 64), (E4M3, BF16, 64), (E4M3, F16, 128), (BF16, BF16, 256)])
+def test_chunk_gives_the_same_bits_while_copies_arrive_in_any_order(dtype, act, dim):
+    """Few rows, whose tiles two streams take in turns, over keys of which some are in L2 and some are not: a stage
+    whose copy is overtaken by the next ones' must be waited for all the same."""
+    lengths = [2900, 1000, 4097, 128, 3333, 700]
+    c = Cache(lengths, 16, 4, dim, dtype, seed=dim)
+    rows = [4, 9, 1, 30, 2, 17]
+    q = randn(gen(11), sum(rows), 8, dim).to(act)
+    want, _ = check_chunk(c, q, starts_of(rows), lengths)
+    args = q.cuda(), c.handle, ints(starts_of(rows)), ints(lengths)
+    keys, outs = c.gk.reshape(-1).view(torch.uint8), [fresh(q)[0] for _ in range(40)]
+    flush = torch.empty(300 << 20, dtype=torch.uint8, device="cuda")
+    for i, out in enumerate(outs):
+        flush.zero_()  # out of L2, then every other call some of the keys back into it
+        if i % 2:
+            keys[: len(keys) // 3].max()
+        w4.w4a4_chunk_attention(*args, out)
+    torch.cuda.synchronize()
+    assert w4.w4a4_device_status() == 0 and all(torch.equal(out, want) for out in outs)
+
+
 def test_chunk_of_one_token_is_the_paged_attention():
     lengths = [700, 33, 1, 0, 2049]
     c = Cache(lengths, 16, 2, 128, F16, seed=4)

@@ -999,10 +999,21 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
                 if (!E4M3) fence_proxy_async_smem();  // copies of some went through the generic proxy
                 return true;
             };
-            auto release = [&](uint32_t at) {  // once by each stream
+            // Both streams' threads go through all stages in their order and each gives every one back: a
+            // thread that left the other's out would wait for a later use of the same place by a
+            // parity that the use before the other's has too.
+            auto release = [&](uint32_t at) {
                 mma_commit(empty(at % P::kStages));
-                if (!shared) mbar_arrive(empty(at % P::kStages));
+                if (P::kStreams == 1) mbar_arrive(empty(at % P::kStages));
             };
+            auto see = [&](uint32_t at) {  // a stage of the other stream
+                if (!wait1(full(at % P::kStages), at / P::kStages & 1)) return false;
+                mbar_arrive(empty(at % P::kStages));
+                return true;
+            };
+            const bool alternate = P::kStreams == 2 && !shared;
+            auto see_keys = [&](int t) { return !alternate || t >= tiles || see(keys_at(t)); };
+            auto see_values = [&](int t) { return !alternate || t >= tiles || see(values_at(t)); };
             if (!wait1(q_full, q_phase)) return;
             q_phase ^= 1;
             fence_proxy_async_smem();
@@ -1038,12 +1049,14 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
             auto pass = [&]() {
                 if (P::kStreams == 2) mbar_arrive(turn(stream ^ 1));
             };
+            if (stream == 1 && !see_keys(0)) return;
             for (int x = 0; x < min(kAhead, mine); ++x)
                 if (!keys_ready(x)) return;
             if (!my_turn()) return;
             for (int x = 0; x < min(kAhead, mine); ++x) scores(x);
             pass();
             for (int x = 0; x < min(kAhead, mine); ++x) release_keys(x);
+            if (stream == 0 ? !see_keys(1) : !see_values(0) || !see_keys(2)) return;
             for (int x = 0; x < max(mine, other); ++x) {
                 if (x >= mine) {
                     if (!my_turn()) return;
@@ -1054,7 +1067,7 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
                 const uint32_t at = values_at(first + x * step);
                 for (int half = 0; half < P::kHalves; ++half)
                     if (!ready(at + half)) return;
-                if (x + kAhead < mine && !keys_ready(x + kAhead)) return;
+                if (P::kStreams == 2 && x + kAhead < mine && !keys_ready(x + kAhead)) return;
                 if (x == 0 && n_o > 0 && !wait1(o_free, (n_o - 1) & 1)) return;  // the last unit's output has been read
 #pragma unroll
                 for (int part = 0; part < 2; ++part) {
@@ -1070,16 +1083,18 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
                 p_phase ^= 1u << buf;
                 if constexpr (P::kStreams == 1) mma_commit(pv_done);
                 if (x == mine - 1) mma_commit(o_full(stream));
+                if constexpr (P::kStreams == 1) {  // nobody waits for a turn: the values' room first
+                    for (int half = 0; half < P::kHalves; ++half) release(at + half);
+                    if (x + kAhead < mine && !keys_ready(x + kAhead)) return;
+                }
                 if (x + kAhead < mine) scores(x + kAhead);
                 pass();
                 if (x + kAhead < mine) release_keys(x + kAhead);
-                for (int half = 0; half < P::kHalves; ++half) release(at + half);
+                if constexpr (P::kStreams == 2) release(at);
+                if (!see_values(first + x * step + 1) || !see_keys(first + x * step + 3)) return;
             }
             for (int t = mine; shared && t < tiles; ++t) {  // tiles of the other stream alone
-                if (!ready(keys_at(t))) return;
-                mbar_arrive(empty(keys_at(t) % P::kStages));
-                if (!ready(values_at(t))) return;
-                mbar_arrive(empty(values_at(t) % P::kStages));
+                if (!see(keys_at(t)) || !see(values_at(t))) return;
             }
             ++n_o;
             stages += 2 * P::kHalves * tiles;

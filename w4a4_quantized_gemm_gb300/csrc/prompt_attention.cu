@@ -1,25 +1,30 @@
 // Entry of the attentions over packed prompts and of chunks over a paged cache
 // (prompt_attention.cuh).
-#include "prompt_attention.cuh"
+#include "kernels.h"
+#include "prompt_args.cuh"
 
 namespace w4a4 {
 namespace {
 
 using prompt::Args;
 
-template <class T, bool E4M3>
-w4a4_status launch_d(Args& A, int dim, cudaStream_t s) {
+w4a4_status run(Args& A, int dim, bool bf16, bool e4m3, cudaStream_t s) {
     switch (dim) {
-        case 64: return prompt::run<64, T, E4M3>(A, s);
-        case 96: return prompt::run<96, T, E4M3>(A, s);
-        case 128: return prompt::run<128, T, E4M3>(A, s);
-        default: return prompt::run<256, T, E4M3>(A, s);
+        case 64: return prompt::run_64(A, bf16, e4m3, s);
+        case 96: return prompt::run_96(A, bf16, e4m3, s);
+        case 128: return prompt::run_128(A, bf16, e4m3, s);
+        default: return prompt::run_256(A, bf16, e4m3, s);
     }
 }
 
 }  // namespace
 
-w4a4_status prompt_read_and_clear_status() { return take_status_word(prompt::g_prompt_status); }
+w4a4_status prompt_read_and_clear_status() {
+    w4a4_status first = W4A4_OK;  // every word is read: reading clears it
+    for (const w4a4_status st : {prompt::status_64(), prompt::status_96(), prompt::status_128(), prompt::status_256()})
+        if (first == W4A4_OK) first = st;
+    return first;
+}
 
 w4a4_status launch_prompt_attention(const w4a4_prompt_attention_args& a, cudaStream_t s) {
     Args A;
@@ -33,7 +38,7 @@ w4a4_status launch_prompt_attention(const w4a4_prompt_attention_args& a, cudaStr
     A.tokens = a.tokens, A.seqs = a.seqs, A.q_heads = a.q_heads, A.kv_heads = a.kv_heads, A.window = a.window;
     A.group = a.q_heads / a.kv_heads, A.by_group = Divisor(A.group);
     A.causal = a.causal != 0;
-    return a.dtype == W4A4_F16 ? launch_d<F16, false>(A, a.head_dim, s) : launch_d<BF16, false>(A, a.head_dim, s);
+    return run(A, a.head_dim, a.dtype == W4A4_BF16, false, s);
 }
 
 w4a4_status launch_chunk_attention(const w4a4_kv_cache& c, const w4a4_chunk_attention_args& a, cudaStream_t s) {
@@ -59,8 +64,7 @@ w4a4_status launch_chunk_attention(const w4a4_kv_cache& c, const w4a4_chunk_atte
     A.causal = a.causal != 0;
     if (attention_parts_bytes() < sizeof(float) * prompt::kMaxParts * prompt::kPartFloats + 32 * prompt::kMaxParts)
         return W4A4_ERR_WORKSPACE;
-    if (a.dtype == W4A4_F16) return e4m3 ? launch_d<F16, true>(A, c.head_dim, s) : launch_d<F16, false>(A, c.head_dim, s);
-    return e4m3 ? launch_d<BF16, true>(A, c.head_dim, s) : launch_d<BF16, false>(A, c.head_dim, s);
+    return run(A, c.head_dim, a.dtype == W4A4_BF16, e4m3, s);
 }
 
 }  // namespace w4a4

@@ -32,6 +32,7 @@
 #include "elem.cuh"
 #include "kernels.h"
 #include "launch.cuh"
+#include "prompt_args.cuh"
 #include "tc_ptx.cuh"
 
 namespace w4a4 {
@@ -42,37 +43,6 @@ constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint32_t kSuspendNs = 20000;
 constexpr int kSoftmaxWarps = 8;
 constexpr int kLostTiles = 16;
-constexpr int kMaxParts = 156;             // of a call
-constexpr int kPartFloats = 256 * 130;     // of one: [rows][D] outputs, [256] maxima, [256] sums
-
-// Keys and values: rows of the packed prompts (table NULL), or of a paged cache.
-struct Keys {
-    const char* pool[2] = {};              // keys, values
-    int64_t page_stride[2] = {};           // in bytes, and so below
-    int token_stride[2] = {}, head_stride[2] = {};
-    const float* scale[2] = {};            // of E4M3 rows, per key-value head
-    const int32_t* table = nullptr;
-    int64_t table_stride = 0;
-    int page_size = 1, pages = 0, longest = 0;
-    int box = 0;                           // keys that one copy of the tensor maps brings, 0: there are no maps
-    Divisor by_page;
-};
-
-struct Args {
-    Keys keys;
-    const char* q;
-    char* out;
-    float* lse;
-    const int32_t *starts, *lengths = nullptr;
-    float* parts = nullptr;                // NULL: units are not split
-    int4* parts_of = nullptr;              // [kMaxParts][2]: (begin, head, row0, rows), (first part, parts of the unit)
-    int64_t q_token, q_head, o_token, o_head;  // elements
-    float scale;
-    int tokens, seqs, q_heads, kv_heads, group, window;
-    bool causal;
-    Divisor by_group;
-    bool q_boxes = false;                  // queries come by the copy engine: 128 rows are whole tokens
-};
 
 struct Sequence {
     int begin, rows, length;               // its rows [begin, begin + rows) of q and its keys
@@ -178,6 +148,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
+// One of each translation unit: there is one a head dimension.
 static __device__ int g_prompt_status = 0;
 
 // Where 16-byte piece c of a row is in a tile of planes of 128 rows of 128 bytes.
@@ -344,7 +315,7 @@ __device__ __forceinline__ Share share_out(const Args& A, const Sequence& mine) 
         });
         if (rows == 256 && tiles < 8 * ctas) continue;
         r.rows = rows;
-        int piece = max(2, int(ceilf(tiles / ctas)));
+        int piece = max(4, int(ceilf(tiles / ctas)));
         for (int tries = 0; tries < 8; ++tries) {
             const float all = A.kv_heads * sum_over_sequences(A, mine, [&](const Sequence& s) {
                 return float(blocks_of(A, s, rows)) * max(1, quotient(most_tiles(A, s) + piece - 1, piece));
@@ -385,6 +356,7 @@ __device__ __forceinline__ void sort_sequences(const Args& A, const Sequence& mi
 // Where unit `want` is, for numbers that grow from call to call (a warp).
 struct Walk {
     const uint8_t* order;    // of the sequences, nullptr: as they are
+    const Sequence& mine;    // this lane's of the first 32, if they are as they are
     int base = -32, before = 0;  // sequences from `base` on, and the units before them
     int b = 0, pieces = 1, units = 0, upto = 0;  // of this lane's: number, pieces of a unit, units, those up to it
     Sequence s{0, 0, 0};
@@ -400,7 +372,7 @@ struct Walk {
                 if (b < A.seqs) {
                     bool bad;
                     if (order) b = order[b];
-                    s = sequence(A, b, bad);
+                    s = order || base > 0 ? sequence(A, b, bad) : mine;
                     if (share.piece > 0) pieces = max(1, quotient(most_tiles(A, s) + share.piece - 1, share.piece));
                     units = blocks_of(A, s, share.rows) * A.kv_heads * pieces;
                 }
@@ -554,7 +526,7 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
         const bool sorted = A.seqs > 1 && A.seqs <= kSorted;
         if (sorted) sort_sequences(A, mine, order);
         const Share share = share_out<D>(A, mine);
-        Walk walk{sorted ? order : nullptr};
+        Walk walk{sorted ? order : nullptr, mine};
         for (uint32_t n = 0;; ++n) {
             const int turn = int(n & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
             Unit U{};
@@ -1460,14 +1432,15 @@ w4a4_status run(Args& A, cudaStream_t s) {
         ready.fetch_or(uint64_t(1) << dev, std::memory_order_release);
     }
     // A CTA per SM, or one per unit where there can be fewer.  Units are fewer than SMs if the
-    // rows of all sequences are; then parts of them are worth a second launch where the cache
-    // can be long.
+    // rows of all sequences are; then parts of them (of four tiles or more) are worth a second launch
+    // where the cache can be long: 5 tokens behind 1500 of one sequence take 17.8 us, 22.9 whole;
+    // behind 3000 19.8 and 37, with parts of two tiles 21.6; behind 700 15.5 either way.
     const int sms = std::min(device_sm_count(), kMaxParts);
     const int64_t rows = int64_t(A.tokens) * A.group;
     const int64_t most = A.kv_heads * ((rows + kTile - 1) / kTile + A.seqs);
     const int64_t least = A.kv_heads * ((rows + P::kStreams * kTile - 1) / (P::kStreams * kTile));
     const int64_t keys = A.window > 0 ? std::min(int64_t(A.keys.longest), int64_t(A.window) + A.tokens) : A.keys.longest;
-    if (!(A.parts && least < sms && keys > 4 * kTile)) A.parts = nullptr;
+    if (!(A.parts && least < sms && keys > 8 * kTile)) A.parts = nullptr;
     const int grid = A.parts ? sms : int(std::min(int64_t(sms), most));
     constexpr bool bf16 = std::is_same_v<T, BF16>;
     // Keys and values by the copy engine, eight rows or more a copy, where pages hold so many side by side.
@@ -1492,6 +1465,13 @@ w4a4_status run(Args& A, cudaStream_t s) {
     w4a4_status st = launch<attention_kernel<D, T, E4M3>>(dim3(unsigned(grid)), P::kThreads, P::kBytes, s, A, maps[0], maps[1], maps[2]);
     if (st == W4A4_OK && A.parts) st = launch<join_kernel<D, T, E4M3>>(dim3(unsigned(grid)), 256, 0, s, A);
     return st;
+}
+
+// Entry of one head dimension.
+template <int D>
+w4a4_status run_dim(Args& A, bool bf16, bool e4m3, cudaStream_t s) {
+    if (e4m3) return bf16 ? run<D, BF16, true>(A, s) : run<D, F16, true>(A, s);
+    return bf16 ? run<D, BF16, false>(A, s) : run<D, F16, false>(A, s);
 }
 
 }  // namespace prompt

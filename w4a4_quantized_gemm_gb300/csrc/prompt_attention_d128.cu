@@ -1,0 +1,11 @@
+// Prompt and chunk attention of 128-wide heads.
+#include "prompt_attention.cuh"
+
+namespace w4a4 {
+namespace prompt {
+
+w4a4_status run_128(Args& A, bool bf16, bool e4m3, cudaStream_t s) { return run_dim<128>(A, bf16, e4m3, s); }
+w4a4_status status_128() { return take_status_word(g_prompt_status); }
+
+}  // namespace prompt
+}  // namespace w4a4

@@ -472,7 +472,8 @@ w4a4_status w4a4_qk_rope(const w4a4_qk_rope_args* args, cudaStream_t stream);
  * outside all sequences are neither read nor written.
  * q, k, v, out: dtype W4A4_F16 or W4A4_BF16, head_dim 64, 96, 128 or 256, row (i, h) at
  * i * token_stride + h * head_stride elements (16-byte aligned); lse fp32 [tokens][q_heads]
- * or NULL.  q_heads % kv_heads == 0.  out overlaps no input.  Scores, statistics and sums
+ * or NULL.  q_heads % kv_heads == 0.  out overlaps no input, and its rows not each other
+ * (refused, as where neither stride goes around the other's rows).  Scores, statistics and sums
  * are fp32, the probabilities go into the product as one number of dtype.  starts that
  * decrease or leave [0, tokens] are clamped (rows that two sequences then share hold either
  * one's result) and set W4A4_ERR_INDEX.  tokens == 0 or seqs == 0: no-op. */
@@ -581,9 +582,9 @@ w4a4_status w4a4_debug_forward_partials(const uint16_t* X, const void* packed, s
                                         int K, int r, void* act_ws, size_t act_ws_bytes, int32_t* P,
                                         cudaStream_t stream);
 /* Reads and clears the device status words written by bounded waits
- * (W4A4_ERR_TIMEOUT) and by the paged-cache kernels, where an index they read
- * from device memory lay outside its table (W4A4_ERR_INDEX); W4A4_OK if
- * neither.  Synchronises the device. */
+ * (W4A4_ERR_TIMEOUT) and by the kernels that read pages, positions, lengths or
+ * starts from device memory, where one lay outside its range (W4A4_ERR_INDEX);
+ * W4A4_OK if neither.  Synchronises the device. */
 w4a4_status w4a4_device_status(void);
 
 /* ---- dispatch and diagnostics ([INT4] "Failure modes": log the kernel chosen) */

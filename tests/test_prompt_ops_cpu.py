@@ -77,6 +77,7 @@ def test_struct_layouts_match_the_header(tmp_path):
     (dict(q_out_token_stride=0), 1), (dict(q_out_head_stride=64), 1), (dict(k_out_token_stride=120), 1),
     (dict(q_out=A), 1), (dict(k_out=A + 4096), 1),  # in place with other strides
     (dict(q_out=A + 16384), 1), (dict(q_out=A + 4096), 1), (dict(k_out=A), 1),  # an output that is another's or another's input
+    (dict(q_out_token_stride=128), 1), (dict(k_out_token_stride=896), 1),  # rows of two tokens in one place
     (dict(q_heads=1 << 17), 2), (dict(tokens=0), 0), (dict(q_heads=0, kv_heads=0), 0),
 ])
 def test_rope_refusals(L, over, status):
@@ -93,6 +94,7 @@ def test_rope_refusals(L, over, status):
     (dict(v=A + 8), 3), (dict(out=A + 4), 3), (dict(lse=A + 2), 3), (dict(starts=A + 1), 3),
     (dict(v_token_stride=4100), 3), (dict(q_head_stride=-128), 3), (dict(k_token_stride=1 << 30), 3),
     (dict(out_token_stride=0), 1), (dict(out_head_stride=120), 1), (dict(out=A), 1), (dict(out=A + 4096), 1),
+    (dict(out_token_stride=1920), 1), (dict(out_token_stride=128, out_head_stride=699 * 128), 1),  # two rows in one place
     (dict(out=A + 6144), 1), (dict(tokens=0), 0), (dict(seqs=0), 0), (dict(tokens=0, q=0), 0),
 ])
 def test_prompt_refusals(L, over, status):
@@ -107,6 +109,7 @@ def test_prompt_refusals(L, over, status):
     (dict(lengths=0), 1), (dict(workspace=0), 1), (dict(workspace_bytes=1000), 4), (dict(workspace=A + 8), 3),
     (dict(q=A + 4), 3), (dict(lse=A + 2), 3), (dict(starts=A + 2), 3), (dict(lengths=A + 1), 3), (dict(q_head_stride=4), 3),
     (dict(out_token_stride=0), 1), (dict(out_head_stride=64), 1), (dict(out=A + 64), 1), (dict(out=A), 1),
+    (dict(out_token_stride=128), 1), (dict(out_token_stride=2040), 1),
     (dict(tokens=0), 0),
 ])
 def test_chunk_refusals(L, over, status):
@@ -136,6 +139,9 @@ def test_good_calls_reach_the_device_check(L):
     assert L.w4a4_prompt_attention(prompt(), None) == GOOD
     assert L.w4a4_prompt_attention(prompt(causal=0, scale=-1.0, dtype=1, lse=A), None) == GOOD
     assert L.w4a4_prompt_attention(prompt(window=1 << 30, k_head_stride=0, v_token_stride=0), None) == GOOD
+    heads_first = dict(out_token_stride=128, out_head_stride=700 * 128)
+    assert L.w4a4_prompt_attention(prompt(**heads_first), None) == GOOD
+    assert L.w4a4_chunk_attention(cache(), chunk(**heads_first), None) == GOOD
     for kind in (0, 1, 3):
         act = 1 if kind == 1 else 0
         assert L.w4a4_chunk_attention(cache(dtype=kind), chunk(dtype=act), None) == GOOD

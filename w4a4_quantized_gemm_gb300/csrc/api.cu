@@ -100,6 +100,13 @@ void used(int64_t& stride, int64_t n) { stride = n > 1 ? stride : 0; }
 // Rows of `dim` elements that n indices reach at this stride, to be written: no two may overlap.
 bool apart(int64_t stride, int64_t n, int dim) { return n <= 1 || stride >= dim; }
 
+// ... and rows (i, h) of n x heads: one of the two lies within the other's steps.
+bool apart(int64_t stride, int64_t n, int64_t head_stride, int64_t heads, int dim) {
+    if (n < 1 || heads < 1) return true;
+    if (!apart(stride, n, dim) || !apart(head_stride, heads, dim)) return false;
+    return n == 1 || heads == 1 || stride >= (heads - 1) * head_stride + dim || head_stride >= (n - 1) * stride + dim;
+}
+
 // Rows of the prompt and chunk attention: their (row, head) pairs, and the pieces that they
 // make with every sequence's odd end, are counted in 31 bits.
 bool many_rows_fit(int tokens, int seqs, int q_heads) {
@@ -664,11 +671,9 @@ w4a4_status w4a4_qk_rope(const w4a4_qk_rope_args* args, cudaStream_t stream) {
     for (const int64_t s : {a->q_token_stride, a->q_head_stride, a->k_token_stride, a->k_head_stride,
                             a->q_out_token_stride, a->q_out_head_stride, a->k_out_token_stride, a->k_out_head_stride})
         if (!good_stride(s, 2)) return W4A4_ERR_MISALIGNED;
-    for (const auto& [stride, n] : {std::pair{a->q_out_token_stride, a->q_heads > 0 ? a->tokens : 0},
-                                    {a->q_out_head_stride, a->q_heads},
-                                    {a->k_out_token_stride, a->kv_heads > 0 ? a->tokens : 0},
-                                    {a->k_out_head_stride, a->kv_heads}})
-        if (!apart(stride, n, a->head_dim)) return W4A4_ERR_INVALID_ARG;
+    if (!apart(a->q_out_token_stride, a->tokens, a->q_out_head_stride, a->q_heads, a->head_dim) ||
+        !apart(a->k_out_token_stride, a->tokens, a->k_out_head_stride, a->kv_heads, a->head_dim))
+        return W4A4_ERR_INVALID_ARG;
     // an output that is its own input has that one's strides, and no output is another's
     if (a->q_heads > 0 && a->q == a->q_out &&
         (a->q_token_stride != a->q_out_token_stride || a->q_head_stride != a->q_out_head_stride))
@@ -706,7 +711,7 @@ w4a4_status w4a4_prompt_attention(const w4a4_prompt_attention_args* args, cudaSt
     for (const int64_t s : {a->q_token_stride, a->q_head_stride, a->k_token_stride, a->k_head_stride,
                             a->v_token_stride, a->v_head_stride, a->out_token_stride, a->out_head_stride})
         if (!good_stride(s, 2)) return W4A4_ERR_MISALIGNED;
-    if (!apart(a->out_token_stride, a->tokens, a->head_dim) || !apart(a->out_head_stride, a->q_heads, a->head_dim))
+    if (!apart(a->out_token_stride, a->tokens, a->out_head_stride, a->q_heads, a->head_dim))
         return W4A4_ERR_INVALID_ARG;
     if (a->out == a->q || a->out == a->k || a->out == a->v) return W4A4_ERR_INVALID_ARG;
     w4a4_status st = check_device();
@@ -738,7 +743,7 @@ w4a4_status w4a4_chunk_attention(const w4a4_kv_cache* cache, const w4a4_chunk_at
         return W4A4_ERR_MISALIGNED;
     for (const int64_t s : {a->q_token_stride, a->q_head_stride, a->out_token_stride, a->out_head_stride})
         if (!good_stride(s, 2)) return W4A4_ERR_MISALIGNED;
-    if (!apart(a->out_token_stride, a->tokens, cache->head_dim) || !apart(a->out_head_stride, a->q_heads, cache->head_dim))
+    if (!apart(a->out_token_stride, a->tokens, a->out_head_stride, a->q_heads, cache->head_dim))
         return W4A4_ERR_INVALID_ARG;
     if (a->out == a->q || a->out == cache->k || a->out == cache->v) return W4A4_ERR_INVALID_ARG;
     if (a->workspace_bytes < attention_workspace_bytes(cache->seqs, a->q_heads, cache->kv_heads))

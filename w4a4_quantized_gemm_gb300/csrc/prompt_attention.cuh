@@ -18,9 +18,16 @@
 //    with the values.  A row of scores is one thread's: 128 registers, no exchange.
 //  * One pass: the running maximum that is subtracted is renewed, and the output rescaled,
 //    only where the scores exceed it by more than kSlack (as a power of two).
-//  * Four warps copy keys and values, 16 bytes a lane, into a ring of stages: any stride, any
-//    page size, E4M3 rows turned into 16-bit ones on the way.  Rows that no query of the unit
-//    sees are not read: they are zeros.
+//  * Keys and values come into a ring of stages by tensor maps, in boxes of 32, 16 or 8 rows (a
+//    page's), where strides and page sizes allow it, else 16 bytes a lane.  E4M3 rows go into a
+//    ring of their own and eight warps turn them into 16-bit ones.  Rows that no query of the
+//    unit sees are zeros.
+//
+// What bounds it: the tensor cores, where rows and keys are many.  A 128 x 128 tile of scores and its
+// product with the values is 16 products of 128 x 128 x 16 at D = 128, 64 cycles each, and four
+// warps need about 1700 cycles for its probabilities, hidden behind the other stream's products.
+// 8192 causal tokens of 32 heads of 128: 410 us, 1.34 PFLOP/s, 0.71 of what a library's matrix
+// product reaches.  Calls of a few rows are bound by what a launch, the plan and cold code take.
 //  * Values of masked keys meet probabilities of zero in the product, and zero times infinity
 //    or NaN is not zero.  A row whose output is not finite is computed again from its own keys
 //    alone, if keys that it does not see hold such values (careful_row).
@@ -73,13 +80,16 @@ struct Plan {
     static constexpr int kStreams = D == 256 ? 1 : 2;
     static constexpr int kQTile = kHalves * kStage;
     static constexpr int kQ = kStreams * kQTile;
+    // Both rings fill the shared memory; 8-bit rows in flight gain less from room than 16-bit ones (D = 128
+    // with stages 3 + 4: 202 us for the 182 below).
     static constexpr int kStages = E4M3 ? (D == 64 ? 6 : 4) : D == 64 ? 11 : 5;
-    static constexpr int kRawStages = E4M3 ? (D == 64 ? 8 : 2) : 0;
+    static constexpr int kRawStages = E4M3 ? (D == 64 ? 10 : 2) : 0;
     static constexpr int kRawStage = kTile * kDs;
     static constexpr bool kRawSwizzled = kDs == 128;
     static constexpr int kRawRing = kRawStages > 0 ? kRawStages : 1;
-    // warps: softmax, copies (twice as many to widen 8-bit rows: 64 streams of 4 tokens ... us with four), then
-    // one that plans, two that issue products, one for the ring of 8-bit rows
+    // warps: softmax, copies (twice as many to widen 8-bit rows: 64 sequences of 4 tokens behind up to 8191,
+    // 32 heads for 8, take 236 us with four and 182 with eight), then one that plans, two that issue
+    // products, one for the ring of 8-bit rows
     static constexpr int kCopyWarps = E4M3 ? 8 : 4;
     static constexpr int kMmaWarp = kSoftmaxWarps + kCopyWarps, kPlanWarp = kMmaWarp + 1, kRawWarp = kMmaWarp + 3;
     static constexpr int kThreads = 32 * (kMmaWarp + 4);
@@ -332,8 +342,8 @@ __device__ __forceinline__ Share share_out(const Args& A, const Sequence& mine) 
 }
 
 // Sequences with the longest units first, for up to kSorted of them: what is left for the last
-// round is short then (six chunks of 417 tokens, the later ones behind more, D = 256: 186 us, and
-// ... in the sequences' order).
+// round is short then (six chunks of 417 tokens, the later ones behind more, D = 256: 99 us, 150 in
+// the sequences' order; 64 of 4 tokens behind up to 8191: 182 and 290).
 constexpr int kSorted = 64;
 __device__ __forceinline__ void sort_sequences(const Args& A, const Sequence& mine, uint8_t* order) {
     const int lane = threadIdx.x & 31;
@@ -363,7 +373,7 @@ struct Walk {
     __device__ __forceinline__ bool find(const Args& A, const Share& share, int want, Unit& U) {
         const int lane = threadIdx.x & 31;
         while (base < A.seqs) {
-            const uint32_t beyond = __ballot_sync(0xffffffffu, before + upto > want);
+            const uint32_t beyond = __ballot_sync(0xffffffffu, upto > want - before);
             if (beyond == 0) {
                 before += __shfl_sync(0xffffffffu, upto, 31);
                 base += 32;
@@ -376,18 +386,19 @@ struct Walk {
                     if (share.piece > 0) pieces = max(1, quotient(most_tiles(A, s) + share.piece - 1, share.piece));
                     units = blocks_of(A, s, share.rows) * A.kv_heads * pieces;
                 }
-                upto = units;
+                upto = units;  // (sequences that overlap, which is an error, can have more than 2^31 in all)
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
                     const int v = __shfl_up_sync(0xffffffffu, upto, o);
-                    if (lane >= o) upto += v;
+                    if (lane >= o) asm("add.sat.s32 %0, %0, %1;\n" : "+r"(upto) : "r"(v));
                 }
                 continue;
             }
             const int at = __ffs(beyond) - 1;
             auto of = [&](int v) { return __shfl_sync(0xffffffffu, v, at); };
+            const int prior = __shfl_sync(0xffffffffu, upto, max(0, at - 1));
             fill(A, share, of(b), Sequence{of(s.begin), of(s.rows), of(s.length)}, of(units), of(pieces), want,
-                 want - before - of(upto - units), U);
+                 want - before - (at > 0 ? prior : 0), U);
             return true;
         }
         return false;
@@ -627,7 +638,7 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
 
     // By the copy engine, each warp 32 rows of a tile, a box of K.box of them a lane; boxes that
     // are not all there by the warp's own loads.  (One warp for all of them has fewer instructions
-    // but sends small boxes more slowly: pages of 24, D = 256 326 us and 180.)
+    // but sends small boxes more slowly: 1.8 times the time for pages of 24, D = 256.)
     auto copy_boxes = [&]() {
         const Keys& K = A.keys;
         const int box = K.box, boxes = 32 / box, w = warp - kSoftmaxWarps, my = 32 * w + lane * box;
@@ -782,7 +793,7 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
             n_tile += tiles;
         }
     };
-    // ... and turned into 16-bit rows by four warps.
+    // ... and turned into 16-bit rows by eight warps.
     auto widen = [&]() {
         uint32_t n_read = 0;
         const volatile uint32_t* const there = reinterpret_cast<const volatile uint32_t*>(smem + P::kThere);
@@ -836,8 +847,9 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
         }
     };
 
-    // By loads of four warps, 32 rows of a tile each: pages of any size, E4M3 rows turned into
-    // 16-bit ones.
+    // By loads of four warps, 32 rows of a tile each, where there are no tensor maps: pages that are
+    // not whole times eight, strides that a map cannot have.  E4M3 rows are turned into 16-bit ones
+    // on the way.
     auto copy_rows = [&]() {
         constexpr int kSize = E4M3 ? 1 : 2;
         constexpr int kPieces = P::kDs * kSize / 16;  // of a stage's row
@@ -907,17 +919,22 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
                     }
                     cp_async_mbar_arrive_noinc(full(st));
                 } else {
-                    uint4 raw[kPieces];
+                    // (all at once do not fit the warp's registers)
+                    constexpr int kAtOnce = kPieces % 4 == 0 ? 4 : 2;
+#pragma unroll 1
+                    for (int from = 0; from < kPieces; from += kAtOnce) {
+                        uint4 raw[kAtOnce];
 #pragma unroll
-                    for (int i = 0; i < kPieces; ++i) {
-                        const int id = i * 32 + lane, r = id / kPieces, c = id - r * kPieces;
-                        const char* src = source(r, c);
-                        raw[i] = there >> r & 1 ? ldg_stream_v4(src) : make_uint4(0, 0, 0, 0);
-                    }
+                        for (int i = 0; i < kAtOnce; ++i) {
+                            const int id = (from + i) * 32 + lane, r = id / kPieces, c = id - r * kPieces;
+                            const char* src = source(r, c);
+                            raw[i] = there >> r & 1 ? ldg_stream_v4(src) : make_uint4(0, 0, 0, 0);
+                        }
 #pragma unroll
-                    for (int i = 0; i < kPieces; ++i) {
-                        const int id = i * 32 + lane, r = id / kPieces, c = id - r * kPieces, row = 32 * w + r;
-                        widen16(raw[i], smem + (to - base), row, c, false);
+                        for (int i = 0; i < kAtOnce; ++i) {
+                            const int id = (from + i) * 32 + lane, r = id / kPieces, c = id - r * kPieces, row = 32 * w + r;
+                            widen16(raw[i], smem + (to - base), row, c, false);
+                        }
                     }
                     fence_proxy_async_smem();
                     mbar_arrive(full(st));
@@ -933,8 +950,8 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
     // The products of a stream, issued by one thread: the queue of the tensor cores holds two or
     // three, so what this thread does between the arrival of the probabilities and the next
     // scores leaves them idle, but for the other stream's.  With both streams' products from one
-    // thread 8192 tokens of 32 heads of 128 take 450 us, and with descriptors that the compiler
-    // sums up 690.
+    // thread 8192 tokens of 32 heads of 128 took 450 us (410 now), and with descriptors that the
+    // compiler sums up 690.
     auto multiply = [&](const int stream) {
         constexpr uint32_t kQk = idesc_m128_16bit(kTile, BF, false);
         constexpr uint32_t kPv = idesc_m128_16bit(P::kDs, BF, true);

@@ -23,14 +23,13 @@
 //    ring of their own and eight warps turn them into 16-bit ones.  Rows that no query of the
 //    unit sees are zeros.
 //
-// What bounds it: the tensor cores, where rows and keys are many.  A 128 x 128 tile of scores and its
-// product with the values is 16 products of 128 x 128 x 16 at D = 128, 64 cycles each, and four
-// warps need about 1700 cycles for its probabilities, hidden behind the other stream's products.
-// 8192 causal tokens of 32 heads of 128: 410 us, 1.34 PFLOP/s, 0.71 of what a library's matrix
-// product reaches.  Calls of a few rows are bound by what a launch, the plan and cold code take.
-//  * Values of masked keys meet probabilities of zero in the product, and zero times infinity
-//    or NaN is not zero.  A row whose output is not finite is computed again from its own keys
-//    alone, if keys that it does not see hold such values (careful_row).
+// What bounds it, where rows and keys are many: a product of 128 x 128 x 16 takes 64 cycles and reads
+// 8 KB of shared memory (4 KB with the first operand in tensor memory), which is all that the port
+// gives, and the copies come on top; 16 of them are a tile's at D = 128.  Four warps take 1700 to
+// 2000 cycles for a tile's probabilities, half of it powers, behind the other stream's products:
+// 3300 cycles for a tile of both.  8192 causal tokens of 32 heads of 128: 410 us, 1.34 PFLOP/s, 0.71
+// of what a library's matrix product reaches.  Calls of a few rows are bound by what a launch, the
+// plan and cold code take.
 #pragma once
 #include <algorithm>
 #include <atomic>

@@ -309,7 +309,9 @@ __device__ __forceinline__ Share share_out(const Args& A, const Sequence& mine) 
         return A.kv_heads * sum_over_sequences(A, mine, [&](const Sequence& s) { return float(blocks_of(A, s, rows)); });
     };
     Share r{128, 0};
-    // 256 rows a unit where there are units enough, or (below) tiles enough to split them into
+    // 256 rows a unit where there are units enough, or (below) tiles enough to split them into: 8192
+    // causal tokens of 32 heads for 8 take 410 us and 470 with 128, eight texts of 1500 both ways with
+    // 16 heads of 64 141 and 153, though the last round of their units is 5% full.
     float units = kStreams == 2 ? units_of(256) : 0.f;
     if (units >= ctas) r.rows = 256;
     if (!A.parts || r.rows == 256) return r;

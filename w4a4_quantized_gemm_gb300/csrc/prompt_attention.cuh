@@ -80,14 +80,14 @@ struct Plan {
     static constexpr int kQTile = kHalves * kStage;
     static constexpr int kQ = kStreams * kQTile;
     // Both rings fill the shared memory; 8-bit rows in flight gain less from room than 16-bit ones (D = 128
-    // with stages 3 + 4: 202 us for the 182 below).
+    // with stages 3 + 4: 202 us for the 181 below).
     static constexpr int kStages = E4M3 ? (D == 64 ? 6 : 4) : D == 64 ? 11 : 5;
     static constexpr int kRawStages = E4M3 ? (D == 64 ? 10 : 2) : 0;
     static constexpr int kRawStage = kTile * kDs;
     static constexpr bool kRawSwizzled = kDs == 128;
     static constexpr int kRawRing = kRawStages > 0 ? kRawStages : 1;
     // warps: softmax, copies (twice as many to widen 8-bit rows: 64 sequences of 4 tokens behind up to 8191,
-    // 32 heads for 8, take 236 us with four and 182 with eight), then one that plans, two that issue
+    // 32 heads for 8, take 236 us with four and 181 with eight), then one that plans, two that issue
     // products, one for the ring of 8-bit rows
     static constexpr int kCopyWarps = E4M3 ? 8 : 4;
     static constexpr int kMmaWarp = kSoftmaxWarps + kCopyWarps, kPlanWarp = kMmaWarp + 1, kRawWarp = kMmaWarp + 3;
@@ -110,6 +110,7 @@ struct Plan {
     // Copies are at most the rings ahead of the scores' products, and those two tiles ahead of
     // the probabilities.
     static_assert(kLostTiles >= (kStages + kRawStages) / 2 + 5, "a word is read before it is written again");
+    static_assert(kThere % 16 == 0, "read four words at once");
     static_assert(kBytes <= 227 * 1024, "shared memory");
     static_assert(kStages >= 2 * kHalves, "the values of a tile and the keys of the next are waited for together");
     // tensor memory: a stream's scores (and probabilities) and its output
@@ -344,7 +345,7 @@ __device__ __forceinline__ Share share_out(const Args& A, const Sequence& mine) 
 
 // Sequences with the longest units first, for up to kSorted of them: what is left for the last
 // round is short then (six chunks of 417 tokens, the later ones behind more, D = 256: 99 us, 150 in
-// the sequences' order; 64 of 4 tokens behind up to 8191: 182 and 290).
+// the sequences' order; 64 of 4 tokens behind up to 8191: 181 and 290).
 constexpr int kSorted = 64;
 __device__ __forceinline__ void sort_sequences(const Args& A, const Sequence& mine, uint8_t* order) {
     const int lane = threadIdx.x & 31;
@@ -741,8 +742,9 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
             if (U->tiles == 0 || box == 0) continue;
             const int key0 = U->key0, end = U->end, tiles = U->tiles, head = U->head;
             const int64_t table = U->b * K.table_stride;
-            int page = -1, slot = 0;  // of this lane's box in the next tile
-            auto look_up = [&](int tile) {
+            // of this lane's box in the next tile and the one after it: a look-up takes longer than a tile
+            int page = -1, slot = 0, page2 = -1, slot2 = 0;
+            auto look_up = [&](int tile, int& page, int& slot) {
                 const int j = key0 + tile * kTile + my;
                 page = -1;
                 if (lane < boxes && tile < tiles && j < end) {
@@ -751,7 +753,8 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
                     page = K.table[table + p];
                 }
             };
-            look_up(0);
+            look_up(0, page, slot);
+            look_up(1, page2, slot2);
             int pages[3] = {}, slots[3] = {};  // of a tile and the two before it,
             uint32_t some[3] = {};             // and boxes on pages of the pool
             auto look = [&](int u) {
@@ -768,7 +771,8 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
                     lost[(n_tile + u) % kLostTiles * 4 + lane] = word;
                 }
                 if (bad && lane == 0) atomicExch(&g_prompt_status, int(W4A4_ERR_INDEX));
-                look_up(u + 1);
+                page = page2, slot = slot2;
+                look_up(u + 2, page2, slot2);
             };
             auto send = [&](int kv, int half, int age, int tile) {
                 const int st = n_raw % P::kRawRing;
@@ -797,7 +801,6 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
     // ... and turned into 16-bit rows by eight warps.
     auto widen = [&]() {
         uint32_t n_read = 0;
-        const volatile uint32_t* const there = reinterpret_cast<const volatile uint32_t*>(smem + P::kThere);
         const int t = tid - 32 * kSoftmaxWarps;
         for (uint32_t n = 0;; done_with(n++)) {
             const Unit* const U = unit(n);
@@ -826,13 +829,21 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
                         return 16 * id;
                     }
                 };
+                const uint32_t* const there = reinterpret_cast<const uint32_t*>(smem + P::kThere) + 4 * from;
+                const uint4 rows = *reinterpret_cast<const uint4*>(there);
                 uint4 raw[kPieces];
 #pragma unroll
                 for (int i = 0; i < kPieces; ++i) {
                     int row, c;
                     raw[i] = *reinterpret_cast<const uint4*>(src + place(i, row, c));
-                    if (!(there[4 * from + (row >> 5)] >> (row & 31) & 1)) raw[i] = make_uint4(0, 0, 0, 0);
                 }
+                if ((rows.x & rows.y & rows.z & rows.w) != 0xffffffffu)
+#pragma unroll
+                    for (int i = 0; i < kPieces; ++i) {
+                        int row, c;
+                        place(i, row, c);
+                        if (!(there[row >> 5] >> (row & 31) & 1)) raw[i] = make_uint4(0, 0, 0, 0);
+                    }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(raw_empty(from));
 #pragma unroll

@@ -79,7 +79,8 @@ class W4A4DecoderLayer:
         self.o_out, self.x_mlp, self.down_out, self.h, self.ws = one.o_out, one.x_mlp, one.down_out, one.h, one.ws
 
     def rows(self, n: int) -> _Rows:
-        """The buffers for n rows, made at their first use (before a graph capture, if it is to use them)."""
+        """The buffers for n rows, made at their first use (before a graph capture, if it is to use them)
+        and kept as long as the layer: a captured graph may hold them."""
         if n not in self._rows:
             self._rows[n] = _Rows(self, n)
         return self._rows[n]

@@ -80,14 +80,14 @@ struct Plan {
     static constexpr int kQTile = kHalves * kStage;
     static constexpr int kQ = kStreams * kQTile;
     // Both rings fill the shared memory; 8-bit rows in flight gain less from room than 16-bit ones (D = 128
-    // with stages 3 + 4: 202 us for the 181 below).
+    // with stages 3 + 4 202 us for 182 with those below).
     static constexpr int kStages = E4M3 ? (D == 64 ? 6 : 4) : D == 64 ? 11 : 5;
     static constexpr int kRawStages = E4M3 ? (D == 64 ? 10 : 2) : 0;
     static constexpr int kRawStage = kTile * kDs;
     static constexpr bool kRawSwizzled = kDs == 128;
     static constexpr int kRawRing = kRawStages > 0 ? kRawStages : 1;
     // warps: softmax, copies (twice as many to widen 8-bit rows: 64 sequences of 4 tokens behind up to 8191,
-    // 32 heads for 8, take 236 us with four and 181 with eight), then one that plans, two that issue
+    // 32 heads for 8, took 236 us with four and 182 with eight), then one that plans, two that issue
     // products, one for the ring of 8-bit rows
     static constexpr int kCopyWarps = E4M3 ? 8 : 4;
     static constexpr int kMmaWarp = kSoftmaxWarps + kCopyWarps, kPlanWarp = kMmaWarp + 1, kRawWarp = kMmaWarp + 3;
@@ -345,7 +345,7 @@ __device__ __forceinline__ Share share_out(const Args& A, const Sequence& mine) 
 
 // Sequences with the longest units first, for up to kSorted of them: what is left for the last
 // round is short then (six chunks of 417 tokens, the later ones behind more, D = 256: 99 us, 150 in
-// the sequences' order; 64 of 4 tokens behind up to 8191: 181 and 290).
+// the sequences' order; 64 of 4 tokens behind up to 8191: 182 and 290).
 constexpr int kSorted = 64;
 __device__ __forceinline__ void sort_sequences(const Args& A, const Sequence& mine, uint8_t* order) {
     const int lane = threadIdx.x & 31;
@@ -484,8 +484,11 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
         abort_flag = (base & 1023u) != 0;  // the swizzle's atoms start on 1024-byte boundaries
         never_abort = 0;
         // a copying warp's lanes arrive when their copies have, and one of them once more: for what the engine
-        // brings, or the warp's other words
-        for (int s = 0; s < P::kStages; ++s) mbar_init(full(s), 33 * (E4M3 && A.keys.box > 0 ? kCopyWarps : 4)), mbar_init(empty(s), 2);
+        // brings, or the warp's other words; or one for all, where the warp itself has written
+        for (int s = 0; s < P::kStages; ++s) {
+            mbar_init(full(s), E4M3 ? (A.keys.box > 0 ? kCopyWarps : 4) : 33 * 4);
+            mbar_init(empty(s), 2);
+        }
         mbar_init(q_full, kCopyThreads), mbar_init(q_free, 2);
         mbar_init(o_free, kSoftmaxWarps), mbar_init(pv_done, 1), mbar_init(all_done, P::kStreams);
         mbar_init(ml_full, kSoftmaxWarps), mbar_init(ml_free, kSoftmaxWarps);
@@ -755,11 +758,11 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
             };
             look_up(0, page, slot);
             look_up(1, page2, slot2);
-            int pages[3] = {}, slots[3] = {};  // of a tile and the two before it,
-            uint32_t some[3] = {};             // and boxes on pages of the pool
+            int pages[3] = {}, slots[3] = {};   // of a tile and the two before it,
+            uint32_t some[3] = {}, mine[3] = {};  // boxes on pages of the pool, and which of rows 32 lane .. + 31 are there
             auto look = [&](int u) {
 #pragma unroll
-                for (int k = 2; k > 0; --k) pages[k] = pages[k - 1], slots[k] = slots[k - 1], some[k] = some[k - 1];
+                for (int k = 2; k > 0; --k) pages[k] = pages[k - 1], slots[k] = slots[k - 1], some[k] = some[k - 1], mine[k] = mine[k - 1];
                 if (u >= tiles) return;
                 const bool in = lane < boxes && key0 + u * kTile + my < end, good = in && page >= 0 && page < K.pages;
                 some[0] = __ballot_sync(0xffffffffu, good), pages[0] = page, slots[0] = slot;
@@ -769,24 +772,21 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
                     for (int k = 0; bad != 0 && k < 32; k += box)
                         if (bad >> quotient(32 * lane + k, box) & 1) word |= (0xffffffffu >> (32 - box)) << k;
                     lost[(n_tile + u) % kLostTiles * 4 + lane] = word;
+                    const int have = end - (key0 + u * kTile + 32 * lane);
+                    mine[0] = (have >= 32 ? 0xffffffffu : have > 0 ? (1u << have) - 1 : 0) & ~word;
                 }
                 if (bad && lane == 0) atomicExch(&g_prompt_status, int(W4A4_ERR_INDEX));
                 page = page2, slot = slot2;
                 look_up(u + 2, page2, slot2);
             };
-            auto send = [&](int kv, int half, int age, int tile) {
+            auto send = [&](int kv, int half, int age, int) {
                 const int st = n_raw % P::kRawRing;
                 if (n_raw >= P::kRawRing && !wait(raw_empty(st), (n_raw / P::kRawRing - 1) & 1)) return false;
                 ++n_raw;
                 const uint32_t s = age == 0 ? some[0] : age == 1 ? some[1] : some[2];
                 const int pg = age == 0 ? pages[0] : age == 1 ? pages[1] : pages[2];
                 const int sl = age == 0 ? slots[0] : age == 1 ? slots[1] : slots[2];
-                if (lane < 4) {
-                    const int have = end - (key0 + tile * kTile + 32 * lane);
-                    uint32_t word = have >= 32 ? 0xffffffffu : have > 0 ? (1u << have) - 1 : 0;
-                    word &= ~lost[(n_tile + tile) % kLostTiles * 4 + lane];
-                    there[4 * st + lane] = word;
-                }
+                if (lane < 4) there[4 * st + lane] = age == 0 ? mine[0] : age == 1 ? mine[1] : mine[2];
                 __syncwarp();
                 if (lane == 0) mbar_expect_tx(raw_full(st), __popc(s) * box * P::kDs);
                 if (s >> lane & 1)
@@ -813,10 +813,7 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
                 const int from = n_read % P::kRawRing;
                 if (!wait(raw_full(from), n_read / P::kRawRing & 1)) return;
                 ++n_read;
-                int st;
-                if (!next_stage(st)) return;
                 const uint8_t* src = smem + P::kRaw + from * P::kRawStage;
-                uint8_t* dst = smem + P::kQ + st * P::kStage;
                 // piece c of a row: eight lanes take eight rows' where rows are 128 bytes (and swizzled),
                 // else what lies side by side
                 auto place = [&](int i, int& row, int& c) {
@@ -846,6 +843,9 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
                     }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(raw_empty(from));
+                int st;  // waited for with the rows in registers, so that the next ones are on their way
+                if (!next_stage(st)) return;
+                uint8_t* dst = smem + P::kQ + st * P::kStage;
 #pragma unroll
                 for (int i = 0; i < kPieces; ++i) {
                     int row, c;
@@ -853,7 +853,7 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
                     widen16(raw[i], dst, row, c, P::kRawSwizzled);
                 }
                 fence_proxy_async_smem();
-                mbar_arrive(full(st));
+                __syncwarp();
                 if (lane == 0) mbar_arrive(full(st));
             }
         }
@@ -949,9 +949,9 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
                         }
                     }
                     fence_proxy_async_smem();
-                    mbar_arrive(full(st));
+                    __syncwarp();
                 }
-                if (lane == 0) mbar_arrive(full(st));  // for the warp's word of `lost`
+                if (lane == 0) mbar_arrive(full(st));  // for the warp's word of `lost`, or its rows
                 return true;
             };
             if (!copy_tiles(tiles, lag_of(*U), look, send)) return;

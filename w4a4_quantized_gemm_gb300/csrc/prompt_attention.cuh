@@ -483,10 +483,10 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
     if (tid == 0) {
         abort_flag = (base & 1023u) != 0;  // the swizzle's atoms start on 1024-byte boundaries
         never_abort = 0;
-        // a copying warp's lanes arrive when their copies have, and one of them once more: for what the engine
-        // brings, or the warp's other words; or one for all, where the warp itself has written
+        // One arrival a copying warp; where its lanes copy all by themselves, one of each and one for the
+        // warp's other words.
         for (int s = 0; s < P::kStages; ++s) {
-            mbar_init(full(s), E4M3 ? (A.keys.box > 0 ? kCopyWarps : 4) : 33 * 4);
+            mbar_init(full(s), A.keys.box > 0 ? kCopyWarps : E4M3 ? 4 : 33 * 4);
             mbar_init(empty(s), 2);
         }
         mbar_init(q_full, kCopyThreads), mbar_init(q_free, 2);
@@ -701,7 +701,13 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
                 const uint32_t there = age == 0 ? whole[0] : age == 1 ? whole[1] : whole[2];
                 const int pg = age == 0 ? pages[0] : age == 1 ? pages[1] : pages[2];
                 const int sl = age == 0 ? slots[0] : age == 1 ? slots[1] : slots[2];
-                if (lane == 0) mbar_expect_tx(full(st), __popc(there) * box * 128 * P::kPlanes);
+                const uint32_t bytes = __popc(there) * box * 128 * P::kPlanes;
+                if (lane == 0) {  // the warp's one arrival, or with rows of its own still to come (below) without it
+                    if (there == all)
+                        mbar_expect_tx(full(st), bytes);
+                    else
+                        mbar_expect_tx_only(full(st), bytes);
+                }
                 // lane 16 p + b: plane p of box b
                 const int from = lane & 15, y = __shfl_sync(0xffffffffu, sl, from), z = __shfl_sync(0xffffffffu, pg, from);
                 if (there >> from & 1 && lane < 16 * P::kPlanes)
@@ -722,8 +728,10 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
                                              r < have ? 16 : 0);
                         }
                     }
+                    cp_async_mbar_arrive(full(st));  // one more to wait for, until they are there
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(full(st));
                 }
-                cp_async_mbar_arrive_noinc(full(st));
                 return true;
             };
             if (!copy_tiles(tiles, lag_of(*U), look, send)) return;

@@ -1,0 +1,66 @@
+"""Corners of the prompt and chunk attention: rows, keys and values that are no numbers or lie at the
+borders of their types, in units that are whole and in units that are split along the keys.
+
+References and tolerances as in test_prompt_ops_gpu."""
+import math
+
+import pytest
+import torch
+
+import w4a4_quantized_gemm_gb300 as w4
+from tests.test_layer_ops_gpu import BF16, E4M3, F16, F64, Cache, gen, randn
+from tests.test_prompt_ops_gpu import check_chunk, check_prompt, ints, qkv, starts_of
+
+pytestmark = pytest.mark.gpu
+NAN = float("nan")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from w4a4_quantized_gemm_gb300 import build
+    build.build()
+    w4.lib()
+    w4.w4a4_device_status()
+
+
+def put(cache, b, tokens, head, pool, value):
+    """Sets rows `tokens` of sequence b of a pool of `cache` (a function of the rows as they are, or a number)."""
+    tokens = torch.as_tensor(tokens)
+    page, slot = cache.table[b, tokens // cache.page].long(), tokens % cache.page
+    x = pool.float()
+    x[page, slot, head] = value(x[page, slot, head]) if callable(value) else value
+    pool.copy_(x.to(pool.dtype))
+
+
+# A row of few over a long cache is split into parts of four tiles or more; 256 rows of a short one are not.
+SPLIT = [("split", [5, 3], [6000, 3000]), ("whole", [5, 3], [900, 300])]
+
+
+@pytest.mark.parametrize("dtype, act, dim", [(F16, F16, 128), (BF16, BF16, 64), (E4M3, BF16, 128), (F16, F16, 256)])
+@pytest.mark.parametrize("how, rows, lengths", SPLIT)
+def test_chunk_rows_whose_scores_are_nan(dtype, act, dim, how, rows, lengths):
+    """A query that is NaN, or a cache whose scale of a head is: the row is NaN and so is its lse, however many parts
+    its keys are shared out into."""
+    c = Cache(lengths, 16, 2, dim, dtype, seed=21)
+    q = randn(gen(22), sum(rows), 4, dim).to(act)
+    q[1, 0, 3], q[6, 3, 0] = NAN, NAN
+    out, lse = check_chunk(c, q, starts_of(rows), lengths, what=f"{how} query")
+    assert torch.isnan(out[1, 0]).all() and torch.isnan(lse[1, 0]) and torch.isfinite(out[1, 1:]).all()
+    if dtype == E4M3:
+        c.ks[1] = NAN
+        c.to_gpu()
+        out, lse = check_chunk(c, q, starts_of(rows), lengths, what=f"{how} scale")
+        assert torch.isnan(out[:, 2:]).all() and torch.isnan(lse[:, 2:]).all()
+
+
+@pytest.mark.parametrize("dtype, act, dim", [(F16, F16, 128), (BF16, BF16, 64), (E4M3, F16, 64), (BF16, BF16, 256)])
+@pytest.mark.parametrize("lo, hi", [(0, 1024), (0, 512), (2048, 4096), (5888, 5995)])
+def test_chunk_parts_whose_keys_are_all_nan(dtype, act, dim, lo, hi):
+    """A part of a row's keys without one number among its scores."""
+    lengths, rows = [6000, 3000], [5, 3]
+    c = Cache(lengths, 16, 2, dim, dtype, seed=23)
+    put(c, 0, range(lo, hi), 0, c.k, NAN)
+    c.to_gpu()
+    q = randn(gen(24), 8, 4, dim).to(act)
+    out, lse = check_chunk(c, q, starts_of(rows), lengths, what=f"keys {lo} to {hi}")
+    assert torch.isnan(out[:5, :2]).all() and torch.isfinite(out[:5, 2:]).all() and torch.isfinite(lse[5:]).all()

@@ -1418,8 +1418,8 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
             const float* p = part + int64_t(i) * kPartFloats;
             const float m = p[256 * 128 + r], l = p[256 * 129 + r];
             const float4 x = *reinterpret_cast<const float4*>(p + r * D + e);
-            if (m == -INFINITY) continue;  // the part saw nothing
-            const float w = ex2(m - most);
+            if (l == 0.f) continue;  // the part saw nothing; scores that are all NaN leave m at -inf, but not l at zero
+            const float w = m == -INFINITY ? 0.f : ex2(m - most);
             sum = fmaf(w, l, sum);
             if (w != 0.f) o.x = fmaf(w, x.x, o.x), o.y = fmaf(w, x.y, o.y), o.z = fmaf(w, x.z, o.z), o.w = fmaf(w, x.w, o.w);
         }

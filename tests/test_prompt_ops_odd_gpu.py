@@ -64,3 +64,13 @@ def test_chunk_parts_whose_keys_are_all_nan(dtype, act, dim, lo, hi):
     q = randn(gen(24), 8, 4, dim).to(act)
     out, lse = check_chunk(c, q, starts_of(rows), lengths, what=f"keys {lo} to {hi}")
     assert torch.isnan(out[:5, :2]).all() and torch.isfinite(out[:5, 2:]).all() and torch.isfinite(lse[5:]).all()
+
+
+@pytest.mark.parametrize("heads, rows, length", [(160, 300, 200), (160, 200, 97), (1, 300, 200), (80, 140, 3)])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 50, 100, 1])
+def test_chunk_longer_than_its_cache_with_a_window(heads, rows, length, window):
+    """Rows before token 0 beside rows that see all tokens, in units of 256 rows (many heads) and of 128."""
+    c = Cache([length], 16, heads, 64, F16, seed=27)
+    q = randn(gen(28), rows, heads, 64).to(F16)
+    out, lse = check_chunk(c, q, [0, rows], [length], window=window, what=f"{heads} heads, window {window}")
+    assert torch.all(out[:rows - length] == 0) and torch.isfinite(lse[rows - length:]).all()

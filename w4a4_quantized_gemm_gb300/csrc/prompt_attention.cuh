@@ -185,7 +185,8 @@ __device__ __forceinline__ Sequence sequence(const Args& A, int b, bool& bad) {
 // Keys [lo, hi) that the row's token at `place` sees.
 __device__ __forceinline__ void sees(const Args& A, int place, int length, int& lo, int& hi) {
     hi = A.causal ? max(0, min(place, length - 1) + 1) : length;
-    lo = A.window > 0 ? max(0, min(place, INT32_MAX - 1) + 1 - A.window) : 0;
+    // a place before token 0 sees nothing, whatever the window: clamped, since their difference can pass 31 bits
+    lo = A.window > 0 ? max(0, max(-1, min(place, INT32_MAX - 1)) + 1 - A.window) : 0;
 }
 
 // Where key j's row of head `head` is, in keys (w = 0) or values (1); nullptr: on no page.

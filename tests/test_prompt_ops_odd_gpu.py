@@ -74,3 +74,20 @@ def test_chunk_longer_than_its_cache_with_a_window(heads, rows, length, window):
     q = randn(gen(28), rows, heads, 64).to(F16)
     out, lse = check_chunk(c, q, [0, rows], [length], window=window, what=f"{heads} heads, window {window}")
     assert torch.all(out[:rows - length] == 0) and torch.isfinite(lse[rows - length:]).all()
+
+
+@pytest.mark.parametrize("dtype, act, dim", [(F16, F16, 128), (BF16, BF16, 64), (E4M3, BF16, 128), (F16, F16, 256)])
+@pytest.mark.parametrize("lengths", [[6000], [900]])
+def test_chunk_a_value_that_is_seen_counts_whatever_its_weight(dtype, act, dim, lengths):
+    """NaN in a value whose key's weight is far below the smallest number, in another part (or another stream's
+    tile) than the keys with weight: the output is NaN, as the sum that it stands for."""
+    c = Cache(lengths, 16, 1, dim, dtype, seed=25, scales=False)
+    n = lengths[0]
+    for at, x in ((range(n), -40.0), (range(650, 760), 40.0)):
+        put(c, 0, at, 0, c.k, lambda rows: torch.cat((torch.full_like(rows[..., :1], x), rows[..., 1:]), -1))
+    put(c, 0, [3], 0, c.v, lambda rows: torch.cat((torch.full_like(rows[..., :1], NAN), rows[..., 1:]), -1))
+    c.to_gpu()
+    q = randn(gen(26), 4, 2, dim).to(act) / 8
+    q[..., 0] = 4.0
+    out, lse = check_chunk(c, q, [0, 4], lengths, scale=1.0, what="a value without weight")
+    assert torch.isnan(out[..., 0]).all() and torch.isfinite(out[..., 1:]).all() and torch.isfinite(lse).all()

@@ -1253,6 +1253,7 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
             const bool has0 = P::kStreams == 2 && shared ? U.tiles0 > 0 : U.tiles > 0;
             const bool has1 = P::kStreams == 2 && (shared ? U.tiles > 0 : U.tiles > 1);
             const bool reads0 = has0 && !(shared && stream == 1), reads1 = has1 && !(shared && stream == 0);
+            bool counts0 = reads0, counts1 = reads1;  // this row saw one of the stream's keys
             float most = top == -INFINITY ? -INFINITY : top * scale2, w0 = 1.f, w1 = 1.f;
             if (!shared) {
                 if (n_ml > 0 && !wait(ml_free, (n_ml - 1) & 1)) return;
@@ -1264,7 +1265,9 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
                 const float m0 = ml[row], m1 = ml[kTile + row];
                 most = fmaxf(m0, m1);
                 w0 = m0 == -INFINITY ? 0.f : ex2(m0 - most), w1 = m1 == -INFINITY ? 0.f : ex2(m1 - most);
-                sum = ml[2 * kTile + row] * w0 + ml[3 * kTile + row] * w1;
+                const float l0 = ml[2 * kTile + row], l1 = ml[3 * kTile + row];
+                sum = l0 * w0 + l1 * w1;
+                counts0 &= l0 != 0.f, counts1 &= l1 != 0.f;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(ml_free);
                 ++n_ml;
@@ -1295,7 +1298,8 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
                     tmem_wait_ld();
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
-                        x[k] = (reads0 && w0 != 0.f ? x[k] * w0 : 0.f) + (reads1 && w1 != 0.f ? y[k] * w1 : 0.f);
+                        // (a weight of zero too: infinite or NaN values among the keys that are seen stay)
+                        x[k] = (counts0 ? x[k] * w0 : 0.f) + (counts1 ? y[k] * w1 : 0.f);
                         if (none) x[k] = 0.f;
                         odd = fmaf(x[k], 0.f, odd);
                     }
@@ -1422,7 +1426,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
             if (l == 0.f) continue;  // the part saw nothing; scores that are all NaN leave m at -inf, but not l at zero
             const float w = m == -INFINITY ? 0.f : ex2(m - most);
             sum = fmaf(w, l, sum);
-            if (w != 0.f) o.x = fmaf(w, x.x, o.x), o.y = fmaf(w, x.y, o.y), o.z = fmaf(w, x.z, o.z), o.w = fmaf(w, x.w, o.w);
+            o.x = fmaf(w, x.x, o.x), o.y = fmaf(w, x.y, o.y), o.z = fmaf(w, x.z, o.z), o.w = fmaf(w, x.w, o.w);
         }
         const bool none = sum == 0.f;
         const float by = none ? 0.f : v_scale / sum;

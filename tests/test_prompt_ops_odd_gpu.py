@@ -91,3 +91,28 @@ def test_chunk_a_value_that_is_seen_counts_whatever_its_weight(dtype, act, dim, 
     q[..., 0] = 4.0
     out, lse = check_chunk(c, q, [0, 4], lengths, scale=1.0, what="a value without weight")
     assert torch.isnan(out[..., 0]).all() and torch.isfinite(out[..., 1:]).all() and torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_bf16_values_near_the_largest_number(dim):
+    """Scores that exceed the first tile's by a little less than what moves the running maximum, whose values are near
+    the largest number: the output is one of them, and the sum on the way to it is a finite number too."""
+    n = 300
+    q, k, v = (torch.zeros(n, 1, dim) for _ in range(3))
+    q[..., 0], k[..., 0] = 1.0, -50.0
+    k[:100, :, 0], v[:100] = 0.0, 1.0
+    k[270, :, 0], v[270] = 5.0, 2.0e38  # 2^7.2 of the first tile's weights
+    q, k, v = (x.to(BF16) for x in (q, k, v))
+    out, _ = check_prompt(q, k, v, [0, n], scale=1.0, what="prompt")
+    assert torch.isfinite(out).all() and float(out[-1, 0, 0]) > 1e37
+    # as a cache's, in whole units and in parts
+    for length in (n, 6000):
+        c = Cache([length], 16, 1, dim, BF16, seed=29)
+        put(c, 0, range(length), 0, c.k, torch.cat((torch.full((1,), -50.0), torch.zeros(dim - 1))))
+        put(c, 0, range(length), 0, c.v, 0.0)
+        for at, score, value in ((range(100), 0.0, 1.0), ([270], 5.0, 2.0e38)):
+            put(c, 0, at, 0, c.k, torch.cat((torch.full((1,), score), torch.zeros(dim - 1))))
+            put(c, 0, at, 0, c.v, value)
+        c.to_gpu()
+        out, _ = check_chunk(c, q[:3], [0, 3], [length], scale=1.0, what=f"chunk behind {length}")
+        assert torch.isfinite(out).all() and float(out[-1, 0, 0]) > 1e37

@@ -158,6 +158,16 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
+// A probability is 2^(its score - the subtracted maximum + lift), the maximum at most slack below the
+// largest score so far.  fp16 ones are taken up to 2^15, so that weights down to 2^-38 of the largest
+// keep the bits of their rounding: thousands of small ones beside one heavy key can make
+// the output.  bf16 ones have fp32's range, and so have their values: up to 1, so that a product with a
+// value is no larger than the value.
+template <class T>
+constexpr float slack = std::is_same_v<T, BF16> ? 8.f : 2.f;
+template <class T>
+constexpr float lift = std::is_same_v<T, BF16> ? -slack<T> : 13.f;
+
 // One of each translation unit: there is one a head dimension.
 static __device__ int g_prompt_status = 0;
 
@@ -450,10 +460,7 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
     using namespace tc;
     using P = Plan<D, E4M3>;
     constexpr bool BF = std::is_same_v<T, BF16>;
-    // fp16 probabilities are taken up to 2^15, so that weights down to 2^-38 of the largest
-    // keep the bits of their rounding: thousands of small ones beside one heavy key can make
-    // the output.  bf16 ones have fp32's range.
-    constexpr float kLift = BF ? 0.f : 13.f, kSlack = BF ? 8.f : 2.f;
+    constexpr float kLift = lift<T>, kSlack = slack<T>;
     constexpr int kCopyWarps = P::kCopyWarps, kCopyThreads = 32 * kCopyWarps;
     constexpr int kMmaWarp = P::kMmaWarp, kPlanWarp = P::kPlanWarp, kRawWarp = P::kRawWarp;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -1401,7 +1408,7 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
 // n-th of the rows.  Four elements a thread.
 template <int D, class T, bool E4M3>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args A) {
-    constexpr float kLift = std::is_same_v<T, BF16> ? 0.f : 13.f;
+    constexpr float kLift = lift<T>;
     constexpr int kPer = D / 4, kRows = 256 / kPer;  // threads of a row, rows at a time
     pdl_wait();
     pdl_launch_dependents();

@@ -34,6 +34,7 @@ struct Args {
     int tokens, seqs, q_heads, kv_heads, group, window;
     bool causal;
     Divisor by_group;
+    uint64_t wait_ns = 0;                  // for a unit to be done with
     bool q_boxes = false;                  // queries come by the copy engine: 128 rows are whole tokens
 };
 

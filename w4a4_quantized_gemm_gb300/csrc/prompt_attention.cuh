@@ -46,6 +46,7 @@ namespace prompt {
 
 constexpr int kTile = 128;                 // keys of a tile, rows of a stream
 constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr uint64_t kDrainNs = 10000000ull;  // of a kernel that gives up: copies that are under way have long landed
 constexpr uint32_t kSuspendNs = 20000;
 constexpr int kSoftmaxWarps = 8;
 constexpr int kLostTiles = 16;
@@ -560,7 +561,10 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
                 A.parts_of[2 * blockIdx.x] = make_int4(U.begin, U.head, U.row0, U.rows);
                 A.parts_of[2 * blockIdx.x + 1] = make_int4(U.first_part, part ? U.pieces : 0, 0, 0);
             }
-            if (n >= 2 && !wait(u_free(n & 1), (n >> 1 & 1) ^ 1)) return;
+            if (n >= 2 && !warp_wait_parity_suspend(u_free(n & 1), (n >> 1 & 1) ^ 1, abort, A.wait_ns, kSuspendNs)) {
+                *abort = 1;
+                return;
+            }
             if (lane == 0) {
                 units[n & 1] = U;
                 mbar_arrive(u_full(n & 1));
@@ -1372,9 +1376,11 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
         }
         cp_async_commit();
         cp_async_wait<0>();
-        if (*abort)  // the copy engine's land before the shared memory goes away
+        if (*abort) {  // the copy engine's land before the shared memory goes away
             for (uint32_t i = n_stage > P::kStages ? n_stage - P::kStages : 0; i < n_stage; ++i)
-                warp_wait_parity_suspend(full(i % P::kStages), i / P::kStages & 1, &never_abort, kWaitNs, kSuspendNs);
+                warp_wait_parity_suspend(full(i % P::kStages), i / P::kStages & 1, &never_abort, kDrainNs, kSuspendNs);
+            if (A.q_boxes && n_q > 0) warp_wait_parity_suspend(q_full, (n_q - 1) & 1, &never_abort, kDrainNs, kSuspendNs);
+        }
     } else {
         regs_dec<P::kOtherRegs>();
         if (warp == kMmaWarp || (P::kStreams == 2 && warp == kMmaWarp + 2)) {
@@ -1391,7 +1397,7 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
             copy_raw();
             if (*abort)
                 for (uint32_t i = n_raw > P::kRawRing ? n_raw - P::kRawRing : 0; i < n_raw; ++i)
-                    warp_wait_parity_suspend(raw_full(i % P::kRawRing), i / P::kRawRing & 1, &never_abort, kWaitNs, kSuspendNs);
+                    warp_wait_parity_suspend(raw_full(i % P::kRawRing), i / P::kRawRing & 1, &never_abort, kDrainNs, kSuspendNs);
         }
     }
     tc_fence_before();

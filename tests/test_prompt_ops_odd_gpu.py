@@ -8,8 +8,8 @@ import pytest
 import torch
 
 import w4a4_quantized_gemm_gb300 as w4
-from tests.test_layer_ops_gpu import BF16, E4M3, F16, F64, Cache, gen, randn
-from tests.test_prompt_ops_gpu import check_chunk, check_prompt, ints, qkv, starts_of
+from tests.test_layer_ops_gpu import BF16, E4M3, F16, F64, Cache, check, gen, randn
+from tests.test_prompt_ops_gpu import check_chunk, check_prompt, fresh, ints, rows_ref, starts_of
 
 pytestmark = pytest.mark.gpu
 NAN = float("nan")
@@ -116,3 +116,80 @@ def test_bf16_values_near_the_largest_number(dim):
         c.to_gpu()
         out, _ = check_chunk(c, q[:3], [0, 3], [length], scale=1.0, what=f"chunk behind {length}")
         assert torch.isfinite(out).all() and float(out[-1, 0, 0]) > 1e37
+
+
+@pytest.mark.parametrize("dtype, act, dim, page, hkv", [
+    (F16, F16, 128, 16, 2), (BF16, BF16, 64, 16, 160), (E4M3, BF16, 128, 64, 2), (E4M3, F16, 96, 7, 160), (BF16, BF16, 256, 24, 1)])
+@pytest.mark.parametrize("window", [0, 1500])
+def test_chunk_rows_beside_a_value_that_they_do_not_see(dtype, act, dim, page, hkv, window):
+    """NaN and infinities among the values (and keys) of a chunk's later rows, and before a window, behind a long
+    context: in whole units (160 heads) and in parts. The rows around them are computed again from their own keys."""
+    length, rows = 4500 if hkv > 2 else 20000, 70
+    c = Cache([length], page, hkv, dim, dtype, seed=30)
+    odd = 1 if hkv > 2 else 0
+    for at, head, pool, value in ((length - 3, odd, c.v, math.inf), (length - 30, odd, c.v, NAN), (length - 9, odd, c.k, NAN),
+                                  (length - rows - 1480, odd, c.v, -math.inf)):
+        put(c, 0, [at], head, pool, lambda x: torch.cat((x[..., :5], torch.full_like(x[..., :1], value), x[..., 6:]), -1))
+    if not window:
+        put(c, 0, [length - rows - 1480], odd, c.v, 1.0)
+    c.to_gpu()
+    q = randn(gen(31), rows, 3 * hkv if hkv < 100 else hkv, dim).to(act)
+    out, _ = check_chunk(c, q, [0, rows], [length], window=window, what=f"{dtype} D={dim} window={window}")
+    g = q.shape[1] // hkv
+    mine = out[:, odd * g:odd * g + g]
+    assert torch.isfinite(mine[20 if window else 0:rows - 30]).all() and torch.isnan(mine[rows - 9:]).all()
+    assert torch.isfinite(out[:, (odd + 1) * g:]).all()
+
+
+def test_chunk_rows_beside_a_value_that_they_do_not_see_behind_millions_of_tokens():
+    """49 rows beside a NaN value behind 8 million tokens (a page, over and over), in the first unit of CTAs that have a
+    second one: computed again for as long as a unit takes, not a row at a time while the other warps wait."""
+    heads, dim, page, rows, pages = 160, 64, 64, 50, 1 << 17
+    g = gen(32)
+    q, k, v = (randn(g, n, heads, dim).to(F16) for n in (rows, 2 * page, 2 * page))
+    # all pages but the last: scores of -25.9 and less where the last one's lse is 1.8 and more
+    q[..., 0], k[:page, :, 0], k[page:, :, 0] = 16.0, -16.0, 0.0
+    v[-1, 140:152] = NAN
+    table = torch.zeros(1, pages, dtype=torch.int32)
+    table[0, -1] = 1
+    handle = w4.PagedKVCache(k.view(2, page, heads, dim).cuda(), v.view(2, page, heads, dim).cuda(), table.cuda())
+    out, lse = fresh(q)
+    w4.w4a4_chunk_attention(q.cuda(), handle, ints([0, rows]), ints([pages * page]), out, lse=lse)
+    torch.cuda.synchronize()
+    assert w4.w4a4_device_status() == 0
+    o, l, ot, lt = rows_ref(q, k[page:].to(F64), v[page:].to(F64), page - rows, dim ** -0.5)
+    rest = 2 ** 23 * math.exp(-27)  # the weight of all other pages beside the last one's
+    check(out, o, ot + rest * (6 + o.abs().nan_to_num(0, 0, 0)), "out")
+    check(lse, l, lt + rest, "lse")
+    assert torch.isfinite(out[:-1]).all() and torch.isnan(out[-1, 140:152]).all()
+
+
+@pytest.mark.parametrize("dtype, dim, hq, hkv, n", [(F16, 128, 80, 40, 700), (BF16, 64, 64, 64, 700), (BF16, 96, 6, 2, 1100),
+                                                    (F16, 256, 12, 12, 600), (BF16, 128, 4, 4, 900)])
+@pytest.mark.parametrize("window, shared", [(0, False), (200, False), (0, True), (130, True)])
+def test_prompt_rows_keep_their_bits_beside_a_value_that_they_do_not_see(dtype, dim, hq, hkv, n, window, shared):
+    """Units of 256 rows and of 128, of one sequence and the next, with tensor maps and (values whose heads share
+    memory) without: what a row does not see leaves its output and lse bit for bit as they are."""
+    g = torch.Generator(device="cuda").manual_seed(n + dim)
+    q, k, v = (torch.randn((n, h, dim), generator=g, device="cuda").to(dtype) for h in (hq, hkv, 1 if shared else hkv))
+    starts, group = [0, n // 3, n], hq // hkv
+    calls = []
+    at = {n // 3 - 20: math.inf, n // 3 + 150: NAN, n - 140: -math.inf, n - 1: NAN}
+    for odd in (False, True):
+        for j, x in at.items():
+            v[j, 0, ::3] = x if odd else 0.5
+        out, lse = fresh(q)
+        w4.w4a4_prompt_attention(q, k, v.expand(n, hkv, dim), ints(starts), out, lse=lse, window=window)
+        calls.append((out, lse))
+    torch.cuda.synchronize()
+    assert w4.w4a4_device_status() == 0
+    (out, lse), (odd, lse2) = calls
+    assert torch.equal(lse, lse2) and torch.isfinite(out).all()
+    row = torch.arange(n, device="cuda")
+    sees = torch.zeros(n, dtype=torch.bool, device="cuda")
+    for j in at:
+        sees |= (row >= j) & (row < (j + window if window else n)) & ((row < n // 3) == (j < n // 3))
+    heads = hq if shared else group
+    assert torch.equal(out[~sees], odd[~sees]) and torch.equal(out[:, heads:], odd[:, heads:])
+    hit = odd[sees][:, :heads]
+    assert not torch.isfinite(hit[..., ::3]).any() and torch.equal(hit[..., 1::3], out[sees][:, :heads, 1::3])

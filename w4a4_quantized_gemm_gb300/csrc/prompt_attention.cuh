@@ -22,6 +22,8 @@
 //    page's), where strides and page sizes allow it, else 16 bytes a lane.  E4M3 rows go into a
 //    ring of their own and eight warps turn them into 16-bit ones.  Rows that no query of the
 //    unit sees are zeros.
+//  * Infinite and NaN values that a row does not see: units with such rows are taken again in a second
+//    pass (see partly_seen), after all others, at the same speed.
 //
 // What bounds it, where rows and keys are many: a product of 128 x 128 x 16 takes 64 cycles and reads
 // 8 KB of shared memory (4 KB with the first operand in tensor memory), which is all that the port
@@ -57,7 +59,7 @@ struct Sequence {
 
 // A unit of work, or a piece of one: what the warps need to know of it.
 struct Unit {
-    int live;                              // 0: there are no more
+    int live;                              // 0: there are no more (of a pass), 1: of the first pass, else see partly_seen
     int b, head;                           // sequence, key-value head
     int row0, rows;                        // rows (token * G + head of the group) of the sequence
     int begin;                             // the sequence's first token in q
@@ -222,54 +224,92 @@ __device__ __forceinline__ float element(const char* row, int e) {
     }
 }
 
-// Whether a value of keys [lo, hi) is infinite or NaN (a warp).
+// The keys among [lo, lo + 32) and below hi with an infinite or NaN value (a warp).
+template <int D, bool E4M3, bool BF>
+__device__ __forceinline__ uint32_t odd_keys(const Args& A, const Unit& U, int lo, int hi) {
+    const int j = lo + int(threadIdx.x & 31);
+    const char* const row = j < hi ? key_row(A, U.b, U.begin, U.head, j, 1) : nullptr;
+    bool odd = false;
+    for (int i = 0; row && i < D * (E4M3 ? 1 : 2) / 16; ++i) {
+        const uint4 v = reinterpret_cast<const uint4*>(row)[i];
+        for (const uint32_t w : {v.x, v.y, v.z, v.w})
+            if constexpr (E4M3) {
+                for (int s = 0; s < 32; s += 8) odd |= (w >> s & 0x7Fu) == 0x7Fu;
+            } else {
+                const uint32_t m = BF ? 0x7F80u : 0x7C00u;
+                odd |= (w & m) == m || (w >> 16 & m) == m;
+            }
+    }
+    return __ballot_sync(0xffffffffu, odd);
+}
+// Whether there are any among [lo, hi).
 template <int D, bool E4M3, bool BF>
 __device__ __noinline__ bool odd_values(const Args& A, const Unit& U, int lo, int hi) {
-    bool odd = false;
-    for (int j = lo + int(threadIdx.x & 31); j < hi; j += 32) {
-        const char* row = key_row(A, U.b, U.begin, U.head, j, 1);
-        if (!row) continue;
-        for (int i = 0; i < D * (E4M3 ? 1 : 2) / 16; ++i) {
-            const uint4 v = reinterpret_cast<const uint4*>(row)[i];
-            for (const uint32_t w : {v.x, v.y, v.z, v.w})
-                if constexpr (E4M3) {
-                    for (int s = 0; s < 32; s += 8) odd |= (w >> s & 0x7Fu) == 0x7Fu;
-                } else {
-                    const uint32_t m = BF ? 0x7F80u : 0x7C00u;
-                    odd |= (w & m) == m || (w >> 16 & m) == m;
-                }
-        }
-    }
-    return __any_sync(0xffffffffu, odd);
+    for (; lo < hi; lo += 32)
+        if (odd_keys<D, E4M3, BF>(A, U, lo, hi) != 0) return true;
+    return false;
 }
 
-// sum_j 2^(a_j - ref) v_j * by over the keys [lo, hi) alone, elements [e0, e1) of the row, by a warp:
-// what the tiles give where no masked value is infinite or NaN.  To `out` in type T, or as fp32.
-template <int D, class T, bool E4M3>
-__device__ __noinline__ void careful_row(const Args& A, const Unit& U, int flat, int lo, int hi, float scale2, float ref,
-                                         float by, void* out, bool fp32, int e0, int e1) {
-    constexpr int kPer = D / 32;
-    const int lane = threadIdx.x & 31;
-    const int token = A.by_group.quotient(flat), h = U.head * A.group + flat - token * A.group;
-    const char* qr = A.q + 2 * ((U.begin + token) * A.q_token + h * A.q_head);
-    float q[kPer], o[kPer] = {};
-    for (int e = 0; e < kPer; ++e) q[e] = element<T, false>(qr, lane + 32 * e);
-    for (int j = lo; j < hi; ++j) {
-        const char *k = key_row(A, U.b, U.begin, U.head, j, 0), *v = key_row(A, U.b, U.begin, U.head, j, 1);
-        if (!k || !v) continue;
-        float a = 0.f;
-        for (int e = 0; e < kPer; ++e) a = fmaf(q[e], element<T, E4M3>(k, lane + 32 * e), a);
-        for (int x = 16; x > 0; x >>= 1) a += __shfl_xor_sync(0xffffffffu, a, x);
-        const float p = ex2(fmaf(a, scale2, -ref));
-        for (int e = 0; e < kPer; ++e) o[e] = fmaf(p, element<T, E4M3>(v, lane + 32 * e), o[e]);
+// Values of keys that a row does not see have a probability of zero, and their product is NaN where the
+// value is infinite or NaN.  A unit with such a row among its outputs is taken again in a second pass, in which
+// these values are zeros in the tiles that some row of the unit does not see whole; the rows that do see them have
+// them added afterwards (the probability is not zero, so that the sum is what the value itself makes of it).
+// A unit's `live` in that pass: 2 + 256 * its first tiles of that kind + 65536 * its last ones (four or so
+// at most: a unit's rows are neighbours).
+__device__ __forceinline__ bool partly_seen(int live, int t, int tiles) {
+    return t < (live >> 8 & 0xFF) || t >= tiles - (live >> 16);
+}
+__device__ __forceinline__ int second_pass(const Args& A, const Unit& U) {
+    int lo, hi, unused;
+    sees(A, U.first + A.by_group.quotient(U.row0), U.length, unused, hi);
+    sees(A, U.first + A.by_group.quotient(U.row0 + U.rows - 1), U.length, lo, unused);
+    const int front = max(0, min(U.tiles, (lo - U.key0 + kTile - 1) / kTile));
+    const int whole = hi >= U.end ? U.tiles : max(0, hi - U.key0) / kTile;
+    return 2 | min(front, 255) << 8 | min(U.tiles - whole, 255) << 16;
+}
+
+// Zeros for the infinite and NaN elements of a stage, by the thread that issues its products: 20 us for a tile.
+template <bool BF, int BYTES>
+__device__ __noinline__ void clean_stage(uint8_t* stage) {
+    constexpr uint32_t kExp = BF ? 0x7F807F80u : 0x7C007C00u, kOne = BF ? 0x00800080u : 0x04000400u;
+    uint32_t* const words = reinterpret_cast<uint32_t*>(stage);
+#pragma unroll 8
+    for (int i = 0; i < BYTES / 16; ++i) {
+        const uint4 v = reinterpret_cast<const uint4*>(stage)[i];
+        // the sign bits: halves whose exponent is all ones
+        if ((((v.x & kExp) + kOne | (v.y & kExp) + kOne | (v.z & kExp) + kOne | (v.w & kExp) + kOne) & 0x80008000u) == 0) continue;
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t w = words[4 * i + k], odd = (w & kExp) + kOne;
+            words[4 * i + k] = w & ~((odd & 0x8000u ? 0xFFFFu : 0u) | (odd & 0x80000000u ? 0xFFFF0000u : 0u));
+        }
     }
-    for (int e = 0; e < kPer; ++e) {
-        const int i = lane + 32 * e;
-        if (i < e0 || i >= e1) continue;
-        if (fp32)
-            static_cast<float*>(out)[i] = o[e] * by;
-        else
-            static_cast<uint16_t*>(out)[i] = uint16_t(T::down(o[e] * by, 0.f));
+    tc::fence_proxy_async_smem();
+}
+
+// Adds the infinite and NaN values of tiles that are partly seen to each lane's row (which sees keys [lo, hi), and some
+// of them if `has`) of the output, elements [e0, e1), of type T or fp32.
+template <int D, class T, bool E4M3>
+__device__ __noinline__ void add_odd_values(const Args& A, const Unit& U, bool has, int lo, int hi, char* out, bool fp32,
+                                            int e0, int e1) {
+    for (int t = 0; t < U.tiles; ++t) {
+        if (!partly_seen(U.live, t, U.tiles)) continue;
+        const int end = min(U.key0 + (t + 1) * kTile, U.end);
+        for (int j0 = U.key0 + t * kTile; j0 < end; j0 += 32)
+            for (uint32_t odd = odd_keys<D, E4M3, std::is_same_v<T, BF16>>(A, U, j0, end); odd != 0; odd &= odd - 1) {
+                const int j = j0 + __ffs(odd) - 1;
+                const char* const row = key_row(A, U.b, U.begin, U.head, j, 1);
+                for (int e = e0; has && j >= lo && j < hi && e < e1; ++e) {
+                    const float v = element<T, E4M3>(row, e);
+                    if (fabsf(v) < INFINITY) continue;
+                    if (fp32) {
+                        reinterpret_cast<float*>(out)[e] += v;
+                    } else {
+                        uint16_t& x = reinterpret_cast<uint16_t*>(out)[e];
+                        x = uint16_t(T::down(T::up(x).x + v, 0.f));
+                    }
+                }
+                __syncwarp();
+            }
     }
 }
 
@@ -468,6 +508,7 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
     int& abort_flag = *reinterpret_cast<int*>(smem + P::kFlags);
     int& never_abort = *reinterpret_cast<int*>(smem + P::kFlags + 4);
     uint32_t& tmem_base = *reinterpret_cast<uint32_t*>(smem + P::kFlags + 8);
+    uint32_t& redo = *reinterpret_cast<uint32_t*>(smem + P::kFlags + 12);  // bit min(m, 31): unit m of the first pass is for the second
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     volatile int* abort = &abort_flag;
     const uint32_t base = smem_u32(smem);
@@ -492,6 +533,7 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
     if (tid == 0) {
         abort_flag = (base & 1023u) != 0;  // the swizzle's atoms start on 1024-byte boundaries
         never_abort = 0;
+        redo = 0;
         // One arrival a copying warp; where its lanes copy all by themselves, one of each and one for the
         // warp's other words.
         for (int s = 0; s < P::kStages; ++s) {
@@ -524,22 +566,47 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
         *abort = 1;
         return false;
     };
-    // Unit n, for every warp that works on it; nullptr: there are no more.  done_with gives its
-    // place back.
-    auto unit = [&](uint32_t n) -> const Unit* {
-        if (!wait(u_full(n & 1), n >> 1 & 1)) return nullptr;
-        return units[n & 1].live ? units + (n & 1) : nullptr;
-    };
-    auto done_with = [&](uint32_t n) {
+    // The next unit, for every warp that works on it; nullptr: there are no more of this pass.  done_with gives
+    // its place back.
+    uint32_t n_unit = 0;
+    auto done_with = [&]() {
         __syncwarp();
-        if (lane == 0) mbar_arrive(u_free(n & 1));
+        if (lane == 0) mbar_arrive(u_free(n_unit & 1));
+        ++n_unit;
+    };
+    auto unit = [&]() -> const Unit* {
+        if (!wait(u_full(n_unit & 1), n_unit >> 1 & 1)) return nullptr;
+        if (units[n_unit & 1].live) return units + (n_unit & 1);
+        done_with();
+        return nullptr;
+    };
+    // The end of a pass: whether a second one follows.
+    auto pass_ends = [&]() {
+        tc_fence_before();
+        __syncthreads();
+        return *static_cast<volatile uint32_t*>(&redo) != 0 && !*abort;
+    };
+    // What a warp does in both: one code for both passes, or (`twice`) a code each, where a loop around the first one costs
+    // it registers.
+    auto passes = [&](auto work) {
+#pragma unroll 1
+        for (int pass = 0; pass < 2; ++pass) {
+            work(pass);
+            if (!pass_ends()) return;
+        }
+    };
+    auto twice = [&](auto work) {
+        work(std::false_type{});
+        if (!pass_ends()) return;
+        work(std::true_type{});
+        pass_ends();
     };
 
-    auto plan = [&]() {
+    auto plan = [&](int pass) {
         Sequence mine{0, 0, 0};
         bool any = false;
         if (lane < A.seqs) mine = sequence(A, lane, any);
-        if (blockIdx.x == 0) {
+        if (blockIdx.x == 0 && pass == 0) {
             for (int b = lane + 32; b < A.seqs; b += 32) {
                 bool bad;
                 sequence(A, b, bad);
@@ -552,10 +619,14 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
         if (sorted) sort_sequences(A, mine, order);
         const Share share = share_out<D>(A, mine);
         Walk walk{sorted ? order : nullptr, mine};
-        for (uint32_t n = 0;; ++n) {
-            const int turn = int(n & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        const uint32_t chosen = pass == 0 ? 0xffffffffu : redo;
+        for (uint32_t m = 0;; ++m) {
+            const int turn = int(m & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
             Unit U{};
-            const bool live = walk.find(A, share, int(n * gridDim.x) + turn, U);
+            const bool live = walk.find(A, share, int(m * gridDim.x) + turn, U);
+            if (live && !(chosen >> min(m, 31u) & 1)) continue;
+            if (live && pass > 0) U.live = second_pass(A, U);
+            const uint32_t n = n_unit++;
             if (n == 0 && A.parts && lane == 0) {
                 const bool part = live && U.part >= 0;
                 A.parts_of[2 * blockIdx.x] = make_int4(U.begin, U.head, U.row0, U.rows);
@@ -575,6 +646,7 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
 
     // ---- queries, keys and values into shared memory
     uint32_t n_stage = 0, n_q = 0;  // copies of stages begun, units whose queries were copied
+    uint32_t n_tile = 0;            // tiles of the units that are done with
     auto copy_queries = [&](const Unit& U) {
         if (n_q > 0 && !wait(q_free, (n_q - 1) & 1)) return false;
         ++n_q;
@@ -660,9 +732,8 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
         const Keys& K = A.keys;
         const int box = K.box, boxes = 32 / box, w = warp - kSoftmaxWarps, my = 32 * w + lane * box;
         const uint32_t all = (1u << boxes) - 1;
-        uint32_t n_tile = 0;
-        for (uint32_t n = 0;; done_with(n++)) {
-            const Unit* const U = unit(n);
+        for (;; done_with()) {
+            const Unit* const U = unit();
             if (!U) return;
             if (U->tiles == 0) continue;
             const int key0 = U->key0, end = U->end, tiles = U->tiles, begin = U->begin, head = U->head;
@@ -758,9 +829,8 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
         const Keys& K = A.keys;
         const int box = K.box, boxes = box > 0 ? kTile / box : 0, my = lane * box;
         uint32_t* const there = reinterpret_cast<uint32_t*>(smem + P::kThere);
-        uint32_t n_tile = 0;
-        for (uint32_t n = 0;; done_with(n++)) {
-            const Unit* const U = unit(n);
+        for (;; done_with()) {
+            const Unit* const U = unit();
             if (!U) return;
             if (U->tiles == 0 || box == 0) continue;
             const int key0 = U->key0, end = U->end, tiles = U->tiles, head = U->head;
@@ -819,11 +889,11 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
         }
     };
     // ... and turned into 16-bit rows by eight warps.
+    uint32_t n_read = 0;
     auto widen = [&]() {
-        uint32_t n_read = 0;
         const int t = tid - 32 * kSoftmaxWarps;
-        for (uint32_t n = 0;; done_with(n++)) {
-            const Unit* const U = unit(n);
+        for (;; done_with()) {
+            const Unit* const U = unit();
             if (!U) return;
             if (U->tiles == 0) continue;
             const int stages = 2 * P::kHalves * U->tiles;
@@ -887,9 +957,8 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
         constexpr int kPieces = P::kDs * kSize / 16;  // of a stage's row
         const Keys& K = A.keys;
         const int w = warp - kSoftmaxWarps;
-        uint32_t n_tile = 0;
-        for (uint32_t n = 0;; done_with(n++)) {
-            const Unit* const U = unit(n);
+        for (;; done_with()) {
+            const Unit* const U = unit();
             if (!U) return;
             if (U->tiles == 0) continue;
             const int key0 = U->key0, end = U->end, tiles = U->tiles, begin = U->begin, head = U->head;
@@ -984,28 +1053,31 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
     // scores leaves them idle, but for the other stream's.  With both streams' products from one
     // thread 8192 tokens of 32 heads of 128 took 450 us (410 now), and with descriptors that the
     // compiler sums up 690.
-    auto multiply = [&](const int stream) {
+    uint32_t stages = 0;                                    // before this unit
+    uint32_t turns = 0, n_o = 0, p_phase = 0, q_phase = 0;  // units with an output; bit i: the parity of p_full(i, .)
+    auto multiply = [&](const int stream, auto second) {
         constexpr uint32_t kQk = idesc_m128_16bit(kTile, BF, false);
         constexpr uint32_t kPv = idesc_m128_16bit(P::kDs, BF, true);
         constexpr int kAhead = P::kStreams == 1 ? 2 : 1;  // tiles whose scores are under way
         // descriptors' low words (their high words are alike)
         const uint32_t keys0 = uint32_t(sdesc_sw128(ring)), values0 = uint32_t(sdesc_sw128(ring, kTile * 128));
         const uint32_t q0 = uint32_t(sdesc_sw128(base)), hi = uint32_t(sdesc_sw128(0) >> 32);
-        uint32_t stages = 0;                            // before this unit
-        uint32_t turns = 0, n_o = 0, p_phase = 0, q_phase = 0;  // units with an output; bit i: the parity of p_full(i, .)
         auto wait1 = [&](uint32_t bar, uint32_t parity) {
             if (wait_parity_suspend(bar, parity, abort, kWaitNs, kSuspendNs)) return true;
             *abort = 1;
             return false;
         };
-        for (uint32_t n = 0;; ++n) {
-            const int i = n & 1;
-            if (!wait1(u_full(i), n >> 1 & 1)) return;
+        for (;; ++n_unit) {
+            const int i = n_unit & 1;
+            if (!wait1(u_full(i), n_unit >> 1 & 1)) return;
             const Unit& U = units[i];
             const bool live = U.live != 0, shared = P::kStreams == 2 && U.shared;
-            const int tiles = U.tiles, tiles0 = U.tiles0;
+            const int tiles = U.tiles, tiles0 = U.tiles0, kind = U.live;
             mbar_arrive(u_free(i));
-            if (!live) return;
+            if (!live) {
+                ++n_unit;
+                return;
+            }
             if (tiles == 0) continue;
             // this stream's tiles: `first`, `first` + `step`, ...
             const int first = P::kStreams == 2 && !shared ? stream : 0, step = P::kStreams == 2 && !shared ? 2 : 1;
@@ -1086,8 +1158,11 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
                 }
                 const int buf = P::kStreams == 1 ? x & 1 : stream;
                 const uint32_t at = values_at(first + x * step);
-                for (int half = 0; half < P::kHalves; ++half)
+                for (int half = 0; half < P::kHalves; ++half) {
                     if (!ready(at + half)) return;
+                    if (second && partly_seen(kind, first + x * step, tiles))
+                        clean_stage<BF, P::kStage>(smem + P::kQ + (at + half) % P::kStages * P::kStage);
+                }
                 if (P::kStreams == 2 && x + kAhead < mine && !keys_ready(x + kAhead)) return;
                 if (x == 0 && n_o > 0 && !wait1(o_free, (n_o - 1) & 1)) return;  // the last unit's output has been read
 #pragma unroll
@@ -1122,13 +1197,13 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
         }
     };
 
+    uint32_t s_phase = 0, o_phase = 0, n_ml = 0;  // bit i: the parity of s_full(i), o_full(i)
     auto softmax = [&]() {
         const int stream = warp >> 2, row = tid & 127;
         const uint32_t lanes = uint32_t(warp & 3) << 21;  // this warp's lanes of tensor memory
         float* ml = reinterpret_cast<float*>(smem + P::kMl);
-        uint32_t s_phase = 0, o_phase = 0, n_tile = 0, n_ml = 0;  // bit i: the parity of s_full(i), o_full(i)
-        for (uint32_t n = 0;; done_with(n++)) {
-            const Unit* const unit_n = unit(n);
+        for (;; done_with()) {
+            const Unit* const unit_n = unit();
             if (!unit_n) return;
             const Unit& U = *unit_n;
             const bool shared = P::kStreams == 2 && U.shared;
@@ -1136,7 +1211,6 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
             // a scale of zero makes them zero
             float scale2 = A.scale * 1.44269504088896341f, flip = 1.f;
             if (E4M3 && A.keys.scale[0]) scale2 *= A.keys.scale[0][U.head];
-            const float signed2 = scale2;
             if (!(scale2 > 0.f)) {
                 flip = scale2 < 0.f ? -1.f : scale2 == 0.f ? 0.f : scale2;  // NaN stays
                 scale2 = scale2 < 0.f ? -scale2 : 1.f;
@@ -1340,68 +1414,75 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
                     A.lse[int64_t(U.begin + token) * A.q_heads + h] =
                         none ? -INFINITY : 0.693147180559945309f * (most - kLift + log2f(sum));
             }
-            const uint32_t again = __ballot_sync(0xffffffffu, valid && odd != 0.f && sum < INFINITY);
-            if (again != 0) {
+            if (U.live != 1) {
+                if (!idle) add_odd_values<D, T, E4M3>(A, U, valid && !none, lo, hi, dst, part != nullptr, e0, e1);
+            } else if (__any_sync(0xffffffffu, valid && odd != 0.f && sum < INFINITY)) {
                 // keys that were in the tiles and that not every row of the warp sees
                 const int last_lo = __reduce_max_sync(0xffffffffu, valid ? lo : 0);
                 const int first_hi = __reduce_min_sync(0xffffffffu, valid ? hi : INT32_MAX);
                 if (odd_values<D, E4M3, BF>(A, U, U.key0, min(U.end, last_lo)) ||
                     odd_values<D, E4M3, BF>(A, U, max(U.key0, first_hi), U.end))
-                    for (uint32_t left = again; left != 0; left &= left - 1) {
-                        const int r = __ffs(left) - 1;
-                        auto of = [&](auto v) { return __shfl_sync(0xffffffffu, v, r); };
-                        careful_row<D, T, E4M3>(A, U, of(flat), max(of(lo), U.key0), min(of(hi), U.end), signed2,
-                                                of(most) - kLift, of(by),
-                                                reinterpret_cast<void*>(of(reinterpret_cast<unsigned long long>(dst))),
-                                                part != nullptr, e0, e1);
-                    }
+                    if (lane == 0) atomicOr(&redo, 1u << min(n_unit, 31u));
             }
         }
     };
 
     if (warp < kSoftmaxWarps) {
         regs_inc<P::kSoftmaxRegs>();
-        softmax();
+        passes([&](int) { softmax(); });
     } else if (warp < kSoftmaxWarps + kCopyWarps) {
         regs_dec<P::kCopyRegs>();
-        if constexpr (E4M3) {
-            if (A.keys.box > 0)
-                widen();
+        auto copies = [&](auto copy) {
+            auto work = [&](auto) {
+                copy();
+                cp_async_commit();
+                cp_async_wait<0>();
+                if (*abort) {  // the copy engine's land before the shared memory goes away
+                    for (uint32_t i = n_stage > P::kStages ? n_stage - P::kStages : 0; i < n_stage; ++i)
+                        warp_wait_parity_suspend(full(i % P::kStages), i / P::kStages & 1, &never_abort, kDrainNs, kSuspendNs);
+                    if (A.q_boxes && n_q > 0) warp_wait_parity_suspend(q_full, (n_q - 1) & 1, &never_abort, kDrainNs, kSuspendNs);
+                }
+            };
+            // (64 sequences of 4 tokens, E4M3, D = 64: 147 us with one code, 139 with two; D = 128 183 and 195)
+            if constexpr (E4M3 && D == 64)
+                twice(work);
             else
-                copy_rows();
-        } else if (A.keys.box > 0) {
-            copy_boxes();
+                passes(work);
+        };
+        if (A.keys.box == 0) {
+            copies(copy_rows);
+        } else if constexpr (E4M3) {
+            copies(widen);
         } else {
-            copy_rows();
-        }
-        cp_async_commit();
-        cp_async_wait<0>();
-        if (*abort) {  // the copy engine's land before the shared memory goes away
-            for (uint32_t i = n_stage > P::kStages ? n_stage - P::kStages : 0; i < n_stage; ++i)
-                warp_wait_parity_suspend(full(i % P::kStages), i / P::kStages & 1, &never_abort, kDrainNs, kSuspendNs);
-            if (A.q_boxes && n_q > 0) warp_wait_parity_suspend(q_full, (n_q - 1) & 1, &never_abort, kDrainNs, kSuspendNs);
+            copies(copy_boxes);
         }
     } else {
         regs_dec<P::kOtherRegs>();
         if (warp == kMmaWarp || (P::kStreams == 2 && warp == kMmaWarp + 2)) {
-            if (lane == 0) {
-                multiply((warp - kMmaWarp) >> 1);
-                // what has been issued ends before its operands and tensor memory go away
-                mma_commit(all_done);
-                wait_parity_suspend(all_done, 0, &never_abort, kWaitNs, kSuspendNs);
-            }
-            __syncwarp();
+            // (a call to clean_stage in the first pass's code takes 2% of 2048 rows behind 30000)
+            twice([&](auto second) {
+                if (lane == 0) {
+                    multiply((warp - kMmaWarp) >> 1, second);
+                    // what has been issued ends before its operands and tensor memory go away
+                    mma_commit(all_done);
+                    wait_parity_suspend(all_done, second, &never_abort, kWaitNs, kSuspendNs);
+                }
+                __syncwarp();
+            });
         } else if (warp == kPlanWarp) {
-            plan();
+            passes(plan);
         } else if (E4M3 && warp == kRawWarp) {
-            copy_raw();
-            if (*abort)
-                for (uint32_t i = n_raw > P::kRawRing ? n_raw - P::kRawRing : 0; i < n_raw; ++i)
-                    warp_wait_parity_suspend(raw_full(i % P::kRawRing), i / P::kRawRing & 1, &never_abort, kDrainNs, kSuspendNs);
+            // (two codes for 2048 rows behind 30000 952 us, one 977)
+            twice([&](auto) {
+                copy_raw();
+                if (*abort)
+                    for (uint32_t i = n_raw > P::kRawRing ? n_raw - P::kRawRing : 0; i < n_raw; ++i)
+                        warp_wait_parity_suspend(raw_full(i % P::kRawRing), i / P::kRawRing & 1, &never_abort, kDrainNs, kSuspendNs);
+            });
+        } else {
+            passes([](int) {});
         }
     }
-    tc_fence_before();
-    __syncthreads();
     if (warp == kMmaWarp) {
         tc_fence_after();
         tmem_relinquish();

@@ -582,10 +582,11 @@ w4a4_status w4a4_debug_forward_partials(const uint16_t* X, const void* packed, s
                                         int K, int r, void* act_ws, size_t act_ws_bytes, int32_t* P,
                                         cudaStream_t stream);
 /* Limit in nanoseconds of what the kernels of w4a4_prompt_attention and
- * w4a4_chunk_attention wait for a unit of their work to be done with, for calls from now on
- * (0: the default, 2 s).  A wait that runs out ends the kernel with W4A4_ERR_TIMEOUT and
- * outputs that are not defined; short limits are for tests of that. */
-void w4a4_debug_prompt_wait_ns(uint64_t ns);
+ * w4a4_chunk_attention wait for a unit of their work to be done with, for calls from now
+ * on: ns + tile_ns for each 128 keys of the unit (ns = 0: the default, 2 s + 20 us).  A wait
+ * that runs out ends the kernel with W4A4_ERR_TIMEOUT and outputs that are not defined;
+ * short limits are for tests of that. */
+void w4a4_debug_prompt_wait_ns(uint64_t ns, uint64_t tile_ns);
 /* Reads and clears the device status words written by bounded waits
  * (W4A4_ERR_TIMEOUT) and by the kernels that read pages, positions, lengths or
  * starts from device memory, where one lay outside its range (W4A4_ERR_INDEX);

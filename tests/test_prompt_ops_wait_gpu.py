@@ -19,15 +19,17 @@ def _lib():
 
 
 def runs_out(call):
-    """`call` under a limit of a nanosecond: a wait is looked at some 20 us after it began, and a unit takes longer."""
-    w4.lib().w4a4_debug_prompt_wait_ns(1)
-    try:
-        call()
-        torch.cuda.synchronize()
-    finally:
-        w4.lib().w4a4_debug_prompt_wait_ns(0)
-    assert w4.w4a4_device_status() == w4.W4A4_ERR_TIMEOUT
-    assert w4.w4a4_device_status() == 0  # read and cleared
+    """`call` under a limit of a nanosecond: a wait is looked at some 20 us after it began, and a unit takes longer.
+    With 20 us more for each tile, a tenth of which it takes, the same wait does not run out."""
+    for tile_ns, status in ((0, w4.W4A4_ERR_TIMEOUT), (20000, 0)):
+        w4.lib().w4a4_debug_prompt_wait_ns(1, tile_ns)
+        try:
+            call()
+            torch.cuda.synchronize()
+        finally:
+            w4.lib().w4a4_debug_prompt_wait_ns(0, 0)
+        assert w4.w4a4_device_status() == status
+        assert w4.w4a4_device_status() == 0  # read and cleared
 
 
 @pytest.mark.parametrize("dtype, dim, hq, hkv", [(F16, 128, 32, 8), (BF16, 64, 16, 16), (F16, 256, 12, 4), (BF16, 96, 40, 8)])
@@ -50,3 +52,11 @@ def test_chunk_wait_runs_out(dtype, act, dim, page):
     out = torch.empty_like(q)
     runs_out(lambda: w4.w4a4_chunk_attention(q, far.handle, ints([0, 9000]), ints([40000]), out))
     check_chunk(c, randn(gen(3), 40, 8, dim).to(act), [0, 40], [300], what="after a call that gave up")
+
+
+def test_one_long_unit_a_cta():
+    """D = 256: half of the softmax's warps have no tiles and wait for the others' through the whole unit."""
+    far = Cache([40000], 16, 2, 256, F16, seed=2, fill=False)
+    q = torch.randn((9000, 2, 256), device="cuda").to(F16)
+    out = torch.empty_like(q)
+    runs_out(lambda: w4.w4a4_chunk_attention(q, far.handle, ints([0, 9000]), ints([40000]), out))

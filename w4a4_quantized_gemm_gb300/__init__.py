@@ -79,7 +79,7 @@ SIGNATURES = {
     "w4a4_qk_rope": (I, [P, P]),
     "w4a4_prompt_attention": (I, [P, P]),
     "w4a4_chunk_attention": (I, [P, P, P]),
-    "w4a4_debug_prompt_wait_ns": (None, [ctypes.c_uint64]),
+    "w4a4_debug_prompt_wait_ns": (None, [ctypes.c_uint64, ctypes.c_uint64]),
     "w4a4_device_status": (I, []),
     "w4a4_status_string": (ctypes.c_char_p, [I]),
     "w4a4_last_dispatch": (ctypes.c_char_p, []),

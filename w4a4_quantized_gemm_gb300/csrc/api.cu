@@ -289,7 +289,7 @@ int w4a4_stream_k(void) { return tc_stream_k_enabled() ? 1 : 0; }
 
 void w4a4_set_stream_k(int on) { g_stream_k.store(on ? 1 : 0); }
 
-void w4a4_debug_prompt_wait_ns(uint64_t ns) { set_prompt_wait_ns(ns); }
+void w4a4_debug_prompt_wait_ns(uint64_t ns, uint64_t tile_ns) { set_prompt_wait_ns(ns, tile_ns); }
 
 static w4a4_status pack_common(const float* W, const int8_t* codes, const uint16_t* scales, const uint16_t* L_down,
                                const uint16_t* L_up, int N, int K, int r, void* packed, size_t packed_bytes,

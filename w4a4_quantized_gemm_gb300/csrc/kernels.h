@@ -77,7 +77,7 @@ w4a4_status launch_paged_attention(const w4a4_kv_cache& c, const w4a4_paged_atte
 w4a4_status launch_qk_rope(const w4a4_qk_rope_args& a, cudaStream_t s);
 // prompt_attention.cu
 w4a4_status launch_prompt_attention(const w4a4_prompt_attention_args& a, cudaStream_t s);
-void set_prompt_wait_ns(uint64_t ns);
+void set_prompt_wait_ns(uint64_t ns, uint64_t tile_ns);
 w4a4_status launch_chunk_attention(const w4a4_kv_cache& c, const w4a4_chunk_attention_args& a, cudaStream_t s);
 // block_norm.cu
 w4a4_status launch_block_norm(const w4a4_block_norm_args& a, cudaStream_t s);

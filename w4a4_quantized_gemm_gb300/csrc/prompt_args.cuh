@@ -34,7 +34,7 @@ struct Args {
     int tokens, seqs, q_heads, kv_heads, group, window;
     bool causal;
     Divisor by_group;
-    uint64_t wait_ns = 0;                  // for a unit to be done with
+    uint64_t wait_ns = 0, tile_ns = 0;     // to wait for a unit to be done with, and more for each of its tiles
     bool q_boxes = false;                  // queries come by the copy engine: 128 rows are whole tokens
 };
 

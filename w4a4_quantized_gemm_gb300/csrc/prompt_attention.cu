@@ -10,11 +10,11 @@ namespace {
 
 using prompt::Args;
 
-std::atomic<uint64_t> g_wait_ns{0};
+std::atomic<uint64_t> g_wait_ns{0}, g_tile_ns{0};
 
 w4a4_status run(Args& A, int dim, bool bf16, bool e4m3, cudaStream_t s) {
-    const uint64_t ns = g_wait_ns.load(std::memory_order_relaxed);
-    A.wait_ns = ns > 0 ? ns : 2000000000ull;
+    A.wait_ns = g_wait_ns.load(std::memory_order_relaxed), A.tile_ns = g_tile_ns.load(std::memory_order_relaxed);
+    if (A.wait_ns == 0) A.wait_ns = 2000000000ull, A.tile_ns = 20000;  // a tile takes 1 to 2 us
     switch (dim) {
         case 64: return prompt::run_64(A, bf16, e4m3, s);
         case 96: return prompt::run_96(A, bf16, e4m3, s);
@@ -25,7 +25,9 @@ w4a4_status run(Args& A, int dim, bool bf16, bool e4m3, cudaStream_t s) {
 
 }  // namespace
 
-void set_prompt_wait_ns(uint64_t ns) { g_wait_ns.store(ns, std::memory_order_relaxed); }
+void set_prompt_wait_ns(uint64_t ns, uint64_t tile_ns) {
+    g_wait_ns.store(ns, std::memory_order_relaxed), g_tile_ns.store(tile_ns, std::memory_order_relaxed);
+}
 
 w4a4_status prompt_read_and_clear_status() {
     w4a4_status first = W4A4_OK;  // every word is read: reading clears it

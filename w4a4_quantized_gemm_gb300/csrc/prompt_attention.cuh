@@ -566,6 +566,12 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
         *abort = 1;
         return false;
     };
+    // The same for what comes when a unit of so many tiles is done with.
+    auto wait_for_unit = [&](uint32_t bar, uint32_t parity, int tiles) {
+        if (warp_wait_parity_suspend(bar, parity, abort, A.wait_ns + tiles * A.tile_ns, kSuspendNs)) return true;
+        *abort = 1;
+        return false;
+    };
     // The next unit, for every warp that works on it; nullptr: there are no more of this pass.  done_with gives
     // its place back.
     uint32_t n_unit = 0;
@@ -619,6 +625,7 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
         if (sorted) sort_sequences(A, mine, order);
         const Share share = share_out<D>(A, mine);
         Walk walk{sorted ? order : nullptr, mine};
+        int last = 0, before = 0;
         const uint32_t chosen = pass == 0 ? 0xffffffffu : redo;
         for (uint32_t m = 0;; ++m) {
             const int turn = int(m & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
@@ -627,15 +634,14 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
             if (live && !(chosen >> min(m, 31u) & 1)) continue;
             if (live && pass > 0) U.live = second_pass(A, U);
             const uint32_t n = n_unit++;
+            const int tiles = before;  // of the unit whose place this one takes
+            before = last, last = U.tiles;
             if (n == 0 && A.parts && lane == 0) {
                 const bool part = live && U.part >= 0;
                 A.parts_of[2 * blockIdx.x] = make_int4(U.begin, U.head, U.row0, U.rows);
                 A.parts_of[2 * blockIdx.x + 1] = make_int4(U.first_part, part ? U.pieces : 0, 0, 0);
             }
-            if (n >= 2 && !warp_wait_parity_suspend(u_free(n & 1), (n >> 1 & 1) ^ 1, abort, A.wait_ns, kSuspendNs)) {
-                *abort = 1;
-                return;
-            }
+            if (n >= 2 && !wait_for_unit(u_free(n & 1), (n >> 1 & 1) ^ 1, tiles)) return;
             if (lane == 0) {
                 units[n & 1] = U;
                 mbar_arrive(u_full(n & 1));
@@ -1346,7 +1352,8 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
                 ml[(2 + stream) * kTile + row] = sum;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(ml_full);
-                if (!wait(ml_full, n_ml & 1)) return;
+                // (with one stream half of the warps have no tiles and wait here for the others'; two end together)
+                if (!(P::kStreams == 1 ? wait_for_unit(ml_full, n_ml & 1, U.tiles) : wait(ml_full, n_ml & 1))) return;
                 const float m0 = ml[row], m1 = ml[kTile + row];
                 most = fmaxf(m0, m1);
                 w0 = m0 == -INFINITY ? 0.f : ex2(m0 - most), w1 = m1 == -INFINITY ? 0.f : ex2(m1 - most);

@@ -125,6 +125,15 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def on_stream(stream):
+    """A context in which tensors are allocated for `stream` (a torch stream, a handle, or None: the current one): memory
+    whose last use before was on that stream."""
+    if stream is not None and not isinstance(stream, torch.cuda.Stream):
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
 def _nbytes(t):
     return t.numel() * t.element_size()
 
@@ -444,11 +453,7 @@ def w4a4_rope_table(rows: int, rot_dim: int, theta: float, out=None, stream=None
     """fp32 [rows, 2, rot_dim / 2]: cosines and sines of position * theta^(-2 i / rot_dim).  A table that
     the call makes belongs to the stream that fills it."""
     if out is None:
-        on = stream
-        if on is not None and not isinstance(on, torch.cuda.Stream):
-            handle = on.cuda_stream if hasattr(on, "cuda_stream") else int(on)
-            on = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
-        with torch.cuda.stream(on):  # None: the current one
+        with on_stream(stream):
             out = torch.empty((rows, 2, rot_dim // 2), dtype=torch.float32, device="cuda")
     if out.shape != (rows, 2, rot_dim // 2) or out.dtype != torch.float32:
         _refuse("w4a4_rope_table")

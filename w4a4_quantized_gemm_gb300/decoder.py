@@ -40,7 +40,8 @@ class _Packed:
 
 
 class _Rows:
-    """The buffers of a layer's pass over so many rows (tokens)."""
+    """The buffers of a layer's pass over so many rows (tokens).  They belong to the stream that they are made for; the
+    allocator learns of others that torch owns."""
 
     def __init__(self, layer, rows: int):
         dev, hq, hkv, dim = layer.qkv.packed.device, layer.q_heads, layer.kv_heads, layer.dim
@@ -55,6 +56,18 @@ class _Rows:
         need = max(w4.act_workspace_bytes(rows, p.K, p.r) for p in (layer.qkv, layer.o, layer.gate_up, layer.down))
         self.ws = torch.empty(need, dtype=torch.uint8, device=dev)
         self.split = self.qkv_out.unflatten(1, (hq + 2 * hkv, dim)).split((hq, hkv, hkv), dim=1)
+        self._streams = set()
+
+    def used_on(self, stream):
+        """Keeps the memory from being handed out again, once these are dropped, before `stream` is done with them."""
+        if stream is None:
+            stream = torch.cuda.current_stream(self.ws.device)
+        handle, number = (getattr(stream, name, None) for name in ("cuda_stream", "stream_id"))
+        if handle is None or handle in self._streams or (handle != 0 and number == handle):
+            return  # a handle or an external stream, which may be gone by then, or one that is known
+        self._streams.add(handle)
+        for t in (self.qkv_out, self.q, self.attn, self.o_out, self.x_mlp, self.down_out, self.h, self.ws):
+            t.record_stream(stream)
 
 
 class W4A4DecoderLayer:
@@ -78,11 +91,14 @@ class W4A4DecoderLayer:
         self.qkv_out, self.q, self.attn, self.split = one.qkv_out, one.q, one.attn, one.split
         self.o_out, self.x_mlp, self.down_out, self.h, self.ws = one.o_out, one.x_mlp, one.down_out, one.h, one.ws
 
-    def rows(self, n: int) -> _Rows:
-        """The buffers for n rows, made at their first use (before a graph capture, if it is to use them)
-        and kept as long as the layer: a captured graph may hold them."""
+    def rows(self, n: int, stream=None) -> _Rows:
+        """The buffers for n rows, made at their first use on `stream` (before a graph capture, if it is to use them)
+        and kept as long as the layer: a captured graph may hold them.  Passes over as many rows use the same ones:
+        those on different streams have to be ordered."""
         if n not in self._rows:
-            self._rows[n] = _Rows(self, n)
+            with w4.on_stream(stream):
+                self._rows[n] = _Rows(self, n)
+        self._rows[n].used_on(stream)
         return self._rows[n]
 
     def _linear(self, p, X, Y, ws, stream):
@@ -103,7 +119,7 @@ class W4A4DecoderLayer:
         """One token of each sequence: x [seqs, hidden] its normalised input, r the residual stream
         (fp16 or fp32, updated in place), positions = lengths - 1 the token's place, lengths the
         cache's with it.  x_next receives the next layer's input under next_gain."""
-        b = self.rows(self.seqs)
+        b = self.rows(self.seqs, stream)
         q, k, v = b.split
         self._linear(self.qkv, x, b.qkv_out, b.ws, stream)
         w4.w4a4_kv_append(q, k, v, positions, cache, b.q, rope=rope, q_gain=self.q_gain, k_gain=self.k_gain,
@@ -115,7 +131,7 @@ class W4A4DecoderLayer:
         """A chunk of new tokens of every sequence, rows starts[b] .. starts[b + 1] - 1 of x [tokens, hidden]
         and r; row t is token positions[t] of sequence owners[t].  They go into the cache, which holds
         lengths[b] tokens of each with them, and are attended to over all of it.  The rest as for step."""
-        b = self.rows(x.shape[0])
+        b = self.rows(x.shape[0], stream)
         q, k, v = b.split
         self._linear(self.qkv, x, b.qkv_out, b.ws, stream)
         w4.w4a4_kv_append(q, k, v, positions, cache, b.q, seqs=owners, rope=rope, q_gain=self.q_gain,
@@ -126,7 +142,7 @@ class W4A4DecoderLayer:
     def prompt(self, x, r, positions, starts, rope, next_gain, x_next, causal=True, stream=None):
         """Whole prompts, packed one behind the other (rows starts[b] .. starts[b + 1] - 1), without a cache.
         Rows of x outside all of them are padding: positions[t] < 0, and their results are not defined."""
-        b = self.rows(x.shape[0])
+        b = self.rows(x.shape[0], stream)
         q, k, v = b.split
         self._linear(self.qkv, x, b.qkv_out, b.ws, stream)
         w4.w4a4_qk_rope(q, k, positions, q, k, rope=rope, q_gain=self.q_gain, k_gain=self.k_gain, eps=self.eps,

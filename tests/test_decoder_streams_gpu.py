@@ -85,3 +85,58 @@ def test_buffers_outlive_the_layer(kind, first):
     spans = [(p, p + n) for p, n in buffers]
     assert busy and not any(lo < t.data_ptr() + t.numel() and t.data_ptr() < hi for t in again for lo, hi in spans)
     assert len(weights) == 7  # they are the caller's to keep, as tensors are
+
+
+def test_passes_over_many_lengths_in_one_room():
+    """Prompts of growing and shrinking length through two layers that share their buffers: each the same as through
+    layers that hold no others."""
+    shared = decoder.Buffers()
+    g = torch.Generator(device="cuda").manual_seed(6)
+    made = [decoder.random_layer(512, 640, HQ, HKV, DIM, 1, seed=i, buffers=shared) for i in range(2)]
+    rope, gain = w4.w4a4_rope_table(500, DIM, 1e6), torch.ones(512, dtype=torch.float16, device="cuda")
+    for n in (300, 20, 301, 500, 1, 299):
+        x, r = torch.randn(n, 512, generator=g, device="cuda").half(), torch.randn(n, 512, generator=g, device="cuda")
+        results = []
+        for rooms in (shared, decoder.Buffers()):
+            stream, xs = r.clone(), [x, torch.empty_like(x), torch.empty_like(x)]
+            for i, layer in enumerate(made):
+                layer.prompt(xs[i], stream, ints(list(range(n))), ints([0, n]), rope, gain, xs[i + 1],
+                             buffers=None if rooms is shared else rooms)
+            results.append((stream, xs[2]))
+        assert all(torch.equal(a, b) for a, b in zip(*results)), n
+    assert w4.w4a4_device_status() == 0
+
+
+def test_two_streams_with_buffers_of_their_own():
+    """A prompt of one layer on each of two streams at the same time, and a decode step on a third."""
+    layer, x, r, gain = layer_and_inputs(ROWS, 1, 7)
+    rope, at, starts = w4.w4a4_rope_table(ROWS, DIM, 1e6), ints(list(range(ROWS))), ints([0, ROWS])
+    cache = decoder.paged_cache(1, 16, HKV, DIM)
+    cache.workspace(HQ)
+    sides, rooms = [torch.cuda.Stream() for _ in range(3)], [decoder.Buffers() for _ in range(2)]
+    inputs = [x, x.flip(0).contiguous()]
+    one, first, place = x[:1].contiguous(), ints([1]), ints([0])
+
+    def prompt(i, streams, outs, stream=None):
+        layer.prompt(inputs[i], streams[i], at, starts, rope, gain, outs[i], stream=stream, buffers=rooms[i])
+
+    def step(streams, outs, stream=None):
+        layer.step(one, streams[2], place, first, cache, rope, gain, outs[2], stream=stream)
+
+    def fresh():
+        return ([r.clone(), r.clone(), r[:1].clone()], [torch.empty_like(x), torch.empty_like(x), torch.empty_like(one)])
+
+    want = fresh()
+    for i in range(2):
+        prompt(i, *want)
+    step(*want)
+    torch.cuda.synchronize()
+    for turn in range(5):
+        got = fresh()
+        torch.cuda.synchronize()
+        for i in range(2):
+            prompt(i, *got, stream=sides[i])
+        step(*got, stream=sides[2])
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for w, g in zip(want, got) for a, b in zip(w, g)), turn
+    assert w4.w4a4_device_status() == 0

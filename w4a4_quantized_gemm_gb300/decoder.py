@@ -40,34 +40,76 @@ class _Packed:
 
 
 class _Rows:
-    """The buffers of a layer's pass over so many rows (tokens).  They belong to the stream that they are made for; the
-    allocator learns of others that torch owns."""
+    """The first n rows of a set of buffers: what a layer's pass over n rows (tokens) writes."""
+
+    def __init__(self, layer, whole, n: int):
+        for name in _ROWS:
+            setattr(self, name, getattr(whole, name)[:n])
+        self.ws = whole.ws[:_workspace_bytes(layer, n)]
+        heads = layer.q_heads, layer.kv_heads, layer.kv_heads
+        self.split = self.qkv_out.unflatten(1, (sum(heads), layer.dim)).split(heads, dim=1)
+
+
+_ROWS = ("qkv_out", "q", "attn", "o_out", "x_mlp", "down_out", "h")
+
+
+def _workspace_bytes(layer, rows: int) -> int:
+    return max(w4.act_workspace_bytes(rows, p.K, p.r) for p in (layer.qkv, layer.o, layer.gate_up, layer.down))
+
+
+class _Set:
+    """Buffers for up to `rows` rows.  They belong to the stream that they are made for; the allocator learns of others
+    that torch owns."""
 
     def __init__(self, layer, rows: int):
-        dev, hq, hkv, dim = layer.qkv.packed.device, layer.q_heads, layer.kv_heads, layer.dim
+        dev, heads, hidden = layer.qkv.packed.device, (layer.q_heads, layer.dim), layer.o.N
+        shapes = (layer.qkv.N,), heads, heads, (hidden,), (hidden,), (hidden,), (layer.gate_up.N // 2,)
+        for name, shape in zip(_ROWS, shapes):
+            setattr(self, name, torch.empty((rows, *shape), dtype=torch.float16, device=dev))
+        self.ws = torch.empty(_workspace_bytes(layer, rows), dtype=torch.uint8, device=dev)
+        self.rows, self._views, self._streams = rows, {}, set()
 
-        def buf(*shape):
-            return torch.empty(shape, dtype=torch.float16, device=dev)
-
-        hidden = layer.o.N
-        self.qkv_out, self.q, self.attn = buf(rows, layer.qkv.N), buf(rows, hq, dim), buf(rows, hq, dim)
-        self.o_out, self.x_mlp, self.down_out = buf(rows, hidden), buf(rows, hidden), buf(rows, hidden)
-        self.h = buf(rows, layer.gate_up.N // 2)
-        need = max(w4.act_workspace_bytes(rows, p.K, p.r) for p in (layer.qkv, layer.o, layer.gate_up, layer.down))
-        self.ws = torch.empty(need, dtype=torch.uint8, device=dev)
-        self.split = self.qkv_out.unflatten(1, (hq + 2 * hkv, dim)).split((hq, hkv, hkv), dim=1)
-        self._streams = set()
+    def first(self, layer, n: int) -> _Rows:
+        views = self._views
+        if n not in views:
+            if len(views) >= 64:  # views are small, but lengths are many
+                views.clear()
+            views[n] = _Rows(layer, self, n)
+        return views[n]
 
     def used_on(self, stream):
         """Keeps the memory from being handed out again, once these are dropped, before `stream` is done with them."""
+        if not self.ws.is_cuda:
+            return
         if stream is None:
             stream = torch.cuda.current_stream(self.ws.device)
         handle, number = (getattr(stream, name, None) for name in ("cuda_stream", "stream_id"))
         if handle is None or handle in self._streams or (handle != 0 and number == handle):
             return  # a handle or an external stream, which may be gone by then, or one that is known
         self._streams.add(handle)
-        for t in (self.qkv_out, self.q, self.attn, self.o_out, self.x_mlp, self.down_out, self.h, self.ws):
-            t.record_stream(stream)
+        for name in (*_ROWS, "ws"):
+            getattr(self, name).record_stream(stream)
+
+
+class Buffers:
+    """Room for passes over any number of rows.  A pass takes the first rows of the largest set of buffers so far; where
+    they do not suffice there is a new set, at least twice as large, and the others stay, since a captured graph may hold
+    them: room for at most four times the rows of the largest pass, and a workspace a set.  Layers of the same
+    shapes may share one, as a stack's do, whose passes follow one another.  Passes that may overlap on the GPU need
+    one each."""
+
+    def __init__(self):
+        self._sets = {}
+
+    def rows(self, layer, n: int, stream=None) -> _Rows:
+        """The buffers that a pass of `layer` over n rows uses, made on `stream` if need be (before a graph capture, if it
+        is to use them)."""
+        sets = self._sets.setdefault(layer.shape, [])
+        if not sets or sets[-1].rows < n:
+            with w4.on_stream(stream):
+                sets.append(_Set(layer, max(n, 2 * sets[-1].rows if sets else 0)))
+        sets[-1].used_on(stream)
+        return sets[-1].first(layer, n)
 
 
 class W4A4DecoderLayer:
@@ -77,29 +119,27 @@ class W4A4DecoderLayer:
     takes them; gate_up has the gate rows first.  q_gain, k_gain: the per-head norms' gains [head_dim]
     (None: no such norm); mlp_gain [hidden]: the norm between attention and MLP.  The norm before
     attention belongs to the layer before (its gain is step's next_gain), so that it is fused with
-    that layer's residual addition.
+    that layer's residual addition.  buffers: what chunk and prompt write on their way (a Buffers of its
+    own by default).
     """
 
     def __init__(self, qkv, o, gate_up, down, q_heads: int, kv_heads: int, head_dim: int, seqs: int, mlp_gain,
-                 q_gain=None, k_gain=None, eps: float = 1e-6):
+                 q_gain=None, k_gain=None, eps: float = 1e-6, buffers=None):
         self.qkv, self.o, self.down = _Packed(*qkv), _Packed(*o), _Packed(*down)
         self.gate_up = _Packed(*gate_up, gate_up=True)
         self.q_heads, self.kv_heads, self.dim, self.seqs, self.eps = q_heads, kv_heads, head_dim, seqs, eps
         self.mlp_gain, self.q_gain, self.k_gain = mlp_gain, q_gain, k_gain
-        self._rows = {}
-        one = self.rows(seqs)
+        packed = self.qkv, self.o, self.gate_up, self.down
+        self.shape = (*((p.N, p.K, p.r) for p in packed), q_heads, kv_heads, head_dim, self.qkv.packed.device)
+        self.buffers = Buffers() if buffers is None else buffers
+        self._step = _Set(self, seqs)
+        one = self._step.first(self, seqs)
         self.qkv_out, self.q, self.attn, self.split = one.qkv_out, one.q, one.attn, one.split
         self.o_out, self.x_mlp, self.down_out, self.h, self.ws = one.o_out, one.x_mlp, one.down_out, one.h, one.ws
 
-    def rows(self, n: int, stream=None) -> _Rows:
-        """The buffers for n rows, made at their first use on `stream` (before a graph capture, if it is to use them)
-        and kept as long as the layer: a captured graph may hold them.  Passes over as many rows use the same ones:
-        those on different streams have to be ordered."""
-        if n not in self._rows:
-            with w4.on_stream(stream):
-                self._rows[n] = _Rows(self, n)
-        self._rows[n].used_on(stream)
-        return self._rows[n]
+    def rows(self, n: int, stream=None, buffers=None) -> _Rows:
+        """The buffers that chunk and prompt use for n rows."""
+        return (self.buffers if buffers is None else buffers).rows(self, n, stream)
 
     def _linear(self, p, X, Y, ws, stream):
         w4.w4a4_forward(X, p.packed, p.colscale, p.bias, Y, p.r, ws, stream=stream)
@@ -119,7 +159,8 @@ class W4A4DecoderLayer:
         """One token of each sequence: x [seqs, hidden] its normalised input, r the residual stream
         (fp16 or fp32, updated in place), positions = lengths - 1 the token's place, lengths the
         cache's with it.  x_next receives the next layer's input under next_gain."""
-        b = self.rows(self.seqs, stream)
+        self._step.used_on(stream)
+        b = self._step.first(self, self.seqs)
         q, k, v = b.split
         self._linear(self.qkv, x, b.qkv_out, b.ws, stream)
         w4.w4a4_kv_append(q, k, v, positions, cache, b.q, rope=rope, q_gain=self.q_gain, k_gain=self.k_gain,
@@ -127,11 +168,13 @@ class W4A4DecoderLayer:
         w4.w4a4_paged_attention(b.q, cache, lengths, b.attn, stream=stream)
         self._after_attention(b, r, next_gain, x_next, stream)
 
-    def chunk(self, x, r, positions, owners, starts, lengths, cache, rope, next_gain, x_next, stream=None):
+    def chunk(self, x, r, positions, owners, starts, lengths, cache, rope, next_gain, x_next, stream=None,
+              buffers=None):
         """A chunk of new tokens of every sequence, rows starts[b] .. starts[b + 1] - 1 of x [tokens, hidden]
         and r; row t is token positions[t] of sequence owners[t].  They go into the cache, which holds
-        lengths[b] tokens of each with them, and are attended to over all of it.  The rest as for step."""
-        b = self.rows(x.shape[0], stream)
+        lengths[b] tokens of each with them, and are attended to over all of it.  buffers: instead of the
+        layer's.  The rest as for step."""
+        b = self.rows(x.shape[0], stream, buffers)
         q, k, v = b.split
         self._linear(self.qkv, x, b.qkv_out, b.ws, stream)
         w4.w4a4_kv_append(q, k, v, positions, cache, b.q, seqs=owners, rope=rope, q_gain=self.q_gain,
@@ -139,10 +182,11 @@ class W4A4DecoderLayer:
         w4.w4a4_chunk_attention(b.q, cache, starts, lengths, b.attn, stream=stream)
         self._after_attention(b, r, next_gain, x_next, stream)
 
-    def prompt(self, x, r, positions, starts, rope, next_gain, x_next, causal=True, stream=None):
+    def prompt(self, x, r, positions, starts, rope, next_gain, x_next, causal=True, stream=None,
+               buffers=None):
         """Whole prompts, packed one behind the other (rows starts[b] .. starts[b + 1] - 1), without a cache.
         Rows of x outside all of them are padding: positions[t] < 0, and their results are not defined."""
-        b = self.rows(x.shape[0], stream)
+        b = self.rows(x.shape[0], stream, buffers)
         q, k, v = b.split
         self._linear(self.qkv, x, b.qkv_out, b.ws, stream)
         w4.w4a4_qk_rope(q, k, positions, q, k, rope=rope, q_gain=self.q_gain, k_gain=self.k_gain, eps=self.eps,
@@ -152,7 +196,7 @@ class W4A4DecoderLayer:
 
 
 def random_layer(hidden: int, inner: int, q_heads: int, kv_heads: int, dim: int, seqs: int, rank: int = 32,
-                 seed: int = 0):
+                 seed: int = 0, buffers=None):
     """A layer with N(0, 0.02) weights (LoRA factors included) and unit gains with some spread."""
     g = torch.Generator(device="cuda").manual_seed(seed)
 
@@ -164,7 +208,7 @@ def random_layer(hidden: int, inner: int, q_heads: int, kv_heads: int, dim: int,
 
     return W4A4DecoderLayer(linear((q_heads + 2 * kv_heads) * dim, hidden), linear(hidden, q_heads * dim),
                             linear(2 * inner, hidden), linear(hidden, inner), q_heads, kv_heads, dim, seqs,
-                            1 + n(hidden, std=0.1), 1 + n(dim, std=0.1), 1 + n(dim, std=0.1))
+                            1 + n(hidden, std=0.1), 1 + n(dim, std=0.1), 1 + n(dim, std=0.1), buffers=buffers)
 
 
 def paged_cache(seqs: int, tokens: int, kv_heads: int, dim: int, page_size: int = 16, dtype=torch.float16):
@@ -185,7 +229,8 @@ def check_status(where: str):
 
 def main(seqs: int = 32, tokens: int = 2048, layers: int = 28):
     hidden, inner, q_heads, kv_heads, dim = 1024, 3072, 16, 8, 128
-    stack = [random_layer(hidden, inner, q_heads, kv_heads, dim, seqs, seed=i) for i in range(layers)]
+    buffers = Buffers()
+    stack = [random_layer(hidden, inner, q_heads, kv_heads, dim, seqs, seed=i, buffers=buffers) for i in range(layers)]
     caches = [paged_cache(seqs, tokens, kv_heads, dim) for _ in range(layers)]
     rope = w4.w4a4_rope_table(tokens, dim, 1e6)
     lengths = torch.full((seqs,), tokens, dtype=torch.int32, device="cuda")

@@ -468,8 +468,9 @@ w4a4_status w4a4_qk_rope(const w4a4_qk_rope_args* args, cudaStream_t stream);
  *   out[i][h] = sum_j exp(a_j - lse) v_j[g].
  * causal: i sees j <= i, with window > 0 only i - window < j; not causal (window must
  * be 0): all rows.  A row whose a_j are all -inf (or that sees none) gives out = 0 and
- * lse = -inf.  Rows that i does not see have no part in its output, whatever they hold; rows
- * outside all sequences are neither read nor written.
+ * lse = -inf.  Rows that i does not see have no part in its output, whatever they hold.  Rows
+ * outside all sequences are not written and have no part in anything; rows of q among them
+ * may be read (queries are copied 128 at a time).
  * q, k, v, out: dtype W4A4_F16 or W4A4_BF16, head_dim 64, 96, 128 or 256, row (i, h) at
  * i * token_stride + h * head_stride elements (16-byte aligned); lse fp32 [tokens][q_heads]
  * or NULL.  q_heads % kv_heads == 0.  out overlaps no input, and its rows not each other

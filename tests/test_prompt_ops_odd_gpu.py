@@ -193,3 +193,26 @@ def test_prompt_rows_keep_their_bits_beside_a_value_that_they_do_not_see(dtype, 
     assert torch.equal(out[~sees], odd[~sees]) and torch.equal(out[:, heads:], odd[:, heads:])
     hit = odd[sees][:, :heads]
     assert not torch.isfinite(hit[..., ::3]).any() and torch.equal(hit[..., 1::3], out[sees][:, :heads, 1::3])
+
+
+@pytest.mark.parametrize("dtype, dim, hq, hkv", [(F16, 128, 4, 2), (BF16, 64, 3, 1), (BF16, 256, 2, 2)])
+def test_rows_outside_all_sequences_have_no_part(dtype, dim, hq, hkv):
+    """With NaN in them the sequences' rows have the bits that they have with numbers."""
+    g = torch.Generator(device="cuda").manual_seed(dim)
+    n, starts = 400, [7, 150, 150, 290]
+    q, k, v = (torch.randn((n, h, dim), generator=g, device="cuda").to(dtype) for h in (hq, hkv, hkv))
+    c = Cache([200, 0, 300], 16, hkv, dim, dtype, seed=33)
+    results = []
+    for outside in (1.0, NAN):
+        for x in (q, k, v):
+            x[:starts[0]], x[starts[-1]:] = outside, outside
+        got = [fresh(q), fresh(q)]
+        w4.w4a4_prompt_attention(q, k, v, ints(starts), got[0][0], lse=got[0][1])
+        w4.w4a4_chunk_attention(q, c.handle, ints(starts), ints(c.lengths), got[1][0], lse=got[1][1])
+        results.append(got)
+    torch.cuda.synchronize()
+    assert w4.w4a4_device_status() == 0
+    for one, other in zip(*results):
+        for a, b in zip(one, other):
+            assert torch.equal(a[7:290], b[7:290]) and torch.isfinite(a[7:290]).all()
+            assert torch.isnan(b[:7]).all() and torch.isnan(b[290:]).all()

@@ -17,7 +17,7 @@
 //    their scores in tensor memory as 16-bit numbers and are the first operand of the product
 //    with the values.  A row of scores is one thread's: 128 registers, no exchange.
 //  * One pass: the running maximum that is subtracted is renewed, and the output rescaled,
-//    only where the scores exceed it by more than kSlack (as a power of two).
+//    only where the scores exceed it by more than `slack` (as a power of two).
 //  * Keys and values come into a ring of stages by tensor maps, in boxes of 32, 16 or 8 rows (a
 //    page's), where strides and page sizes allow it, else 16 bytes a lane.  E4M3 rows go into a
 //    ring of their own and eight warps turn them into 16-bit ones.  Rows that no query of the
@@ -25,13 +25,13 @@
 //  * Infinite and NaN values that a row does not see: units with such rows are taken again in a second
 //    pass (see partly_seen), after all others, at the same speed.
 //
-// What bounds it, where rows and keys are many: a product of 128 x 128 x 16 takes 64 cycles and reads
-// 8 KB of shared memory (4 KB with the first operand in tensor memory), which is all that the port
-// gives, and the copies come on top; 16 of them are a tile's at D = 128.  Four warps take 1700 to
-// 2000 cycles for a tile's probabilities, half of it powers, behind the other stream's products:
-// 3300 cycles for a tile of both.  8192 causal tokens of 32 heads of 128: 410 us, 1.34 PFLOP/s, 0.71
-// of what a library's matrix product reaches.  Calls of a few rows are bound by what a launch, the
-// plan and cold code take.
+// What bounds it, where rows and keys are many: the chain of a tile, scores, maximum, powers, product with the
+// values, next scores, of which two run side by side.  At D = 128 a pair of tiles takes 3330 cycles; its
+// products (32 of 128 x 128 x 16, 64 cycles each) take 2048 of them, and so does the shared memory's port (192 KB
+// of operands and 64 KB of copies at 128 bytes a cycle).  Four warps take 1700 to 2000 cycles for a tile's
+// probabilities, half of it powers, behind the other stream's products.  With D = 256 there is one chain, and the
+// port takes 2560 cycles of its 4000.  8192 causal tokens of 32 heads of 128: 413 us, 1.33 PFLOP/s, 0.71 of what a
+// library's matrix product reaches.  Calls of a few rows are bound by what a launch, the plan and cold code take.
 #pragma once
 #include <algorithm>
 #include <atomic>
@@ -82,16 +82,15 @@ struct Plan {
     static constexpr int kStreams = D == 256 ? 1 : 2;
     static constexpr int kQTile = kHalves * kStage;
     static constexpr int kQ = kStreams * kQTile;
-    // Both rings fill the shared memory; 8-bit rows in flight gain less from room than 16-bit ones (D = 128
-    // with stages 3 + 4 202 us for 182 with those below).
+    // Both rings fill the shared memory; 8-bit rows in flight gain less from room than 16-bit ones (D = 128, 64 sequences
+    // of 4 tokens behind up to 8191, 32 heads for 8: 195 us with stages 3 + 4, 183 with those below).
     static constexpr int kStages = E4M3 ? (D == 64 ? 6 : 4) : D == 64 ? 11 : 5;
     static constexpr int kRawStages = E4M3 ? (D == 64 ? 10 : 2) : 0;
     static constexpr int kRawStage = kTile * kDs;
     static constexpr bool kRawSwizzled = kDs == 128;
     static constexpr int kRawRing = kRawStages > 0 ? kRawStages : 1;
-    // warps: softmax, copies (twice as many to widen 8-bit rows: 64 sequences of 4 tokens behind up to 8191,
-    // 32 heads for 8, took 236 us with four and 182 with eight), then one that plans, two that issue
-    // products, one for the ring of 8-bit rows
+    // warps: softmax, copies (twice as many to widen 8-bit rows: the same sequences took 236 us with four and 182
+    // with eight when they were added), then one that plans, two that issue products, one for the ring of 8-bit rows
     static constexpr int kCopyWarps = E4M3 ? 8 : 4;
     static constexpr int kMmaWarp = kSoftmaxWarps + kCopyWarps, kPlanWarp = kMmaWarp + 1, kRawWarp = kMmaWarp + 3;
     static constexpr int kThreads = 32 * (kMmaWarp + 4);
@@ -363,8 +362,8 @@ __device__ __forceinline__ Share share_out(const Args& A, const Sequence& mine) 
     };
     Share r{128, 0};
     // 256 rows a unit where there are units enough, or (below) tiles enough to split them into: 8192
-    // causal tokens of 32 heads for 8 take 410 us and 470 with 128, eight texts of 1500 both ways with
-    // 16 heads of 64 141 and 153, though the last round of their units is 5% full.
+    // causal tokens of 32 heads for 8 take 413 us and 464 with 128, eight texts of 1500 both ways with
+    // 16 heads of 64 139 and 151, though the last round of their units is 5% full.
     float units = kStreams == 2 ? units_of(256) : 0.f;
     if (units >= ctas) r.rows = 256;
     if (!A.parts || r.rows == 256) return r;
@@ -395,9 +394,9 @@ __device__ __forceinline__ Share share_out(const Args& A, const Sequence& mine) 
     return r;
 }
 
-// Sequences with the longest units first, for up to kSorted of them: what is left for the last
-// round is short then (six chunks of 417 tokens, the later ones behind more, D = 256: 99 us, 150 in
-// the sequences' order; 64 of 4 tokens behind up to 8191: 182 and 290).
+// Sequences with the longest units first, for up to kSorted of them (two a lane): what is left for the last
+// round is short then (six chunks of 417 tokens, the later ones behind more, D = 256: 89 us, 134 in
+// the sequences' order; 64 of 4 tokens behind up to 8191, E4M3: 183 and 274).  More are taken as they come.
 constexpr int kSorted = 64;
 __device__ __forceinline__ void sort_sequences(const Args& A, const Sequence& mine, uint8_t* order) {
     const int lane = threadIdx.x & 31;
@@ -1061,7 +1060,7 @@ attention_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtenso
     // The products of a stream, issued by one thread: the queue of the tensor cores holds two or
     // three, so what this thread does between the arrival of the probabilities and the next
     // scores leaves them idle, but for the other stream's.  With both streams' products from one
-    // thread 8192 tokens of 32 heads of 128 took 450 us (410 now), and with descriptors that the
+    // thread 8192 tokens of 32 heads of 128 took 450 us (413 now), and with descriptors that the
     // compiler sums up 690.
     uint32_t stages = 0;                                    // before this unit
     uint32_t turns = 0, n_o = 0, p_phase = 0, q_phase = 0;  // units with an output; bit i: the parity of p_full(i, .)

@@ -216,3 +216,44 @@ def test_rows_outside_all_sequences_have_no_part(dtype, dim, hq, hkv):
         for a, b in zip(one, other):
             assert torch.equal(a[7:290], b[7:290]) and torch.isfinite(a[7:290]).all()
             assert torch.isnan(b[:7]).all() and torch.isnan(b[290:]).all()
+
+
+def test_odd_values_that_come_and_go_between_replays():
+    """A captured prompt and chunk (split and whole units), replayed with numbers, with NaN in the last tokens' values and
+    with numbers again."""
+    g = torch.Generator(device="cuda").manual_seed(8)
+    q, k, v = (torch.randn((600, h, 128), generator=g, device="cuda").half() for h in (8, 4, 4))
+    c = Cache([5000, 300], 16, 4, 128, E4M3, seed=34)
+    c.handle.workspace(8)
+    starts, few = ints([0, 250, 600]), ints([0, 3, 40])
+    outs = [torch.empty_like(q), torch.empty_like(q[:40]), torch.empty_like(q)]
+    calls = [lambda: w4.w4a4_prompt_attention(q, k, v, starts, outs[0]),
+             lambda: w4.w4a4_chunk_attention(q[:40], c.handle, few, ints_of[0], outs[1]),
+             lambda: w4.w4a4_chunk_attention(q, c.handle, starts, ints_of[0], outs[2])]
+    ints_of = [ints([5000, 300])]
+    for call in calls:
+        call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for call in calls:
+            call()
+    page, slot = int(c.table[0, 4999 // 16]), 4999 % 16
+    held, seen = c.gv[page, slot, 1].clone(), []
+    for odd in (False, True, False, True):
+        v[599, 1, 7] = NAN if odd else 0.25
+        c.gv.view(torch.uint8)[page, slot, 1] = 0x7F if odd else held.view(torch.uint8)
+        for out in outs:
+            out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert w4.w4a4_device_status() == 0
+        seen.append([out.clone() for out in outs])
+    for a, b in ((0, 2), (1, 3)):
+        assert all(torch.equal(x.view(torch.int16), y.view(torch.int16)) for x, y in zip(seen[a], seen[b]))
+    number, nan = seen[:2]
+    rows = [599, 2, 249]  # the rows that see the last token
+    for i, row in enumerate(rows):
+        assert torch.isfinite(number[i]).all()
+        assert torch.equal(number[i][:, :2], nan[i][:, :2]) and torch.equal(number[i][:row], nan[i][:row])
+        assert torch.isnan(nan[i][row, 2:4, 7]).all() and torch.equal(number[i][row + 1:], nan[i][row + 1:])
